@@ -433,9 +433,119 @@ int fak_prefill_kernels(const fak_prefill* ctx);
 int fak_prefill_status(fak_prefill* ctx, fak_stream_t stream);
 void fak_prefill_destroy(fak_prefill* ctx);
 
+/* ------------------------------------------------------------------ paged KV cache
+ * A key / value cache that many sequences share, in pages, for the full-attention
+ * layers' chunks of new tokens and batches of single tokens (the one-launch decode
+ * above keeps its own f32 cache of one sequence).  A cache holds, for keys and for
+ * values, codes [n_pages][n_kv][page][dh] and, in the 8-bit kinds, one f32 scale
+ * per vector [n_pages][n_kv][page]; a cached vector is code * scale.
+ *   FAK_KV_BF16: codes are the vector rounded to bf16; no scales (NULL).
+ *   FAK_KV_E4M3: a = max|x|, scale = a / 448, code = e4m3(x * (448 / a)).
+ *   FAK_KV_I8:   scale = a / 127, code = rint(x * (127 / a)), int8.
+ * In the 8-bit kinds a vector with a < 2^-100 is held as zeros, and one that
+ * holds a NaN or an infinity reads back as NaN in every element.
+ * dh is 64, 128 or 256; page is 16, 32, 64, 128 or 256 tokens; n_pages * n_kv *
+ * page < 2^31; codes 16-byte aligned.  The memory is the caller's.
+ */
+enum { FAK_KV_BF16 = 0, FAK_KV_E4M3 = 1, FAK_KV_I8 = 2 };
+enum { FAK_ROWS_F32 = 0, FAK_ROWS_BF16 = 1 };
+
+typedef struct {
+    int32_t kind, n_kv, dh, page;
+    int64_t n_pages;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} fak_kv_cache;
+
+/* A ragged batch, in device memory, read when the kernels run (so a captured
+ * graph may be replayed with other numbers in it).  Rows row_start[s] ..
+ * row_start[s+1]-1 are sequence s's, the last of its kv_len[s] positions: row
+ * row_start[s] + i stands at position kv_len[s] - (row_start[s+1] -
+ * row_start[s]) + i.  Position p lies in page page_table[s][p / page], slot
+ * p % page.  Rows at negative positions are padding, rows from
+ * row_start[n_seqs] on belong to no sequence.  A sequence may have no rows.
+ * A sequence whose numbers are out of range (row_start not rising within
+ * 0 .. the call's rows, kv_len negative or above max_pages * page) is left
+ * out: nothing of it is read or written, and FAK_ERR_DEVICE is recorded.  A
+ * page number outside [0, n_pages) is recorded too: a write to it is dropped,
+ * a read takes page 0 in its place. */
+typedef struct {
+    int32_t n_seqs, max_pages;
+    const int32_t* page_table; /* device [n_seqs][max_pages] */
+    const int32_t* row_start;  /* device [n_seqs + 1] */
+    const int32_t* kv_len;     /* device [n_seqs], with the new rows */
+} fak_kv_batch;
+
+/* The new rows' projections, f32 (as the GEMMs write them) or bf16: head h of
+ * row r of x stands at x + r * x_row + h * x_head (elements), dh values next to
+ * each other, so slices of a fused projection need no copy.  Vectors start on
+ * 16-byte boundaries. */
+typedef struct {
+    int32_t type;                    /* FAK_ROWS_F32 or FAK_ROWS_BF16 */
+    int32_t nq, rot;                 /* query heads (0: none); rotary dims, 0 or a multiple of 16, <= dh */
+    float eps;                       /* RMSNorm's */
+    int64_t rows;
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const float *q_norm_w, *k_norm_w; /* device [dh] gains, 16-byte aligned; NULL: no norm */
+    const uint64_t* rope;             /* device [rot / 2], from fak_rope_table; NULL when rot is 0 */
+    void* q_out;                      /* device bf16 [rows][nq][dh], 16-byte aligned (NULL when nq is 0) */
+} fak_kv_rows;
+
+/* table (host, rot / 2 values): the rotary frequencies theta^(-2i/rot) as 64-bit
+ * fractions of a turn per position, so that position * table[i] modulo 2^64 is
+ * the angle with the whole turns already gone, at any position.  rot even, 2 to 256. */
+int fak_rope_table(int rot, double theta, uint64_t* table);
+
+/* Puts the rows' keys and values into the cache at their positions, quantising
+ * them as they are written, and the queries into q_out.  q and k first go through
+ * RMSNorm over the head with gain (where a gain is given), then RoPE on dims
+ * [0, rot), pairs (i, i + rot/2), as in the FA layer above; all in f32, rounded
+ * once.  Padding rows and rows of no sequence are left as they were, in the cache
+ * and in q_out.  Two rows of one call at one place of the cache race.  One launch. */
+int fak_kv_append(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_kv_rows* rows, fak_stream_t stream);
+
+/* The cached vectors of the rows' positions: k_out, v_out [rows][n_kv][dh], f32 or
+ * bf16 by `type`, 16-byte aligned; either may be NULL.  With row_start over the
+ * whole lengths it reads whole sequences back.  Padding rows read as zeros; rows of
+ * no sequence are left as they were.  One launch. */
+int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch, int64_t rows, int type, void* k_out, void* v_out,
+                fak_stream_t stream);
+
+/* Softmax attention of the rows over the cache (which must hold their own keys and
+ * values by then): row r at position p, query head h, with the KV head g = h /
+ * (nq / n_kv) of its sequence:
+ *   out = sum_j w_j v_j / sum_j w_j * sigmoid(gate),  w_j = exp(scale * q . k_j),
+ *   over positions j <= p, and if window > 0 only j > p - window or j < sinks.
+ * Sequences may have one row (a decode step), a chunk, or a whole prompt, mixed in
+ * one call.  Scores, maxima and sums are f32; w is rounded to bf16 for the product
+ * with v (each weight off by at most 2^-8 of itself); out is rounded once.
+ * What stands at positions that a row does not see (NaN and infinities too) does
+ * not reach it.  A padding row, which sees nothing, gets zeros; rows of no sequence
+ * are left as they were.  Deterministic. */
+typedef struct {
+    int32_t nq;             /* query heads, a multiple of n_kv, nq / n_kv <= 128 */
+    int32_t window, sinks;  /* window 0: all positions */
+    int32_t max_q, max_kv;  /* bounds on the sequences' rows and kv_len (a sequence above them is left out, recorded) */
+    float scale;            /* > 0 */
+    int64_t rows;
+    const void* q;          /* device bf16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned */
+    int64_t q_row, q_head;
+    const float* gate;      /* device f32, NULL: none; same form, 16-byte aligned */
+    int64_t gate_row, gate_head;
+    void* out;              /* device bf16, same form, 16-byte aligned */
+    int64_t out_row, out_head;
+    void* workspace;        /* device, 256-byte aligned, fak_paged_attn_workspace_bytes bytes, not shared with a concurrent call */
+    size_t workspace_bytes;
+} fak_attn_args;
+
+/* The workspace's size for these bounds (pointers are not looked at); 0: none is needed. */
+size_t fak_paged_attn_workspace_bytes(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_attn_args* args);
+int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_attn_args* args, fak_stream_t stream);
+
 /* ------------------------------------------------------------------ status
  * Synchronizes `stream`, then reads and clears the status word shared by the
- * stateless calls (GEMV, batched GEMV, MLP, GEMM). */
+ * stateless calls (GEMV, batched GEMV, MLP, GEMM, paged KV cache and attention). */
 int fak_device_status(fak_stream_t stream);
 
 #ifdef __cplusplus

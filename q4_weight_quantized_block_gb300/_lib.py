@@ -20,6 +20,8 @@ FAK_MLP_NOALLOC_MAX_FF = 18432
 FAK_LAYER_GDN, FAK_LAYER_FA = 0, 1
 FAK_DECODE_ONE_LAUNCH, FAK_DECODE_PER_MATMUL, FAK_DECODE_ONE_LAUNCH_I8X, FAK_DECODE_PER_MATMUL_I8X = 0, 1, 2, 3
 FAK_DECODE_PER_MATMUL_HOST_WAIT = 4
+FAK_KV_BF16, FAK_KV_E4M3, FAK_KV_I8 = 0, 1, 2
+FAK_ROWS_F32, FAK_ROWS_BF16 = 0, 1
 
 P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 
@@ -54,6 +56,30 @@ class DecodeDesc(ctypes.Structure):
                 ("embedding", P), ("mixer", ctypes.POINTER(MixerDesc))]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("dh", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_pages", I64), ("k", P), ("v", P), ("k_scale", P), ("v_scale", P)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_table", P), ("row_start", P),
+                ("kv_len", P)]
+
+
+class KvRows(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("nq", ctypes.c_int32), ("rot", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rows", I64), ("q", P), ("k", P), ("v", P), ("q_row", I64), ("q_head", I64), ("k_row", I64),
+                ("k_head", I64), ("v_row", I64), ("v_head", I64), ("q_norm_w", P), ("k_norm_w", P), ("rope", P),
+                ("q_out", P)]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("nq", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32), ("scale", ctypes.c_float), ("rows", I64),
+                ("q", P), ("q_row", I64), ("q_head", I64), ("gate", P), ("gate_row", I64), ("gate_head", I64),
+                ("out", P), ("out_row", I64), ("out_head", I64), ("workspace", P), ("workspace_bytes", SZ)]
+
+
 _SIGS = {
     "fak_strerror": ([I32], ctypes.c_char_p),
     "fak_version": ([], ctypes.c_char_p),
@@ -82,6 +108,11 @@ _SIGS = {
     "fak_decode_debug_unreachable_wait": ([P, I32], I32),
     "fak_decode_destroy": ([P], None),
     "fak_device_status": ([P], I32),
+    "fak_rope_table": ([I32, ctypes.c_double, P], I32),
+    "fak_kv_append": ([P, P, P, P], I32),
+    "fak_kv_read": ([P, P, I64, I32, P, P, P], I32),
+    "fak_paged_attn_workspace_bytes": ([P, P, P], SZ),
+    "fak_paged_attn": ([P, P, P, P], I32),
     "fak_prefill_create": ([ctypes.POINTER(DecodeDesc), I64, ctypes.POINTER(P)], I32),
     "fak_prefill_run": ([P, P, P, P, P], I32),
     "fak_prefill_read_hidden": ([P, P, SZ, P], I32),
@@ -212,6 +243,106 @@ def fak_q4k_interleave_gate_up(Wg, Wu, F, K, W13, stream=None):
 
 def fak_device_status(stream=None):
     return int(lib.fak_device_status(_stream(stream)))
+
+
+# ------------------------------------------------------------------ paged KV cache and attention
+class KVCache:
+    """A paged cache's description: codes k, v [n_pages, n_kv, page, dh] (contiguous; bf16, or one byte each)
+    and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive."""
+
+    def __init__(self, kind, k, v, k_scale=None, v_scale=None):
+        width, scales = (2 if kind == FAK_KV_BF16 else 1), (k_scale, v_scale)
+        if k.shape != v.shape or k.dim() != 4 or any(t is not None and t.shape != k.shape[:3] for t in scales):
+            raise FakError(2, "KVCache")
+        if any(t.element_size() != width or not t.is_contiguous() for t in (k, v)) or any(
+                t is not None and (t.element_size() != 4 or not t.is_contiguous()) for t in scales):
+            raise FakError(1, "KVCache")
+        self._keep = (k, v, k_scale, v_scale)
+        n_pages, n_kv, page, dh = k.shape
+        self.kind, self.n_kv, self.dh = kind, n_kv, dh
+        self.desc = KvCacheDesc(kind, n_kv, dh, page, n_pages, _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class KVBatch:
+    """A ragged batch's description: int32 device tensors page_table [n_seqs, max_pages], row_start [n_seqs + 1]
+    and kv_len [n_seqs], read when the kernels run.  Keeps the tensors alive."""
+
+    def __init__(self, page_table, row_start, kv_len):
+        n = page_table.shape[0]
+        if page_table.dim() != 2 or row_start.shape != (n + 1,) or kv_len.shape != (n,):
+            raise FakError(2, "KVBatch")
+        if any(t.element_size() != 4 or not t.is_contiguous() for t in (page_table, row_start, kv_len)):
+            raise FakError(1, "KVBatch")
+        self._keep = (page_table, row_start, kv_len)
+        self.desc = KvBatchDesc(n, page_table.shape[1], _ptr(page_table), _ptr(row_start), _ptr(kv_len))
+        self.ref = ctypes.addressof(self.desc)
+
+
+def _heads(t, heads, dh, size, where):
+    """Pointer, row stride and head stride of rows [rows, heads, dh] with neighbouring values in a head."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
+        raise FakError(2, where)
+    if t.element_size() != size or t.stride(2) != 1:
+        raise FakError(1, where)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def fak_rope_table(rot, theta):
+    """Host int64 [rot / 2]: the rotary frequencies as 64-bit fractions of a turn (copy it to the device)."""
+    out = np.empty(max(0, rot // 2), dtype=np.int64)
+    _check(lib.fak_rope_table(int(rot), float(theta), out.ctypes.data), "fak_rope_table")
+    return out
+
+
+def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_w=None, eps=1e-6, rope=None, rot=0,
+                  stream=None):
+    """k, v [rows, n_kv, dh] and q [rows, nq, dh], f32 or bf16 (views with strides are fine); q_out bf16."""
+    size = k.element_size()
+    if size not in (2, 4) or (q is not None and (q_out is None or not q_out.is_contiguous())):
+        raise FakError(1, "fak_kv_append")
+    if v.shape[0] != k.shape[0] or (q is not None and (q.shape[0] != k.shape[0] or q_out.shape != q.shape)):
+        raise FakError(2, "fak_kv_append")
+    kp, kr, kh = _heads(k, cache.n_kv, cache.dh, size, "fak_kv_append")
+    vp, vr, vh = _heads(v, cache.n_kv, cache.dh, size, "fak_kv_append")
+    nq = 0 if q is None else q.shape[1]
+    qp, qr, qh = (None, 0, 0) if q is None else _heads(q, nq, cache.dh, size, "fak_kv_append")
+    r = KvRows(FAK_ROWS_F32 if size == 4 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
+               vh, _ptr(q_norm_w), _ptr(k_norm_w), _ptr(rope), _ptr(q_out))
+    _check(lib.fak_kv_append(cache.ref, batch.ref, ctypes.addressof(r), _stream(stream)), "fak_kv_append")
+
+
+def fak_kv_read(cache, batch, k_out, v_out, stream=None):
+    """k_out, v_out [rows, n_kv, dh] contiguous, both f32 or both bf16; either may be None."""
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs or any(not t.is_contiguous() or t.element_size() not in (2, 4) for t in outs) or (
+            outs[0].dtype != outs[-1].dtype):
+        raise FakError(1, "fak_kv_read")
+    if any(t.dim() != 3 or t.shape[1:] != (cache.n_kv, cache.dh) or t.shape[0] != outs[0].shape[0] for t in outs):
+        raise FakError(2, "fak_kv_read")
+    kind = FAK_ROWS_F32 if outs[0].element_size() == 4 else FAK_ROWS_BF16
+    _check(lib.fak_kv_read(cache.ref, batch.ref, outs[0].shape[0], kind, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "fak_kv_read")
+
+
+def fak_paged_attn_workspace_bytes(cache, batch, nq, rows, max_q, max_kv, window=0, sinks=0):
+    a = AttnArgs(nq, window, sinks, max_q, max_kv, 1.0, rows)
+    return int(lib.fak_paged_attn_workspace_bytes(cache.ref, batch.ref, ctypes.addressof(a)))
+
+
+def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, sinks=0, gate=None, workspace=None,
+                   stream=None):
+    """q, out [rows, nq, dh] bf16 and gate f32 (views with strides are fine); scale defaults to dh^-1/2."""
+    nq = q.shape[1]
+    if out.shape != q.shape or (gate is not None and gate.shape != q.shape):
+        raise FakError(2, "fak_paged_attn")
+    qp, qr, qh = _heads(q, nq, cache.dh, 2, "fak_paged_attn")
+    op, orow, oh = _heads(out, nq, cache.dh, 2, "fak_paged_attn")
+    gp, gr, gh = (None, 0, 0) if gate is None else _heads(gate, nq, cache.dh, 4, "fak_paged_attn")
+    a = AttnArgs(nq, window, sinks, max_q, max_kv, cache.dh ** -0.5 if scale is None else scale, q.shape[0], qp, qr, qh,
+                 gp, gr, gh, op, orow, oh, _ptr(workspace),
+                 0 if workspace is None else workspace.numel() * workspace.element_size())
+    _check(lib.fak_paged_attn(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)), "fak_paged_attn")
 
 
 # ------------------------------------------------------------------ decode context

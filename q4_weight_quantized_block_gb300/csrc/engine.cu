@@ -1649,7 +1649,11 @@ extern "C" int fak_device_status(fak_stream_t stream) {
   cudaMemcpyToSymbol(g_fak_status, &zero, sizeof(int));
   const int g = fak_gemm_take_status();
   const int b = fak_bgemv_take_status();
-  return v != 0 ? v : (g != 0 ? g : b);
+  const int k = fak_kv_take_status();
+  const int a = fak_attn_take_status();
+  for (const int st : {v, g, b, k, a})
+    if (st != 0) return st;
+  return FAK_OK;
 }
 
 // ------------------------------------------------------------------ MLP decode

@@ -1,0 +1,163 @@
+"""Host-side refusals of the paged KV cache and the attention over it, before any device call (no GPU needed)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+OK = 1 << 20  # 16-byte aligned, never dereferenced: the checks come first
+
+
+@pytest.fixture(scope="module")
+def fak():
+    from q4_weight_quantized_block_gb300 import build
+    build.build()
+    import q4_weight_quantized_block_gb300 as m
+    return m
+
+
+def structs():
+    from q4_weight_quantized_block_gb300 import _lib as L
+    cache = L.KvCacheDesc(1, 4, 256, 64, 100, OK, OK, OK, OK)
+    batch = L.KvBatchDesc(2, 8, OK, OK, OK)
+    rows = L.KvRows(0, 24, 64, 1e-6, 10, OK, OK, OK, 512 * 24, 512, 1024, 256, 1024, 256, OK, OK, OK, OK)
+    args = L.AttnArgs(24, 0, 0, 4, 512, 0.0625, 10, OK, 6144, 256, OK, 12288, 512, OK, 6144, 256, OK, 1 << 40)
+    return cache, batch, rows, args
+
+
+def ref(x):
+    return None if x is None else ctypes.addressof(x)
+
+
+BAD_CACHE = [("kind", 3, 1), ("kind", -1, 1), ("k", None, 1), ("v", None, 1), ("k_scale", None, 1), ("v_scale", None, 1),
+             ("dh", 96, 2), ("dh", 512, 2), ("page", 8, 2), ("page", 48, 2), ("page", 512, 2), ("n_kv", 0, 2),
+             ("n_pages", 0, 2), ("n_pages", 1 << 31, 2), ("n_pages", 1 << 23, 2), ("k", OK + 8, 3), ("v", OK + 4, 3),
+             ("v_scale", OK + 2, 3)]
+BAD_BATCH = [("n_seqs", -1, 2), ("max_pages", 0, 2), ("page_table", None, 1), ("row_start", None, 1), ("kv_len", None, 1),
+             ("kv_len", OK + 2, 3)]
+BAD_ROWS = [("type", 2, 1), ("nq", -1, 2), ("rows", -1, 2), ("rows", 1 << 31, 2), ("rot", 24, 2), ("rot", 272, 2),
+            ("rot", -16, 2), ("k", None, 1), ("v", None, 1), ("q", None, 1), ("q_out", None, 1), ("rope", None, 1),
+            ("eps", -1.0, 1), ("eps", math.nan, 1), ("q_head", 510, 3), ("k_row", 1026, 3), ("v_head", 2, 3),
+            ("q", OK + 4, 3), ("q_out", OK + 8, 3), ("k_norm_w", OK + 4, 3), ("rope", OK + 4, 3)]
+BAD_ARGS = [("nq", 0, 2), ("nq", 22, 2), ("nq", 4 * 129, 2), ("window", -1, 1), ("sinks", -1, 1), ("scale", 0.0, 1),
+            ("scale", -1.0, 1), ("scale", math.inf, 1), ("scale", math.nan, 1), ("rows", -1, 2), ("rows", 1 << 31, 2),
+            ("max_q", -1, 2), ("max_kv", -1, 2), ("max_kv", (1 << 30) + 1, 2), ("q", None, 1), ("out", None, 1),
+            ("q", OK + 8, 3), ("out", OK + 2, 3), ("gate", OK + 4, 3), ("q_row", 6145, 3), ("out_head", 252, 3),
+            ("gate_head", 513, 3), ("workspace", OK + 16, 3)]
+
+
+def calls(fak):
+    lib = fak.lib
+    return {"append": lambda c, b, r, a: lib.fak_kv_append(ref(c), ref(b), ref(r), None),
+            "read": lambda c, b, r, a: lib.fak_kv_read(ref(c), ref(b), 10, 0, OK, OK, None),
+            "attn": lambda c, b, r, a: lib.fak_paged_attn(ref(c), ref(b), ref(a), None)}
+
+
+@pytest.mark.parametrize("which", ["append", "read", "attn"])
+def test_bad_caches_and_batches(fak, which):
+    call = calls(fak)[which]
+    for i, table in ((0, BAD_CACHE), (1, BAD_BATCH)):
+        for field, value, status in table:
+            s = structs()
+            setattr(s[i], field, value)
+            assert call(*s) == status, (which, field, value)
+    c, b, r, a = structs()
+    assert call(None, b, r, a) == 1 and call(c, None, r, a) == 1
+
+
+def test_bad_rows(fak):
+    for field, value, status in BAD_ROWS:
+        s = structs()
+        setattr(s[2], field, value)
+        assert calls(fak)["append"](*s) == status, (field, value)
+    c, b, r, a = structs()
+    assert calls(fak)["append"](c, b, None, a) == 1
+
+
+def test_bad_attention_arguments(fak):
+    for field, value, status in BAD_ARGS:
+        s = structs()
+        setattr(s[3], field, value)
+        assert calls(fak)["attn"](*s) == status, (field, value)
+    c, b, r, a = structs()
+    assert calls(fak)["attn"](c, b, r, None) == 1
+
+
+def test_bad_reads(fak):
+    c, b, _, _ = structs()
+    read = fak.lib.fak_kv_read
+    assert read(ref(c), ref(b), 10, 2, OK, OK, None) == 1
+    assert read(ref(c), ref(b), 10, 0, None, None, None) == 1
+    assert read(ref(c), ref(b), -1, 0, OK, OK, None) == 2
+    assert read(ref(c), ref(b), 1 << 31, 0, OK, OK, None) == 2
+    assert read(ref(c), ref(b), 10, 0, OK + 4, OK, None) == 3
+
+
+def test_nothing_to_do_is_fine(fak):
+    c, b, r, a = structs()
+    r.rows = a.rows = 0
+    assert calls(fak)["append"](c, b, r, a) == 0 and calls(fak)["attn"](c, b, r, a) == 0
+    assert fak.lib.fak_kv_read(ref(c), ref(b), 0, 0, OK, None, None) == 0
+    c, b, r, a = structs()
+    b.n_seqs = 0
+    assert all(call(c, b, r, a) == 0 for call in calls(fak).values())
+
+
+def test_workspace_size_and_its_check(fak):
+    c, b, _, a = structs()
+    size = fak.lib.fak_paged_attn_workspace_bytes
+    for nulls in ((None, b, a), (c, None, a), (c, b, None)):
+        assert size(*(ref(x) for x in nulls)) == 0
+    a.nq = 23
+    assert size(ref(c), ref(b), ref(a)) == 0
+    for new, past in ((1, 100000), (64, 30000)):
+        c, b, _, a = structs()
+        b.n_seqs, a.max_q, a.max_kv, a.rows = 1, new, past, new
+        n = size(ref(c), ref(b), ref(a))
+        if n:  # too small a workspace, or none, is refused
+            a.workspace_bytes = n - 1
+            assert calls(fak)["attn"](c, b, None, a) == 2
+            a.workspace, a.workspace_bytes = None, n
+            assert calls(fak)["attn"](c, b, None, a) == 1
+
+
+def test_rope_table(fak):
+    t = fak.fak_rope_table(64, 1e7).astype(np.uint64).astype(np.float64) / 2.0**64
+    want = 1e7 ** (-2.0 * np.arange(32) / 64) / (2 * math.pi)
+    assert np.all(np.abs(t - want) <= want * 2.0**-51 + 2.0**-63)
+    for rot, theta, status in ((0, 1e4, 2), (3, 1e4, 2), (258, 1e4, 2), (64, 0.5, 1), (64, math.inf, 1), (64, math.nan, 1)):
+        with pytest.raises(fak.FakError) as e:
+            fak.fak_rope_table(rot, theta)
+        assert e.value.status == status
+    assert fak.lib.fak_rope_table(64, 1e4, None) == 1
+
+
+def test_binding_refuses_wrong_tensors(fak):
+    torch = pytest.importorskip("torch")
+    u8 = torch.zeros(4, 2, 16, 64, dtype=torch.uint8)
+    sc = torch.zeros(4, 2, 16)
+    cache = fak.KVCache(fak.FAK_KV_E4M3, u8, u8, sc, sc)
+    for bad in ((fak.FAK_KV_BF16, u8, u8), (fak.FAK_KV_I8, u8, u8[..., :32], sc, sc), (fak.FAK_KV_I8, u8, u8, sc, sc[:2]),
+                (fak.FAK_KV_E4M3, u8.transpose(0, 1), u8.transpose(0, 1), None, None)):
+        with pytest.raises(fak.FakError):
+            fak.KVCache(*bad)
+    i32 = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    batch = fak.KVBatch(*i32)
+    for bad in ((i32[0], i32[1][:2], i32[2]), (i32[0], i32[1], i32[2].long()), (i32[0].T, i32[1], i32[2])):
+        with pytest.raises(fak.FakError):
+            fak.KVBatch(*bad)
+    x = torch.zeros(5, 2, 64)
+    q = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    for k, v in ((x[:, :1], x), (x, x[:4]), (x.to(torch.float64), x), (x[..., ::2], x), (x, x.to(torch.bfloat16))):
+        with pytest.raises(fak.FakError):
+            fak.fak_kv_append(cache, batch, k, v, stream=0)
+    with pytest.raises(fak.FakError):
+        fak.fak_kv_append(cache, batch, x, x, q=torch.zeros(5, 4, 64), stream=0)
+    for a, o in ((q, q[:4]), (q.float(), q.float()), (q[..., ::2], q[..., ::2]), (q, q.float())):
+        with pytest.raises(fak.FakError):
+            fak.fak_paged_attn(cache, batch, a, o, 1, 1, stream=0)
+    with pytest.raises(fak.FakError):
+        fak.fak_paged_attn(cache, batch, q, q, 1, 1, gate=q, stream=0)
+    for a, o in ((None, None), (x, x[:4]), (x, x.to(torch.bfloat16)), (x.transpose(0, 1), None)):
+        with pytest.raises(fak.FakError):
+            fak.fak_kv_read(cache, batch, a, o, stream=0)

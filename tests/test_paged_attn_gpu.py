@@ -1,0 +1,279 @@
+"""GPU parity of the attention over the paged KV cache (fak_paged_attn) against plain attention in 64 bits on what the
+cache holds, with the bar that tests/_kv.py derives: single tokens, chunks and prompts, mixed in ragged batches, every
+head dim, cache type and page, windows and sinks, gates, and what a row must not see."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import _kv
+
+pytestmark = pytest.mark.gpu
+KINDS = ["bf16", "e4m3", "i8"]
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def fak():
+    from q4_weight_quantized_block_gb300 import build
+    build.build()
+    import q4_weight_quantized_block_gb300 as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda")
+
+
+class Setup:
+    def __init__(self, fak, kind, nq, n_kv, dh, page, lengths, seed=0, gate=False, pad_rows=0, sharp=1.0, window=0, sinks=0,
+                 edit=None):
+        self.fak, self.kind, self.nq, self.dh, self.page, self.lengths = fak, kind, nq, dh, page, lengths
+        self.window, self.sinks = window, sinks
+        self.table, self.start, self.kv_len, self.rows, n_pages = _kv.batch_tensors(lengths, page, seed=seed, pad_rows=pad_rows)
+        self.cache, self.mem = _kv.empty_cache(fak, kind, n_pages, n_kv, page, dh)
+        K = [randn(seed + 100 + i, t, n_kv, dh) for i, (_, t) in enumerate(lengths)]
+        V = [randn(seed + 200 + i, t, n_kv, dh) + 0.25 for i, (_, t) in enumerate(lengths)]
+        if edit:
+            edit(K, V)
+        _kv.fill(self.mem, kind, self.table, self.kv_len, page, K, V)
+        self.batch = fak.KVBatch(self.table, self.start, self.kv_len)
+        # queries, gates and results as slices of wider rows
+        self.q = (sharp * randn(seed + 1, self.rows, nq, 2 * dh)).to(torch.bfloat16)[..., dh:]
+        self.gate = randn(seed + 2, self.rows, 2 * nq, dh)[:, 1::2] if gate else None
+        self.out = torch.full((self.rows, nq + 1, dh), 9.0, dtype=torch.bfloat16, device="cuda")[:, :nq]
+        self.max_q, self.max_kv = max(n for n, _ in lengths), max(t for _, t in lengths)
+        self.scale = dh**-0.5
+
+    def workspace(self, max_q=None, max_kv=None):
+        n = self.fak.fak_paged_attn_workspace_bytes(self.cache, self.batch, self.nq, self.rows, max_q or self.max_q,
+                                                    max_kv or self.max_kv, window=self.window, sinks=self.sinks)
+        return torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN wherever it is read unwritten
+
+    def run(self, out=None, workspace=None, max_q=None, max_kv=None, stream=None):
+        ws = self.workspace(max_q, max_kv) if workspace is None else workspace
+        self.fak.fak_paged_attn(self.cache, self.batch, self.q, self.out if out is None else out, max_q or self.max_q,
+                                max_kv or self.max_kv, scale=self.scale, window=self.window, sinks=self.sinks, gate=self.gate,
+                                workspace=ws, stream=stream)
+        return ws
+
+    def want(self, lengths=None):
+        """Per sequence: rows, values, tolerance."""
+        t, row = self.table.cpu(), 0
+        for s, (n, total) in enumerate(lengths or self.lengths):
+            pos = torch.arange(total)
+            k, v = _kv.held(self.mem, self.kind, t[s, pos // self.page].long(), pos % self.page)
+            r = slice(row, row + n)
+            o, tol = _kv.attention(self.q[r], k, v, total - n, self.scale, self.window, self.sinks,
+                                   None if self.gate is None else self.gate[r])
+            yield r, o, tol
+            row += n
+
+    def check(self, lengths=None):
+        torch.cuda.synchronize()
+        assert self.fak.fak_device_status() == 0
+        for s, (r, o, tol) in enumerate(self.want(lengths)):
+            _kv.check(self.out[r], o, tol, "sequence %d" % s)
+        assert bool((self.out[int(self.start[-1]):] == 9.0).all())
+        assert bool((self.out.as_strided((self.rows, self.dh), (self.out.stride(0), 1), self.nq * self.dh) == 9.0).all())
+
+
+def case(fak, *a, **kw):
+    s = Setup(fak, *a, **kw)
+    s.run()
+    s.check()
+    return s
+
+
+HEADS = [(24, 4, 256), (6, 6, 256), (16, 1, 256), (32, 8, 128), (3, 1, 128), (40, 1, 128), (8, 2, 64), (5, 5, 64)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,n_kv,dh", HEADS)
+def test_single_tokens(fak, kind, nq, n_kv, dh):
+    case(fak, kind, nq, n_kv, dh, 16, [(1, 1), (1, 2), (1, 17), (1, 128), (1, 129), (1, 500)], seed=nq, gate=dh == 256)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nq,n_kv,dh", HEADS)
+def test_chunks(fak, kind, nq, n_kv, dh):
+    case(fak, kind, nq, n_kv, dh, 32, [(33, 33), (50, 300), (2, 131), (0, 40), (129, 129)], seed=nq + 1, gate=dh != 128)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_pages(fak, kind, page):
+    case(fak, kind, 6, 1, 256, page, [(1, 257), (40, 255), (7, 640), (1, page), (1, page + 1)], seed=page)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,total", [(1, 5000), (3, 4097), (20, 3333), (64, 2048), (300, 2500)])
+def test_few_rows_over_a_long_past(fak, kind, new, total):
+    # the keys are split over several blocks and joined
+    case(fak, kind, 12, 2, 256, 64, [(new, total)], seed=new, gate=True)
+    case(fak, kind, 8, 1, 128, 64, [(new, total)], seed=new + 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (100, 0), (128, 130), (500, 3), (5000, 4)])
+def test_window_and_sinks(fak, kind, window, sinks):
+    lengths = [(1, 1), (1, 700), (90, 700), (200, 200), (5, 70)]
+    case(fak, kind, 8, 2, 128, 16, lengths, seed=window, window=window, sinks=sinks, gate=True)
+    case(fak, kind, 6, 1, 256, 64, lengths, seed=window + 1, window=window, sinks=sinks)
+
+
+def test_sinks_without_a_window_change_nothing(fak):
+    a = case(fak, "bf16", 4, 1, 128, 16, [(20, 90)])
+    b = Setup(fak, "bf16", 4, 1, 128, 16, [(20, 90)], sinks=9)
+    b.run()
+    assert torch.equal(a.out, b.out)
+
+
+def test_a_prompt_of_many_tiles(fak):
+    case(fak, "bf16", 6, 1, 256, 64, [(1500, 1500)], seed=5)
+    case(fak, "e4m3", 4, 1, 128, 16, [(1100, 2000), (900, 900)], seed=6)
+
+
+def test_a_full_batch_of_single_tokens(fak):
+    lengths = [(1, 1 + (37 * i) % 900) for i in range(64)]
+    case(fak, "e4m3", 24, 4, 256, 64, lengths, seed=7, gate=True)
+    case(fak, "bf16", 8, 1, 64, 16, lengths + [(3, 90)] * 3, seed=8)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_sharp_scores(fak, kind):
+    # scores of +-100 and more: one key takes all the weight, maxima jump along the row
+    case(fak, kind, 6, 1, 256, 64, [(70, 600), (1, 999)], seed=9, sharp=30.0)
+
+
+def test_padding_rows_get_zeros_and_others_nothing(fak):
+    # more rows than positions: the first rows see nothing
+    case(fak, "bf16", 4, 2, 128, 16, [(1, 30), (8, 5), (200, 140), (3, 0), (1, 0)], seed=10, pad_rows=6, gate=True)
+    case(fak, "i8", 4, 2, 256, 16, [(1, 30), (1, 0), (2, 1)], seed=11, pad_rows=1)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("new,total,at", [(100, 100, 60), (100, 300, 290), (1, 200, 3), (3, 140, 138)])
+def test_odd_values_reach_only_the_rows_that_see_them(fak, bad, new, total, at):
+    def edit(K, V):
+        V[0][at, 0, 5] = bad
+
+    case(fak, "bf16", 6, 1, 256, 16, [(new, total)], seed=12, edit=edit)
+    case(fak, "bf16", 4, 2, 128, 16, [(new, total)], seed=13, edit=edit, window=50, sinks=2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_nan_keys_and_values_behind_a_row_are_not_seen(fak, kind):
+    def edit(K, V):
+        K[0][70:75] = NAN
+        V[0][70:75] = NAN
+
+    s = Setup(fak, kind, 6, 1, 256, 16, [(100, 100)], seed=14, edit=edit)
+    s.run()
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(s.out[:70]).all()) and bool(torch.isnan(s.out[70:]).all())
+    for r, o, tol in s.want():
+        _kv.check(s.out[:70], o[:70], tol[:70], "rows before")
+    w = Setup(fak, kind, 6, 1, 256, 16, [(3, 500)], seed=15, edit=edit, window=100, sinks=8)
+    w.run()
+    w.check()
+
+
+def test_equal_scores_of_the_lowest_value(fak):
+    # keys of zero: all weights equal, whatever the mask
+    def edit(K, V):
+        K[0].zero_()
+
+    case(fak, "bf16", 4, 1, 128, 16, [(40, 333)], seed=16, edit=edit, window=37, sinks=3)
+
+
+def test_bounds_above_the_lengths(fak):
+    s = Setup(fak, "bf16", 12, 2, 256, 64, [(1, 300), (4, 90)], seed=17)
+    s.run(max_q=64, max_kv=100000)
+    s.check()
+    s.out.fill_(9.0)
+    s.run(max_q=2000, max_kv=301)
+    s.check()
+
+
+def test_sequences_out_of_bounds_are_left_out(fak):
+    s = Setup(fak, "bf16", 4, 1, 128, 16, [(2, 60), (5, 40), (1, 90)], seed=18)
+    s.run(max_q=4, max_kv=90)
+    assert fak.fak_device_status() == 7
+    want = list(s.want())
+    for i in (0, 2):
+        _kv.check(s.out[want[i][0]], want[i][1], want[i][2], "sequence %d" % i)
+    assert bool((s.out[want[1][0]] == 9.0).all())
+    s.out.fill_(9.0)
+    s.run(max_q=5, max_kv=80)
+    assert fak.fak_device_status() == 7
+    for i in (0, 1):
+        _kv.check(s.out[want[i][0]], want[i][1], want[i][2], "sequence %d" % i)
+    assert bool((s.out[want[2][0]] == 9.0).all())
+
+
+def test_a_bad_page_is_recorded(fak):
+    for lengths in ([(1, 60), (1, 40)], [(30, 60), (40, 40)]):
+        s = Setup(fak, "i8", 4, 1, 128, 16, lengths, seed=19)
+        s.table[1, 1] = 1 << 30
+        s.run()
+        assert fak.fak_device_status() == 7
+        r, o, tol = next(iter(s.want()))
+        _kv.check(s.out[r], o, tol, "the other sequence")
+
+
+def test_same_bits_every_time_and_on_another_stream(fak):
+    for lengths in ([(1, 3000)], [(77, 900), (1, 40)]):
+        s = Setup(fak, "e4m3", 24, 4, 256, 64, lengths, seed=20, gate=True)
+        s.run()
+        torch.cuda.synchronize()
+        first = s.out.clone()
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            s.out.fill_(9.0)
+            side.wait_stream(torch.cuda.current_stream())
+            s.run(stream=side)
+            side.synchronize()
+            assert torch.equal(first.view(torch.int16), s.out.view(torch.int16))
+
+
+def test_two_calls_at_once_with_their_own_workspaces(fak):
+    a = Setup(fak, "bf16", 24, 4, 256, 64, [(1, 4000)], seed=21)
+    b = Setup(fak, "bf16", 24, 4, 256, 64, [(60, 2000)], seed=22)
+    wa, wb = a.workspace(), b.workspace()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a.run(workspace=wa, stream=s)
+        b.run(workspace=wb, stream=t)
+    a.check()
+    b.check()
+
+
+def test_captured_once_replayed_with_other_lengths(fak):
+    full = [(1, 2000), (1, 700), (1, 64)]
+    s = Setup(fak, "i8", 12, 2, 256, 64, full, seed=23, gate=True)
+    ws = s.workspace()
+    s.run(workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.run(workspace=ws)
+    for lengths in (full, [(1, 1999), (1, 1), (1, 33)], [(1, 130), (1, 699), (1, 64)]):
+        s.kv_len.copy_(torch.tensor([t for _, t in lengths], dtype=torch.int32))
+        s.out.fill_(9.0)
+        g.replay()
+        s.check(lengths)
+    # and with rows divided otherwise: the second sequence has them all
+    s2 = Setup(fak, "bf16", 12, 2, 256, 64, [(10, 100), (10, 900)], seed=24)
+    ws2 = s2.workspace(max_q=20)
+    g2 = torch.cuda.CUDAGraph()
+    s2.run(workspace=ws2, max_q=20)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g2):
+        s2.run(workspace=ws2, max_q=20)
+    for lengths in ([(10, 100), (10, 900)], [(0, 100), (20, 900)], [(1, 100), (3, 500)]):
+        s2.start.copy_(torch.tensor([0, lengths[0][0], lengths[0][0] + lengths[1][0]], dtype=torch.int32))
+        s2.kv_len.copy_(torch.tensor([t for _, t in lengths], dtype=torch.int32))
+        s2.out.fill_(9.0)
+        g2.replay()
+        s2.check(lengths)
