@@ -1,117 +1,106 @@
 // Softmax attention of new rows over the paged KV cache (fak_paged_attn).
 //
-// One warp per (row, query head): each lane holds dh / 32 neighbouring dims of q and
-// of the output, a score is one warp sum, and the softmax runs along the keys with
-// the running maximum and sum.  Only positions that the row sees are read.
+// The call's checks, the cut of its keys into pieces where there are few rows, and the kernel that
+// joins the pieces.  The attention itself: attn_tile.cu.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
+#include "attn_device.cuh"
 #include "fak.h"
 #include "fak_device.cuh"
-#include "kv_device.cuh"
 
 namespace {
 
 __device__ int g_attn_status;
 
-struct AttnParams {
-  KvView c;
-  const __nv_bfloat16* q;
-  const float* gate;
-  __nv_bfloat16* out;
-  int64_t q_row, q_head, gate_row, gate_head, out_row, out_head;
-  float scale;
-  int nq, window, sinks;
-};
+constexpr int kPlanSms = 152;  // GB300's SMs: the workspace's size must not depend on the current device
 
-template <int N, int KIND>
-FAK_DEV void load_vector(const uint8_t* codes, const float* scales, int64_t at, int lane, float (&x)[N]) {
-  if constexpr (KIND == FAK_KV_BF16) {
-    const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(codes) + at * (32 * N) + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __bfloat162float(p[i]);
-  } else {
-    const uint8_t* p = codes + at * (32 * N) + lane * N;
-    const float s = scales[at];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (KIND == FAK_KV_E4M3)
-        x[i] = half_bits_to_float(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3).x) * s;
-      else
-        x[i] = (float)(int8_t)p[i] * s;
-    }
-  }
-}
-
-template <int DH, int KIND>
-__global__ void __launch_bounds__(256) attn_kernel(const __grid_constant__ AttnParams p) {
+// Adds up the pieces of the blocks of rows whose keys were cut: one warp per (row, query head).
+//   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i * sigmoid(gate),  M = max m_i
+// in the pieces' order, so the result does not depend on which finished first.
+template <int DH>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int N = DH / 32;
   const int lane = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int64_t row = blockIdx.x;
   if (h >= p.nq) return;
   const int s = kv_find_seq(p.c, row, lane);
   const KvSeq sq = kv_seq(p.c, s);
-  if (!sq.ok) {
-    if (lane == 0) atomicCAS(&g_attn_status, 0, FAK_ERR_DEVICE);
-    return;
+  if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
+  const int64_t r = (row - sq.r0) * p.group + h % p.group, total = (int64_t)(sq.r1 - sq.r0) * p.group;
+  const int64_t base = r / kTileM * kTileM, last = min(base + kTileM, total) - 1;
+  const int p0 = sq.len - (sq.r1 - sq.r0);
+  const KeyTiles kt = key_tiles(p0 + (int)(base / p.group), p0 + (int)(last / p.group), p.window, p.sinks);
+  if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
+  const int pos = p0 + (int)(row - sq.r0), pieces = min(p.splits, ceil_div(kt.n, p.per_split));
+  const int64_t slot = row * p.nq + h, step = p.c.rows * p.nq;
+  float top = -INFINITY;
+  for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.stat[slot + i * step].x);
+  const float zero = top == -INFINITY ? 0.0f : top;
+  float o[N] = {}, l = 0.0f;
+  for (int i = 0; i < pieces; ++i) {
+    const float2 st = p.stat[slot + i * step];
+    const float f = exp2f(st.x - zero);
+    l = fmaf(f, st.y, l);
+    const float* x = p.part + (slot + i * step) * DH + lane * N;
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[k], o[k]);
   }
-  if (row < sq.r0 || row >= sq.r1) return;
-  const int pos = sq.len - (sq.r1 - (int)row), g = h / (p.nq / p.c.n_kv);
-  float q[N], o[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = __bfloat162float(p.q[row * p.q_row + h * p.q_head + lane * N + i]);
-    o[i] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const int low = p.window ? max(0, pos - p.window + 1) : 0;
-  for (int j = min(p.sinks, low) ? 0 : low; j <= pos; ++j) {
-    if (j < low && j >= p.sinks) j = low;
-    int64_t at = kv_place(p.c, s, j, g);
-    if (at < 0) {
-      if (lane == 0) atomicCAS(&g_attn_status, 0, FAK_ERR_DEVICE);
-      at = -1 - at;
-    }
-    float x[N], d = 0.0f;
-    load_vector<N, KIND>(p.c.k, p.c.ks, at, lane, x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) d = fmaf(q[i], x[i], d);
-#pragma unroll
-    for (int b = 16; b > 0; b >>= 1) d += __shfl_xor_sync(0xffffffffu, d, b);
-    d *= p.scale;
-    const float top = fmaxf(m, d), base = top == -INFINITY ? 0.0f : top;  // all scores so far -inf: weights 0
-    const float was = expf(m - base), w = expf(d - base);
-    l = l * was + w;
-    load_vector<N, KIND>(p.c.v, p.c.vs, at, lane, x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(w, x[i], o[i] * was);
-    m = top;
-  }
-  const float r = pos < 0 ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float y = o[i] * r;
-    if (p.gate) y = y / (1.0f + expf(-p.gate[row * p.gate_row + h * p.gate_head + lane * N + i]));
-    if (pos < 0) y = 0.0f;
-    p.out[row * p.out_row + h * p.out_head + lane * N + i] = __float2bfloat16_rn(y);
+  for (int k = 0; k < N; ++k) {
+    float y = o[k] / l;
+    if (p.gate) y /= 1.0f + expf(-p.gate[row * p.gate_row + h * p.gate_head + lane * N + k]);
+    p.out[row * p.out_row + h * p.out_head + lane * N + k] = __float2bfloat16_rn(pos < 0 ? 0.0f : y);
   }
 }
 
-template <int DH>
-cudaError_t launch_attn(int kind, const AttnParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)p.c.rows, (unsigned)((p.nq + 7) / 8));
-  if (kind == FAK_KV_BF16)
-    attn_kernel<DH, FAK_KV_BF16><<<grid, 256, 0, s>>>(p);
-  else if (kind == FAK_KV_E4M3)
-    attn_kernel<DH, FAK_KV_E4M3><<<grid, 256, 0, s>>>(p);
-  else
-    attn_kernel<DH, FAK_KV_I8><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+// How a call's keys are cut.
+struct Plan {
+  int64_t blocks;  // blocks of rows of one KV head, at most
+  int splits, per_split;
+};
+
+Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args* a, int sms) {
+  Plan pl;
+  const int group = a->nq / c->n_kv;
+  // blocks by row count (see find_unit), or by every sequence having max_q rows
+  pl.blocks = a->rows * group / kTileM + b->n_seqs;
+  int64_t tiles = ((int64_t)a->max_kv + kTileN - 1) / kTileN;
+  if (a->window) {
+    const int64_t span = (kTileM + group - 1) / group;
+    tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / kTileN + 2 +
+                                         std::min<int64_t>((int64_t)a->sinks / kTileN + 1, tiles));
+  }
+  tiles = std::max<int64_t>(tiles, 1);
+  // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each
+  // as long as a piece and about three tiles' time to begin and to end; a cut costs two more for the join.
+  const int64_t busy = std::min<int64_t>(pl.blocks, (int64_t)b->n_seqs * (((int64_t)a->max_q * group + kTileM - 1) / kTileM));
+  int64_t best = -1;
+  pl.splits = 1;
+  pl.per_split = (int)tiles;
+  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+    const int64_t per = (tiles + s - 1) / s, n = (tiles + per - 1) / per;
+    const int64_t cost = (busy * c->n_kv * n + sms - 1) / sms * (per + 3) + (n > 1 ? 2 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.splits = (int)n;
+      pl.per_split = (int)per;
+    }
+  }
+  return pl;
+}
+
+// Workspace: the pieces' sums, then their bases and weight sums.
+size_t part_bytes(const fak_kv_cache* c, const fak_attn_args* a, const Plan& pl) {
+  return pl.splits < 2 ? 0 : (size_t)pl.splits * a->rows * a->nq * c->dh * 4;
+}
+size_t stat_bytes(const fak_attn_args* a, const Plan& pl) {
+  return pl.splits < 2 ? 0 : (size_t)pl.splits * a->rows * a->nq * 8;
 }
 
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
@@ -126,8 +115,9 @@ int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
 
 extern "C" size_t fak_paged_attn_workspace_bytes(const fak_kv_cache* cache, const fak_kv_batch* batch,
                                                  const fak_attn_args* a) {
-  if (!cache || !batch || !a) return 0;
-  return 0;
+  if (!cache || !batch || !a || cache->n_kv < 1 || batch->n_seqs < 0 || attn_shape(cache, a) != FAK_OK) return 0;
+  const Plan pl = make_plan(cache, batch, a, kPlanSms);
+  return part_bytes(cache, a, pl) + stat_bytes(a, pl);
 }
 
 extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_attn_args* a,
@@ -142,12 +132,16 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
       ((a->q_row | a->q_head | a->out_row | a->out_head) & 7) || (a->gate && ((a->gate_row | a->gate_head) & 3)) ||
       ((uintptr_t)a->workspace & 255))
     return FAK_ERR_ALIGN;
-  const size_t need = fak_paged_attn_workspace_bytes(cache, batch, a);
+  const Plan pl = make_plan(cache, batch, a, kPlanSms);
+  const size_t parts = part_bytes(cache, a, pl), need = parts + stat_bytes(a, pl);
   if (need && !a->workspace) return FAK_ERR_INVALID_ARG;
   if (a->workspace_bytes < need) return FAK_ERR_SHAPE;
+  if (pl.blocks > 0x7fffffff || cache->n_kv > 65535) return FAK_ERR_SHAPE;
   if (a->rows == 0 || batch->n_seqs == 0) return FAK_OK;
-  int sms = 0;
-  if ((st = kv_device(&sms)) != FAK_OK) return st;
+  if ((st = kv_device(nullptr)) != FAK_OK) return st;
+  void* status = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&status, g_attn_status);
+  if (e != cudaSuccess) return fak_cuda_status(e);
   p.c.rows = a->rows;
   p.c.max_q = a->max_q;
   p.c.max_kv = a->max_kv;
@@ -160,14 +154,29 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.gate_head = a->gate_head;
   p.out_row = a->out_row;
   p.out_head = a->out_head;
-  p.scale = a->scale;
+  p.scale = a->scale * 1.4426950408889634f;
   p.nq = a->nq;
+  p.group = a->nq / cache->n_kv;
   p.window = a->window;
   p.sinks = a->window ? a->sinks : 0;
+  p.splits = pl.splits;
+  p.per_split = pl.per_split;
+  p.part = static_cast<float*>(a->workspace);
+  p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + parts);
+  p.timeout_ns = 2000000000ull;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = cache->dh == 64    ? launch_attn<64>(cache->kind, p, s)
-                        : cache->dh == 128 ? launch_attn<128>(cache->kind, p, s)
-                                           : launch_attn<256>(cache->kind, p, s);
+  e = attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p, pl.blocks,
+                       static_cast<int*>(status), s);
+  if (e == cudaSuccess && pl.splits > 1) {
+    const dim3 grid((unsigned)a->rows, (unsigned)((a->nq + 7) / 8));
+    if (cache->dh == 64)
+      attn_join_kernel<64><<<grid, 256, 0, s>>>(p);
+    else if (cache->dh == 128)
+      attn_join_kernel<128><<<grid, 256, 0, s>>>(p);
+    else
+      attn_join_kernel<256><<<grid, 256, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
   return fak_cuda_status(e);
 }
 
