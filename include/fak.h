@@ -445,7 +445,7 @@ void fak_prefill_destroy(fak_prefill* ctx);
  * In the 8-bit kinds a vector with a < 2^-100 is held as zeros, and one that
  * holds a NaN or an infinity reads back as NaN in every element.
  * dh is 64, 128 or 256; page is 16, 32, 64, 128 or 256 tokens; n_pages * n_kv *
- * page < 2^31; codes 16-byte aligned.  The memory is the caller's.
+ * page < 2^31; codes and scales 16-byte aligned.  The memory is the caller's.
  */
 enum { FAK_KV_BF16 = 0, FAK_KV_E4M3 = 1, FAK_KV_I8 = 2 };
 enum { FAK_ROWS_F32 = 0, FAK_ROWS_BF16 = 1 };

@@ -8,21 +8,26 @@
 //
 //   warps 0-7      softmax: warp w and w + 4 share rows 32 (w % 4) .. +31, half of the keys each
 //   warp 8         MMA issuer and TMEM owner
-//   warps 9 ...    producers: Q, then K and V in 16 KB stages of a ring, in the order the MMAs take them
+//   warp 9         TMA: K and V by pages in 16 KB stages of a ring, in the order the MMAs take them
 //                  (K 0, K 1, V 0, K 2, V 1, ...), in the 128-byte-swizzled layouts the MMAs read: Q and K
 //                  64 dims wide with the dims running (K-major), V keys by dims as stored (MN-major)
+//   warps 10-13    Q's rows; then, for an 8-bit cache, codes to bf16: the copies land in a ring of their own and
+//                  these warps fill the MMAs' ring from it; for a bf16 cache, V of the tiles that a mask cuts
 // S has two or three buffers, so the next tile's S = Q K^T runs while the softmax works.
-// Cached 8-bit codes become bf16 exactly on their way into shared memory; their scales multiply the scores' columns
-// and the weights instead.  What lies past the last row's position is zeros in shared memory, and in the tiles
-// that a mask cuts so are values that are not finite: a weight of zero times them would be NaN.  Rows that do see such a
-// value get it added at the end.
+// 8-bit codes become bf16 exactly; their scales multiply the scores' columns and the weights instead.
+// A weight of zero times a value that is not finite would be NaN, so in the tiles that a mask cuts a bf16 V is
+// mended in shared memory: keys past the last row's position are made zeros, and so are values that are not
+// finite, which the rows that do see them get added at the end.  (Codes are always finite, and a weight of zero is not
+// multiplied by a scale.)  Scores of masked keys are replaced, whatever they are.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "attn_device.cuh"
 #include "fak.h"
@@ -32,7 +37,8 @@
 namespace {
 
 constexpr int kStageBytes = 16384;
-constexpr int kSlots = 8;  // tiles whose scales are held at once (8-bit caches)
+constexpr int kSlots = 16;  // tiles whose scales are held at once (8-bit caches): more than the rings hold
+constexpr int kRawBytes = kStageBytes / 2;
 
 template <int DH, int KIND>
 struct Cfg {
@@ -40,14 +46,15 @@ struct Cfg {
   static constexpr int chunks = DH / 64;             // stages of one tile of K or of V
   static constexpr int vkeys = 8192 / DH;            // keys of one V stage
   static constexpr int sbufs = DH == 256 ? 2 : 3;    // S buffers: 512 TMEM columns, less O's
-  static constexpr int stages = DH == 256 ? 9 : DH == 128 ? 11 : 8;
-  static constexpr int prod_warps = quant ? 8 : 4;
-  static constexpr int threads = (9 + prod_warps) * 32;
+  static constexpr int stages = quant ? (DH == 256 ? 6 : 8) : DH == 256 ? 9 : DH == 128 ? 11 : 12;
+  static constexpr int raw = !quant ? 0 : DH == 64 ? 6 : 5;  // stages of codes on their way to bf16
+  static constexpr int threads = 14 * 32;
   static constexpr int off_ring = kTileM * DH * 2;
-  static constexpr int off_scales = off_ring + stages * kStageBytes;
+  static constexpr int off_raw = off_ring + stages * kStageBytes;
+  static constexpr int off_scales = off_raw + raw * kRawBytes;
   static constexpr int off_red = off_scales + (quant ? kSlots * 2 * kTileN * 4 : 0);
   static constexpr int off_bar = off_red + 2 * 2 * kTileM * 4;
-  static constexpr int smem = off_bar + 512 + 1024;
+  static constexpr int smem = off_bar + 640 + 1024;
   static_assert(smem <= 232448 - 1024, "shared memory exceeds the 227 KB per-block limit");
 };
 
@@ -168,7 +175,8 @@ FAK_DEV void find_unit(const AttnParams& p, int64_t x, int split, int lane, Unit
 
 template <int DH, int KIND>
 __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
-    attn_tile_kernel(const __grid_constant__ AttnParams p, int* status) {
+    attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, int* status) {
   using C = Cfg<DH, KIND>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -176,18 +184,21 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
   float* red = reinterpret_cast<float*>(smem + C::off_red);        // [parity][half][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::off_bar);
   uint64_t* empty = full + C::stages;
-  uint64_t* sfull = empty + C::stages;
+  uint64_t* clean = empty + C::stages;  // bf16: the stage's V has landed and is to be mended
+  uint64_t* rfull = clean + (C::quant ? 0 : C::stages);
+  uint64_t* rempty = rfull + C::raw;
+  uint64_t* scfull = rempty + C::raw;
+  uint64_t* sfull = scfull + (C::quant ? kSlots : 0);
   uint64_t* pfull = sfull + 3;
   uint64_t* odone = pfull + 3;
-  uint64_t* scfull = odone + 2;
-  uint64_t* pair = scfull + kSlots;
+  uint64_t* pair = odone + 2;
   uint64_t* qfull = pair + 4;
   uint64_t* pdone = qfull + 1;
   uint64_t* drain = pdone + 1;
-  static_assert((2 * C::stages + 3 + 3 + 2 + kSlots + 4 + 3) * 8 + 16 <= 512, "barriers exceed their area");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 496);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 500);
-  volatile int* odd = reinterpret_cast<volatile int*>(smem + C::off_bar + 504);
+  static_assert((3 * C::stages + 2 * C::raw + kSlots + 3 + 3 + 2 + 4 + 3) * 8 <= 624, "barriers exceed their area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 624);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 628);
+  volatile int* odd = reinterpret_cast<volatile int*>(smem + C::off_bar + 632);
   __shared__ Unit unit;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,18 +208,23 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
     if (lane == 0) unit = u;
   } else if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::stages; ++s) {
-      mbar_init(&full[s], C::prod_warps);
+      mbar_init(&full[s], 4);
       mbar_init(&empty[s], 1);
+      if (!C::quant) mbar_init(&clean[s], 1);
     }
+    for (int s = 0; s < C::raw; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], 4);
+    }
+    for (int s = 0; s < (C::quant ? kSlots : 0); ++s) mbar_init(&scfull[s], 1);
     for (int s = 0; s < 3; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 8);
     }
     for (int s = 0; s < 2; ++s) mbar_init(&odone[s], 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&scfull[s], C::prod_warps);
     for (int s = 0; s < 4; ++s) mbar_init(&pair[s], 2);
-    mbar_init(qfull, C::prod_warps);
-    mbar_init(pdone, C::prod_warps);
+    mbar_init(qfull, 4);
+    mbar_init(pdone, 4);
     mbar_init(drain, 1);
     *abort = 0;
     *odd = 0;
@@ -237,12 +253,14 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
   const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
   const int n = u.n, g = blockIdx.y;
   const uint64_t tmo = p.timeout_ns;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
+  auto wait_one = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait_bounded(bar, parity, abort, tmo)) return true;
     if (!*abort) attn_record(status, FAK_ERR_TIMEOUT);
     *abort = 1;
     return false;
   };
+  // a whole warp waits: it goes on or gives up as one
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_one(bar, parity)); };
 
   if (warp < 8) {
     // ---------------- softmax
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pair[quarter]);
         if (!(ok = wait(&pair[quarter], i & 1))) break;
-        mx = fmaxf(mx, mine[(half ^ 1) * kTileM + row]) * (C::quant ? 1.0f : p.scale);
+        mx = fmaxf(mx, mine[(half ^ 1) * kTileM + row]) * p.scale;
         // a new base when the maximum passed it by 8, or is the first one seen
         const bool up = mx > m + 8.0f;
         if (__any_sync(0xffffffffu, up)) {
@@ -312,8 +330,8 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 64; k += 2) {
-          const float a = exp2_approx(C::quant ? t[k] - base : fmaf(t[k], p.scale, -base));
-          const float c = exp2_approx(C::quant ? t[k + 1] - base : fmaf(t[k + 1], p.scale, -base));
+          const float a = exp2_approx(fmaf(t[k], p.scale, -base));
+          const float c = exp2_approx(fmaf(t[k + 1], p.scale, -base));
           sum[0] += a;
           sum[1] += c;
           if constexpr (C::quant) {
@@ -420,9 +438,9 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
       const uint32_t ring = smem_u32(smem + C::off_ring);
       const uint64_t qdesc = umma_desc_sw128(smem_u32(smem));
       int it = 0;
-      bool ok = wait(qfull, 0);
+      bool ok = wait_one(qfull, 0);
       auto take = [&]() {  // the next stage, once it is full
-        ok = ok && wait(&full[it % C::stages], (it / C::stages) & 1);
+        ok = ok && wait_one(&full[it % C::stages], (it / C::stages) & 1);
         tc_fence_after_sync();
         return ok;
       };
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
       };
       for (int i = 0; i < min(C::sbufs, n) && ok; ++i) scores(i);
       for (int i = 0; i < n && ok; ++i) {
-        if (!(ok = wait(&pfull[i % C::sbufs], (i / C::sbufs) & 1))) break;
+        if (!(ok = wait_one(&pfull[i % C::sbufs], (i / C::sbufs) & 1))) break;
         const uint32_t a = tmem_s + (uint32_t)((i % C::sbufs) * kTileN);
         for (int c = 0; c < C::chunks; ++c, ++it) {
           if (!take()) break;
@@ -465,10 +483,102 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
           if (globaltimer_ns() - t0 > 200000000ull) break;
       }
     }
+  } else if (warp == 9) {
+    // ---------------- TMA: every lane waits; the lanes share a stage's boxes
+    const int page = 1 << p.c.page_shift;
+    const int krows = min(page, kTileN), vrows = min(page, C::vkeys);  // the maps' boxes
+    const int kboxes = kTileN / krows, vsub = C::vkeys / vrows;
+    int it = 0, sc = 0;
+    bool ok = true;
+    // the vector index of key j0 + lane * krows, at the tile's start; keys past the last that a row sees
+    // take its page: what lies there is masked
+    auto places = [&](int i) {
+      const int j = min(key_tile(u.kt, u.begin + i) * kTileN + min(lane, kboxes - 1) * krows, u.p_hi & ~(krows - 1));
+      int64_t at = kv_place(p.c, u.seq, j, g);
+      if (at < 0) {
+        attn_record(status, FAK_ERR_DEVICE);
+        at = -1 - at;
+      }
+      return (int)at;
+    };
+    auto stage = [&](uint8_t*& dst, uint64_t*& bar, bool mend) {  // the next stage, once it is free
+      constexpr int S = C::quant ? C::raw : C::stages;
+      uint64_t* free = C::quant ? rempty : empty;
+      const int st = it % S;
+      if (it >= S) ok = ok && wait(&free[st], ((it / S) - 1) & 1);
+      dst = smem + (C::quant ? C::off_raw + st * kRawBytes : C::off_ring + st * kStageBytes);
+      bar = C::quant ? &rfull[st] : mend ? &clean[st] : &full[st];
+      if (ok && lane == 0) mbar_arrive_expect_tx(bar, C::quant ? kRawBytes : kStageBytes);
+      if (ok && !C::quant && !mend && lane > 0 && lane < 4) mbar_arrive(bar);  // in place of four mending warps
+      __syncwarp();
+    };
+    constexpr int kw = C::quant ? 64 : 128;  // bytes of a K stage's row
+    auto keys = [&](int i, int at) {
+      uint8_t* dst;
+      uint64_t* bar;
+      if constexpr (C::quant) {
+        const int slot = i % kSlots;
+        float* to = scales + slot * 2 * kTileN + lane * krows;
+        if (lane == 0) mbar_arrive_expect_tx(&scfull[slot], 2 * kTileN * 4);
+        __syncwarp();
+        if (lane < kboxes) {
+          bulk_g2s_nohint(to, p.c.ks + at, krows * 4, &scfull[slot]);
+          bulk_g2s_nohint(to + kTileN, p.c.vs + at, krows * 4, &scfull[slot]);
+        }
+        ++sc;
+      }
+      for (int c = 0; c < C::chunks && ok; ++c, ++it) {
+        stage(dst, bar, false);
+        if (!ok) return;
+        if (lane < kboxes) tma_load_2d_tx(dst + lane * krows * kw, &kmap, c * 64, at, bar);
+      }
+    };
+    auto values = [&](int i, int at) {
+      const bool mend = !C::quant && tile_cut(u, key_tile(u.kt, u.begin + i), p.window, p.sinks);
+      uint8_t* dst;
+      uint64_t* bar;
+      for (int c = 0; c < C::chunks && ok; ++c, ++it) {
+        stage(dst, bar, mend);
+        if (!ok) return;
+        // box (d, r): 64 dims (bf16) or all (codes), keys c * vkeys + r * vrows .. + vrows - 1
+        const int r = lane % vsub, d = lane / vsub, key = c * C::vkeys + r * vrows;
+        const int row = __shfl_sync(0xffffffffu, at, key / krows) + (key & (krows - 1));
+        if (C::quant) {
+          if (d == 0) tma_load_2d_tx(dst + r * vrows * DH, &vmap, 0, row, bar);
+        } else if (d < DH / 64) {
+          tma_load_2d_tx(dst + d * C::vkeys * 128 + r * vrows * 128, &vmap, d * 64, row, bar);
+        }
+      }
+    };
+    // the places of a tile's keys stay in a register of each lane until its values are loaded
+    int at[4];
+    int ahead = n > 0 ? places(0) : 0;  // the next tile's, loaded early
+    auto next_keys = [&](int i) {
+      at[i & 3] = ahead;
+      if (i + 1 < n) ahead = places(i + 1);
+      keys(i, i & 2 ? (i & 1 ? at[3] : at[2]) : (i & 1 ? at[1] : at[0]));
+    };
+    for (int i = 0; i < min(C::sbufs, n) && ok; ++i) next_keys(i);
+    for (int i = 0; i < n && ok; ++i) {
+      values(i, i & 2 ? (i & 1 ? at[3] : at[2]) : (i & 1 ? at[1] : at[0]));
+      if (ok && i + C::sbufs < n) next_keys(i + C::sbufs);
+    }
+    // copies in flight land before the block can end
+    constexpr int S = C::quant ? C::raw : C::stages;
+    for (int q = max(0, it - S); q < it; ++q) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(C::quant ? &rfull[q % S] : &full[q % S], (q / S) & 1))
+        if (globaltimer_ns() - t0 > 200000000ull) break;
+    }
+    for (int q = max(0, sc - kSlots); q < sc; ++q) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&scfull[q % kSlots], (q / kSlots) & 1))
+        if (globaltimer_ns() - t0 > 200000000ull) break;
+    }
   } else {
-    // ---------------- producers
-    constexpr int T = C::prod_warps * 32;
-    const int tid = threadIdx.x - 9 * 32;
+    // ---------------- Q, codes to bf16, V of cut tiles
+    constexpr int T = 128;
+    const int tid = threadIdx.x - 10 * 32;
     bool ok = true;
     // Q: rows of the block, 64 dims to a 16 KB panel; rows past the block's are zeros
     for (int k = tid; k < kTileM * DH / 8; k += T) {
@@ -484,57 +594,28 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(qfull);
-    auto place = [&](int j) {  // vector index of key j, which some row sees
-      int64_t at = kv_place(p.c, u.seq, j, g);
-      if (at < 0) {
-        attn_record(status, FAK_ERR_DEVICE);
-        at = -1 - at;
-      }
-      return at;
-    };
-    int it = 0;
-    auto put = [&](bool value, int i) {
-      const int tile = key_tile(u.kt, u.begin + i), j0 = tile * kTileN;
-      if constexpr (C::quant) {
-        const uint8_t* src = value ? p.c.v : p.c.k;
-        if (!value) {
-          // the tile's scales: the keys' with the scores' factor in them
-          for (int k = tid; k < 2 * kTileN; k += T) {
-            const int j = j0 + (k & (kTileN - 1));
-            float x = 0.0f;
-            if (j <= u.p_hi) x = k < kTileN ? p.c.ks[place(j)] * p.scale : p.c.vs[place(j)];
-            scales[(i % kSlots) * 2 * kTileN + k] = x;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&scfull[i % kSlots]);
-        }
-        // 16 codes to a thread and step: keys of 64 dims (K) or of all dims (V)
-        const int width = value ? DH / 16 : 4;
-        constexpr int steps = 512 / T;
-        uint4 x[C::chunks * steps];
-#pragma unroll
-        for (int c = 0; c < C::chunks; ++c)
-#pragma unroll
-          for (int k = 0; k < steps; ++k) {
-            const int e = tid + k * T, key = e / width + (value ? c * C::vkeys : 0), j = j0 + key;
-            x[c * steps + k] = make_uint4(0, 0, 0, 0);
-            if (j <= u.p_hi)
-              x[c * steps + k] = *reinterpret_cast<const uint4*>(src + place(j) * DH + (value ? 0 : c * 64) + (e % width) * 16);
-          }
-#pragma unroll
+    if constexpr (C::quant) {
+      int it = 0;
+      auto convert = [&](bool value) {
+        const int width = value ? DH / 16 : 4;  // 16 codes to a thread and step
         for (int c = 0; c < C::chunks; ++c, ++it) {
-          if (ok && it >= C::stages) ok = wait(&empty[it % C::stages], ((it / C::stages) - 1) & 1);
+          const int rs = it % C::raw, st = it % C::stages;
+          ok = ok && wait(&rfull[rs], (it / C::raw) & 1);
+          if (ok && it >= C::stages) ok = wait(&empty[st], ((it / C::stages) - 1) & 1);
           if (!ok) return;
-          uint8_t* dst = smem + C::off_ring + (it % C::stages) * kStageBytes;
+          const uint4* src = reinterpret_cast<const uint4*>(smem + C::off_raw + rs * kRawBytes);
+          uint8_t* dst = smem + C::off_ring + st * kStageBytes;
+          uint4 q[4];
 #pragma unroll
-          for (int k = 0; k < steps; ++k) {
+          for (int k = 0; k < 4; ++k) q[k] = src[tid + k * T];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
             const int e = tid + k * T, key = e / width, d = (e % width) * 16;
-            const uint4 q = x[c * steps + k];
             uint4 a, b;
-            codes_to_bf16<KIND>(q.x, a.x, a.y);
-            codes_to_bf16<KIND>(q.y, a.z, a.w);
-            codes_to_bf16<KIND>(q.z, b.x, b.y);
-            codes_to_bf16<KIND>(q.w, b.z, b.w);
+            codes_to_bf16<KIND>(q[k].x, a.x, a.y);
+            codes_to_bf16<KIND>(q[k].y, a.z, a.w);
+            codes_to_bf16<KIND>(q[k].z, b.x, b.y);
+            codes_to_bf16<KIND>(q[k].w, b.z, b.w);
             uint8_t* line = dst + (value ? (d >> 6) * C::vkeys * 128 : 0) + key * 128;
             const int e16 = (d & 63) >> 3;
             *reinterpret_cast<uint4*>(line + ((e16 ^ (key & 7)) << 4)) = a;
@@ -542,49 +623,50 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[it % C::stages]);
-        }
-      } else {
-        const bool cut = tile_cut(u, tile, p.window, p.sinks);
-        for (int c = 0; c < C::chunks; ++c, ++it) {
-          const int width = value ? DH / 8 : 8;
-          uint4 x[1024 / T];
-#pragma unroll
-          for (int k = 0; k < 1024 / T; ++k) {
-            const int e = tid + k * T, j = j0 + e / width + (value ? c * C::vkeys : 0);
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (j <= u.p_hi)
-              x[k] = *reinterpret_cast<const uint4*>((value ? p.c.v : p.c.k) + (place(j) * DH + (value ? 0 : c * 64)) * 2 +
-                                                     (e % width) * 16);
+          if (lane == 0) {
+            mbar_arrive(&full[st]);
+            mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
           }
-          if (ok && it >= C::stages) ok = wait(&empty[it % C::stages], ((it / C::stages) - 1) & 1);
-          if (!ok) return;
-          uint8_t* dst = smem + C::off_ring + (it % C::stages) * kStageBytes;
+        }
+      };
+      for (int i = 0; i < min(C::sbufs, n) && ok; ++i) convert(false);
+      for (int i = 0; i < n && ok; ++i) {
+        convert(true);
+        if (ok && i + C::sbufs < n) convert(false);
+      }
+    } else {
+      uint32_t landed = 0;  // parity of each stage's next use of `clean`
+      for (int i = 0; i < n && ok; ++i) {
+        const int tile = key_tile(u.kt, u.begin + i);
+        if (!tile_cut(u, tile, p.window, p.sinks)) continue;
+        int it = (i + min(C::sbufs + i, n)) * C::chunks;  // V i comes after that many tiles
+        for (int c = 0; c < C::chunks && ok; ++c, ++it) {
+          const int st = it % C::stages;
+          if (!(ok = wait(&clean[st], (landed >> st) & 1))) break;
+          landed ^= 1u << st;
+          uint4* v = reinterpret_cast<uint4*>(smem + C::off_ring + st * kStageBytes);
           bool bad = false;
 #pragma unroll
-          for (int k = 0; k < 1024 / T; ++k) {
-            const int e = tid + k * T, key = e / width, e16 = e % width;
-            uint4 y = x[k];
-            if (value && cut) {
-              y.x = finite2(y.x, bad);
-              y.y = finite2(y.y, bad);
-              y.z = finite2(y.z, bad);
-              y.w = finite2(y.w, bad);
-            }
-            *reinterpret_cast<uint4*>(dst + (value ? (e16 >> 3) * C::vkeys * 128 : 0) + key * 128 +
-                                      (((e16 & 7) ^ (key & 7)) << 4)) = y;
+          for (int k = 0; k < 8; ++k) {
+            const int e = tid + k * T, j = tile * kTileN + c * C::vkeys + (e >> 3) % C::vkeys;
+            bool change = false;
+            uint4 y = v[e];
+            y.x = finite2(y.x, change);
+            y.y = finite2(y.y, change);
+            y.z = finite2(y.z, change);
+            y.w = finite2(y.w, change);
+            if (j > u.p_hi)
+              v[e] = make_uint4(0, 0, 0, 0);
+            else if (change)
+              v[e] = y;
+            bad |= change && j <= u.p_hi;
           }
           if (bad) *odd = 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[it % C::stages]);
+          if (lane == 0) mbar_arrive(&full[st]);
         }
       }
-    };
-    for (int i = 0; i < min(C::sbufs, n) && ok; ++i) put(false, i);
-    for (int i = 0; i < n && ok; ++i) {
-      put(true, i);
-      if (ok && i + C::sbufs < n) put(false, i + C::sbufs);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(pdone);
@@ -597,29 +679,61 @@ __global__ void __launch_bounds__(Cfg<DH, KIND>::threads, 1)
   }
 }
 
+std::mutex g_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+cudaError_t encoder() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_encode) return cudaSuccess;
+  cudaDriverEntryPointQueryResult q;
+  void* fn = nullptr;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+  g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return cudaSuccess;
+}
+
+// Codes as rows of dh values, one to a vector; boxes of `width` values and `rows` vectors of one page.
+bool code_map(CUtensorMap* map, void* base, bool quant, int dh, int64_t n_vec, int width, int rows) {
+  memset(map, 0, sizeof(*map));
+  const cuuint64_t dim[2] = {(cuuint64_t)dh, (cuuint64_t)n_vec};
+  const cuuint64_t stride[1] = {(cuuint64_t)dh * (quant ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows}, one[2] = {1, 1};
+  return g_encode(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dim, stride,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DH, int KIND>
-cudaError_t launch(const AttnParams& p, int64_t blocks, int* status, cudaStream_t s) {
+cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status, cudaStream_t s) {
   using C = Cfg<DH, KIND>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_tile_kernel<DH, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  cudaError_t e = encoder();
+  if (e != cudaSuccess) return e;
+  CUtensorMap kmap, vmap;
+  if (!code_map(&kmap, p.c.k, C::quant, DH, n_vec, 64, std::min(page, kTileN)) ||
+      !code_map(&vmap, p.c.v, C::quant, DH, n_vec, C::quant ? DH : 64, std::min(page, C::vkeys)))
+    return cudaErrorInvalidValue;
+  e = cudaFuncSetAttribute(attn_tile_kernel<DH, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)blocks, (unsigned)p.c.n_kv, (unsigned)p.splits);
-  attn_tile_kernel<DH, KIND><<<grid, C::threads, C::smem, s>>>(p, status);
+  attn_tile_kernel<DH, KIND><<<grid, C::threads, C::smem, s>>>(p, kmap, vmap, status);
   return cudaGetLastError();
 }
 
 template <int DH>
-cudaError_t by_kind(int kind, const AttnParams& p, int64_t blocks, int* status, cudaStream_t s) {
-  return kind == FAK_KV_BF16   ? launch<DH, FAK_KV_BF16>(p, blocks, status, s)
-         : kind == FAK_KV_E4M3 ? launch<DH, FAK_KV_E4M3>(p, blocks, status, s)
-                               : launch<DH, FAK_KV_I8>(p, blocks, status, s);
+cudaError_t by_kind(int kind, const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status,
+                    cudaStream_t s) {
+  return kind == FAK_KV_BF16   ? launch<DH, FAK_KV_BF16>(p, page, n_vec, blocks, status, s)
+         : kind == FAK_KV_E4M3 ? launch<DH, FAK_KV_E4M3>(p, page, n_vec, blocks, status, s)
+                               : launch<DH, FAK_KV_I8>(p, page, n_vec, blocks, status, s);
 }
 
 }  // namespace
 
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
                              int* status, cudaStream_t s) {
-  return dh == 64    ? by_kind<64>(kind, p, blocks, status, s)
-         : dh == 128 ? by_kind<128>(kind, p, blocks, status, s)
-                     : by_kind<256>(kind, p, blocks, status, s);
+  return dh == 64    ? by_kind<64>(kind, p, page, n_vec, blocks, status, s)
+         : dh == 128 ? by_kind<128>(kind, p, page, n_vec, blocks, status, s)
+                     : by_kind<256>(kind, p, page, n_vec, blocks, status, s);
 }

@@ -72,7 +72,7 @@ static inline int kv_view(const fak_kv_cache* c, const fak_kv_batch* b, KvView* 
   if (c->n_kv >= (1LL << 31) / c->page / c->n_pages) return FAK_ERR_SHAPE;  // n_pages * n_kv * page < 2^31
   const uintptr_t bits = (uintptr_t)c->k | (uintptr_t)c->v;
   if (bits & 15) return FAK_ERR_ALIGN;
-  if (quant && (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3)) return FAK_ERR_ALIGN;
+  if (quant && (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 15)) return FAK_ERR_ALIGN;
   if (((uintptr_t)b->page_table | (uintptr_t)b->row_start | (uintptr_t)b->kv_len) & 3) return FAK_ERR_ALIGN;
   w->table = b->page_table;
   w->row_start = b->row_start;
