@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const KvSeq sq = kv_seq(p.c, s);
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
   const int64_t r = (row - sq.r0) * p.group + h % p.group, total = (int64_t)(sq.r1 - sq.r0) * p.group;
-  const int64_t base = r / kTileM * kTileM, last = min(base + kTileM, total) - 1;
+  const int64_t base = r / p.block * p.block, last = min(base + p.block, total) - 1;
   const int p0 = sq.len - (sq.r1 - sq.r0);
   const KeyTiles kt = key_tiles(p0 + (int)(base / p.group), p0 + (int)(last / p.group), p.window, p.sinks);
   if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
@@ -62,24 +62,28 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // How a call's keys are cut.
 struct Plan {
   int64_t blocks;  // blocks of rows of one KV head, at most
+  int block;       // rows of a block
   int splits, per_split;
 };
 
 Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args* a, int sms) {
   Plan pl;
   const int group = a->nq / c->n_kv;
-  // blocks by row count (see find_unit), or by every sequence having max_q rows
-  pl.blocks = a->rows * group / kTileM + b->n_seqs;
+  // pairs of CTAs where sequences have more rows than one CTA holds (and a half of V is at least 64 dims)
+  pl.block = c->dh > 64 && (int64_t)a->max_q * group > kTileM ? 2 * kTileM : kTileM;
+  pl.blocks = a->rows * group / pl.block + b->n_seqs;  // see find_unit
   int64_t tiles = ((int64_t)a->max_kv + kTileN - 1) / kTileN;
   if (a->window) {
-    const int64_t span = (kTileM + group - 1) / group;
+    const int64_t span = (pl.block + group - 1) / group;
     tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / kTileN + 2 +
                                          std::min<int64_t>((int64_t)a->sinks / kTileN + 1, tiles));
   }
   tiles = std::max<int64_t>(tiles, 1);
   // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each
   // as long as a piece and about three tiles' time to begin and to end; a cut costs two more for the join.
-  const int64_t busy = std::min<int64_t>(pl.blocks, (int64_t)b->n_seqs * (((int64_t)a->max_q * group + kTileM - 1) / kTileM));
+  const int ctas = pl.block / kTileM;
+  const int64_t each = ((int64_t)a->max_q * group + pl.block - 1) / pl.block;  // blocks of a sequence, at most
+  const int64_t busy = std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas;
   int64_t best = -1;
   pl.splits = 1;
   pl.per_split = (int)tiles;
@@ -136,7 +140,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   const size_t parts = part_bytes(cache, a, pl), need = parts + stat_bytes(a, pl);
   if (need && !a->workspace) return FAK_ERR_INVALID_ARG;
   if (a->workspace_bytes < need) return FAK_ERR_SHAPE;
-  if (pl.blocks > 0x7fffffff || cache->n_kv > 65535) return FAK_ERR_SHAPE;
+  if (pl.blocks > 0x3fffffff || cache->n_kv > 65535) return FAK_ERR_SHAPE;
   if (a->rows == 0 || batch->n_seqs == 0) return FAK_OK;
   if ((st = kv_device(nullptr)) != FAK_OK) return st;
   void* status = nullptr;
@@ -157,6 +161,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.scale = a->scale * 1.4426950408889634f;
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
+  p.block = pl.block;
   p.window = a->window;
   p.sinks = a->window ? a->sinks : 0;
   p.splits = pl.splits;

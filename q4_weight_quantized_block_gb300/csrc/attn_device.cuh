@@ -14,6 +14,7 @@ struct AttnParams {
   int64_t q_row, q_head, gate_row, gate_head, out_row, out_head;
   float scale;  // times log2(e): scores are held in powers of two
   int nq, group, window, sinks;
+  int block;  // rows of a block: 128, or 256 in a pair of CTAs
   // the keys of a block of rows are cut into at most `splits` pieces of `per_split` key tiles; a block with more
   // than one piece leaves, for each piece, row and head, the unnormalised sum (part, dh values) and its base and
   // weight sum (stat), which the join kernel adds up
@@ -23,7 +24,7 @@ struct AttnParams {
   unsigned long long timeout_ns;
 };
 
-constexpr int kTileM = 128;  // rows (token, query head of the group) of a block
+constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA
 constexpr int kTileN = 128;  // keys of a tile
 
 FAK_DEV int ceil_div(int a, int b) { return (a + b - 1) / b; }
