@@ -131,12 +131,18 @@ FAK_DEV uint32_t map_to(const void* p, uint32_t rank) {
   return a;
 }
 
+// Arrives on CTA 0's barrier, for its MMA issuer.  What that reads was written to TMEM or through
+// fence.proxy.async, which order it; a release at cluster scope would wait a thousand cycles for every other store.
 template <int CG>
-FAK_DEV void arrive_at(uint64_t* bar, uint32_t rank) {
+FAK_DEV void arrive_first(uint64_t* bar) {
   if constexpr (CG == 1)
     mbar_arrive(bar);
   else
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, rank)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, 0)) : "memory");
+}
+
+FAK_DEV void arrive_release_cluster(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, rank)) : "memory");
 }
 
 FAK_DEV void cluster_sync() {
@@ -217,28 +223,22 @@ FAK_DEV bool elect_one() {
   return p != 0;
 }
 
-template <int CG>
-FAK_DEV bool try_wait(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  if constexpr (CG == 1) return mbar_try_wait_suspend(bar, parity, hint_ns);
+FAK_DEV bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, "
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
       "p;\n}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
 
 // Bounded wait; the clock, which takes hundreds of cycles to read, only after 64 tries.
-template <int CG>
 FAK_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
   for (int i = 0; i < 64; ++i)
-    if (try_wait<CG>(bar, parity, 20000u)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait<CG>(bar, parity, 20000u))
-    if (*abort || globaltimer_ns() - t0 > timeout_ns) return false;
-  return true;
+    if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
+  return mbar_wait_bounded(bar, parity, abort, timeout_ns);
 }
 
 FAK_DEV bool sees(int pos, int j, int window, int sinks) {
@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   uint64_t* qfull = pair + 4;
   uint64_t* pdone = qfull + 1;
   uint64_t* drain = pdone + 1;
-  static_assert((C::quant ? 2 * C::stages + 2 * C::raw + kSlots : 4 * C::stages) * 8 + 15 * 8 <= 640,
+  uint64_t* tready = drain + 1;
+  static_assert((C::quant ? 2 * C::stages + 2 * C::raw + kSlots : 4 * C::stages) * 8 + 16 * 8 <= 640,
                 "barriers exceed their area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 640);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 644);
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     mbar_init(qfull, 15 * CG);
     mbar_init(pdone, 4 * CG);
     mbar_init(drain, 1);
+    mbar_init(tready, 1);
     *abort = 0;
     *odd = 0;
     fence_mbar_init();
@@ -358,7 +360,11 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     for (int i = lane; i < p.c.n_seqs; i += 32) bad |= !kv_seq(p.c, i).ok;
     if (bad) attn_record(status, FAK_ERR_DEVICE);
   }
-  __syncthreads();
+  __syncwarp();
+  if constexpr (CG == 2)
+    cluster_sync();  // both CTAs' barriers stand
+  else
+    __syncthreads();
   const Unit& u = unit;
   if (u.skip) return;  // (a pair's CTAs agree)
   if (warp == 8) {
@@ -374,20 +380,11 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
   }
-  __syncwarp();
-  tc_fence_before_sync();
-  if constexpr (CG == 2)
-    cluster_sync();
-  else
-    __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
   const int n = u.n, g = blockIdx.y;
   const uint64_t tmo = p.timeout_ns;
   // a whole warp waits: it goes on or gives up as one
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool done = __all_sync(0xffffffffu, wait_bounded<CG>(bar, parity, abort, tmo));
+    const bool done = __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, tmo));
     if (!done) {
       if (!*abort) attn_record(status, FAK_ERR_TIMEOUT);
       *abort = 1;
@@ -417,8 +414,18 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0) arrive_at<CG>(qfull, 0);
+    if (lane == 0) arrive_first<CG>(qfull);
+    if (warp == 8) {
+      tc_fence_before_sync();
+      if (lane == 0) mbar_arrive(tready);
+    }
   }
+  if (warp <= 8) {
+    wait(tready, 0);
+    tc_fence_after_sync();
+  }
+  const uint32_t tmem = warp <= 8 ? *reinterpret_cast<volatile uint32_t*>(tmem_slot) : 0;
+  const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
 
   if (warp < 8) {
     // ---------------- softmax
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) arrive_at<CG>(&pfull[b], 0);
+      if (lane == 0) arrive_first<CG>(&pfull[b]);
     }
     // ---------------- the row's result
     // (the same barrier's phase before first: three tiles' products may still be under way here, and a
@@ -515,6 +522,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     if (ok && n > 2) ok = wait(&odone[(n - 1) & 1], ((n - 3) >> 1) & 1);
     if (ok && n > 0) ok = wait(&odone[(n - 1) & 1], ((n - 1) >> 1) & 1);
     if (ok) ok = wait(pdone, 0);
+    if (CG == 2 && ok) ok = try_wait_cluster(pdone, 0);  // (done: for its acquire of `odd`)
     if (ok && live) {
       tc_fence_after_sync();
       float* mine = red + (n & 1) * 2 * kTileM;
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            arrive_at<CG>(&full[st], 0);
+            arrive_first<CG>(&full[st]);
             mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
           }
           if (++rs == C::raw) {
@@ -889,14 +897,18 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) arrive_at<CG>(&mended[st], 0);
+          if (lane == 0) arrive_first<CG>(&mended[st]);
         }
       }
     }
     __syncwarp();
     if (lane == 0) {
-      arrive_at<CG>(pdone, rank);
-      if constexpr (CG == 2) arrive_at<CG>(pdone, rank ^ 1);
+      if constexpr (CG == 1) {
+        mbar_arrive(pdone);
+      } else {
+        arrive_release_cluster(pdone, 0);
+        arrive_release_cluster(pdone, 1);
+      }
     }
   }
   __syncwarp();
