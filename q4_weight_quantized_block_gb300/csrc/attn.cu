@@ -33,9 +33,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const KvSeq sq = kv_seq(p.c, s);
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
   const int64_t r = (row - sq.r0) * p.group + h % p.group, total = (int64_t)(sq.r1 - sq.r0) * p.group;
-  const int64_t base = r / p.block * p.block, last = min(base + p.block, total) - 1;
+  const int64_t base = r >> p.block_shift << p.block_shift, last = min(base + (1 << p.block_shift), total) - 1;
   const int p0 = sq.len - (sq.r1 - sq.r0);
-  const KeyTiles kt = key_tiles(p0 + (int)(base / p.group), p0 + (int)(last / p.group), p.window, p.sinks);
+  const KeyTiles kt = key_tiles(p0 + p.by_group((int)base), p0 + p.by_group((int)last), p.window, p.sinks);
   if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
   const int pos = p0 + (int)(row - sq.r0), pieces = min(p.splits, ceil_div(kt.n, p.per_split));
   const int64_t slot = row * p.nq + h, step = p.c.rows * p.nq;
@@ -161,7 +161,13 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.scale = a->scale * 1.4426950408889634f;
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
-  p.block = pl.block;
+  p.block_shift = pl.block == kTileM ? 7 : 8;
+  if (p.group > 1) {  // ceil(2^(31 + s) / group), s = ceil(log2 group): exact for r below 2^31
+    int s = 1;
+    while ((1 << s) < p.group) ++s;
+    p.group_mul = (uint32_t)(((1ull << (31 + s)) + p.group - 1) / p.group);
+    p.group_shift = s - 1;
+  }
   p.window = a->window;
   p.sinks = a->window ? a->sinks : 0;
   p.splits = pl.splits;

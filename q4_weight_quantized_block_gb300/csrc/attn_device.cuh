@@ -14,7 +14,9 @@ struct AttnParams {
   int64_t q_row, q_head, gate_row, gate_head, out_row, out_head;
   float scale;  // times log2(e): scores are held in powers of two
   int nq, group, window, sinks;
-  int block;  // rows of a block: 128, or 256 in a pair of CTAs
+  int block_shift;  // rows of a block: 128, or 256 in a pair of CTAs
+  uint32_t group_mul;  // r / group = r group_mul / 2^(32 + group_shift) for 0 <= r < 2^31 (group 1: group_mul 0)
+  int group_shift;
   // the keys of a block of rows are cut into at most `splits` pieces of `per_split` key tiles; a block with more
   // than one piece leaves, for each piece, row and head, the unnormalised sum (part, dh values) and its base and
   // weight sum (stat), which the join kernel adds up
@@ -22,6 +24,10 @@ struct AttnParams {
   float* part;   // [splits][rows][nq][dh]
   float2* stat;  // [splits][rows][nq]
   unsigned long long timeout_ns;
+
+  __device__ __forceinline__ int by_group(int r) const {
+    return group_mul ? (int)(__umulhi((uint32_t)r, group_mul) >> group_shift) : r;
+  }
 };
 
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA

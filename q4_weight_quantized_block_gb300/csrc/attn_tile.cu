@@ -14,11 +14,11 @@
 //
 //   warps 0-7      softmax: warp w and w + 4 share rows 32 (w % 4) .. +31, half of the keys each
 //   warp 8         TMEM owner; in the first CTA the MMA issuer
-//   warp 9         TMA: K and V by pages in 16 KB stages of a ring, in the order the MMAs take them
-//                  (K 0, K 1, V 0, K 2, V 1, ...), in the 128-byte-swizzled layouts the MMAs read: Q and K
-//                  64 dims wide with the dims running (K-major), V keys by dims as stored (MN-major)
-//   warps 12-15    for an 8-bit cache, codes to bf16: the copies land in a ring of their own and these warps fill
-//                  the MMAs' ring from it; for a bf16 cache, V of the tiles that a mask cuts
+//   warps 9, 10    TMA of K and of V by pages, each into a ring of its own (one warp needs some 500 cycles for a
+//                  stage), in the 128-byte-swizzled layouts the MMAs read: Q and K 64 dims wide with the dims
+//                  running (K-major), V keys by dims as stored (MN-major)
+//   warps 12-15    for an 8-bit cache, codes to bf16: the copies land in rings of their own and these warps fill
+//                  the MMAs' rings from them; for a bf16 cache, V of the tiles that a mask cuts
 // S has two or three buffers, so the next tile's S = Q K^T runs while the softmax works.
 // 8-bit codes become bf16 exactly; their scales multiply the scores' columns and the weights instead.
 // A weight of zero times a value that is not finite would be NaN, so in the tiles that a mask cuts a bf16 V is
@@ -42,25 +42,33 @@
 
 namespace {
 
-constexpr int kStageBytes = 16384;
-constexpr int kSlots = 16;  // tiles whose scales are held at once (8-bit caches): more than the rings hold
-constexpr int kRawBytes = kStageBytes / 2;
+constexpr int kPanel = 16384;  // 64 dims of Q's 128 rows
 
 template <int DH, int KIND, int CG>
 struct Cfg {
   static constexpr bool quant = KIND != FAK_KV_BF16;
   static constexpr int dv = DH / CG;                 // dims of V a CTA holds
-  static constexpr int chunks = dv / 64;             // stages of one tile of K or of V
-  static constexpr int vkeys = 8192 / dv;            // keys of one V stage
-  static constexpr int panels = DH == 64 ? 1 : 2;    // a K stage: 64 keys by this many 64 dims (dh 64: twice 64 keys)
+  static constexpr int stage = !quant && CG == 2 && DH == 256 ? 32768 : 16384;
+  static constexpr int raw = stage / 2;              // bytes of a stage's codes
+  static constexpr int chunks = 256 * dv / stage;    // stages of one tile of K or of V
+  static constexpr int vkeys = kTileN / chunks;      // keys of one V stage
+  static constexpr int panels = stage / 8192 < DH / 64 ? stage / 8192 : DH / 64;  // 64 dims in a K stage, by 64 keys
+  static constexpr int khalves = stage / 8192 / panels;  // (dh 64: two halves of a tile's keys)
   static constexpr int sbufs = DH == 256 ? 2 : 3;    // S buffers: 512 TMEM columns, less O's
-  static constexpr int stages = quant ? (DH == 256 ? 6 : 8) : DH == 256 ? 9 : DH == 128 ? 11 : 12;
-  static constexpr int raw = !quant ? 0 : DH == 64 ? 6 : 5;  // stages of codes on their way to bf16
+  // stages of K, of V, and of their codes on their way to bf16
+  static constexpr int ks = stage == 32768 ? 2 : quant ? (DH == 256 ? 3 : 4) : DH == 256 ? 4 : 5;
+  static constexpr int vs = stage == 32768 ? 2 : quant ? (DH == 256 ? 3 : 4) : DH == 256 ? 5 : 6;
+  static constexpr int rs = quant ? 3 : 0;
+  // tiles whose scales are held at once: a tile's are loaded when the K of the tile rs + ks stages back is done
+  // with, and with it the softmax of the tile sbufs further back
+  static constexpr int slots = (rs + ks + chunks - 1) / chunks + sbufs;
   static constexpr int threads = 16 * 32;
-  static constexpr int off_ring = kTileM * DH * 2;
-  static constexpr int off_raw = off_ring + stages * kStageBytes;
-  static constexpr int off_scales = off_raw + raw * kRawBytes;
-  static constexpr int off_red = off_scales + (quant ? kSlots * 2 * kTileN * 4 : 0);
+  static constexpr int off_k = kTileM * DH * 2;
+  static constexpr int off_v = off_k + ks * stage;
+  static constexpr int off_rk = off_v + vs * stage;
+  static constexpr int off_rv = off_rk + rs * raw;
+  static constexpr int off_scales = off_rv + rs * raw;
+  static constexpr int off_red = off_scales + (quant ? slots * 2 * kTileN * 4 : 0);
   static constexpr int off_bar = off_red + 2 * 2 * kTileM * 4;
   static constexpr int smem = off_bar + 656 + 1024;
   static_assert(smem <= 232448 - 1024, "shared memory exceeds the 227 KB per-block limit");
@@ -174,6 +182,32 @@ FAK_DEV float exp2_approx(float x) {
   return y;
 }
 
+// two f32 operations in one instruction
+FAK_DEV uint64_t two(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+FAK_DEV void of_two(float& a, float& b, uint64_t d) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+FAK_DEV void mul2(float& a, float& b, float x, float y) {  // a *= x, b *= y
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two(a, b)), "l"(two(x, y)));
+  of_two(a, b, d);
+}
+FAK_DEV void add2(float& a, float& b, float x, float y) {  // a += x, b += y
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two(a, b)), "l"(two(x, y)));
+  of_two(a, b, d);
+}
+FAK_DEV void fma2(float& a, float& b, float x, float y, float f, float c) {  // a = x f + c, b = y f + c
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(two(x, y)), "l"(two(f, f)), "l"(two(c, c)));
+  of_two(a, b, d);
+}
+
+// y * sigmoid(x); x = infinity: y
+FAK_DEV float gated_by(float y, float x) { return __fdividef(y, 1.0f + __expf(-x)); }
+
 FAK_DEV uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -258,7 +292,7 @@ FAK_DEV void find_unit(const AttnParams& p, int64_t x, int split, int rank, int 
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, i = lo + lane * step;
     const unsigned b =
-        __ballot_sync(0xffffffffu, i < hi && (int64_t)p.c.row_start[i] * p.group / p.block + i <= x);
+        __ballot_sync(0xffffffffu, i < hi && ((int64_t)p.c.row_start[i] * p.group >> p.block_shift) + i <= x);
     const int n = __popc(b);
     if (n > 1) lo += (n - 1) * step;
     hi = min(lo + step, hi);
@@ -267,18 +301,18 @@ FAK_DEV void find_unit(const AttnParams& p, int64_t x, int split, int rank, int 
   u.seq = lo;
   u.skip = 1;
   if (!sq.ok) return;
-  const int64_t first = (x - ((int64_t)sq.r0 * p.group / p.block + lo)) * p.block;
+  const int64_t first = (x - (((int64_t)sq.r0 * p.group >> p.block_shift) + lo)) << p.block_shift;
   const int64_t total = (int64_t)(sq.r1 - sq.r0) * p.group;
   if (first < 0 || first >= total) return;
-  const int rows = (int)min((int64_t)p.block, total - first);
+  const int rows = (int)min((int64_t)1 << p.block_shift, total - first);
   u.row0 = sq.r0;
   u.rbase = (int)first + rank * kTileM;
   u.nrows = max(0, min(kTileM, rows - rank * kTileM));
   u.p0 = sq.len - (sq.r1 - sq.r0);
-  u.p_lo = u.p0 + (int)first / p.group;
-  u.p_hi = u.p0 + ((int)first + rows - 1) / p.group;
-  u.own_lo = u.p0 + u.rbase / p.group;
-  u.own_hi = u.p0 + (u.rbase + max(u.nrows, 1) - 1) / p.group;
+  u.p_lo = u.p0 + p.by_group((int)first);
+  u.p_hi = u.p0 + p.by_group((int)first + rows - 1);
+  u.own_lo = u.p0 + p.by_group(u.rbase);
+  u.own_hi = u.p0 + p.by_group(u.rbase + max(u.nrows, 1) - 1);
   u.kt = key_tiles(u.p_lo, u.p_hi, p.window, p.sinks);
   u.direct = p.splits == 1 || u.kt.n <= p.per_split;
   u.begin = split * p.per_split;
@@ -298,15 +332,19 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   float* scales = reinterpret_cast<float*>(smem + C::off_scales);  // [slot][key, value][128]
   float* red = reinterpret_cast<float*>(smem + C::off_red);        // [parity][half][128]
-  // in a pair the MMA issuer's own are those of CTA 0: full, mended, pfull, qfull
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::off_bar);
-  uint64_t* empty = full + C::stages;
-  uint64_t* clean = empty + C::stages;  // bf16: the stage's V has landed and is to be mended
-  uint64_t* mended = clean + (C::quant ? 0 : C::stages);
-  uint64_t* rfull = mended + (C::quant ? 0 : C::stages);
-  uint64_t* rempty = rfull + C::raw;
-  uint64_t* scfull = rempty + C::raw;
-  uint64_t* sfull = scfull + (C::quant ? kSlots : 0);
+  // in a pair the MMA issuer waits on CTA 0's: kfull, vfull, mended, pfull, qfull
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + C::off_bar);
+  uint64_t* kempty = kfull + C::ks;
+  uint64_t* vfull = kempty + C::ks;
+  uint64_t* vempty = vfull + C::vs;
+  uint64_t* clean = vempty + C::vs;  // bf16: the stage's V has landed and is to be mended
+  uint64_t* mended = clean + (C::quant ? 0 : C::vs);
+  uint64_t* rkfull = mended + (C::quant ? 0 : C::vs);  // codes
+  uint64_t* rkempty = rkfull + C::rs;
+  uint64_t* rvfull = rkempty + C::rs;
+  uint64_t* rvempty = rvfull + C::rs;
+  uint64_t* scfull = rvempty + C::rs;
+  uint64_t* sfull = scfull + (C::quant ? C::slots : 0);
   uint64_t* pfull = sfull + 3;
   uint64_t* odone = pfull + 3;
   uint64_t* pair = odone + 2;
@@ -314,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   uint64_t* pdone = qfull + 1;
   uint64_t* drain = pdone + 1;
   uint64_t* tready = drain + 1;
-  static_assert((C::quant ? 2 * C::stages + 2 * C::raw + kSlots : 4 * C::stages) * 8 + 16 * 8 <= 640,
+  static_assert((2 * C::ks + (C::quant ? 2 : 4) * C::vs + 4 * C::rs + (C::quant ? C::slots : 0) + 16) * 8 <= 640,
                 "barriers exceed their area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 640);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 644);
@@ -328,26 +366,32 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     find_unit(p, (gridDim.x - 1 - blockIdx.x) / CG, blockIdx.z, rank, lane, u);
     if (lane == 0) unit = u;
   } else if (warp == 1 && lane == 0) {
-    for (int s = 0; s < C::stages; ++s) {
-      mbar_init(&full[s], C::quant ? 4 * CG : 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < C::ks; ++s) {
+      mbar_init(&kfull[s], C::quant ? 4 * CG : 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < C::vs; ++s) {
+      mbar_init(&vfull[s], C::quant ? 4 * CG : 1);
+      mbar_init(&vempty[s], 1);
       if (!C::quant) {
         mbar_init(&clean[s], 1);
         mbar_init(&mended[s], 4 * CG);
       }
     }
-    for (int s = 0; s < C::raw; ++s) {
-      mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], 4);
+    for (int s = 0; s < C::rs; ++s) {
+      mbar_init(&rkfull[s], 1);
+      mbar_init(&rkempty[s], 4);
+      mbar_init(&rvfull[s], 1);
+      mbar_init(&rvempty[s], 4);
     }
-    for (int s = 0; s < (C::quant ? kSlots : 0); ++s) mbar_init(&scfull[s], 1);
+    for (int s = 0; s < (C::quant ? C::slots : 0); ++s) mbar_init(&scfull[s], 1);
     for (int s = 0; s < 3; ++s) {
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 8 * CG);
     }
     for (int s = 0; s < 2; ++s) mbar_init(&odone[s], 1);
     for (int s = 0; s < 4; ++s) mbar_init(&pair[s], 2);
-    mbar_init(qfull, 15 * CG);
+    mbar_init(qfull, 14 * CG);
     mbar_init(pdone, 4 * CG);
     mbar_init(drain, 1);
     mbar_init(tready, 1);
@@ -391,26 +435,24 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     }
     return done;
   };
-  if (warp != 9) {
+  if (warp != 9 && warp != 10) {
     // Q: rows of the block, 64 dims to a 16 KB panel, by all warps but the TMA's; rows past the block's are zeros
-    const int w = warp < 9 ? warp : warp - 1;
-    constexpr int T = 15 * 32, total = kTileM * DH / 8;
-    const int tid = w * 32 + lane;
-    constexpr int each = (total + T - 1) / T;
+    constexpr int lanes = DH / 8, each = (kTileM * lanes + 14 * 32 - 1) / (14 * 32);  // 16 bytes to a lane
+    const int tid = (warp < 9 ? warp : warp - 2) * 32 + lane, c = tid % lanes;
     uint4 x[each];
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const int e = k * T + tid, row = e / (DH / 8), c = e % (DH / 8), r = u.rbase + row;
+      const int row = (k * 14 * 32 + tid) / lanes, r = u.rbase + row, token = p.by_group(r);
       x[k] = make_uint4(0, 0, 0, 0);
       if (row < u.nrows)
-        x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.row0 + r / p.group) * p.q_row +
-                                               (int64_t)(g * p.group + r % p.group) * p.q_head + c * 8);
+        x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.row0 + token) * p.q_row +
+                                               (int64_t)(g * p.group + r - token * p.group) * p.q_head + c * 8);
     }
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const int e = k * T + tid, row = e / (DH / 8), c = e % (DH / 8);
-      if (e < total)
-        *reinterpret_cast<uint4*>(smem + (c >> 3) * kStageBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
+      const int row = (k * 14 * 32 + tid) / lanes;
+      if (row < kTileM)
+        *reinterpret_cast<uint4*>(smem + (c >> 3) * kPanel + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -432,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const bool live = 32 * quarter < u.nrows;
-    const int r = u.rbase + row, pos = u.p0 + r / p.group;
+    const int r = u.rbase + row, token = p.by_group(r), pos = u.p0 + token;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
@@ -440,20 +482,27 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       const int tile = key_tile(u.kt, u.begin + i), j0 = tile * kTileN + 64 * half;
       if (!(ok = wait(&sfull[b], (i / C::sbufs) & 1))) break;
       if constexpr (C::quant)
-        if (!(ok = wait(&scfull[i % kSlots], (i / kSlots) & 1))) break;
+        if (!(ok = wait(&scfull[i % C::slots], (i / C::slots) & 1))) break;
       tc_fence_after_sync();
       const uint32_t scol = tmem_s + lanes + (uint32_t)(b * kTileN + 64 * half);
       if (live) {
-        uint32_t raw[2][32];
-        tmem_ld_cols<32>(scol, raw[0]);
-        tmem_ld_cols<32>(scol + 32, raw[1]);
-        tmem_wait_ld();
         float t[64];
-        const float* ks = scales + (i % kSlots) * 2 * kTileN + 64 * half;
+        {
+          uint32_t raw[2][32];
+          tmem_ld_cols<32>(scol, raw[0]);
+          tmem_ld_cols<32>(scol + 32, raw[1]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          t[k] = __uint_as_float(raw[k >> 5][k & 31]);
-          if constexpr (C::quant) t[k] *= ks[k];
+          for (int k = 0; k < 64; ++k) t[k] = __uint_as_float(raw[k >> 5][k & 31]);
+        }
+        const float* sc = scales + (C::quant ? (i % C::slots) * 2 * kTileN + 64 * half : 0);
+        if constexpr (C::quant) {
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + k);
+            mul2(t[k], t[k + 1], f.x, f.y);
+            mul2(t[k + 2], t[k + 3], f.z, f.w);
+          }
         }
         if (tile_cut(u.own_lo, u.own_hi, tile, p.window, p.sinks)) {
 #pragma unroll
@@ -495,18 +544,24 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
         float sum[2] = {0.0f, 0.0f};
         uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          const float a = exp2_approx(fmaf(t[k], p.scale, -base));
-          const float c = exp2_approx(fmaf(t[k + 1], p.scale, -base));
-          sum[0] += a;
-          sum[1] += c;
+        for (int k = 0; k < 64; k += 4) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            fma2(e[j], e[j + 1], t[k + j], t[k + j + 1], p.scale, -base);
+            e[j] = exp2_approx(e[j]);
+            e[j + 1] = exp2_approx(e[j + 1]);
+            add2(sum[0], sum[1], e[j], e[j + 1]);
+          }
           if constexpr (C::quant) {
             // a weight of zero stays zero, whatever scale stands at its place
-            const float va = ks[kTileN + k], vc = ks[kTileN + k + 1];
-            w[k / 2] = pack_bf16(a == 0.0f ? 0.0f : a * va, c == 0.0f ? 0.0f : c * vc);
-          } else {
-            w[k / 2] = pack_bf16(a, c);
+            const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + k);
+            const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = e[j] == 0.0f ? 0.0f : e[j] * v[j];
           }
+          w[k / 2] = pack_bf16(e[0], e[1]);
+          w[k / 2 + 1] = pack_bf16(e[2], e[3]);
         }
         l += sum[0] + sum[1];
         tmem_st32(scol, w);
@@ -533,30 +588,33 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       l += mine[(half ^ 1) * kTileM + row];
     }
     if (ok && live) {
-      const int64_t grow = u.row0 + r / p.group;
-      const int head = g * p.group + r % p.group;
-      const bool mine = row < u.nrows;
-      const int64_t slot = ((int64_t)blockIdx.z * p.c.rows + grow) * p.nq + head;
+      const int head = g * p.group + r - token * p.group;
       // a row that sees nothing is zeros; one whose scores are all -inf is NaN, as 0 / 0 is
-      const float inv = pos < 0 ? 0.0f : 1.0f / l;
+      const float scale = u.direct ? 1.0f / l : 1.0f;
+      const bool mine = row < u.nrows, zero = pos < 0 || n == 0;
+      const int64_t grow = u.row0 + token;
+      const int64_t slot = ((int64_t)blockIdx.z * p.c.rows + grow) * p.nq + head;
       if (!u.direct && mine && half == 0) p.stat[slot] = make_float2(m, l);
+      // 32 dims at a time turn in shared memory (Q's and the rings', all read by now), so that rows are stored
+      // 128 bytes in a piece: eight lanes a row, four rows a step
+      const int64_t to = u.direct ? grow * p.out_row + head * p.out_head : slot * DH;
+      const int64_t from = p.gate ? grow * p.gate_row + head * p.gate_head : 0;
+      float* turn = reinterpret_cast<float*>(smem) + warp * 1024;
 #pragma unroll 1
       for (int c = 0; c < DH / 2; c += 32) {
         const int d0 = half * (DH / 2) + c;
-        uint32_t o[32];
+        uint32_t o[32] = {};
         if (n > 0) {
           tmem_ld_cols<32>(tmem + lanes + (uint32_t)d0, o);
           tmem_wait_ld();
         }
-        if (pos < 0 || n == 0) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        }
         if (!C::quant && mine && *odd) {
           // values that are not finite, in tiles where they were left out: added for the rows that see them
+#pragma unroll 1
           for (int i = 0; i < n; ++i) {
             const int tile = key_tile(u.kt, u.begin + i);
             if (!tile_cut(u.p_lo, u.p_hi, tile, p.window, p.sinks)) continue;
+#pragma unroll 1
             for (int j = tile * kTileN; j < min((tile + 1) * kTileN, pos + 1); ++j) {
               if (!sees(pos, j, p.window, p.sinks)) continue;
               int64_t at = kv_place(p.c, u.seq, j, g);
@@ -569,34 +627,42 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
             }
           }
         }
-        if (mine && !u.direct) {
-          float4* dst = reinterpret_cast<float4*>(p.part + slot * DH + d0);
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            dst[k / 4] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
-                                     __uint_as_float(o[k + 3]));
-        } else if (mine) {
-        float y[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * inv;
-        if (p.gate && pos >= 0) {
-          const float4* gp = reinterpret_cast<const float4*>(p.gate + grow * p.gate_row + head * p.gate_head + d0);
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 x = gp[k / 4];
-            y[k] /= 1.0f + __expf(-x.x);
-            y[k + 1] /= 1.0f + __expf(-x.y);
-            y[k + 2] /= 1.0f + __expf(-x.z);
-            y[k + 3] /= 1.0f + __expf(-x.w);
-          }
-        }
-        uint4* dst = reinterpret_cast<uint4*>(p.out + grow * p.out_row + head * p.out_head + d0);
-#pragma unroll
-        for (int k = 0; k < 32; k += 8)
-          dst[k / 8] = make_uint4(pack_bf16(y[k], y[k + 1]), pack_bf16(y[k + 2], y[k + 3]),
-                                  pack_bf16(y[k + 4], y[k + 5]), pack_bf16(y[k + 6], y[k + 7]));
+        for (int k = 0; k < 8; ++k) {
+          const float4 y = make_float4(__uint_as_float(o[4 * k]) * scale, __uint_as_float(o[4 * k + 1]) * scale,
+                                       __uint_as_float(o[4 * k + 2]) * scale, __uint_as_float(o[4 * k + 3]) * scale);
+          *reinterpret_cast<float4*>(turn + lane * 32 + ((k ^ (lane & 7)) << 2)) = y;
         }
         __syncwarp();
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0 += 4) {
+          float4 y[4], x[4];
+          int64_t at[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 4 * (k0 + k) + (lane >> 3);
+            at[k] = __shfl_sync(0xffffffffu, to, rr) + d0 + 4 * (lane & 7);
+            const int64_t gf = __shfl_sync(0xffffffffu, from, rr) + d0 + 4 * (lane & 7);
+            const bool blank = __shfl_sync(0xffffffffu, (int)zero, rr);
+            y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            x[k] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
+            if (32 * quarter + rr >= u.nrows || blank) continue;
+            y[k] = *reinterpret_cast<const float4*>(turn + rr * 32 + (((lane & 7) ^ (rr & 7)) << 2));
+            if (p.gate && u.direct) x[k] = *reinterpret_cast<const float4*>(p.gate + gf);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (32 * quarter + 4 * (k0 + k) + (lane >> 3) >= u.nrows) continue;
+            if (u.direct) {
+              const uint2 w = make_uint2(pack_bf16(gated_by(y[k].x, x[k].x), gated_by(y[k].y, x[k].y)),
+                                         pack_bf16(gated_by(y[k].z, x[k].z), gated_by(y[k].w, x[k].w)));
+              *reinterpret_cast<uint2*>(p.out + at[k]) = w;
+            } else {
+              *reinterpret_cast<float4*>(p.part + at[k]) = y[k];
+            }
+          }
+        }
       }
     }
   } else if (warp == 8) {
@@ -604,42 +670,38 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     if (n > 0 && rank == 0) {
       // K: one CTA takes a tile as twice 64 keys, since its panels are 64 keys high; a pair holds 64 keys each
       constexpr uint32_t id_s = kIdescAttn<kTileM * CG, 64 * CG, false>, id_o = kIdescAttn<kTileM * CG, DH, true>;
-      const uint64_t kd0 = umma_desc_sw128(smem_u32(smem + C::off_ring)), qd = umma_desc_sw128(smem_u32(smem));
+      const uint64_t kd0 = umma_desc_sw128(smem_u32(smem + C::off_k)), qd = umma_desc_sw128(smem_u32(smem));
       // a stage's V: panels of 64 dims by vrows keys, all dims of the first keys, then of the next
       const int vshift = C::quant ? 31 - __clz(C::vkeys) : min(p.c.page_shift, 31 - __clz(C::vkeys));
-      const uint64_t vd0 = desc_mn(smem_u32(smem + C::off_ring), 128u << vshift);
-      // a stage that is mended has a barrier of its own, so the parities of both go by their uses
-      int st = 0;
-      uint32_t fulls = 0, mends = 0;
+      const uint64_t vd0 = desc_mn(smem_u32(smem + C::off_v), 128u << vshift);
+      int kst = 0, kph = 0, vst = 0;
+      uint32_t fulls = 0, mends = 0;  // a V stage that is mended has a barrier of its own: the parities go by uses
       bool ok = wait(qfull, 0);
-      auto take = [&](bool mend) {  // the next stage, once it is full
-        ok = ok && wait(mend ? &mended[st] : &full[st], ((mend ? mends : fulls) >> st) & 1);
-        (mend ? mends : fulls) ^= 1u << st;
-        tc_fence_after_sync();
-        return ok;
-      };
       auto scores = [&](int sb) {
         const uint32_t d = tmem_s + (uint32_t)(sb * kTileN);
 #pragma unroll
         for (int c = 0; c < C::chunks; ++c) {
-          if (!take(false)) return;
-          const uint64_t kd = kd0 + (uint64_t)(st * (kStageBytes >> 4));
+          if (!(ok = wait(&kfull[kst], kph))) return;
+          tc_fence_after_sync();
+          const uint64_t kd = kd0 + (uint64_t)(kst * (C::stage >> 4));
           if (elect_one()) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // the stage's halves: 64 dims of 64 keys
-              constexpr int per = DH / 128;  // stages of 64 keys
-              const int half = CG == 2 ? 0 : DH == 64 ? x : c / (per ? per : 1);
-              const int panel = DH == 64 ? 0 : (CG == 2 ? c : c % (per ? per : 1)) * 2 + x;
+            for (int x = 0; x < C::stage / 8192; ++x) {  // the stage's parts: 64 dims of 64 keys
+              const int part = c * (C::stage / 8192) + x;  // of the tile: the first 64 keys' panels, then the others'
+              const int panel = part % (DH / 64), half = part / (DH / 64);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ss<CG>(d + 64 * half, qd + (uint64_t)((panel * kStageBytes + 32 * k) >> 4),
+                mma_ss<CG>(d + 64 * half, qd + (uint64_t)((panel * kPanel + 32 * k) >> 4),
                            kd + (uint64_t)((x * 8192 + 32 * k) >> 4), id_s, panel | k);
             }
-            commit<CG>(&empty[st]);
+            commit<CG>(&kempty[kst]);
             if (c == C::chunks - 1) commit<CG>(&sfull[sb]);
           }
           __syncwarp();
-          st = st + 1 == C::stages ? 0 : st + 1;
+          if (++kst == C::ks) {
+            kst = 0;
+            kph ^= 1;
+          }
         }
       };
       for (int i = 0; i < min(C::sbufs, n) && ok; ++i) scores(i);
@@ -650,8 +712,10 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
         const uint32_t a = tmem_s + (uint32_t)(sb * kTileN);
 #pragma unroll
         for (int c = 0; c < C::chunks; ++c) {
-          if (!take(mend)) break;
-          const uint64_t vd = vd0 + (uint64_t)(st * (kStageBytes >> 4));
+          if (!(ok = wait(mend ? &mended[vst] : &vfull[vst], ((mend ? mends : fulls) >> vst) & 1))) break;
+          (mend ? mends : fulls) ^= 1u << vst;
+          tc_fence_after_sync();
+          const uint64_t vd = vd0 + (uint64_t)(vst * (C::stage >> 4));
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < C::vkeys / 16; ++k) {
@@ -660,11 +724,11 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
               mma_ts<CG>(tmem, a + (uint32_t)((key >> 6) * 64 + (key & 63) / 2),
                          vd + (uint64_t)(((box << vshift) * (C::dv * 2) + in * 128) >> 4), id_o, (i | key) != 0);
             }
-            commit<CG>(&empty[st]);
+            commit<CG>(&vempty[vst]);
             if (c == C::chunks - 1) commit<CG>(&odone[i & 1]);
           }
           __syncwarp();
-          st = st + 1 == C::stages ? 0 : st + 1;
+          if (++vst == C::vs) vst = 0;
         }
         if (ok && i + C::sbufs < n) scores(sb);
         if (++sb == C::sbufs) {
@@ -681,17 +745,20 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 9) {
-    // ---------------- TMA
+  } else if (warp == 9 || warp == 10) {
+    // ---------------- TMA: warp 9 K (and the scales), warp 10 V
+    const bool value = warp == 10;
     const int kshift = min(p.c.page_shift, 6), krows = 1 << kshift;  // the maps' boxes: keys of K, of V
     const int vshift = min(p.c.page_shift, 31 - __clz(C::vkeys)), vrows = 1 << vshift;
     const int kpanels = krows == 64 ? C::panels : 1;  // and panels of K, which stand 64 keys apart
     const int boxes = kTileN >> kshift;
-    constexpr int S = C::quant ? C::raw : C::stages;
+    const int S = C::quant ? C::rs : value ? C::vs : C::ks;
     constexpr int kw = C::panels * 64;  // 8-bit: bytes of a K stage's row
-    uint64_t* const free = C::quant ? rempty : empty;
-    int st = 0, ph = 1, sc = 0;  // the stage, the parity of its `free` (the first round is free already)
-    uint32_t fulls = 0xffffffffu, lands = 0xffffffffu;  // the parity of each stage's last use of `full`, of `clean`
+    uint64_t* const free = C::quant ? (value ? rvempty : rkempty) : value ? vempty : kempty;
+    uint64_t* const lands = C::quant ? (value ? rvfull : rkfull) : value ? vfull : kfull;
+    uint8_t* const to = smem + (C::quant ? (value ? C::off_rv : C::off_rk) : value ? C::off_v : C::off_k);
+    int st = 0, ph = 1;  // the stage, the parity of its `free` (the first round is free already)
+    uint32_t uses = 0xffffffffu, mends = 0xffffffffu;  // the parity of each stage's last use of `lands`, of `clean`
     bool ok = true;
     // lane l: the vector index of key l * krows of the tile; keys past the last that a row sees take its
     // page: what lies there is masked
@@ -705,93 +772,65 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       return (int)at;
     };
     int ahead = n > 0 ? places(0) : 0;  // the next tile's, looked up early
-    int held[4];                        // those of the tiles whose V is still to come
-    auto next = [&]() {
-      if (++st == S) {
-        st = 0;
-        ph ^= 1;
-      }
-    };
-    // the next stage, once it is free; its bytes count on CTA 0's barrier, but for V that is to be mended
-    auto stage = [&](bool mend, uint64_t*& bar, uint8_t*& dst) {
-      if (!(ok = ok && wait(&free[st], ph))) return false;
-      bar = C::quant ? &rfull[st] : mend ? &clean[st] : &full[st];
-      dst = smem + (C::quant ? C::off_raw + st * kRawBytes : C::off_ring + st * kStageBytes);
-      const bool local = C::quant || mend;
-      if ((local || rank == 0) && elect_one())
-        mbar_arrive_expect_tx(bar, C::quant ? kRawBytes : local ? kStageBytes : kStageBytes * CG);
-      __syncwarp();
-      (mend ? lands : fulls) ^= 1u << st;
-      return true;
-    };
-    auto keys = [&](int i, int at) {
-      if constexpr (C::quant) {
-        const int slot = i % kSlots;
-        float* to = scales + slot * 2 * kTileN;
+    for (int i = 0; i < n && ok; ++i) {
+      const int at = ahead;
+      if (i + 1 < n) ahead = places(i + 1);
+      if (C::quant && !value) {
+        const int slot = i % C::slots;
+        float* sc = scales + slot * 2 * kTileN;
+        // (its last tile is done with: the rings hold fewer tiles than there are slots)
         if (elect_one()) mbar_arrive_expect_tx(&scfull[slot], 2 * kTileN * 4);
         __syncwarp();
         if (lane < boxes) {
-          bulk_g2s_nohint(to + lane * krows, p.c.ks + at, krows * 4, &scfull[slot]);
-          bulk_g2s_nohint(to + kTileN + lane * krows, p.c.vs + at, krows * 4, &scfull[slot]);
+          bulk_g2s_nohint(sc + lane * krows, p.c.ks + at, krows * 4, &scfull[slot]);
+          bulk_g2s_nohint(sc + kTileN + lane * krows, p.c.vs + at, krows * 4, &scfull[slot]);
         }
         __syncwarp();
-        ++sc;
       }
-      uint64_t* bar;
-      uint8_t* dst;
-#pragma unroll
+      const bool mend =
+          !C::quant && value && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p.window, p.sinks);
+#pragma unroll 1
       for (int c = 0; c < C::chunks; ++c) {
-        if (!stage(false, bar, dst)) return;
-        constexpr int per = DH / 128;  // stages of 64 keys
-        const int half = CG == 2 ? rank : c / (per ? per : 1);  // dh 64: the stage has both halves
-        const int panel = (CG == 2 ? c : c % (per ? per : 1)) * 2;
-        for (int k = 0; k < (DH == 64 ? kTileN : 64); k += krows) {
-          const int row = __shfl_sync(0xffffffffu, at, (half * 64 + k) >> kshift);
-          if constexpr (C::quant) {
-            if (elect_one()) tma_load_2d_tx(dst + k * kw, &kmap, panel * 64, row, bar);
-          } else {
-            for (int x = 0; x < C::panels; x += kpanels)
-              if (elect_one()) load_3d<CG>(dst + x * 8192 + k * 128, &kmap, 0, row, panel + x, bar, false);
+        if (!(ok = wait(&free[st], ph))) break;
+        // a pair's bytes count on CTA 0's barrier, but for codes and for V that is to be mended
+        const bool local = C::quant || mend;
+        uint64_t* bar = mend ? &clean[st] : &lands[st];
+        uint8_t* dst = to + st * (C::quant ? C::raw : C::stage);
+        if ((local || rank == 0) && elect_one())
+          mbar_arrive_expect_tx(bar, C::quant ? C::raw : local ? C::stage : C::stage * CG);
+        __syncwarp();
+        (mend ? mends : uses) ^= 1u << st;
+        if (!value) {
+          // parts of 64 dims by 64 keys; a pair's CTA has its half of the keys
+          const int part = c * (C::stage / 8192), panel = part % (DH / 64);
+          const int first = 64 * (CG == 2 ? rank : part / (DH / 64));
+          for (int k = 0; k < 64 * C::khalves; k += krows) {
+            const int row = __shfl_sync(0xffffffffu, at, (first + k) >> kshift);
+            if constexpr (C::quant) {
+              if (elect_one()) tma_load_2d_tx(dst + k * kw, &kmap, panel * 64, row, bar);
+            } else {
+              for (int x = 0; x < C::panels; x += kpanels)
+                if (elect_one()) load_3d<CG>(dst + x * 8192 + k * 128, &kmap, 0, row, panel + x, bar, false);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        next();
-      }
-    };
-    auto values = [&](int i, int at) {
-      const bool mend = !C::quant && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p.window, p.sinks);
-      uint64_t* bar;
-      uint8_t* dst;
-#pragma unroll
-      for (int c = 0; c < C::chunks; ++c) {
-        if (!stage(mend, bar, dst)) return;
-        for (int r = 0; r < C::vkeys; r += vrows) {
-          const int key = c * C::vkeys + r, row = __shfl_sync(0xffffffffu, at, key >> kshift) + (key & (krows - 1));
-          if (elect_one()) {
-            if constexpr (C::quant)
-              tma_load_2d_tx(dst + r * C::dv, &vmap, rank * C::dv, row, bar);
-            else
-              load_3d<CG>(dst + r * C::dv * 2, &vmap, 0, row, rank * C::chunks, bar, mend);
+        } else {
+          for (int r = 0; r < C::vkeys; r += vrows) {
+            const int key = c * C::vkeys + r, row = __shfl_sync(0xffffffffu, at, key >> kshift) + (key & (krows - 1));
+            if (elect_one()) {
+              if constexpr (C::quant)
+                tma_load_2d_tx(dst + r * C::dv, &vmap, rank * C::dv, row, bar);
+              else
+                load_3d<CG>(dst + r * C::dv * 2, &vmap, 0, row, rank * (C::dv / 64), bar, mend);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
-        next();
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-    };
-    auto step = [&](int i) {  // K of tile i, its places kept for V
-#pragma unroll
-      for (int k = 3; k > 0; --k) held[k] = held[k - 1];
-      held[0] = ahead;
-      if (i + 1 < n) ahead = places(i + 1);
-      keys(i, held[0]);
-    };
-    // V i follows K i + sbufs - 1 (or the last K): its places were kept that many tiles ago
-    const int lead = min(C::sbufs, n);
-    for (int i = 0; i < lead && ok; ++i) step(i);
-    for (int i = 0; i < n && ok; ++i) {
-      const int back = min(lead, n - i) - 1;
-      values(i, back == 2 ? held[2] : back == 1 ? held[1] : held[0]);
-      if (ok && i + C::sbufs < n) step(i + C::sbufs);
     }
     // copies in flight land before the block can end (one that ran to its end has used every copy)
     if (lane == 0 && *abort) {
@@ -801,10 +840,14 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           if (globaltimer_ns() - t0 > 200000000ull) break;
       };
       for (int q = 0; q < S; ++q) {
-        landed(C::quant ? &rfull[q] : &full[q], fulls >> q);
-        if (!C::quant) landed(&clean[q], lands >> q);
+        landed(&lands[q], uses >> q);
+        if (!C::quant && value) landed(&clean[q], mends >> q);
       }
-      for (int q = max(0, sc - kSlots); q < sc; ++q) landed(&scfull[q % kSlots], q / kSlots);
+      if (C::quant && !value) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {  // scales: a kilobyte a tile, landed long before this
+        }
+      }
     }
     __syncwarp();
   } else if (warp >= 12) {
@@ -813,18 +856,23 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     const int tid = threadIdx.x - 12 * 32;
     bool ok = true;
     if constexpr (C::quant) {
-      int rs = 0, rph = 0, st = 0, ph = 1;
-      auto convert = [&](bool value) {
+      // two streams of stages, K's and V's, in the order the MMAs take them: K 0, K 1, V 0, K 2, V 1, ...
+      struct Stream {
+        int rs, rph, st, ph;
+      };
+      Stream sk{0, 0, 0, 1}, sv{0, 0, 0, 1};
+      auto convert = [&](bool value, Stream& m) {
         // 16 codes to a thread and step
         constexpr int kwidth = C::panels * 4, vwidth = C::dv / 16;
+#pragma unroll 1
         for (int c = 0; c < C::chunks; ++c) {
-          ok = ok && wait(&rfull[rs], rph) && wait(&empty[st], ph);
-          if (!ok) return;
-          const uint4* src = reinterpret_cast<const uint4*>(smem + C::off_raw + rs * kRawBytes);
-          uint8_t* dst = smem + C::off_ring + st * kStageBytes;
+          if (!(ok = ok && wait(&(value ? rvfull : rkfull)[m.rs], m.rph))) return;
+          const uint4* src = reinterpret_cast<const uint4*>(smem + (value ? C::off_rv : C::off_rk) + m.rs * C::raw);
+          uint8_t* dst = smem + (value ? C::off_v : C::off_k) + m.st * C::stage;
           uint4 q[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) q[k] = src[tid + k * T];
+          if (!(ok = wait(&(value ? vempty : kempty)[m.st], m.ph))) return;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int e = tid + k * T;
@@ -842,23 +890,23 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            arrive_first<CG>(&full[st]);
-            mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
+            arrive_first<CG>(&(value ? vfull : kfull)[m.st]);
+            mbar_arrive(&(value ? rvempty : rkempty)[m.rs]);  // after the stores, which came after the loads
           }
-          if (++rs == C::raw) {
-            rs = 0;
-            rph ^= 1;
+          if (++m.rs == C::rs) {
+            m.rs = 0;
+            m.rph ^= 1;
           }
-          if (++st == C::stages) {
-            st = 0;
-            ph ^= 1;
+          if (++m.st == (value ? C::vs : C::ks)) {
+            m.st = 0;
+            m.ph ^= 1;
           }
         }
       };
-      for (int i = 0; i < min(C::sbufs, n) && ok; ++i) convert(false);
+      for (int i = 0; i < min(C::sbufs, n) && ok; ++i) convert(false, sk);
       for (int i = 0; i < n && ok; ++i) {
-        convert(true);
-        if (ok && i + C::sbufs < n) convert(false);
+        convert(true, sv);
+        if (ok && i + C::sbufs < n) convert(false, sk);
       }
     } else {
       uint32_t landed = 0;  // parity of each stage's next use of `clean`
@@ -866,15 +914,14 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       for (int i = 0; i < n && ok; ++i) {
         const int tile = key_tile(u.kt, u.begin + i);
         if (!tile_cut(u.p_lo, u.p_hi, tile, p.window, p.sinks)) continue;
-        int it = (i + min(C::sbufs + i, n)) * C::chunks;  // V i comes after that many tiles
-        for (int c = 0; c < C::chunks && ok; ++c, ++it) {
-          const int st = it % C::stages;
+        for (int c = 0; c < C::chunks && ok; ++c) {
+          const int st = (i * C::chunks + c) % C::vs;
           if (!(ok = wait(&clean[st], (landed >> st) & 1))) break;
           landed ^= 1u << st;
-          uint4* v = reinterpret_cast<uint4*>(smem + C::off_ring + st * kStageBytes);
+          uint4* v = reinterpret_cast<uint4*>(smem + C::off_v + st * C::stage);
           bool bad = false;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < C::stage / 16 / T; ++k) {
             const int e = tid + k * T, box = e / (C::dv / 8) >> vshift;  // a box: dv dims of 2^vshift keys
             const int j = tile * kTileN + c * C::vkeys + (box << vshift) + ((e >> 3) & ((1 << vshift) - 1));
             bool change = false;
@@ -962,7 +1009,7 @@ cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks,
   CUtensorMap kmap, vmap;
   const int krows = std::min(page, 64), vrows = std::min(page, C::vkeys);
   if (!code_map(&kmap, p.c.k, C::quant, DH, n_vec, C::quant ? C::panels * 64 : 64, krows, krows == 64 ? C::panels : 1) ||
-      !code_map(&vmap, p.c.v, C::quant, DH, n_vec, C::quant ? C::dv : 64, vrows, C::chunks))
+      !code_map(&vmap, p.c.v, C::quant, DH, n_vec, C::quant ? C::dv : 64, vrows, C::dv / 64))
     return cudaErrorInvalidValue;
   e = cudaFuncSetAttribute(attn_tile_kernel<DH, KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
@@ -993,7 +1040,7 @@ cudaError_t by_kind(int kind, const AttnParams& p, int page, int64_t n_vec, int6
 
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
                              int* status, cudaStream_t s) {
-  if (p.block == 2 * kTileM)
+  if (p.block_shift == 8)
     return dh == 128 ? by_kind<128, 2>(kind, p, page, n_vec, blocks, status, s)
                      : by_kind<256, 2>(kind, p, page, n_vec, blocks, status, s);
   return dh == 64    ? by_kind<64, 1>(kind, p, page, n_vec, blocks, status, s)
