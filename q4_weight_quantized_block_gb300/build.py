@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfak.so")
 
-SOURCES = ["engine.cu", "batch.cu", "gemm.cu", "prefill.cu", "kv.cu", "attn.cu", "attn_tile.cu", "pack.cpp", "pack_device.cu"]
+SOURCES = ["engine.cu", "batch.cu", "gemm.cu", "prefill.cu", "kv.cu", "attn.cu", "attn_tile.cu", "attn_rows.cu", "pack.cpp", "pack_device.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

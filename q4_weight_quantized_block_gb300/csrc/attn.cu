@@ -1,7 +1,7 @@
 // Softmax attention of new rows over the paged KV cache (fak_paged_attn).
 //
 // The call's checks, the cut of its keys into pieces where there are few rows, and the kernel that
-// joins the pieces.  The attention itself: attn_tile.cu.
+// joins the pieces.  The attention itself: attn_rows.cu for few rows (decode steps), attn_tile.cu for more.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,81 +20,106 @@ __device__ int g_attn_status;
 
 constexpr int kPlanSms = 152;  // GB300's SMs: the workspace's size must not depend on the current device
 
-// Adds up the pieces of the blocks of rows whose keys were cut: one warp per (row, query head).
+// Adds up the pieces of the blocks of rows whose keys were cut: one block per (row, query head), a warp for every
+// eighth piece.
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i * sigmoid(gate),  M = max m_i
-// in the pieces' order, so the result does not depend on which finished first.
+// in an order that the pieces' number alone sets, so the result does not depend on which finished first.
 template <int DH>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int N = DH / 32;
-  const int lane = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  __shared__ float so[8][DH], sl[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
   const int64_t row = blockIdx.x;
-  if (h >= p.nq) return;
   const int s = kv_find_seq(p.c, row, lane);
   const KvSeq sq = kv_seq(p.c, s);
+  // the pieces' kernel is done (every block waits: this grid must not end before that one)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
-  const int64_t r = (row - sq.r0) * p.group + h % p.group, total = (int64_t)(sq.r1 - sq.r0) * p.group;
+  const int hh = h % p.group;
+  const int64_t r = (row - sq.r0) * p.group + hh, total = (int64_t)(sq.r1 - sq.r0) * p.group;
   const int64_t base = r >> p.block_shift << p.block_shift, last = min(base + (1 << p.block_shift), total) - 1;
   const int p0 = sq.len - (sq.r1 - sq.r0);
-  const KeyTiles kt = key_tiles(p0 + p.by_group((int)base), p0 + p.by_group((int)last), p.window, p.sinks);
+  const KeyTiles kt =
+      key_tiles(p0 + p.by_group((int)base), p0 + p.by_group((int)last), p.window, p.sinks, p.tile_shift);
   if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
   const int pos = p0 + (int)(row - sq.r0), pieces = min(p.splits, ceil_div(kt.n, p.per_split));
   const int64_t slot = row * p.nq + h, step = p.c.rows * p.nq;
   float top = -INFINITY;
-  for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.stat[slot + i * step].x);
+  for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.stat[slot + i * step].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   const float zero = top == -INFINITY ? 0.0f : top;
   float o[N] = {}, l = 0.0f;
-  for (int i = 0; i < pieces; ++i) {
+#pragma unroll 4
+  for (int i = warp; i < pieces; i += 8) {
     const float2 st = p.stat[slot + i * step];
-    const float f = exp2f(st.x - zero);
+    const float f = exp2_approx(st.x - zero);
     l = fmaf(f, st.y, l);
-    const float* x = p.part + (slot + i * step) * DH + lane * N;
+    const float* x = p.part + (slot + i * step) * DH + lane;
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[k], o[k]);
+    for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[32 * k], o[k]);
   }
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    float y = o[k] / l;
-    if (p.gate) y /= 1.0f + expf(-p.gate[row * p.gate_row + h * p.gate_head + lane * N + k]);
-    p.out[row * p.out_row + h * p.out_head + lane * N + k] = __float2bfloat16_rn(pos < 0 ? 0.0f : y);
+  for (int k = 0; k < N; ++k) so[warp][lane + 32 * k] = o[k];
+  if (lane == 0) sl[warp] = l;
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= DH) return;
+  float y = 0.0f;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    y += so[w][d];
+    l += sl[w];
   }
+  y /= l;
+  if (p.gate) y = gated_by(y, p.gate[row * p.gate_row + h * p.gate_head + d]);
+  p.out[row * p.out_row + h * p.out_head + d] = __float2bfloat16_rn(pos < 0 ? 0.0f : y);
 }
 
-// How a call's keys are cut.
+// How a call is cut.
 struct Plan {
-  int64_t blocks;  // blocks of rows of one KV head, at most
-  int block;       // rows of a block
+  bool few;                     // the kernel for few rows
+  int64_t blocks;               // blocks of rows of one KV head, at most
+  int block, tile;              // rows of a block, keys of a tile
   int splits, per_split;
 };
 
-Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args* a, int sms) {
+Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args* a) {
   Plan pl;
   const int group = a->nq / c->n_kv;
+  const int64_t rows = (int64_t)a->max_q * group;
+  pl.few = rows <= kRowsMax;
   // pairs of CTAs where sequences have more rows than one CTA holds (and a half of V is at least 64 dims)
-  pl.block = c->dh > 64 && (int64_t)a->max_q * group > kTileM ? 2 * kTileM : kTileM;
-  pl.blocks = a->rows * group / pl.block + b->n_seqs;  // see find_unit
-  int64_t tiles = ((int64_t)a->max_kv + kTileN - 1) / kTileN;
+  pl.block = c->dh > 64 && rows > kTileM ? 2 * kTileM : kTileM;
+  pl.blocks = pl.few ? b->n_seqs : a->rows * group / pl.block + b->n_seqs;  // see find_unit
+  pl.tile = pl.few ? kRowsN : kTileN;
+  int64_t tiles = ((int64_t)a->max_kv + pl.tile - 1) / pl.tile;
   if (a->window) {
     const int64_t span = (pl.block + group - 1) / group;
-    tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / kTileN + 2 +
-                                         std::min<int64_t>((int64_t)a->sinks / kTileN + 1, tiles));
+    tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / pl.tile + 2 +
+                                         std::min<int64_t>((int64_t)a->sinks / pl.tile + 1, tiles));
   }
   tiles = std::max<int64_t>(tiles, 1);
-  // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each
-  // as long as a piece and about three tiles' time to begin and to end; a cut costs two more for the join.
+  // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs (few rows: two to an
+  // SM), each as long as a piece and about three (two) tiles' time to begin and to end; a cut costs two more for the
+  // join.
   const int ctas = pl.block / kTileM;
-  const int64_t each = ((int64_t)a->max_q * group + pl.block - 1) / pl.block;  // blocks of a sequence, at most
-  const int64_t busy = std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas;
+  const int64_t each = pl.few ? 1 : (rows + pl.block - 1) / pl.block;  // blocks of a sequence, at most
+  const int64_t busy = std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas * c->n_kv;
+  const int64_t places = pl.few ? 2 * kPlanSms : kPlanSms;
   int64_t best = -1;
   pl.splits = 1;
   pl.per_split = (int)tiles;
-  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+  for (int64_t s = 1; s <= 512 && s <= tiles; ++s) {
     const int64_t per = (tiles + s - 1) / s, n = (tiles + per - 1) / per;
-    const int64_t cost = (busy * c->n_kv * n + sms - 1) / sms * (per + 3) + (n > 1 ? 2 : 0);
+    const int64_t cost = (busy * n + places - 1) / places * (per + (pl.few ? 2 : 3)) + (n > 1 ? 2 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       pl.splits = (int)n;
       pl.per_split = (int)per;
     }
+    if (busy * n > 4 * places) break;
   }
   return pl;
 }
@@ -105,6 +130,21 @@ size_t part_bytes(const fak_kv_cache* c, const fak_attn_args* a, const Plan& pl)
 }
 size_t stat_bytes(const fak_attn_args* a, const Plan& pl) {
   return pl.splits < 2 ? 0 : (size_t)pl.splits * a->rows * a->nq * 8;
+}
+
+template <int DH>
+cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)p.c.rows, (unsigned)p.nq);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<DH>, p);
 }
 
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
@@ -120,7 +160,7 @@ int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
 extern "C" size_t fak_paged_attn_workspace_bytes(const fak_kv_cache* cache, const fak_kv_batch* batch,
                                                  const fak_attn_args* a) {
   if (!cache || !batch || !a || cache->n_kv < 1 || batch->n_seqs < 0 || attn_shape(cache, a) != FAK_OK) return 0;
-  const Plan pl = make_plan(cache, batch, a, kPlanSms);
+  const Plan pl = make_plan(cache, batch, a);
   return part_bytes(cache, a, pl) + stat_bytes(a, pl);
 }
 
@@ -136,7 +176,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
       ((a->q_row | a->q_head | a->out_row | a->out_head) & 7) || (a->gate && ((a->gate_row | a->gate_head) & 3)) ||
       ((uintptr_t)a->workspace & 255))
     return FAK_ERR_ALIGN;
-  const Plan pl = make_plan(cache, batch, a, kPlanSms);
+  const Plan pl = make_plan(cache, batch, a);
   const size_t parts = part_bytes(cache, a, pl), need = parts + stat_bytes(a, pl);
   if (need && !a->workspace) return FAK_ERR_INVALID_ARG;
   if (a->workspace_bytes < need) return FAK_ERR_SHAPE;
@@ -162,6 +202,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
   p.block_shift = pl.block == kTileM ? 7 : 8;
+  p.tile_shift = pl.few ? 6 : 7;
   if (p.group > 1) {  // ceil(2^(31 + s) / group), s = ceil(log2 group): exact for r below 2^31
     int s = 1;
     while ((1 << s) < p.group) ++s;
@@ -176,18 +217,12 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + parts);
   p.timeout_ns = 2000000000ull;
   cudaStream_t s = (cudaStream_t)stream;
-  e = attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p, pl.blocks,
-                       static_cast<int*>(status), s);
-  if (e == cudaSuccess && pl.splits > 1) {
-    const dim3 grid((unsigned)a->rows, (unsigned)((a->nq + 7) / 8));
-    if (cache->dh == 64)
-      attn_join_kernel<64><<<grid, 256, 0, s>>>(p);
-    else if (cache->dh == 128)
-      attn_join_kernel<128><<<grid, 256, 0, s>>>(p);
-    else
-      attn_join_kernel<256><<<grid, 256, 0, s>>>(p);
-    e = cudaGetLastError();
-  }
+  int* st_word = static_cast<int*>(status);
+  e = pl.few ? attn_rows_launch(cache->kind, cache->dh, p, st_word, s)
+             : attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p,
+                                pl.blocks, st_word, s);
+  if (e == cudaSuccess && pl.splits > 1)
+    e = cache->dh == 64 ? launch_join<64>(p, s) : cache->dh == 128 ? launch_join<128>(p, s) : launch_join<256>(p, s);
   return fak_cuda_status(e);
 }
 

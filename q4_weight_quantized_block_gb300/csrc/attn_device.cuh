@@ -15,6 +15,7 @@ struct AttnParams {
   float scale;  // times log2(e): scores are held in powers of two
   int nq, group, window, sinks;
   int block_shift;  // rows of a block: 128, or 256 in a pair of CTAs
+  int tile_shift;   // keys of a tile
   uint32_t group_mul;  // r / group = r group_mul / 2^(32 + group_shift) for 0 <= r < 2^31 (group 1: group_mul 0)
   int group_shift;
   // the keys of a block of rows are cut into at most `splits` pieces of `per_split` key tiles; a block with more
@@ -31,29 +32,89 @@ struct AttnParams {
 };
 
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA
-constexpr int kTileN = 128;  // keys of a tile
+constexpr int kTileN = 128;  // keys of a tile of the blocks' kernel
+constexpr int kRowsMax = 16;  // most rows of a sequence and KV head that the kernel for few rows takes
+constexpr int kRowsN = 64;    // keys of its tiles
 
 FAK_DEV int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// The key tiles that rows at positions p_lo .. p_hi see: those of the first few positions that lie
-// before the window's tiles, then the window's.
+// The key tiles (of 2^shift keys) that rows at positions p_lo .. p_hi see: those of the first few positions
+// that lie before the window's tiles, then the window's.
 struct KeyTiles {
   int n, head, first;  // tiles in all, tiles of the sinks, first tile of the window
 };
 
-FAK_DEV KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks) {
+FAK_DEV KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks, int shift) {
   KeyTiles t{0, 0, 0};
   if (p_hi < 0) return t;
   if (window) {
     const int low = max(0, max(0, p_lo) - window + 1);
-    t.first = low / kTileN;
-    t.head = min(ceil_div(min(sinks, p_hi + 1), kTileN), t.first);
+    t.first = low >> shift;
+    t.head = min((min(sinks, p_hi + 1) + (1 << shift) - 1) >> shift, t.first);
   }
-  t.n = t.head + p_hi / kTileN - t.first + 1;
+  t.n = t.head + (p_hi >> shift) - t.first + 1;
   return t;
 }
 
 FAK_DEV int key_tile(const KeyTiles& t, int i) { return i < t.head ? i : t.first + i - t.head; }
+
+FAK_DEV bool sees(int pos, int j, int window, int sinks) {
+  return j <= pos && (!window || j > pos - window || j < sinks);
+}
+
+// Whether some row at positions p_lo .. p_hi does not see some key of j0 .. j1.
+FAK_DEV bool keys_cut(int p_lo, int p_hi, int j0, int j1, int window, int sinks) {
+  return !(j1 <= p_lo && (!window || j0 > p_hi - window || j1 < sinks));
+}
+
+FAK_DEV float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// y * sigmoid(x); x = infinity: y
+FAK_DEV float gated_by(float y, float x) { return __fdividef(y, 1.0f + __expf(-x)); }
+
+FAK_DEV uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+FAK_DEV uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+FAK_DEV uint32_t hsub2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four 8-bit codes as four bf16, exactly.  e4m3: its exponent and significand bits set as bf16's stand for the
+// value times 2^-120 (subnormals too).  int8: 128 + the low seven bits, less 128 or, for the negative, 256.
+template <int KIND>
+FAK_DEV void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KIND == FAK_KV_E4M3) {
+    const uint32_t a = prmt(w, 0, 0x1404), b = prmt(w, 0, 0x3424);
+    lo = hmul2_bf16(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), 0x7B807B80u);
+    hi = hmul2_bf16(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), 0x7B807B80u);
+  } else {
+    const uint32_t a = prmt(w, 0, 0x4140), b = prmt(w, 0, 0x4342);
+    lo = hsub2_bf16((a & 0x007F007Fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
+    hi = hsub2_bf16((b & 0x007F007Fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
+  }
+}
+
+// bf16 pair with values that are not finite made zero; sets odd if there was one
+FAK_DEV uint32_t finite2(uint32_t w, bool& odd) {
+  uint32_t m = 0xffffffffu;
+  if ((w & 0x7F80u) == 0x7F80u) m &= 0xffff0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) m &= 0x0000ffffu;
+  odd |= m != 0xffffffffu;
+  return w & m;
+}
 
 // Records a device-side error of the call (attn.cu's status word).
 FAK_DEV void attn_record(int* status, int code) { atomicCAS(status, 0, code); }
@@ -61,3 +122,4 @@ FAK_DEV void attn_record(int* status, int code) { atomicCAS(status, 0, code); }
 // Host: launches of the kernels in the other files.
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
                              int* status, cudaStream_t s);
+cudaError_t attn_rows_launch(int kind, int dh, const AttnParams& p, int* status, cudaStream_t s);

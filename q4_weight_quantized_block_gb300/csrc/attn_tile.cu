@@ -176,12 +176,6 @@ FAK_DEV uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-FAK_DEV float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // two f32 operations in one instruction
 FAK_DEV uint64_t two(float a, float b) {
   uint64_t d;
@@ -203,49 +197,6 @@ FAK_DEV void fma2(float& a, float& b, float x, float y, float f, float c) {  // 
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(two(x, y)), "l"(two(f, f)), "l"(two(c, c)));
   of_two(a, b, d);
-}
-
-// y * sigmoid(x); x = infinity: y
-FAK_DEV float gated_by(float y, float x) { return __fdividef(y, 1.0f + __expf(-x)); }
-
-FAK_DEV uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-FAK_DEV uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-FAK_DEV uint32_t hsub2_bf16(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Four 8-bit codes as four bf16, exactly.  e4m3: its exponent and significand bits set as bf16's stand for the
-// value times 2^-120 (subnormals too).  int8: 128 + the low seven bits, less 128 or, for the negative, 256.
-template <int KIND>
-FAK_DEV void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KIND == FAK_KV_E4M3) {
-    const uint32_t a = prmt(w, 0, 0x1404), b = prmt(w, 0, 0x3424);
-    lo = hmul2_bf16(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), 0x7B807B80u);
-    hi = hmul2_bf16(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), 0x7B807B80u);
-  } else {
-    const uint32_t a = prmt(w, 0, 0x4140), b = prmt(w, 0, 0x4342);
-    lo = hsub2_bf16((a & 0x007F007Fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
-    hi = hsub2_bf16((b & 0x007F007Fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
-  }
-}
-
-// bf16 pair with values that are not finite made zero; sets odd if there was one
-FAK_DEV uint32_t finite2(uint32_t w, bool& odd) {
-  uint32_t m = 0xffffffffu;
-  if ((w & 0x7F80u) == 0x7F80u) m &= 0xffff0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) m &= 0x0000ffffu;
-  odd |= m != 0xffffffffu;
-  return w & m;
 }
 
 // One lane of a converged warp, the same each time: the compiler keeps what the lanes share in uniform registers
@@ -275,14 +226,8 @@ FAK_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, u
   return mbar_wait_bounded(bar, parity, abort, timeout_ns);
 }
 
-FAK_DEV bool sees(int pos, int j, int window, int sinks) {
-  return j <= pos && (!window || j > pos - window || j < sinks);
-}
-
-// Whether some row at positions p_lo .. p_hi does not see some key of the tile.
-FAK_DEV bool tile_cut(int p_lo, int p_hi, int tile, int window, int sinks) {
-  const int j0 = tile * kTileN, j1 = j0 + kTileN - 1;
-  return !(j1 <= p_lo && (!window || j0 > p_hi - window || j1 < sinks));
+FAK_DEV bool tile_cut(int p_lo, int p_hi, int tile, const AttnParams& p) {
+  return keys_cut(p_lo, p_hi, tile * kTileN, tile * kTileN + kTileN - 1, p.window, p.sinks);
 }
 
 // Block x's sequence: the one of the last s with r0(s) * group / block + s <= x.  These starts rise by at
@@ -313,7 +258,7 @@ FAK_DEV void find_unit(const AttnParams& p, int64_t x, int split, int rank, int 
   u.p_hi = u.p0 + p.by_group((int)first + rows - 1);
   u.own_lo = u.p0 + p.by_group(u.rbase);
   u.own_hi = u.p0 + p.by_group(u.rbase + max(u.nrows, 1) - 1);
-  u.kt = key_tiles(u.p_lo, u.p_hi, p.window, p.sinks);
+  u.kt = key_tiles(u.p_lo, u.p_hi, p.window, p.sinks, 7);
   u.direct = p.splits == 1 || u.kt.n <= p.per_split;
   u.begin = split * p.per_split;
   const int end = u.direct || split == p.splits - 1 ? u.kt.n : min(u.kt.n, u.begin + p.per_split);
@@ -504,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
             mul2(t[k + 2], t[k + 3], f.z, f.w);
           }
         }
-        if (tile_cut(u.own_lo, u.own_hi, tile, p.window, p.sinks)) {
+        if (tile_cut(u.own_lo, u.own_hi, tile, p)) {
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!sees(pos, j0 + k, p.window, p.sinks)) t[k] = -INFINITY;
@@ -613,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
 #pragma unroll 1
           for (int i = 0; i < n; ++i) {
             const int tile = key_tile(u.kt, u.begin + i);
-            if (!tile_cut(u.p_lo, u.p_hi, tile, p.window, p.sinks)) continue;
+            if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
 #pragma unroll 1
             for (int j = tile * kTileN; j < min((tile + 1) * kTileN, pos + 1); ++j) {
               if (!sees(pos, j, p.window, p.sinks)) continue;
@@ -707,7 +652,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       for (int i = 0; i < min(C::sbufs, n) && ok; ++i) scores(i);
       int sb = 0, ph = 0;
       for (int i = 0; i < n && ok; ++i) {
-        const bool mend = !C::quant && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p.window, p.sinks);
+        const bool mend = !C::quant && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
         if (!(ok = wait(&pfull[sb], ph))) break;
         const uint32_t a = tmem_s + (uint32_t)(sb * kTileN);
 #pragma unroll
@@ -788,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
         __syncwarp();
       }
       const bool mend =
-          !C::quant && value && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p.window, p.sinks);
+          !C::quant && value && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
 #pragma unroll 1
       for (int c = 0; c < C::chunks; ++c) {
         if (!(ok = wait(&free[st], ph))) break;
@@ -913,7 +858,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       const int vshift = min(p.c.page_shift, 31 - __clz(C::vkeys));
       for (int i = 0; i < n && ok; ++i) {
         const int tile = key_tile(u.kt, u.begin + i);
-        if (!tile_cut(u.p_lo, u.p_hi, tile, p.window, p.sinks)) continue;
+        if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
         for (int c = 0; c < C::chunks && ok; ++c) {
           const int st = (i * C::chunks + c) % C::vs;
           if (!(ok = wait(&clean[st], (landed >> st) & 1))) break;
