@@ -23,5 +23,6 @@ __all__ = [
 
 def __getattr__(name):
     if name in __all__:
-        return getattr(importlib.import_module("._lib", __name__), name)
+        value = globals()[name] = getattr(importlib.import_module("._lib", __name__), name)
+        return value
     raise AttributeError(name)

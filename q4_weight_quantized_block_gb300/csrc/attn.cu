@@ -20,29 +20,30 @@ __device__ int g_attn_status;
 
 constexpr int kPlanSms = 152;  // GB300's SMs: the workspace's size must not depend on the current device
 
-// Adds up the pieces of the blocks of rows whose keys were cut: one block per (row, query head), a warp for every
-// eighth piece.
+// Adds up the pieces of the blocks of rows whose keys were cut: W warps (1 or 8) to a (row, query head), each for
+// every W-th piece.
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i * sigmoid(gate),  M = max m_i
 // in an order that the pieces' number alone sets, so the result does not depend on which finished first.
-template <int DH>
+template <int DH, int W>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int N = DH / 32;
   __shared__ float so[8][DH], sl[8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * (8 / W) + warp / W;
   const int64_t row = blockIdx.x;
   const int s = kv_find_seq(p.c, row, lane);
   const KvSeq sq = kv_seq(p.c, s);
   // the pieces' kernel is done (every block waits: this grid must not end before that one)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
-  const int hh = h % p.group;
-  const int64_t r = (row - sq.r0) * p.group + hh, total = (int64_t)(sq.r1 - sq.r0) * p.group;
+  if (W == 1 && h >= p.nq) return;
+  const int token = (int)(row - sq.r0), hh = h - p.by_group(h) * p.group;
+  const int64_t r = (int64_t)token * p.group + hh, total = (int64_t)(sq.r1 - sq.r0) * p.group;
   const int64_t base = r >> p.block_shift << p.block_shift, last = min(base + (1 << p.block_shift), total) - 1;
-  const int p0 = sq.len - (sq.r1 - sq.r0);
+  const int p0 = sq.len - (sq.r1 - sq.r0), pos = p0 + token;
   const KeyTiles kt =
       key_tiles(p0 + p.by_group((int)base), p0 + p.by_group((int)last), p.window, p.sinks, p.tile_shift);
   if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
-  const int pos = p0 + (int)(row - sq.r0), pieces = min(p.splits, ceil_div(kt.n, p.per_split));
+  const int pieces = min(p.splits, ceil_div(kt.n, p.per_split));
   const int64_t slot = row * p.nq + h, step = p.c.rows * p.nq;
   float top = -INFINITY;
   for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.stat[slot + i * step].x);
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const float zero = top == -INFINITY ? 0.0f : top;
   float o[N] = {}, l = 0.0f;
 #pragma unroll 4
-  for (int i = warp; i < pieces; i += 8) {
+  for (int i = warp % W; i < pieces; i += W) {
     const float2 st = p.stat[slot + i * step];
     const float f = exp2_approx(st.x - zero);
     l = fmaf(f, st.y, l);
@@ -59,22 +60,26 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[32 * k], o[k]);
   }
+  if constexpr (W > 1) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) so[warp][lane + 32 * k] = o[k];
-  if (lane == 0) sl[warp] = l;
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= DH) return;
-  float y = 0.0f;
-  l = 0.0f;
+    for (int k = 0; k < N; ++k) so[warp][lane + 32 * k] = o[k];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp >= N) return;
+    o[0] = l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    y += so[w][d];
-    l += sl[w];
+    for (int w = 0; w < 8; ++w) {
+      o[0] += so[w][warp * 32 + lane];
+      l += sl[w];
+    }
   }
-  y /= l;
-  if (p.gate) y = gated_by(y, p.gate[row * p.gate_row + h * p.gate_head + d]);
-  p.out[row * p.out_row + h * p.out_head + d] = __float2bfloat16_rn(pos < 0 ? 0.0f : y);
+#pragma unroll
+  for (int k = 0; k < (W > 1 ? 1 : N); ++k) {
+    const int d = lane + 32 * (W > 1 ? warp : k);
+    float y = o[k] / l;
+    if (p.gate) y = gated_by(y, p.gate[row * p.gate_row + h * p.gate_head + d]);
+    p.out[row * p.out_row + h * p.out_head + d] = __float2bfloat16_rn(pos < 0 ? 0.0f : y);
+  }
 }
 
 // How a call is cut.
@@ -101,25 +106,34 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
                                          std::min<int64_t>((int64_t)a->sinks / pl.tile + 1, tiles));
   }
   tiles = std::max<int64_t>(tiles, 1);
-  // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs (few rows: two to an
-  // SM), each as long as a piece and about three (two) tiles' time to begin and to end; a cut costs two more for the
-  // join.
   const int ctas = pl.block / kTileM;
   const int64_t each = pl.few ? 1 : (rows + pl.block - 1) / pl.block;  // blocks of a sequence, at most
-  const int64_t busy = std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas * c->n_kv;
-  const int64_t places = pl.few ? 2 * kPlanSms : kPlanSms;
-  int64_t best = -1;
+  const int64_t busy = std::max<int64_t>(1, std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas * c->n_kv);
   pl.splits = 1;
   pl.per_split = (int)tiles;
-  for (int64_t s = 1; s <= 512 && s <= tiles; ++s) {
+  if (pl.few) {
+    // Two or three blocks to an SM.  Pieces of 8 tiles (512 keys) or more, four rounds of them where there are that
+    // many: the sequences' lengths differ, and small pieces even that out.  With less than one round, pieces down to
+    // one tile.
+    const int64_t places = (rows <= 8 ? 3 : 2) * kPlanSms;
+    const int64_t four = std::max<int64_t>(1, 4 * places / busy), one = std::max<int64_t>(1, places / busy);
+    int64_t per = std::max<int64_t>(8, (tiles + four - 1) / four);
+    if ((tiles + per - 1) / per * busy < places) per = (tiles + one - 1) / one;
+    pl.per_split = (int)std::min(per, tiles);
+    pl.splits = (int)((tiles + pl.per_split - 1) / pl.per_split);
+    return pl;
+  }
+  // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each as long as a piece
+  // and about three tiles' time to begin and to end; a cut costs two more for the join.
+  int64_t best = -1;
+  for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
     const int64_t per = (tiles + s - 1) / s, n = (tiles + per - 1) / per;
-    const int64_t cost = (busy * n + places - 1) / places * (per + (pl.few ? 2 : 3)) + (n > 1 ? 2 : 0);
+    const int64_t cost = (busy * n + kPlanSms - 1) / kPlanSms * (per + 3) + (n > 1 ? 2 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       pl.splits = (int)n;
       pl.per_split = (int)per;
     }
-    if (busy * n > 4 * places) break;
   }
   return pl;
 }
@@ -134,9 +148,10 @@ size_t stat_bytes(const fak_attn_args* a, const Plan& pl) {
 
 template <int DH>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
+  const bool many = p.splits > 8;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)p.c.rows, (unsigned)p.nq);
+  cfg.gridDim = dim3((unsigned)p.c.rows, (unsigned)(many ? p.nq : (p.nq + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -144,7 +159,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<DH>, p);
+  return many ? cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 8>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 1>, p);
 }
 
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
@@ -182,10 +197,16 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   if (a->workspace_bytes < need) return FAK_ERR_SHAPE;
   if (pl.blocks > 0x3fffffff || cache->n_kv > 65535) return FAK_ERR_SHAPE;
   if (a->rows == 0 || batch->n_seqs == 0) return FAK_OK;
-  if ((st = kv_device(nullptr)) != FAK_OK) return st;
-  void* status = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&status, g_attn_status);
-  if (e != cudaSuccess) return fak_cuda_status(e);
+  int dev = 0;
+  if ((st = kv_device(&dev, nullptr)) != FAK_OK) return st;
+  static std::atomic<int*> words[64];  // the status word's address on each device
+  int* st_word = words[dev].load(std::memory_order_relaxed);
+  cudaError_t e = cudaSuccess;
+  if (!st_word) {
+    e = cudaGetSymbolAddress(reinterpret_cast<void**>(&st_word), g_attn_status);
+    if (e != cudaSuccess) return fak_cuda_status(e);
+    words[dev].store(st_word, std::memory_order_relaxed);
+  }
   p.c.rows = a->rows;
   p.c.max_q = a->max_q;
   p.c.max_kv = a->max_kv;
@@ -217,10 +238,9 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + parts);
   p.timeout_ns = 2000000000ull;
   cudaStream_t s = (cudaStream_t)stream;
-  int* st_word = static_cast<int*>(status);
-  e = pl.few ? attn_rows_launch(cache->kind, cache->dh, p, st_word, s)
+  e = pl.few ? attn_rows_launch(cache->kind, cache->dh, p, st_word, dev, s)
              : attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p,
-                                pl.blocks, st_word, s);
+                                pl.blocks, st_word, dev, s);
   if (e == cudaSuccess && pl.splits > 1)
     e = cache->dh == 64 ? launch_join<64>(p, s) : cache->dh == 128 ? launch_join<128>(p, s) : launch_join<256>(p, s);
   return fak_cuda_status(e);

@@ -121,5 +121,5 @@ FAK_DEV void attn_record(int* status, int code) { atomicCAS(status, 0, code); }
 
 // Host: launches of the kernels in the other files.
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
-                             int* status, cudaStream_t s);
-cudaError_t attn_rows_launch(int kind, int dh, const AttnParams& p, int* status, cudaStream_t s);
+                             int* status, int dev, cudaStream_t s);
+cudaError_t attn_rows_launch(int kind, int dh, const AttnParams& p, int* status, int dev, cudaStream_t s);

@@ -1,15 +1,16 @@
 // Attention of few rows over the paged KV cache: decode steps, where a sequence and KV head has at most 16 rows
 // (token, query head of the group) and all that counts is reading K and V once, at the memory's rate.
 //
-// A warp takes 16 keys at a time straight from memory into registers, in the layouts of the m16n8k16 matrix
-// instruction, with the keys and dims as its 16 and the rows as its 8 (6 rows of a group of 6 waste 2, not 10):
+// A warp takes 16 keys at a time, in the layouts of the m16n8k16 matrix instruction without any turning, with the keys and dims as its 16 and the rows as its 8 (6 rows of a group of 6 waste 2, not 10):
 //   S^T = K Q^T      A = K: lane (g, t) loads 16 bytes of keys g and g + 8, which are its dims of two (8-bit codes:
 //                    four) instructions; the dims come in another order than they stand, the same for Q
 //   O^T += V^T P^T   A = V^T: lane (g, t) loads 16 bytes of keys 2t, 2t + 1, 2t + 8 and 2t + 9 and pairs up
 //                    neighbouring keys' values; P^T from S^T by an 8 x 8 transpose within the warp
-// The next keys' loads are issued as soon as the registers are free, K's before the softmax and V's after the
-// product, so 8 warps keep 64 KB (8-bit: half) on their way on an SM.  Four warps share a block's keys in tiles
-// of 64 and add their sums at the end; a sequence's keys are cut over blocks, which the join kernel adds.
+// The bytes a lane will need come by asynchronous copies into shared memory slots of its own, which nothing but the lane
+// reads: no barrier, no bank conflict, and 12 warps with 16 KB each keep up to 192 KB on their way on an SM.
+// (Loads into registers instead, one step ahead, kept 32 to 64 KB: 86 us against a floor of 41 for a sequence of 131072
+// at 8 bits.)  Four warps share a block's keys in tiles of 64 and add their sums at the end; a sequence's keys
+// are cut over blocks, which the join kernel adds.
 // Each row's maximum moves only when passed by 8, as in the blocks' kernel (attn_tile.cu).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,15 +38,12 @@ FAK_DEV uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-FAK_DEV uint4 load_once(const void* p) {  // read once: not kept in L1
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-FAK_DEV uint2 load_once8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+template <int N>
+FAK_DEV void copy_async(void* dst, const void* src) {  // N = 4, 8 or 16 bytes
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(N) : "memory");
 }
 
 template <int DH, int KIND, int NT>
@@ -57,15 +55,22 @@ struct RCfg {
   static constexpr int ve = 16 / bytes < DH / 8 ? 16 / bytes : DH / 8;  // dims of a lane's V load
   static constexpr int vb = DH / (8 * ve);                     // V loads of a key and lane
   static constexpr int vw = ve * bytes / 4;                    // words of one
-  static constexpr int row = DH + 8;                           // floats of a row in shared memory
-  static constexpr int smem = kWarps * 8 * NT * row * 4;
+  // a lane's slots: halves of a step in turn, K and V of 16 keys
+  static constexpr int half = 16 * DH * bytes + (quant ? 512 : 0);  // bytes of a warp's (with 16 of scales a lane)
+  static constexpr int room = NT == 1 ? 18432 : 27648;  // a warp's: three (two) blocks of four on an SM
+  static constexpr int halves = room / half < 8 ? room / half & ~1 : 8;
+  static constexpr int row = DH + 8;  // floats of a row where the warps' sums meet
+  static constexpr int sums = kWarps * 8 * NT * row * 4;
+  static constexpr int smem = kWarps * halves * half > sums ? kWarps * halves * half : sums;
+  static_assert(halves >= 2 && halves % 2 == 0, "K and V take turns");
 };
 
 template <int DH, int KIND, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     attn_rows_kernel(const __grid_constant__ AttnParams p, int* status) {
   using C = RCfg<DH, KIND, NT>;
-  extern __shared__ float so[];  // [warp][8 NT rows][C::row]
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);  // at the end: [warp][8 NT rows][C::row]
   __shared__ float sm[kWarps][8 * NT], sl[kWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int seq = blockIdx.x, kvh = blockIdx.y;
@@ -101,49 +106,61 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     return at;
   };
-  uint4 kx[2][C::kb];
-  float ksc[2] = {}, vsc[2] = {};
-  uint32_t vx[4][C::vb][C::vw];
-  auto load_k = [&](int64_t at) {
+  uint8_t* const mine = smem + warp * (C::halves * C::half) + lane * 16;            // K's
+  uint8_t* const mine_v = smem + warp * (C::halves * C::half) + lane * C::vw * 4;  // V's
+  constexpr int vstep = 32 * C::vw * 4;
+  // lane (g, t)'s part of K, of V
+  auto fetch_k = [&](uint8_t* to, int64_t at) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t v = at + g + 8 * h;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int b = 0; b < C::kb; ++b) kx[h][b] = load_once(p.c.k + (v * DH + b * 4 * C::ke + t * C::ke) * C::bytes);
-      if constexpr (C::quant) {
-        ksc[h] = p.c.ks[v];
-        vsc[h] = p.c.vs[v];
+      for (int b = 0; b < C::kb; ++b)
+        copy_async<16>(to + (h * C::kb + b) * 512,
+                       p.c.k + ((at + g + 8 * h) * DH + b * 4 * C::ke + t * C::ke) * C::bytes);
+    if constexpr (C::quant) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        copy_async<4>(to + 2 * C::kb * 512 + 4 * h, p.c.ks + at + g + 8 * h);
+        copy_async<4>(to + 2 * C::kb * 512 + 8 + 4 * h, p.c.vs + at + g + 8 * h);
       }
     }
   };
-  auto load_v = [&](int64_t at) {
+  auto fetch_v = [&](uint8_t* to, int64_t at) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t v = at + 2 * t + (k & 1) + 8 * (k >> 1);
+    for (int b = 0; b < C::vb; ++b)
 #pragma unroll
-      for (int b = 0; b < C::vb; ++b) {
-        const uint8_t* src = p.c.v + (v * DH + b * 8 * C::ve + g * C::ve) * C::bytes;
-        if constexpr (C::vw == 4) {
-          const uint4 x = load_once(src);
-          vx[k][b][0] = x.x;
-          vx[k][b][1] = x.y;
-          vx[k][b][2] = x.z;
-          vx[k][b][3] = x.w;
-        } else {
-          const uint2 x = load_once8(src);
-          vx[k][b][0] = x.x;
-          vx[k][b][1] = x.y;
-        }
-      }
+      for (int k = 0; k < 4; ++k)
+        copy_async<C::vw * 4>(to + (b * 4 + k) * vstep,
+                              p.c.v + ((at + 2 * t + (k & 1) + 8 * (k >> 1)) * DH + b * 8 * C::ve + g * C::ve) * C::bytes);
+  };
+  // the steps: fetched up to halves / 2 ahead of the one at work
+  auto next = [&](int& i, int& j0) {
+    do {
+      j0 = first_key(++i);
+    } while (j0 < 0 && i < end);
+  };
+  int fi = begin - 1, fj;  // the step that is fetched
+  int64_t fat;
+  next(fi, fj);
+  fat = place(fj);
+  int i = fi, j0 = fj;
+  auto fetch = [&](int slot) {  // a half; a group without copies past the last step
+    if (fj >= 0) {
+      if (slot & 1)
+        fetch_v(mine_v + slot * C::half, fat);
+      else
+        fetch_k(mine + slot * C::half, fat);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (slot & 1) {
+      next(fi, fj);
+      fat = place(fj);
     }
   };
-  int i = begin, j0 = first_key(i);
-  while (j0 < 0 && i < end) j0 = first_key(++i);  // (a warp may have none at all)
-  int64_t at = place(j0);
-  if (j0 >= 0) {
-    load_k(at);
-    load_v(at);
-  }
+#pragma unroll
+  for (int h = 0; h < C::halves; ++h) fetch(h);
+  int slot = 0;
+  auto landed = [&]() { asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 1) : "memory"); };
 
   // Q: lane (g, t) holds row g's (and g + 8's) dims as K's loads bring them
   uint32_t q[NT][DH / 8];
@@ -180,23 +197,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
 
   while (j0 >= 0) {
-    int ni = i + 1, nj = first_key(ni);
-    while (nj < 0 && ni < end) nj = first_key(++ni);
-    const int64_t nat = place(nj);
+    landed();
+    const uint8_t* from = mine + slot * C::half;
     // scores of 16 keys: s[nt][c + 2 h] of key g + 8 h, row 2t + c + 8 nt
     float s[NT][4] = {};
 #pragma unroll
     for (int b = 0; b < C::kb; ++b) {
-      const uint32_t a0[4] = {kx[0][b].x, kx[0][b].y, kx[0][b].z, kx[0][b].w};
-      const uint32_t a1[4] = {kx[1][b].x, kx[1][b].y, kx[1][b].z, kx[1][b].w};
+      const uint4 x0 = *reinterpret_cast<const uint4*>(from + b * 512);
+      const uint4 x1 = *reinterpret_cast<const uint4*>(from + (C::kb + b) * 512);
+      const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
       if constexpr (C::quant) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          uint32_t x0, x1, y0, y1;
-          codes_to_bf16<KIND>(a0[w], x0, x1);
-          codes_to_bf16<KIND>(a1[w], y0, y1);
+          uint32_t k0, k1, l0, l1;
+          codes_to_bf16<KIND>(a0[w], k0, k1);
+          codes_to_bf16<KIND>(a1[w], l0, l1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], x0, y0, x1, y1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], k0, l0, k1, l1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
         }
       } else {
 #pragma unroll
@@ -208,13 +225,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     float kf[2] = {p.scale, p.scale}, vf[2];
     if constexpr (C::quant) {
-      kf[0] *= ksc[0];
-      kf[1] *= ksc[1];
-      vf[0] = vsc[0];
-      vf[1] = vsc[1];
+      const float4 f = *reinterpret_cast<const float4*>(from + 2 * C::kb * 512);
+      kf[0] *= f.x;
+      kf[1] *= f.y;
+      vf[0] = f.z;
+      vf[1] = f.w;
     }
     const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 15, p.window, p.sinks);
-    if (nj >= 0) load_k(nat);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -222,6 +239,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         s[nt][c] *= kf[c >> 1];
         if (cut && !sees(pos[nt][c & 1], j0 + g + 8 * (c >> 1), p.window, p.sinks)) s[nt][c] = -INFINITY;
       }
+    fetch(slot);  // (what stood there has been multiplied)
     uint32_t pb[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -260,54 +278,50 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       pb[nt][0] = transpose8(pack_bf16(w[0], w[1]));
       pb[nt][1] = transpose8(pack_bf16(w[2], w[3]));
     }
-    if (!C::quant && cut) {
-      // a weight of zero times a value that is not finite would be NaN: such values are left out of the product, and
-      // added for the rows that do see them; keys past the last that is seen are zeros
-      bool odd = false;
+    landed();
+    from = mine_v + (slot + 1) * C::half;
+    bool odd = false;
+#pragma unroll
+    for (int b = 0; b < C::vb; ++b) {
+      uint32_t vx[4][C::vw];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool past = j0 + 2 * t + (k & 1) + 8 * (k >> 1) > p_hi;
+        if constexpr (C::vw == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(from + (b * 4 + k) * vstep);
+          vx[k][0] = x.x;
+          vx[k][1] = x.y;
+          vx[k][2] = x.z;
+          vx[k][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(from + (b * 4 + k) * vstep);
+          vx[k][0] = x.x;
+          vx[k][1] = x.y;
+        }
+      }
+      if (!C::quant && cut) {
+        // a weight of zero times a value that is not finite would be NaN: such values are left out of the product,
+        // and added for the rows that do see them; keys past the last that is seen are zeros
 #pragma unroll
-        for (int b = 0; b < C::vb; ++b)
+        for (int k = 0; k < 4; ++k) {
+          const bool past = j0 + 2 * t + (k & 1) + 8 * (k >> 1) > p_hi;
 #pragma unroll
           for (int w = 0; w < C::vw; ++w) {
             bool change = false;
-            const uint32_t y = finite2(vx[k][b][w], change);
-            vx[k][b][w] = past ? 0u : y;
+            const uint32_t y = finite2(vx[k][w], change);
+            vx[k][w] = past ? 0u : y;
             odd |= change && !past;
           }
+        }
       }
-      if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-        for (int j = 0; j < min(16, p_hi + 1 - j0); ++j)
-#pragma unroll
-          for (int d = 0; d < DH / 16; ++d) {
-            // row sums of dims 8 (or ve) g + 2 (d % (ve / 2)), + 1 of block d / (ve / 2)
-            const uint32_t y = *reinterpret_cast<const uint32_t*>(
-                p.c.v + ((at + j) * DH + d / (C::ve / 2) * 8 * C::ve + g * C::ve + 2 * (d % (C::ve / 2))) * 2);
-            const float lo = __uint_as_float(y << 16), hi = __uint_as_float(y & 0xffff0000u);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                if (sees(pos[nt][c], j0 + j, p.window, p.sinks)) {
-                  if ((y & 0x7F80u) == 0x7F80u) o[nt][d][c] += lo;
-                  if ((y & 0x7F800000u) == 0x7F800000u) o[nt][d][c + 2] += hi;
-                }
-          }
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < C::vb; ++b) {
 #pragma unroll
       for (int w = 0; w < C::vw; ++w) {
         uint32_t x[4][2];  // key, pair of dims (bf16: one)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if constexpr (C::quant)
-            codes_to_bf16<KIND>(vx[k][b][w], x[k][0], x[k][1]);
+            codes_to_bf16<KIND>(vx[k][w], x[k][0], x[k][1]);
           else
-            x[k][0] = vx[k][b][w];
+            x[k][0] = vx[k][w];
         }
 #pragma unroll
         for (int h = 0; h < (C::quant ? 2 : 1); ++h) {
@@ -319,12 +333,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         }
       }
     }
-    if (nj >= 0) load_v(nat);
-    i = ni;
-    j0 = nj;
-    at = nat;
+    if (!C::quant && cut && __any_sync(0xffffffffu, odd)) {
+      int64_t at = place(j0);
+#pragma unroll 1
+      for (int j = 0; j < min(16, p_hi + 1 - j0); ++j)
+#pragma unroll
+        for (int d = 0; d < DH / 16; ++d) {
+          // o[nt][d]: dims ve g + 2 (d % (ve / 2)), + 1 of block d / (ve / 2)
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(
+              p.c.v + ((at + j) * DH + d / (C::ve / 2) * 8 * C::ve + g * C::ve + 2 * (d % (C::ve / 2))) * 2);
+          const float lo = __uint_as_float(y << 16), hi = __uint_as_float(y & 0xffff0000u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (sees(pos[nt][c], j0 + j, p.window, p.sinks)) {
+                if ((y & 0x7F80u) == 0x7F80u) o[nt][d][c] += lo;
+                if ((y & 0x7F800000u) == 0x7F800000u) o[nt][d][c + 2] += hi;
+              }
+        }
+    }
+    fetch(slot + 1);
+    slot = slot + 2 == C::halves ? 0 : slot + 2;
+    next(i, j0);
   }
 
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // the slots become the place where the sums meet
   // the four warps' sums
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -381,10 +416,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 template <int DH, int KIND, int NT>
-cudaError_t launch(const AttnParams& p, int* status, cudaStream_t s) {
+cudaError_t launch(const AttnParams& p, int* status, int dev, cudaStream_t s) {
   using C = RCfg<DH, KIND, NT>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_rows_kernel<DH, KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = kv_smem_limit(attn_rows_kernel<DH, KIND, NT>, C::smem, dev, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)p.c.n_seqs, (unsigned)p.c.n_kv, (unsigned)p.splits);
   attn_rows_kernel<DH, KIND, NT><<<grid, kWarps * 32, C::smem, s>>>(p, status);
@@ -392,21 +427,21 @@ cudaError_t launch(const AttnParams& p, int* status, cudaStream_t s) {
 }
 
 template <int DH, int KIND>
-cudaError_t by_rows(const AttnParams& p, int* status, cudaStream_t s) {
-  return p.c.max_q * p.group <= 8 ? launch<DH, KIND, 1>(p, status, s) : launch<DH, KIND, 2>(p, status, s);
+cudaError_t by_rows(const AttnParams& p, int* status, int dev, cudaStream_t s) {
+  return p.c.max_q * p.group <= 8 ? launch<DH, KIND, 1>(p, status, dev, s) : launch<DH, KIND, 2>(p, status, dev, s);
 }
 
 template <int DH>
-cudaError_t by_kind(int kind, const AttnParams& p, int* status, cudaStream_t s) {
-  return kind == FAK_KV_BF16   ? by_rows<DH, FAK_KV_BF16>(p, status, s)
-         : kind == FAK_KV_E4M3 ? by_rows<DH, FAK_KV_E4M3>(p, status, s)
-                               : by_rows<DH, FAK_KV_I8>(p, status, s);
+cudaError_t by_kind(int kind, const AttnParams& p, int* status, int dev, cudaStream_t s) {
+  return kind == FAK_KV_BF16   ? by_rows<DH, FAK_KV_BF16>(p, status, dev, s)
+         : kind == FAK_KV_E4M3 ? by_rows<DH, FAK_KV_E4M3>(p, status, dev, s)
+                               : by_rows<DH, FAK_KV_I8>(p, status, dev, s);
 }
 
 }  // namespace
 
-cudaError_t attn_rows_launch(int kind, int dh, const AttnParams& p, int* status, cudaStream_t s) {
-  return dh == 64    ? by_kind<64>(kind, p, status, s)
-         : dh == 128 ? by_kind<128>(kind, p, status, s)
-                     : by_kind<256>(kind, p, status, s);
+cudaError_t attn_rows_launch(int kind, int dh, const AttnParams& p, int* status, int dev, cudaStream_t s) {
+  return dh == 64    ? by_kind<64>(kind, p, status, dev, s)
+         : dh == 128 ? by_kind<128>(kind, p, status, dev, s)
+                     : by_kind<256>(kind, p, status, dev, s);
 }

@@ -947,7 +947,7 @@ bool code_map(CUtensorMap* map, void* base, bool quant, int dh, int64_t n_vec, i
 }
 
 template <int DH, int KIND, int CG>
-cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status, cudaStream_t s) {
+cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status, int dev, cudaStream_t s) {
   using C = Cfg<DH, KIND, CG>;
   cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
@@ -956,7 +956,8 @@ cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks,
   if (!code_map(&kmap, p.c.k, C::quant, DH, n_vec, C::quant ? C::panels * 64 : 64, krows, krows == 64 ? C::panels : 1) ||
       !code_map(&vmap, p.c.v, C::quant, DH, n_vec, C::quant ? C::dv : 64, vrows, C::dv / 64))
     return cudaErrorInvalidValue;
-  e = cudaFuncSetAttribute(attn_tile_kernel<DH, KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  static std::atomic<uint64_t> done{0};
+  e = kv_smem_limit(attn_tile_kernel<DH, KIND, CG>, C::smem, dev, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -974,21 +975,21 @@ cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks,
 }
 
 template <int DH, int CG>
-cudaError_t by_kind(int kind, const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status,
+cudaError_t by_kind(int kind, const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status, int dev,
                     cudaStream_t s) {
-  return kind == FAK_KV_BF16   ? launch<DH, FAK_KV_BF16, CG>(p, page, n_vec, blocks, status, s)
-         : kind == FAK_KV_E4M3 ? launch<DH, FAK_KV_E4M3, CG>(p, page, n_vec, blocks, status, s)
-                               : launch<DH, FAK_KV_I8, CG>(p, page, n_vec, blocks, status, s);
+  return kind == FAK_KV_BF16   ? launch<DH, FAK_KV_BF16, CG>(p, page, n_vec, blocks, status, dev, s)
+         : kind == FAK_KV_E4M3 ? launch<DH, FAK_KV_E4M3, CG>(p, page, n_vec, blocks, status, dev, s)
+                               : launch<DH, FAK_KV_I8, CG>(p, page, n_vec, blocks, status, dev, s);
 }
 
 }  // namespace
 
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
-                             int* status, cudaStream_t s) {
+                             int* status, int dev, cudaStream_t s) {
   if (p.block_shift == 8)
-    return dh == 128 ? by_kind<128, 2>(kind, p, page, n_vec, blocks, status, s)
-                     : by_kind<256, 2>(kind, p, page, n_vec, blocks, status, s);
-  return dh == 64    ? by_kind<64, 1>(kind, p, page, n_vec, blocks, status, s)
-         : dh == 128 ? by_kind<128, 1>(kind, p, page, n_vec, blocks, status, s)
-                     : by_kind<256, 1>(kind, p, page, n_vec, blocks, status, s);
+    return dh == 128 ? by_kind<128, 2>(kind, p, page, n_vec, blocks, status, dev, s)
+                     : by_kind<256, 2>(kind, p, page, n_vec, blocks, status, dev, s);
+  return dh == 64    ? by_kind<64, 1>(kind, p, page, n_vec, blocks, status, dev, s)
+         : dh == 128 ? by_kind<128, 1>(kind, p, page, n_vec, blocks, status, dev, s)
+                     : by_kind<256, 1>(kind, p, page, n_vec, blocks, status, dev, s);
 }

@@ -384,7 +384,7 @@ extern "C" int fak_kv_append(const fak_kv_cache* cache, const fak_kv_batch* batc
   if ((strides & m) || (bits & 15) || ((uintptr_t)r->rope & 7)) return FAK_ERR_ALIGN;
   if (r->rows == 0 || batch->n_seqs == 0) return FAK_OK;
   int sms = 0;
-  if ((st = kv_device(&sms)) != FAK_OK) return st;
+  if ((st = kv_device(nullptr, &sms)) != FAK_OK) return st;
   p.c.rows = r->rows;
   p.q = r->q;
   p.k = r->k;
@@ -426,7 +426,7 @@ extern "C" int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch,
   if (rows < 0 || rows > 0x7fffffff || cache->n_kv > 65535 * (kReadVec / 2)) return FAK_ERR_SHAPE;
   if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return FAK_ERR_ALIGN;
   if (rows == 0 || batch->n_seqs == 0) return FAK_OK;
-  if ((st = kv_device(nullptr)) != FAK_OK) return st;
+  if ((st = kv_device(nullptr, nullptr)) != FAK_OK) return st;
   p.c.rows = rows;
   p.k = k_out;
   p.v = v_out;

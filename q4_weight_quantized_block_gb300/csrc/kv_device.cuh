@@ -1,6 +1,7 @@
 // The paged KV cache as its kernels see it: the ragged batch, the places of
 // positions, and the host-side checks shared by kv.cu and attn.cu.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -90,15 +91,34 @@ static inline int kv_view(const fak_kv_cache* c, const fak_kv_batch* b, KvView* 
   return FAK_OK;
 }
 
-// FAK_OK when the current device is sm_103; its SM count into *sms.
-static inline int kv_device(int* sms) {
+// FAK_OK when the current device is sm_103.  The device's number into *dev, its SM count into *sms (either may
+// be null).  What a device is does not change: looked up once.
+static inline int kv_device(int* dev_out, int* sms) {
+  static std::atomic<int> known[64];  // 0: not looked up; SM count + 1, or -1 when it is another kind
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fak_cuda_status(e);
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) return FAK_ERR_UNSUPPORTED;
-  if (sms) cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 0 || dev >= 64) return FAK_ERR_UNSUPPORTED;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    int major = 0, minor = 0, count = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+    k = major == 10 && minor == 3 ? count + 1 : -1;
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  if (k < 0) return FAK_ERR_UNSUPPORTED;
+  if (dev_out) *dev_out = dev;
+  if (sms) *sms = k - 1;
   return FAK_OK;
+}
+
+// Raises a kernel's shared memory limit on device `dev` at its first launch there.
+template <typename K>
+static inline cudaError_t kv_smem_limit(K* kernel, int bytes, int dev, std::atomic<uint64_t>& done) {
+  if (done.load(std::memory_order_relaxed) >> dev & 1) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
 }
