@@ -20,15 +20,15 @@ __device__ int g_attn_status;
 
 constexpr int kPlanSms = 152;  // GB300's SMs: the workspace's size must not depend on the current device
 
-// Adds up the pieces of the blocks of rows whose keys were cut: W warps (1 or 8) to a (row, query head), each for
-// every W-th piece.
+// Adds up the pieces of the blocks of rows whose keys were cut: W warps (1, eight (row, query head)s to a block, or 16)
+// to a (row, query head), each for every W-th piece.
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i * sigmoid(gate),  M = max m_i
 // in an order that the pieces' number alone sets, so the result does not depend on which finished first.
 template <int DH, int W>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int N = DH / 32;
-  __shared__ float so[8][DH], sl[8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * (8 / W) + warp / W;
+__global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int N = DH / 32, kJoin = W == 1 ? 8 : 1;  // (row, query head)s of a block
+  __shared__ float so[W][DH], sl[W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * kJoin + warp / W;
   const int64_t row = blockIdx.x;
   const int s = kv_find_seq(p.c, row, lane);
   const KvSeq sq = kv_seq(p.c, s);
@@ -51,14 +51,28 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   const float zero = top == -INFINITY ? 0.0f : top;
   float o[N] = {}, l = 0.0f;
-#pragma unroll 4
-  for (int i = warp % W; i < pieces; i += W) {
-    const float2 st = p.stat[slot + i * step];
-    const float f = exp2_approx(st.x - zero);
-    l = fmaf(f, st.y, l);
-    const float* x = p.part + (slot + i * step) * DH + lane;
+  constexpr int U = 4;  // pieces in flight
+  for (int i0 = warp % W; i0 < pieces; i0 += U * W) {
+    float2 st[U];
+    float x[U][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[32 * k], o[k]);
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = slot + (int64_t)(i0 + u * W) * step;
+      st[u] = make_float2(-INFINITY, 0.0f);
+      if (i0 + u * W < pieces) {
+        st[u] = p.stat[at];
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[u][k] = p.part[at * DH + lane + 32 * k];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * W >= pieces) break;
+      const float f = exp2_approx(st[u].x - zero);
+      l = fmaf(f, st[u].y, l);
+#pragma unroll
+      for (int k = 0; k < N; ++k) o[k] = fmaf(f, x[u][k], o[k]);
+    }
   }
   if constexpr (W > 1) {
 #pragma unroll
@@ -68,7 +82,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     if (warp >= N) return;
     o[0] = l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < W; ++w) {
       o[0] += so[w][warp * 32 + lane];
       l += sl[w];
     }
@@ -98,7 +112,7 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   // pairs of CTAs where sequences have more rows than one CTA holds (and a half of V is at least 64 dims)
   pl.block = c->dh > 64 && rows > kTileM ? 2 * kTileM : kTileM;
   pl.blocks = pl.few ? b->n_seqs : a->rows * group / pl.block + b->n_seqs;  // see find_unit
-  pl.tile = pl.few ? kRowsN : kTileN;
+  pl.tile = !pl.few ? kTileN : c->kind == FAK_KV_BF16 || c->dh > 128 ? kRowsN : 2 * kRowsN;
   int64_t tiles = ((int64_t)a->max_kv + pl.tile - 1) / pl.tile;
   if (a->window) {
     const int64_t span = (pl.block + group - 1) / group;
@@ -112,13 +126,12 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   pl.splits = 1;
   pl.per_split = (int)tiles;
   if (pl.few) {
-    // Two or three blocks to an SM.  Pieces of 8 tiles (512 keys) or more, four rounds of them where there are that
-    // many: the sequences' lengths differ, and small pieces even that out.  With less than one round, pieces down to
-    // one tile.
-    const int64_t places = (rows <= 8 ? 3 : 2) * kPlanSms;
+    // Two or three blocks to an SM.  One sequence's pieces are all alike: one round of them.  Several sequences
+    // differ in length, which smaller pieces even out: four rounds, of pieces of 512 keys or more.
+    const int64_t places = (rows <= 8 && (c->kind != FAK_KV_BF16 || c->dh <= 128) ? 3 : 2) * kPlanSms, least = 512 / pl.tile;
     const int64_t four = std::max<int64_t>(1, 4 * places / busy), one = std::max<int64_t>(1, places / busy);
-    int64_t per = std::max<int64_t>(8, (tiles + four - 1) / four);
-    if ((tiles + per - 1) / per * busy < places) per = (tiles + one - 1) / one;
+    int64_t per = std::max<int64_t>(least, (tiles + four - 1) / four);
+    if (b->n_seqs == 1 || (tiles + per - 1) / per * busy < places) per = (tiles + one - 1) / one;
     pl.per_split = (int)std::min(per, tiles);
     pl.splits = (int)((tiles + pl.per_split - 1) / pl.per_split);
     return pl;
@@ -152,14 +165,14 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)p.c.rows, (unsigned)(many ? p.nq : (p.nq + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(many ? 512 : 256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 8>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 1>, p);
+  return many ? cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 16>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<DH, 1>, p);
 }
 
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
@@ -223,7 +236,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
   p.block_shift = pl.block == kTileM ? 7 : 8;
-  p.tile_shift = pl.few ? 6 : 7;
+  p.tile_shift = pl.tile == 64 ? 6 : 7;
   if (p.group > 1) {  // ceil(2^(31 + s) / group), s = ceil(log2 group): exact for r below 2^31
     int s = 1;
     while ((1 << s) < p.group) ++s;

@@ -34,7 +34,7 @@ struct AttnParams {
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA
 constexpr int kTileN = 128;  // keys of a tile of the blocks' kernel
 constexpr int kRowsMax = 16;  // most rows of a sequence and KV head that the kernel for few rows takes
-constexpr int kRowsN = 64;    // keys of its tiles
+constexpr int kRowsN = 64;    // keys of its tiles (8-bit codes and dh up to 128: twice as many)
 
 FAK_DEV int ceil_div(int a, int b) { return (a + b - 1) / b; }
 

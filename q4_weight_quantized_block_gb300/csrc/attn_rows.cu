@@ -7,9 +7,7 @@
 //   O^T += V^T P^T   A = V^T: lane (g, t) loads 16 bytes of keys 2t, 2t + 1, 2t + 8 and 2t + 9 and pairs up
 //                    neighbouring keys' values; P^T from S^T by an 8 x 8 transpose within the warp
 // The bytes a lane will need come by asynchronous copies into shared memory slots of its own, which nothing but the lane
-// reads: no barrier, no bank conflict, and 12 warps with 16 KB each keep up to 192 KB on their way on an SM.
-// (Loads into registers instead, one step ahead, kept 32 to 64 KB: 86 us against a floor of 41 for a sequence of 131072
-// at 8 bits.)  Four warps share a block's keys in tiles of 64 and add their sums at the end; a sequence's keys
+// reads: no barrier, no bank conflict, and 8 or 12 warps keep up to 200 KB on their way on an SM.  Four warps share a block's keys in tiles of 64 and add their sums at the end; a sequence's keys
 // are cut over blocks, which the join kernel adds.
 // Each row's maximum moves only when passed by 8, as in the blocks' kernel (attn_tile.cu).
 #include <cuda_bf16.h>
@@ -55,18 +53,22 @@ struct RCfg {
   static constexpr int ve = 16 / bytes < DH / 8 ? 16 / bytes : DH / 8;  // dims of a lane's V load
   static constexpr int vb = DH / (8 * ve);                     // V loads of a key and lane
   static constexpr int vw = ve * bytes / 4;                    // words of one
-  // a lane's slots: halves of a step in turn, K and V of 16 keys
-  static constexpr int half = 16 * DH * bytes + (quant ? 512 : 0);  // bytes of a warp's (with 16 of scales a lane)
-  static constexpr int room = NT == 1 ? 18432 : 27648;  // a warp's: three (two) blocks of four on an SM
-  static constexpr int halves = room / half < 8 ? room / half & ~1 : 8;
+  static constexpr int groups = quant && DH <= 128 ? 2 : 1;  // 16 keys each, of a step
+  // a lane's slots: halves of a step in turn, K and V
+  static constexpr int part = 16 * DH * bytes;                         // bytes of a warp's 16 keys
+  static constexpr int half = groups * (part + (quant ? 512 : 0));     // of a half (with 16 of scales a lane and group)
+  // three (16 rows, or steps of 16 KB: two) blocks of four warps on an SM, as many halves as then have room
+  static constexpr int blocks = NT == 1 && half < 8192 ? 3 : 2;
+  static constexpr int room = 113000 * 2 / blocks / kWarps - 512;
+  static constexpr int halves = room / half < 8 ? room / half : 8;
   static constexpr int row = DH + 8;  // floats of a row where the warps' sums meet
   static constexpr int sums = kWarps * 8 * NT * row * 4;
   static constexpr int smem = kWarps * halves * half > sums ? kWarps * halves * half : sums;
-  static_assert(halves >= 2 && halves % 2 == 0, "K and V take turns");
+  static_assert(halves >= 3, "a half is worked on while others come");
 };
 
 template <int DH, int KIND, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     attn_rows_kernel(const __grid_constant__ AttnParams p, int* status) {
   using C = RCfg<DH, KIND, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -84,22 +86,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
   const int nrows = (sq.r1 - sq.r0) * p.group;
   if (nrows == 0) return;
   const int p0 = sq.len - (sq.r1 - sq.r0), p_lo = p0, p_hi = sq.len - 1;
-  const KeyTiles kt = key_tiles(p_lo, p_hi, p.window, p.sinks, 6);
+  constexpr int tile = kWarps * 16 * C::groups;  // keys of a tile: 64 or 128
+  const KeyTiles kt = key_tiles(p_lo, p_hi, p.window, p.sinks, tile == 64 ? 6 : 7);
   const bool direct = p.splits == 1 || kt.n <= p.per_split;
   const int begin = direct ? 0 : (int)blockIdx.z * p.per_split;
   const int end = direct || (int)blockIdx.z == p.splits - 1 ? kt.n : min(kt.n, begin + p.per_split);
   if (direct ? blockIdx.z != 0 : begin >= end) return;
 
-  // this warp's 16 keys of tile i: their first, and its vector index; none of them seen: -1
-  auto first_key = [&](int i) {
-    if (i >= end) return -1;
-    const int j0 = key_tile(kt, i) * kRowsN + 16 * warp;
-    const bool none = j0 > p_hi || (p.window && j0 + 15 <= p_lo - p.window && j0 >= p.sinks);
-    return none ? -1 : j0;
+  // A warp's steps: its keys of one tile after the other, the sinks' tiles first.  Keys past the last that a row
+  // sees take that one's page; what lies there is masked.
+  auto next = [&](int& i, int& j0) {
+    ++i;
+    j0 = i >= end ? -1 : i == begin || i == kt.head ? key_tile(kt, i) * tile + 16 * C::groups * warp : j0 + tile;
   };
-  auto place = [&](int j0) {
-    if (j0 < 0) return (int64_t)0;
-    int64_t at = kv_place(p.c, seq, j0, kvh);
+  auto place = [&](int j) {
+    int64_t at = kv_place(p.c, seq, min(j, p_hi & ~15), kvh);
     if (at < 0) {
       attn_record(status, FAK_ERR_DEVICE);
       at = -1 - at;
@@ -111,56 +112,63 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
   constexpr int vstep = 32 * C::vw * 4;
   // lane (g, t)'s part of K, of V
   auto fetch_k = [&](uint8_t* to, int64_t at) {
+    const uint8_t* src = p.c.k + (at + g) * (DH * C::bytes) + t * 16;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int b = 0; b < C::kb; ++b)
-        copy_async<16>(to + (h * C::kb + b) * 512,
-                       p.c.k + ((at + g + 8 * h) * DH + b * 4 * C::ke + t * C::ke) * C::bytes);
+        copy_async<16>(to + (h * C::kb + b) * 512, src + h * 8 * DH * C::bytes + b * 64);
     if constexpr (C::quant) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        copy_async<4>(to + 2 * C::kb * 512 + 4 * h, p.c.ks + at + g + 8 * h);
-        copy_async<4>(to + 2 * C::kb * 512 + 8 + 4 * h, p.c.vs + at + g + 8 * h);
-      }
+      const float *ks = p.c.ks + at + g, *vs = p.c.vs + at + g;
+      copy_async<4>(to + C::part, ks);
+      copy_async<4>(to + C::part + 4, ks + 8);
+      copy_async<4>(to + C::part + 8, vs);
+      copy_async<4>(to + C::part + 12, vs + 8);
     }
   };
   auto fetch_v = [&](uint8_t* to, int64_t at) {
+    const uint8_t* src = p.c.v + (at + 2 * t) * (DH * C::bytes) + g * (C::vw * 4);
 #pragma unroll
     for (int b = 0; b < C::vb; ++b)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        copy_async<C::vw * 4>(to + (b * 4 + k) * vstep,
-                              p.c.v + ((at + 2 * t + (k & 1) + 8 * (k >> 1)) * DH + b * 8 * C::ve + g * C::ve) * C::bytes);
+        copy_async<C::vw * 4>(to + (b * 4 + k) * vstep, src + ((k & 1) + 8 * (k >> 1)) * DH * C::bytes + b * 8 * C::vw * 4);
   };
-  // the steps: fetched up to halves / 2 ahead of the one at work
-  auto next = [&](int& i, int& j0) {
-    do {
-      j0 = first_key(++i);
-    } while (j0 < 0 && i < end);
-  };
-  int fi = begin - 1, fj;  // the step that is fetched
-  int64_t fat;
+  // fetched up to halves / 2 steps ahead of the one at work
+  constexpr int G = C::groups, gpart = C::half / G;
+  int fi = begin - 1, fj = 0;  // the step that is fetched
   next(fi, fj);
-  fat = place(fj);
   int i = fi, j0 = fj;
-  auto fetch = [&](int slot) {  // a half; a group without copies past the last step
+  int64_t fat[G];
+  auto places = [&]() {
     if (fj >= 0) {
-      if (slot & 1)
-        fetch_v(mine_v + slot * C::half, fat);
-      else
-        fetch_k(mine + slot * C::half, fat);
+#pragma unroll
+      for (int x = 0; x < G; ++x) fat[x] = place(fj + 16 * x);
+    }
+  };
+  places();
+  auto fetch = [&](int slot, bool value) {  // a half; a group without copies past the last step
+    if (fj >= 0) {
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        if (value)
+          fetch_v(mine_v + slot * C::half + x * gpart, fat[x]);
+        else
+          fetch_k(mine + slot * C::half + x * gpart, fat[x]);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (slot & 1) {
+    if (value) {
       next(fi, fj);
-      fat = place(fj);
+      places();
     }
   };
+  constexpr bool oddly = C::halves % 2;  // then the half that comes into K's slot is V, and the other way round
 #pragma unroll
-  for (int h = 0; h < C::halves; ++h) fetch(h);
+  for (int h = 0; h < C::halves; ++h) fetch(h, h & 1);
   int slot = 0;
   auto landed = [&]() { asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 1) : "memory"); };
+  auto advance = [&]() { slot = slot + 1 == C::halves ? 0 : slot + 1; };
 
   // Q: lane (g, t) holds row g's (and g + 8's) dims as K's loads bring them
   uint32_t q[NT][DH / 8];
@@ -199,56 +207,68 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
   while (j0 >= 0) {
     landed();
     const uint8_t* from = mine + slot * C::half;
-    // scores of 16 keys: s[nt][c + 2 h] of key g + 8 h, row 2t + c + 8 nt
-    float s[NT][4] = {};
+    // scores: s[x][nt][c + 2 h] of key 16 x + g + 8 h, row 2t + c + 8 nt
+    float s[G][NT][4] = {};
+    float vf[G][2];
 #pragma unroll
-    for (int b = 0; b < C::kb; ++b) {
-      const uint4 x0 = *reinterpret_cast<const uint4*>(from + b * 512);
-      const uint4 x1 = *reinterpret_cast<const uint4*>(from + (C::kb + b) * 512);
-      const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
-      if constexpr (C::quant) {
+    for (int b = 0; b < C::kb; ++b)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t k0, k1, l0, l1;
-          codes_to_bf16<KIND>(a0[w], k0, k1);
-          codes_to_bf16<KIND>(a1[w], l0, l1);
+      for (int x = 0; x < G; ++x) {
+        const uint4 x0 = *reinterpret_cast<const uint4*>(from + x * gpart + b * 512);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(from + x * gpart + (C::kb + b) * 512);
+        const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
+        if constexpr (C::quant) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], k0, l0, k1, l1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
+          for (int w = 0; w < 4; ++w) {
+            uint32_t k0, k1, l0, l1;
+            codes_to_bf16<KIND>(a0[w], k0, k1);
+            codes_to_bf16<KIND>(a1[w], l0, l1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(s[x][nt], k0, l0, k1, l1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < 4; w += 2)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(s[x][nt], a0[w], a1[w], a0[w + 1], a1[w + 1], q[nt][4 * b + w], q[nt][4 * b + w + 1]);
         }
-      } else {
-#pragma unroll
-        for (int w = 0; w < 4; w += 2)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(s[nt], a0[w], a1[w], a0[w + 1], a1[w + 1], q[nt][4 * b + w], q[nt][4 * b + w + 1]);
       }
-    }
-    float kf[2] = {p.scale, p.scale}, vf[2];
-    if constexpr (C::quant) {
-      const float4 f = *reinterpret_cast<const float4*>(from + 2 * C::kb * 512);
-      kf[0] *= f.x;
-      kf[1] *= f.y;
-      vf[0] = f.z;
-      vf[1] = f.w;
-    }
-    const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 15, p.window, p.sinks);
+    const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 16 * G - 1, p.window, p.sinks);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s[nt][c] *= kf[c >> 1];
-        if (cut && !sees(pos[nt][c & 1], j0 + g + 8 * (c >> 1), p.window, p.sinks)) s[nt][c] = -INFINITY;
+    for (int x = 0; x < G; ++x) {
+      float kf[2] = {p.scale, p.scale};
+      if constexpr (C::quant) {
+        const float4 f = *reinterpret_cast<const float4*>(from + x * gpart + C::part);
+        kf[0] *= f.x;
+        kf[1] *= f.y;
+        vf[x][0] = f.z;
+        vf[x][1] = f.w;
       }
-    fetch(slot);  // (what stood there has been multiplied)
-    uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[x][nt][c] *= kf[c >> 1];
+          if (cut && !sees(pos[nt][c & 1], j0 + 16 * x + g + 8 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
+        }
+    }
+    fetch(slot, oddly);  // (what stood there has been multiplied)
+    advance();
+    uint32_t pb[G][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[c] = fmaxf(s[nt][c], s[nt][c + 2]);
+        top[c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+        if constexpr (G == 2) top[c] = fmaxf(top[c], fmaxf(s[G - 1][nt][c], s[G - 1][nt][c + 2]));
+      }
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], x));
+      for (int x = 4; x < 32; x <<= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], x));
+        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
       }
       const bool up0 = top[0] > m[nt][0] + 8.0f, up1 = top[1] > m[nt][1] + 8.0f;
       if (__any_sync(0xffffffffu, up0 || up1)) {
@@ -266,75 +286,80 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
           o[nt][d][3] *= f1;
         }
       }
-      float w[4];
+      const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float base = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1];
-        w[c] = exp2_approx(s[nt][c] - base);
-        l[nt][c & 1] += w[c];
-        // a weight of zero stays zero, whatever scale stands at its place
-        if constexpr (C::quant) w[c] = w[c] == 0.0f ? 0.0f : w[c] * vf[c >> 1];
+      for (int x = 0; x < G; ++x) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          w[c] = exp2_approx(s[x][nt][c] - base[c & 1]);
+          l[nt][c & 1] += w[c];
+          // a weight of zero stays zero, whatever scale stands at its place
+          if constexpr (C::quant) w[c] = w[c] == 0.0f ? 0.0f : w[c] * vf[x][c >> 1];
+        }
+        pb[x][nt][0] = transpose8(pack_bf16(w[0], w[1]));
+        pb[x][nt][1] = transpose8(pack_bf16(w[2], w[3]));
       }
-      pb[nt][0] = transpose8(pack_bf16(w[0], w[1]));
-      pb[nt][1] = transpose8(pack_bf16(w[2], w[3]));
     }
     landed();
-    from = mine_v + (slot + 1) * C::half;
+    from = mine_v + slot * C::half;
     bool odd = false;
 #pragma unroll
-    for (int b = 0; b < C::vb; ++b) {
-      uint32_t vx[4][C::vw];
+    for (int x = 0; x < G; ++x)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (C::vw == 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(from + (b * 4 + k) * vstep);
-          vx[k][0] = x.x;
-          vx[k][1] = x.y;
-          vx[k][2] = x.z;
-          vx[k][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(from + (b * 4 + k) * vstep);
-          vx[k][0] = x.x;
-          vx[k][1] = x.y;
-        }
-      }
-      if (!C::quant && cut) {
-        // a weight of zero times a value that is not finite would be NaN: such values are left out of the product,
-        // and added for the rows that do see them; keys past the last that is seen are zeros
+      for (int b = 0; b < C::vb; ++b) {
+        uint32_t vx[4][C::vw];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const bool past = j0 + 2 * t + (k & 1) + 8 * (k >> 1) > p_hi;
+          if constexpr (C::vw == 4) {
+            const uint4 y = *reinterpret_cast<const uint4*>(from + x * gpart + (b * 4 + k) * vstep);
+            vx[k][0] = y.x;
+            vx[k][1] = y.y;
+            vx[k][2] = y.z;
+            vx[k][3] = y.w;
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(from + x * gpart + (b * 4 + k) * vstep);
+            vx[k][0] = y.x;
+            vx[k][1] = y.y;
+          }
+        }
+        if (!C::quant && cut) {
+          // a weight of zero times a value that is not finite would be NaN: such values are left out of the
+          // product, and added for the rows that do see them; keys past the last that is seen are zeros
 #pragma unroll
-          for (int w = 0; w < C::vw; ++w) {
-            bool change = false;
-            const uint32_t y = finite2(vx[k][w], change);
-            vx[k][w] = past ? 0u : y;
-            odd |= change && !past;
+          for (int k = 0; k < 4; ++k) {
+            const bool past = j0 + 2 * t + (k & 1) + 8 * (k >> 1) > p_hi;
+#pragma unroll
+            for (int w = 0; w < C::vw; ++w) {
+              bool change = false;
+              const uint32_t y = finite2(vx[k][w], change);
+              vx[k][w] = past ? 0u : y;
+              odd |= change && !past;
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < C::vw; ++w) {
+          uint32_t y[4][2];  // key, pair of dims (bf16: one)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (C::quant)
+              codes_to_bf16<KIND>(vx[k][w], y[k][0], y[k][1]);
+            else
+              y[k][0] = vx[k][w];
+          }
+#pragma unroll
+          for (int h = 0; h < (C::quant ? 2 : 1); ++h) {
+            const int d = b * (C::ve / 2) + w * (C::quant ? 2 : 1) + h;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[nt][d], prmt(y[0][h], y[1][h], 0x5410), prmt(y[0][h], y[1][h], 0x7632),
+                       prmt(y[2][h], y[3][h], 0x5410), prmt(y[2][h], y[3][h], 0x7632), pb[x][nt][0], pb[x][nt][1]);
           }
         }
       }
-#pragma unroll
-      for (int w = 0; w < C::vw; ++w) {
-        uint32_t x[4][2];  // key, pair of dims (bf16: one)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (C::quant)
-            codes_to_bf16<KIND>(vx[k][w], x[k][0], x[k][1]);
-          else
-            x[k][0] = vx[k][w];
-        }
-#pragma unroll
-        for (int h = 0; h < (C::quant ? 2 : 1); ++h) {
-          const int d = b * (C::ve / 2) + w * (C::quant ? 2 : 1) + h;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(o[nt][d], prmt(x[0][h], x[1][h], 0x5410), prmt(x[0][h], x[1][h], 0x7632),
-                     prmt(x[2][h], x[3][h], 0x5410), prmt(x[2][h], x[3][h], 0x7632), pb[nt][0], pb[nt][1]);
-        }
-      }
-    }
     if (!C::quant && cut && __any_sync(0xffffffffu, odd)) {
-      int64_t at = place(j0);
+      const int64_t at = place(j0);
 #pragma unroll 1
       for (int j = 0; j < min(16, p_hi + 1 - j0); ++j)
 #pragma unroll
@@ -353,8 +378,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               }
         }
     }
-    fetch(slot + 1);
-    slot = slot + 2 == C::halves ? 0 : slot + 2;
+    fetch(slot, !oddly);
+    advance();
     next(i, j0);
   }
 
