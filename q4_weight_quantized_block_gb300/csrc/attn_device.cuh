@@ -92,19 +92,29 @@ FAK_DEV uint32_t hsub2_bf16(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Four 8-bit codes as four bf16, exactly.  e4m3: its exponent and significand bits set as bf16's stand for the
-// value times 2^-120 (subnormals too).  int8: 128 + the low seven bits, less 128 or, for the negative, 256.
+// Two 8-bit codes, spread to the halves of a word by prmt, as two bf16, exactly.
+//   e4m3 (in the halves' upper bytes): its exponent and significand bits set as bf16's stand for the value times 2^-120,
+//   subnormals too.  int8 (in the lower bytes): 128 + the low seven bits, less 128 or, for the negative, 256.
+// The other bytes may hold anything.
+template <int KIND>
+FAK_DEV uint32_t spread_to_bf16(uint32_t a) {
+  if constexpr (KIND == FAK_KV_E4M3)
+    return hmul2_bf16(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), 0x7B807B80u);
+  else
+    return hsub2_bf16((a & 0x007F007Fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
+}
+
+// The four codes of a word, in order.
 template <int KIND>
 FAK_DEV void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KIND == FAK_KV_E4M3) {
-    const uint32_t a = prmt(w, 0, 0x1404), b = prmt(w, 0, 0x3424);
-    lo = hmul2_bf16(((a >> 4) & 0x07F007F0u) | (a & 0x80008000u), 0x7B807B80u);
-    hi = hmul2_bf16(((b >> 4) & 0x07F007F0u) | (b & 0x80008000u), 0x7B807B80u);
-  } else {
-    const uint32_t a = prmt(w, 0, 0x4140), b = prmt(w, 0, 0x4342);
-    lo = hsub2_bf16((a & 0x007F007Fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
-    hi = hsub2_bf16((b & 0x007F007Fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
-  }
+  lo = spread_to_bf16<KIND>(prmt(w, w, 0x1100));
+  hi = spread_to_bf16<KIND>(prmt(w, w, 0x3322));
+}
+
+// Code e of word v, code e of word w.
+template <int KIND>
+FAK_DEV uint32_t code_pair(uint32_t v, uint32_t w, int e) {
+  return spread_to_bf16<KIND>(prmt(v, w, 0x4400u + 0x1111u * (uint32_t)e));
 }
 
 // bf16 pair with values that are not finite made zero; sets odd if there was one

@@ -24,7 +24,7 @@ namespace {
 constexpr int kWarps = 4;
 
 FAK_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -166,10 +166,6 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   constexpr bool oddly = C::halves % 2;  // then the half that comes into K's slot is V, and the other way round
 #pragma unroll
   for (int h = 0; h < C::halves; ++h) fetch(h, h & 1);
-  int slot = 0;
-  auto landed = [&]() { asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 1) : "memory"); };
-  auto advance = [&]() { slot = slot + 1 == C::halves ? 0 : slot + 1; };
-
   // Q: lane (g, t) holds row g's (and g + 8's) dims as K's loads bring them
   uint32_t q[NT][DH / 8];
   int pos[NT][2];
@@ -204,12 +200,18 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
       l[nt][c] = 0.0f;
     }
 
-  while (j0 >= 0) {
-    landed();
-    const uint8_t* from = mine + slot * C::half;
-    // scores: s[x][nt][c + 2 h] of key 16 x + g + 8 h, row 2t + c + 8 nt
-    float s[G][NT][4] = {};
-    float vf[G][2];
+  // The product of a step runs beside the scores of the next, which do not depend on it: converting codes, half the
+  // instructions, fills the gaps that one of the two would leave.
+  float s[G][NT][4];  // s[x][nt][c + 2 h]: key 16 x + g + 8 h, row 2t + c + 8 nt
+  float kf[G][2], vn[G][2] = {}, vf[G][2];  // the scales of the scores' keys and values, of the weights' values
+  uint32_t pb[G][NT][2];
+  auto scores = [&](const uint8_t* from) {
+#pragma unroll
+    for (int x = 0; x < G; ++x)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[x][nt][c] = 0.0f;
 #pragma unroll
     for (int b = 0; b < C::kb; ++b)
 #pragma unroll
@@ -235,28 +237,31 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
               mma16816(s[x][nt], a0[w], a1[w], a0[w + 1], a1[w + 1], q[nt][4 * b + w], q[nt][4 * b + w + 1]);
         }
       }
-    const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 16 * G - 1, p.window, p.sinks);
+    if constexpr (C::quant) {
+#pragma unroll
+      for (int x = 0; x < G; ++x) {
+        const float4 f = *reinterpret_cast<const float4*>(from + x * gpart + C::part);
+        vn[x][0] = f.z;
+        vn[x][1] = f.w;
+        kf[x][0] = f.x * p.scale;
+        kf[x][1] = f.y * p.scale;
+      }
+    }
+  };
+  auto softmax = [&](int sj) {
+    const bool scut = keys_cut(p_lo, p_hi, sj, sj + 16 * G - 1, p.window, p.sinks);
 #pragma unroll
     for (int x = 0; x < G; ++x) {
-      float kf[2] = {p.scale, p.scale};
-      if constexpr (C::quant) {
-        const float4 f = *reinterpret_cast<const float4*>(from + x * gpart + C::part);
-        kf[0] *= f.x;
-        kf[1] *= f.y;
-        vf[x][0] = f.z;
-        vf[x][1] = f.w;
-      }
+      vf[x][0] = vn[x][0];
+      vf[x][1] = vn[x][1];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s[x][nt][c] *= kf[c >> 1];
-          if (cut && !sees(pos[nt][c & 1], j0 + 16 * x + g + 8 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
+          s[x][nt][c] *= C::quant ? kf[x][c >> 1] : p.scale;
+          if (scut && !sees(pos[nt][c & 1], sj + 16 * x + g + 8 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
         }
     }
-    fetch(slot, oddly);  // (what stood there has been multiplied)
-    advance();
-    uint32_t pb[G][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top[2];
@@ -301,8 +306,22 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         pb[x][nt][1] = transpose8(pack_bf16(w[2], w[3]));
       }
     }
-    landed();
-    from = mine_v + slot * C::half;
+  };
+  if (j0 >= 0) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 1) : "memory");
+    scores(mine);
+    fetch(0, oddly);  // (what stood there has been multiplied)
+    softmax(j0);
+  }
+  int slot = 1;
+  while (j0 >= 0) {
+    int ni = i, nj = j0;
+    next(ni, nj);
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 2) : "memory");
+    const int kslot = slot + 1 == C::halves ? 0 : slot + 1;
+    const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 16 * G - 1, p.window, p.sinks);
+    scores(mine + kslot * C::half);  // (past the last step: of what stood there, and not used)
+    const uint8_t* from = mine_v + slot * C::half;
     bool odd = false;
 #pragma unroll
     for (int x = 0; x < G; ++x)
@@ -340,21 +359,25 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         }
 #pragma unroll
         for (int w = 0; w < C::vw; ++w) {
-          uint32_t y[4][2];  // key, pair of dims (bf16: one)
+          // (key 2t, 2t + 1), (2t + 8, 2t + 9): each of the word's dims
+          uint32_t y[C::quant ? 4 : 2][2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (C::quant)
-              codes_to_bf16<KIND>(vx[k][w], y[k][0], y[k][1]);
-            else
-              y[k][0] = vx[k][w];
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t v0 = vx[2 * k][w], v1 = vx[2 * k + 1][w];
+            if constexpr (C::quant) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e][k] = code_pair<KIND>(v0, v1, e);
+            } else {
+              y[0][k] = prmt(v0, v1, 0x5410);
+              y[1][k] = prmt(v0, v1, 0x7632);
+            }
           }
 #pragma unroll
           for (int h = 0; h < (C::quant ? 2 : 1); ++h) {
             const int d = b * (C::ve / 2) + w * (C::quant ? 2 : 1) + h;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(o[nt][d], prmt(y[0][h], y[1][h], 0x5410), prmt(y[0][h], y[1][h], 0x7632),
-                       prmt(y[2][h], y[3][h], 0x5410), prmt(y[2][h], y[3][h], 0x7632), pb[x][nt][0], pb[x][nt][1]);
+              mma16816(o[nt][d], y[2 * h][0], y[2 * h + 1][0], y[2 * h][1], y[2 * h + 1][1], pb[x][nt][0], pb[x][nt][1]);
           }
         }
       }
@@ -379,8 +402,11 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         }
     }
     fetch(slot, !oddly);
-    advance();
-    next(i, j0);
+    fetch(kslot, oddly);
+    if (nj >= 0) softmax(nj);
+    slot = kslot + 1 == C::halves ? 0 : kslot + 1;
+    i = ni;
+    j0 = nj;
   }
 
   asm volatile("cp.async.wait_all;" ::: "memory");
