@@ -17,8 +17,8 @@
 //   warps 9, 10    TMA of K and of V by pages, each into a ring of its own (one warp needs some 500 cycles for a
 //                  stage), in the 128-byte-swizzled layouts the MMAs read: Q and K 64 dims wide with the dims
 //                  running (K-major), V keys by dims as stored (MN-major)
-//   warps 12-15    for an 8-bit cache, codes to bf16: the copies land in rings of their own and these warps fill
-//                  the MMAs' rings from them; for a bf16 cache, V of the tiles that a mask cuts
+//   warps 12-19    for an 8-bit cache, codes to bf16, four warps K's and four V's: the copies land in rings of their own and they fill the
+//                  MMAs' rings from them (12-15, for a bf16 cache: V of the tiles that a mask cuts is mended)
 // S has two or three buffers, so the next tile's S = Q K^T runs while the softmax works.
 // 8-bit codes become bf16 exactly; their scales multiply the scores' columns and the weights instead.
 // A weight of zero times a value that is not finite would be NaN, so in the tiles that a mask cuts a bf16 V is
@@ -62,7 +62,8 @@ struct Cfg {
   // tiles whose scales are held at once: a tile's are loaded when the K of the tile rs + ks stages back is done
   // with, and with it the softmax of the tile sbufs further back
   static constexpr int slots = (rs + ks + chunks - 1) / chunks + sbufs;
-  static constexpr int threads = 16 * 32;
+  static constexpr int warps = quant ? 20 : 16;
+  static constexpr int threads = warps * 32;
   static constexpr int off_k = kTileM * DH * 2;
   static constexpr int off_v = off_k + ks * stage;
   static constexpr int off_rk = off_v + vs * stage;
@@ -336,8 +337,8 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     }
     for (int s = 0; s < 2; ++s) mbar_init(&odone[s], 1);
     for (int s = 0; s < 4; ++s) mbar_init(&pair[s], 2);
-    mbar_init(qfull, 14 * CG);
-    mbar_init(pdone, 4 * CG);
+    mbar_init(qfull, (C::warps - 2) * CG);
+    mbar_init(pdone, (C::warps - 12) * CG);
     mbar_init(drain, 1);
     mbar_init(tready, 1);
     *abort = 0;
@@ -382,12 +383,13 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   };
   if (warp != 9 && warp != 10) {
     // Q: rows of the block, 64 dims to a 16 KB panel, by all warps but the TMA's; rows past the block's are zeros
-    constexpr int lanes = DH / 8, each = (kTileM * lanes + 14 * 32 - 1) / (14 * 32);  // 16 bytes to a lane
+    constexpr int lanes = DH / 8, loaders = (C::warps - 2) * 32;
+    constexpr int each = (kTileM * lanes + loaders - 1) / loaders;  // 16 bytes to a lane
     const int tid = (warp < 9 ? warp : warp - 2) * 32 + lane, c = tid % lanes;
     uint4 x[each];
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const int row = (k * 14 * 32 + tid) / lanes, r = u.rbase + row, token = p.by_group(r);
+      const int row = (k * loaders + tid) / lanes, r = u.rbase + row, token = p.by_group(r);
       x[k] = make_uint4(0, 0, 0, 0);
       if (row < u.nrows)
         x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.row0 + token) * p.q_row +
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     }
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const int row = (k * 14 * 32 + tid) / lanes;
+      const int row = (k * loaders + tid) / lanes;
       if (row < kTileM)
         *reinterpret_cast<uint4*>(smem + (c >> 3) * kPanel + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
     }
@@ -414,6 +416,15 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   const uint32_t tmem = warp <= 8 ? *reinterpret_cast<volatile uint32_t*>(tmem_slot) : 0;
   const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
 
+  // Twenty warps start with 96 registers each (61440 in all): 128 for the softmax, 80 for the conversion, 56 for the rest.
+  if constexpr (C::quant) {
+    if (warp < 8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    else if (warp < 12)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
   if (warp < 8) {
     // ---------------- softmax
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
@@ -449,7 +460,8 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
             mul2(t[k + 2], t[k + 3], f.z, f.w);
           }
         }
-        if (tile_cut(u.own_lo, u.own_hi, tile, p)) {
+        const bool cut = tile_cut(u.own_lo, u.own_hi, tile, p);
+        if (cut) {
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!sees(pos, j0 + k, p.window, p.sinks)) t[k] = -INFINITY;
@@ -499,11 +511,17 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
             add2(sum[0], sum[1], e[j], e[j + 1]);
           }
           if constexpr (C::quant) {
-            // a weight of zero stays zero, whatever scale stands at its place
             const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + k);
-            const float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e[j] = e[j] == 0.0f ? 0.0f : e[j] * v[j];
+            if (cut) {
+              // a weight of zero stays zero, whatever scale stands at the place of a key that is not seen
+              e[0] = e[0] == 0.0f ? 0.0f : e[0] * f.x;
+              e[1] = e[1] == 0.0f ? 0.0f : e[1] * f.y;
+              e[2] = e[2] == 0.0f ? 0.0f : e[2] * f.z;
+              e[3] = e[3] == 0.0f ? 0.0f : e[3] * f.w;
+            } else {
+              mul2(e[0], e[1], f.x, f.y);
+              mul2(e[2], e[3], f.z, f.w);
+            }
           }
           w[k / 2] = pack_bf16(e[0], e[1]);
           w[k / 2 + 1] = pack_bf16(e[2], e[3]);
@@ -798,62 +816,62 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   } else if (warp >= 12) {
     // ---------------- codes to bf16, V of cut tiles
     constexpr int T = 128;
-    const int tid = threadIdx.x - 12 * 32;
     bool ok = true;
     if constexpr (C::quant) {
-      // two streams of stages, K's and V's, in the order the MMAs take them: K 0, K 1, V 0, K 2, V 1, ...
-      struct Stream {
-        int rs, rph, st, ph;
-      };
-      Stream sk{0, 0, 0, 1}, sv{0, 0, 0, 1};
-      auto convert = [&](bool value, Stream& m) {
-        // 16 codes to a thread and step
-        constexpr int kwidth = C::panels * 4, vwidth = C::dv / 16;
-#pragma unroll 1
-        for (int c = 0; c < C::chunks; ++c) {
-          if (!(ok = ok && wait(&(value ? rvfull : rkfull)[m.rs], m.rph))) return;
-          const uint4* src = reinterpret_cast<const uint4*>(smem + (value ? C::off_rv : C::off_rk) + m.rs * C::raw);
-          uint8_t* dst = smem + (value ? C::off_v : C::off_k) + m.st * C::stage;
-          uint4 q[4];
+      // warps 12-15 K's stages, 16-19 V's; 16 codes to a thread and step
+      const bool value = warp >= 16;
+      const int tid = threadIdx.x - (value ? 16 : 12) * 32;
+      constexpr int kwidth = C::panels * 4, vwidth = C::dv / 16;
+      const int width_shift = value ? 31 - __clz(vwidth) : 31 - __clz(kwidth);
+      const int panel = value ? C::vkeys * 128 : 8192;
+      uint64_t *const rfull = value ? rvfull : rkfull, *const rempty = value ? rvempty : rkempty;
+      uint64_t *const free = value ? vempty : kempty, *const fills = value ? vfull : kfull;
+      const uint32_t fills_first = CG == 1 ? smem_u32(fills) : map_to(fills, 0);
+      const int stages = value ? C::vs : C::ks;
+      const uint8_t* const raw = smem + (value ? C::off_rv : C::off_rk);
+      uint8_t* const ring = smem + (value ? C::off_v : C::off_k);
+      int rs = 0, rph = 0, st = 0, ph = 1;
+      for (int i = 0; i < n * C::chunks && ok; ++i) {
+        if (!(ok = wait(&rfull[rs], rph))) break;
+        const uint4* src = reinterpret_cast<const uint4*>(raw + rs * C::raw);
+        uint8_t* dst = ring + st * C::stage;
+        uint4 q[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q[k] = src[tid + k * T];
-          if (!(ok = wait(&(value ? vempty : kempty)[m.st], m.ph))) return;
+        for (int k = 0; k < 4; ++k) q[k] = src[tid + k * T];
+        if (!(ok = wait(&free[st], ph))) break;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = tid + k * T;
-            const int key = value ? e / vwidth : e / kwidth, d = (value ? e % vwidth : e % kwidth) * 16;
-            uint4 a, b;
-            codes_to_bf16<KIND>(q[k].x, a.x, a.y);
-            codes_to_bf16<KIND>(q[k].y, a.z, a.w);
-            codes_to_bf16<KIND>(q[k].z, b.x, b.y);
-            codes_to_bf16<KIND>(q[k].w, b.z, b.w);
-            uint8_t* line = dst + (d >> 6) * (value ? C::vkeys * 128 : 8192) + key * 128;
-            const int e16 = (d & 63) >> 3;
-            *reinterpret_cast<uint4*>(line + ((e16 ^ (key & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(line + (((e16 + 1) ^ (key & 7)) << 4)) = b;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            arrive_first<CG>(&(value ? vfull : kfull)[m.st]);
-            mbar_arrive(&(value ? rvempty : rkempty)[m.rs]);  // after the stores, which came after the loads
-          }
-          if (++m.rs == C::rs) {
-            m.rs = 0;
-            m.rph ^= 1;
-          }
-          if (++m.st == (value ? C::vs : C::ks)) {
-            m.st = 0;
-            m.ph ^= 1;
-          }
+        for (int k = 0; k < 4; ++k) {
+          const int e = tid + k * T, key = e >> width_shift, d = (e & ((1 << width_shift) - 1)) * 16;
+          uint4 a, b;
+          codes_to_bf16<KIND>(q[k].x, a.x, a.y);
+          codes_to_bf16<KIND>(q[k].y, a.z, a.w);
+          codes_to_bf16<KIND>(q[k].z, b.x, b.y);
+          codes_to_bf16<KIND>(q[k].w, b.z, b.w);
+          uint8_t* line = dst + (d >> 6) * panel + key * 128;
+          const int e16 = (d & 63) >> 3;
+          *reinterpret_cast<uint4*>(line + ((e16 ^ (key & 7)) << 4)) = a;
+          *reinterpret_cast<uint4*>(line + (((e16 + 1) ^ (key & 7)) << 4)) = b;
         }
-      };
-      for (int i = 0; i < min(C::sbufs, n) && ok; ++i) convert(false, sk);
-      for (int i = 0; i < n && ok; ++i) {
-        convert(true, sv);
-        if (ok && i + C::sbufs < n) convert(false, sk);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1)
+            mbar_arrive(&fills[st]);
+          else
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(fills_first + 8 * st) : "memory");
+          mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
+        }
+        if (++rs == C::rs) {
+          rs = 0;
+          rph ^= 1;
+        }
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
     } else {
+      const int tid = threadIdx.x - 12 * 32;
       uint32_t landed = 0;  // parity of each stage's next use of `clean`
       const int vshift = min(p.c.page_shift, 31 - __clz(C::vkeys));
       for (int i = 0; i < n && ok; ++i) {
