@@ -30,8 +30,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __g
   __shared__ float so[W][DH], sl[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * kJoin + warp / W;
   const int64_t row = blockIdx.x;
-  const int s = kv_find_seq(p.c, row, lane);
-  const KvSeq sq = kv_seq(p.c, s);
+  int s;
+  const KvSeq sq = kv_locate(p.c, row, lane, s);
   // the pieces' kernel is done (every block waits: this grid must not end before that one)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;

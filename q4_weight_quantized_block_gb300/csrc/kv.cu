@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
                        : static_cast<const T*>(p.v) + row * p.v_row + (h - p.nq - p.c.n_kv) * p.v_head;
     load_vals<N>(src + lane * N, x[u]);
   }
-  const int s = kv_find_seq(p.c, row, lane);
-  const KvSeq q = kv_seq(p.c, s);
+  int s;
+  const KvSeq q = kv_locate(p.c, row, lane, s);
   if (!q.ok) {
     if (threadIdx.x == 0) kv_record();
     return;
@@ -192,6 +192,20 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     cs[threadIdx.x] = make_float2(co, sn);
   }
   if (half) __syncthreads();
+  // this lane's sines and cosines, and where its rotary partners are; the gains stay while the vectors are of one kind
+  const int span = half / N;  // lanes of one half; N divides rot / 2
+  const bool in = lane < 2 * span, low = lane < span;
+  const int other = in ? (low ? lane + span : lane - span) : lane;
+  float co[N], si[N], gain[N];
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 c = cs[(low ? lane : other) * N + i];
+      co[i] = c.x;
+      si[i] = low ? -c.y : c.y;
+    }
+  }
+  const float* held = nullptr;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int h = first + u;
@@ -199,28 +213,23 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
     const bool isq = h < p.nq, isk = !isq && h < p.nq + p.c.n_kv;
     const float* w = isq ? p.qw : isk ? p.kw : nullptr;
     if (w) {
+      if (w != held) load_vals<N>(w + lane * N, gain);
+      held = w;
       float ss = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) ss = fmaf(x[u][i], x[u][i], ss);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = 1.0f / sqrtf(ss / (float)DH + p.eps);
-      float g[N];
-      load_vals<N>(w + lane * N, g);
+      // (rsqrtf is off by 2 units in the last place at most; a square root and a division take 40 instructions)
+      const float r = rsqrtf(fmaf(ss, 1.0f / DH, p.eps));
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[u][i] = x[u][i] * r * g[i];
+      for (int i = 0; i < N; ++i) x[u][i] *= r * gain[i];
     }
     if (half && (isq || isk)) {
-      const int span = half / N;  // lanes of one half; N divides rot / 2
-      const bool low = lane < span, in = lane < 2 * span;
-      const int other = in ? (low ? lane + span : lane - span) : lane;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float y = __shfl_sync(0xffffffffu, x[u][i], other);
-        if (in) {
-          const float2 c = cs[(low ? lane : other) * N + i];
-          x[u][i] = low ? x[u][i] * c.x - y * c.y : x[u][i] * c.x + y * c.y;
-        }
+        if (in) x[u][i] = fmaf(y, si[i], x[u][i] * co[i]);
       }
     }
     if (isq) {
@@ -251,8 +260,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
   if (row >= p.c.rows) return;
-  const int s = kv_find_seq(p.c, row, lane);
-  const KvSeq q = kv_seq(p.c, s);
+  int s;
+  const KvSeq q = kv_locate(p.c, row, lane, s);
   if (!q.ok) {
     if (lane == 0) kv_record();
     return;

@@ -27,13 +27,17 @@ struct KvSeq {
   bool ok;
 };
 
+FAK_DEV bool kv_seq_ok(const KvView& c, const KvSeq& q) {
+  return q.r0 >= 0 && q.r0 <= q.r1 && q.r1 <= c.rows && q.len >= 0 &&
+         (int64_t)q.len <= ((int64_t)c.max_pages << c.page_shift) && q.r1 - q.r0 <= c.max_q && q.len <= c.max_kv;
+}
+
 FAK_DEV KvSeq kv_seq(const KvView& c, int s) {
   KvSeq q;
   q.r0 = c.row_start[s];
   q.r1 = c.row_start[s + 1];
   q.len = c.kv_len[s];
-  q.ok = q.r0 >= 0 && q.r0 <= q.r1 && q.r1 <= c.rows && q.len >= 0 &&
-         (int64_t)q.len <= ((int64_t)c.max_pages << c.page_shift) && q.r1 - q.r0 <= c.max_q && q.len <= c.max_kv;
+  q.ok = kv_seq_ok(c, q);
   return q;
 }
 
@@ -48,6 +52,24 @@ FAK_DEV int kv_find_seq(const KvView& c, int64_t row, int lane) {
     hi = min(lo + step, hi);
   }
   return lo;
+}
+
+// A row's sequence s and its numbers (a whole warp calls).  Up to 31 sequences' numbers are read at once, which
+// saves a trip to memory.
+FAK_DEV KvSeq kv_locate(const KvView& c, int64_t row, int lane, int& s) {
+  if (c.n_seqs < 32) {
+    const int start = lane <= c.n_seqs ? c.row_start[lane] : 0x7fffffff;
+    const int len = lane < c.n_seqs ? c.kv_len[lane] : 0;
+    s = max(__popc(__ballot_sync(0xffffffffu, lane < c.n_seqs && start <= row)) - 1, 0);
+    KvSeq q;
+    q.r0 = __shfl_sync(0xffffffffu, start, s);
+    q.r1 = __shfl_sync(0xffffffffu, start, s + 1);
+    q.len = __shfl_sync(0xffffffffu, len, s);
+    q.ok = kv_seq_ok(c, q);
+    return q;
+  }
+  s = kv_find_seq(c, row, lane);
+  return kv_seq(c, s);
 }
 
 // The vector index (page, head, slot) of position `pos` of sequence s; -1 - that of page 0 when the
