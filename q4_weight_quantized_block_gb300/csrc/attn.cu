@@ -36,12 +36,10 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __g
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
   if (W == 1 && h >= p.nq) return;
-  const int token = (int)(row - sq.r0), hh = h - p.by_group(h) * p.group;
-  const int64_t r = (int64_t)token * p.group + hh, total = (int64_t)(sq.r1 - sq.r0) * p.group;
-  const int64_t base = r >> p.block_shift << p.block_shift, last = min(base + (1 << p.block_shift), total) - 1;
-  const int p0 = sq.len - (sq.r1 - sq.r0), pos = p0 + token;
-  const KeyTiles kt =
-      key_tiles(p0 + p.by_group((int)base), p0 + p.by_group((int)last), p.window, p.sinks, p.tile_shift);
+  const int token = (int)(row - sq.r0);
+  const int tokens = sq.r1 - sq.r0, base = token / p.block * p.block, last = base + min(p.block, tokens - base) - 1;
+  const int p0 = sq.len - tokens, pos = p0 + token;
+  const KeyTiles kt = key_tiles(p0 + base, p0 + last, p.window, p.sinks, p.tile_shift);
   if (kt.n <= p.per_split) return;  // one piece: the block wrote its result itself
   const int pieces = min(p.splits, ceil_div(kt.n, p.per_split));
   const int64_t slot = row * p.nq + h, step = p.c.rows * p.nq;
@@ -100,7 +98,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __g
 struct Plan {
   bool few;                     // the kernel for few rows
   int64_t blocks;               // blocks of rows of one KV head, at most
-  int block, tile;              // rows of a block, keys of a tile
+  int block, tile;              // tokens of a block, keys of a tile
   int splits, per_split;
 };
 
@@ -109,19 +107,19 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   const int group = a->nq / c->n_kv;
   const int64_t rows = (int64_t)a->max_q * group;
   pl.few = rows <= kRowsMax;
-  // pairs of CTAs where sequences have more rows than one CTA holds (and a half of V is at least 64 dims)
-  pl.block = c->dh > 64 && rows > kTileM ? 2 * kTileM : kTileM;
-  pl.blocks = pl.few ? b->n_seqs : a->rows * group / pl.block + b->n_seqs;  // see find_unit
+  // whole tokens to a block; pairs of CTAs where sequences have more than one CTA holds (and half of V's dims are 64)
+  const int own = kTileM / group, ctas = !pl.few && c->dh > 64 && a->max_q > own ? 2 : 1;
+  pl.block = pl.few ? kRowsMax : own * ctas;
+  pl.blocks = pl.few ? b->n_seqs : a->rows / pl.block + b->n_seqs;  // see find_unit
   pl.tile = !pl.few ? kTileN : c->kind == FAK_KV_BF16 || c->dh > 128 ? kRowsN : 2 * kRowsN;
   int64_t tiles = ((int64_t)a->max_kv + pl.tile - 1) / pl.tile;
   if (a->window) {
-    const int64_t span = (pl.block + group - 1) / group;
+    const int64_t span = pl.block;
     tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / pl.tile + 2 +
                                          std::min<int64_t>((int64_t)a->sinks / pl.tile + 1, tiles));
   }
   tiles = std::max<int64_t>(tiles, 1);
-  const int ctas = pl.block / kTileM;
-  const int64_t each = pl.few ? 1 : (rows + pl.block - 1) / pl.block;  // blocks of a sequence, at most
+  const int64_t each = pl.few ? 1 : (a->max_q + pl.block - 1) / pl.block;  // blocks of a sequence, at most
   const int64_t busy = std::max<int64_t>(1, std::min<int64_t>(pl.blocks, b->n_seqs * each) * ctas * c->n_kv);
   pl.splits = 1;
   pl.per_split = (int)tiles;
@@ -235,14 +233,10 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.scale = a->scale * 1.4426950408889634f;
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
-  p.block_shift = pl.block == kTileM ? 7 : 8;
+  p.block = pl.block;
   p.tile_shift = pl.tile == 64 ? 6 : 7;
-  if (p.group > 1) {  // ceil(2^(31 + s) / group), s = ceil(log2 group): exact for r below 2^31
-    int s = 1;
-    while ((1 << s) < p.group) ++s;
-    p.group_mul = (uint32_t)(((1ull << (31 + s)) + p.group - 1) / p.group);
-    p.group_shift = s - 1;
-  }
+  p.by_group = quotient(p.group);
+  p.by_block = quotient(p.block);
   p.window = a->window;
   p.sinks = a->window ? a->sinks : 0;
   p.splits = pl.splits;

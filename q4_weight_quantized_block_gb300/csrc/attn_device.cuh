@@ -6,6 +6,22 @@
 
 #include "kv_device.cuh"
 
+// r / d for 0 <= r < 2^31, by a multiplication: mul = ceil(2^(31 + s) / d), s = ceil(log2 d), shift = s - 1; d = 1: mul 0.
+struct Quotient {
+  uint32_t mul;
+  int shift;
+  __device__ __forceinline__ int operator()(int r) const {
+    return mul ? (int)(__umulhi((uint32_t)r, mul) >> shift) : r;
+  }
+};
+
+static inline Quotient quotient(int d) {
+  if (d <= 1) return Quotient{0, 0};
+  int s = 1;
+  while (s < 31 && (1 << s) < d) ++s;
+  return Quotient{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+
 struct AttnParams {
   KvView c;
   const __nv_bfloat16* q;
@@ -14,10 +30,9 @@ struct AttnParams {
   int64_t q_row, q_head, gate_row, gate_head, out_row, out_head;
   float scale;  // times log2(e): scores are held in powers of two
   int nq, group, window, sinks;
-  int block_shift;  // rows of a block: 128, or 256 in a pair of CTAs
-  int tile_shift;   // keys of a tile
-  uint32_t group_mul;  // r / group = r group_mul / 2^(32 + group_shift) for 0 <= r < 2^31 (group 1: group_mul 0)
-  int group_shift;
+  int block;       // tokens of a block
+  int tile_shift;  // keys of a tile
+  Quotient by_group, by_block;  // r / group, r / block
   // the keys of a block of rows are cut into at most `splits` pieces of `per_split` key tiles; a block with more
   // than one piece leaves, for each piece, row and head, the unnormalised sum (part, dh values) and its base and
   // weight sum (stat), which the join kernel adds up
@@ -25,10 +40,6 @@ struct AttnParams {
   float* part;   // [splits][rows][nq][dh]
   float2* stat;  // [splits][rows][nq]
   unsigned long long timeout_ns;
-
-  __device__ __forceinline__ int by_group(int r) const {
-    return group_mul ? (int)(__umulhi((uint32_t)r, group_mul) >> group_shift) : r;
-  }
 };
 
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA

@@ -1,7 +1,8 @@
 // Attention of blocks of rows over the paged KV cache on the 5th-generation tensor cores.
 //
-// A block holds 128 rows of one sequence and KV head (256 in a pair of CTAs); a row is a (token, query head of
-// the group) pair, so grouped heads fill the block whether the sequence has one new token or thousands.  Per
+// A block holds up to 128 rows of one sequence and KV head (twice that in a pair of CTAs): whole tokens, a row for
+// each of their query heads of the group, so grouped heads fill the block whether the sequence has one new token or
+// thousands.  Per
 // tile of 128 keys
 //   S = Q K^T (f32 in TMEM),  P = exp2(c S - m) (bf16, in S's own TMEM columns),  O += P V (f32 in TMEM)
 // with the running maximum m and sum of the softmax.  m moves only when a row's maximum passes it by 8: until then
@@ -12,13 +13,19 @@
 // keys at dh 256 reads 192 KB and takes 128 KB of copies through shared memory in the 2048 cycles that its MMAs last,
 // more than the 128 bytes a cycle that it has; the pair halves K's and V's part, and the L2 traffic with it.
 //
-//   warps 0-7      softmax: warp w and w + 4 share rows 32 (w % 4) .. +31, half of the keys each
+// A CTA (a pair) works on one block after the other until none is left: it takes over blocks of the grid that have not
+// started (cluster launch control), so the longest, which come first, are dealt out as CTAs get free, and a block's
+// loads and first scores run while the block before it is still being finished.
+//
+//   warps 0-7      softmax and results: warp w and w + 4 share rows 32 (w % 4) .. +31, half of the keys each
 //   warp 8         TMEM owner; in the first CTA the MMA issuer
-//   warps 9, 10    TMA of K and of V by pages, each into a ring of its own (one warp needs some 500 cycles for a
+//   warps 9, 10    TMA of Q and K, and of V, by pages, each into a ring of its own (one warp needs some 500 cycles for a
 //                  stage), in the 128-byte-swizzled layouts the MMAs read: Q and K 64 dims wide with the dims
 //                  running (K-major), V keys by dims as stored (MN-major)
-//   warps 12-19    for an 8-bit cache, codes to bf16, four warps K's and four V's: the copies land in rings of their own and they fill the
-//                  MMAs' rings from them (12-15, for a bf16 cache: V of the tiles that a mask cuts is mended)
+//   warp 11        the next block: takes it, works out its rows and keys
+//   warps 12-19    for an 8-bit cache, codes to bf16, four warps K's and four V's: the copies land in rings of their own
+//                  and they fill the MMAs' rings from them (12-15, for a bf16 cache: V of the tiles that a mask cuts
+//                  is mended)
 // S has two or three buffers, so the next tile's S = Q K^T runs while the softmax works.
 // 8-bit codes become bf16 exactly; their scales multiply the scores' columns and the weights instead.
 // A weight of zero times a value that is not finite would be NaN, so in the tiles that a mask cuts a bf16 V is
@@ -57,11 +64,11 @@ struct Cfg {
   static constexpr int sbufs = DH == 256 ? 2 : 3;    // S buffers: 512 TMEM columns, less O's
   // stages of K, of V, and of their codes on their way to bf16
   static constexpr int ks = stage == 32768 ? 2 : quant ? (DH == 256 ? 3 : 4) : DH == 256 ? 4 : 5;
-  static constexpr int vs = stage == 32768 ? 2 : quant ? (DH == 256 ? 3 : 4) : DH == 256 ? 5 : 6;
-  static constexpr int rs = quant ? 3 : 0;
-  // tiles whose scales are held at once: a tile's are loaded when the K of the tile rs + ks stages back is done
-  // with, and with it the softmax of the tile sbufs further back
-  static constexpr int slots = (rs + ks + chunks - 1) / chunks + sbufs;
+  static constexpr int vs = ks;
+  static constexpr int rs = quant ? 2 : 0;
+  // tiles whose scales are held at once: a tile's are loaded when the stage rs + ks stages before its first is
+  // done with, as that tile's K was loaded, so the softmax is at most sbufs tiles further back
+  static constexpr int slots = 1 + (rs + ks + chunks - 1) / chunks + sbufs;
   static constexpr int warps = quant ? 20 : 16;
   static constexpr int threads = warps * 32;
   static constexpr int off_k = kTileM * DH * 2;
@@ -70,14 +77,18 @@ struct Cfg {
   static constexpr int off_rv = off_rk + rs * raw;
   static constexpr int off_scales = off_rv + rs * raw;
   static constexpr int off_red = off_scales + (quant ? slots * 2 * kTileN * 4 : 0);
-  static constexpr int off_bar = off_red + 2 * 2 * kTileM * 4;
-  static constexpr int smem = off_bar + 656 + 1024;
+  static constexpr int off_turn = off_red + 2 * 2 * kTileM * 4;  // where results turn, 2 KB to a softmax warp
+  static constexpr int off_bar = off_turn + 8 * 2048;
+  static constexpr int smem = off_bar + 688 + 1024;
   static_assert(smem <= 232448 - 1024, "shared memory exceeds the 227 KB per-block limit");
 };
 
-// A block of rows: the whole pair's keys, this CTA's rows.
+// A block: the whole pair's keys, this CTA's rows.
 struct Unit {
-  int seq, row0, rbase, nrows, p0, p_lo, p_hi, own_lo, own_hi, n, begin, direct, skip;
+  int seq, head, split;                  // KV head, piece of the keys
+  int row0, token, nrows;                // the sequence's first row, the CTA's first token, its rows
+  int p0, p_lo, p_hi, own_lo, own_hi;    // positions: of the sequence's first row, of the block's rows, of the CTA's
+  int n, begin, direct, stop;            // key tiles, the first of them; the keys are one piece; there is no block
   KeyTiles kt;
 };
 
@@ -231,54 +242,96 @@ FAK_DEV bool tile_cut(int p_lo, int p_hi, int tile, const AttnParams& p) {
   return keys_cut(p_lo, p_hi, tile * kTileN, tile * kTileN + kTileN - 1, p.window, p.sinks);
 }
 
-// Block x's sequence: the one of the last s with r0(s) * group / block + s <= x.  These starts rise by at
-// least the sequence's number of blocks, so every block of rows has an x, and some x have none.
-FAK_DEV void find_unit(const AttnParams& p, int64_t x, int split, int rank, int lane, Unit& u) {
-  int lo = 0, hi = p.c.n_seqs;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const unsigned b =
-        __ballot_sync(0xffffffffu, i < hi && ((int64_t)p.c.row_start[i] * p.group >> p.block_shift) + i <= x);
-    const int n = __popc(b);
-    if (n > 1) lo += (n - 1) * step;
-    hi = min(lo + step, hi);
+// The cluster of the grid that is taken over, if one had not started: its first CTA's coordinates.
+FAK_DEV void take_over(void* answer, uint64_t* bar, bool pair) {
+  if (pair)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+        "[%0], [%1];" ::"r"(smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+  else
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+
+FAK_DEV bool taken_over(const void* answer, int& x, int& y, int& z) {
+  uint32_t got, a = 0, b = 0, c = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%4];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %3, 1, 0, p;\n"
+      " mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n}"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(got)
+      : "r"(smem_u32(answer))
+      : "memory");
+  x = (int)a;
+  y = (int)b;
+  z = (int)c;
+  return got != 0;
+}
+
+// Block x's sequence: the one of the last s with r0(s) / block + s <= x.  These starts rise by at least the
+// sequence's number of blocks, so every block of rows has an x, and some x have none.  False: nothing to do.
+FAK_DEV bool find_unit(const AttnParams& p, int x, int head, int split, int rank, int lane, Unit& u) {
+  int lo;
+  KvSeq sq;
+  if (p.c.n_seqs < 32) {
+    const int start = lane <= p.c.n_seqs ? p.c.row_start[lane] : 0;
+    const int len = lane < p.c.n_seqs ? p.c.kv_len[lane] : 0;
+    lo = max(__popc(__ballot_sync(0xffffffffu, lane < p.c.n_seqs && p.by_block(start) + lane <= x)) - 1, 0);
+    sq.r0 = __shfl_sync(0xffffffffu, start, lo);
+    sq.r1 = __shfl_sync(0xffffffffu, start, lo + 1);
+    sq.len = __shfl_sync(0xffffffffu, len, lo);
+    sq.ok = kv_seq_ok(p.c, sq);
+  } else {
+    lo = 0;
+    int hi = p.c.n_seqs;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && p.by_block(p.c.row_start[i]) + i <= x));
+      if (n > 1) lo += (n - 1) * step;
+      hi = min(lo + step, hi);
+    }
+    sq = kv_seq(p.c, lo);
   }
-  const KvSeq sq = kv_seq(p.c, lo);
+  if (!sq.ok) return false;
+  const int64_t first = (int64_t)(x - (p.by_block(sq.r0) + lo)) * p.block;  // token
+  if (first < 0 || first >= sq.r1 - sq.r0) return false;
+  const int t0 = (int)first, tokens = min(p.block, sq.r1 - sq.r0 - t0), own = min(kTileM / p.group, p.block);
   u.seq = lo;
-  u.skip = 1;
-  if (!sq.ok) return;
-  const int64_t first = (x - (((int64_t)sq.r0 * p.group >> p.block_shift) + lo)) << p.block_shift;
-  const int64_t total = (int64_t)(sq.r1 - sq.r0) * p.group;
-  if (first < 0 || first >= total) return;
-  const int rows = (int)min((int64_t)1 << p.block_shift, total - first);
+  u.head = head;
+  u.split = split;
   u.row0 = sq.r0;
-  u.rbase = (int)first + rank * kTileM;
-  u.nrows = max(0, min(kTileM, rows - rank * kTileM));
+  u.token = t0 + rank * own;
+  const int mine = max(0, min(own, tokens - rank * own));
+  u.nrows = mine * p.group;
   u.p0 = sq.len - (sq.r1 - sq.r0);
-  u.p_lo = u.p0 + p.by_group((int)first);
-  u.p_hi = u.p0 + p.by_group((int)first + rows - 1);
-  u.own_lo = u.p0 + p.by_group(u.rbase);
-  u.own_hi = u.p0 + p.by_group(u.rbase + max(u.nrows, 1) - 1);
+  u.p_lo = u.p0 + t0;
+  u.p_hi = u.p0 + t0 + tokens - 1;
+  u.own_lo = u.p0 + u.token;
+  u.own_hi = u.own_lo + max(mine, 1) - 1;
   u.kt = key_tiles(u.p_lo, u.p_hi, p.window, p.sinks, 7);
   u.direct = p.splits == 1 || u.kt.n <= p.per_split;
-  u.begin = split * p.per_split;
-  const int end = u.direct || split == p.splits - 1 ? u.kt.n : min(u.kt.n, u.begin + p.per_split);
-  if (u.direct) u.begin = 0;
-  u.n = end - u.begin;
+  u.begin = u.direct ? 0 : split * p.per_split;
+  u.n = (u.direct || split == p.splits - 1 ? u.kt.n : min(u.kt.n, u.begin + p.per_split)) - u.begin;
+  u.stop = 0;
   // a block whose keys are one piece, or that sees nothing at all, is the first split's
-  u.skip = u.direct ? (split != 0) : (u.n <= 0);
+  return u.direct ? split == 0 : u.n > 0;
 }
 
 template <int DH, int KIND, int CG>
 __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
-    attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, int* status) {
+    attn_tile_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int* status) {
   using C = Cfg<DH, KIND, CG>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   float* scales = reinterpret_cast<float*>(smem + C::off_scales);  // [slot][key, value][128]
   float* red = reinterpret_cast<float*>(smem + C::off_red);        // [parity][half][128]
-  // in a pair the MMA issuer waits on CTA 0's: kfull, vfull, mended, pfull, qfull
+  // in a pair the MMA issuer waits on CTA 0's: kfull, vfull, mended, pfull, ofree, qfull
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + C::off_bar);
   uint64_t* kempty = kfull + C::ks;
   uint64_t* vfull = kempty + C::ks;
@@ -295,23 +348,25 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   uint64_t* odone = pfull + 3;
   uint64_t* pair = odone + 2;
   uint64_t* qfull = pair + 4;
-  uint64_t* pdone = qfull + 1;
-  uint64_t* drain = pdone + 1;
-  uint64_t* tready = drain + 1;
-  static_assert((2 * C::ks + (C::quant ? 2 : 4) * C::vs + 4 * C::rs + (C::quant ? C::slots : 0) + 16) * 8 <= 640,
+  uint64_t* qempty = qfull + 1;
+  uint64_t* ofree = qempty + 1;  // the block's results have left TMEM
+  uint64_t* pdone = ofree + 1;   // bf16: V has been mended where it had to be (two: one CTA may be a block ahead)
+  uint64_t* ufull = pdone + 2;   // blocks: handed out, done with
+  uint64_t* uempty = ufull + 2;
+  uint64_t* asked = uempty + 2;  // take_over's answer, and that both CTAs have read it
+  uint64_t* heard = asked + 1;
+  uint64_t* drain = heard + 1;
+  static_assert((2 * C::ks + (C::quant ? 2 : 4) * C::vs + 4 * C::rs + (C::quant ? C::slots : 0) + 24) * 8 <= 656,
                 "barriers exceed their area");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 640);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 644);
-  volatile int* odd = reinterpret_cast<volatile int*>(smem + C::off_bar + 648);
-  __shared__ Unit unit;
+  uint8_t* answer = smem + C::off_bar + 656;  // 16 bytes
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 672);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 676);
+  volatile int* odd = reinterpret_cast<volatile int*>(smem + C::off_bar + 680);
+  __shared__ Unit units[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 1 ? 0 : (int)cta_rank();
-  if (warp == 0) {
-    Unit u;
-    find_unit(p, (gridDim.x - 1 - blockIdx.x) / CG, blockIdx.z, rank, lane, u);
-    if (lane == 0) unit = u;
-  } else if (warp == 1 && lane == 0) {
+  if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::ks; ++s) {
       mbar_init(&kfull[s], C::quant ? 4 * CG : 1);
       mbar_init(&kempty[s], 1);
@@ -335,28 +390,23 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       mbar_init(&sfull[s], 1);
       mbar_init(&pfull[s], 8 * CG);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&odone[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&odone[s], 1);
+      mbar_init(&pdone[s], 4 * CG);
+      mbar_init(&ufull[s], 1);
+      mbar_init(&uempty[s], 11 + C::warps - 12);
+    }
     for (int s = 0; s < 4; ++s) mbar_init(&pair[s], 2);
-    mbar_init(qfull, (C::warps - 2) * CG);
-    mbar_init(pdone, (C::warps - 12) * CG);
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(ofree, 8 * CG);
+    mbar_init(asked, 1);
+    mbar_init(heard, CG);
     mbar_init(drain, 1);
-    mbar_init(tready, 1);
     *abort = 0;
     *odd = 0;
     fence_mbar_init();
   }
-  if (warp == 2 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) {
-    bool bad = false;  // every sequence's numbers are looked at once, also those that no block finds
-    for (int i = lane; i < p.c.n_seqs; i += 32) bad |= !kv_seq(p.c, i).ok;
-    if (bad) attn_record(status, FAK_ERR_DEVICE);
-  }
-  __syncwarp();
-  if constexpr (CG == 2)
-    cluster_sync();  // both CTAs' barriers stand
-  else
-    __syncthreads();
-  const Unit& u = unit;
-  if (u.skip) return;  // (a pair's CTAs agree)
   if (warp == 8) {
     if constexpr (CG == 1) {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -370,7 +420,20 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
   }
-  const int n = u.n, g = blockIdx.y;
+  if (warp == 2 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) {
+    bool bad = false;  // every sequence's numbers are looked at once, also those that no block finds
+    for (int i = lane; i < p.c.n_seqs; i += 32) bad |= !kv_seq(p.c, i).ok;
+    if (bad) attn_record(status, FAK_ERR_DEVICE);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  if constexpr (CG == 2)
+    cluster_sync();  // both CTAs' barriers and TMEM stand
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
   const uint64_t tmo = p.timeout_ns;
   // a whole warp waits: it goes on or gives up as one
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -381,40 +444,12 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     }
     return done;
   };
-  if (warp != 9 && warp != 10) {
-    // Q: rows of the block, 64 dims to a 16 KB panel, by all warps but the TMA's; rows past the block's are zeros
-    constexpr int lanes = DH / 8, loaders = (C::warps - 2) * 32;
-    constexpr int each = (kTileM * lanes + loaders - 1) / loaders;  // 16 bytes to a lane
-    const int tid = (warp < 9 ? warp : warp - 2) * 32 + lane, c = tid % lanes;
-    uint4 x[each];
-#pragma unroll
-    for (int k = 0; k < each; ++k) {
-      const int row = (k * loaders + tid) / lanes, r = u.rbase + row, token = p.by_group(r);
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (row < u.nrows)
-        x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.row0 + token) * p.q_row +
-                                               (int64_t)(g * p.group + r - token * p.group) * p.q_head + c * 8);
-    }
-#pragma unroll
-    for (int k = 0; k < each; ++k) {
-      const int row = (k * loaders + tid) / lanes;
-      if (row < kTileM)
-        *reinterpret_cast<uint4*>(smem + (c >> 3) * kPanel + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // block k of this CTA; a warp is done with it
+  auto handed = [&](int k) { return wait(&ufull[k & 1], (k >> 1) & 1) && !units[k & 1].stop; };
+  auto release = [&](int k) {
     __syncwarp();
-    if (lane == 0) arrive_first<CG>(qfull);
-    if (warp == 8) {
-      tc_fence_before_sync();
-      if (lane == 0) mbar_arrive(tready);
-    }
-  }
-  if (warp <= 8) {
-    wait(tready, 0);
-    tc_fence_after_sync();
-  }
-  const uint32_t tmem = warp <= 8 ? *reinterpret_cast<volatile uint32_t*>(tmem_slot) : 0;
-  const uint32_t tmem_s = tmem + DH;  // O in columns [0, DH), then the S buffers
+    if (lane == 0) mbar_arrive(&uempty[k & 1]);
+  };
 
   // Twenty warps start with 96 registers each (61440 in all): 128 for the softmax, 80 for the conversion, 56 for the rest.
   if constexpr (C::quant) {
@@ -429,287 +464,322 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     // ---------------- softmax
     const int half = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const bool live = 32 * quarter < u.nrows;
-    const int r = u.rbase + row, token = p.by_group(r), pos = u.p0 + token;
-    float m = -INFINITY, l = 0.0f;
+    const int row_token = p.by_group(row), row_head = row - row_token * p.group;
+    // running over the blocks: S buffer and its parity, slot of the scales, products so far, exchanges with the other half
+    int sb = 0, sph = 0, slot = 0, scph = 0, done = 0, meets = 0;
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const int b = i % C::sbufs;
-      const int tile = key_tile(u.kt, u.begin + i), j0 = tile * kTileN + 64 * half;
-      if (!(ok = wait(&sfull[b], (i / C::sbufs) & 1))) break;
-      if constexpr (C::quant)
-        if (!(ok = wait(&scfull[i % C::slots], (i / C::slots) & 1))) break;
-      tc_fence_after_sync();
-      const uint32_t scol = tmem_s + lanes + (uint32_t)(b * kTileN + 64 * half);
-      if (live) {
-        float t[64];
-        {
-          uint32_t raw[2][32];
-          tmem_ld_cols<32>(scol, raw[0]);
-          tmem_ld_cols<32>(scol + 32, raw[1]);
-          tmem_wait_ld();
+    for (int k = 0; ok && handed(k); ++k) {
+      const Unit& u = units[k & 1];
+      const int n = u.n;
+      const bool live = 32 * quarter < u.nrows;
+      const int token = u.token + row_token, pos = u.p0 + token;
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < n; ++i) {
+        const int tile = key_tile(u.kt, u.begin + i), j0 = tile * kTileN + 64 * half;
+        if (!(ok = wait(&sfull[sb], sph))) break;
+        if constexpr (C::quant)
+          if (!(ok = wait(&scfull[slot], scph))) break;
+        // The product two tiles back is done.  With it known before this tile's weights are handed over, a barrier of
+        // `odone` is never two phases past one that is waited for.  (Two S buffers: it came before these scores.)
+        if (C::sbufs == 3 && i > 1 && !(ok = wait(&odone[done & 1], ((done - 2) >> 1) & 1))) break;
+        tc_fence_after_sync();
+        const uint32_t scol = tmem_s + lanes + (uint32_t)(sb * kTileN + 64 * half);
+        if (live) {
+          float t[64];
+          {
+            uint32_t raw[2][32];
+            tmem_ld_cols<32>(scol, raw[0]);
+            tmem_ld_cols<32>(scol + 32, raw[1]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 64; ++k) t[k] = __uint_as_float(raw[k >> 5][k & 31]);
-        }
-        const float* sc = scales + (C::quant ? (i % C::slots) * 2 * kTileN + 64 * half : 0);
-        if constexpr (C::quant) {
-#pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sc + k);
-            mul2(t[k], t[k + 1], f.x, f.y);
-            mul2(t[k + 2], t[k + 3], f.z, f.w);
+            for (int c = 0; c < 64; ++c) t[c] = __uint_as_float(raw[c >> 5][c & 31]);
           }
-        }
-        const bool cut = tile_cut(u.own_lo, u.own_hi, tile, p);
-        if (cut) {
+          const float* sc = scales + (C::quant ? slot * 2 * kTileN + 64 * half : 0);
+          if constexpr (C::quant) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (!sees(pos, j0 + k, p.window, p.sinks)) t[k] = -INFINITY;
-        }
-        float mx = -INFINITY;
+            for (int c = 0; c < 64; c += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + c);
+              mul2(t[c], t[c + 1], f.x, f.y);
+              mul2(t[c + 2], t[c + 3], f.z, f.w);
+            }
+          }
+          const bool cut = tile_cut(u.own_lo, u.own_hi, tile, p);
+          if (cut) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) mx = fmaxf(mx, t[k]);
-        float* mine = red + (i & 1) * 2 * kTileM;
-        mine[half * kTileM + row] = mx;
+            for (int c = 0; c < 64; ++c)
+              if (!sees(pos, j0 + c, p.window, p.sinks)) t[c] = -INFINITY;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) mx = fmaxf(mx, t[c]);
+          float* mine = red + (meets & 1) * 2 * kTileM;
+          mine[half * kTileM + row] = mx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pair[quarter]);
+          if (!(ok = wait(&pair[quarter], meets & 1))) break;
+          ++meets;
+          mx = fmaxf(mx, mine[(half ^ 1) * kTileM + row]) * p.scale;
+          // a new base when the maximum passed it by 8, or is the first one seen
+          const bool up = mx > m + 8.0f;
+          if (__any_sync(0xffffffffu, up)) {
+            const float next = up ? mx : m;
+            const float f = up ? exp2_approx(m - next) : 1.0f;
+            m = next;
+            l *= f;
+            if (i > 0) {
+              if (!(ok = wait(&odone[(done + 1) & 1], ((done - 1) >> 1) & 1))) break;  // the product before
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < DH / 2; c += 32) {
+                uint32_t o[32];
+                const uint32_t at = tmem + lanes + (uint32_t)(half * (DH / 2) + c);
+                tmem_ld_cols<32>(at, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(at, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.0f : m;
+          float sum[2] = {0.0f, 0.0f};
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              fma2(e[j], e[j + 1], t[c + j], t[c + j + 1], p.scale, -base);
+              e[j] = exp2_approx(e[j]);
+              e[j + 1] = exp2_approx(e[j + 1]);
+              add2(sum[0], sum[1], e[j], e[j + 1]);
+            }
+            if constexpr (C::quant) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + c);
+              if (cut) {
+                // a weight of zero stays zero, whatever scale stands at the place of a key that is not seen
+                e[0] = e[0] == 0.0f ? 0.0f : e[0] * f.x;
+                e[1] = e[1] == 0.0f ? 0.0f : e[1] * f.y;
+                e[2] = e[2] == 0.0f ? 0.0f : e[2] * f.z;
+                e[3] = e[3] == 0.0f ? 0.0f : e[3] * f.w;
+              } else {
+                mul2(e[0], e[1], f.x, f.y);
+                mul2(e[2], e[3], f.z, f.w);
+              }
+            }
+            w[c / 2] = pack_bf16(e[0], e[1]);
+            w[c / 2 + 1] = pack_bf16(e[2], e[3]);
+          }
+          l += sum[0] + sum[1];
+          tmem_st32(scol, w);
+          tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_first<CG>(&pfull[sb]);
+        ++done;
+        if (++sb == C::sbufs) {
+          sb = 0;
+          sph ^= 1;
+        }
+        if (++slot == C::slots) {
+          slot = 0;
+          scph ^= 1;
+        }
+      }
+      // ---------------- the rows' results
+      if (ok && n > 0) ok = wait(&odone[(done - 1) & 1], ((done - 1) >> 1) & 1);
+      if constexpr (!C::quant) {
+        if (ok) ok = wait(&pdone[k & 1], (k >> 1) & 1);
+        if (CG == 2 && ok) (void)try_wait_cluster(&pdone[k & 1], (k >> 1) & 1);  // (done: for its acquire of `odd`)
+      }
+      if (ok && live && n > 0) {
+        tc_fence_after_sync();
+        float* mine = red + (meets & 1) * 2 * kTileM;
+        mine[half * kTileM + row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&pair[quarter]);
-        if (!(ok = wait(&pair[quarter], i & 1))) break;
-        mx = fmaxf(mx, mine[(half ^ 1) * kTileM + row]) * p.scale;
-        // a new base when the maximum passed it by 8, or is the first one seen
-        const bool up = mx > m + 8.0f;
-        if (__any_sync(0xffffffffu, up)) {
-          const float next = up ? mx : m;
-          const float f = up ? exp2_approx(m - next) : 1.0f;
-          m = next;
-          l *= f;
-          if (i > 0) {
-            if (!(ok = wait(&odone[(i - 1) & 1], ((i - 1) >> 1) & 1))) break;
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < DH / 2; c += 32) {
-              uint32_t o[32];
-              const uint32_t at = tmem + lanes + (uint32_t)(half * (DH / 2) + c);
-              tmem_ld_cols<32>(at, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(at, o);
-            }
-          }
-        }
-        const float base = m == -INFINITY ? 0.0f : m;
-        float sum[2] = {0.0f, 0.0f};
-        uint32_t w[32];
-#pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          float e[4];
-#pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            fma2(e[j], e[j + 1], t[k + j], t[k + j + 1], p.scale, -base);
-            e[j] = exp2_approx(e[j]);
-            e[j + 1] = exp2_approx(e[j + 1]);
-            add2(sum[0], sum[1], e[j], e[j + 1]);
-          }
-          if constexpr (C::quant) {
-            const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + k);
-            if (cut) {
-              // a weight of zero stays zero, whatever scale stands at the place of a key that is not seen
-              e[0] = e[0] == 0.0f ? 0.0f : e[0] * f.x;
-              e[1] = e[1] == 0.0f ? 0.0f : e[1] * f.y;
-              e[2] = e[2] == 0.0f ? 0.0f : e[2] * f.z;
-              e[3] = e[3] == 0.0f ? 0.0f : e[3] * f.w;
-            } else {
-              mul2(e[0], e[1], f.x, f.y);
-              mul2(e[2], e[3], f.z, f.w);
-            }
-          }
-          w[k / 2] = pack_bf16(e[0], e[1]);
-          w[k / 2 + 1] = pack_bf16(e[2], e[3]);
-        }
-        l += sum[0] + sum[1];
-        tmem_st32(scol, w);
-        tmem_wait_st();
+        ok = wait(&pair[quarter], meets & 1);
+        ++meets;
+        l += mine[(half ^ 1) * kTileM + row];
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive_first<CG>(&pfull[b]);
-    }
-    // ---------------- the row's result
-    // (the same barrier's phase before first: three tiles' products may still be under way here, and a
-    // phase two back looks like the one that is waited for)
-    if (ok && n > 2) ok = wait(&odone[(n - 1) & 1], ((n - 3) >> 1) & 1);
-    if (ok && n > 0) ok = wait(&odone[(n - 1) & 1], ((n - 1) >> 1) & 1);
-    if (ok) ok = wait(pdone, 0);
-    if (CG == 2 && ok) ok = try_wait_cluster(pdone, 0);  // (done: for its acquire of `odd`)
-    if (ok && live) {
-      tc_fence_after_sync();
-      float* mine = red + (n & 1) * 2 * kTileM;
-      mine[half * kTileM + row] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pair[quarter]);
-      ok = wait(&pair[quarter], n & 1);
-      l += mine[(half ^ 1) * kTileM + row];
-    }
-    if (ok && live) {
-      const int head = g * p.group + r - token * p.group;
-      // a row that sees nothing is zeros; one whose scores are all -inf is NaN, as 0 / 0 is
-      const float scale = u.direct ? 1.0f / l : 1.0f;
-      const bool mine = row < u.nrows, zero = pos < 0 || n == 0;
-      const int64_t grow = u.row0 + token;
-      const int64_t slot = ((int64_t)blockIdx.z * p.c.rows + grow) * p.nq + head;
-      if (!u.direct && mine && half == 0) p.stat[slot] = make_float2(m, l);
-      // 32 dims at a time turn in shared memory (Q's and the rings', all read by now), so that rows are stored
-      // 128 bytes in a piece: eight lanes a row, four rows a step
-      const int64_t to = u.direct ? grow * p.out_row + head * p.out_head : slot * DH;
-      const int64_t from = p.gate ? grow * p.gate_row + head * p.gate_head : 0;
-      float* turn = reinterpret_cast<float*>(smem) + warp * 1024;
+      auto freed = [&]() {  // O may be written again
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_first<CG>(ofree);
+      };
+      if (ok && !live && n > 0) freed();
+      if (ok && live) {
+        const int head = u.head * p.group + row_head;
+        // a row that sees nothing is zeros; one whose scores are all -inf is NaN, as 0 / 0 is
+        const float scale = u.direct ? 1.0f / l : 1.0f;
+        const bool mine = row < u.nrows, zero = pos < 0 || n == 0;
+        const int64_t grow = u.row0 + token;
+        const int64_t place = ((int64_t)u.split * p.c.rows + grow) * p.nq + head;
+        if (!u.direct && mine && half == 0) p.stat[place] = make_float2(m, l);
+        // 16 dims at a time turn in shared memory, so that a row's are stored 32 bytes (as f32: 64) in a piece:
+        // four lanes a row, eight rows a step
+        const int64_t to = u.direct ? grow * p.out_row + head * p.out_head : place * DH;
+        const int64_t from = p.gate ? grow * p.gate_row + head * p.gate_head : 0;
+        float* turn = reinterpret_cast<float*>(smem + C::off_turn) + warp * 512;
 #pragma unroll 1
-      for (int c = 0; c < DH / 2; c += 32) {
-        const int d0 = half * (DH / 2) + c;
-        uint32_t o[32] = {};
-        if (n > 0) {
-          tmem_ld_cols<32>(tmem + lanes + (uint32_t)d0, o);
-          tmem_wait_ld();
-        }
-        if (!C::quant && mine && *odd) {
-          // values that are not finite, in tiles where they were left out: added for the rows that see them
+        for (int c = 0; c < DH / 2; c += 16) {
+          const int d0 = half * (DH / 2) + c;
+          uint32_t o[16] = {};
+          if (n > 0) {
+            tmem_ld_cols<16>(tmem + lanes + (uint32_t)d0, o);
+            tmem_wait_ld();
+            if (c == DH / 2 - 16) freed();
+          }
+          if (!C::quant && mine && *odd) {
+            // values that are not finite, in tiles where they were left out: added for the rows that see them
 #pragma unroll 1
-          for (int i = 0; i < n; ++i) {
-            const int tile = key_tile(u.kt, u.begin + i);
-            if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
+            for (int i = 0; i < n; ++i) {
+              const int tile = key_tile(u.kt, u.begin + i);
+              if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
 #pragma unroll 1
-            for (int j = tile * kTileN; j < min((tile + 1) * kTileN, pos + 1); ++j) {
-              if (!sees(pos, j, p.window, p.sinks)) continue;
-              int64_t at = kv_place(p.c, u.seq, j, g);
-              if (at < 0) at = -1 - at;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v) + at * DH + d0;
+              for (int j = tile * kTileN; j < min((tile + 1) * kTileN, pos + 1); ++j) {
+                if (!sees(pos, j, p.window, p.sinks)) continue;
+                int64_t at = kv_place(p.c, u.seq, j, u.head);
+                if (at < 0) at = -1 - at;
+                const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v) + at * DH + d0;
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if ((v[k] & 0x7F80u) == 0x7F80u)
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float((uint32_t)v[k] << 16));
+                for (int e = 0; e < 16; ++e)
+                  if ((v[e] & 0x7F80u) == 0x7F80u)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float((uint32_t)v[e] << 16));
+              }
             }
           }
-        }
-        __syncwarp();
+          __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 y = make_float4(__uint_as_float(o[4 * k]) * scale, __uint_as_float(o[4 * k + 1]) * scale,
-                                       __uint_as_float(o[4 * k + 2]) * scale, __uint_as_float(o[4 * k + 3]) * scale);
-          *reinterpret_cast<float4*>(turn + lane * 32 + ((k ^ (lane & 7)) << 2)) = y;
-        }
-        __syncwarp();
-#pragma unroll 1
-        for (int k0 = 0; k0 < 8; k0 += 4) {
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(turn + lane * 16 + ((e ^ ((lane >> 1) & 3)) << 2)) =
+                make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
+                            __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
+          __syncwarp();
           float4 y[4], x[4];
           int64_t at[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = 4 * (k0 + k) + (lane >> 3);
-            at[k] = __shfl_sync(0xffffffffu, to, rr) + d0 + 4 * (lane & 7);
-            const int64_t gf = __shfl_sync(0xffffffffu, from, rr) + d0 + 4 * (lane & 7);
+          for (int e = 0; e < 4; ++e) {
+            const int rr = 8 * e + (lane >> 2), d = d0 + 4 * (lane & 3);
+            at[e] = __shfl_sync(0xffffffffu, to, rr) + d;
+            const int64_t gf = __shfl_sync(0xffffffffu, from, rr) + d;
             const bool blank = __shfl_sync(0xffffffffu, (int)zero, rr);
-            y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            x[k] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
+            y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            x[e] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
             if (32 * quarter + rr >= u.nrows || blank) continue;
-            y[k] = *reinterpret_cast<const float4*>(turn + rr * 32 + (((lane & 7) ^ (rr & 7)) << 2));
-            if (p.gate && u.direct) x[k] = *reinterpret_cast<const float4*>(p.gate + gf);
+            y[e] = *reinterpret_cast<const float4*>(turn + rr * 16 + (((lane & 3) ^ ((rr >> 1) & 3)) << 2));
+            if (p.gate && u.direct) x[e] = *reinterpret_cast<const float4*>(p.gate + gf);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (32 * quarter + 4 * (k0 + k) + (lane >> 3) >= u.nrows) continue;
+          for (int e = 0; e < 4; ++e) {
+            if (32 * quarter + 8 * e + (lane >> 2) >= u.nrows) continue;
             if (u.direct) {
-              const uint2 w = make_uint2(pack_bf16(gated_by(y[k].x, x[k].x), gated_by(y[k].y, x[k].y)),
-                                         pack_bf16(gated_by(y[k].z, x[k].z), gated_by(y[k].w, x[k].w)));
-              *reinterpret_cast<uint2*>(p.out + at[k]) = w;
+              const uint2 w = make_uint2(pack_bf16(gated_by(y[e].x, x[e].x), gated_by(y[e].y, x[e].y)),
+                                         pack_bf16(gated_by(y[e].z, x[e].z), gated_by(y[e].w, x[e].w)));
+              *reinterpret_cast<uint2*>(p.out + at[e]) = w;
             } else {
-              *reinterpret_cast<float4*>(p.part + at[k]) = y[k];
+              *reinterpret_cast<float4*>(p.part + at[e]) = y[e];
             }
           }
         }
       }
+      release(k);
     }
   } else if (warp == 8) {
     // ---------------- MMA issuer
-    if (n > 0 && rank == 0) {
-      // K: one CTA takes a tile as twice 64 keys, since its panels are 64 keys high; a pair holds 64 keys each
-      constexpr uint32_t id_s = kIdescAttn<kTileM * CG, 64 * CG, false>, id_o = kIdescAttn<kTileM * CG, DH, true>;
-      const uint64_t kd0 = umma_desc_sw128(smem_u32(smem + C::off_k)), qd = umma_desc_sw128(smem_u32(smem));
-      // a stage's V: panels of 64 dims by vrows keys, all dims of the first keys, then of the next
-      const int vshift = C::quant ? 31 - __clz(C::vkeys) : min(p.c.page_shift, 31 - __clz(C::vkeys));
-      const uint64_t vd0 = desc_mn(smem_u32(smem + C::off_v), 128u << vshift);
-      int kst = 0, kph = 0, vst = 0;
-      uint32_t fulls = 0, mends = 0;  // a V stage that is mended has a barrier of its own: the parities go by uses
-      bool ok = wait(qfull, 0);
-      auto scores = [&](int sb) {
-        const uint32_t d = tmem_s + (uint32_t)(sb * kTileN);
+    // K: one CTA takes a tile as twice 64 keys, since its panels are 64 keys high; a pair holds 64 keys each
+    constexpr uint32_t id_s = kIdescAttn<kTileM * CG, 64 * CG, false>, id_o = kIdescAttn<kTileM * CG, DH, true>;
+    const uint64_t kd0 = umma_desc_sw128(smem_u32(smem + C::off_k)), qd = umma_desc_sw128(smem_u32(smem));
+    // a stage's V: panels of 64 dims by vrows keys, all dims of the first keys, then of the next
+    const int vshift = C::quant ? 31 - __clz(C::vkeys) : min(p.c.page_shift, 31 - __clz(C::vkeys));
+    const uint64_t vd0 = desc_mn(smem_u32(smem + C::off_v), 128u << vshift);
+    int kst = 0, kph = 0, vst = 0, sq = 0, sp = 0, pph = 0, blocks = 0, done = 0;
+    uint32_t fulls = 0, mends = 0;  // a V stage that is mended has a barrier of its own: the parities go by uses
+    bool ok = true;
+    auto scores = [&](bool last) {
+      const uint32_t d = tmem_s + (uint32_t)(sq * kTileN);
 #pragma unroll
-        for (int c = 0; c < C::chunks; ++c) {
-          if (!(ok = wait(&kfull[kst], kph))) return;
-          tc_fence_after_sync();
-          const uint64_t kd = kd0 + (uint64_t)(kst * (C::stage >> 4));
-          if (elect_one()) {
+      for (int c = 0; c < C::chunks; ++c) {
+        if (!(ok = wait(&kfull[kst], kph))) return;
+        tc_fence_after_sync();
+        const uint64_t kd = kd0 + (uint64_t)(kst * (C::stage >> 4));
+        if (elect_one()) {
 #pragma unroll
-            for (int x = 0; x < C::stage / 8192; ++x) {  // the stage's parts: 64 dims of 64 keys
-              const int part = c * (C::stage / 8192) + x;  // of the tile: the first 64 keys' panels, then the others'
-              const int panel = part % (DH / 64), half = part / (DH / 64);
+          for (int x = 0; x < C::stage / 8192; ++x) {  // the stage's parts: 64 dims of 64 keys
+            const int part = c * (C::stage / 8192) + x;  // of the tile: the first 64 keys' panels, then the others'
+            const int panel = part % (DH / 64), half = part / (DH / 64);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ss<CG>(d + 64 * half, qd + (uint64_t)((panel * kPanel + 32 * k) >> 4),
-                           kd + (uint64_t)((x * 8192 + 32 * k) >> 4), id_s, panel | k);
-            }
-            commit<CG>(&kempty[kst]);
-            if (c == C::chunks - 1) commit<CG>(&sfull[sb]);
+            for (int k = 0; k < 4; ++k)
+              mma_ss<CG>(d + 64 * half, qd + (uint64_t)((panel * kPanel + 32 * k) >> 4),
+                         kd + (uint64_t)((x * 8192 + 32 * k) >> 4), id_s, panel | k);
           }
-          __syncwarp();
-          if (++kst == C::ks) {
-            kst = 0;
-            kph ^= 1;
+          commit<CG>(&kempty[kst]);
+          if (c == C::chunks - 1) {
+            commit<CG>(&sfull[sq]);
+            if (last) commit<CG>(qempty);
           }
         }
-      };
-      for (int i = 0; i < min(C::sbufs, n) && ok; ++i) scores(i);
-      int sb = 0, ph = 0;
-      for (int i = 0; i < n && ok; ++i) {
-        const bool mend = !C::quant && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
-        if (!(ok = wait(&pfull[sb], ph))) break;
-        const uint32_t a = tmem_s + (uint32_t)(sb * kTileN);
-#pragma unroll
-        for (int c = 0; c < C::chunks; ++c) {
-          if (!(ok = wait(mend ? &mended[vst] : &vfull[vst], ((mend ? mends : fulls) >> vst) & 1))) break;
-          (mend ? mends : fulls) ^= 1u << vst;
-          tc_fence_after_sync();
-          const uint64_t vd = vd0 + (uint64_t)(vst * (C::stage >> 4));
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < C::vkeys / 16; ++k) {
-              const int key = c * C::vkeys + 16 * k;  // weights: 64 keys in 32 columns, twice
-              const int box = 16 * k >> vshift, in = 16 * k & ((1 << vshift) - 1);
-              mma_ts<CG>(tmem, a + (uint32_t)((key >> 6) * 64 + (key & 63) / 2),
-                         vd + (uint64_t)(((box << vshift) * (C::dv * 2) + in * 128) >> 4), id_o, (i | key) != 0);
-            }
-            commit<CG>(&vempty[vst]);
-            if (c == C::chunks - 1) commit<CG>(&odone[i & 1]);
-          }
-          __syncwarp();
-          if (++vst == C::vs) vst = 0;
-        }
-        if (ok && i + C::sbufs < n) scores(sb);
-        if (++sb == C::sbufs) {
-          sb = 0;
-          ph ^= 1;
+        __syncwarp();
+        if (++kst == C::ks) {
+          kst = 0;
+          kph ^= 1;
         }
       }
-      if (!ok && elect_one()) {
-        // what was issued completes before TMEM is freed
-        commit<CG>(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0))
-          if (globaltimer_ns() - t0 > 200000000ull) break;
+      sq = sq + 1 == C::sbufs ? 0 : sq + 1;
+    };
+    for (int k = 0; ok && handed(k); ++k) {
+      const Unit& u = units[k & 1];
+      const int n = u.n;
+      if (rank == 0 && n > 0) {
+        ok = wait(qfull, blocks & 1);
+        for (int i = 0; i < min(C::sbufs, n) && ok; ++i) scores(i == n - 1);
+        for (int i = 0; i < n && ok; ++i) {
+          const bool mend = !C::quant && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
+          if (!(ok = wait(&pfull[sp], pph))) break;
+          if (i == 0 && blocks > 0 && !(ok = wait(ofree, (blocks - 1) & 1))) break;
+          const uint32_t a = tmem_s + (uint32_t)(sp * kTileN);
+#pragma unroll
+          for (int c = 0; c < C::chunks; ++c) {
+            if (!(ok = wait(mend ? &mended[vst] : &vfull[vst], ((mend ? mends : fulls) >> vst) & 1))) break;
+            (mend ? mends : fulls) ^= 1u << vst;
+            tc_fence_after_sync();
+            const uint64_t vd = vd0 + (uint64_t)(vst * (C::stage >> 4));
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 0; e < C::vkeys / 16; ++e) {
+                const int key = c * C::vkeys + 16 * e;  // weights: 64 keys in 32 columns, twice
+                const int box = 16 * e >> vshift, in = 16 * e & ((1 << vshift) - 1);
+                mma_ts<CG>(tmem, a + (uint32_t)((key >> 6) * 64 + (key & 63) / 2),
+                           vd + (uint64_t)(((box << vshift) * (C::dv * 2) + in * 128) >> 4), id_o, (i | key) != 0);
+              }
+              commit<CG>(&vempty[vst]);
+              if (c == C::chunks - 1) commit<CG>(&odone[done & 1]);
+            }
+            __syncwarp();
+            if (++vst == C::vs) vst = 0;
+          }
+          ++done;
+          if (ok && i + C::sbufs < n) scores(i + C::sbufs == n - 1);
+          if (++sp == C::sbufs) {
+            sp = 0;
+            pph ^= 1;
+          }
+        }
+        ++blocks;
       }
-      __syncwarp();
+      release(k);
     }
+    if ((!ok || *abort) && rank == 0 && elect_one()) {
+      // what was issued completes before TMEM is freed
+      commit<CG>(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0))
+        if (globaltimer_ns() - t0 > 200000000ull) break;
+    }
+    __syncwarp();
   } else if (warp == 9 || warp == 10) {
-    // ---------------- TMA: warp 9 K (and the scales), warp 10 V
+    // ---------------- TMA: warp 9 Q, K and the scales, warp 10 V
     const bool value = warp == 10;
     const int kshift = min(p.c.page_shift, 6), krows = 1 << kshift;  // the maps' boxes: keys of K, of V
     const int vshift = min(p.c.page_shift, 31 - __clz(C::vkeys)), vrows = 1 << vshift;
@@ -721,81 +791,101 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     uint64_t* const lands = C::quant ? (value ? rvfull : rkfull) : value ? vfull : kfull;
     uint8_t* const to = smem + (C::quant ? (value ? C::off_rv : C::off_rk) : value ? C::off_v : C::off_k);
     int st = 0, ph = 1;  // the stage, the parity of its `free` (the first round is free already)
+    int blocks = 0, slot = 0;
     uint32_t uses = 0xffffffffu, mends = 0xffffffffu;  // the parity of each stage's last use of `lands`, of `clean`
     bool ok = true;
-    // lane l: the vector index of key l * krows of the tile; keys past the last that a row sees take its
-    // page: what lies there is masked
-    auto places = [&](int i) {
-      const int j = min(key_tile(u.kt, u.begin + i) * kTileN + (min(lane, boxes - 1) << kshift), u.p_hi & ~(krows - 1));
-      int64_t at = kv_place(p.c, u.seq, j, g);
-      if (at < 0) {
-        attn_record(status, FAK_ERR_DEVICE);
-        at = -1 - at;
-      }
-      return (int)at;
-    };
-    int ahead = n > 0 ? places(0) : 0;  // the next tile's, looked up early
-    for (int i = 0; i < n && ok; ++i) {
-      const int at = ahead;
-      if (i + 1 < n) ahead = places(i + 1);
-      if (C::quant && !value) {
-        const int slot = i % C::slots;
-        float* sc = scales + slot * 2 * kTileN;
-        // (its last tile is done with: the rings hold fewer tiles than there are slots)
-        if (elect_one()) mbar_arrive_expect_tx(&scfull[slot], 2 * kTileN * 4);
-        __syncwarp();
-        if (lane < boxes) {
-          bulk_g2s_nohint(sc + lane * krows, p.c.ks + at, krows * 4, &scfull[slot]);
-          bulk_g2s_nohint(sc + kTileN + lane * krows, p.c.vs + at, krows * 4, &scfull[slot]);
+    for (int k = 0; ok && handed(k); ++k) {
+      const Unit& u = units[k & 1];
+      const int n = u.n, g = u.head;
+      // lane l: the vector index of key l * krows of the tile; keys past the last that a row sees take its
+      // page: what lies there is masked
+      auto places = [&](int i) {
+        const int j =
+            min(key_tile(u.kt, u.begin + i) * kTileN + (min(lane, boxes - 1) << kshift), u.p_hi & ~(krows - 1));
+        int64_t at = kv_place(p.c, u.seq, j, g);
+        if (at < 0) {
+          attn_record(status, FAK_ERR_DEVICE);
+          at = -1 - at;
         }
+        return (int)at;
+      };
+      int ahead = n > 0 ? places(0) : 0;  // the next tile's, looked up early
+      if (!value && n > 0) {
+        // Q: panels of 64 dims, the group's heads of a token after token; rows past the block's are other rows', or zeros
+        if (blocks > 0) ok = wait(qempty, (blocks - 1) & 1);
+        if (!ok) break;
+        ++blocks;
+        const int bytes = kTileM / p.group * p.group * 128;
+        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(qfull, CG * (DH / 64) * bytes);
         __syncwarp();
+        for (int c = 0; c < DH / 64; ++c) {
+          if (elect_one())
+            load_3d<CG>(smem + c * kPanel, &qmap, c * 64, g * p.group, u.row0 + u.token, qfull, false);
+          __syncwarp();
+        }
       }
-      const bool mend =
-          !C::quant && value && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
+      for (int i = 0; i < n && ok; ++i) {
+        const int at = ahead;
+        if (i + 1 < n) ahead = places(i + 1);
+        if (C::quant && !value) {
+          float* sc = scales + slot * 2 * kTileN;
+          // (its last tile is done with: the rings hold fewer tiles than there are slots)
+          if (elect_one()) mbar_arrive_expect_tx(&scfull[slot], 2 * kTileN * 4);
+          __syncwarp();
+          if (lane < boxes) {
+            bulk_g2s_nohint(sc + lane * krows, p.c.ks + at, krows * 4, &scfull[slot]);
+            bulk_g2s_nohint(sc + kTileN + lane * krows, p.c.vs + at, krows * 4, &scfull[slot]);
+          }
+          __syncwarp();
+          slot = slot + 1 == C::slots ? 0 : slot + 1;
+        }
+        const bool mend = !C::quant && value && tile_cut(u.p_lo, u.p_hi, key_tile(u.kt, u.begin + i), p);
 #pragma unroll 1
-      for (int c = 0; c < C::chunks; ++c) {
-        if (!(ok = wait(&free[st], ph))) break;
-        // a pair's bytes count on CTA 0's barrier, but for codes and for V that is to be mended
-        const bool local = C::quant || mend;
-        uint64_t* bar = mend ? &clean[st] : &lands[st];
-        uint8_t* dst = to + st * (C::quant ? C::raw : C::stage);
-        if ((local || rank == 0) && elect_one())
-          mbar_arrive_expect_tx(bar, C::quant ? C::raw : local ? C::stage : C::stage * CG);
-        __syncwarp();
-        (mend ? mends : uses) ^= 1u << st;
-        if (!value) {
-          // parts of 64 dims by 64 keys; a pair's CTA has its half of the keys
-          const int part = c * (C::stage / 8192), panel = part % (DH / 64);
-          const int first = 64 * (CG == 2 ? rank : part / (DH / 64));
-          for (int k = 0; k < 64 * C::khalves; k += krows) {
-            const int row = __shfl_sync(0xffffffffu, at, (first + k) >> kshift);
-            if constexpr (C::quant) {
-              if (elect_one()) tma_load_2d_tx(dst + k * kw, &kmap, panel * 64, row, bar);
-            } else {
-              for (int x = 0; x < C::panels; x += kpanels)
-                if (elect_one()) load_3d<CG>(dst + x * 8192 + k * 128, &kmap, 0, row, panel + x, bar, false);
+        for (int c = 0; c < C::chunks; ++c) {
+          if (!(ok = wait(&free[st], ph))) break;
+          // a pair's bytes count on CTA 0's barrier, but for codes and for V that is to be mended
+          const bool local = C::quant || mend;
+          uint64_t* bar = mend ? &clean[st] : &lands[st];
+          uint8_t* dst = to + st * (C::quant ? C::raw : C::stage);
+          if ((local || rank == 0) && elect_one())
+            mbar_arrive_expect_tx(bar, C::quant ? C::raw : local ? C::stage : C::stage * CG);
+          __syncwarp();
+          (mend ? mends : uses) ^= 1u << st;
+          if (!value) {
+            // parts of 64 dims by 64 keys; a pair's CTA has its half of the keys
+            const int part = c * (C::stage / 8192), panel = part % (DH / 64);
+            const int first = 64 * (CG == 2 ? rank : part / (DH / 64));
+            for (int r = 0; r < 64 * C::khalves; r += krows) {
+              const int row = __shfl_sync(0xffffffffu, at, (first + r) >> kshift);
+              if constexpr (C::quant) {
+                if (elect_one()) tma_load_2d_tx(dst + r * kw, &kmap, panel * 64, row, bar);
+              } else {
+                for (int x = 0; x < C::panels; x += kpanels)
+                  if (elect_one()) load_3d<CG>(dst + x * 8192 + r * 128, &kmap, 0, row, panel + x, bar, false);
+              }
+              __syncwarp();
             }
-            __syncwarp();
-          }
-        } else {
-          for (int r = 0; r < C::vkeys; r += vrows) {
-            const int key = c * C::vkeys + r, row = __shfl_sync(0xffffffffu, at, key >> kshift) + (key & (krows - 1));
-            if (elect_one()) {
-              if constexpr (C::quant)
-                tma_load_2d_tx(dst + r * C::dv, &vmap, rank * C::dv, row, bar);
-              else
-                load_3d<CG>(dst + r * C::dv * 2, &vmap, 0, row, rank * (C::dv / 64), bar, mend);
+          } else {
+            for (int r = 0; r < C::vkeys; r += vrows) {
+              const int key = c * C::vkeys + r, row = __shfl_sync(0xffffffffu, at, key >> kshift) + (key & (krows - 1));
+              if (elect_one()) {
+                if constexpr (C::quant)
+                  tma_load_2d_tx(dst + r * C::dv, &vmap, rank * C::dv, row, bar);
+                else
+                  load_3d<CG>(dst + r * C::dv * 2, &vmap, 0, row, rank * (C::dv / 64), bar, mend);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
-        }
-        if (++st == S) {
-          st = 0;
-          ph ^= 1;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
+      release(k);
     }
-    // copies in flight land before the block can end (one that ran to its end has used every copy)
+    // copies in flight land before the CTA can end (one that ran to its end has used every copy)
     if (lane == 0 && *abort) {
       auto landed = [&](uint64_t* bar, uint32_t parity) {
         const uint64_t t0 = globaltimer_ns();
@@ -806,13 +896,48 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
         landed(&lands[q], uses >> q);
         if (!C::quant && value) landed(&clean[q], mends >> q);
       }
-      if (C::quant && !value) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) {  // scales: a kilobyte a tile, landed long before this
-        }
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {  // Q and scales: a few kilobytes, landed long before this
       }
     }
     __syncwarp();
+  } else if (warp == 11) {
+    // ---------------- the blocks
+    int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z, k = 0;
+    bool ok = true;
+    auto hand = [&](const Unit& u) {
+      if (!(ok = wait(&uempty[k & 1], ((k >> 1) & 1) ^ 1))) return;
+      if (lane == 0) {
+        units[k & 1] = u;
+        mbar_arrive(&ufull[k & 1]);
+      }
+      __syncwarp();
+      ++k;
+    };
+    for (int asks = 0; ok; ++asks) {
+      // ask for the next one while this one is worked out
+      if (rank == 0 && asks > 0 && !(ok = wait(heard, (asks - 1) & 1))) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(asked, 16);
+        if (rank == 0) take_over(answer, asked, CG == 2);
+      }
+      __syncwarp();
+      Unit u;
+      if (find_unit(p, ((int)gridDim.x - 1 - x) / CG, y, z, rank, lane, u)) hand(u);
+      // (also after a failure: the answer must not arrive in a CTA that has ended)
+      const bool came = wait(asked, asks & 1);
+      ok = ok && came && !*abort;
+      if (!ok) break;
+      const bool more = taken_over(answer, x, y, z);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive_first<CG>(heard);
+      if (!more) break;
+    }
+    Unit none;
+    none.stop = 1;
+    none.n = 0;
+    if (ok) hand(none);
   } else if (warp >= 12) {
     // ---------------- codes to bf16, V of cut tiles
     constexpr int T = 128;
@@ -831,93 +956,103 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       const uint8_t* const raw = smem + (value ? C::off_rv : C::off_rk);
       uint8_t* const ring = smem + (value ? C::off_v : C::off_k);
       int rs = 0, rph = 0, st = 0, ph = 1;
-      for (int i = 0; i < n * C::chunks && ok; ++i) {
-        if (!(ok = wait(&rfull[rs], rph))) break;
-        const uint4* src = reinterpret_cast<const uint4*>(raw + rs * C::raw);
-        uint8_t* dst = ring + st * C::stage;
-        uint4 q[4];
+      for (int k = 0; ok && handed(k); ++k) {
+        const int count = units[k & 1].n * C::chunks;
+        for (int i = 0; i < count; ++i) {
+          if (!(ok = wait(&rfull[rs], rph))) break;
+          const uint4* src = reinterpret_cast<const uint4*>(raw + rs * C::raw);
+          uint8_t* dst = ring + st * C::stage;
+          uint4 q[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = src[tid + k * T];
-        if (!(ok = wait(&free[st], ph))) break;
+          for (int e = 0; e < 4; ++e) q[e] = src[tid + e * T];
+          if (!(ok = wait(&free[st], ph))) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int e = tid + k * T, key = e >> width_shift, d = (e & ((1 << width_shift) - 1)) * 16;
-          uint4 a, b;
-          codes_to_bf16<KIND>(q[k].x, a.x, a.y);
-          codes_to_bf16<KIND>(q[k].y, a.z, a.w);
-          codes_to_bf16<KIND>(q[k].z, b.x, b.y);
-          codes_to_bf16<KIND>(q[k].w, b.z, b.w);
-          uint8_t* line = dst + (d >> 6) * panel + key * 128;
-          const int e16 = (d & 63) >> 3;
-          *reinterpret_cast<uint4*>(line + ((e16 ^ (key & 7)) << 4)) = a;
-          *reinterpret_cast<uint4*>(line + (((e16 + 1) ^ (key & 7)) << 4)) = b;
+          for (int f = 0; f < 4; ++f) {
+            const int e = tid + f * T, key = e >> width_shift, d = (e & ((1 << width_shift) - 1)) * 16;
+            uint4 a, b;
+            codes_to_bf16<KIND>(q[f].x, a.x, a.y);
+            codes_to_bf16<KIND>(q[f].y, a.z, a.w);
+            codes_to_bf16<KIND>(q[f].z, b.x, b.y);
+            codes_to_bf16<KIND>(q[f].w, b.z, b.w);
+            uint8_t* line = dst + (d >> 6) * panel + key * 128;
+            const int e16 = (d & 63) >> 3;
+            *reinterpret_cast<uint4*>(line + ((e16 ^ (key & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(line + (((e16 + 1) ^ (key & 7)) << 4)) = b;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 1)
+              mbar_arrive(&fills[st]);
+            else
+              asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(fills_first + 8 * st) : "memory");
+            mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
+          }
+          if (++rs == C::rs) {
+            rs = 0;
+            rph ^= 1;
+          }
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1;
+          }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 1)
-            mbar_arrive(&fills[st]);
-          else
-            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(fills_first + 8 * st) : "memory");
-          mbar_arrive(&rempty[rs]);  // after the stores, which came after the loads
-        }
-        if (++rs == C::rs) {
-          rs = 0;
-          rph ^= 1;
-        }
-        if (++st == stages) {
-          st = 0;
-          ph ^= 1;
-        }
+        release(k);
       }
     } else {
       const int tid = threadIdx.x - 12 * 32;
       uint32_t landed = 0;  // parity of each stage's next use of `clean`
+      int before = 0;       // V's stages of the blocks before
       const int vshift = min(p.c.page_shift, 31 - __clz(C::vkeys));
-      for (int i = 0; i < n && ok; ++i) {
-        const int tile = key_tile(u.kt, u.begin + i);
-        if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
-        for (int c = 0; c < C::chunks && ok; ++c) {
-          const int st = (i * C::chunks + c) % C::vs;
-          if (!(ok = wait(&clean[st], (landed >> st) & 1))) break;
-          landed ^= 1u << st;
-          uint4* v = reinterpret_cast<uint4*>(smem + C::off_v + st * C::stage);
-          bool bad = false;
+      for (int k = 0; ok && handed(k); ++k) {
+        const Unit& u = units[k & 1];
+        for (int i = 0; i < u.n && ok; ++i) {
+          const int tile = key_tile(u.kt, u.begin + i);
+          if (!tile_cut(u.p_lo, u.p_hi, tile, p)) continue;
+          for (int c = 0; c < C::chunks; ++c) {
+            const int st = (before + i * C::chunks + c) % C::vs;
+            if (!(ok = wait(&clean[st], (landed >> st) & 1))) break;
+            landed ^= 1u << st;
+            uint4* v = reinterpret_cast<uint4*>(smem + C::off_v + st * C::stage);
+            bool bad = false;
 #pragma unroll
-          for (int k = 0; k < C::stage / 16 / T; ++k) {
-            const int e = tid + k * T, box = e / (C::dv / 8) >> vshift;  // a box: dv dims of 2^vshift keys
-            const int j = tile * kTileN + c * C::vkeys + (box << vshift) + ((e >> 3) & ((1 << vshift) - 1));
-            bool change = false;
-            uint4 y = v[e];
-            y.x = finite2(y.x, change);
-            y.y = finite2(y.y, change);
-            y.z = finite2(y.z, change);
-            y.w = finite2(y.w, change);
-            if (j > u.p_hi)
-              v[e] = make_uint4(0, 0, 0, 0);
-            else if (change)
-              v[e] = y;
-            bad |= change && j <= u.p_hi;
+            for (int f = 0; f < C::stage / 16 / T; ++f) {
+              const int e = tid + f * T, box = e / (C::dv / 8) >> vshift;  // a box: dv dims of 2^vshift keys
+              const int j = tile * kTileN + c * C::vkeys + (box << vshift) + ((e >> 3) & ((1 << vshift) - 1));
+              bool change = false;
+              uint4 y = v[e];
+              y.x = finite2(y.x, change);
+              y.y = finite2(y.y, change);
+              y.z = finite2(y.z, change);
+              y.w = finite2(y.w, change);
+              if (j > u.p_hi)
+                v[e] = make_uint4(0, 0, 0, 0);
+              else if (change)
+                v[e] = y;
+              bad |= change && j <= u.p_hi;
+            }
+            if (bad) {
+              *odd = 1;  // (stays: later blocks of this CTA look for such values too, and find none of theirs)
+              if constexpr (CG == 2)  // the other CTA's rows have these dims too
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to((const void*)odd, rank ^ 1)), "r"(1)
+                             : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_first<CG>(&mended[st]);
           }
-          if (bad) {
-            *odd = 1;
-            if constexpr (CG == 2)  // the other CTA's rows have these dims too
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to((const void*)odd, rank ^ 1)), "r"(1)
-                           : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) arrive_first<CG>(&mended[st]);
         }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if constexpr (CG == 1) {
-        mbar_arrive(pdone);
-      } else {
-        arrive_release_cluster(pdone, 0);
-        arrive_release_cluster(pdone, 1);
+        before = (before + u.n * C::chunks) % C::vs;
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) {
+            mbar_arrive(&pdone[k & 1]);
+          } else {
+            arrive_release_cluster(&pdone[k & 1], 0);
+            arrive_release_cluster(&pdone[k & 1], 1);
+          }
+        }
+        release(k);
       }
     }
   }
@@ -964,13 +1099,27 @@ bool code_map(CUtensorMap* map, void* base, bool quant, int dh, int64_t n_vec, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries: [row][head][dh], boxes of 64 dims of a group's heads of as many whole tokens as 128 rows hold.
+bool query_map(CUtensorMap* map, const AttnParams& p, int dh) {
+  memset(map, 0, sizeof(*map));
+  const cuuint64_t dim[3] = {(cuuint64_t)dh, (cuuint64_t)p.nq, (cuuint64_t)p.c.rows};
+  // (a stride that is never taken may be anything)
+  const cuuint64_t head = p.nq > 1 ? (cuuint64_t)p.q_head * 2 : (cuuint64_t)dh * 2;
+  const cuuint64_t stride[2] = {head, p.c.rows > 1 ? (cuuint64_t)p.q_row * 2 : head * p.nq};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(kTileM / p.group)}, one[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dim, stride, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DH, int KIND, int CG>
 cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks, int* status, int dev, cudaStream_t s) {
   using C = Cfg<DH, KIND, CG>;
   cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
-  CUtensorMap kmap, vmap;
+  CUtensorMap qmap, kmap, vmap;
   const int krows = std::min(page, 64), vrows = std::min(page, C::vkeys);
+  if (!query_map(&qmap, p, DH)) return cudaErrorInvalidValue;
   if (!code_map(&kmap, p.c.k, C::quant, DH, n_vec, C::quant ? C::panels * 64 : 64, krows, krows == 64 ? C::panels : 1) ||
       !code_map(&vmap, p.c.v, C::quant, DH, n_vec, C::quant ? C::dv : 64, vrows, C::dv / 64))
     return cudaErrorInvalidValue;
@@ -989,7 +1138,7 @@ cudaError_t launch(const AttnParams& p, int page, int64_t n_vec, int64_t blocks,
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_tile_kernel<DH, KIND, CG>, p, kmap, vmap, status);
+  return cudaLaunchKernelEx(&cfg, attn_tile_kernel<DH, KIND, CG>, p, qmap, kmap, vmap, status);
 }
 
 template <int DH, int CG>
@@ -1004,7 +1153,7 @@ cudaError_t by_kind(int kind, const AttnParams& p, int page, int64_t n_vec, int6
 
 cudaError_t attn_tile_launch(int kind, int dh, int page, int64_t n_vec, const AttnParams& p, int64_t blocks,
                              int* status, int dev, cudaStream_t s) {
-  if (p.block_shift == 8)
+  if (p.block > kTileM / p.group)
     return dh == 128 ? by_kind<128, 2>(kind, p, page, n_vec, blocks, status, dev, s)
                      : by_kind<256, 2>(kind, p, page, n_vec, blocks, status, dev, s);
   return dh == 64    ? by_kind<64, 1>(kind, p, page, n_vec, blocks, status, dev, s)

@@ -133,6 +133,17 @@ def test_a_prompt_of_many_tiles(fak):
     case(fak, "e4m3", 4, 1, 128, 16, [(1100, 2000), (900, 900)], seed=6)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_blocks_to_an_sm(fak, kind):
+    # each SM works on several blocks one after the other: short ones (a window), cut ones, ragged ones, one tile only,
+    # and blocks that see nothing between others
+    case(fak, kind, 32, 8, 128, 32, [(2048, 5000)], seed=30, window=1024, sinks=4)
+    case(fak, kind, 24, 4, 256, 64, [(700, 3000)], seed=31, gate=True)
+    case(fak, kind, 16, 16, 64, 16, [(900, 1300), (1, 2000), (0, 70), (640, 640)], seed=32)
+    case(fak, kind, 24, 4, 256, 16, [(200 + 37 * i, 200 + 37 * i) for i in range(9)], seed=33, window=100, sinks=1)
+    case(fak, kind, 32, 8, 128, 16, [(40 + i, 100 * (i % 3) + 3) for i in range(40)], seed=34)
+
+
 def test_a_full_batch_of_single_tokens(fak):
     lengths = [(1, 1 + (37 * i) % 900) for i in range(64)]
     case(fak, "e4m3", 24, 4, 256, 64, lengths, seed=7, gate=True)
