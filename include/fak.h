@@ -526,7 +526,8 @@ int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch, int64_t ro
 typedef struct {
     int32_t nq;             /* query heads, a multiple of n_kv, nq / n_kv <= 128 */
     int32_t window, sinks;  /* window 0: all positions */
-    int32_t max_q, max_kv;  /* bounds on the sequences' rows and kv_len (a sequence above them is left out, recorded) */
+    int32_t max_q, max_kv;  /* bounds on the sequences' rows (<= 2^28) and kv_len (<= 2^29); a sequence above them is
+                               left out, recorded */
     float scale;            /* > 0 */
     int64_t rows;
     const void* q;          /* device bf16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned */

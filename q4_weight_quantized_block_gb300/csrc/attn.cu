@@ -113,7 +113,7 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   pl.blocks = pl.few ? b->n_seqs : a->rows / pl.block + b->n_seqs;  // see find_unit
   pl.tile = !pl.few ? kTileN : c->kind == FAK_KV_BF16 || c->dh > 128 ? kRowsN : 2 * kRowsN;
   int64_t tiles = ((int64_t)a->max_kv + pl.tile - 1) / pl.tile;
-  if (a->window) {
+  if (a->window && a->window < a->max_kv) {
     const int64_t span = pl.block;
     tiles = std::min<int64_t>(tiles, ((int64_t)a->window + span) / pl.tile + 2 +
                                          std::min<int64_t>((int64_t)a->sinks / pl.tile + 1, tiles));
@@ -176,7 +176,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
   if (a->window < 0 || a->sinks < 0 || !(a->scale > 0.0f) || !std::isfinite(a->scale)) return FAK_ERR_INVALID_ARG;
   if (a->nq < 1 || a->nq % c->n_kv || a->nq / c->n_kv > 128 || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
-      a->max_kv < 0 || a->max_kv > 1 << 30 || a->nq > 65535)
+      a->max_kv < 0 || a->max_q > 1 << 28 || a->max_kv > 1 << 29 || a->nq > 65535)
     return FAK_ERR_SHAPE;
   return FAK_OK;
 }
@@ -237,8 +237,8 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.tile_shift = pl.tile == 64 ? 6 : 7;
   p.by_group = quotient(p.group);
   p.by_block = quotient(p.block);
-  p.window = a->window;
-  p.sinks = a->window ? a->sinks : 0;
+  p.window = a->window >= a->max_kv ? 0 : a->window;  // (as wide as the longest sequence: none)
+  p.sinks = p.window ? std::min(a->sinks, a->max_kv) : 0;
   p.splits = pl.splits;
   p.per_split = pl.per_split;
   p.part = static_cast<float*>(a->workspace);

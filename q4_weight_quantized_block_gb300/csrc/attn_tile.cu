@@ -41,6 +41,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_device.cuh"
 #include "fak.h"
@@ -237,6 +238,9 @@ FAK_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort, u
     if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
   return mbar_wait_bounded(bar, parity, abort, timeout_ns);
 }
+
+// The n lowest bits (none for n <= 0, all from 64 on).
+FAK_DEV uint64_t first_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 FAK_DEV bool tile_cut(int p_lo, int p_hi, int tile, const AttnParams& p) {
   return keys_cut(p_lo, p_hi, tile * kTileN, tile * kTileN + kTileN - 1, p.window, p.sinks);
@@ -505,9 +509,13 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           }
           const bool cut = tile_cut(u.own_lo, u.own_hi, tile, p);
           if (cut) {
+            // the keys c that the row sees: c <= pos - j0, and beyond the window's edge or before the sinks' end
+            uint64_t seen = first_bits(pos - j0 + 1);
+            if (p.window) seen &= ~first_bits(pos - p.window - j0 + 1) | first_bits(p.sinks - j0);
+            const uint32_t bits[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (!sees(pos, j0 + c, p.window, p.sinks)) t[c] = -INFINITY;
+              if (!(bits[c >> 5] & (1u << (c & 31)))) t[c] = -INFINITY;
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -544,32 +552,37 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           const float base = m == -INFINITY ? 0.0f : m;
           float sum[2] = {0.0f, 0.0f};
           uint32_t w[32];
+          auto weights = [&](auto masked) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            float e[4];
+            for (int c = 0; c < 64; c += 4) {
+              float e[4];
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              fma2(e[j], e[j + 1], t[c + j], t[c + j + 1], p.scale, -base);
-              e[j] = exp2_approx(e[j]);
-              e[j + 1] = exp2_approx(e[j + 1]);
-              add2(sum[0], sum[1], e[j], e[j + 1]);
-            }
-            if constexpr (C::quant) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + c);
-              if (cut) {
-                // a weight of zero stays zero, whatever scale stands at the place of a key that is not seen
-                e[0] = e[0] == 0.0f ? 0.0f : e[0] * f.x;
-                e[1] = e[1] == 0.0f ? 0.0f : e[1] * f.y;
-                e[2] = e[2] == 0.0f ? 0.0f : e[2] * f.z;
-                e[3] = e[3] == 0.0f ? 0.0f : e[3] * f.w;
-              } else {
-                mul2(e[0], e[1], f.x, f.y);
-                mul2(e[2], e[3], f.z, f.w);
+              for (int j = 0; j < 4; j += 2) {
+                fma2(e[j], e[j + 1], t[c + j], t[c + j + 1], p.scale, -base);
+                e[j] = exp2_approx(e[j]);
+                e[j + 1] = exp2_approx(e[j + 1]);
+                add2(sum[0], sum[1], e[j], e[j + 1]);
               }
+              if constexpr (C::quant) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + kTileN + c);
+                const float v[4] = {f.x, f.y, f.z, f.w};
+                if constexpr (decltype(masked)::value) {
+                  // a weight of zero stays zero, whatever scale stands at the place of a key that is not seen
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) e[j] = e[j] == 0.0f ? 0.0f : e[j] * v[j];
+                } else {
+                  mul2(e[0], e[1], v[0], v[1]);
+                  mul2(e[2], e[3], v[2], v[3]);
+                }
+              }
+              w[c / 2] = pack_bf16(e[0], e[1]);
+              w[c / 2 + 1] = pack_bf16(e[2], e[3]);
             }
-            w[c / 2] = pack_bf16(e[0], e[1]);
-            w[c / 2 + 1] = pack_bf16(e[2], e[3]);
-          }
+          };
+          if (C::quant && cut)
+            weights(std::true_type());
+          else
+            weights(std::false_type());
           l += sum[0] + sum[1];
           tmem_st32(scol, w);
           tmem_wait_st();
@@ -618,18 +631,37 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
         const int64_t place = ((int64_t)u.split * p.c.rows + grow) * p.nq + head;
         if (!u.direct && mine && half == 0) p.stat[place] = make_float2(m, l);
         // 16 dims at a time turn in shared memory, so that a row's are stored 32 bytes (as f32: 64) in a piece:
-        // four lanes a row, eight rows a step
+        // four lanes a row, eight rows a step.  The next dims leave TMEM meanwhile.
         const int64_t to = u.direct ? grow * p.out_row + head * p.out_head : place * DH;
         const int64_t from = p.gate ? grow * p.gate_row + head * p.gate_head : 0;
         float* turn = reinterpret_cast<float*>(smem + C::off_turn) + warp * 512;
-#pragma unroll 1
+        const int d1 = half * (DH / 2);
+        const bool gated = p.gate && u.direct;
+        int64_t at[4], gate_at[4];
+        bool there[4], blank[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int rr = 8 * e + (lane >> 2);
+          at[e] = __shfl_sync(0xffffffffu, to, rr) + d1 + 4 * (lane & 3);
+          gate_at[e] = __shfl_sync(0xffffffffu, from, rr) + d1 + 4 * (lane & 3);
+          blank[e] = __shfl_sync(0xffffffffu, (int)zero, rr);
+          there[e] = 32 * quarter + rr < u.nrows;
+        }
+        uint32_t o[2][16] = {};
+        if (n > 0) tmem_ld_cols<16>(tmem + lanes + (uint32_t)d1, o[0]);
+#pragma unroll 2
         for (int c = 0; c < DH / 2; c += 16) {
-          const int d0 = half * (DH / 2) + c;
-          uint32_t o[16] = {};
+          uint32_t(&x)[16] = o[(c >> 4) & 1];
+          float4 gate[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (gated && there[e] && !blank[e]) gate[e] = *reinterpret_cast<const float4*>(p.gate + gate_at[e] + c);
           if (n > 0) {
-            tmem_ld_cols<16>(tmem + lanes + (uint32_t)d0, o);
             tmem_wait_ld();
-            if (c == DH / 2 - 16) freed();
+            if (c + 16 < DH / 2)
+              tmem_ld_cols<16>(tmem + lanes + (uint32_t)(d1 + c + 16), o[((c >> 4) & 1) ^ 1]);
+            else
+              freed();
           }
           if (!C::quant && mine && *odd) {
             // values that are not finite, in tiles where they were left out: added for the rows that see them
@@ -640,13 +672,13 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
 #pragma unroll 1
               for (int j = tile * kTileN; j < min((tile + 1) * kTileN, pos + 1); ++j) {
                 if (!sees(pos, j, p.window, p.sinks)) continue;
-                int64_t at = kv_place(p.c, u.seq, j, u.head);
-                if (at < 0) at = -1 - at;
-                const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v) + at * DH + d0;
+                int64_t v_at = kv_place(p.c, u.seq, j, u.head);
+                if (v_at < 0) v_at = -1 - v_at;
+                const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v) + v_at * DH + d1 + c;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   if ((v[e] & 0x7F80u) == 0x7F80u)
-                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float((uint32_t)v[e] << 16));
+                    x[e] = __float_as_uint(__uint_as_float(x[e]) + __uint_as_float((uint32_t)v[e] << 16));
               }
             }
           }
@@ -654,33 +686,26 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<float4*>(turn + lane * 16 + ((e ^ ((lane >> 1) & 3)) << 2)) =
-                make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
-                            __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
+                make_float4(__uint_as_float(x[4 * e]) * scale, __uint_as_float(x[4 * e + 1]) * scale,
+                            __uint_as_float(x[4 * e + 2]) * scale, __uint_as_float(x[4 * e + 3]) * scale);
           __syncwarp();
-          float4 y[4], x[4];
-          int64_t at[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int rr = 8 * e + (lane >> 2), d = d0 + 4 * (lane & 3);
-            at[e] = __shfl_sync(0xffffffffu, to, rr) + d;
-            const int64_t gf = __shfl_sync(0xffffffffu, from, rr) + d;
-            const bool blank = __shfl_sync(0xffffffffu, (int)zero, rr);
-            y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            x[e] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
-            if (32 * quarter + rr >= u.nrows || blank) continue;
-            y[e] = *reinterpret_cast<const float4*>(turn + rr * 16 + (((lane & 3) ^ ((rr >> 1) & 3)) << 2));
-            if (p.gate && u.direct) x[e] = *reinterpret_cast<const float4*>(p.gate + gf);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (32 * quarter + 8 * e + (lane >> 2) >= u.nrows) continue;
-            if (u.direct) {
-              const uint2 w = make_uint2(pack_bf16(gated_by(y[e].x, x[e].x), gated_by(y[e].y, x[e].y)),
-                                         pack_bf16(gated_by(y[e].z, x[e].z), gated_by(y[e].w, x[e].w)));
-              *reinterpret_cast<uint2*>(p.out + at[e]) = w;
-            } else {
-              *reinterpret_cast<float4*>(p.part + at[e]) = y[e];
+            const int rr = 8 * e + (lane >> 2);
+            if (!there[e]) continue;
+            float4 y = *reinterpret_cast<const float4*>(turn + rr * 16 + (((lane & 3) ^ ((rr >> 1) & 3)) << 2));
+            if (blank[e]) y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!u.direct) {
+              *reinterpret_cast<float4*>(p.part + at[e] + c) = y;
+              continue;
             }
+            if (gated && !blank[e]) {
+              y.x = gated_by(y.x, gate[e].x);
+              y.y = gated_by(y.y, gate[e].y);
+              y.z = gated_by(y.z, gate[e].z);
+              y.w = gated_by(y.w, gate[e].w);
+            }
+            *reinterpret_cast<uint2*>(p.out + at[e] + c) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
           }
         }
       }
