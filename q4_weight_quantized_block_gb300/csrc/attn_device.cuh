@@ -122,12 +122,6 @@ FAK_DEV void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   hi = spread_to_bf16<KIND>(prmt(w, w, 0x3322));
 }
 
-// Code e of word v, code e of word w.
-template <int KIND>
-FAK_DEV uint32_t code_pair(uint32_t v, uint32_t w, int e) {
-  return spread_to_bf16<KIND>(prmt(v, w, 0x4400u + 0x1111u * (uint32_t)e));
-}
-
 // bf16 pair with values that are not finite made zero; sets odd if there was one
 FAK_DEV uint32_t finite2(uint32_t w, bool& odd) {
   uint32_t m = 0xffffffffu;

@@ -11,9 +11,11 @@
 // are cut over blocks, which the join kernel adds.
 // Each row's maximum moves only when passed by 8, as in the blocks' kernel (attn_tile.cu).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_device.cuh"
 #include "fak.h"
@@ -23,11 +25,74 @@ namespace {
 
 constexpr int kWarps = 4;
 
+// d += A B, bf16 or (F16) f16.
+template <bool F16>
 FAK_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8-bit codes as f16, exactly.  e4m3: one conversion for two.  int8, with the sign bit turned over: 0x6400 + code is
+// 1024 + code in f16, less 1152.
+FAK_DEV uint32_t less_1152(uint32_t x) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(0x64806480u));
+  return d;
+}
+FAK_DEV uint32_t e4m3_to_f16(uint32_t two) {
+  uint32_t d;
+  asm("{ .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(two));
+  return d;
+}
+
+// The four codes of a word, in order.
+template <int KIND>
+FAK_DEV void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KIND == FAK_KV_E4M3) {
+    lo = e4m3_to_f16(w & 0xffffu);
+    hi = e4m3_to_f16(w >> 16);
+  } else {
+    const uint32_t x = w ^ 0x80808080u;
+    lo = less_1152(prmt(x, 0x64646464u, 0x4140));
+    hi = less_1152(prmt(x, 0x64646464u, 0x4342));
+  }
+}
+
+// Each code of v beside the same code of w.
+template <int KIND>
+FAK_DEV void pairs_to_f16(uint32_t v, uint32_t w, uint32_t (&d)[4]) {
+  if constexpr (KIND == FAK_KV_E4M3) {
+    uint32_t v0, v1, w0, w1;
+    codes_to_f16<KIND>(v, v0, v1);
+    codes_to_f16<KIND>(w, w0, w1);
+    d[0] = prmt(v0, w0, 0x5410);
+    d[1] = prmt(v0, w0, 0x7632);
+    d[2] = prmt(v1, w1, 0x5410);
+    d[3] = prmt(v1, w1, 0x7632);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      d[e] = less_1152((prmt(v, w, 0x4400u + 0x1111u * (uint32_t)e) & 0x00FF00FFu) ^ 0x64806480u);
+  }
+}
+
+FAK_DEV uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+constexpr float kLeast = -80.0f;
+
+FAK_DEV float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 FAK_DEV uint32_t transpose8(uint32_t x) {
@@ -57,10 +122,11 @@ struct RCfg {
   // a lane's slots: halves of a step in turn, K and V
   static constexpr int part = 16 * DH * bytes;                         // bytes of a warp's 16 keys
   static constexpr int half = groups * (part + (quant ? 512 : 0));     // of a half (with 16 of scales a lane and group)
-  // three (16 rows, or steps of 16 KB: two) blocks of four warps on an SM, as many halves as then have room
-  static constexpr int blocks = NT == 1 && half < 8192 ? 3 : 2;
-  static constexpr int room = 113000 * 2 / blocks / kWarps - 512;
+  // blocks of four warps on an SM, as many halves as then have room
+  static constexpr int blocks = quant && NT == 1 ? 3 : 2;
+  static constexpr int room = (233472 / blocks - 1536) / kWarps;
   static constexpr int halves = room / half < 8 ? room / half : 8;
+  static constexpr float above = quant ? 7.0f : 0.0f, reach = above + 8.0f;
   static constexpr int row = DH + 8;  // floats of a row where the warps' sums meet
   static constexpr int sums = kWarps * 8 * NT * row * 4;
   static constexpr int smem = kWarps * halves * half > sums ? kWarps * halves * half : sums;
@@ -190,6 +256,28 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
       pos[nt][c] = rr < nrows ? p0 + p.by_group(rr) : -1;
     }
   }
+  // 8-bit: Q as f16, which holds a bf16's significand, each row by the power of two that brings its largest to 1 .. 2
+  // (what is then below 2^-24 is lost, 2^-24 of the largest); its inverse goes into the scores
+  float qf[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    uint32_t top = 0;
+    if constexpr (C::quant) {
+#pragma unroll
+      for (int w = 0; w < DH / 8; ++w) top = max(top, max(q[nt][w] << 16 & 0x7fff0000u, q[nt][w] & 0x7fff0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = min(max(top & 0x7f800000u, 0x00800000u), 0x7e800000u);  // the exponent alone, and one that has an inverse
+      const float up = __uint_as_float(top), down = __uint_as_float(0x7f000000u - top);
+#pragma unroll
+      for (int w = 0; w < DH / 8; ++w)
+        q[nt][w] = pack_f16(__uint_as_float(q[nt][w] << 16) * down, __uint_as_float(q[nt][w] & 0xffff0000u) * down);
+      qf[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t) * p.scale;      // rows 2t, 2t + 1 are lanes (2t, .), (2t + 1, .)
+      qf[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4) * p.scale;
+    } else {
+      qf[nt][0] = qf[nt][1] = p.scale;
+    }
+  }
   float o[NT][DH / 16][4] = {};
   float m[NT][2], l[NT][2];
 #pragma unroll
@@ -200,10 +288,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
       l[nt][c] = 0.0f;
     }
 
-  // The product of a step runs beside the scores of the next, which do not depend on it: converting codes, half the
-  // instructions, fills the gaps that one of the two would leave.
   float s[G][NT][4];  // s[x][nt][c + 2 h]: key 16 x + g + 8 h, row 2t + c + 8 nt
-  float kf[G][2], vn[G][2] = {}, vf[G][2];  // the scales of the scores' keys and values, of the weights' values
+  float kf[G][2], vl[G][2];  // 8-bit: the keys' scales, log2 of the values'
   uint32_t pb[G][NT][2];
   auto scores = [&](const uint8_t* from) {
 #pragma unroll
@@ -223,28 +309,31 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t k0, k1, l0, l1;
-            codes_to_bf16<KIND>(a0[w], k0, k1);
-            codes_to_bf16<KIND>(a1[w], l0, l1);
+            codes_to_f16<KIND>(a0[w], k0, k1);
+            codes_to_f16<KIND>(a1[w], l0, l1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[x][nt], k0, l0, k1, l1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
+              mma16816<true>(s[x][nt], k0, l0, k1, l1, q[nt][8 * b + 2 * w], q[nt][8 * b + 2 * w + 1]);
           }
         } else {
 #pragma unroll
           for (int w = 0; w < 4; w += 2)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[x][nt], a0[w], a1[w], a0[w + 1], a1[w + 1], q[nt][4 * b + w], q[nt][4 * b + w + 1]);
+              mma16816<false>(s[x][nt], a0[w], a1[w], a0[w + 1], a1[w + 1], q[nt][4 * b + w], q[nt][4 * b + w + 1]);
         }
       }
     if constexpr (C::quant) {
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         const float4 f = *reinterpret_cast<const float4*>(from + x * gpart + C::part);
-        vn[x][0] = f.z;
-        vn[x][1] = f.w;
-        kf[x][0] = f.x * p.scale;
-        kf[x][1] = f.y * p.scale;
+        kf[x][0] = f.x;
+        kf[x][1] = f.y;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = log2_approx(h ? f.w : f.z);
+          vl[x][h] = y < kLeast ? kLeast : y;  // (NaN stays)
+        }
       }
     }
   };
@@ -252,32 +341,36 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     const bool scut = keys_cut(p_lo, p_hi, sj, sj + 16 * G - 1, p.window, p.sinks);
 #pragma unroll
     for (int x = 0; x < G; ++x) {
-      vf[x][0] = vn[x][0];
-      vf[x][1] = vn[x][1];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s[x][nt][c] *= C::quant ? kf[x][c >> 1] : p.scale;
+          s[x][nt][c] *= C::quant ? kf[x][c >> 1] * qf[nt][c & 1] : qf[nt][c & 1];
           if (scut && !sees(pos[nt][c & 1], sj + 16 * x + g + 8 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
         }
     }
+    // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m the maximum of those exponents (so
+    // that weights fit f16 whatever the scales are); the weights' sum is of 2^(t - m)
+    auto heavy = [&](int x, int nt, int c) {
+      if constexpr (C::quant) return s[x][nt][c] + vl[x][c >> 1];
+      return s[x][nt][c];
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-        if constexpr (G == 2) top[c] = fmaxf(top[c], fmaxf(s[G - 1][nt][c], s[G - 1][nt][c + 2]));
+        top[c] = fmaxf(heavy(0, nt, c), heavy(0, nt, c + 2));
+        if constexpr (G == 2) top[c] = fmaxf(top[c], fmaxf(heavy(G - 1, nt, c), heavy(G - 1, nt, c + 2)));
       }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
         top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], x));
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
       }
-      const bool up0 = top[0] > m[nt][0] + 8.0f, up1 = top[1] > m[nt][1] + 8.0f;
+      const bool up0 = top[0] > m[nt][0] + C::reach, up1 = top[1] > m[nt][1] + C::reach;
       if (__any_sync(0xffffffffu, up0 || up1)) {
-        const float n0 = up0 ? top[0] : m[nt][0], n1 = up1 ? top[1] : m[nt][1];
+        const float n0 = up0 ? top[0] - C::above : m[nt][0], n1 = up1 ? top[1] - C::above : m[nt][1];
         const float f0 = up0 ? exp2_approx(m[nt][0] - n0) : 1.0f, f1 = up1 ? exp2_approx(m[nt][1] - n1) : 1.0f;
         m[nt][0] = n0;
         m[nt][1] = n1;
@@ -299,29 +392,19 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         for (int c = 0; c < 4; ++c) {
           w[c] = exp2_approx(s[x][nt][c] - base[c & 1]);
           l[nt][c & 1] += w[c];
-          // a weight of zero stays zero, whatever scale stands at its place
-          if constexpr (C::quant) w[c] = w[c] == 0.0f ? 0.0f : w[c] * vf[x][c >> 1];
+          if constexpr (C::quant) {
+            w[c] = exp2_approx(heavy(x, nt, c) - base[c & 1]);
+            // (the scale of a key that is not seen may be anything)
+            if (scut && s[x][nt][c] == -INFINITY) w[c] = 0.0f;
+          }
         }
-        pb[x][nt][0] = transpose8(pack_bf16(w[0], w[1]));
-        pb[x][nt][1] = transpose8(pack_bf16(w[2], w[3]));
+        pb[x][nt][0] = transpose8(C::quant ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]));
+        pb[x][nt][1] = transpose8(C::quant ? pack_f16(w[2], w[3]) : pack_bf16(w[2], w[3]));
       }
     }
   };
-  if (j0 >= 0) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 1) : "memory");
-    scores(mine);
-    fetch(0, oddly);  // (what stood there has been multiplied)
-    softmax(j0);
-  }
-  int slot = 1;
-  while (j0 >= 0) {
-    int ni = i, nj = j0;
-    next(ni, nj);
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::halves - 2) : "memory");
-    const int kslot = slot + 1 == C::halves ? 0 : slot + 1;
+  auto product = [&](const uint8_t* from) {
     const bool cut = keys_cut(p_lo, p_hi, j0, j0 + 16 * G - 1, p.window, p.sinks);
-    scores(mine + kslot * C::half);  // (past the last step: of what stood there, and not used)
-    const uint8_t* from = mine_v + slot * C::half;
     bool odd = false;
 #pragma unroll
     for (int x = 0; x < G; ++x)
@@ -340,6 +423,16 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
             const uint2 y = *reinterpret_cast<const uint2*>(from + x * gpart + (b * 4 + k) * vstep);
             vx[k][0] = y.x;
             vx[k][1] = y.y;
+          }
+        }
+        if (C::quant && cut) {
+          // codes that no row sees may be e4m3's NaN
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + 16 * x + 2 * t + (k & 1) + 8 * (k >> 1);
+            const bool seen = j <= p_hi && (!p.window || j > p_lo - p.window || j < p.sinks);
+#pragma unroll
+            for (int w = 0; w < C::vw; ++w) vx[k][w] = seen ? vx[k][w] : 0u;
           }
         }
         if (!C::quant && cut) {
@@ -365,8 +458,10 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           for (int k = 0; k < 2; ++k) {
             const uint32_t v0 = vx[2 * k][w], v1 = vx[2 * k + 1][w];
             if constexpr (C::quant) {
+              uint32_t d[4];
+              pairs_to_f16<KIND>(v0, v1, d);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e][k] = code_pair<KIND>(v0, v1, e);
+              for (int e = 0; e < 4; ++e) y[e][k] = d[e];
             } else {
               y[0][k] = prmt(v0, v1, 0x5410);
               y[1][k] = prmt(v0, v1, 0x7632);
@@ -377,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
             const int d = b * (C::ve / 2) + w * (C::quant ? 2 : 1) + h;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(o[nt][d], y[2 * h][0], y[2 * h + 1][0], y[2 * h][1], y[2 * h + 1][1], pb[x][nt][0], pb[x][nt][1]);
+              mma16816<C::quant>(o[nt][d], y[2 * h][0], y[2 * h + 1][0], y[2 * h][1], y[2 * h + 1][1], pb[x][nt][0], pb[x][nt][1]);
           }
         }
       }
@@ -401,10 +496,32 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
               }
         }
     }
+  };
+  int slot = 0;
+  auto advance = [&]() { slot = slot + 1 == C::halves ? 0 : slot + 1; };
+  auto landed = [&](auto behind) {  // all but the last `behind` halves asked for
+    asm volatile("cp.async.wait_group %0;" ::"n"(decltype(behind)::value) : "memory");
+  };
+  // the product of a step runs beside the scores of the next, which do not depend on it
+  if (j0 >= 0) {
+    landed(std::integral_constant<int, C::halves - 1>());
+    scores(mine);
+    fetch(0, oddly);  // (what stood there has been multiplied)
+    advance();
+    softmax(j0);
+  }
+  while (j0 >= 0) {
+    int ni = i, nj = j0;
+    next(ni, nj);
+    landed(std::integral_constant<int, C::halves - 2>());
+    const int kslot = slot + 1 == C::halves ? 0 : slot + 1;
+    scores(mine + kslot * C::half);  // (past the last step: of what stood there, and not used)
+    product(mine_v + slot * C::half);
     fetch(slot, !oddly);
     fetch(kslot, oddly);
     if (nj >= 0) softmax(nj);
-    slot = kslot + 1 == C::halves ? 0 : kslot + 1;
+    advance();
+    advance();
     i = ni;
     j0 = nj;
   }
