@@ -131,6 +131,15 @@ FAK_DEV uint32_t finite2(uint32_t w, bool& odd) {
   return w & m;
 }
 
+// One lane of a converged warp, the same each time: the compiler keeps what the lanes share in uniform registers
+// around it, where TMA and MMA instructions want their operands (a branch on the lane's number costs 100
+// cycles a load or MMA more).
+FAK_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // Records a device-side error of the call (attn.cu's status word).
 FAK_DEV void attn_record(int* status, int code) { atomicCAS(status, 0, code); }
 

@@ -15,7 +15,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
 
 #include "attn_device.cuh"
 #include "fak.h"
@@ -101,12 +100,12 @@ FAK_DEV uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int N>
-FAK_DEV void copy_async(void* dst, const void* src) {  // N = 4, 8 or 16 bytes
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(N) : "memory");
+// Bulk copy of consecutive bytes into shared memory, counted on an mbarrier; addresses and bytes multiples of 16.
+FAK_DEV void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 template <int DH, int KIND, int NT>
@@ -120,8 +119,8 @@ struct RCfg {
   static constexpr int vw = ve * bytes / 4;                    // words of one
   static constexpr int groups = quant && DH <= 128 ? 2 : 1;  // 16 keys each, of a step
   // a lane's slots: halves of a step in turn, K and V
-  static constexpr int part = 16 * DH * bytes;                         // bytes of a warp's 16 keys
-  static constexpr int half = groups * (part + (quant ? 512 : 0));     // of a half (with 16 of scales a lane and group)
+  static constexpr int row_bytes = DH * bytes, part = 16 * row_bytes;  // of a key, of a warp's 16 keys
+  static constexpr int half = groups * (part + (quant ? 128 : 0));     // of a half (with a group's scales)
   // blocks of four warps on an SM, as many halves as then have room
   static constexpr int blocks = quant && NT == 1 ? 3 : 2;
   static constexpr int room = (233472 / blocks - 1536) / kWarps;
@@ -173,33 +172,14 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     }
     return at;
   };
-  uint8_t* const mine = smem + warp * (C::halves * C::half) + lane * 16;            // K's
-  uint8_t* const mine_v = smem + warp * (C::halves * C::half) + lane * C::vw * 4;  // V's
-  constexpr int vstep = 32 * C::vw * 4;
-  // lane (g, t)'s part of K, of V
-  auto fetch_k = [&](uint8_t* to, int64_t at) {
-    const uint8_t* src = p.c.k + (at + g) * (DH * C::bytes) + t * 16;
+  uint8_t* const slots = smem + warp * (C::halves * C::half);
+  __shared__ uint64_t bars[kWarps][C::halves];  // a slot's bytes are there
+  if (lane == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int b = 0; b < C::kb; ++b)
-        copy_async<16>(to + (h * C::kb + b) * 512, src + h * 8 * DH * C::bytes + b * 64);
-    if constexpr (C::quant) {
-      const float *ks = p.c.ks + at + g, *vs = p.c.vs + at + g;
-      copy_async<4>(to + C::part, ks);
-      copy_async<4>(to + C::part + 4, ks + 8);
-      copy_async<4>(to + C::part + 8, vs);
-      copy_async<4>(to + C::part + 12, vs + 8);
-    }
-  };
-  auto fetch_v = [&](uint8_t* to, int64_t at) {
-    const uint8_t* src = p.c.v + (at + 2 * t) * (DH * C::bytes) + g * (C::vw * 4);
-#pragma unroll
-    for (int b = 0; b < C::vb; ++b)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        copy_async<C::vw * 4>(to + (b * 4 + k) * vstep, src + ((k & 1) + 8 * (k >> 1)) * DH * C::bytes + b * 8 * C::vw * 4);
-  };
+    for (int h = 0; h < C::halves; ++h) mbar_init(&bars[warp][h], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   // fetched up to halves / 2 steps ahead of the one at work
   constexpr int G = C::groups, gpart = C::half / G;
   int fi = begin - 1, fj = 0;  // the step that is fetched
@@ -213,17 +193,21 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     }
   };
   places();
-  auto fetch = [&](int slot, bool value) {  // a half; a group without copies past the last step
-    if (fj >= 0) {
+  auto fetch = [&](int slot, bool value) {  // a half; nothing past the last step
+    __syncwarp();  // (what stood there has been read)
+    if (fj >= 0 && elect_one()) {
+      uint64_t* const bar = &bars[warp][slot];
+      mbar_arrive_expect_tx(bar, G * (C::part + (C::quant && !value ? 128 : 0)));
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        if (value)
-          fetch_v(mine_v + slot * C::half + x * gpart, fat[x]);
-        else
-          fetch_k(mine + slot * C::half + x * gpart, fat[x]);
+        uint8_t* const to = slots + slot * C::half + x * gpart;
+        copy_bulk(to, (value ? p.c.v : p.c.k) + fat[x] * C::row_bytes, C::part, bar);
+        if (C::quant && !value) {
+          copy_bulk(to + C::part, p.c.ks + fat[x], 64, bar);
+          copy_bulk(to + C::part + 64, p.c.vs + fat[x], 64, bar);
+        }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     if (value) {
       next(fi, fj);
       places();
@@ -302,8 +286,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     for (int b = 0; b < C::kb; ++b)
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(from + x * gpart + b * 512);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(from + x * gpart + (C::kb + b) * 512);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(from + x * gpart + g * C::row_bytes + b * 64 + t * 16);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(from + x * gpart + (g + 8) * C::row_bytes + b * 64 + t * 16);
         const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
         if constexpr (C::quant) {
 #pragma unroll
@@ -326,12 +310,12 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     if constexpr (C::quant) {
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        const float4 f = *reinterpret_cast<const float4*>(from + x * gpart + C::part);
-        kf[x][0] = f.x;
-        kf[x][1] = f.y;
+        const float* f = reinterpret_cast<const float*>(from + x * gpart + C::part);
+        kf[x][0] = f[g];
+        kf[x][1] = f[g + 8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float y = log2_approx(h ? f.w : f.z);
+          const float y = log2_approx(f[16 + g + 8 * h]);
           vl[x][h] = y < kLeast ? kLeast : y;  // (NaN stays)
         }
       }
@@ -413,14 +397,16 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         uint32_t vx[4][C::vw];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          const uint8_t* const at =
+              from + x * gpart + (2 * t + (k & 1) + 8 * (k >> 1)) * C::row_bytes + (b * 8 + g) * C::vw * 4;
           if constexpr (C::vw == 4) {
-            const uint4 y = *reinterpret_cast<const uint4*>(from + x * gpart + (b * 4 + k) * vstep);
+            const uint4 y = *reinterpret_cast<const uint4*>(at);
             vx[k][0] = y.x;
             vx[k][1] = y.y;
             vx[k][2] = y.z;
             vx[k][3] = y.w;
           } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(from + x * gpart + (b * 4 + k) * vstep);
+            const uint2 y = *reinterpret_cast<const uint2*>(at);
             vx[k][0] = y.x;
             vx[k][1] = y.y;
           }
@@ -499,24 +485,36 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   };
   int slot = 0;
   auto advance = [&]() { slot = slot + 1 == C::halves ? 0 : slot + 1; };
-  auto landed = [&](auto behind) {  // all but the last `behind` halves asked for
-    asm volatile("cp.async.wait_group %0;" ::"n"(decltype(behind)::value) : "memory");
+  uint32_t phases = 0;  // of the slots
+  auto landed = [&](int h) {
+    uint64_t* const bar = &bars[warp][h];
+    const uint32_t parity = phases >> h & 1;
+    phases ^= 1u << h;
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_suspend(bar, parity, 20000u))
+      if (globaltimer_ns() - t0 > p.timeout_ns) {
+        attn_record(status, FAK_ERR_TIMEOUT);
+        return;
+      }
   };
   // the product of a step runs beside the scores of the next, which do not depend on it
   if (j0 >= 0) {
-    landed(std::integral_constant<int, C::halves - 1>());
-    scores(mine);
-    fetch(0, oddly);  // (what stood there has been multiplied)
+    landed(0);
+    scores(slots);
+    fetch(0, oddly);
     advance();
     softmax(j0);
   }
   while (j0 >= 0) {
     int ni = i, nj = j0;
     next(ni, nj);
-    landed(std::integral_constant<int, C::halves - 2>());
     const int kslot = slot + 1 == C::halves ? 0 : slot + 1;
-    scores(mine + kslot * C::half);  // (past the last step: of what stood there, and not used)
-    product(mine_v + slot * C::half);
+    landed(slot);
+    if (nj >= 0) landed(kslot);
+    scores(slots + kslot * C::half);  // (past the last step: of what stood there, and not used)
+    product(slots + slot * C::half);
     fetch(slot, !oddly);
     fetch(kslot, oddly);
     if (nj >= 0) softmax(nj);
@@ -526,7 +524,6 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     j0 = nj;
   }
 
-  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();  // the slots become the place where the sums meet
   // the four warps' sums
 #pragma unroll

@@ -212,15 +212,6 @@ FAK_DEV void fma2(float& a, float& b, float x, float y, float f, float c) {  // 
   of_two(a, b, d);
 }
 
-// One lane of a converged warp, the same each time: the compiler keeps what the lanes share in uniform registers
-// around it, where TMA and MMA instructions want their operands (a branch on the lane's number costs 100
-// cycles a load or MMA more).
-FAK_DEV bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
 FAK_DEV bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
