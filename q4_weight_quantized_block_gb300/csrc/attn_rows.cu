@@ -108,6 +108,8 @@ FAK_DEV void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar
                : "memory");
 }
 
+FAK_DEV int key_of(int i) { return ((i >> 1) ^ (i & 1) << 1) * 4 + (i & 1); }
+
 template <int DH, int KIND, int NT>
 struct RCfg {
   static constexpr bool quant = KIND != FAK_KV_BF16;
@@ -119,7 +121,10 @@ struct RCfg {
   static constexpr int vw = ve * bytes / 4;                    // words of one
   static constexpr int groups = quant && DH <= 128 ? 2 : 1;  // 16 keys each, of a step
   // a lane's slots: halves of a step in turn, K and V
-  static constexpr int row_bytes = DH * bytes, part = 16 * row_bytes;  // of a key, of a warp's 16 keys
+  // 16 keys come in four copies, 32 bytes apart in the banks, and index i of the instructions' 8 (and i + 8) is key
+  // key_of(i) (and that + 2): what 8 lanes load at once, two neighbouring indices' 64 bytes of K or four's 32 bytes of
+  // V (every other index), then lies in different banks
+  static constexpr int row_bytes = DH * bytes, four = 4 * row_bytes + 32, part = 4 * four;
   static constexpr int half = groups * (part + (quant ? 128 : 0));     // of a half (with a group's scales)
   // blocks of four warps on an SM, as many halves as then have room
   static constexpr int blocks = quant && NT == 1 ? 3 : 2;
@@ -197,11 +202,13 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     __syncwarp();  // (what stood there has been read)
     if (fj >= 0 && elect_one()) {
       uint64_t* const bar = &bars[warp][slot];
-      mbar_arrive_expect_tx(bar, G * (C::part + (C::quant && !value ? 128 : 0)));
+      mbar_arrive_expect_tx(bar, G * (16 * C::row_bytes + (C::quant && !value ? 128 : 0)));
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         uint8_t* const to = slots + slot * C::half + x * gpart;
-        copy_bulk(to, (value ? p.c.v : p.c.k) + fat[x] * C::row_bytes, C::part, bar);
+        const uint8_t* const src = (value ? p.c.v : p.c.k) + fat[x] * C::row_bytes;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) copy_bulk(to + c * C::four, src + c * 4 * C::row_bytes, 4 * C::row_bytes, bar);
         if (C::quant && !value) {
           copy_bulk(to + C::part, p.c.ks + fat[x], 64, bar);
           copy_bulk(to + C::part + 64, p.c.vs + fat[x], 64, bar);
@@ -272,7 +279,9 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
       l[nt][c] = 0.0f;
     }
 
-  float s[G][NT][4];  // s[x][nt][c + 2 h]: key 16 x + g + 8 h, row 2t + c + 8 nt
+  const int kg = key_of(g), krow = (kg >> 2) * C::four + (kg & 3) * C::row_bytes;
+  const int vrow[2] = {t * C::four, (t ^ 2) * C::four + C::row_bytes};  // keys key_of(2t), key_of(2t + 1)
+  float s[G][NT][4];  // s[x][nt][c + 2 h]: key 16 x + kg + 2 h, row 2t + c + 8 nt
   float kf[G][2], vl[G][2];  // 8-bit: the keys' scales, log2 of the values'
   uint32_t pb[G][NT][2];
   auto scores = [&](const uint8_t* from) {
@@ -286,8 +295,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     for (int b = 0; b < C::kb; ++b)
 #pragma unroll
       for (int x = 0; x < G; ++x) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(from + x * gpart + g * C::row_bytes + b * 64 + t * 16);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(from + x * gpart + (g + 8) * C::row_bytes + b * 64 + t * 16);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(from + x * gpart + krow + b * 64 + t * 16);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(from + x * gpart + krow + 2 * C::row_bytes + b * 64 + t * 16);
         const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
         if constexpr (C::quant) {
 #pragma unroll
@@ -311,11 +320,11 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         const float* f = reinterpret_cast<const float*>(from + x * gpart + C::part);
-        kf[x][0] = f[g];
-        kf[x][1] = f[g + 8];
+        kf[x][0] = f[kg];
+        kf[x][1] = f[kg + 2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float y = log2_approx(f[16 + g + 8 * h]);
+          const float y = log2_approx(f[16 + kg + 2 * h]);
           vl[x][h] = y < kLeast ? kLeast : y;  // (NaN stays)
         }
       }
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           s[x][nt][c] *= C::quant ? kf[x][c >> 1] * qf[nt][c & 1] : qf[nt][c & 1];
-          if (scut && !sees(pos[nt][c & 1], sj + 16 * x + g + 8 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
+          if (scut && !sees(pos[nt][c & 1], sj + 16 * x + kg + 2 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
         }
     }
     // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m the maximum of those exponents (so
@@ -397,8 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         uint32_t vx[4][C::vw];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint8_t* const at =
-              from + x * gpart + (2 * t + (k & 1) + 8 * (k >> 1)) * C::row_bytes + (b * 8 + g) * C::vw * 4;
+          const uint8_t* const at = from + x * gpart + vrow[k & 1] + (k >> 1) * 2 * C::row_bytes + (b * 8 + g) * C::vw * 4;
           if constexpr (C::vw == 4) {
             const uint4 y = *reinterpret_cast<const uint4*>(at);
             vx[k][0] = y.x;
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           // codes that no row sees may be e4m3's NaN
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int j = j0 + 16 * x + 2 * t + (k & 1) + 8 * (k >> 1);
+            const int j = j0 + 16 * x + key_of(2 * t + (k & 1)) + 2 * (k >> 1);
             const bool seen = j <= p_hi && (!p.window || j > p_lo - p.window || j < p.sinks);
 #pragma unroll
             for (int w = 0; w < C::vw; ++w) vx[k][w] = seen ? vx[k][w] : 0u;
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           // product, and added for the rows that do see them; keys past the last that is seen are zeros
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const bool past = j0 + 2 * t + (k & 1) + 8 * (k >> 1) > p_hi;
+            const bool past = j0 + key_of(2 * t + (k & 1)) + 2 * (k >> 1) > p_hi;
 #pragma unroll
             for (int w = 0; w < C::vw; ++w) {
               bool change = false;
