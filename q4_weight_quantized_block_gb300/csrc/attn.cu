@@ -124,9 +124,9 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   pl.splits = 1;
   pl.per_split = (int)tiles;
   if (pl.few) {
-    // Two or three blocks to an SM.  One sequence's pieces are all alike: one round of them.  Several sequences
+    // One sequence's pieces are all alike: one round of them.  Several sequences
     // differ in length, which smaller pieces even out: four rounds, of pieces of 512 keys or more.
-    const int64_t places = (rows <= 8 && (c->kind != FAK_KV_BF16 || c->dh <= 128) ? 3 : 2) * kPlanSms, least = 512 / pl.tile;
+    const int64_t places = rows_blocks(c->kind != FAK_KV_BF16, c->dh, (int)rows) * kPlanSms, least = 512 / pl.tile;
     const int64_t four = std::max<int64_t>(1, 4 * places / busy), one = std::max<int64_t>(1, places / busy);
     int64_t per = std::max<int64_t>(least, (tiles + four - 1) / four);
     if (b->n_seqs == 1 || (tiles + per - 1) / per * busy < places) per = (tiles + one - 1) / one;
@@ -135,11 +135,12 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
     return pl;
   }
   // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each as long as a piece
-  // and about three tiles' time to begin and to end; a cut costs two more for the join.
+  // and the time of about three tiles to begin and to end, seven where it leaves its sums in memory, and four more for
+  // the join.  (512 rows after 8,191 keys of 256: whole 105 us, in two 127, in four 120; after 30,000: 313, 333, 277.)
   int64_t best = -1;
   for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
     const int64_t per = (tiles + s - 1) / s, n = (tiles + per - 1) / per;
-    const int64_t cost = (busy * n + kPlanSms - 1) / kPlanSms * (per + 3) + (n > 1 ? 2 : 0);
+    const int64_t cost = (busy * n + kPlanSms - 1) / kPlanSms * (per + (n > 1 ? 7 : 3)) + (n > 1 ? 4 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       pl.splits = (int)n;
@@ -159,7 +160,9 @@ size_t stat_bytes(const fak_attn_args* a, const Plan& pl) {
 
 template <int DH>
 cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
-  const bool many = p.splits > 8;
+  // 16 warps to a (row, query head) where pieces are many and the blocks run all at once (512 rows' nine pieces took
+  // 16 warps 190 us longer than one)
+  const bool many = p.splits > 8 && p.c.rows * p.nq <= 4 * kPlanSms;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)p.c.rows, (unsigned)(many ? p.nq : (p.nq + 7) / 8));

@@ -45,6 +45,9 @@ struct AttnParams {
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA
 constexpr int kTileN = 128;  // keys of a tile of the blocks' kernel
 constexpr int kRowsMax = 16;  // most rows of a sequence and KV head that the kernel for few rows takes
+// its blocks on an SM, as registers allow (64 sequences of up to 4,000 bf16 keys of 128: three 64 us, two 66; of up to
+// 8,191 e4m3 keys of 256: three 130, two 142, four, which spill, 160)
+constexpr int rows_blocks(bool quant, int dh, int rows) { return rows > 8 || (!quant && dh > 128) ? 2 : 3; }
 constexpr int kRowsN = 64;    // keys of its tiles (8-bit codes and dh up to 128: twice as many)
 
 FAK_DEV int ceil_div(int a, int b) { return (a + b - 1) / b; }

@@ -127,7 +127,7 @@ struct RCfg {
   static constexpr int row_bytes = DH * bytes, four = 4 * row_bytes + 32, part = 4 * four;
   static constexpr int half = groups * (part + (quant ? 128 : 0));     // of a half (with a group's scales)
   // blocks of four warps on an SM, as many halves as then have room
-  static constexpr int blocks = quant && NT == 1 ? 3 : 2;
+  static constexpr int blocks = rows_blocks(quant, DH, 8 * NT);
   static constexpr int room = (233472 / blocks - 1536) / kWarps;
   static constexpr int halves = room / half < 8 ? room / half : 8;
   static constexpr float above = quant ? 7.0f : 0.0f, reach = above + 8.0f;

@@ -350,8 +350,9 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
   uint64_t* uempty = ufull + 2;
   uint64_t* asked = uempty + 2;  // take_over's answer, and that both CTAs have read it
   uint64_t* heard = asked + 1;
-  uint64_t* drain = heard + 1;
-  static_assert((2 * C::ks + (C::quant ? 2 : 4) * C::vs + 4 * C::rs + (C::quant ? C::slots : 0) + 24) * 8 <= 656,
+  uint64_t* last = heard + 1;  // a block's copies of K have all been asked for
+  uint64_t* drain = last + 1;
+  static_assert((2 * C::ks + (C::quant ? 2 : 4) * C::vs + 4 * C::rs + (C::quant ? C::slots : 0) + 25) * 8 <= 656,
                 "barriers exceed their area");
   uint8_t* answer = smem + C::off_bar + 656;  // 16 bytes
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 672);
@@ -397,6 +398,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
     mbar_init(ofree, 8 * CG);
     mbar_init(asked, 1);
     mbar_init(heard, CG);
+    mbar_init(last, 1);
     mbar_init(drain, 1);
     *abort = 0;
     *odd = 0;
@@ -899,6 +901,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
           }
         }
       }
+      if (!value && lane == 0) mbar_arrive(last);
       release(k);
     }
     // copies in flight land before the CTA can end (one that ran to its end has used every copy)
@@ -931,15 +934,19 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       ++k;
     };
     for (int asks = 0; ok; ++asks) {
-      // ask for the next one while this one is worked out
+      Unit u;
+      if (find_unit(p, ((int)gridDim.x - 1 - x) / CG, y, z, rank, lane, u)) hand(u);
+      if (!ok) break;
+      // Ask for the next one when this one's last keys are on their way: a few tiles before it is needed, and late
+      // enough that it is not one that another SM would have begun at once (asked for at the start, 16 sequences' 64
+      // blocks of 32 tiles were done by some 45 pairs of CTAs: 112 us, and 70 as it is).
+      if (rank == 0 && k > 0 && !(ok = wait(last, (k - 1) & 1))) break;
       if (rank == 0 && asks > 0 && !(ok = wait(heard, (asks - 1) & 1))) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(asked, 16);
         if (rank == 0) take_over(answer, asked, CG == 2);
       }
       __syncwarp();
-      Unit u;
-      if (find_unit(p, ((int)gridDim.x - 1 - x) / CG, y, z, rank, lane, u)) hand(u);
       // (also after a failure: the answer must not arrive in a CTA that has ended)
       const bool came = wait(asked, asks & 1);
       ok = ok && came && !*abort;
