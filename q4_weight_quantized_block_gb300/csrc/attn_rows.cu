@@ -86,6 +86,8 @@ FAK_DEV uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// With m that of the exponents' maximum, less 7, weights reach 2^15 and keep f16's 11 bits down to 2^-14: 21 powers of two
+// below the largest, or where all values are tiny down to scales of 2^-101.  A weight is lost 32 below the largest.
 constexpr float kLeast = -80.0f;
 
 FAK_DEV float log2_approx(float x) {
@@ -322,11 +324,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         const float* f = reinterpret_cast<const float*>(from + x * gpart + C::part);
         kf[x][0] = f[kg];
         kf[x][1] = f[kg + 2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float y = log2_approx(f[16 + kg + 2 * h]);
-          vl[x][h] = y < kLeast ? kLeast : y;  // (NaN stays)
-        }
+        vl[x][0] = log2_approx(f[16 + kg]);
+        vl[x][1] = log2_approx(f[16 + kg + 2]);
       }
     }
   };
@@ -342,10 +341,11 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           if (scut && !sees(pos[nt][c & 1], sj + 16 * x + kg + 2 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
         }
     }
-    // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m the maximum of those exponents (so
-    // that weights fit f16 whatever the scales are); the weights' sum is of 2^(t - m)
+    // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m set by the largest of those
+    // exponents, so that weights fit f16 whatever the scales are; the weights' sum is of 2^(t - m).  Scales below
+    // 2^kLeast (zero too) count as that for m, or the sum could leave f32.
     auto heavy = [&](int x, int nt, int c) {
-      if constexpr (C::quant) return s[x][nt][c] + vl[x][c >> 1];
+      if constexpr (C::quant) return s[x][nt][c] + fmaxf(vl[x][c >> 1], kLeast);
       return s[x][nt][c];
     };
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           w[c] = exp2_approx(s[x][nt][c] - base[c & 1]);
           l[nt][c & 1] += w[c];
           if constexpr (C::quant) {
-            w[c] = exp2_approx(heavy(x, nt, c) - base[c & 1]);
+            w[c] = exp2_approx(s[x][nt][c] + vl[x][c >> 1] - base[c & 1]);
             // (the scale of a key that is not seen may be anything)
             if (scut && s[x][nt][c] == -INFINITY) w[c] = 0.0f;
           }

@@ -64,7 +64,7 @@ def fill(mem, kind, table, kv_len, page, K, V):
                 codes[pg, :, sl] = x.to(torch.bfloat16)
                 continue
             most = x.abs().amax(-1)
-            y = x * (TOP[kind] / most)[..., None]
+            y = x * torch.where(most > 0, TOP[kind] / most, 0.0)[..., None]  # (zeros are held as zeros)
             codes[pg, :, sl] = y.to(torch.float8_e4m3fn).view(torch.uint8) if kind == "e4m3" else y.round().to(torch.int8)
             scales[pg, :, sl] = most / TOP[kind]
 
