@@ -443,7 +443,9 @@ void fak_prefill_destroy(fak_prefill* ctx);
  *   FAK_KV_E4M3: a = max|x|, scale = a / 448, code = e4m3(x * (448 / a)).
  *   FAK_KV_I8:   scale = a / 127, code = rint(x * (127 / a)), int8.
  * In the 8-bit kinds a vector with a < 2^-100 is held as zeros, and one that
- * holds a NaN or an infinity reads back as NaN in every element.
+ * holds a NaN or an infinity reads back as NaN in every element (by its scale:
+ * codes are finite, and e4m3's NaN codes in a cache written otherwise count as
+ * NaN or as 480).
  * dh is 64, 128 or 256; page is 16, 32, 64, 128 or 256 tokens; n_pages * n_kv *
  * page < 2^31; codes and scales 16-byte aligned.  The memory is the caller's.
  */
@@ -479,7 +481,7 @@ typedef struct {
 /* The new rows' projections, f32 (as the GEMMs write them) or bf16: head h of
  * row r of x stands at x + r * x_row + h * x_head (elements), dh values next to
  * each other, so slices of a fused projection need no copy.  Vectors start on
- * 16-byte boundaries. */
+ * 16-byte boundaries; here and below the stride of a dimension of 1 is not looked at. */
 typedef struct {
     int32_t type;                    /* FAK_ROWS_F32 or FAK_ROWS_BF16 */
     int32_t nq, rot;                 /* query heads (0: none); rotary dims, 0 or a multiple of 16, <= dh */
@@ -518,8 +520,9 @@ int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch, int64_t ro
  *   out = sum_j w_j v_j / sum_j w_j * sigmoid(gate),  w_j = exp(scale * q . k_j),
  *   over positions j <= p, and if window > 0 only j > p - window or j < sinks.
  * Sequences may have one row (a decode step), a chunk, or a whole prompt, mixed in
- * one call.  Scores, maxima and sums are f32; w is rounded to bf16 for the product
- * with v (each weight off by at most 2^-8 of itself); out is rounded once.
+ * one call.  Scores, maxima and sums are f32; w (few rows over an 8-bit cache: w
+ * times v's scale, as f16) is rounded to bf16 for the product with v (each weight
+ * off by at most 2^-8 of itself); out is rounded once.
  * What stands at positions that a row does not see (NaN and infinities too) does
  * not reach it.  A padding row, which sees nothing, gets zeros; rows of no sequence
  * are left as they were.  Deterministic. */
@@ -530,7 +533,8 @@ typedef struct {
                                left out, recorded */
     float scale;            /* > 0 */
     int64_t rows;
-    const void* q;          /* device bf16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned */
+    const void* q;          /* device bf16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned, strides
+                               above 0, and below 2^40 bytes */
     int64_t q_row, q_head;
     const float* gate;      /* device f32, NULL: none; same form, 16-byte aligned */
     int64_t gate_row, gate_head;

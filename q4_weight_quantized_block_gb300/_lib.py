@@ -292,11 +292,20 @@ class KVBatch:
         self.ref = ctypes.addressof(self.desc)
 
 
-def _heads(t, heads, dh, size, where):
+def _float_types():
+    """torch's float32 and bfloat16 (this module does without torch until a call brings tensors)."""
+    global _float_types
+    import torch
+    types = torch.float32, torch.bfloat16
+    _float_types = lambda: types
+    return types
+
+
+def _heads(t, heads, dh, dtype, where):
     """Pointer, row stride and head stride of rows [rows, heads, dh] with neighbouring values in a head."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
         raise FakError(2, where)
-    if t.element_size() != size or t.stride(2) != 1:
+    if t.dtype != dtype or t.stride(2) != 1:
         raise FakError(1, where)
     return t.data_ptr(), t.stride(0), t.stride(1)
 
@@ -311,16 +320,17 @@ def fak_rope_table(rot, theta):
 def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_w=None, eps=1e-6, rope=None, rot=0,
                   stream=None):
     """k, v [rows, n_kv, dh] and q [rows, nq, dh], f32 or bf16 (views with strides are fine); q_out bf16."""
-    size = k.element_size()
-    if size not in (2, 4) or (q is not None and (q_out is None or not q_out.is_contiguous())):
+    dtype, (f32, bf16) = k.dtype, _float_types()
+    if (dtype != f32 and dtype != bf16) or (q is not None and (
+            q_out is None or q_out.dtype != bf16 or not q_out.is_contiguous())):
         raise FakError(1, "fak_kv_append")
     if v.shape[0] != k.shape[0] or (q is not None and (q.shape[0] != k.shape[0] or q_out.shape != q.shape)):
         raise FakError(2, "fak_kv_append")
-    kp, kr, kh = _heads(k, cache.n_kv, cache.dh, size, "fak_kv_append")
-    vp, vr, vh = _heads(v, cache.n_kv, cache.dh, size, "fak_kv_append")
+    kp, kr, kh = _heads(k, cache.n_kv, cache.dh, dtype, "fak_kv_append")
+    vp, vr, vh = _heads(v, cache.n_kv, cache.dh, dtype, "fak_kv_append")
     nq = 0 if q is None else q.shape[1]
-    qp, qr, qh = (None, 0, 0) if q is None else _heads(q, nq, cache.dh, size, "fak_kv_append")
-    r = KvRows(FAK_ROWS_F32 if size == 4 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
+    qp, qr, qh = (None, 0, 0) if q is None else _heads(q, nq, cache.dh, dtype, "fak_kv_append")
+    r = KvRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
                vh, _ptr(q_norm_w), _ptr(k_norm_w), _ptr(rope), _ptr(q_out))
     _check(lib.fak_kv_append(cache.ref, batch.ref, ctypes.addressof(r), _stream(stream)), "fak_kv_append")
 
@@ -328,7 +338,7 @@ def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_
 def fak_kv_read(cache, batch, k_out, v_out, stream=None):
     """k_out, v_out [rows, n_kv, dh] contiguous, both f32 or both bf16; either may be None."""
     outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs or any(not t.is_contiguous() or t.element_size() not in (2, 4) for t in outs) or (
+    if not outs or any(not t.is_contiguous() or t.dtype not in _float_types() for t in outs) or (
             outs[0].dtype != outs[-1].dtype):
         raise FakError(1, "fak_kv_read")
     if any(t.dim() != 3 or t.shape[1:] != (cache.n_kv, cache.dh) or t.shape[0] != outs[0].shape[0] for t in outs):
@@ -346,12 +356,12 @@ def fak_paged_attn_workspace_bytes(cache, batch, nq, rows, max_q, max_kv, window
 def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, sinks=0, gate=None, workspace=None,
                    stream=None):
     """q, out [rows, nq, dh] bf16 and gate f32 (views with strides are fine); scale defaults to dh^-1/2."""
-    nq = q.shape[1]
+    nq, (f32, bf16) = q.shape[1], _float_types()
     if out.shape != q.shape or (gate is not None and gate.shape != q.shape):
         raise FakError(2, "fak_paged_attn")
-    qp, qr, qh = _heads(q, nq, cache.dh, 2, "fak_paged_attn")
-    op, orow, oh = _heads(out, nq, cache.dh, 2, "fak_paged_attn")
-    gp, gr, gh = (None, 0, 0) if gate is None else _heads(gate, nq, cache.dh, 4, "fak_paged_attn")
+    qp, qr, qh = _heads(q, nq, cache.dh, bf16, "fak_paged_attn")
+    op, orow, oh = _heads(out, nq, cache.dh, bf16, "fak_paged_attn")
+    gp, gr, gh = (None, 0, 0) if gate is None else _heads(gate, nq, cache.dh, f32, "fak_paged_attn")
     a = AttnArgs(nq, window, sinks, max_q, max_kv, cache.dh ** -0.5 if scale is None else scale, q.shape[0], qp, qr, qh,
                  gp, gr, gh, op, orow, oh, _ptr(workspace),
                  0 if workspace is None else workspace.numel() * workspace.element_size())

@@ -179,7 +179,7 @@ cudaError_t launch_join(const AttnParams& p, cudaStream_t s) {
 int attn_shape(const fak_kv_cache* c, const fak_attn_args* a) {
   if (a->window < 0 || a->sinks < 0 || !(a->scale > 0.0f) || !std::isfinite(a->scale)) return FAK_ERR_INVALID_ARG;
   if (a->nq < 1 || a->nq % c->n_kv || a->nq / c->n_kv > 128 || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
-      a->max_kv < 0 || a->max_q > 1 << 28 || a->max_kv > 1 << 29 || a->nq > 65535)
+      a->max_kv < 0 || a->max_q > 1 << 28 || a->max_kv > 1 << 29 || a->nq > 65535 || a->rows * a->nq > 1LL << 40)
     return FAK_ERR_SHAPE;
   return FAK_OK;
 }
@@ -201,8 +201,18 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   if (st != FAK_OK) return st;
   if (!a || !a->q || !a->out) return FAK_ERR_INVALID_ARG;
   if ((st = attn_shape(cache, a)) != FAK_OK) return st;
+  p.q_row = kv_stride(a->q_row, a->rows);
+  p.q_head = kv_stride(a->q_head, a->nq);
+  p.out_row = kv_stride(a->out_row, a->rows);
+  p.out_head = kv_stride(a->out_head, a->nq);
+  p.gate_row = a->gate ? kv_stride(a->gate_row, a->rows) : 0;
+  p.gate_head = a->gate ? kv_stride(a->gate_head, a->nq) : 0;
+  // (a tensor map's strides are above zero and below 2^40 bytes)
+  constexpr int64_t least = 1, most = 1LL << 38;
+  if ((a->rows > 1 && (p.q_row < least || p.q_row > most)) || (a->nq > 1 && (p.q_head < least || p.q_head > most)))
+    return FAK_ERR_SHAPE;
   if ((((uintptr_t)a->q | (uintptr_t)a->out | (uintptr_t)a->gate) & 15) ||
-      ((a->q_row | a->q_head | a->out_row | a->out_head) & 7) || (a->gate && ((a->gate_row | a->gate_head) & 3)) ||
+      ((p.q_row | p.q_head | p.out_row | p.out_head) & 7) || ((p.gate_row | p.gate_head) & 3) ||
       ((uintptr_t)a->workspace & 255))
     return FAK_ERR_ALIGN;
   const Plan pl = make_plan(cache, batch, a);
@@ -227,12 +237,6 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.gate = a->gate;
   p.out = static_cast<__nv_bfloat16*>(a->out);
-  p.q_row = a->q_row;
-  p.q_head = a->q_head;
-  p.gate_row = a->gate_row;
-  p.gate_head = a->gate_head;
-  p.out_row = a->out_row;
-  p.out_head = a->out_head;
   p.scale = a->scale * 1.4426950408889634f;
   p.nq = a->nq;
   p.group = a->nq / cache->n_kv;
@@ -246,7 +250,8 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.per_split = pl.per_split;
   p.part = static_cast<float*>(a->workspace);
   p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + parts);
-  p.timeout_ns = 2000000000ull;
+  // (a wait may be for a whole block: 2 s, and 20 us for each of its tiles)
+  p.timeout_ns = 2000000000ull + 20000ull * (unsigned)pl.per_split;
   cudaStream_t s = (cudaStream_t)stream;
   e = pl.few ? attn_rows_launch(cache->kind, cache->dh, p, st_word, dev, s)
              : attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p,

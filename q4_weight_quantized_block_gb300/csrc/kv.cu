@@ -387,7 +387,13 @@ extern "C" int fak_kv_append(const fak_kv_cache* cache, const fak_kv_batch* batc
   if (!(r->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
   // vectors on 16-byte boundaries: 4 f32 or 8 bf16 elements
   const int64_t m = r->type == FAK_ROWS_F32 ? 3 : 7;
-  const int64_t strides = r->k_row | r->k_head | r->v_row | r->v_head | (r->nq ? r->q_row | r->q_head : 0);
+  p.q_row = kv_stride(r->q_row, r->rows);
+  p.q_head = kv_stride(r->q_head, r->nq);
+  p.k_row = kv_stride(r->k_row, r->rows);
+  p.k_head = kv_stride(r->k_head, cache->n_kv);
+  p.v_row = kv_stride(r->v_row, r->rows);
+  p.v_head = kv_stride(r->v_head, cache->n_kv);
+  const int64_t strides = p.k_row | p.k_head | p.v_row | p.v_head | (r->nq ? p.q_row | p.q_head : 0);
   const uintptr_t bits = (uintptr_t)r->k | (uintptr_t)r->v | (uintptr_t)r->q_norm_w | (uintptr_t)r->k_norm_w |
                          (r->nq ? (uintptr_t)r->q | (uintptr_t)r->q_out : 0);
   if ((strides & m) || (bits & 15) || ((uintptr_t)r->rope & 7)) return FAK_ERR_ALIGN;
@@ -398,12 +404,6 @@ extern "C" int fak_kv_append(const fak_kv_cache* cache, const fak_kv_batch* batc
   p.q = r->q;
   p.k = r->k;
   p.v = r->v;
-  p.q_row = r->q_row;
-  p.q_head = r->q_head;
-  p.k_row = r->k_row;
-  p.k_head = r->k_head;
-  p.v_row = r->v_row;
-  p.v_head = r->v_head;
   p.qw = r->q_norm_w;
   p.kw = r->k_norm_w;
   p.rope = r->rope;

@@ -81,6 +81,9 @@ FAK_DEV int64_t kv_place(const KvView& c, int s, int pos, int head) {
   return (((int64_t)pg * c.n_kv + head) << c.page_shift) + slot;
 }
 
+// Host side: the stride of a dimension of n; one that is never taken may be anything.
+static inline int64_t kv_stride(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
+
 // Host side: checks of the cache and the batch; fills the view.
 static inline int kv_view(const fak_kv_cache* c, const fak_kv_batch* b, KvView* w) {
   if (!c || !b) return FAK_ERR_INVALID_ARG;

@@ -161,3 +161,50 @@ def test_binding_refuses_wrong_tensors(fak):
     for a, o in ((None, None), (x, x[:4]), (x, x.to(torch.bfloat16)), (x.transpose(0, 1), None)):
         with pytest.raises(fak.FakError):
             fak.fak_kv_read(cache, batch, a, o, stream=0)
+
+
+@pytest.mark.parametrize("field,value", [("q_row", 0), ("q_row", -6144), ("q_head", 0), ("q_head", -256),
+                                         ("q_row", (1 << 38) + 8), ("q_head", 1 << 40)])
+def test_query_strides_are_positive(fak, field, value):
+    c, b, r, a = structs()
+    setattr(a, field, value)
+    assert calls(fak)["attn"](c, b, r, a) == 2
+
+
+def test_strides_that_are_never_taken(fak):
+    c, b, r, a = structs()
+    b.n_seqs = 0  # (nothing to do: no device call)
+    r.rows = a.rows = 1
+    for x, names in ((r, ("q_row", "k_row", "v_row")), (a, ("q_row", "gate_row", "out_row"))):
+        for name in names:
+            setattr(x, name, -3)
+    assert calls(fak)["append"](c, b, r, a) == 0 and calls(fak)["attn"](c, b, r, a) == 0
+    r.rows = a.rows = 2
+    assert calls(fak)["append"](c, b, r, a) == 3 and calls(fak)["attn"](c, b, r, a) == 2
+
+
+def test_more_queries_than_memory_holds(fak):
+    c, b, r, a = structs()
+    a.nq, a.rows = 65532, (1 << 31) - 1
+    c.n_kv = 65532
+    assert calls(fak)["attn"](c, b, r, a) == 2
+    assert fak.lib.fak_paged_attn_workspace_bytes(ref(c), ref(b), ref(a)) == 0
+
+
+def test_binding_refuses_other_float_types(fak):
+    torch = pytest.importorskip("torch")
+    u8, sc = torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2, 16)
+    cache = fak.KVCache(fak.FAK_KV_I8, u8, u8, sc, sc)
+    batch = fak.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                        torch.zeros(2, dtype=torch.int32))
+    x, q = torch.zeros(5, 2, 64), torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    for call in (lambda: fak.fak_kv_append(cache, batch, x.half(), x.half(), stream=0),
+                 lambda: fak.fak_kv_append(cache, batch, x, x, q=torch.zeros(5, 4, 64), q_out=q.half(), stream=0),
+                 lambda: fak.fak_kv_append(cache, batch, x.int(), x.int(), stream=0),
+                 lambda: fak.fak_paged_attn(cache, batch, q.half(), q, 1, 1, stream=0),
+                 lambda: fak.fak_paged_attn(cache, batch, q, q.half(), 1, 1, stream=0),
+                 lambda: fak.fak_paged_attn(cache, batch, q, q, 1, 1, gate=torch.zeros(5, 4, 64, dtype=torch.int32), stream=0),
+                 lambda: fak.fak_kv_read(cache, batch, x.half(), None, stream=0)):
+        with pytest.raises(fak.FakError) as e:
+            call()
+        assert e.value.status == 1

@@ -288,3 +288,39 @@ def test_captured_once_replayed_with_other_lengths(fak):
         s2.out.fill_(9.0)
         g2.replay()
         s2.check(lengths)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dh,new", [(64, 1), (128, 1), (256, 1), (256, 2), (128, 70)])
+def test_values_of_any_size(fak, kind, dh, new):
+    """Zeros first, which count in the sum alone; all tiny; sizes from 1e-18 to 1e18 beside each other."""
+    def edit(K, V):
+        V[0][:600] = 0.0
+        V[1].mul_(1e-25)
+        size = torch.rand(V[2].shape[0], 1, 1, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+        V[2].mul_(10.0 ** (36.0 * size - 18.0))
+
+    case(fak, kind, 8, 2, dh, 32, [(new, 900), (new, 700), (new, 800)], seed=dh + new, edit=edit)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sharp", [1e-38, 1e-20, 12.0])
+def test_queries_of_any_size(fak, kind, sharp):
+    case(fak, kind, 24, 4, 256, 64, [(1, 300), (2, 77)], seed=5, sharp=sharp)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_pieces_of_many_rows(fak, kind):
+    case(fak, kind, 24, 4, 256, 64, [(64, 8255)], seed=6, gate=True)
+
+
+@pytest.mark.parametrize("kind,max_q", [("bf16", 1), ("i8", 40)])
+def test_strides_that_are_never_taken(fak, kind, max_q):
+    s = Setup(fak, kind, 4, 4, 128, 16, [(1, 90)], seed=8)
+    s.max_q = max_q
+    s.q, s.out = s.q.as_strided((1, 4, 128), (1, s.q.stride(1), 1)), s.out.as_strided((1, 4, 128), (3, 128, 1))
+    s.run()
+    torch.cuda.synchronize()
+    assert fak.fak_device_status() == 0
+    for r, o, tol in s.want():
+        _kv.check(s.out[r], o, tol, "one row")
