@@ -442,6 +442,7 @@ void fak_prefill_destroy(fak_prefill* ctx);
  *   FAK_KV_BF16: codes are the vector rounded to bf16; no scales (NULL).
  *   FAK_KV_E4M3: a = max|x|, scale = a / 448, code = e4m3(x * (448 / a)).
  *   FAK_KV_I8:   scale = a / 127, code = rint(x * (127 / a)), int8.
+ * (448 / a and 127 / a are taken as 448 * (1 / a) and 127 * (1 / a) in f32.)
  * In the 8-bit kinds a vector with a < 2^-100 is held as zeros, and one that
  * holds a NaN or an infinity reads back as NaN in every element (by its scale:
  * codes are finite, and e4m3's NaN codes in a cache written otherwise count as

@@ -303,11 +303,12 @@ def _float_types():
 
 def _heads(t, heads, dh, dtype, where):
     """Pointer, row stride and head stride of rows [rows, heads, dh] with neighbouring values in a head."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dh:
         raise FakError(2, where)
-    if t.dtype != dtype or t.stride(2) != 1:
+    if t.dtype != dtype or stride[2] != 1:
         raise FakError(1, where)
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), stride[0], stride[1]
 
 
 def fak_rope_table(rot, theta):

@@ -1,15 +1,31 @@
 // Attention of few rows over the paged KV cache: decode steps, where a sequence and KV head has at most 16 rows
 // (token, query head of the group) and all that counts is reading K and V once, at the memory's rate.
 //
-// A warp takes 16 keys at a time, in the layouts of the m16n8k16 matrix instruction without any turning, with the keys and dims as its 16 and the rows as its 8 (6 rows of a group of 6 waste 2, not 10):
-//   S^T = K Q^T      A = K: lane (g, t) loads 16 bytes of keys g and g + 8, which are its dims of two (8-bit codes:
-//                    four) instructions; the dims come in another order than they stand, the same for Q
-//   O^T += V^T P^T   A = V^T: lane (g, t) loads 16 bytes of keys 2t, 2t + 1, 2t + 8 and 2t + 9 and pairs up
-//                    neighbouring keys' values; P^T from S^T by an 8 x 8 transpose within the warp
-// The bytes a lane will need come by asynchronous copies into shared memory slots of its own, which nothing but the lane
-// reads: no barrier, no bank conflict, and 8 or 12 warps keep up to 200 KB on their way on an SM.  Four warps share a block's keys in tiles of 64 and add their sums at the end; a sequence's keys
-// are cut over blocks, which the join kernel adds.
+// A warp takes 16 keys at a time, in the layouts of the m16n8k16 matrix instruction without any turning, with the keys
+// and dims as its 16 and the rows as its 8 (6 rows of a group of 6 waste 2, not 10):
+//   S^T = K Q^T      A = K: lane (g, t) loads 16 bytes of two keys, which are its dims of two (8-bit codes: four)
+//                    instructions; the dims come in another order than they stand, the same for Q
+//   O^T += V^T P^T   A = V^T: lane (g, t) loads 16 bytes of four keys and pairs up neighbouring keys' values; P^T from
+//                    S^T by an 8 x 8 transpose within the warp
+// Few rows leave the tensor cores idle whatever instruction is used, so the plain one does.
+//
+// K and V of 16 keys are consecutive in a page: they come by bulk copies into slots of the warp's own, each with a
+// barrier of its own, two to four steps ahead.  (As asynchronous copies of 16 bytes by each lane the loads alone reached
+// 4.9 TB/s, as bulk copies 6.6: 64 sequences of up to 8,191 bf16 keys of 256 took 258 us, then 212, and without bank
+// conflicts 202.)  Four warps share a block's keys in tiles of 64 or 128 and add their sums at the end; a sequence's
+// keys are cut over blocks, which the join kernel adds.  The product of a step runs beside the scores of the next,
+// which do not depend on it.
+//
+// 8-bit codes are multiplied as f16, which holds both kinds exactly and takes one conversion for two e4m3 codes (as bf16
+// they took twice as many instructions: 131,071 int8 keys of 128, 78 us, then 64).  Q goes in as f16 too, each row
+// scaled by a power of two; weights are 2^(score + log2 of the value's scale), under a maximum of those exponents.
+//
+// Bound: bf16 by memory, 64 x 8,191 keys in 202 us, 6.1 TB/s (the copies alone 189); 8-bit by the instructions of the
+// conversion, the same in e4m3 130 us, 4.9 TB/s (the copies alone 104); few keys by the launches and one block's chain
+// of loads.
 // Each row's maximum moves only when passed by 8, as in the blocks' kernel (attn_tile.cu).
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -19,6 +35,7 @@
 #include "attn_device.cuh"
 #include "fak.h"
 #include "fak_device.cuh"
+#include "fak_tc.cuh"
 
 namespace {
 
@@ -86,8 +103,8 @@ FAK_DEV uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// With m that of the exponents' maximum, less 7, weights reach 2^15 and keep f16's 11 bits down to 2^-14: 21 powers of two
-// below the largest, or where all values are tiny down to scales of 2^-101.  A weight is lost 32 below the largest.
+// With m the exponents' maximum less 7, weights reach 2^15 and keep f16's 11 bits down to 2^-14: 21 powers of two below
+// the largest, and where all values are tiny down to scales of 2^-101.  A weight is lost 32 powers below the largest.
 constexpr float kLeast = -80.0f;
 
 FAK_DEV float log2_approx(float x) {
@@ -102,14 +119,6 @@ FAK_DEV uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Bulk copy of consecutive bytes into shared memory, counted on an mbarrier; addresses and bytes multiples of 16.
-FAK_DEV void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 FAK_DEV int key_of(int i) { return ((i >> 1) ^ (i & 1) << 1) * 4 + (i & 1); }
 
 template <int DH, int KIND, int NT>
@@ -122,13 +131,12 @@ struct RCfg {
   static constexpr int vb = DH / (8 * ve);                     // V loads of a key and lane
   static constexpr int vw = ve * bytes / 4;                    // words of one
   static constexpr int groups = quant && DH <= 128 ? 2 : 1;  // 16 keys each, of a step
-  // a lane's slots: halves of a step in turn, K and V
   // 16 keys come in four copies, 32 bytes apart in the banks, and index i of the instructions' 8 (and i + 8) is key
   // key_of(i) (and that + 2): what 8 lanes load at once, two neighbouring indices' 64 bytes of K or four's 32 bytes of
   // V (every other index), then lies in different banks
   static constexpr int row_bytes = DH * bytes, four = 4 * row_bytes + 32, part = 4 * four;
   static constexpr int half = groups * (part + (quant ? 128 : 0));     // of a half (with a group's scales)
-  // blocks of four warps on an SM, as many halves as then have room
+  // blocks of four warps on an SM; a warp's slots, halves of a step in turn, K and V, as many as then have room
   static constexpr int blocks = rows_blocks(quant, DH, 8 * NT);
   static constexpr int room = (233472 / blocks - 1536) / kWarps;
   static constexpr int halves = room / half < 8 ? room / half : 8;
@@ -210,10 +218,10 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         uint8_t* const to = slots + slot * C::half + x * gpart;
         const uint8_t* const src = (value ? p.c.v : p.c.k) + fat[x] * C::row_bytes;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) copy_bulk(to + c * C::four, src + c * 4 * C::row_bytes, 4 * C::row_bytes, bar);
+        for (int c = 0; c < 4; ++c) bulk_g2s_nohint(to + c * C::four, src + c * 4 * C::row_bytes, 4 * C::row_bytes, bar);
         if (C::quant && !value) {
-          copy_bulk(to + C::part, p.c.ks + fat[x], 64, bar);
-          copy_bulk(to + C::part + 64, p.c.vs + fat[x], 64, bar);
+          bulk_g2s_nohint(to + C::part, p.c.ks + fat[x], 64, bar);
+          bulk_g2s_nohint(to + C::part + 64, p.c.vs + fat[x], 64, bar);
         }
       }
     }
@@ -338,7 +346,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           s[x][nt][c] *= C::quant ? kf[x][c >> 1] * qf[nt][c & 1] : qf[nt][c & 1];
-          if (scut && !sees(pos[nt][c & 1], sj + 16 * x + kg + 2 * (c >> 1), p.window, p.sinks)) s[x][nt][c] = -INFINITY;
+          if (scut && !sees(pos[nt][c & 1], sj + 16 * x + kg + 2 * (c >> 1), p.window, p.sinks))
+            s[x][nt][c] = -INFINITY;
         }
     }
     // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m set by the largest of those
@@ -406,7 +415,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         uint32_t vx[4][C::vw];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint8_t* const at = from + x * gpart + vrow[k & 1] + (k >> 1) * 2 * C::row_bytes + (b * 8 + g) * C::vw * 4;
+          const uint8_t* const at =
+              from + x * gpart + vrow[k & 1] + (k >> 1) * 2 * C::row_bytes + (b * 8 + g) * C::vw * 4;
           if constexpr (C::vw == 4) {
             const uint4 y = *reinterpret_cast<const uint4*>(at);
             vx[k][0] = y.x;
@@ -466,7 +476,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
             const int d = b * (C::ve / 2) + w * (C::quant ? 2 : 1) + h;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816<C::quant>(o[nt][d], y[2 * h][0], y[2 * h + 1][0], y[2 * h][1], y[2 * h + 1][1], pb[x][nt][0], pb[x][nt][1]);
+              mma16816<C::quant>(o[nt][d], y[2 * h][0], y[2 * h + 1][0], y[2 * h][1], y[2 * h + 1][1],
+                                 pb[x][nt][0], pb[x][nt][1]);
           }
         }
       }

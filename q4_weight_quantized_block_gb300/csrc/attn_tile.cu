@@ -32,6 +32,11 @@
 // mended in shared memory: keys past the last row's position are made zeros, and so are values that are not
 // finite, which the rows that do see them get added at the end.  (Codes are always finite, and a weight of zero is not
 // multiplied by a scale.)  Scores of masked keys are replaced, whatever they are.
+//
+// A prompt of 8,192 tokens, 24 query and 4 KV heads of 256, in bf16: 594 us, 1.39 PFLOP/s, under the power limit's
+// clocks (526 us, 1.57, from a rest); 512 tokens after 7,680 keys 100 us.  Heads of 128 are bound by the softmax warps,
+// whose phases (scores, maximum, exponents) follow one another; 8-bit codes by those warps' scales and the conversion
+// beside them: 8 x 1,024 tokens after 4,001 keys in bf16 613 us, in e4m3 931, with no unit above 45% busy.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

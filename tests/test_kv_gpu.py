@@ -233,3 +233,22 @@ def test_offsets_past_32_bits(fak):
     want, tol = _kv.attention(q, x.double(), y.double(), 0, dh**-0.5)
     _kv.check(out, want, tol, "attention over far pages")
     assert math.isfinite(float(out.float().sum()))
+
+
+def test_int8_codes_bit_for_bit(fak):
+    """No norm, no RoPE: rint(x * (127 * (1 / a))) in f32, to the last code."""
+    lengths = [(700, 700), (300, 333)]
+    table, start, kv_len, rows, n_pages = _kv.batch_tensors(lengths, 64, seed=4)
+    cache, mem = _kv.empty_cache(fak, "i8", n_pages, 4, 64, 256)
+    k, v = randn(41, rows, 4, 256), randn(42, rows, 4, 256) * 1e-3
+    fak.fak_kv_append(cache, fak.KVBatch(table, start, kv_len), k, v)
+    assert fak.fak_device_status() == 0
+    t, row = table.cpu(), 0
+    for s, (n, total) in enumerate(lengths):
+        pos = torch.arange(total - n, total)
+        pages, slots = t[s, pos // 64].long().cuda(), (pos % 64).cuda()
+        for codes, x in ((mem[0], k), (mem[1], v)):
+            x = x[row:row + n]
+            inv = torch.ones_like(x[..., 0]).div(x.abs().amax(-1)).mul(127.0)
+            assert torch.equal(codes[pages, :, slots], (x * inv[..., None]).round().to(torch.int8))
+        row += n
