@@ -10,7 +10,7 @@
 // Few rows leave the tensor cores idle whatever instruction is used, so the plain one does.
 //
 // K and V of 16 keys are consecutive in a page: they come by bulk copies into slots of the warp's own, each with a
-// barrier of its own, two to four steps ahead.  (As asynchronous copies of 16 bytes by each lane the loads alone reached
+// barrier of its own, one to four steps ahead.  (As asynchronous copies of 16 bytes by each lane the loads alone reached
 // 4.9 TB/s, as bulk copies 6.6: 64 sequences of up to 8,191 bf16 keys of 256 took 258 us, then 212, and without bank
 // conflicts 202.)  Four warps share a block's keys in tiles of 64 or 128 and add their sums at the end; a sequence's
 // keys are cut over blocks, which the join kernel adds.  The product of a step runs beside the scores of the next,
