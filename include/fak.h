@@ -446,7 +446,7 @@ void fak_prefill_destroy(fak_prefill* ctx);
  * In the 8-bit kinds a vector with a < 2^-100 is held as zeros, and one that
  * holds a NaN or an infinity reads back as NaN in every element (by its scale:
  * codes are finite, and e4m3's NaN codes in a cache written otherwise count as
- * NaN or as 480).
+ * NaN or as 480 where they are seen).
  * dh is 64, 128 or 256; page is 16, 32, 64, 128 or 256 tokens; n_pages * n_kv *
  * page < 2^31; codes and scales 16-byte aligned.  The memory is the caller's.
  */

@@ -324,3 +324,26 @@ def test_strides_that_are_never_taken(fak, kind, max_q):
     assert fak.fak_device_status() == 0
     for r, o, tol in s.want():
         _kv.check(s.out[r], o, tol, "one row")
+
+
+
+@pytest.mark.parametrize("code", [0x7F, 0xFF])
+@pytest.mark.parametrize("nq,n_kv,dh", [(6, 1, 256), (4, 2, 256), (6, 3, 128), (8, 1, 128), (4, 1, 64), (8, 1, 64)])
+@pytest.mark.parametrize("new,total,at,window,blind", [
+    (2, 100, 99, 0, [0]),  # the last token's own key
+    (2, 200, 149, 50, [1]),  # the first token's window still holds it, the second's does not
+    (2, 2000, 1999, 0, [0]),  # in the last piece of many
+    (2, 128, 5, 30, [0, 1]),  # in nobody's window
+])
+def test_nan_codes_reach_only_the_rows_that_see_them(fak, code, nq, n_kv, dh, new, total, at, window, blind):
+    s = Setup(fak, "e4m3", nq, n_kv, dh, 16, [(new, total)], seed=at, window=window)
+    page, slot = int(s.table[0, at // 16]), at % 16
+    for d in (5, dh - 2):
+        s.mem[1][page, 0, slot, d] = code
+    s.run()
+    torch.cuda.synchronize()
+    assert fak.fak_device_status() == 0
+    (_, o, tol), = s.want()
+    others = [d for d in range(dh) if d not in (5, dh - 2)]
+    _kv.check(s.out[blind], o[blind], tol[blind], "rows that do not see it")
+    _kv.check(s.out[..., others], o[..., others], tol[..., others], "the other elements")
