@@ -521,9 +521,10 @@ int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch, int64_t ro
  *   out = sum_j w_j v_j / sum_j w_j * sigmoid(gate),  w_j = exp(scale * q . k_j),
  *   over positions j <= p, and if window > 0 only j > p - window or j < sinks.
  * Sequences may have one row (a decode step), a chunk, or a whole prompt, mixed in
- * one call.  Scores, maxima and sums are f32; w (few rows over an 8-bit cache: w
- * times v's scale, as f16) is rounded to bf16 for the product with v (each weight
- * off by at most 2^-8 of itself); out is rounded once.
+ * one call.  Scores, maxima and sums are f32.  For the product with v, w (8-bit: w
+ * times v's scale) is rounded to bf16, off by at most 2^-8 of itself; over an 8-bit
+ * cache with max_q * nq / n_kv <= 16 to f16, off by at most 2^-11 of itself or 2^-32
+ * of the row's largest, whichever is more.  out is rounded once.
  * What stands at positions that a row does not see (NaN and infinities too) does
  * not reach it.  A padding row, which sees nothing, gets zeros; rows of no sequence
  * are left as they were.  Deterministic. */

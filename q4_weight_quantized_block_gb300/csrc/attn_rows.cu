@@ -18,7 +18,8 @@
 //
 // 8-bit codes are multiplied as f16, which holds both kinds exactly and takes one conversion for two e4m3 codes (as bf16
 // they took twice as many instructions: 131,071 int8 keys of 128, 78 us, then 64).  Q goes in as f16 too, each row
-// scaled by a power of two; weights are 2^(score + log2 of the value's scale), under a maximum of those exponents.
+// scaled by a power of two; weights are 2^(score + log2 of the value's scale), under a maximum of those exponents.  Their
+// sum, which the values have no part in, has a base of its own in each lane.
 //
 // Bound: bf16 by memory, 64 x 8,191 keys in 202 us, 6.1 TB/s (the copies alone 189); 8-bit by the instructions of the
 // conversion, the same in e4m3 130 us, 4.9 TB/s (the copies alone 104); few keys by the launches and one block's chain
@@ -103,9 +104,8 @@ FAK_DEV uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// With m the exponents' maximum less 7, weights reach 2^15 and keep f16's 11 bits down to 2^-14: 21 powers of two below
-// the largest, and where all values are tiny down to scales of 2^-101.  A weight is lost 32 powers below the largest.
-constexpr float kLeast = -80.0f;
+// With m the exponents' maximum less 7, the largest weight (times its value's scale) is 2^7 to 2^15: f16 keeps 11 bits of
+// those down to 2^-14, and half a step of 2^-24 below, 2^-32 of the largest.
 
 FAK_DEV float log2_approx(float x) {
   float y;
@@ -120,6 +120,9 @@ FAK_DEV uint32_t transpose8(uint32_t x) {
 }
 
 FAK_DEV int key_of(int i) { return ((i >> 1) ^ (i & 1) << 1) * 4 + (i & 1); }
+
+// A row's base before any score.  (Minus infinity would need a look at each exponent: minus infinity less itself is NaN.)
+constexpr float kNone = -3.402823466e38f;
 
 template <int DH, int KIND, int NT>
 struct RCfg {
@@ -138,7 +141,7 @@ struct RCfg {
   static constexpr int half = groups * (part + (quant ? 128 : 0));     // of a half (with a group's scales)
   // blocks of four warps on an SM; a warp's slots, halves of a step in turn, K and V, as many as then have room
   static constexpr int blocks = rows_blocks(quant, DH, 8 * NT);
-  static constexpr int room = (233472 / blocks - 1536) / kWarps;
+  static constexpr int room = (233472 / blocks - 1792) / kWarps;
   static constexpr int halves = room / half < 8 ? room / half : 8;
   static constexpr float above = quant ? 7.0f : 0.0f, reach = above + 8.0f;
   static constexpr int row = DH + 8;  // floats of a row where the warps' sums meet
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   using C = RCfg<DH, KIND, NT>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem);  // at the end: [warp][8 NT rows][C::row]
-  __shared__ float sm[kWarps][8 * NT], sl[kWarps][8 * NT];
+  __shared__ float sm[kWarps][8 * NT], sl[kWarps][8 * NT], sb[kWarps][8 * NT];  // bases of O, the weights' sums, theirs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int seq = blockIdx.x, kvh = blockIdx.y;
   // (the join kernel may be scheduled from here on; it waits for this grid's end itself)
@@ -280,12 +283,12 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     }
   }
   float o[NT][DH / 16][4] = {};
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2], lm[NT][2];  // lm: 8-bit, the base of l, this lane's own (8 above the score that set it)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m[nt][c] = -INFINITY;
+      m[nt][c] = lm[nt][c] = kNone;
       l[nt][c] = 0.0f;
     }
 
@@ -351,19 +354,23 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         }
     }
     // 8-bit: a value's scale is part of its weight, 2^(t + log2 scale - m), with m set by the largest of those
-    // exponents, so that weights fit f16 whatever the scales are; the weights' sum is of 2^(t - m).  Scales below
-    // 2^kLeast (zero too) count as that for m, or the sum could leave f32.
+    // exponents, so that weights fit f16 whatever the scales are.  The sum is of 2^(t - lm): with m as its base it would
+    // lose what came before a value 2^126 times as large, zeros too.
     auto heavy = [&](int x, int nt, int c) {
-      if constexpr (C::quant) return s[x][nt][c] + fmaxf(vl[x][c >> 1], kLeast);
+      if constexpr (C::quant) return s[x][nt][c] + vl[x][c >> 1];
       return s[x][nt][c];
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top[2];
+      float top[2], own[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         top[c] = fmaxf(heavy(0, nt, c), heavy(0, nt, c + 2));
         if constexpr (G == 2) top[c] = fmaxf(top[c], fmaxf(heavy(G - 1, nt, c), heavy(G - 1, nt, c + 2)));
+        if constexpr (C::quant) {
+          own[c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+          if constexpr (G == 2) own[c] = fmaxf(own[c], fmaxf(s[G - 1][nt][c], s[G - 1][nt][c + 2]));
+        }
       }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
@@ -371,13 +378,22 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
       }
       const bool up0 = top[0] > m[nt][0] + C::reach, up1 = top[1] > m[nt][1] + C::reach;
-      if (__any_sync(0xffffffffu, up0 || up1)) {
+      const bool on0 = C::quant && own[0] > lm[nt][0], on1 = C::quant && own[1] > lm[nt][1];
+      if (__any_sync(0xffffffffu, up0 || up1 || on0 || on1)) {
         const float n0 = up0 ? top[0] - C::above : m[nt][0], n1 = up1 ? top[1] - C::above : m[nt][1];
         const float f0 = up0 ? exp2_approx(m[nt][0] - n0) : 1.0f, f1 = up1 ? exp2_approx(m[nt][1] - n1) : 1.0f;
         m[nt][0] = n0;
         m[nt][1] = n1;
-        l[nt][0] *= f0;
-        l[nt][1] *= f1;
+        if constexpr (C::quant) {
+          const float l0 = on0 ? own[0] + 8.0f : lm[nt][0], l1 = on1 ? own[1] + 8.0f : lm[nt][1];
+          if (on0) l[nt][0] *= exp2_approx(lm[nt][0] - l0);
+          if (on1) l[nt][1] *= exp2_approx(lm[nt][1] - l1);
+          lm[nt][0] = l0;
+          lm[nt][1] = l1;
+        } else {
+          l[nt][0] *= f0;
+          l[nt][1] *= f1;
+        }
 #pragma unroll
         for (int d = 0; d < DH / 16; ++d) {
           o[nt][d][0] *= f0;
@@ -386,16 +402,15 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
           o[nt][d][3] *= f1;
         }
       }
-      const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
       for (int x = 0; x < G; ++x) {
         float w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          w[c] = exp2_approx(s[x][nt][c] - base[c & 1]);
+          w[c] = exp2_approx(s[x][nt][c] - (C::quant ? lm : m)[nt][c & 1]);
           l[nt][c & 1] += w[c];
           if constexpr (C::quant) {
-            w[c] = exp2_approx(s[x][nt][c] + vl[x][c >> 1] - base[c & 1]);
+            w[c] = exp2_approx(s[x][nt][c] + vl[x][c >> 1] - m[nt][c & 1]);
             // (the scale of a key that is not seen may be anything)
             if (scut && s[x][nt][c] == -INFINITY) w[c] = 0.0f;
           }
@@ -585,11 +600,18 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      float b = C::quant ? lm[nt][c] : m[nt][c];
+      if constexpr (C::quant) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, x));
+        l[nt][c] *= exp2_approx(lm[nt][c] - b);
+      }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
       const int r = 2 * t + c + 8 * nt;
       if (g == 0) {
         sm[warp][r] = m[nt][c];
+        sb[warp][r] = b;
         sl[warp][r] = l[nt][c];
       }
 #pragma unroll
@@ -602,20 +624,41 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     const int r = k / (DH / 4), d = k % (DH / 4) * 4, token = p.by_group(r);
     const int head = kvh * p.group + r - token * p.group;
     const int64_t row = sq.r0 + token;
-    float top = -INFINITY, sum = 0.0f;
+    float top = kNone, sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w][r]);
-    const float base = top == -INFINITY ? 0.0f : top;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sb[w][r]);
+    const float base = top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum = fmaf(exp2_approx(sb[w][r] - base), sl[w][r], sum);
+    // what the sums are multiplied with.  8-bit: it goes into the factors of O, which holds the values' scales: these
+    // factors are taken in two halves, as one may be beyond f32 where their product with O is not, and a piece has the
+    // whole powers of two of its weights' sum in its base, so that large values do not add up beyond f32
+    float inv = 1.0f;
+    if (direct) {
+      inv = 1.0f / sum;
+    } else if (C::quant && sum > 0.0f && sum < INFINITY) {  // (at least 2^-8 then)
+      const uint32_t e = __float_as_uint(sum) & 0x7f800000u;
+      inv = __uint_as_float(0x7f000000u - e);
+      sum *= inv;
+      top += (float)((int)(e >> 23) - 127);
+    }
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2_approx(sm[w][r] - base);
       const float4 x = *reinterpret_cast<const float4*>(so + (w * 8 * NT + r) * C::row + d);
-      sum = fmaf(f, sl[w][r], sum);
-      y.x = fmaf(f, x.x, y.x);
-      y.y = fmaf(f, x.y, y.y);
-      y.z = fmaf(f, x.z, y.z);
-      y.w = fmaf(f, x.w, y.w);
+      if constexpr (C::quant) {
+        const float f = exp2_approx(0.5f * (sm[w][r] - base)), h = f * inv;
+        y.x = fmaf(x.x * f, h, y.x);
+        y.y = fmaf(x.y * f, h, y.y);
+        y.z = fmaf(x.z * f, h, y.z);
+        y.w = fmaf(x.w * f, h, y.w);
+      } else {
+        const float f = exp2_approx(sm[w][r] - base);
+        y.x = fmaf(f, x.x, y.x);
+        y.y = fmaf(f, x.y, y.y);
+        y.z = fmaf(f, x.z, y.z);
+        y.w = fmaf(f, x.w, y.w);
+      }
     }
     if (!direct) {
       const int64_t slot = ((int64_t)blockIdx.z * p.c.rows + row) * p.nq + head;
@@ -627,7 +670,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     float4 x = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
     const bool blank = p0 + token < 0;
     if (p.gate && !blank) x = *reinterpret_cast<const float4*>(p.gate + row * p.gate_row + head * p.gate_head + d);
-    const float inv = 1.0f / sum;
+    if constexpr (C::quant) inv = 1.0f;
     uint2 w = make_uint2(pack_bf16(gated_by(y.x * inv, x.x), gated_by(y.y * inv, x.y)),
                          pack_bf16(gated_by(y.z * inv, x.z), gated_by(y.w * inv, x.w)));
     if (blank) w = make_uint2(0, 0);

@@ -347,3 +347,53 @@ def test_nan_codes_reach_only_the_rows_that_see_them(fak, code, nq, n_kv, dh, ne
     others = [d for d in range(dh) if d not in (5, dh - 2)]
     _kv.check(s.out[blind], o[blind], tol[blind], "rows that do not see it")
     _kv.check(s.out[..., others], o[..., others], tol[..., others], "the other elements")
+
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [1e17, 1e30])
+@pytest.mark.parametrize("where", ["later keys", "earlier keys", "every second step", "one warp's keys", "one key"])
+@pytest.mark.parametrize("new,total", [(1, 300), (2, 300), (1, 6000), (40, 300)])
+def test_zeros_beside_large_values(fak, kind, size, where, new, total):
+    """Equal scores: a value's share is one part in as many as a row sees, whatever its size."""
+    def edit(K, V):
+        K[0].zero_()
+        j = torch.arange(total, device="cuda")
+        large = {"later keys": j >= total // 2, "earlier keys": j < total // 2, "every second step": (j // 128) % 2 == 1,
+                 "one warp's keys": (j // 16) % 8 == 5, "one key": j == 17}[where]
+        V[0].mul_(torch.where(large, size, 0.0)[:, None, None])
+
+    case(fak, kind, 4, 2, 128, 16, [(new, total)], seed=3, edit=edit)
+    case(fak, kind, 6, 1, 256, 16, [(new, total)], seed=4, edit=edit)
+
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,total", [(1, 300), (2, 300), (1, 6000), (40, 300)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_smallest_values(fak, kind, new, total, zeros):
+    """Values just above the size that the 8-bit kinds hold as zeros, the same at each key, with zeros between or without."""
+    def edit(K, V):
+        sign = torch.where(V[0][:1] < 0, -1.0, 1.0)
+        V[0].copy_(sign.expand_as(V[0]) * 1e-30)
+        if zeros:
+            V[0][:total // 2] = 0
+
+    for nq, n_kv, dh in ((4, 2, 128), (6, 1, 256)):
+        s = Setup(fak, kind, nq, n_kv, dh, 16, [(new, total)], seed=5, edit=edit)
+        s.run()
+        torch.cuda.synchronize()
+        assert fak.fak_device_status() == 0
+        for r, o, tol in s.want():
+            _kv.check(s.out[r], o, tol - 1e-30, "1e-30")  # (the bar without its absolute part)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("new,total", [(1, 300), (2, 300), (1, 6000)])
+def test_largest_values_of_few_rows(fak, kind, new, total):
+    """Values whose sum over the keys is beyond f32, and their mean is not; sharp scores beside equal ones."""
+    def edit(K, V):
+        V[0].mul_(1e37)
+
+    case(fak, kind, 4, 2, 128, 16, [(new, total)], seed=6, edit=edit)
+    case(fak, kind, 6, 1, 256, 16, [(new, total)], seed=7, edit=edit, sharp=8.0)
