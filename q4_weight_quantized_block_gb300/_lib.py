@@ -260,15 +260,18 @@ def fak_device_status(stream=None):
 
 # ------------------------------------------------------------------ paged KV cache and attention
 class KVCache:
-    """A paged cache's description: codes k, v [n_pages, n_kv, page, dh] (contiguous; bf16, or one byte each)
-    and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive."""
+    """A paged cache's description: codes k, v [n_pages, n_kv, page, dh] (contiguous; bfloat16, or for e4m3 uint8 or
+    float8_e4m3fn, for int8 int8 or uint8) and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive."""
 
     def __init__(self, kind, k, v, k_scale=None, v_scale=None):
-        width, scales = (2 if kind == FAK_KV_BF16 else 1), (k_scale, v_scale)
-        if k.shape != v.shape or k.dim() != 4 or any(t is not None and t.shape != k.shape[:3] for t in scales):
+        import torch
+        types = {FAK_KV_BF16: (torch.bfloat16,), FAK_KV_E4M3: (torch.uint8, torch.float8_e4m3fn),
+                 FAK_KV_I8: (torch.int8, torch.uint8)}.get(kind, ())
+        scales = [t for t in (k_scale, v_scale) if t is not None]
+        if k.shape != v.shape or k.dim() != 4 or any(t.shape != k.shape[:3] for t in scales):
             raise FakError(2, "KVCache")
-        if any(t.element_size() != width or not t.is_contiguous() for t in (k, v)) or any(
-                t is not None and (t.element_size() != 4 or not t.is_contiguous()) for t in scales):
+        if any(t.dtype not in types or not t.is_contiguous() for t in (k, v)) or any(
+                t.dtype != torch.float32 or not t.is_contiguous() for t in scales):
             raise FakError(1, "KVCache")
         self._keep = (k, v, k_scale, v_scale)
         n_pages, n_kv, page, dh = k.shape
@@ -282,10 +285,11 @@ class KVBatch:
     and kv_len [n_seqs], read when the kernels run.  Keeps the tensors alive."""
 
     def __init__(self, page_table, row_start, kv_len):
+        import torch
         n = page_table.shape[0]
         if page_table.dim() != 2 or row_start.shape != (n + 1,) or kv_len.shape != (n,):
             raise FakError(2, "KVBatch")
-        if any(t.element_size() != 4 or not t.is_contiguous() for t in (page_table, row_start, kv_len)):
+        if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (page_table, row_start, kv_len)):
             raise FakError(1, "KVBatch")
         self._keep = (page_table, row_start, kv_len)
         self.desc = KvBatchDesc(n, page_table.shape[1], _ptr(page_table), _ptr(row_start), _ptr(kv_len))
@@ -311,6 +315,28 @@ def _heads(t, heads, dh, dtype, where):
     return t.data_ptr(), stride[0], stride[1]
 
 
+def _gain(w, dh, f32, where):
+    """Pointer of a norm's gain: f32, dh values next to each other; None: no norm."""
+    if w is None:
+        return None
+    if w.dtype != f32 or not w.is_contiguous():
+        raise FakError(1, where)
+    if w.numel() != dh:
+        raise FakError(2, where)
+    return w.data_ptr()
+
+
+def _rope(table, rot, where):
+    """Pointer of a rotary table: 64-bit integers, rot / 2 or more of them."""
+    if table is None:
+        return None
+    if table.element_size() != 8 or table.is_floating_point() or table.is_complex() or not table.is_contiguous():
+        raise FakError(1, where)
+    if 2 * table.numel() < rot:
+        raise FakError(2, where)
+    return table.data_ptr()
+
+
 def fak_rope_table(rot, theta):
     """Host int64 [rot / 2]: the rotary frequencies as 64-bit fractions of a turn (copy it to the device)."""
     out = np.empty(max(0, rot // 2), dtype=np.int64)
@@ -320,7 +346,8 @@ def fak_rope_table(rot, theta):
 
 def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_w=None, eps=1e-6, rope=None, rot=0,
                   stream=None):
-    """k, v [rows, n_kv, dh] and q [rows, nq, dh], f32 or bf16 (views with strides are fine); q_out bf16."""
+    """k, v [rows, n_kv, dh] and q [rows, nq, dh], f32 or bf16 (views with strides are fine); q_out bf16; gains f32 [dh];
+    rope int64, fak_rope_table's values on the device."""
     dtype, (f32, bf16) = k.dtype, _float_types()
     if (dtype != f32 and dtype != bf16) or (q is not None and (
             q_out is None or q_out.dtype != bf16 or not q_out.is_contiguous())):
@@ -332,7 +359,8 @@ def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_
     nq = 0 if q is None else q.shape[1]
     qp, qr, qh = (None, 0, 0) if q is None else _heads(q, nq, cache.dh, dtype, "fak_kv_append")
     r = KvRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
-               vh, _ptr(q_norm_w), _ptr(k_norm_w), _ptr(rope), _ptr(q_out))
+               vh, _gain(q_norm_w, cache.dh, f32, "fak_kv_append"), _gain(k_norm_w, cache.dh, f32, "fak_kv_append"),
+               _rope(rope, rot, "fak_kv_append"), _ptr(q_out))
     _check(lib.fak_kv_append(cache.ref, batch.ref, ctypes.addressof(r), _stream(stream)), "fak_kv_append")
 
 
@@ -360,6 +388,8 @@ def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, si
     nq, (f32, bf16) = q.shape[1], _float_types()
     if out.shape != q.shape or (gate is not None and gate.shape != q.shape):
         raise FakError(2, "fak_paged_attn")
+    if workspace is not None and not workspace.is_contiguous():
+        raise FakError(1, "fak_paged_attn")
     qp, qr, qh = _heads(q, nq, cache.dh, bf16, "fak_paged_attn")
     op, orow, oh = _heads(out, nq, cache.dh, bf16, "fak_paged_attn")
     gp, gr, gh = (None, 0, 0) if gate is None else _heads(gate, nq, cache.dh, f32, "fak_paged_attn")

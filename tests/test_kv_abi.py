@@ -208,3 +208,52 @@ def test_binding_refuses_other_float_types(fak):
         with pytest.raises(fak.FakError) as e:
             call()
         assert e.value.status == 1
+
+
+def status_of(fak, call):
+    try:
+        call()
+    except fak.FakError as e:
+        return e.status
+    return 0
+
+
+def test_binding_looks_at_the_types_of_caches_and_batches(fak):
+    torch = pytest.importorskip("torch")
+    shape = (4, 2, 16, 64)
+    z = lambda dtype, *s: torch.zeros(*(s or shape), dtype=dtype)
+    sc = z(torch.float32, *shape[:3])
+    u8, i8, f8 = z(torch.uint8), z(torch.int8), z(torch.uint8).view(torch.float8_e4m3fn)
+    bf, half, e5 = z(torch.bfloat16), z(torch.float16), z(torch.uint8).view(torch.float8_e5m2)
+    bf16, e4m3, int8 = fak.FAK_KV_BF16, fak.FAK_KV_E4M3, fak.FAK_KV_I8
+    for good in ((bf16, bf, bf), (e4m3, u8, u8, sc, sc), (e4m3, f8, f8, sc, sc), (int8, i8, i8, sc, sc), (int8, u8, u8, sc, sc)):
+        fak.KVCache(*good)
+    for bad in ((bf16, half, half), (bf16, bf, half), (bf16, z(torch.int16), z(torch.int16)), (e4m3, e5, e5, sc, sc),
+                (e4m3, z(torch.bool), u8, sc, sc), (int8, f8, f8, sc, sc), (int8, i8, i8, sc.int(), sc), (int8, i8, i8, sc, sc.int()),
+                (3, u8, u8, sc, sc)):
+        assert status_of(fak, lambda: fak.KVCache(*bad)) == 1, bad[0]
+    t, s, n = z(torch.int32, 2, 3), z(torch.int32, 3), z(torch.int32, 2)
+    fak.KVBatch(t, s, n)
+    for bad in ((t.float(), s, n), (t, s.float(), n), (t, s, n.float()), (t, s.view(torch.uint32), n)):
+        assert status_of(fak, lambda: fak.KVBatch(*bad)) == 1
+
+
+def test_binding_looks_at_gains_tables_and_workspaces(fak):
+    torch = pytest.importorskip("torch")
+    u8, sc = torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2, 16)
+    cache = fak.KVCache(fak.FAK_KV_I8, u8, u8, sc, sc)
+    batch = fak.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                        torch.zeros(2, dtype=torch.int32))
+    batch.desc.n_seqs = 0  # (nothing to do, whatever is let through)
+    x, q = torch.zeros(5, 2, 64), torch.zeros(5, 4, 64)
+    out, w = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.ones(64)
+    append = lambda **kw: status_of(fak, lambda: fak.fak_kv_append(cache, batch, x, x, q=q, q_out=out, stream=0, **kw))
+    for gain, status in ((w.to(torch.bfloat16), 1), (w.double(), 1), (torch.ones(128)[::2], 1), (w[:3], 2), (torch.ones(256), 2),
+                         (w[:0], 2), (w[:1].expand(64), 1)):
+        assert append(q_norm_w=gain) == status and append(k_norm_w=gain) == status
+    rope = torch.zeros(32, dtype=torch.int64)
+    for table, status in ((rope[:1], 2), (rope[:31], 2), (rope.double(), 1), (torch.zeros(64, dtype=torch.int32), 1), (rope[:1].expand(32), 1),
+                          (torch.zeros(64, dtype=torch.int64)[::2], 1)):
+        assert append(rope=table, rot=64) == status
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
+    assert status_of(fak, lambda: fak.fak_paged_attn(cache, batch, out, out, 1, 1, workspace=ws, stream=0)) == 1
