@@ -259,9 +259,38 @@ def fak_device_status(stream=None):
 
 
 # ------------------------------------------------------------------ paged KV cache and attention
+def _current_device():
+    """torch's current CUDA device; as _current_stream."""
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return torch.cuda.current_device()
+
+
+def _one_device(where, tensors):
+    """The CUDA device of all the tensors that are given (-1: the host's)."""
+    tensors = [t for t in tensors if t is not None]
+    if any(t.device != tensors[0].device for t in tensors):
+        raise FakError(8, where)
+    return tensors[0].get_device()
+
+
+def _on_device(where, cache, batch, *tensors):
+    """The kernels run on the current device and read there: everything has to be on it, and nothing on the host."""
+    device = cache.device
+    if device < 0 or batch.device != device:
+        raise FakError(8, where)
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise FakError(8, where)
+    if _current_device() != device:
+        raise FakError(8, where)
+
+
 class KVCache:
     """A paged cache's description: codes k, v [n_pages, n_kv, page, dh] (contiguous; bfloat16, or for e4m3 uint8 or
-    float8_e4m3fn, for int8 int8 or uint8) and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive."""
+    float8_e4m3fn, for int8 int8 or uint8) and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive.  Calls on tensors of the host or of
+    another device than the current one are refused (FAK_ERR_UNSUPPORTED)."""
 
     def __init__(self, kind, k, v, k_scale=None, v_scale=None):
         import torch
@@ -273,6 +302,7 @@ class KVCache:
         if any(t.dtype not in types or not t.is_contiguous() for t in (k, v)) or any(
                 t.dtype != torch.float32 or not t.is_contiguous() for t in scales):
             raise FakError(1, "KVCache")
+        self.device = _one_device("KVCache", (k, v, k_scale, v_scale))
         self._keep = (k, v, k_scale, v_scale)
         n_pages, n_kv, page, dh = k.shape
         self.kind, self.n_kv, self.dh = kind, n_kv, dh
@@ -291,6 +321,7 @@ class KVBatch:
             raise FakError(2, "KVBatch")
         if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (page_table, row_start, kv_len)):
             raise FakError(1, "KVBatch")
+        self.device = _one_device("KVBatch", (page_table, row_start, kv_len))
         self._keep = (page_table, row_start, kv_len)
         self.desc = KvBatchDesc(n, page_table.shape[1], _ptr(page_table), _ptr(row_start), _ptr(kv_len))
         self.ref = ctypes.addressof(self.desc)
@@ -361,6 +392,7 @@ def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_
     r = KvRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
                vh, _gain(q_norm_w, cache.dh, f32, "fak_kv_append"), _gain(k_norm_w, cache.dh, f32, "fak_kv_append"),
                _rope(rope, rot, "fak_kv_append"), _ptr(q_out))
+    _on_device("fak_kv_append", cache, batch, k, v, q, q_out, q_norm_w, k_norm_w, rope)
     _check(lib.fak_kv_append(cache.ref, batch.ref, ctypes.addressof(r), _stream(stream)), "fak_kv_append")
 
 
@@ -373,6 +405,7 @@ def fak_kv_read(cache, batch, k_out, v_out, stream=None):
     if any(t.dim() != 3 or t.shape[1:] != (cache.n_kv, cache.dh) or t.shape[0] != outs[0].shape[0] for t in outs):
         raise FakError(2, "fak_kv_read")
     kind = FAK_ROWS_F32 if outs[0].element_size() == 4 else FAK_ROWS_BF16
+    _on_device("fak_kv_read", cache, batch, *outs)
     _check(lib.fak_kv_read(cache.ref, batch.ref, outs[0].shape[0], kind, _ptr(k_out), _ptr(v_out), _stream(stream)),
            "fak_kv_read")
 
@@ -396,6 +429,7 @@ def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, si
     a = AttnArgs(nq, window, sinks, max_q, max_kv, cache.dh ** -0.5 if scale is None else scale, q.shape[0], qp, qr, qh,
                  gp, gr, gh, op, orow, oh, _ptr(workspace),
                  0 if workspace is None else workspace.numel() * workspace.element_size())
+    _on_device("fak_paged_attn", cache, batch, q, out, gate, workspace)
     _check(lib.fak_paged_attn(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)), "fak_paged_attn")
 
 

@@ -257,3 +257,27 @@ def test_binding_looks_at_gains_tables_and_workspaces(fak):
         assert append(rope=table, rot=64) == status
     ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
     assert status_of(fak, lambda: fak.fak_paged_attn(cache, batch, out, out, 1, 1, workspace=ws, stream=0)) == 1
+
+
+def test_binding_refuses_tensors_of_the_host(fak):
+    """The kernels read what they are given on the device: a host tensor (a batch's lengths, say) must not get that far."""
+    torch = pytest.importorskip("torch")
+    u8, sc = torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2, 16)
+    cache = fak.KVCache(fak.FAK_KV_I8, u8, u8, sc, sc)
+    batch = fak.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                        torch.zeros(2, dtype=torch.int32))
+    batch.desc.n_seqs = 0  # (nothing to do, whatever is let through)
+    x, q = torch.zeros(5, 2, 64), torch.zeros(5, 4, 64)
+    out = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    calls = [lambda: fak.fak_kv_append(cache, batch, x, x, q=q, q_out=out, stream=0), lambda: fak.fak_kv_read(cache, batch, x, x, stream=0),
+             lambda: fak.fak_paged_attn(cache, batch, out, out, 1, 1, stream=0)]
+    for call in calls:
+        assert status_of(fak, call) == 8
+    # a cache and lengths of device 0, as far as the binding sees, and rows of the host
+    cache.device = batch.device = 0
+    for call in calls:
+        assert status_of(fak, call) == 8
+    with pytest.raises(fak.FakError) as e:
+        fak.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                    torch.zeros(2, dtype=torch.int32, device="meta"))
+    assert e.value.status == 8
