@@ -469,7 +469,10 @@ typedef struct {
  * row_start[n_seqs] on belong to no sequence.  A sequence may have no rows.
  * A sequence whose numbers are out of range (row_start not rising within
  * 0 .. the call's rows, kv_len negative or above max_pages * page) is left
- * out: nothing of it is read or written, and FAK_ERR_DEVICE is recorded.  A
+ * out: nothing of it is read or written, and FAK_ERR_DEVICE is recorded.  (Where
+ * a row_start within 0 .. rows lies below one before it, attention may leave out
+ * the sequences before it too, and a row that two sequences claim is one of theirs
+ * in the cache's writes and reads, and may hold anything after attention.)  A
  * page number outside [0, n_pages) is recorded too: a write to it is dropped,
  * a read takes page 0 in its place. */
 typedef struct {

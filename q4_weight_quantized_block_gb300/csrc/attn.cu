@@ -31,10 +31,12 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y * kJoin + warp / W;
   const int64_t row = blockIdx.x;
   int s;
-  const KvSeq sq = kv_locate(p.c, row, lane, s);
+  KvSeq sq = kv_locate(p.c, row, lane, s);
+  bool bad;
+  if (!kv_has(sq, row)) sq = kv_locate_all(p.c, row, lane, s, bad);
   // the pieces' kernel is done (every block waits: this grid must not end before that one)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!sq.ok || row < sq.r0 || row >= sq.r1) return;
+  if (!sq.ok) return;
   if (W == 1 && h >= p.nq) return;
   const int token = (int)(row - sq.r0);
   const int tokens = sq.r1 - sq.r0, base = token / p.block * p.block, last = base + min(p.block, tokens - base) - 1;

@@ -275,25 +275,31 @@ FAK_DEV bool taken_over(const void* answer, int& x, int& y, int& z) {
 
 // Block x's sequence: the one of the last s with r0(s) / block + s <= x.  These starts rise by at least the
 // sequence's number of blocks, so every block of rows has an x, and some x have none.  False: nothing to do.
+// (Starts that are out of range are passed over, so that they leave out their own sequences alone.)
 FAK_DEV bool find_unit(const AttnParams& p, int x, int head, int split, int rank, int lane, Unit& u) {
+  auto before = [&](int start, int i) { return (unsigned)start <= (unsigned)p.c.rows && p.by_block(start) + i <= x; };
   int lo;
   KvSeq sq;
   if (p.c.n_seqs < 32) {
     const int start = lane <= p.c.n_seqs ? p.c.row_start[lane] : 0;
     const int len = lane < p.c.n_seqs ? p.c.kv_len[lane] : 0;
-    lo = max(__popc(__ballot_sync(0xffffffffu, lane < p.c.n_seqs && p.by_block(start) + lane <= x)) - 1, 0);
+    lo = max(31 - __clz(__ballot_sync(0xffffffffu, lane < p.c.n_seqs && before(start, lane))), 0);
     sq.r0 = __shfl_sync(0xffffffffu, start, lo);
     sq.r1 = __shfl_sync(0xffffffffu, start, lo + 1);
     sq.len = __shfl_sync(0xffffffffu, len, lo);
     sq.ok = kv_seq_ok(p.c, sq);
   } else {
     lo = 0;
-    int hi = p.c.n_seqs;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && p.by_block(p.c.row_start[i]) + i <= x));
-      if (n > 1) lo += (n - 1) * step;
-      hi = min(lo + step, hi);
+    for (int hi = p.c.n_seqs;;) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step, start = i < hi ? p.c.row_start[i] : -1;
+      const bool yes = before(start, i);
+      const int n = 32 - __clz(__ballot_sync(0xffffffffu, yes)), from = lo + max(n - 1, 0) * step;
+      const unsigned later = __ballot_sync(0xffffffffu, !yes && (unsigned)start <= (unsigned)p.c.rows) & ~first_bits(n);
+      const int to = later ? lo + (__ffs(later) - 1) * step : hi;
+      const bool stuck = from == lo && to == hi;  // (all starts but lo's are out of range: not worth a search)
+      lo = from;
+      hi = to;
+      if (step == 1 || stuck) break;
     }
     sq = kv_seq(p.c, lo);
   }

@@ -54,8 +54,8 @@ FAK_DEV int kv_find_seq(const KvView& c, int64_t row, int lane) {
   return lo;
 }
 
-// A row's sequence s and its numbers (a whole warp calls).  Up to 31 sequences' numbers are read at once, which
-// saves a trip to memory.
+// A row's sequence s and its numbers where the starts rise (a whole warp calls).  Up to 31 sequences' numbers are read at
+// once, which saves a trip to memory.  What is found may not have the row: kv_has tells.
 FAK_DEV KvSeq kv_locate(const KvView& c, int64_t row, int lane, int& s) {
   if (c.n_seqs < 32) {
     const int start = lane <= c.n_seqs ? c.row_start[lane] : 0x7fffffff;
@@ -70,6 +70,30 @@ FAK_DEV KvSeq kv_locate(const KvView& c, int64_t row, int lane, int& s) {
   }
   s = kv_find_seq(c, row, lane);
   return kv_seq(c, s);
+}
+
+FAK_DEV bool kv_has(const KvSeq& q, int64_t row) { return q.ok && q.r0 <= row && row < q.r1; }
+
+// The same where they may fall, as they do beside numbers that are out of range: all sequences are looked at (a row that
+// several have is one of theirs).  ok is false where none has the row; bad: some numbers are out of range.
+FAK_DEV KvSeq kv_locate_all(const KvView& c, int64_t row, int lane, int& s, bool& bad) {
+  bad = false;
+#pragma unroll 1
+  for (int base = 0; base < c.n_seqs; base += 32) {
+    KvSeq q{0, 0, 0, true};
+    if (base + lane < c.n_seqs) q = kv_seq(c, base + lane);
+    bad |= __any_sync(0xffffffffu, !q.ok);
+    const unsigned has = __ballot_sync(0xffffffffu, kv_has(q, row));
+    if (!has) continue;
+    const int src = 31 - __clz(has);
+    s = base + src;
+    q.r0 = __shfl_sync(0xffffffffu, q.r0, src);
+    q.r1 = __shfl_sync(0xffffffffu, q.r1, src);
+    q.len = __shfl_sync(0xffffffffu, q.len, src);
+    q.ok = bad = true;  // (with rising starts it had been found)
+    return q;
+  }
+  return KvSeq{0, 0, 0, false};
 }
 
 // The vector index (page, head, slot) of position `pos` of sequence s; -1 - that of page 0 when the

@@ -252,3 +252,35 @@ def test_int8_codes_bit_for_bit(fak):
             inv = torch.ones_like(x[..., 0]).div(x.abs().amax(-1)).mul(127.0)
             assert torch.equal(codes[pages, :, slots], (x * inv[..., None]).round().to(torch.int8))
         row += n
+
+
+
+@pytest.mark.parametrize("bad", [1000, -5])
+@pytest.mark.parametrize("n,new", [(4, 3), (31, 1), (32, 1), (70, 3)])
+def test_a_bad_start_leaves_out_its_own_sequences_only(fak, n, new, bad):
+    dh, page, n_kv, total = 64, 16, 2, 20
+    table, start, kv_len, rows, n_pages = _kv.batch_tensors([(new, total)] * n, page, pad_rows=2)
+    cache, mem = _kv.empty_cache(fak, "bf16", n_pages, n_kv, page, dh)
+    good = fak.KVBatch(table, start, kv_len)
+    old, x, q = randn(90, rows, n_kv, dh), randn(91, rows, n_kv, dh), randn(92, rows, n_kv, dh)
+    fak.fak_kv_append(cache, good, old, old)
+    i = n // 2 // 2 * 2
+    st = start.clone()
+    st[i] = bad if bad < 0 else rows + bad  # sequences i - 1 and i
+    broken = fak.KVBatch(table, st, kv_len)
+    ok = [r for r in range(n * new) if not (i - 1) * new <= r < (i + 1) * new]
+    left = [r for r in range(n * new) if r not in ok]
+    assert fak.fak_device_status() == 0
+    got = torch.full((rows, n_kv, dh), 9.0, device="cuda")
+    fak.fak_kv_read(cache, broken, got, None)
+    assert fak.fak_device_status() == 7
+    assert torch.equal(got[ok], old[ok].to(torch.bfloat16).float())
+    assert bool((got[left] == 9.0).all()) and bool((got[n * new:] == 9.0).all())
+    q_out = torch.full((rows, n_kv, dh), 9.0, dtype=torch.bfloat16, device="cuda")
+    fak.fak_kv_append(cache, broken, x, x, q=q, q_out=q_out)
+    assert fak.fak_device_status() == 7
+    fak.fak_kv_read(cache, good, got, None)
+    assert fak.fak_device_status() == 0
+    assert torch.equal(got[ok], x[ok].to(torch.bfloat16).float()) and torch.equal(got[left], old[left].to(torch.bfloat16).float())
+    assert torch.equal(q_out[ok], q[ok].to(torch.bfloat16))
+    assert bool((q_out[left] == 9.0).all()) and bool((q_out[n * new:] == 9.0).all())

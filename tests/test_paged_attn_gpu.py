@@ -397,3 +397,21 @@ def test_largest_values_of_few_rows(fak, kind, new, total):
 
     case(fak, kind, 4, 2, 128, 16, [(new, total)], seed=6, edit=edit)
     case(fak, kind, 6, 1, 256, 16, [(new, total)], seed=7, edit=edit, sharp=8.0)
+
+
+
+@pytest.mark.parametrize("bad", [1000, -5])
+@pytest.mark.parametrize("kind,new,total,n", [("bf16", 1, 60, 4), ("e4m3", 1, 3000, 4), ("bf16", 40, 90, 4), ("i8", 200, 3000, 4),
+                                              ("e4m3", 1, 3000, 40), ("bf16", 40, 90, 40), ("i8", 3, 70, 70)])
+def test_a_bad_start_leaves_out_its_own_sequences_only(fak, kind, new, total, n, bad):
+    s = Setup(fak, kind, 4, 1, 128, 16, [(new, total)] * n, seed=21)
+    i = n // 2 // 2 * 2
+    s.start[i] = bad if bad < 0 else s.rows + bad  # sequences i - 1 and i
+    s.run()
+    torch.cuda.synchronize()
+    assert fak.fak_device_status() == 7
+    for q, (r, o, tol) in enumerate(s.want()):
+        if q in (i - 1, i):
+            assert bool((s.out[r] == 9.0).all()), q
+        else:
+            _kv.check(s.out[r], o, tol, "sequence %d" % q)
