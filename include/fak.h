@@ -553,6 +553,13 @@ typedef struct {
 size_t fak_paged_attn_workspace_bytes(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_attn_args* args);
 int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* batch, const fak_attn_args* args, fak_stream_t stream);
 
+/* Every wait of its kernels is bounded (2 s, and 20 us for each key tile of a
+ * block); one that runs out records FAK_ERR_TIMEOUT, and its block ends without
+ * results (rows whose keys were cut may then get anything).
+ * Test hooks, for all later calls of the process: the limit in nanoseconds (0:
+ * the default), and with unreachable = 1 a wait that can never complete. */
+int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable);
+
 /* ------------------------------------------------------------------ status
  * Synchronizes `stream`, then reads and clears the status word shared by the
  * stateless calls (GEMV, batched GEMV, MLP, GEMM, paged KV cache and attention). */

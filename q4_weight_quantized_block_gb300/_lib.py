@@ -113,6 +113,7 @@ _SIGS = {
     "fak_kv_read": ([P, P, I64, I32, P, P, P], I32),
     "fak_paged_attn_workspace_bytes": ([P, P, P], SZ),
     "fak_paged_attn": ([P, P, P, P], I32),
+    "fak_paged_attn_debug_wait": ([I64, I32], I32),
     "fak_prefill_create": ([ctypes.POINTER(DecodeDesc), I64, ctypes.POINTER(P)], I32),
     "fak_prefill_run": ([P, P, P, P, P], I32),
     "fak_prefill_read_hidden": ([P, P, SZ, P], I32),
@@ -431,6 +432,11 @@ def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, si
                  0 if workspace is None else workspace.numel() * workspace.element_size())
     _on_device("fak_paged_attn", cache, batch, q, out, gate, workspace)
     _check(lib.fak_paged_attn(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)), "fak_paged_attn")
+
+
+def fak_paged_attn_debug_wait(timeout_ns=0, unreachable=0):
+    """Test hooks: the limit of the attention's waits (0: the default), and a wait that can never complete."""
+    _check(lib.fak_paged_attn_debug_wait(int(timeout_ns), int(unreachable)), "fak_paged_attn_debug_wait")
 
 
 # ------------------------------------------------------------------ decode context

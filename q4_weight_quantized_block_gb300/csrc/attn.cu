@@ -18,6 +18,9 @@ namespace {
 
 __device__ int g_attn_status;
 
+std::atomic<int64_t> g_wait_ns{0};       // fak_paged_attn_debug_wait's
+std::atomic<int> g_unreachable{0};
+
 constexpr int kPlanSms = 152;  // GB300's SMs: the workspace's size must not depend on the current device
 
 // Adds up the pieces of the blocks of rows whose keys were cut: W warps (1, eight (row, query head)s to a block, or 16)
@@ -254,7 +257,9 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   p.part = static_cast<float*>(a->workspace);
   p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + parts);
   // (a wait may be for a whole block: 2 s, and 20 us for each of its tiles)
-  p.timeout_ns = 2000000000ull + 20000ull * (unsigned)pl.per_split;
+  const int64_t wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  p.timeout_ns = wait_ns ? (unsigned long long)wait_ns : 2000000000ull + 20000ull * (unsigned)pl.per_split;
+  p.unreachable = g_unreachable.load(std::memory_order_relaxed);
   cudaStream_t s = (cudaStream_t)stream;
   e = pl.few ? attn_rows_launch(cache->kind, cache->dh, p, st_word, dev, s)
              : attn_tile_launch(cache->kind, cache->dh, cache->page, cache->n_pages * cache->n_kv * cache->page, p,
@@ -262,6 +267,13 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   if (e == cudaSuccess && pl.splits > 1)
     e = cache->dh == 64 ? launch_join<64>(p, s) : cache->dh == 128 ? launch_join<128>(p, s) : launch_join<256>(p, s);
   return fak_cuda_status(e);
+}
+
+extern "C" int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable) {
+  if (timeout_ns < 0 || (unreachable != 0 && unreachable != 1)) return FAK_ERR_INVALID_ARG;
+  g_wait_ns.store(timeout_ns, std::memory_order_relaxed);
+  g_unreachable.store(unreachable, std::memory_order_relaxed);
+  return FAK_OK;
 }
 
 int fak_attn_take_status() {

@@ -40,6 +40,7 @@ struct AttnParams {
   float* part;   // [splits][rows][nq][dh]
   float2* stat;  // [splits][rows][nq]
   unsigned long long timeout_ns;
+  int unreachable;  // a test's: 1 where copies are never to count as landed
 };
 
 constexpr int kTileM = 128;  // rows (token, query head of the group) of a CTA

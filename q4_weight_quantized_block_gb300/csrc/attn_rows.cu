@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   __shared__ uint64_t bars[kWarps][C::halves];  // a slot's bytes are there
   if (lane == 0) {
 #pragma unroll
-    for (int h = 0; h < C::halves; ++h) mbar_init(&bars[warp][h], 1);
+    for (int h = 0; h < C::halves; ++h) mbar_init(&bars[warp][h], 1 + p.unreachable);
     fence_mbar_init();
   }
   __syncwarp();
@@ -211,8 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     }
   };
   places();
-  auto fetch = [&](int slot, bool value) {  // a half; nothing past the last step
-    __syncwarp();  // (what stood there has been read)
+  auto fetch = [&](int slot, bool value) {  // a half, where what stood there has been read; nothing past the last step
     if (fj >= 0 && elect_one()) {
       uint64_t* const bar = &bars[warp][slot];
       mbar_arrive_expect_tx(bar, G * (16 * C::row_bytes + (C::quant && !value ? 128 : 0)));
@@ -553,38 +552,48 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
   int slot = 0;
   auto advance = [&]() { slot = slot + 1 == C::halves ? 0 : slot + 1; };
   uint32_t phases = 0;  // of the slots
-  auto landed = [&](int h) {
+  auto landed = [&](int h) {  // false: the limit ran out
     uint64_t* const bar = &bars[warp][h];
     const uint32_t parity = phases >> h & 1;
     phases ^= 1u << h;
     for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_suspend(bar, parity, 20000u)) return;
+      if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait_suspend(bar, parity, 20000u))
-      if (globaltimer_ns() - t0 > p.timeout_ns) {
-        attn_record(status, FAK_ERR_TIMEOUT);
-        return;
-      }
+      if (globaltimer_ns() - t0 > p.timeout_ns) return false;
+    return true;
   };
-  // the product of a step runs beside the scores of the next, which do not depend on it
+  // The product of a step runs beside the scores of the next, which do not depend on it.  What stands in a slot is read
+  // whether it landed or not; before the slot is filled again the lanes agree on that.  (As a vote ahead of the scores
+  // this took 1 to 3% longer.)
+  bool ok = true;
+  int used = 0;  // where the limit runs out: halves that were waited for before
   if (j0 >= 0) {
-    landed(0);
+    const bool there = landed(0);
     scores(slots);
-    fetch(0, oddly);
-    advance();
-    softmax(j0);
+    ok = __all_sync(0xffffffffu, there);
+    if (ok) {
+      __syncwarp();
+      fetch(0, oddly);
+      advance();
+      softmax(j0);
+    }
   }
-  while (j0 >= 0) {
+  while (ok && j0 >= 0) {
     int ni = i, nj = j0;
     next(ni, nj);
     const int kslot = slot + 1 == C::halves ? 0 : slot + 1;
-    landed(slot);
-    if (nj >= 0) landed(kslot);
+    const bool there = landed(slot) && (nj < 0 || landed(kslot));
     // (here, not between the scores and the product: there it took 2 to 8% longer)
     if (KIND == FAK_KV_E4M3 && p_lo < p_hi && keys_cut(p_lo, p_hi, j0, j0 + 16 * G - 1, p.window, p.sinks))
       nan_codes(slots + slot * C::half);
     scores(slots + kslot * C::half);  // (past the last step: of what stood there, and not used)
     product(slots + slot * C::half);
+    if (!(ok = __all_sync(0xffffffffu, there))) {
+      used = 1 + 2 * (i - begin);
+      break;
+    }
+    __syncwarp();
     fetch(slot, !oddly);
     fetch(kslot, oddly);
     if (nj >= 0) softmax(nj);
@@ -594,7 +603,16 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     j0 = nj;
   }
 
-  __syncthreads();  // the slots become the place where the sums meet
+  if (!ok) {
+    // the limit ran out: the copies in flight land (or a fifth of a second passes), and the block ends without results
+    if (lane == 0) attn_record(status, FAK_ERR_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns(), limit = p.timeout_ns < 200000000ull ? p.timeout_ns : 200000000ull;
+    for (int n = used; n < min(used + C::halves, 2 * (end - begin)); ++n)
+      while (!mbar_try_wait_suspend(&bars[warp][n % C::halves], n / C::halves & 1, 20000u))
+        if (globaltimer_ns() - t0 > limit) break;
+    __syncwarp();
+  }
+  if (__syncthreads_or(!ok)) return;  // (from here on the slots are the place where the sums meet)
   // the four warps' sums
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)

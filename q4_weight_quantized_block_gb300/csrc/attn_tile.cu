@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<DH, KIND, CG>::threads, 1)
       mbar_init(&uempty[s], 11 + C::warps - 12);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&pair[s], 2);
-    mbar_init(qfull, 1);
+    mbar_init(qfull, 1 + p.unreachable);
     mbar_init(qempty, 1);
     mbar_init(ofree, 8 * CG);
     mbar_init(asked, 1);

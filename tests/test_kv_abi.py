@@ -281,3 +281,9 @@ def test_binding_refuses_tensors_of_the_host(fak):
         fak.KVBatch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
                     torch.zeros(2, dtype=torch.int32, device="meta"))
     assert e.value.status == 8
+
+
+def test_wait_hooks(fak):
+    hook = fak.lib.fak_paged_attn_debug_wait
+    assert hook(-1, 0) == 1 and hook(0, 2) == 1 and hook(0, -1) == 1
+    assert hook(10**9, 0) == 0 and hook(0, 0) == 0

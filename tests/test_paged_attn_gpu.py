@@ -415,3 +415,21 @@ def test_a_bad_start_leaves_out_its_own_sequences_only(fak, kind, new, total, n,
             assert bool((s.out[r] == 9.0).all()), q
         else:
             _kv.check(s.out[r], o, tol, "sequence %d" % q)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,total", [(1, 16), (2, 60), (1, 90), (1, 3000), (20, 90), (40, 90), (100, 300)])
+def test_a_wait_that_runs_out_is_recorded_and_ends(fak, kind, new, total):
+    s = Setup(fak, kind, 4, 1, 128, 16, [(new, total)], seed=25)
+    ws = s.workspace()
+    fak.fak_paged_attn_debug_wait(5_000_000, 1)
+    try:
+        s.run(workspace=ws)
+        torch.cuda.synchronize()
+        assert fak.fak_device_status() == 5
+    finally:
+        fak.fak_paged_attn_debug_wait()
+    assert ws.numel() > 16 or bool((s.out == 9.0).all())  # (where keys are cut, pieces that never came were joined)
+    s.out.fill_(9.0)
+    s.run(workspace=ws)
+    s.check()
