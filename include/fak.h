@@ -466,7 +466,8 @@ typedef struct {
  * row_start[s] + i stands at position kv_len[s] - (row_start[s+1] -
  * row_start[s]) + i.  Position p lies in page page_table[s][p / page], slot
  * p % page.  Rows at negative positions are padding, rows from
- * row_start[n_seqs] on belong to no sequence.  A sequence may have no rows.
+ * row_start[n_seqs] on belong to no sequence.  A sequence may have no rows; a call
+ * without rows or without sequences does nothing (then their pointers may be NULL).
  * A sequence whose numbers are out of range (row_start not rising within
  * 0 .. the call's rows, kv_len negative or above max_pages * page) is left
  * out: nothing of it is read or written, and FAK_ERR_DEVICE is recorded.  (Where

@@ -205,7 +205,7 @@ extern "C" int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* bat
   memset(&p, 0, sizeof(p));
   int st = kv_view(cache, batch, &p.c);
   if (st != FAK_OK) return st;
-  if (!a || !a->q || !a->out) return FAK_ERR_INVALID_ARG;
+  if (!a || (a->rows && (!a->q || !a->out))) return FAK_ERR_INVALID_ARG;
   if ((st = attn_shape(cache, a)) != FAK_OK) return st;
   p.q_row = kv_stride(a->q_row, a->rows);
   p.q_head = kv_stride(a->q_head, a->nq);

@@ -392,7 +392,8 @@ extern "C" int fak_kv_append(const fak_kv_cache* cache, const fak_kv_batch* batc
   if (r->nq < 0 || r->rows < 0 || r->rows > 0x7fffffff || r->rot < 0 || r->rot % 16 || r->rot > cache->dh ||
       (int64_t)r->nq + 2 * cache->n_kv > 65535 * kKvWarps)
     return FAK_ERR_SHAPE;
-  if (!r->k || !r->v || (r->nq && (!r->q || !r->q_out)) || (r->rot && !r->rope)) return FAK_ERR_INVALID_ARG;
+  if (r->rows && (!r->k || !r->v || (r->nq && (!r->q || !r->q_out)))) return FAK_ERR_INVALID_ARG;
+  if (r->rot && !r->rope) return FAK_ERR_INVALID_ARG;
   if (!(r->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
   // vectors on 16-byte boundaries: 4 f32 or 8 bf16 elements
   const int64_t m = r->type == FAK_ROWS_F32 ? 3 : 7;
@@ -440,7 +441,7 @@ extern "C" int fak_kv_read(const fak_kv_cache* cache, const fak_kv_batch* batch,
   memset(&p, 0, sizeof(p));
   int st = kv_view(cache, batch, &p.c);
   if (st != FAK_OK) return st;
-  if ((type != FAK_ROWS_F32 && type != FAK_ROWS_BF16) || (!k_out && !v_out)) return FAK_ERR_INVALID_ARG;
+  if ((type != FAK_ROWS_F32 && type != FAK_ROWS_BF16) || (rows && !k_out && !v_out)) return FAK_ERR_INVALID_ARG;
   if (rows < 0 || rows > 0x7fffffff || cache->n_kv > 65535 * (kReadVec / 2)) return FAK_ERR_SHAPE;
   if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return FAK_ERR_ALIGN;
   if (rows == 0 || batch->n_seqs == 0) return FAK_OK;

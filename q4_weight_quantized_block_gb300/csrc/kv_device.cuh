@@ -114,10 +114,11 @@ static inline int kv_view(const fak_kv_cache* c, const fak_kv_batch* b, KvView* 
   if (c->kind != FAK_KV_BF16 && c->kind != FAK_KV_E4M3 && c->kind != FAK_KV_I8) return FAK_ERR_INVALID_ARG;
   const bool quant = c->kind != FAK_KV_BF16;
   if (!c->k || !c->v || (quant && (!c->k_scale || !c->v_scale))) return FAK_ERR_INVALID_ARG;
-  if (!b->page_table || !b->row_start || !b->kv_len) return FAK_ERR_INVALID_ARG;
+  const bool none = b->n_seqs == 0;  // (an empty tensor has no address)
+  if (!none && (!b->page_table || !b->row_start || !b->kv_len)) return FAK_ERR_INVALID_ARG;
   if ((c->dh != 64 && c->dh != 128 && c->dh != 256) || c->page < 16 || c->page > 256 || (c->page & (c->page - 1)))
     return FAK_ERR_SHAPE;
-  if (c->n_kv < 1 || c->n_pages < 1 || c->n_pages >= (1LL << 31) || b->n_seqs < 0 || b->max_pages < 1)
+  if (c->n_kv < 1 || c->n_pages < 1 || c->n_pages >= (1LL << 31) || b->n_seqs < 0 || (!none && b->max_pages < 1))
     return FAK_ERR_SHAPE;
   if (c->n_kv >= (1LL << 31) / c->page / c->n_pages) return FAK_ERR_SHAPE;  // n_pages * n_kv * page < 2^31
   const uintptr_t bits = (uintptr_t)c->k | (uintptr_t)c->v;

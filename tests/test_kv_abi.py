@@ -287,3 +287,19 @@ def test_wait_hooks(fak):
     hook = fak.lib.fak_paged_attn_debug_wait
     assert hook(-1, 0) == 1 and hook(0, 2) == 1 and hook(0, -1) == 1
     assert hook(10**9, 0) == 0 and hook(0, 0) == 0
+
+
+def test_empty_tensors_have_no_address(fak):
+    """A step without rows, or without sequences: torch gives empty tensors the address 0."""
+    c, b, r, a = structs()
+    r.rows = a.rows = 0
+    r.k = r.v = r.q = r.q_out = a.q = a.out = a.gate = None
+    assert calls(fak)["append"](c, b, r, a) == 0 and calls(fak)["attn"](c, b, r, a) == 0
+    assert fak.lib.fak_kv_read(ref(c), ref(b), 0, 1, None, None, None) == 0
+    c, b, r, a = structs()
+    b.n_seqs = 0
+    b.page_table = b.kv_len = None
+    b.max_pages = 0
+    assert all(call(c, b, r, a) == 0 for call in calls(fak).values())
+    b.n_seqs = 1  # (only then)
+    assert all(call(c, b, r, a) == 1 for call in calls(fak).values())

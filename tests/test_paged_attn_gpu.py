@@ -433,3 +433,16 @@ def test_a_wait_that_runs_out_is_recorded_and_ends(fak, kind, new, total):
     s.out.fill_(9.0)
     s.run(workspace=ws)
     s.check()
+
+
+@pytest.mark.parametrize("n_seqs", [0, 2])
+def test_a_step_without_rows(fak, n_seqs):
+    cache, mem = _kv.empty_cache(fak, "i8", 4, 2, 16, 64)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    batch = fak.KVBatch(i32(n_seqs, 3), i32(n_seqs + 1), i32(n_seqs))
+    x, q = torch.empty(0, 2, 64, device="cuda"), torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    fak.fak_kv_append(cache, batch, x, x, q=torch.empty(0, 4, 64, device="cuda"), q_out=q)
+    fak.fak_kv_read(cache, batch, x, x)
+    n = fak.fak_paged_attn_workspace_bytes(cache, batch, 4, 0, 0, 0)
+    fak.fak_paged_attn(cache, batch, q, torch.empty_like(q), 0, 0, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+    assert fak.fak_device_status() == 0
