@@ -194,10 +194,14 @@ __global__ void __launch_bounds__(kKvThreads, V * DH == 1024 ? 3 : 1) kv_append_
   if (pos < 0) return;  // padding
   const int half = p.rot / 2;
   if (threadIdx.x < half) {
-    const long long turns = (long long)(p.rope[threadIdx.x] * (uint64_t)pos);
+    // the nearest quarter of a turn goes first, so that f32 rounds an eighth at most: 2^-27 half turns, and small sines
+    // and cosines are as good at every quarter as at none
+    const uint64_t turn = p.rope[threadIdx.x] * (uint64_t)pos;
+    const uint64_t quarter = (turn + (1ull << 61)) >> 62;
     float sn, co;
-    sincospif((float)turns * 1.0842021724855044e-19f, &sn, &co);  // 2^-63: in half turns
-    cs[threadIdx.x] = make_float2(co, sn);
+    sincospif((float)(long long)(turn - (quarter << 62)) * 1.0842021724855044e-19f, &sn, &co);  // 2^-63: in half turns
+    const float c = quarter & 1 ? -sn : co, s = quarter & 1 ? co : sn;
+    cs[threadIdx.x] = quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
   }
   if (half) __syncthreads();
   // this lane's sines and cosines, and where its rotary partners are; the gains stay while the vectors are of one kind

@@ -284,3 +284,31 @@ def test_a_bad_start_leaves_out_its_own_sequences_only(fak, n, new, bad):
     assert torch.equal(got[ok], x[ok].to(torch.bfloat16).float()) and torch.equal(got[left], old[left].to(torch.bfloat16).float())
     assert torch.equal(q_out[ok], q[ok].to(torch.bfloat16))
     assert bool((q_out[left] == 9.0).all()) and bool((q_out[n * new:] == 9.0).all())
+
+
+def test_rope_near_whole_quarters_of_a_turn(fak):
+    """The rotation of (1, 0) is (cos, sin): next to a multiple of a quarter turn one of them is small, and as good as it
+    would be next to zero.  An angle less the quarters is off by 2^-24 of itself, a sine or cosine by 2 units in the last
+    place, 2^-22 of itself; the result is rounded to bf16, 2^-8 of itself."""
+    dh, n_kv, rows = 64, 1, 9
+    g = torch.Generator().manual_seed(5)
+    # fractions of a turn: quarters plus up to 2^-10 .. 2^-30 of a turn, as 64-bit integers that wrap
+    off = (torch.rand(32, generator=g, dtype=torch.float64) - 0.5) * 2.0 ** (54 - torch.arange(32, dtype=torch.float64) % 21)
+    turn = off.round().to(torch.int64) + ((torch.arange(32, dtype=torch.int64) % 4) << 62)
+    table, start, kv_len, _, n_pages = _kv.batch_tensors([(rows, rows)], 16)
+    cache, mem = _kv.empty_cache(fak, "bf16", n_pages, n_kv, 16, dh)
+    k = torch.zeros(rows, n_kv, dh, device="cuda")
+    k[..., :32] = 1.0
+    fak.fak_kv_append(cache, fak.KVBatch(table, start, kv_len), k, k.clone(), rope=turn.cuda(), rot=64)
+    assert fak.fak_device_status() == 0
+    (r, pg, sl), = _kv.places(table, start, kv_len, 16)
+    got, _ = _kv.held(mem, "bf16", pg, sl)
+    angle = turn * torch.arange(rows)[:, None]  # wraps at whole turns
+    quarter = (angle + (1 << 61)) >> 62
+    rest = (angle - (quarter << 62)).double() * (2.0 * math.pi / 2.0**64)
+    c, s = torch.cos(rest), torch.sin(rest)
+    q = quarter % 4
+    cos = torch.where(q == 0, c, torch.where(q == 1, -s, torch.where(q == 2, -c, s)))
+    sin = torch.where(q == 0, s, torch.where(q == 1, c, torch.where(q == 2, -s, -c)))
+    want = torch.cat([cos, sin], -1)[:, None].cuda()
+    _kv.check(got, want, (2.0**-8 + 2.0**-22) * want.abs(), "cosines and sines")
