@@ -157,14 +157,23 @@ FAK_DEV void put_vector(uint8_t* codes, float* scales, int64_t at, const float (
   }
 }
 
+// Blocks on an SM, as many as the registers of a row's own path leave (0: as the compiler has it): the search that only
+// bad numbers need must not take more.  (Left alone it takes 104 where 80 do at dh 256, and 8 ragged chunks of 1,024 rows
+// 60 us, not 48; bf16 at dh 128 76.7 us, not 72.5; 8-bit at dh 64 is faster left alone, 51.4 us and 53.8.)
+constexpr int append_blocks(int dh, int kind, int v, int bytes) {
+  if (v == 1) return 0;
+  if (dh == 256) return 3;
+  if (dh == 128) return kind == FAK_KV_BF16 && bytes == 4 ? 5 : 4;
+  return kind == FAK_KV_BF16 ? 7 : 0;
+}
+
 // Block (x, y): row x, vectors [y * 8 V, +8 V) of its nq queries, n_kv keys and n_kv values, V to a
 // warp with all their loads in flight before the first is used.  The row's rotary sines and cosines
 // are made once for the block, from 64-bit fractions of a turn: position * frequency wraps at whole
 // turns by itself, so the angle is as good at position 2^30 as at 1.
-// Four vectors of 256 to a warp: three blocks to an SM, with 80 registers.  (Left alone the compiler takes 104 for the
-// search that bad numbers alone need, and 8 chunks of 1,024 rows 60 us in place of 48.)
 template <int DH, int KIND, int V, typename T>
-__global__ void __launch_bounds__(kKvThreads, V * DH == 1024 ? 3 : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kKvThreads, append_blocks(DH, KIND, V, sizeof(T)))
+    kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = DH / 32;
   __shared__ float2 cs[128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(kKvThreads, V * DH == 1024 ? 3 : 1) kv_append_
   }
   int s;
   KvSeq q = kv_locate(p.c, row, lane, s);
-  if (!kv_has(q, row)) {
+  if (!__any_sync(0xffffffffu, kv_has(q, row))) {  // (all lanes or none)
     bool bad;
     q = kv_locate_all(p.c, row, lane, s, bad);
     if (bad && threadIdx.x == 0) kv_record();
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_consta
   if (row >= p.c.rows) return;
   int s;
   KvSeq q = kv_locate(p.c, row, lane, s);
-  if (!kv_has(q, row)) {
+  if (!__any_sync(0xffffffffu, kv_has(q, row))) {  // (all lanes or none)
     bool bad;
     q = kv_locate_all(p.c, row, lane, s, bad);
     if (bad && lane == 0) kv_record();
