@@ -438,7 +438,8 @@ void fak_prefill_destroy(fak_prefill* ctx);
  * layers' chunks of new tokens and batches of single tokens (the one-launch decode
  * above keeps its own f32 cache of one sequence).  A cache holds, for keys and for
  * values, codes [n_pages][n_kv][page][dh] and, in the 8-bit kinds, one f32 scale
- * per vector [n_pages][n_kv][page]; a cached vector is code * scale.
+ * per vector [n_pages][n_kv][page]; a cached vector is code * scale.  No scale is
+ * negative.
  *   FAK_KV_BF16: codes are the vector rounded to bf16; no scales (NULL).
  *   FAK_KV_E4M3: a = max|x|, scale = a / 448, code = e4m3(x * (448 / a)).
  *   FAK_KV_I8:   scale = a / 127, code = rint(x * (127 / a)), int8.

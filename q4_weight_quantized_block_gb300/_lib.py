@@ -260,6 +260,8 @@ def fak_device_status(stream=None):
 
 
 # ------------------------------------------------------------------ paged KV cache and attention
+# The kernels run on the current device and read what they are given there: every call looks whether all of it is on that
+# device, and nothing on the host (whose tensors' device is -1).
 def _current_device():
     """torch's current CUDA device; as _current_stream."""
     global _current_device
@@ -276,22 +278,10 @@ def _one_device(where, tensors):
     return tensors[0].get_device()
 
 
-def _on_device(where, cache, batch, *tensors):
-    """The kernels run on the current device and read there: everything has to be on it, and nothing on the host."""
-    device = cache.device
-    if device < 0 or batch.device != device:
-        raise FakError(8, where)
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise FakError(8, where)
-    if _current_device() != device:
-        raise FakError(8, where)
-
-
 class KVCache:
     """A paged cache's description: codes k, v [n_pages, n_kv, page, dh] (contiguous; bfloat16, or for e4m3 uint8 or
-    float8_e4m3fn, for int8 int8 or uint8) and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors alive.  Calls on tensors of the host or of
-    another device than the current one are refused (FAK_ERR_UNSUPPORTED)."""
+    float8_e4m3fn, for int8 int8 or uint8) and in the 8-bit kinds scales [n_pages, n_kv, page] f32.  Keeps the tensors
+    alive.  Calls on tensors of the host or of another device than the current one are refused (FAK_ERR_UNSUPPORTED)."""
 
     def __init__(self, kind, k, v, k_scale=None, v_scale=None):
         import torch
@@ -337,6 +327,15 @@ def _float_types():
     return types
 
 
+def _index_types():
+    """torch's 64-bit integers."""
+    global _index_types
+    import torch
+    types = torch.int64, torch.uint64
+    _index_types = lambda: types
+    return types
+
+
 def _heads(t, heads, dh, dtype, where):
     """Pointer, row stride and head stride of rows [rows, heads, dh] with neighbouring values in a head."""
     shape, stride = t.shape, t.stride()
@@ -362,7 +361,7 @@ def _rope(table, rot, where):
     """Pointer of a rotary table: 64-bit integers, rot / 2 or more of them."""
     if table is None:
         return None
-    if table.element_size() != 8 or table.is_floating_point() or table.is_complex() or not table.is_contiguous():
+    if table.dtype not in _index_types() or not table.is_contiguous():
         raise FakError(1, where)
     if 2 * table.numel() < rot:
         raise FakError(2, where)
@@ -393,7 +392,14 @@ def fak_kv_append(cache, batch, k, v, q=None, q_out=None, q_norm_w=None, k_norm_
     r = KvRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nq, rot, eps, k.shape[0], qp, kp, vp, qr, qh, kr, kh, vr,
                vh, _gain(q_norm_w, cache.dh, f32, "fak_kv_append"), _gain(k_norm_w, cache.dh, f32, "fak_kv_append"),
                _rope(rope, rot, "fak_kv_append"), _ptr(q_out))
-    _on_device("fak_kv_append", cache, batch, k, v, q, q_out, q_norm_w, k_norm_w, rope)
+    # (written out: these calls are bound by the host where rows are few)
+    d = cache.device
+    if (d < 0 or batch.device != d or k.get_device() != d or v.get_device() != d
+            or (q is not None and (q.get_device() != d or q_out.get_device() != d))
+            or (q_norm_w is not None and q_norm_w.get_device() != d)
+            or (k_norm_w is not None and k_norm_w.get_device() != d)
+            or (rope is not None and rope.get_device() != d) or _current_device() != d):
+        raise FakError(8, "fak_kv_append")
     _check(lib.fak_kv_append(cache.ref, batch.ref, ctypes.addressof(r), _stream(stream)), "fak_kv_append")
 
 
@@ -406,7 +412,9 @@ def fak_kv_read(cache, batch, k_out, v_out, stream=None):
     if any(t.dim() != 3 or t.shape[1:] != (cache.n_kv, cache.dh) or t.shape[0] != outs[0].shape[0] for t in outs):
         raise FakError(2, "fak_kv_read")
     kind = FAK_ROWS_F32 if outs[0].element_size() == 4 else FAK_ROWS_BF16
-    _on_device("fak_kv_read", cache, batch, *outs)
+    d = cache.device
+    if d < 0 or batch.device != d or any(t.get_device() != d for t in outs) or _current_device() != d:
+        raise FakError(8, "fak_kv_read")
     _check(lib.fak_kv_read(cache.ref, batch.ref, outs[0].shape[0], kind, _ptr(k_out), _ptr(v_out), _stream(stream)),
            "fak_kv_read")
 
@@ -430,7 +438,11 @@ def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, si
     a = AttnArgs(nq, window, sinks, max_q, max_kv, cache.dh ** -0.5 if scale is None else scale, q.shape[0], qp, qr, qh,
                  gp, gr, gh, op, orow, oh, _ptr(workspace),
                  0 if workspace is None else workspace.numel() * workspace.element_size())
-    _on_device("fak_paged_attn", cache, batch, q, out, gate, workspace)
+    d = cache.device
+    if (d < 0 or batch.device != d or q.get_device() != d or out.get_device() != d
+            or (gate is not None and gate.get_device() != d)
+            or (workspace is not None and workspace.get_device() != d) or _current_device() != d):
+        raise FakError(8, "fak_paged_attn")
     _check(lib.fak_paged_attn(cache.ref, batch.ref, ctypes.addressof(a), _stream(stream)), "fak_paged_attn")
 
 

@@ -131,7 +131,7 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   if (pl.few) {
     // One sequence's pieces are all alike: as many as blocks fit at once.  Several sequences differ in length, which
     // smaller pieces even out: four times as many, of 512 keys or more.  (64 of up to 8,191 e4m3 keys of 256, in pieces
-    // of 512 keys 157 us, of 1,024 130, of 2,048 144, whole 218.)
+    // of 512 keys 157 us, of 1,024 130, of 2,048 144, whole 218; measured on this batch alone.)
     const int64_t places = rows_blocks(c->kind != FAK_KV_BF16, c->dh, (int)rows) * kPlanSms, least = 512 / pl.tile;
     const int64_t four = std::max<int64_t>(1, 4 * places / busy), one = std::max<int64_t>(1, places / busy);
     int64_t per = std::max<int64_t>(least, (tiles + four - 1) / four);
@@ -142,7 +142,9 @@ Plan make_plan(const fak_kv_cache* c, const fak_kv_batch* b, const fak_attn_args
   }
   // The cut that is over soonest if every block saw all `tiles`: waves of blocks over the SMs, each as long as a piece
   // and the time of about three tiles to begin and to end, seven where it leaves its sums in memory, and four more for
-  // the join.  (512 rows after 8,191 keys of 256: whole 105 us, in two 127, in four 120; after 30,000: 313, 333, 277.)
+  // the join.  (512 rows after 8,191 keys of 256: whole 105 us, in two 127, in four 120; after 30,000: 313, 333, 277.
+  // The three times are from this form alone, bf16 at dh 256; other forms' tiles take 0.8 to 1.3 times as long, and
+  // theirs were not measured.)
   int64_t best = -1;
   for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
     const int64_t per = (tiles + s - 1) / s, n = (tiles + per - 1) / per;

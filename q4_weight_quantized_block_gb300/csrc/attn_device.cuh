@@ -82,13 +82,16 @@ FAK_DEV bool keys_cut(int p_lo, int p_hi, int j0, int j1, int window, int sinks)
   return !(j1 <= p_lo && (!window || j0 > p_hi - window || j1 < sinks));
 }
 
+// Weights' exponentials take one instruction, off by 2^-22 of the result, where rounding the weight to bf16 or f16 may
+// be off by 2^-8 or 2^-11.  Results below 2^-126 are zero.
 FAK_DEV float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// y * sigmoid(x); x = infinity: y
+// y * sigmoid(x); x = infinity: y.  The fast forms, off by some 2^-21, where the result is rounded to bf16 at once
+// (below x = -87 a sigmoid of 2^-126 and less counts as zero).
 FAK_DEV float gated_by(float y, float x) { return __fdividef(y, 1.0f + __expf(-x)); }
 
 FAK_DEV uint32_t pack_bf16(float a, float b) {

@@ -23,7 +23,8 @@
 //
 // Bound: bf16 by memory, 64 x 8,191 keys in 202 us, 6.1 TB/s (the copies alone 189); 8-bit by the instructions of the
 // conversion, the same in e4m3 130 us, 4.9 TB/s (the copies alone 104); few keys by the launches and one block's chain
-// of loads.
+// of loads.  9 to 16 rows (255 registers, two blocks an SM): 64 sequences' two tokens over 4,000 keys in 187 us in bf16,
+// 5.6 TB/s, 173 in e4m3, 175 in int8, 3.1.
 // Each row's maximum moves only when passed by 8, as in the blocks' kernel (attn_tile.cu).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -107,6 +108,8 @@ FAK_DEV uint32_t pack_f16(float a, float b) {
 // With m the exponents' maximum less 7, the largest weight (times its value's scale) is 2^7 to 2^15: f16 keeps 11 bits of
 // those down to 2^-14, and half a step of 2^-24 below, 2^-32 of the largest.
 
+// (a value's scale in its weight's exponent: off by 2^-22 at scales near 1, by 2^-18 at the exponent's ends, as the sum of
+// the two is rounded there too)
 FAK_DEV float log2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -26,6 +26,8 @@
 //   warps 12-19    for an 8-bit cache, codes to bf16, four warps K's and four V's: the copies land in rings of their own
 //                  and they fill the MMAs' rings from them (12-15, for a bf16 cache: V of the tiles that a mask cuts
 //                  is mended)
+// Weights are rounded to bf16, off by 2^-8 of themselves at most: that is V's type, and a weight is A to V's B.  (8-bit
+// codes could be f16, which would keep weights to 2^-11 but wants a base that holds the values' scales, as few rows have.)
 // S has two or three buffers, so the next tile's S = Q K^T runs while the softmax works.
 // 8-bit codes become bf16 exactly; their scales multiply the scores' columns and the weights instead.
 // A weight of zero times a value that is not finite would be NaN, so in the tiles that a mask cuts a bf16 V is
@@ -33,10 +35,10 @@
 // finite, which the rows that do see them get added at the end.  (Codes are always finite, and a weight of zero is not
 // multiplied by a scale.)  Scores of masked keys are replaced, whatever they are.
 //
-// A prompt of 8,192 tokens, 24 query and 4 KV heads of 256, in bf16: 594 us, 1.39 PFLOP/s, under the power limit's
-// clocks (526 us, 1.57, from a rest); 512 tokens after 7,680 keys 100 us.  Heads of 128 are bound by the softmax warps,
+// A prompt of 8,192 tokens, 24 query and 4 KV heads of 256, in bf16: 594 to 620 us, 1.33 to 1.39 PFLOP/s, under the power
+// limit's clocks (527 us, 1.56, from a rest); 512 tokens after 7,680 keys 98 us.  Heads of 128 are bound by the softmax warps,
 // whose phases (scores, maximum, exponents) follow one another; 8-bit codes by those warps' scales and the conversion
-// beside them: 8 x 1,024 tokens after 4,001 keys in bf16 613 us, in e4m3 931, with no unit above 45% busy.
+// beside them: 8 x 1,024 tokens after 4,001 keys in bf16 611 us, in e4m3 927, with no unit above 45% busy.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
