@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512) attn_join_kernel(const __g
   for (int i = lane; i < pieces; i += 32) top = fmaxf(top, p.stat[slot + i * step].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float zero = top == -INFINITY ? 0.0f : top;
+  // (2^12 above the largest: there are fewer pieces, so pieces as large as f32 holds do not add up beyond it)
+  const float zero = top == -INFINITY ? 0.0f : top + 12.0f;
   float o[N] = {}, l = 0.0f;
   constexpr int U = 4;  // pieces in flight
   for (int i0 = warp % W; i0 < pieces; i0 += U * W) {

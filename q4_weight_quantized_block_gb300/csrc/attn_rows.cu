@@ -653,15 +653,15 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
     for (int w = 0; w < kWarps; ++w) sum = fmaf(exp2_approx(sb[w][r] - base), sl[w][r], sum);
     // what the sums are multiplied with.  8-bit: it goes into the factors of O, which holds the values' scales: these
     // factors are taken in two halves, as one may be beyond f32 where their product with O is not, and a piece has the
-    // whole powers of two of its weights' sum in its base, so that large values do not add up beyond f32
+    // whole powers of two of its weights' sum in its base, which leaves a half to 1: it is no larger than its values
     float inv = 1.0f;
     if (direct) {
       inv = 1.0f / sum;
     } else if (C::quant && sum > 0.0f && sum < INFINITY) {  // (at least 2^-8 then)
       const uint32_t e = __float_as_uint(sum) & 0x7f800000u;
-      inv = __uint_as_float(0x7f000000u - e);
+      inv = __uint_as_float(0x7e800000u - e);
       sum *= inv;
-      top += (float)((int)(e >> 23) - 127);
+      top += (float)((int)(e >> 23) - 126);
     }
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll

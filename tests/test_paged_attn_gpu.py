@@ -446,3 +446,15 @@ def test_a_step_without_rows(fak, n_seqs):
     n = fak.fak_paged_attn_workspace_bytes(cache, batch, 4, 0, 0, 0)
     fak.fak_paged_attn(cache, batch, q, torch.empty_like(q), 0, 0, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
     assert fak.fak_device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("new,total", [(1, 90), (2, 3000), (1, 60000)])
+def test_values_at_the_top_of_f32(fak, kind, new, total):
+    """Every value 3e38 in size: their mean is too, whatever number of keys, warps and pieces is added up."""
+    def edit(K, V):
+        sign = torch.where(V[0][:1] < 0, -1.0, 1.0)
+        V[0].copy_((sign * 3e38).expand_as(V[0]))
+
+    case(fak, kind, 4, 2, 128, 16, [(new, total)], seed=26, edit=edit)
+    case(fak, kind, 6, 1, 256, 16, [(new, total)], seed=27, edit=edit)
