@@ -107,9 +107,8 @@ FAK_DEV uint32_t pack_f16(float a, float b) {
 
 // With m the exponents' maximum less 7, the largest weight (times its value's scale) is 2^7 to 2^15: f16 keeps 11 bits of
 // those down to 2^-14, and half a step of 2^-24 below, 2^-32 of the largest.
-
-// (a value's scale in its weight's exponent: off by 2^-22 at scales near 1, by 2^-18 at the exponent's ends, as the sum of
-// the two is rounded there too)
+// The logarithm puts a value's scale in its weight's exponent: off by 2^-22 at scales near 1, by 2^-18 at the exponent's
+// ends, as the sum of the two is rounded there too.
 FAK_DEV float log2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -443,7 +442,8 @@ __global__ void __launch_bounds__(kWarps * 32, RCfg<DH, KIND, NT>::blocks)
 #pragma unroll
       for (int d = 0; d < DH / 16; ++d) {
         // o[nt][d]: dims ve g + 2 (d % (ve / 2)), + 1 of block d / (ve / 2)
-        const uint32_t y = *reinterpret_cast<const uint16_t*>(v + d / (C::ve / 2) * 8 * C::ve + g * C::ve + 2 * (d % (C::ve / 2)));
+        const uint32_t y =
+            *reinterpret_cast<const uint16_t*>(v + d / (C::ve / 2) * 8 * C::ve + g * C::ve + 2 * (d % (C::ve / 2)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

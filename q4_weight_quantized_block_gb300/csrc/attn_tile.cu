@@ -36,8 +36,8 @@
 // multiplied by a scale.)  Scores of masked keys are replaced, whatever they are.
 //
 // A prompt of 8,192 tokens, 24 query and 4 KV heads of 256, in bf16: 594 to 620 us, 1.33 to 1.39 PFLOP/s, under the power
-// limit's clocks (527 us, 1.56, from a rest); 512 tokens after 7,680 keys 98 us.  Heads of 128 are bound by the softmax warps,
-// whose phases (scores, maximum, exponents) follow one another; 8-bit codes by those warps' scales and the conversion
+// limit's clocks (527 us, 1.56, from a rest); 512 tokens after 7,680 keys 98 us.  Heads of 128 are bound by the softmax
+// warps, whose phases (scores, maximum, exponents) follow one another; 8-bit codes by those warps' scales and the conversion
 // beside them: 8 x 1,024 tokens after 4,001 keys in bf16 611 us, in e4m3 927, with no unit above 45% busy.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -8,9 +8,9 @@
 // lanes away because rot is a multiple of 16.
 //
 // Bound by memory where rows are many: 8 chunks of 1,024 f32 rows of 24 + 4 + 4 heads of 256 written in 72 us as bf16,
-// 5.6 TB/s, and in 83 us as e4m3, 4.6; 16 sequences of up to 8,192 int8 vectors of 4 + 4 heads read in 63 us, 6.2 TB/s.  Every load of a warp is asked for
-// before the first is used, and a block lives for one row: with blocks of two vectors a warp, or registers for more
-// blocks, writes took 1 to 17% longer.  Few rows: bound by the launch.
+// 5.6 TB/s, and in 83 us as e4m3, 4.6; 16 sequences of up to 8,192 int8 vectors of 4 + 4 heads read in 63 us, 6.2 TB/s.
+// Every load of a warp is asked for before the first is used, and a block lives for one row: with blocks of two vectors
+// a warp, or registers for more blocks, writes took 1 to 17% longer.  Few rows: bound by the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
