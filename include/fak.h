@@ -562,9 +562,112 @@ int fak_paged_attn(const fak_kv_cache* cache, const fak_kv_batch* batch, const f
  * the default), and with unreachable = 1 a wait that can never complete. */
 int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable);
 
+/* ------------------------------------------------------------------ Gated DeltaNet layers on ragged batches
+ * The GDN layer's body (the mixer above) for many sequences at once and for any number of
+ * new rows of each: single tokens, drafted tokens, chunks and whole prompts, mixed in one
+ * call.  Key and value heads of 128; a sequence's state is a place ("slot") of two pools
+ * that the caller keeps: the last three inputs of the convolution, [n_slots][3][(2 nk +
+ * nv) 128] f32, newest last, and S, [n_slots][nv][128 (key)][128 (value)] f32.
+ *
+ * A ragged batch, in device memory, read when the kernels run.  Rows and positions as in
+ * fak_kv_batch: rows row_start[s] .. row_start[s+1]-1 are sequence s's, the last of its
+ * kv_len[s] positions; rows at negative positions are padding, rows from row_start[n_seqs]
+ * on belong to no sequence.  A sequence whose first new row stands at position 0 begins
+ * with an empty state (what its slot holds is not read); any other goes on with its
+ * slot's.  Its slot is left with the state behind its last row; a sequence without new
+ * rows leaves its slot as it was.  Two sequences of one call in one slot race.  A sequence
+ * whose numbers are out of range (row_start as in fak_kv_batch, kv_len negative, slot
+ * outside [0, n_slots)) is left out: nothing of it is read or written, and FAK_ERR_DEVICE
+ * is recorded. */
+typedef struct {
+    int32_t n_seqs;
+    const int32_t* row_start; /* device [n_seqs + 1] */
+    const int32_t* kv_len;    /* device [n_seqs], with the new rows */
+    const int32_t* slot;      /* device [n_seqs] */
+} fak_gdn_batch;
+
+/* fak_gdn_conv: from the input projection's rows to what the linear attention takes:
+ *   c_t = silu(sum_j conv_w[.][j] x_{t-3+j});  its channels are nk queries, nk keys, nv values of 128;
+ *   q, k = c / sqrt(sum c^2 + eps) per head, to f16 (no value is above 1: f16 holds them three bits finer
+ *   than bf16); v = c, to bf16;  beta = sigmoid(b),  g = -exp(a_log) softplus(a + dt_bias), f32.
+ * x, b and a are f32 or bf16 rows with strides (slices of a fused projection need no copy), loaded four values at a
+ * time where every row of x stands on a multiple of four elements.  All sums are f32.  Padding rows and rows of no sequence
+ * are left as they were.  One launch. */
+typedef struct {
+    int32_t type;               /* of x, b and a: FAK_ROWS_F32 or FAK_ROWS_BF16 */
+    int32_t nk, nv;             /* key heads, value heads */
+    int32_t n_slots;            /* of conv_state */
+    float eps;
+    int64_t rows;
+    const void *x, *b, *a;      /* device [rows][(2 nk + nv) 128], [rows][nv], [rows][nv] */
+    int64_t x_row, b_row, a_row; /* elements */
+    const float *conv_w, *a_log, *dt_bias; /* device [(2 nk + nv) 128][4], 16-byte aligned; [nv]; [nv] */
+    float* conv_state;          /* device [n_slots][3][(2 nk + nv) 128], 16-byte aligned */
+    void *q, *k, *v;            /* device f16 [rows][nk][128], f16 [rows][nk][128], bf16 [rows][nv][128], 16-byte aligned */
+    float *g, *beta;            /* device [rows][nv] */
+} fak_gdn_rows;
+int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_stream_t stream);
+
+/* fak_gdn_attn: the gated delta rule, linear attention with a decay for each head.  Per value head h, with key
+ * head h / (nv / nk), over a sequence's rows in order:
+ *   S = exp(g) S;  S += k (beta (v - S^T k))^T;  o = scale S^T q;
+ *   if norm_w: o = o / sqrt(mean o^2 + eps) * norm_w;  if z: o = o * silu(z).
+ * Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and 0 <= beta <= 2, g <= 0: beyond
+ * that the rule itself grows without bound, and a result may be an infinity or NaN before its f32 form is.
+ * State, products with it and sums are f32 (of prompts: products of 22 significand bits, sums of f32); out is
+ * rounded once.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds reaches
+ * its own sequence alone.  Deterministic. */
+typedef struct {
+    int32_t nk, nv;             /* key heads, value heads, nv a multiple of nk */
+    int32_t max_q;              /* bound on the sequences' rows; a sequence above it is left out, recorded */
+    int32_t out_type;           /* FAK_ROWS_F32 or FAK_ROWS_BF16 */
+    int32_t n_slots;            /* of state */
+    float scale, eps;           /* scale > 0 */
+    int64_t rows;
+    const void *q, *k;          /* device f16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned, strides too */
+    const void* v;              /* device bf16, same form */
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const float *g, *beta;      /* device [rows][nv] */
+    float* state;               /* device [n_slots][nv][128][128], 16-byte aligned */
+    const float* norm_w;        /* device [128], 16-byte aligned; NULL: no norm */
+    const float* z;             /* device f32, any strides (wide loads where vectors stand on 16 bytes); NULL: no gate */
+    int64_t z_row, z_head;
+    void* out;                  /* device, same form, 16-byte aligned */
+    int64_t out_row, out_head;
+} fak_gdn_args;
+int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* args, fak_stream_t stream);
+
+/* ------------------------------------------------------------------ norms around a block
+ * What stands between one block's output and the next block's input, in one pass over a row of d values:
+ *   y' = y;  if post_norm: y' = y / sqrt(mean y^2 + eps) * (gain_offset + y_w)
+ *   if gate: y' = y' * gate, or * sigmoid(gate);   h += scale * y'
+ *   n = h / sqrt(mean h^2 + eps) * (gain_offset + w)
+ * in f32 (n from h before h's own rounding), each result rounded once.  gain_offset is 0, or 1 for gains
+ * stored as w - 1; a NULL gain is a gain of 1, whatever the offset.  y NULL: h stays as it is (and is not
+ * written), n is its norm; n NULL: no norm.  gate is f32: one value for each value, channel or row, by strides
+ * (gate_row, gate_col; a stride of 0 repeats).  h, y, n and gate do not overlap.
+ * d is 1 to 32768.  Rows whose starts and strides are multiples of 16 bytes (and d of 4) take wide loads;
+ * any others are as right.  One launch. */
+enum { FAK_GATE_LINEAR = 0, FAK_GATE_SIGMOID = 1 };
+typedef struct {
+    int32_t h_type, y_type, n_type; /* FAK_ROWS_F32 or FAK_ROWS_BF16 */
+    int32_t d, post_norm, gate_kind;
+    float scale, eps, gain_offset;
+    int64_t rows;
+    void* h;                        /* device [rows][d] */
+    const void* y;
+    void* n;
+    int64_t h_row, y_row, n_row;    /* elements */
+    const float *w, *y_w;           /* device [d] */
+    const float* gate;
+    int64_t gate_row, gate_col;     /* gate_col 0 or 1 */
+} fak_norm_args;
+int fak_residual_norm(const fak_norm_args* args, fak_stream_t stream);
+
 /* ------------------------------------------------------------------ status
  * Synchronizes `stream`, then reads and clears the status word shared by the
- * stateless calls (GEMV, batched GEMV, MLP, GEMM, paged KV cache and attention). */
+ * stateless calls (GEMV, batched GEMV, MLP, GEMM, paged KV cache and attention,
+ * Gated DeltaNet operators). */
 int fak_device_status(fak_stream_t stream);
 
 #ifdef __cplusplus

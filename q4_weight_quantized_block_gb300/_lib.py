@@ -22,6 +22,7 @@ FAK_DECODE_ONE_LAUNCH, FAK_DECODE_PER_MATMUL, FAK_DECODE_ONE_LAUNCH_I8X, FAK_DEC
 FAK_DECODE_PER_MATMUL_HOST_WAIT = 4
 FAK_KV_BF16, FAK_KV_E4M3, FAK_KV_I8 = 0, 1, 2
 FAK_ROWS_F32, FAK_ROWS_BF16 = 0, 1
+FAK_GATE_LINEAR, FAK_GATE_SIGMOID = 0, 1
 
 P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 
@@ -80,6 +81,33 @@ class AttnArgs(ctypes.Structure):
                 ("out", P), ("out_row", I64), ("out_head", I64), ("workspace", P), ("workspace_bytes", SZ)]
 
 
+class GdnBatchDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("row_start", P), ("kv_len", P), ("slot", P)]
+
+
+class GdnRows(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("nk", ctypes.c_int32), ("nv", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rows", I64), ("x", P), ("b", P), ("a", P), ("x_row", I64), ("b_row", I64),
+                ("a_row", I64), ("conv_w", P), ("a_log", P), ("dt_bias", P), ("conv_state", P), ("q", P), ("k", P),
+                ("v", P), ("g", P), ("beta", P)]
+
+
+class GdnArgs(ctypes.Structure):
+    _fields_ = [("nk", ctypes.c_int32), ("nv", ctypes.c_int32), ("max_q", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("rows", I64), ("q", P),
+                ("k", P), ("v", P), ("q_row", I64), ("q_head", I64), ("k_row", I64), ("k_head", I64), ("v_row", I64),
+                ("v_head", I64), ("g", P), ("beta", P), ("state", P), ("norm_w", P), ("z", P), ("z_row", I64),
+                ("z_head", I64), ("out", P), ("out_row", I64), ("out_head", I64)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("h_type", ctypes.c_int32), ("y_type", ctypes.c_int32), ("n_type", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("gain_offset", ctypes.c_float), ("rows", I64),
+                ("h", P), ("y", P), ("n", P), ("h_row", I64), ("y_row", I64), ("n_row", I64), ("w", P), ("y_w", P),
+                ("gate", P), ("gate_row", I64), ("gate_col", I64)]
+
+
 _SIGS = {
     "fak_strerror": ([I32], ctypes.c_char_p),
     "fak_version": ([], ctypes.c_char_p),
@@ -114,6 +142,9 @@ _SIGS = {
     "fak_paged_attn_workspace_bytes": ([P, P, P], SZ),
     "fak_paged_attn": ([P, P, P, P], I32),
     "fak_paged_attn_debug_wait": ([I64, I32], I32),
+    "fak_gdn_conv": ([P, P, P], I32),
+    "fak_gdn_attn": ([P, P, P], I32),
+    "fak_residual_norm": ([P, P], I32),
     "fak_prefill_create": ([ctypes.POINTER(DecodeDesc), I64, ctypes.POINTER(P)], I32),
     "fak_prefill_run": ([P, P, P, P, P], I32),
     "fak_prefill_read_hidden": ([P, P, SZ, P], I32),
@@ -449,6 +480,128 @@ def fak_paged_attn(cache, batch, q, out, max_q, max_kv, scale=None, window=0, si
 def fak_paged_attn_debug_wait(timeout_ns=0, unreachable=0):
     """Test hooks: the limit of the attention's waits (0: the default), and a wait that can never complete."""
     _check(lib.fak_paged_attn_debug_wait(int(timeout_ns), int(unreachable)), "fak_paged_attn_debug_wait")
+
+
+# ------------------------------------------------------------------ Gated DeltaNet layers, norms around a block
+class GDNBatch:
+    """A ragged batch's description for the Gated DeltaNet operators: int32 device tensors row_start [n_seqs + 1],
+    kv_len [n_seqs] (positions, with the new rows) and slot [n_seqs] (places in the pools of states), read when the
+    kernels run.  Keeps the tensors alive."""
+
+    def __init__(self, row_start, kv_len, slot):
+        import torch
+        n = slot.shape[0] if slot.dim() == 1 else -1
+        if row_start.shape != (n + 1,) or kv_len.shape != (n,):
+            raise FakError(2, "GDNBatch")
+        if any(t.dtype != torch.int32 or not t.is_contiguous() for t in (row_start, kv_len, slot)):
+            raise FakError(1, "GDNBatch")
+        self.device = _one_device("GDNBatch", (row_start, kv_len, slot))
+        self._keep = (row_start, kv_len, slot)
+        self.desc = GdnBatchDesc(n, _ptr(row_start), _ptr(kv_len), _ptr(slot))
+        self.ref = ctypes.addressof(self.desc)
+
+
+def _half_type():
+    """torch's float16."""
+    global _half_type
+    import torch
+    t = torch.float16
+    _half_type = lambda: t
+    return t
+
+
+def _whole(t, shape, dtype, where):
+    """Pointer of a contiguous tensor of this shape and type."""
+    if t.shape != shape:
+        raise FakError(2, where)
+    if t.dtype != dtype or not t.is_contiguous():
+        raise FakError(1, where)
+    return t.data_ptr()
+
+
+def _cols(t, rows, cols, dtype, where):
+    """Pointer and row stride of rows [rows, cols] with neighbouring values in a row."""
+    if t.shape != (rows, cols):
+        raise FakError(2, where)
+    if t.dtype != dtype or (t.stride(1) != 1 and cols > 1):
+        raise FakError(1, where)
+    return t.data_ptr(), t.stride(0)
+
+
+def _on_device(d, tensors, where):
+    """Whether all that are given are on CUDA device d, the current one."""
+    if d < 0 or any(t is not None and t.get_device() != d for t in tensors) or _current_device() != d:
+        raise FakError(8, where)
+
+
+def fak_gdn_conv(batch, x, b, a, conv_w, a_log, dt_bias, conv_state, q, k, v, g, beta, eps=1e-6, stream=None):
+    """x [rows, (2 nk + nv) 128], b and a [rows, nv], f32 or bf16 (views with row strides are fine); conv_w
+    [(2 nk + nv) 128, 4], a_log and dt_bias [nv], conv_state [n_slots, 3, (2 nk + nv) 128] f32; out: q, k
+    [rows, nk, 128] f16, v [rows, nv, 128] bf16, g and beta [rows, nv] f32."""
+    where, dtype, (f32, bf16), f16 = "fak_gdn_conv", x.dtype, _float_types(), _half_type()
+    if q.dim() != 3 or v.dim() != 3 or conv_state.dim() != 3:
+        raise FakError(2, where)
+    if dtype != f32 and dtype != bf16:
+        raise FakError(1, where)
+    rows, nk, nv = x.shape[0], q.shape[1], v.shape[1]
+    chans = (2 * nk + nv) * 128
+    xp, xr = _cols(x, rows, chans, dtype, where)
+    bp, br = _cols(b, rows, nv, dtype, where)
+    ap, ar = _cols(a, rows, nv, dtype, where)
+    r = GdnRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nk, nv, conv_state.shape[0], eps, rows, xp, bp, ap, xr,
+                br, ar, _whole(conv_w, (chans, 4), f32, where), _whole(a_log, (nv,), f32, where),
+                _whole(dt_bias, (nv,), f32, where), _whole(conv_state, (conv_state.shape[0], 3, chans), f32, where),
+                _whole(q, (rows, nk, 128), f16, where), _whole(k, (rows, nk, 128), f16, where),
+                _whole(v, (rows, nv, 128), bf16, where), _whole(g, (rows, nv), f32, where),
+                _whole(beta, (rows, nv), f32, where))
+    _on_device(batch.device, (x, b, a, conv_w, a_log, dt_bias, conv_state, q, k, v, g, beta), where)
+    _check(lib.fak_gdn_conv(batch.ref, ctypes.addressof(r), _stream(stream)), where)
+
+
+def fak_gdn_attn(batch, q, k, v, g, beta, state, out, max_q, scale=None, z=None, norm_w=None, eps=1e-6, stream=None):
+    """q, k [rows, nk, 128] f16, v [rows, nv, 128] bf16, z (f32) and out (f32 or bf16) as v (views with strides are fine);
+    g, beta [rows, nv] f32; state [n_slots, nv, 128, 128] f32; scale defaults to 128^-1/2."""
+    where, (f32, bf16), f16 = "fak_gdn_attn", _float_types(), _half_type()
+    if q.dim() != 3 or v.dim() != 3 or k.shape != q.shape or v.shape[0] != q.shape[0] or out.shape != v.shape or (
+            z is not None and z.shape != v.shape) or state.dim() != 4:
+        raise FakError(2, where)
+    if out.dtype != f32 and out.dtype != bf16:
+        raise FakError(1, where)
+    rows, nk, nv = q.shape[0], q.shape[1], v.shape[1]
+    qp, qr, qh = _heads(q, nk, 128, f16, where)
+    kp, kr, kh = _heads(k, nk, 128, f16, where)
+    vp, vr, vh = _heads(v, nv, 128, bf16, where)
+    op, orow, oh = _heads(out, nv, 128, out.dtype, where)
+    zp, zr, zh = (None, 0, 0) if z is None else _heads(z, nv, 128, f32, where)
+    a = GdnArgs(nk, nv, max_q, FAK_ROWS_F32 if out.dtype == f32 else FAK_ROWS_BF16, state.shape[0],
+                128 ** -0.5 if scale is None else scale, eps, rows, qp, kp, vp, qr, qh, kr, kh, vr, vh,
+                _whole(g, (rows, nv), f32, where), _whole(beta, (rows, nv), f32, where),
+                _whole(state, (state.shape[0], nv, 128, 128), f32, where), _gain(norm_w, 128, f32, where), zp, zr, zh, op,
+                orow, oh)
+    _on_device(batch.device, (q, k, v, g, beta, state, out, z, norm_w), where)
+    _check(lib.fak_gdn_attn(batch.ref, ctypes.addressof(a), _stream(stream)), where)
+
+
+def fak_residual_norm(h, y=None, n=None, w=None, post_norm=False, y_w=None, gate=None, gate_sigmoid=False, scale=1.0,
+                      eps=1e-6, gain_offset=0.0, stream=None):
+    """h, y and n [rows, d], each f32 or bf16 (views with row strides are fine); gains w and y_w [d] f32; gate f32, of h's
+    shape (expanded from one row, one column or one value too)."""
+    where, types, f32 = "fak_residual_norm", _float_types(), _float_types()[0]
+    if h.dim() != 2 or any(t is not None and t.shape != h.shape for t in (y, n, gate)):
+        raise FakError(2, where)
+    rows, d = h.shape
+    for t in (h, y, n):
+        if t is not None and (t.dtype not in types or (t.stride(1) != 1 and d > 1)):
+            raise FakError(1, where)
+    if gate is not None and (gate.dtype != f32 or (gate.stride(1) not in (0, 1) and d > 1)):
+        raise FakError(1, where)
+    kind = lambda t: FAK_ROWS_F32 if t is None or t.dtype == f32 else FAK_ROWS_BF16
+    row = lambda t: 0 if t is None else t.stride(0)
+    a = NormArgs(kind(h), kind(y), kind(n), d, int(post_norm), FAK_GATE_SIGMOID if gate_sigmoid else FAK_GATE_LINEAR, scale,
+                 eps, gain_offset, rows, _ptr(h), _ptr(y), _ptr(n), row(h), row(y), row(n), _gain(w, d, f32, where),
+                 _gain(y_w, d, f32, where), _ptr(gate), row(gate), 0 if gate is None or d == 1 else gate.stride(1))
+    _on_device(h.get_device(), (h, y, n, w, y_w, gate), where)
+    _check(lib.fak_residual_norm(ctypes.addressof(a), _stream(stream)), where)
 
 
 # ------------------------------------------------------------------ decode context

@@ -1651,7 +1651,8 @@ extern "C" int fak_device_status(fak_stream_t stream) {
   const int b = fak_bgemv_take_status();
   const int k = fak_kv_take_status();
   const int a = fak_attn_take_status();
-  for (const int st : {v, g, b, k, a})
+  const int d = fak_gdn_take_status();
+  for (const int st : {v, g, b, k, a, d})
     if (st != 0) return st;
   return FAK_OK;
 }

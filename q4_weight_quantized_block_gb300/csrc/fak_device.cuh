@@ -209,6 +209,8 @@ int fak_bgemv_take_status();
 // The same for the paged KV cache's writes and reads, and for the attention over it.
 int fak_kv_take_status();
 int fak_attn_take_status();
+// The same for the Gated DeltaNet operators.
+int fak_gdn_take_status();
 // Stream-ordered scratch for one call: from a library-owned pool per device
 // that keeps its memory for the next call (no allocation cost once warm), or,
 // while the stream is being captured into a graph, cudaMallocAsync (a graph

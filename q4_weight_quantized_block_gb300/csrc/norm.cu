@@ -1,0 +1,211 @@
+// fak_residual_norm: the norm after a block, its gate and scale, the residual sum and the norm before the next block, in
+// one pass: a block of threads holds a row in registers from its loads to its stores.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "fak.h"
+#include "fak_device.cuh"
+#include "kv_device.cuh"
+
+namespace {
+
+struct NormParams {
+  void *h, *n;
+  const void* y;
+  const float *w, *y_w, *gate;
+  int64_t h_row, y_row, n_row, gate_row, gate_col;
+  int64_t rows;
+  float scale, eps, offset;
+  int d;
+  bool h_bf16, y_bf16, n_bf16, post, sigmoid;
+};
+
+// V neighbouring values (1 or 4) of an f32 or bf16 row.
+template <int V>
+FAK_DEV void get(const void* p, bool bf16, int64_t at, float (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]) : static_cast<const float*>(p)[at];
+  } else if (bf16) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
+    x[0] = __uint_as_float(w.x << 16);
+    x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16);
+    x[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+    const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    x[0] = w.x;
+    x[1] = w.y;
+    x[2] = w.z;
+    x[3] = w.w;
+  }
+}
+
+template <int V>
+FAK_DEV void put(void* p, bool bf16, int64_t at, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    if (bf16)
+      static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(x[0]);
+    else
+      static_cast<float*>(p)[at] = x[0];
+  } else if (bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// The block's sum, the same in every thread; `red` is used once.
+FAK_DEV float block_sum(float x, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  x = lane < warps ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Block r: row r; thread t holds the values V (t + i * threads) .. + V - 1 for i < PER.  A row's loads are all asked for
+// before the first is used.
+template <int V, int PER>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[2][32];
+  const int64_t row = blockIdx.x;
+  float h[PER][V], y[PER][V], gate[PER][V];
+  bool in[PER];
+  int at[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    at[i] = V * (threadIdx.x + i * blockDim.x);
+    in[i] = at[i] < p.d;
+    if (!in[i]) continue;
+    get<V>(p.h, p.h_bf16, row * p.h_row + at[i], h[i]);
+    if (p.y) get<V>(p.y, p.y_bf16, row * p.y_row + at[i], y[i]);
+    if (p.gate) {
+      if (p.gate_col) {
+        get<V>(p.gate, false, row * p.gate_row + at[i], gate[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) gate[i][j] = p.gate[row * p.gate_row];
+      }
+    }
+  }
+  if (p.y) {
+    float r = 1.0f;
+    if (p.post) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (in[i])
+#pragma unroll
+          for (int j = 0; j < V; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+      r = rsqrtf(block_sum(ss, red[0]) / p.d + p.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!in[i]) continue;
+      float w[V];
+      const bool gain = p.post && p.y_w;
+      if (gain) get<V>(p.y_w, false, at[i], w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float x = y[i][j];
+        if (p.post) x *= r;
+        if (gain) x *= p.offset + w[j];
+        if (p.gate) x *= p.sigmoid ? 1.0f / (1.0f + expf(-gate[i][j])) : gate[i][j];
+        h[i][j] = fmaf(p.scale, x, h[i][j]);
+      }
+      put<V>(p.h, p.h_bf16, row * p.h_row + at[i], h[i]);
+    }
+  }
+  if (!p.n) return;
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (in[i])
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+  const float r = rsqrtf(block_sum(ss, red[1]) / p.d + p.eps);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (!in[i]) continue;
+    float w[V], x[V];
+    if (p.w) get<V>(p.w, false, at[i], w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = h[i][j] * r * (p.w ? p.offset + w[j] : 1.0f);
+    put<V>(p.n, p.n_bf16, row * p.n_row + at[i], x);
+  }
+}
+
+template <int V, int PER>
+cudaError_t launch(const NormParams& p, cudaStream_t s) {
+  const int units = (p.d + V - 1) / V;
+  const int threads = ((units + PER - 1) / PER + 31) / 32 * 32;
+  residual_norm_kernel<V, PER><<<(unsigned)p.rows, threads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
+  if (!a) return FAK_ERR_INVALID_ARG;
+  for (const int t : {a->h_type, a->y_type, a->n_type})
+    if (t != FAK_ROWS_F32 && t != FAK_ROWS_BF16) return FAK_ERR_INVALID_ARG;
+  if (a->gate_kind != FAK_GATE_LINEAR && a->gate_kind != FAK_GATE_SIGMOID) return FAK_ERR_INVALID_ARG;
+  if (a->d < 1 || a->d > 32768 || a->rows < 0 || a->rows > 0x7fffffff) return FAK_ERR_SHAPE;
+  if (!(a->eps >= 0.0f) || !std::isfinite(a->scale) || !std::isfinite(a->gain_offset) || (a->gate_col != 0 && a->gate_col != 1))
+    return FAK_ERR_INVALID_ARG;
+  if (a->rows && !a->h) return FAK_ERR_INVALID_ARG;
+  NormParams p;
+  memset(&p, 0, sizeof(p));
+  p.h_row = kv_stride(a->h_row, a->rows);
+  p.y_row = kv_stride(a->y_row, a->rows);
+  p.n_row = kv_stride(a->n_row, a->rows);
+  p.gate_row = kv_stride(a->gate_row, a->rows);
+  p.gate_col = a->gate_col;
+  const bool hb = a->h_type == FAK_ROWS_BF16, yb = a->y_type == FAK_ROWS_BF16, nb = a->n_type == FAK_ROWS_BF16;
+  const uintptr_t f32s = (uintptr_t)a->w | (uintptr_t)a->y_w | (uintptr_t)a->gate | (hb ? 0 : (uintptr_t)a->h) |
+                         (yb ? 0 : (uintptr_t)a->y) | (nb ? 0 : (uintptr_t)a->n);
+  const uintptr_t all = (uintptr_t)a->h | (uintptr_t)a->y | (uintptr_t)a->n;
+  if ((f32s & 3) || (all & 1)) return FAK_ERR_ALIGN;
+  if (a->rows == 0 || (!a->y && !a->n)) return FAK_OK;
+  const int st = kv_device(nullptr, nullptr);
+  if (st != FAK_OK) return st;
+  p.h = a->h;
+  p.y = a->y;
+  p.n = a->n;
+  p.w = a->w;
+  p.y_w = a->y_w;
+  p.gate = a->y ? a->gate : nullptr;
+  p.rows = a->rows;
+  p.scale = a->scale;
+  p.eps = a->eps;
+  p.offset = a->gain_offset;
+  p.d = a->d;
+  p.h_bf16 = hb;
+  p.y_bf16 = yb;
+  p.n_bf16 = nb;
+  p.post = a->post_norm != 0;
+  p.sigmoid = a->gate_kind == FAK_GATE_SIGMOID;
+  // four values at a time where every row of every operand stands on a multiple of 16 bytes
+  const int64_t strides = p.h_row * (hb ? 2 : 4) | (a->y ? p.y_row * (yb ? 2 : 4) : 0) | (a->n ? p.n_row * (nb ? 2 : 4) : 0) |
+                          (p.gate && p.gate_col ? p.gate_row * 4 : 0);
+  const uintptr_t starts = (uintptr_t)a->h | (uintptr_t)a->y | (uintptr_t)a->n | (uintptr_t)a->w | (uintptr_t)a->y_w |
+                           (p.gate && p.gate_col ? (uintptr_t)a->gate : 0);
+  const bool wide = a->d % 4 == 0 && !(strides & 15) && !(starts & 15);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (wide)
+    e = a->d <= 4096 ? launch<4, 1>(p, s) : a->d <= 8192 ? launch<4, 2>(p, s) : a->d <= 16384 ? launch<4, 4>(p, s) : launch<4, 8>(p, s);
+  else
+    e = a->d <= 1024 ? launch<1, 1>(p, s) : a->d <= 8192 ? launch<1, 8>(p, s) : launch<1, 32>(p, s);
+  return fak_cuda_status(e);
+}

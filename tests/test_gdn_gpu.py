@@ -1,0 +1,357 @@
+"""fak_gdn_conv and fak_gdn_attn against the rule row by row in 64 bits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+import _gdn as G
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def fak():
+    from q4_weight_quantized_block_gb300 import build
+    build.build()
+    import q4_weight_quantized_block_gb300 as m
+    assert torch.cuda.is_available()
+    return m
+
+
+# (new rows, positions in all): single tokens, none, chunks around the sizes that kernels cut at, padding, beginnings
+BATCHES = {
+    "token": [(1, 9)],
+    "first token": [(1, 1)],
+    "tokens": [(1, 5), (1, 1), (0, 4), (1, 300), (1, 2)],
+    "none": [(0, 3), (0, 0)],
+    "drafts": [(4, 10), (4, 4), (2, 100), (5, 5), (7, 9)],
+    "padded": [(5, 3), (4, 0), (1, 0), (3, 1), (70, 66), (68, 4)],
+    "one chunk": [(64, 64), (64, 100), (63, 63), (17, 18)],
+    "chunks": [(65, 65), (128, 130), (129, 129), (200, 1000), (1, 7), (0, 2), (31, 31)],
+    "prompt": [(700, 700)],
+    "mixed": [(1, 800), (333, 333), (1, 1), (9, 20), (190, 191), (16, 16), (33, 40)],
+}
+
+
+def attn_case(fak, lengths, nk, nv, seed=1, out=torch.bfloat16, z=True, norm=True, wild=False, pad_rows=3, scale=None, views=False,
+              max_q=None):
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, seed, pad_rows)
+    q, k, v, g, beta, zz, w = G.inputs(nk, nv, rows, seed, wild=wild)
+    state = torch.randn(slots, nv, 128, 128, device="cuda") * 0.3
+    for (n, t), s in zip(lengths, slot.tolist()):
+        if t <= n:
+            state[s] = NAN  # not read
+    keep = state.clone()
+    o = torch.full((rows, nv, 128), 7.0, dtype=out, device="cuda")
+    if views:  # rows and heads of larger tensors
+        def view(t, by):
+            big = torch.full((t.shape[0], t.shape[1] + 1, 128 + by), NAN, dtype=t.dtype, device="cuda")
+            big[:, :t.shape[1], :128] = t
+            return big[:, :t.shape[1], :128]
+        q, k, v, zz, o = view(q, 8), view(k, 16), view(v, 8), view(zz, 4), view(o, 8)
+    batch = fak.GDNBatch(start, kv_len, slot)
+    most = max([n for n, _ in lengths]) if max_q is None else max_q
+    fak.fak_gdn_attn(batch, q, k, v, g, beta, state, o, most, scale=scale, z=zz if z else None, norm_w=w if norm else None, eps=G.EPS)
+    assert fak.fak_device_status() == 0
+    sc = 128 ** -0.5 if scale is None else scale
+    at = 0
+    for (n, t), (first, end, fresh), s in zip(lengths, G.real_rows(lengths), slot.tolist()):
+        assert bool((o[at:first] == 0).all())  # padding
+        at += n
+        if first == end:
+            assert torch.equal(state[s].nan_to_num(1e9), keep[s].nan_to_num(1e9))
+            continue
+        r = slice(first, end)
+        S0 = torch.zeros_like(keep[s]) if fresh else keep[s]
+        want, S, most = G.gdn_ref(q[r], k[r], v[r], g[r], beta[r], S0, sc)
+        # a product of the state is off by 2^-24 of itself in f32, or 2^-22 where it is split over two f16; the rule only
+        # shrinks what is there, so the errors of its sums of 128, of either sign, add up over the rows like their root
+        tol = 2.0 ** -20 * (end - first) ** 0.5 * max(most, 1e-30)
+        err = float((state[s].double() - S).abs().max())
+        assert err <= tol, ("state", (n, t), err / tol)
+        tol_o = torch.full_like(want, tol * sc)
+        if norm:
+            tol_o = tol_o / torch.sqrt((want * want).mean(-1, keepdim=True) + G.EPS) * 2 * w.double().abs()
+        if z:
+            zd = zz[r].double()
+            tol_o = tol_o * (zd / (1 + torch.exp(-zd))).abs()
+        want = G.gated(want, w if norm else None, zz[r] if z else None)
+        tol_o = tol_o + want.abs() * (2.0 ** -18 + torch.finfo(out).eps / 2) + 1e-30
+        diff = (o[r].double() - want).abs()
+        assert bool((diff <= tol_o).all()), ("out", (n, t), float((diff / tol_o).max()))
+    assert bool((o[rows - pad_rows:] == 7).all())  # rows of no sequence
+    rest = [i for i in range(slots) if i not in slot.tolist()]
+    assert torch.equal(state[rest], keep[rest])
+
+
+@pytest.mark.parametrize("name", list(BATCHES))
+@pytest.mark.parametrize("nk,nv", [(2, 6), (3, 3)])
+def test_attn_lengths(fak, name, nk, nv):
+    attn_case(fak, BATCHES[name], nk, nv)
+
+
+@pytest.mark.parametrize("name", ["tokens", "drafts", "chunks"])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("z,norm", [(False, False), (True, False), (False, True)])
+def test_attn_outputs(fak, name, out, z, norm):
+    attn_case(fak, BATCHES[name], 1, 2, out=out, z=z, norm=norm, scale=0.3, seed=4)
+
+
+@pytest.mark.parametrize("name", ["tokens", "drafts", "mixed"])
+def test_attn_strides(fak, name):
+    attn_case(fak, BATCHES[name], 2, 4, views=True, seed=5)
+
+
+@pytest.mark.parametrize("name", ["drafts", "padded", "chunks", "prompt"])
+def test_attn_resets_and_repeated_keys(fak, name):
+    """Decays of 0 and -inf, strengths of 0 and 1, the same key twice, values 10^4 times the others."""
+    attn_case(fak, BATCHES[name], 2, 2, wild=True, out=torch.float32, seed=6)
+
+
+def test_attn_many_heads(fak):
+    attn_case(fak, [(1, 3)] * 9 + [(2, 2), (130, 131)], 16, 48, seed=7)
+
+
+def test_attn_large_bound(fak):
+    """max_q is a bound: one far above the rows changes nothing that matters."""
+    attn_case(fak, BATCHES["drafts"], 1, 3, max_q=100000, seed=8)
+
+
+def test_attn_split_prompt_goes_on(fak):
+    """A prompt in one call, and in pieces with the state between them."""
+    n, nk, nv = 300, 2, 4
+    q, k, v, g, beta, z, w = G.inputs(nk, nv, n, 11)
+    ident = torch.tensor([0], dtype=torch.int32, device="cuda")
+    results = []
+    for cuts in ([0, n], [0, 1, 64, 65, 70, 200, 201, n]):
+        state = torch.full((1, nv, 128, 128), NAN, device="cuda")
+        o = torch.empty(n, nv, 128, device="cuda")
+        for a, b in zip(cuts, cuts[1:]):
+            batch = fak.GDNBatch(torch.tensor([0, b - a], dtype=torch.int32, device="cuda"),
+                                 torch.tensor([b], dtype=torch.int32, device="cuda"), ident)
+            fak.fak_gdn_attn(batch, *(t[a:b] for t in (q, k, v, g, beta)), state, o[a:b], b - a, z=z[a:b], norm_w=w)
+        results.append((o, state))
+    (o1, s1), (o2, s2) = results
+    assert fak.fak_device_status() == 0
+    tol = 2 * 2.0 ** -20 * n ** 0.5 * float(s1.norm(dim=2).max())
+    assert float((s1 - s2).abs().max()) <= tol
+    assert float((o1 - o2).norm() / o1.norm()) < 1e-4
+
+
+def test_attn_bad_values_stay_in_their_sequence(fak):
+    """Infinities and NaN in one sequence's rows and in the rows of no sequence reach no other sequence."""
+    lengths = [(70, 70), (70, 75), (1, 4), (70, 70), (1, 2)]
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 3, 5)
+    got = []
+    for bad in (False, True):
+        q, k, v, g, beta, z, w = G.inputs(1, 2, rows, 12)
+        state = torch.randn(slots, 2, 128, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+        if bad:
+            for r in (slice(70, 140), slice(140, 141), slice(rows - 5, rows)):
+                q[r], k[r], v[r], g[r], beta[r], z[r] = NAN, float("inf"), NAN, NAN, float("inf"), NAN
+            state[[i for i in range(slots) if i not in slot.tolist()]] = NAN
+        o = torch.zeros(rows, 2, 128, device="cuda")
+        fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, state, o, 70, z=z, norm_w=w)
+        got.append((o, state))
+    for s in (0, 3, 4):
+        r = slice(int(start[s]), int(start[s + 1]))
+        assert torch.equal(got[0][0][r], got[1][0][r]) and torch.equal(got[0][1][slot[s]], got[1][1][slot[s]])
+    assert fak.fak_device_status() == 0
+
+
+@pytest.mark.parametrize("most", [1, 300])
+def test_bad_batches_are_left_out(fak, most):
+    """Numbers out of range: the sequence is left out and recorded, the others come out."""
+    good = [(1, 4), (most, most), (1, 9), (1, 1)]
+    for what in ("len", "slot low", "slot high", "max_q", "start"):
+        start, kv_len, slot, rows, slots = G.batch_tensors(good, 2)
+        q, k, v, g, beta, z, w = G.inputs(1, 2, rows, 13)
+        state = torch.randn(slots, 2, 128, 128, device="cuda")
+        keep = state.clone()
+        old, max_q = slot.clone(), most
+        if what == "len":
+            kv_len[2] = -1
+        elif what == "slot low":
+            slot[2] = -1
+        elif what == "slot high":
+            slot[2] = slots
+        elif what == "start":
+            start[3] = rows + 9  # the last two sequences' bounds
+        else:
+            if most == 1:
+                continue
+            max_q = most - 1
+        o = torch.full((rows, 2, 128), 7.0, device="cuda")
+        fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, state, o, max_q, z=z, norm_w=w)
+        assert fak.fak_device_status() == 7, what
+        out = {"max_q": [1], "start": [2, 3]}.get(what, [2])
+        for s, (first, end, fresh) in enumerate(G.real_rows(good)):
+            if s in out:
+                assert bool((o[first:end] == 7).all()) and torch.equal(state[old[s]], keep[old[s]]), what
+                continue
+            want, S, m = G.gdn_ref(*(t[first:end] for t in (q, k, v, g, beta)),
+                                   keep[old[s]] * 0 if fresh else keep[old[s]], 128 ** -0.5)
+            assert float((state[old[s]].double() - S).abs().max()) <= 2.0 ** -20 * (end - first) ** 0.5 * m
+        assert fak.fak_device_status() == 0
+
+
+def test_attn_same_bits_again_captured_and_on_another_stream(fak):
+    lengths = BATCHES["mixed"]
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 9)
+    q, k, v, g, beta, z, w = G.inputs(2, 4, rows, 14)
+    s0 = torch.randn(slots, 4, 128, 128, device="cuda")
+    batch = fak.GDNBatch(start, kv_len, slot)
+
+    def call(state, o):
+        fak.fak_gdn_attn(batch, q, k, v, g, beta, state, o, 333, z=z, norm_w=w)
+
+    a, oa = s0.clone(), torch.zeros(rows, 4, 128, device="cuda")
+    call(a, oa)
+    b, ob = s0.clone(), torch.zeros_like(oa)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(b, ob)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(a, b) and torch.equal(oa, ob)
+    c, oc = s0.clone(), torch.zeros_like(oa)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c, oc)
+    assert torch.equal(c, s0)
+    graph.replay()
+    assert torch.equal(a, c) and torch.equal(oa, oc)
+    # the numbers are read when the graph runs
+    c.copy_(s0)
+    oc.zero_()
+    kv_len[0], kv_len[1] = 1, 900
+    slot.copy_(slot.flip(0))
+    graph.replay()
+    d, od = s0.clone(), torch.zeros_like(oa)
+    call(d, od)
+    assert torch.equal(c, d) and torch.equal(oc, od) and not torch.equal(oa, oc)
+    assert fak.fak_device_status() == 0
+
+
+# ------------------------------------------------------------------ the convolution
+def conv_case(fak, lengths, nk, nv, kind=torch.float32, seed=1, pad_rows=2, views=True):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, seed, pad_rows)
+    chans = (2 * nk + nv) * 128
+    t = rand(rows, chans + 2 * nv + 8).to(kind)
+    x, b, a = t[:, :chans], t[:, chans:chans + nv], t[:, chans + nv:chans + 2 * nv]
+    if not views:
+        x, b, a = (u.contiguous() for u in (x, b, a))
+    if rows > 9:
+        b[5], a[6], a[7] = 60.0, -90.0, 90.0
+    w, a_log, dt = 0.5 * rand(chans, 4), torch.log(1 + 15 * torch.rand(nv, device="cuda")), rand(nv)
+    state = rand(slots, 3, chans)
+    for (n, ln), s in zip(lengths, slot.tolist()):
+        if ln <= n:
+            state[s] = NAN
+    keep = state.clone()
+    q, k = (torch.full((rows, nk, 128), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    v = torch.full((rows, nv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    g, beta = (torch.full((rows, nv), 7.0, device="cuda") for _ in range(2))
+    fak.fak_gdn_conv(fak.GDNBatch(start, kv_len, slot), x, b, a, w, a_log, dt, state, q, k, v, g, beta, eps=G.EPS)
+    assert fak.fak_device_status() == 0
+    seen = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for (first, end, fresh), s in zip(G.real_rows(lengths), slot.tolist()):
+        if first == end:
+            assert torch.equal(state[s].nan_to_num(1e9), keep[s].nan_to_num(1e9))
+            continue
+        r = slice(first, end)
+        seen[r] = True
+        c, after = G.conv_ref(x[r], w, torch.zeros_like(keep[s]) if fresh else keep[s])
+        assert torch.equal(state[s], after.float())  # inputs, kept as they are
+        c = c.view(end - first, -1, 128)
+        # four products of f32 (sums off by 4 * 2^-24 of the terms' magnitudes, here below 16), silu by fast functions (2^-20)
+        near = 16 * 2.0 ** -22 + c.abs() * 2.0 ** -20
+        for got, want in ((q[r], c[:, :nk]), (k[r], c[:, nk:2 * nk])):
+            size = torch.sqrt((want * want).sum(-1, keepdim=True) + G.EPS)
+            tol = want.abs() / size * (2.0 ** -11 + 2.0 ** -18) + 2.0 ** -25 + 4 * 16 * 2.0 ** -22 / size
+            assert bool(((got.double() - want / size).abs() <= tol).all())
+        want = c[:, 2 * nk:]
+        assert bool(((v[r].double() - want).abs() <= want.abs() * 2.0 ** -8 + near[:, 2 * nk:]).all())
+        u = a[r].double() + dt.double()
+        want = -torch.exp(a_log.double()) * torch.nn.functional.softplus(u, threshold=1000.0)
+        # u is off by 2^-24 of its terms, and so softplus by as much of its own slope; a few roundings of f32 behind it
+        off = torch.exp(a_log.double()) * torch.sigmoid(u) * (a[r].double().abs() + dt.abs()) * 2.0 ** -23
+        assert bool(((g[r].double() - want).abs() <= want.abs() * 2.0 ** -20 + off).all())
+        want = torch.sigmoid(b[r].double())
+        assert bool(((beta[r].double() - want).abs() <= want * 2.0 ** -21).all())
+    for t in (q, k, v, g, beta):
+        assert bool((t[~seen] == 7).all())
+    rest = [i for i in range(slots) if i not in slot.tolist()]
+    assert torch.equal(state[rest], keep[rest])
+
+
+@pytest.mark.parametrize("name", list(BATCHES))
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_conv_lengths(fak, name, kind):
+    conv_case(fak, BATCHES[name], 2, 3, kind)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_conv_many_short_sequences(fak, seed):
+    """Over 608 rows, so that a block has several: sequences of 0 to 12 rows begin and end anywhere in a block's range."""
+    rng = np.random.default_rng(seed)
+    lengths = [(int(n), int(n + rng.integers(-1, 3)) if n else 3) for n in rng.integers(0, 13, 160)]
+    lengths = [(n, max(t, 0)) for n, t in lengths] + [(40, 40), (3, 3), (2, 2)]
+    conv_case(fak, lengths, 1, 2, seed=20 + seed, views=seed % 2 == 0)
+
+
+def test_conv_large(fak):
+    conv_case(fak, [(2000, 2000), (1, 5), (700, 701)], 16, 48, seed=30)
+
+
+def test_conv_bad_batches_are_left_out(fak):
+    for rows_each in (2, 200):
+        good = [(rows_each, rows_each + 3)] * 4
+        for what in ("len", "slot low", "slot high", "start"):
+            start, kv_len, slot, rows, slots = G.batch_tensors(good, 2)
+            chans = 3 * 128
+            x, ba = torch.randn(rows, chans, device="cuda"), torch.randn(rows, 1, device="cuda")
+            state = torch.randn(slots, 3, chans, device="cuda")
+            keep, old = state.clone(), slot.tolist()
+            out = [2]
+            if what == "len":
+                kv_len[2] = -1
+            elif what == "slot low":
+                slot[2] = -2
+            elif what == "slot high":
+                slot[2] = slots
+            else:
+                start[3], out = rows + 1, [2, 3]
+            q, k = (torch.full((rows, 1, 128), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+            v = torch.full((rows, 1, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+            g, beta = (torch.full((rows, 1), 7.0, device="cuda") for _ in range(2))
+            w = torch.randn(chans, 4, device="cuda")
+            zero = torch.zeros(1, device="cuda")
+            fak.fak_gdn_conv(fak.GDNBatch(start, kv_len, slot), x, ba, ba, w, zero, zero, state, q, k, v, g, beta)
+            assert fak.fak_device_status() == 7, what
+            for s in range(4):
+                r = slice(s * rows_each, (s + 1) * rows_each)
+                if s in out:
+                    assert bool((v[r] == 7).all()) and bool((g[r] == 7).all()) and torch.equal(state[old[s]], keep[old[s]])
+                else:
+                    c, after = G.conv_ref(x[r], w, keep[old[s]])
+                    assert torch.equal(state[old[s]], after.float())
+                    assert float((v[r].double() - c.view(-1, 3, 128)[:, 2:]).abs().max()) <= 2.0 ** -8 * float(c.abs().max()) + 1e-4
+            assert fak.fak_device_status() == 0
+
+
+def test_calls_without_rows_or_sequences(fak):
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+    state = torch.randn(1, 2, 128, 128, device="cuda")
+    for start, ln, slot, rows in ((i32(0), i32(), i32(), 3), (i32(0, 0), i32(4), i32(0), 0)):
+        batch = fak.GDNBatch(start, ln, slot)
+        keep = state.clone()
+        o = torch.full((rows, 2, 128), 7.0, device="cuda")
+        h = e(rows, 1, 128, dtype=torch.float16)
+        fak.fak_gdn_attn(batch, h, h, e(rows, 2, 128, dtype=torch.bfloat16), e(rows, 2), e(rows, 2), state, o, 5)
+        fak.fak_gdn_conv(batch, e(rows, 512), e(rows, 2), e(rows, 2), e(512, 4), e(2), e(2), e(1, 3, 512), h, h,
+                         e(rows, 2, 128, dtype=torch.bfloat16), e(rows, 2), e(rows, 2))
+        assert fak.fak_device_status() == 0 and torch.equal(state, keep) and bool((o == 7).all())
