@@ -18,7 +18,7 @@ __all__ = [
     "fak_q4k_pack", "fak_q4k_pack_device", "fak_q8_0_gemv", "fak_q8_0_pack", "fak_q8_0_pack_device", "fak_strerror", "fak_swiglu_bf16", "fak_version", "lib",
     "FAK_KV_BF16", "FAK_KV_E4M3", "FAK_KV_I8", "FAK_ROWS_F32", "FAK_ROWS_BF16", "KVCache", "KVBatch", "fak_rope_table",
     "fak_kv_append", "fak_kv_read", "fak_paged_attn", "fak_paged_attn_workspace_bytes", "fak_paged_attn_debug_wait",
-    "FAK_GATE_LINEAR", "FAK_GATE_SIGMOID", "GDNBatch", "fak_gdn_conv", "fak_gdn_attn", "fak_residual_norm",
+    "FAK_GATE_LINEAR", "FAK_GATE_SIGMOID", "GDNBatch", "fak_gdn_conv", "fak_gdn_attn", "fak_gdn_debug_wait", "fak_residual_norm",
 ]
 
 

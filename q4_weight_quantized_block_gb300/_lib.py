@@ -144,6 +144,7 @@ _SIGS = {
     "fak_paged_attn_debug_wait": ([I64, I32], I32),
     "fak_gdn_conv": ([P, P, P], I32),
     "fak_gdn_attn": ([P, P, P], I32),
+    "fak_gdn_debug_wait": ([I64, I32], I32),
     "fak_residual_norm": ([P, P], I32),
     "fak_prefill_create": ([ctypes.POINTER(DecodeDesc), I64, ctypes.POINTER(P)], I32),
     "fak_prefill_run": ([P, P, P, P, P], I32),
@@ -580,6 +581,11 @@ def fak_gdn_attn(batch, q, k, v, g, beta, state, out, max_q, scale=None, z=None,
                 orow, oh)
     _on_device(batch.device, (q, k, v, g, beta, state, out, z, norm_w), where)
     _check(lib.fak_gdn_attn(batch.ref, ctypes.addressof(a), _stream(stream)), where)
+
+
+def fak_gdn_debug_wait(timeout_ns=0, unreachable=0):
+    """Test hooks: the limit of the linear attention's waits (0: the default), and waits that can never complete."""
+    _check(lib.fak_gdn_debug_wait(int(timeout_ns), int(unreachable)), "fak_gdn_debug_wait")
 
 
 def fak_residual_norm(h, y=None, n=None, w=None, post_norm=False, y_w=None, gate=None, gate_sigmoid=False, scale=1.0,

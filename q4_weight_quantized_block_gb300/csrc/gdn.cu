@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -16,6 +17,11 @@
 namespace {
 
 __device__ int g_gdn_status;
+
+constexpr unsigned long long kGdnTimeout = 2000000000ull;
+std::atomic<unsigned long long> g_gdn_timeout{kGdnTimeout};
+std::atomic<int> g_gdn_unreachable{0};
+constexpr int kFew = 8;
 
 FAK_DEV void gdn_record() { atomicCAS(&g_gdn_status, 0, FAK_ERR_DEVICE); }
 
@@ -193,14 +199,15 @@ __global__ void __launch_bounds__(kStepThreads, 2) gdn_step_kernel(const __grid_
   const int s = blockIdx.x / p.nv, h = blockIdx.x - s * p.nv;
   const KvSeq seq = kv_seq(p.c, s);
   const GdnSeq d = gdn_seq(p.c, seq, s);
+  const int n = d.r1 - d.first;
+  if (d.ok && n > p.few) return;  // the chunks' kernel's
   if (!d.ok) {
     if (h == 0 && threadIdx.x == 0) gdn_record();
     return;
   }
   for (int row = d.r0 + warp; row < d.first; row += 8)
     gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + 4 * lane, gdn_zero4());
-  const int n = d.r1 - d.first;
-  if (n == 0 || n > p.few) return;
+  if (n == 0) return;
 
   float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + 16 * warp) * kGdnDim + 4 * lane;
   float4 S[16];
@@ -374,7 +381,8 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
       (((uintptr_t)a->g | (uintptr_t)a->beta | (uintptr_t)a->z) & 3))
     return FAK_ERR_ALIGN;
   if (a->rows == 0 || batch->n_seqs == 0) return FAK_OK;
-  if ((st = kv_device(nullptr, nullptr)) != FAK_OK) return st;
+  int dev = 0;
+  if ((st = kv_device(&dev, nullptr)) != FAK_OK) return st;
   p.c.rows = a->rows;
   p.c.max_q = a->max_q;
   p.q = static_cast<const __half*>(a->q);
@@ -392,9 +400,26 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   p.nv = a->nv;
   p.group = a->nv / a->nk;
   p.out_bf16 = a->out_type == FAK_ROWS_BF16;
-  p.few = 0x7fffffff;
-  gdn_step_kernel<<<(unsigned)(batch->n_seqs * a->nv), kStepThreads, 0, (cudaStream_t)stream>>>(p);
-  return fak_cuda_status(cudaGetLastError());
+  cudaStream_t s = (cudaStream_t)stream;
+  // Sequences of more than kFew rows go over chunks of 64, the others row by row.
+  if (a->max_q <= kFew || batch->n_seqs > 1) {
+    p.few = kFew;
+    gdn_step_kernel<<<(unsigned)(batch->n_seqs * a->nv), kStepThreads, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a->max_q <= kFew) return fak_cuda_status(e);
+  }
+  void* status = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
+  if (e != cudaSuccess) return fak_cuda_status(e);
+  return fak_cuda_status(gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
+                                          static_cast<int*>(status), dev, s));
+}
+
+extern "C" int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable) {
+  if (timeout_ns < 0 || (unreachable != 0 && unreachable != 1)) return FAK_ERR_INVALID_ARG;
+  g_gdn_timeout = timeout_ns ? (unsigned long long)timeout_ns : kGdnTimeout;
+  g_gdn_unreachable = unreachable;
+  return FAK_OK;
 }
 
 int fak_gdn_take_status() {

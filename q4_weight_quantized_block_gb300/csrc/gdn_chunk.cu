@@ -1,0 +1,880 @@
+// The gated delta rule over 64 rows at a time, on the tensor cores: chunks and prompts of fak_gdn_attn.
+//
+// With G_t = g_1 + .. + g_t since the chunk began, S the state before it, and
+//   A_ts = beta_t exp(G_t - G_s) k_t.k_s (s < t),  P_ts = exp(G_t - G_s) q_t.k_s (s <= t),  T = (I + A)^-1,
+// the rule's rows are
+//   R = diag(beta) (V - diag(exp G) K S),   U = T R,   O = diag(exp G) Q S + (P T) R,
+//   S' = exp(G_64) S + K^T diag(exp(G_64 - G)) U,
+// so that what goes from chunk to chunk is three products: [K; Q] S, [T; P T] R (128 rows each) and K^T U.  T and P T
+// depend on no state: other warps make them a chunk ahead.
+//
+// Precision.  The state is held in f32 registers, and its products keep 22 bits: the f32 operand goes as the sum of two
+// f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents
+// take them because a chunk's S, R and U are scaled by one power of two: with m the largest of |S| and |V|, lengths of k
+// of at most 1 and 0 <= beta <= 2, |R| <= 25 m and |U|, |S'| <= 281 m, so m goes to 2^5 .. 2^6; what f16 drops is below
+// 2^-25, so 2^-30 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and
+// kept as two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
+//
+// A cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own rule: only the
+// norm needs the whole row, and its sums of squares go to the other CTAs by asynchronous stores.  Warps:
+//   0 .. 7    the chain: a warp reads the accumulators' 32 lanes (w % 4) and half their columns (w / 4); lanes 0..63 are K's
+//             or T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128
+//   8 .. 11   T and P T: decays into A and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T,
+//             by m16n8k16 instructions
+//   12        issues the products;  13  copies K, Q and z, sums the decays.
+// The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
+// B's columns, so B's two parts stand side by side as 2 n columns, one read of A for both.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_device.cuh"
+#include "fak.h"
+#include "fak_device.cuh"
+#include "fak_tc.cuh"
+#include "gdn_device.cuh"
+#include "kv_device.cuh"
+
+namespace {
+
+constexpr int kRows = 64;  // of a chunk
+constexpr int kChainThreads = 256, kPrepThreads = 128;
+constexpr int kThreads = kChainThreads + kPrepThreads + 64;
+constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
+constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
+
+// What a chunk's rows decay by, four chunks' worth (the chain may still read the last one's when the loader is two on).
+struct Decays {
+  float keep[kRows];           // exp G_t
+  float left[kRows];           // exp(G_64 - G_t)
+  float beta[kRows];
+  float hi[kRows], lo[kRows];  // G_t log2(e): a multiple of 2^-9, and the rest
+  float mid[kRows];            // t >= 32: exp(G_t - G_31), else exp(G_31 - G_t)
+};
+
+template <int NS>
+struct Cfg {
+  static constexpr int n = kGdnDim / NS;        // value columns of a CTA
+  static constexpr int cols = n / 2;            // of a chain thread
+  static constexpr int panels = (n + 63) / 64;  // of 64 columns, 128 bytes
+  static constexpr int off_kq = 0;                                 // two stages of [K; Q]: two panels of 128 rows
+  static constexpr int off_tp = off_kq + 2 * 32768;                // [T; P T], two parts
+  static constexpr int off_ap = off_tp + 2 * kPart;                // [A; P], two parts
+  static constexpr int off_s = off_ap + 2 * kPart;                 // S, two parts
+  static constexpr int off_u = off_s + 2 * panels * 16384;         // R, then U, two parts
+  static constexpr int off_z = off_u + 2 * panels * 8192;          // two stages of z
+  static constexpr int off_a = off_z + 2 * kRows * n * 4;          // A's blocks of 16 x 16 on the diagonal in f32
+  static constexpr int off_dec = off_a + 4 * 16 * kLd * 4;
+  static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 2][64]
+  static constexpr int off_gain = off_sum + 2 * NS * 2 * kRows * 4;
+  static constexpr int off_max = off_gain + n * 4;  // [8]
+  static constexpr int off_bar = off_max + 32;
+  static constexpr int smem = off_bar + 160 + 1024;
+  static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
+  static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n, dkk = 6 * n;  // TMEM columns
+  static constexpr int tmem_cols = 512;
+  static_assert(dkk + 64 <= tmem_cols, "TMEM");
+};
+
+enum Bars { kD1, kD2, kD3, kKK, kTP, kKQ0, kKQ1, kZ0, kZ1, kZFree0, kZFree1, kS, kR, kU, kSum0, kSum1, kDrain, kBars };
+
+template <int M, int N, bool A_MN, bool B_MN>
+constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+                            ((uint32_t)(M >> 4) << 24);
+
+FAK_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+// 128-byte swizzle with M or N running: 64 of them by 8 k atoms, the next 64 `lbo` bytes on, the next 8 k 1024 bytes on
+FAK_DEV uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+FAK_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+FAK_DEV uint32_t rank_in_cluster() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+FAK_DEV uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+// A value into shared memory of a CTA of the cluster, its 4 bytes counted on a barrier there.
+FAK_DEV void st_async(uint32_t addr, float x, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(x)), "r"(bar)
+               : "memory");
+}
+
+FAK_DEV bool try_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+FAK_DEV void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Two f32 as the sum of two pairs of f16.
+FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 b = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Columns col .. col + 7 (a multiple of 8) of a row of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
+// second part `part` bytes behind the first.
+FAK_DEV void put_halves8(unsigned char* tile, int panel, int part, int row, int col, const float* x) {
+  uint4 hi, lo;
+  split_half(x[0], x[1], hi.x, lo.x);
+  split_half(x[2], x[3], hi.y, lo.y);
+  split_half(x[4], x[5], hi.z, lo.z);
+  split_half(x[6], x[7], hi.w, lo.w);
+  unsigned char* at = tile + (col >> 6) * panel + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
+  *reinterpret_cast<uint4*>(at) = hi;
+  *reinterpret_cast<uint4*>(at + part) = lo;
+}
+
+template <int N>
+FAK_DEV void ld_cols(uint32_t addr, float (&x)[N]) {
+  uint32_t r[N];
+  tmem_ld_cols<N>(addr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+}
+// The sums of two columns each, `apart` columns apart.
+template <int N>
+FAK_DEV void ld_sums(uint32_t addr, int apart, float (&x)[N]) {
+  uint32_t r[N], u[N];
+  tmem_ld_cols<N>(addr, r);
+  tmem_ld_cols<N>(addr + apart, u);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]) + __uint_as_float(u[i]);
+}
+
+// Operands of m16n8k16, both parts, from a tile of rows of 64 f16.  A: rows r0 .. +15, columns c0 .. +15; B: the same rows,
+// columns 8 j .. +7.
+struct FragA {
+  uint32_t hi[4], lo[4];
+};
+struct FragB {
+  uint32_t hi[2], lo[2];
+};
+FAK_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FAK_DEV void load_a(FragA& a, uint32_t tile, int r0, int c0, int lane) {
+  const int row = r0 + (lane & 15);
+  const uint32_t at = tile + row * 128 + ((((c0 >> 3) + (lane >> 4)) ^ (row & 7)) << 4);
+  ldsm4(a.hi, at);
+  ldsm4(a.lo, at + kPart);
+}
+FAK_DEV void load_b(FragB& b, uint32_t tile, int r0, int j, int lane) {
+  const int row = r0 + (lane & 15);
+  const uint32_t at = tile + row * 128 + ((j ^ (row & 7)) << 4) + (lane >> 4) * kPart;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(b.hi[0]), "=r"(b.hi[1]), "=r"(b.lo[0]), "=r"(b.lo[1])
+               : "r"(at)
+               : "memory");
+}
+FAK_DEV void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// A product's 16 x 8 as an operand B.
+FAK_DEV void turn_b(FragB& b, const float (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t hi, lo;
+    split_half(c[2 * i], c[2 * i + 1], hi, lo);
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(b.hi[i]) : "r"(hi));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(b.lo[i]) : "r"(lo));
+  }
+}
+// sign * a product's 16 x 8, both parts, at rows r0 .. +15, columns 8 j .. +7 of a tile
+FAK_DEV void put_block(unsigned char* tile, int r0, int j, const float (&c)[4], float sign, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = r0 + 8 * i + (lane >> 2);
+    uint32_t hi, lo;
+    split_half(sign * c[2 * i], sign * c[2 * i + 1], hi, lo);
+    unsigned char* at = tile + row * 128 + ((j ^ (row & 7)) << 4) + 4 * (lane & 3);
+    *reinterpret_cast<uint32_t*>(at) = hi;
+    *reinterpret_cast<uint32_t*>(at + kPart) = lo;
+  }
+}
+
+struct ChunkDebug {
+  unsigned long long timeout_ns;
+  int unreachable;  // a test's: 1 where K and Q are never to count as landed
+};
+
+template <int NS>
+__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, ChunkDebug dbg, int* status) {
+  using C = Cfg<NS>;
+  constexpr int n = C::n, W = C::cols, B = 16;  // B: columns a chain thread takes at a time
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::off_bar);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 8 * kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 8 * kBars + 4);
+  float* gain = reinterpret_cast<float*>(smem + C::off_gain);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int slice = blockIdx.x % NS, unit = blockIdx.x / NS;
+  const int s = unit / p.nv, h = unit - s * p.nv;
+  const KvSeq seq = kv_seq(p.c, s);
+  const GdnSeq d = gdn_seq(p.c, seq, s);
+  if (!d.ok) {
+    if (threadIdx.x == 0) atomicCAS(status, 0, FAK_ERR_DEVICE);
+    return;
+  }
+  const int rows = d.r1 - d.first;
+  if (p.few && rows <= p.few) return;  // the steps' kernel's
+  const int col0 = slice * n;
+  for (int i = threadIdx.x; i < (d.first - d.r0) * (n / 4); i += kThreads) {
+    const int row = d.r0 + i / (n / 4);
+    gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (n / 4)), gdn_zero4());
+  }
+  if (rows == 0) return;
+  const int chunks = (rows + kRows - 1) / kRows;
+
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 8 : i == kTP || i == kR || i == kU || i == kZFree0 || i == kZFree1 ? 4 : 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
+  // T and P T are zero above their blocks on the diagonal, which nothing writes
+  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + C::off_tp + 16 * i) = make_uint4(0, 0, 0, 0);
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(C::tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_async();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  // One that runs out is recorded, and no wait of the block waits after it: every warp goes through its chunks, without
+  // results, so that the named barriers, each of one group of warps, stay in step.
+  auto wait = [&](int b, int phase) {
+    bool done = *abort != 0;
+    for (int i = 0; i < 512 && !done; ++i) done = mbar_try_wait(&bar[b], phase & 1);
+    if (!done && !mbar_wait_bounded(&bar[b], phase & 1, abort, dbg.timeout_ns)) {
+      if (!*abort) atomicCAS(status, 0, FAK_ERR_TIMEOUT);
+      *abort = 1;
+    }
+    __syncwarp();
+  };
+  // What the warp wrote to shared memory and read from TMEM comes before what waits on the barrier, MMAs too.
+  auto arrive = [&](int b) {
+    fence_async();
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[b]);
+  };
+  auto decays = [&](int c) { return reinterpret_cast<Decays*>(smem + C::off_dec) + (c & 3); };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ the chain
+    const int quarter = warp & 3, half = warp >> 2;
+    const int col = half * W;                        // of the CTA's columns
+    const uint32_t acc = tmem + ((uint32_t)quarter << 21) + col;  // TMEM: lane 32 quarter
+    const int key = 32 * quarter + lane;             // the row of S
+    const bool top = quarter < 2;                    // K's and T's rows, else Q's and P T's
+    const int t = 32 * (quarter & 1) + lane;         // the row of the chunk
+    float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + col;
+    float* most = reinterpret_cast<float*>(smem + C::off_max);
+    float S[W];
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 x = d.fresh ? gdn_zero4() : *reinterpret_cast<const float4*>(st + i);
+      S[i] = x.x;
+      S[i + 1] = x.y;
+      S[i + 2] = x.z;
+      S[i + 3] = x.w;
+    }
+    uint32_t v[W / 2];  // of the next chunk
+    auto fetch_v = [&](int c) {
+      const int row = c * kRows + t;
+      if (row < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.v + (int64_t)(d.first + row) * p.v_row + h * p.v_head + col0 + col);
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i) {
+          const uint4 x = src[i];
+          v[4 * i] = x.x;
+          v[4 * i + 1] = x.y;
+          v[4 * i + 2] = x.z;
+          v[4 * i + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[i] = 0;
+      }
+    };
+    float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
+    // S scaled and in two parts to shared memory; all chain threads' S and V are looked at
+    auto put_state = [&]() {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; i += 2) m = fmaxf(fmaxf(m, fabsf(S[i])), fabsf(S[i + 1]));
+      if (top) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i)
+          m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i] << 16))), fabsf(__uint_as_float(v[i] & 0xffff0000u)));
+      }
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      if (lane == 0) most[warp] = m;
+      named_bar_sync(1, kChainThreads);
+      const float4 a = *reinterpret_cast<const float4*>(most), b = *reinterpret_cast<const float4*>(most + 4);
+      m = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+      // m = 2^e 1.f goes to 2^5 1.f (zeros and infinities: as they are); the inverse is a normal number too
+      const int e = (int)(__float_as_uint(m) >> 23);
+      const int by = e == 0 || e == 255 ? 0 : min(max(132 - e, -120), 120);
+      up = __uint_as_float((uint32_t)(127 + by) << 23);
+      down = __uint_as_float((uint32_t)(127 - by) << 23);
+#pragma unroll
+      for (int i = 0; i < W; i += 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = S[i + j] * up;
+        put_halves8(smem + C::off_s, 16384, C::panels * 16384, key, col + i, x);
+      }
+    };
+    const uint32_t sum_to = smem_u32(smem + C::off_sum);
+    const int me = NS > 1 ? (int)rank_in_cluster() : 0;
+    if (top) fetch_v(0);
+    put_state();
+    wait(kKQ0, 0);
+    arrive(kS);
+    for (int c = 0; c < chunks; ++c) {
+      const Decays* dec = decays(c);
+      const float keep = dec->keep[t], all = dec->keep[kRows - 1];
+      if (top) {
+        const float left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
+        wait(kD1, c);
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < W; i += B) {
+          float x[B];
+          ld_sums<B>(acc + C::d1 + i, n, x);
+#pragma unroll
+          for (int j = 0; j < B; j += 2) {
+            x[j] = fmaf(bk, x[j], __uint_as_float(v[(i + j) / 2] << 16) * bu);
+            x[j + 1] = fmaf(bk, x[j + 1], __uint_as_float(v[(i + j) / 2] & 0xffff0000u) * bu);
+          }
+#pragma unroll
+          for (int j = 0; j < B; j += 8) put_halves8(smem + C::off_u, 8192, C::panels * 8192, t, col + i + j, x + j);
+        }
+        arrive(kR);
+        wait(kD2, c);
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < W; i += B) {
+          float x[B];
+          ld_sums<B>(acc + C::d2 + i, n, x);
+#pragma unroll
+          for (int j = 0; j < B; ++j) x[j] *= left;
+#pragma unroll
+          for (int j = 0; j < B; j += 8) put_halves8(smem + C::off_u, 8192, C::panels * 8192, t, col + i + j, x + j);
+        }
+        arrive(kU);
+        fetch_v(c + 1);
+      } else {
+        const int64_t row = d.first + c * kRows + t;
+        const float by = down * p.scale;
+        float o[W];
+        wait(kD1, c);
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < W; i += B) {
+          float x[B];
+          ld_sums<B>(acc + C::d1 + i, n, x);
+#pragma unroll
+          for (int j = 0; j < B; ++j) o[i + j] = keep * x[j];
+        }
+        wait(kD2, c);
+        tc_fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < W; i += B) {
+          float x[B];
+          ld_sums<B>(acc + C::d2 + i, n, x);
+#pragma unroll
+          for (int j = 0; j < B; ++j) o[i + j] = (o[i + j] + x[j]) * by;
+        }
+        float r = 1.0f;
+        if (p.norm_w) {
+          // the row's sum of squares over the cluster's columns
+          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], NS * 2 * kRows * 4);
+          float ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < W; ++i) ss = fmaf(o[i], o[i], ss);
+          const uint32_t at = sum_to + (((c & 1) * NS * 2 + me * 2 + half) * kRows + t) * 4;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) st_async(map_rank(at, i), ss, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
+          wait(kSum0 + (c & 1), c >> 1);
+          if constexpr (NS > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
+          const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 2 * kRows + t;
+          ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 2 * NS; ++i) ss += sums[i * kRows];
+          r = rsqrtf(fmaf(ss, 1.0f / kGdnDim, p.eps));
+        }
+        if (p.z) wait(kZ0 + (c & 1), c >> 1);
+        const unsigned char* zs = smem + C::off_z + ((c & 1) * kRows + t) * n * 4;
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(gain + col + i);
+          o[i] *= r * w.x;
+          o[i + 1] *= r * w.y;
+          o[i + 2] *= r * w.z;
+          o[i + 3] *= r * w.w;
+          if (p.z) {
+            const float4 z = *reinterpret_cast<const float4*>(zs + ((((col + i) >> 2) ^ (t & 7)) << 4));
+            o[i] *= gdn_silu(z.x);
+            o[i + 1] *= gdn_silu(z.y);
+            o[i + 2] *= gdn_silu(z.z);
+            o[i + 3] *= gdn_silu(z.w);
+          }
+        }
+        if (p.z) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[kZFree0 + (c & 1)]);
+        }
+        if (c * kRows + t < rows && !*abort) {
+          const int64_t to = row * p.out_row + h * p.out_head + col0 + col;
+          if (p.out_bf16) {
+#pragma unroll
+            for (int i = 0; i < W; i += 8)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + i) =
+                  make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]), pack_bf16(o[i + 4], o[i + 5]),
+                             pack_bf16(o[i + 6], o[i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+      }
+      wait(kD3, c);
+      tc_fence_after_sync();
+#pragma unroll
+      for (int i = 0; i < W; i += B) {
+        float x[B];
+        ld_sums<B>(acc + C::d3 + i, n, x);
+#pragma unroll
+        for (int j = 0; j < B; ++j) S[i + j] = fmaf(all, S[i + j], x[j] * down);
+      }
+      if (c + 1 < chunks) {
+        put_state();
+        wait(kKQ0 + ((c + 1) & 1), (c + 1) >> 1);
+        arrive(kS);
+      }
+    }
+    if (!*abort) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(st + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ T and P T
+    const int w = warp - 8, r = threadIdx.x - kChainThreads;
+    float* diag = reinterpret_cast<float*>(smem + C::off_a);
+    unsigned char *tp = smem + C::off_tp, *ap = smem + C::off_ap;
+    const uint32_t tps = smem_u32(tp), aps = smem_u32(ap);
+    const bool top = w < 2, late = w & 1;  // K K^T's rows; rows from 32 on
+    const int t = r & (kRows - 1);
+    const uint32_t acc = tmem + ((uint32_t)w << 21) + C::dkk;
+    for (int c = 0; c < chunks; ++c) {
+      wait(kKQ0 + (c & 1), c >> 1);
+      wait(kKK, c);
+      tc_fence_after_sync();
+      const Decays* dec = decays(c);
+      {
+        // row r of [A; P], from K K^T and Q K^T by the decays: over the row's own 32 columns one exponential each; to the 32
+        // before them by way of row 31
+        const float hi = dec->hi[t], lo = dec->lo[t], b = top ? dec->beta[t] : 1.0f;
+        const int own = 32 * late, last = (top ? lane - 1 : lane);
+        float x[32];
+        ld_cols<32>(acc + own, x);
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + i + j]);
+            const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + i + j]);
+            y[j] = b * exp2_approx((hi - u.x) + (lo - l.x)) * x[i + j];
+            y[j + 1] = b * exp2_approx((hi - u.y) + (lo - l.y)) * x[i + j + 1];
+            y[j + 2] = b * exp2_approx((hi - u.z) + (lo - l.z)) * x[i + j + 2];
+            y[j + 3] = b * exp2_approx((hi - u.w) + (lo - l.w)) * x[i + j + 3];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = i + j <= last ? y[j] : 0.0f;
+          put_halves8(ap, 0, kPart, r, own + i, y);
+          if (top && (lane >> 4) == i >> 4) {
+            float* to = diag + t * kLd + (i & 8);
+            *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
+          }
+        }
+        if (late) {
+          const float f = b * dec->mid[t];
+          ld_cols<32>(acc, x);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(&dec->mid[i + j]);
+              y[j] = f * u.x * x[i + j];
+              y[j + 1] = f * u.y * x[i + j + 1];
+              y[j + 2] = f * u.z * x[i + j + 2];
+              y[j + 3] = f * u.w * x[i + j + 3];
+            }
+            put_halves8(ap, 0, kPart, r, i, y);
+          }
+        }
+      }
+      named_bar_sync(2, kPrepThreads);
+      {
+        // row lane % 16 of the inverse of the 16 x 16 block of I + A at 16 w
+        const int row = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == row ? 1.0f : 0.0f;
+        const float* a = diag + 16 * w * kLd;
+#pragma unroll
+        for (int i = 15; i > 0; --i) {
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < i; j += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(a + i * kLd + j);
+            y[j] = u.x;
+            y[j + 1] = u.y;
+            y[j + 2] = u.z;
+            y[j + 3] = u.w;
+          }
+#pragma unroll
+          for (int j = i - 1; j >= 0; --j) x[j] = fmaf(-x[i], y[j], x[j]);
+        }
+        if (lane < 16) {
+          put_halves8(tp, 0, kPart, 16 * w + row, 16 * w, x);
+          put_halves8(tp, 0, kPart, 16 * w + row, 16 * w + 8, x + 8);
+        }
+      }
+      named_bar_sync(2, kPrepThreads);
+      {
+        // two blocks of 32: the lower left is -T22 (A21 T11), eight columns to a warp
+        const int at = 32 * (w >> 1), j = (at >> 3) + (w & 1);
+        float x[4] = {}, y[4] = {};
+        FragA a, u;
+        FragB b;
+        load_a(a, aps, at + 16, at, lane);
+        load_a(u, tps, at + 16, at + 16, lane);
+        load_b(b, tps, at, j, lane);
+        mma16(x, a.lo, b.hi);
+        mma16(x, a.hi, b.lo);
+        mma16(x, a.hi, b.hi);
+        turn_b(b, x);
+        mma16(y, u.lo, b.hi);
+        mma16(y, u.hi, b.lo);
+        mma16(y, u.hi, b.hi);
+        put_block(tp, at + 16, j, y, -1.0f, lane);
+      }
+      named_bar_sync(2, kPrepThreads);
+      {
+        // the block of 64's, 32 x 32, eight columns to a warp
+        float x[2][4] = {}, y[2][4] = {};
+        FragA a[2];
+        FragB b;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          load_b(b, tps, 16 * k, w, lane);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) load_a(a[m], aps, 32 + 16 * m, 16 * k, lane);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma16(x[m], a[m].lo, b.hi);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma16(x[m], a[m].hi, b.lo);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) mma16(x[m], a[m].hi, b.hi);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          turn_b(b, x[k]);
+#pragma unroll
+          for (int m = k; m < 2; ++m) load_a(a[m], tps, 32 + 16 * m, 32 + 16 * k, lane);
+#pragma unroll
+          for (int m = k; m < 2; ++m) mma16(y[m], a[m].lo, b.hi);
+#pragma unroll
+          for (int m = k; m < 2; ++m) mma16(y[m], a[m].hi, b.lo);
+#pragma unroll
+          for (int m = k; m < 2; ++m) mma16(y[m], a[m].hi, b.hi);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) put_block(tp, 32 + 16 * m, w, y[m], -1.0f, lane);
+      }
+      named_bar_sync(2, kPrepThreads);
+      // P T, eight columns at a time: tiles 0 and 1 take ten steps, 2 and 3 six, 4 and 5 three, 6 and 7 one
+      for (int j = w; j < 8; j += w < 2 ? 8 : 2) {
+        float y[4][4] = {};
+        FragB b;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < j >> 1) continue;
+          load_b(b, tps, 16 * k, j, lane);
+          FragA a[4];
+#pragma unroll
+          for (int m = k; m < 4; ++m) load_a(a[m], aps, kRows + 16 * m, 16 * k, lane);
+#pragma unroll
+          for (int m = k; m < 4; ++m) mma16(y[m], a[m].lo, b.hi);
+#pragma unroll
+          for (int m = k; m < 4; ++m) mma16(y[m], a[m].hi, b.lo);
+#pragma unroll
+          for (int m = k; m < 4; ++m) mma16(y[m], a[m].hi, b.hi);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (m >= j >> 1) put_block(tp, kRows + 16 * m, j, y[m], 1.0f, lane);
+      }
+      // (the next chunk's K K^T comes after the product that reads this: nothing is written over before)
+      arrive(kTP);
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------------ the products
+    const uint32_t kq = smem_u32(smem + C::off_kq), tp = smem_u32(smem + C::off_tp), ss = smem_u32(smem + C::off_s),
+                   us = smem_u32(smem + C::off_u);
+    auto overlap = [&](int c) {  // [K; Q] K^T of chunk c
+      wait(kKQ0 + (c & 1), c >> 1);
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = umma_desc_sw128(kq + (c & 1) * 32768);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t at = a + (k >> 2) * (16384 >> 4) + (k & 3) * 2;
+          mma_f16(tmem + C::dkk, at, at, kIdesc<128, 64, false, false>, k > 0);
+        }
+        umma_commit(&bar[kKK]);
+      }
+      __syncwarp();
+    };
+    overlap(0);
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t kqc = kq + (c & 1) * 32768;
+      wait(kS, c);
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = umma_desc_sw128(kqc), b = desc_mn(ss, 16384);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_f16(tmem + C::d1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
+        umma_commit(&bar[kD1]);
+      }
+      __syncwarp();
+      wait(kTP, c);
+      wait(kR, c);
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = umma_desc_sw128(tp), b = desc_mn(us, 8192);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_f16(tmem + C::d2, a + 2 * k, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
+          mma_f16(tmem + C::d2, a + (kPart >> 4) + 2 * k, b + k * (2048 >> 4), kIdesc<128, n, false, true>, 1);
+        }
+        umma_commit(&bar[kD2]);
+      }
+      __syncwarp();
+      if (c + 1 < chunks) overlap(c + 1);
+      wait(kU, c);
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = desc_mn(kqc, 16384), b = desc_mn(us, 8192);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16(tmem + C::d3, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc<128, 2 * n, true, true>, k > 0);
+        umma_commit(&bar[kD3]);
+      }
+      __syncwarp();
+    }
+    if (*abort) {  // what was issued is done with before the TMEM goes
+      if (elect_one()) {
+        umma_commit(&bar[kDrain]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_suspend(&bar[kDrain], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ K, Q, z and the decays
+    const int hk = h / p.group;
+    // 16 lanes to a row of K or Q, so rows x0, x0 + 2, ..; a row's piece moves with its number's low three bits
+    const int piece = lane & 15, x0 = lane >> 4;
+    const __half* k0 = p.k + (d.first + x0) * p.k_row + hk * p.k_head + 8 * piece;
+    const __half* q0 = p.q + (d.first + x0) * p.q_row + hk * p.q_head + 8 * piece;
+    for (int c = 0; c < chunks; ++c) {
+      if (c >= 2) wait(kD3, c - 2);
+      const int first = c * kRows, have = min(kRows, rows - first);
+      const uint32_t to = smem_u32(smem + C::off_kq + (c & 1) * 32768) + (piece >> 3) * 16384 + x0 * 128;
+      auto copy = [&](const __half* src, int64_t step, uint32_t dst) {
+        src += (int64_t)first * step;
+#pragma unroll 8
+        for (int u = 0; u < kRows / 2; ++u) {
+          const bool there = 2 * u + x0 < have;
+          copy16(dst + u * 256 + (((piece & 7) ^ ((2 * u + x0) & 7)) << 4), there ? src + 2 * u * step : k0, there);
+        }
+      };
+      copy(k0, p.k_row, to);
+      copy(q0, p.q_row, to + 8192);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      Decays* dec = decays(c);
+      {
+        // Sums of g log2(e), two rows to a lane, in units of 2^-40; a decay of 2^-150 and below is as good as none left
+        // (and sums that grow are cut where 2^G is infinite by far).  A NaN stays one from its row on.
+        const int64_t row = d.first + first + 2 * lane;
+        float g[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (2 * lane + j < have) {
+            g[j] = p.g[(row + j) * p.nv + h];
+            b[j] = p.beta[(row + j) * p.nv + h];
+          }
+        long long x[2];
+        bool odd[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          odd[j] = g[j] != g[j];
+          const float y = fminf(fmaxf(g[j], -104.0f), 5000.0f);  // -150 log(2)
+          const float hi = y * 1.44269504f, lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
+          x[j] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
+        }
+        const unsigned any = __ballot_sync(0xffffffffu, odd[0] || odd[1]);
+        long long sum = x[0] + x[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += y;
+        }
+        const bool before = any & ((1u << lane) - 1);
+        const long long G[2] = {sum - x[1], sum};
+        float hi[2], lo[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const long long u = (G[j] + (1ll << 30)) >> 31;
+          hi[j] = (float)(int)u * (1.0f / 512.0f);
+          lo[j] = (float)(int)(G[j] - (u << 31)) * 9.094947017729282e-13f;  // 2^-40
+          if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
+        }
+        const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
+        const float hi_mid = __shfl_sync(0xffffffffu, hi[1], 15), lo_mid = __shfl_sync(0xffffffffu, lo[1], 15);
+        auto put2 = [&](float* at, float a, float c2) { *reinterpret_cast<float2*>(at + 2 * lane) = make_float2(a, c2); };
+        put2(dec->hi, hi[0], hi[1]);
+        put2(dec->lo, lo[0], lo[1]);
+        put2(dec->beta, b[0], b[1]);
+        put2(dec->keep, exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
+        put2(dec->left, exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
+        float m[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float e = (hi_mid - hi[j]) + (lo_mid - lo[j]);
+          m[j] = exp2_approx(lane < 16 ? e : -e);
+        }
+        put2(dec->mid, m[0], m[1]);
+      }
+      if (p.z) {
+        if (c >= 2) wait(kZFree0 + (c & 1), (c - 2) >> 1);
+        const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
+        const uint32_t zs = smem_u32(smem + C::off_z) + (c & 1) * kRows * n * 4;
+        if (p.z_wide) {
+          constexpr int lanes = n / 4;  // of a row
+#pragma unroll 8
+          for (int u = 0; u < kRows * lanes / 32; ++u) {
+            const int at = u * 32 + lane, x = at / lanes, pc = at % lanes;
+            const bool there = x < have;
+            copy16(zs + x * n * 4 + ((pc ^ (x & 7)) << 4), z0 + (there ? x * p.z_row : 0) + 4 * pc, there);
+          }
+        } else {
+          for (int u = 0; u < kRows * n / 32; ++u) {
+            const int at = u * 32 + lane, x = at / n, cl = at % n;
+            const bool there = x < have;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(zs + x * n * 4 + (((cl >> 2) ^ (x & 7)) << 4) + 4 * (cl & 3)),
+                         "l"(z0 + (there ? x * p.z_row : 0) + cl), "r"(there ? 4 : 0)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      if (!dbg.unreachable) arrive(kKQ0 + (c & 1));
+      if (p.z) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kZ0 + (c & 1)]);
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  // (no CTA leaves while another may still store into it)
+  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 12) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
+  }
+}
+
+template <int NS>
+cudaError_t launch(const GdnParams& p, const ChunkDebug& dbg, int* status, int dev, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = kv_smem_limit(gdn_chunk_kernel<NS>, Cfg<NS>::smem, dev, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * NS));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<NS>::smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = NS;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, dbg, status);
+}
+
+}  // namespace
+
+cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, cudaStream_t s) {
+  const ChunkDebug dbg{timeout_ns, unreachable};
+  return launch<2>(p, dbg, status, dev, s);
+}

@@ -41,8 +41,13 @@ struct GdnParams {
   int few;  // most rows of a sequence that goes through the steps' kernel
 };
 
-// x silu(x) and 1 / (1 + exp(-x)) by the fast exponential and division: off by some 2^-21 of themselves.
-FAK_DEV float gdn_silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+// x / (1 + exp(-x)) by the fast exponential and reciprocal: off by some 2^-21 of itself (below x = -88: zero).
+FAK_DEV float gdn_silu(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return x * r;
+}
 
 FAK_DEV float4 gdn_zero4() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
 
@@ -72,3 +77,6 @@ FAK_DEV float gdn_warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+
+// Host: the launch of the chunks' kernel (gdn_chunk.cu).
+cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, cudaStream_t s);

@@ -355,3 +355,24 @@ def test_calls_without_rows_or_sequences(fak):
         fak.fak_gdn_conv(batch, e(rows, 512), e(rows, 2), e(rows, 2), e(512, 4), e(2), e(2), e(1, 3, 512), h, h,
                          e(rows, 2, 128, dtype=torch.bfloat16), e(rows, 2), e(rows, 2))
         assert fak.fak_device_status() == 0 and torch.equal(state, keep) and bool((o == 7).all())
+
+
+@pytest.mark.parametrize("lengths", [[(130, 130)], [(70, 75), (1, 3), (300, 300)]])
+def test_a_wait_that_runs_out_is_recorded_and_ends(fak, lengths):
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 1)
+    q, k, v, g, beta, z, w = G.inputs(1, 2, rows, 15)
+    s0 = torch.randn(slots, 2, 128, 128, device="cuda")
+    batch = fak.GDNBatch(start, kv_len, slot)
+    fak.fak_gdn_debug_wait(1000000, 1)
+    try:
+        fak.fak_gdn_attn(batch, q, k, v, g, beta, s0.clone(), torch.empty(rows, 2, 128, device="cuda"), 300, z=z, norm_w=w)
+        assert fak.fak_device_status() == 5
+    finally:
+        fak.fak_gdn_debug_wait()
+    outs = []
+    for _ in range(2):
+        s, o = s0.clone(), torch.zeros(rows, 2, 128, device="cuda")
+        fak.fak_gdn_attn(batch, q, k, v, g, beta, s, o, 300, z=z, norm_w=w)
+        outs.append((s, o))
+    assert fak.fak_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and bool(torch.isfinite(outs[0][1]).all())
