@@ -624,7 +624,8 @@ typedef struct {
     int32_t n_slots;            /* of state */
     float scale, eps;           /* scale > 0 */
     int64_t rows;
-    const void *q, *k;          /* device f16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned, strides too */
+    const void *q, *k;          /* device f16; head h of row r at q + r * q_row + h * q_head; 16-byte aligned, strides too,
+                                   above 0, and below 2^40 bytes */
     const void* v;              /* device bf16, same form */
     int64_t q_row, q_head, k_row, k_head, v_row, v_head;
     const float *g, *beta;      /* device [rows][nv] */
@@ -632,7 +633,7 @@ typedef struct {
     const float* norm_w;        /* device [128], 16-byte aligned; NULL: no norm */
     const float* z;             /* device f32, any strides (wide loads where vectors stand on 16 bytes); NULL: no gate */
     int64_t z_row, z_head;
-    void* out;                  /* device, same form, 16-byte aligned */
+    void* out;                  /* device, 16-byte aligned, strides too */
     int64_t out_row, out_head;
 } fak_gdn_args;
 int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* args, fak_stream_t stream);

@@ -377,6 +377,10 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
                          (uintptr_t)a->out;
   const int64_t two = p.q_row | p.q_head | p.k_row | p.k_head | p.v_row | p.v_head;  // strides of 16-bit rows
   const int64_t out = p.out_row | p.out_head;
+  const auto fits = [](int64_t stride, int64_t n, int elem) { return n <= 1 || (stride > 0 && stride < (1LL << 40) / elem); };
+  if (!fits(p.q_row, a->rows, 2) || !fits(p.q_head, a->nk, 2) || !fits(p.k_row, a->rows, 2) || !fits(p.k_head, a->nk, 2) ||
+      !fits(p.v_row, a->rows, 2) || !fits(p.v_head, a->nv, 2))
+    return FAK_ERR_INVALID_ARG;
   if ((bits & 15) || (two & 7) || (out & (a->out_type == FAK_ROWS_F32 ? 3 : 7)) || 
       (((uintptr_t)a->g | (uintptr_t)a->beta | (uintptr_t)a->z) & 3))
     return FAK_ERR_ALIGN;
@@ -392,7 +396,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   p.beta = a->beta;
   p.norm_w = a->norm_w;
   p.z = a->z;
-  p.z_wide = !(((uintptr_t)a->z & 15) | ((p.z_row | p.z_head) & 3));
+  p.z_wide = !(((uintptr_t)a->z & 15) | ((p.z_row | p.z_head) & 3)) && fits(p.z_row, a->rows, 4) && fits(p.z_head, a->nv, 4);
   p.state = a->state;
   p.out = a->out;
   p.scale = a->scale;

@@ -21,14 +21,19 @@
 //             or T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128
 //   8 .. 11   T and P T: decays into A and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T,
 //             by m16n8k16 instructions
-//   12        issues the products;  13  copies K, Q and z, sums the decays.
+//   12        issues the products;  13  copies K, Q and z by TMA;  14  sums the decays.
 // The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
 // B's columns, so B's two parts stand side by side as 2 n columns, one read of A for both.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
+#include <cstring>
+#include <mutex>
 
 #include "attn_device.cuh"
 #include "fak.h"
@@ -41,7 +46,7 @@ namespace {
 
 constexpr int kRows = 64;  // of a chunk
 constexpr int kChainThreads = 256, kPrepThreads = 128;
-constexpr int kThreads = kChainThreads + kPrepThreads + 64;
+constexpr int kThreads = kChainThreads + kPrepThreads + 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
 constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
 
@@ -64,21 +69,22 @@ struct Cfg {
   static constexpr int off_ap = off_tp + 2 * kPart;                // [A; P], two parts
   static constexpr int off_s = off_ap + 2 * kPart;                 // S, two parts
   static constexpr int off_u = off_s + 2 * panels * 16384;         // R, then U, two parts
-  static constexpr int off_z = off_u + 2 * panels * 8192;          // two stages of z
-  static constexpr int off_a = off_z + 2 * kRows * n * 4;          // A's blocks of 16 x 16 on the diagonal in f32
+  static constexpr int off_v = off_u + 2 * panels * 8192;          // two stages of V: panels of 64 columns
+  static constexpr int off_z = off_v + 2 * panels * 8192;          // z, then the output: panels of 32 columns, 128 bytes
+  static constexpr int off_a = off_z + kRows * n * 4;          // A's blocks of 16 x 16 on the diagonal in f32
   static constexpr int off_dec = off_a + 4 * 16 * kLd * 4;
   static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 2][64]
   static constexpr int off_gain = off_sum + 2 * NS * 2 * kRows * 4;
   static constexpr int off_max = off_gain + n * 4;  // [8]
   static constexpr int off_bar = off_max + 32;
-  static constexpr int smem = off_bar + 160 + 1024;
+  static constexpr int smem = off_bar + 192 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
   static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n, dkk = 6 * n;  // TMEM columns
   static constexpr int tmem_cols = 512;
   static_assert(dkk + 64 <= tmem_cols, "TMEM");
 };
 
-enum Bars { kD1, kD2, kD3, kKK, kTP, kKQ0, kKQ1, kZ0, kZ1, kZFree0, kZFree1, kS, kR, kU, kSum0, kSum1, kDrain, kBars };
+enum Bars { kLand0, kLand1, kD1, kD2, kD3, kKK, kTP, kKQ0, kKQ1, kV0, kV1, kZ, kZFree, kS, kR, kU, kSum0, kSum1, kDrain, kBars };
 
 template <int M, int N, bool A_MN, bool B_MN>
 constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -127,8 +133,8 @@ FAK_DEV bool try_cluster(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-FAK_DEV void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+FAK_DEV void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
 // Two f32 as the sum of two pairs of f16.
@@ -140,17 +146,20 @@ FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// Columns col .. col + 7 (a multiple of 8) of a row of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
-// second part `part` bytes behind the first.
-FAK_DEV void put_halves8(unsigned char* tile, int panel, int part, int row, int col, const float* x) {
-  uint4 hi, lo;
-  split_half(x[0], x[1], hi.x, lo.x);
-  split_half(x[2], x[3], hi.y, lo.y);
-  split_half(x[4], x[5], hi.z, lo.z);
-  split_half(x[6], x[7], hi.w, lo.w);
-  unsigned char* at = tile + (col >> 6) * panel + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
-  *reinterpret_cast<uint4*>(at) = hi;
-  *reinterpret_cast<uint4*>(at + part) = lo;
+// Columns of a row (from a multiple of 8 on) of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
+// second part `part` bytes behind the first.  Every value is made before the first is stored, so that none waits for a store's turn.
+template <int N>
+FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int col, const float (&x)[N]) {
+  uint32_t hi[N / 2], lo[N / 2];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) split_half(x[i], x[i + 1], hi[i / 2], lo[i / 2]);
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    const int c = col + i;
+    unsigned char* at = tile + (c >> 6) * panel + row * 128 + ((((c >> 3) & 7) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[i / 2], hi[i / 2 + 1], hi[i / 2 + 2], hi[i / 2 + 3]);
+    *reinterpret_cast<uint4*>(at + part) = make_uint4(lo[i / 2], lo[i / 2 + 1], lo[i / 2 + 2], lo[i / 2 + 3]);
+  }
 }
 
 template <int N>
@@ -228,15 +237,20 @@ FAK_DEV void put_block(unsigned char* tile, int r0, int j, const float (&c)[4], 
   }
 }
 
+struct ChunkMaps {
+  CUtensorMap k, q, v, z;
+};
+
 struct ChunkDebug {
   unsigned long long timeout_ns;
   int unreachable;  // a test's: 1 where K and Q are never to count as landed
 };
 
 template <int NS>
-__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, ChunkDebug dbg, int* status) {
+__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, const __grid_constant__ ChunkMaps maps, ChunkDebug dbg,
+                                                                 int* status) {
   using C = Cfg<NS>;
-  constexpr int n = C::n, W = C::cols, B = 16;  // B: columns a chain thread takes at a time
+  constexpr int n = C::n, W = C::cols, B = 32;  // B: columns a chain thread takes at a time
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::off_bar);
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 8 : i == kTP || i == kR || i == kU || i == kZFree0 || i == kZFree1 ? 4 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 8 : i == kTP || i == kR || i == kU || i == kZFree ? 4 : i == kKQ0 || i == kKQ1 ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
@@ -303,6 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   };
   auto decays = [&](int c) { return reinterpret_cast<Decays*>(smem + C::off_dec) + (c & 3); };
 
+  // registers: the chain's threads hold S; 2 * 160 + 128 + 56 of the 4 * 128 that the block has
+  if (warp < 8)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+  else if (warp >= 12)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+
   if (warp < 8) {
     // ------------------------------------------------------------------ the chain
     const int quarter = warp & 3, half = warp >> 2;
@@ -324,33 +344,30 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     }
     uint32_t v[W / 2];  // of the next chunk
     auto fetch_v = [&](int c) {
-      const int row = c * kRows + t;
-      if (row < rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.v + (int64_t)(d.first + row) * p.v_row + h * p.v_head + col0 + col);
+      wait(kV0 + (c & 1), c >> 1);
+      const unsigned char* src = smem + C::off_v + (c & 1) * C::panels * 8192 + (col >> 6) * 8192 + t * 128;
+      const bool there = c * kRows + t < rows;  // (what stands behind the last row is another's, whatever it holds)
 #pragma unroll
-        for (int i = 0; i < W / 8; ++i) {
-          const uint4 x = src[i];
-          v[4 * i] = x.x;
-          v[4 * i + 1] = x.y;
-          v[4 * i + 2] = x.z;
-          v[4 * i + 3] = x.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) v[i] = 0;
+      for (int i = 0; i < W / 8; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + (((((col & 63) >> 3) + i) ^ (t & 7)) << 4));
+        v[4 * i] = there ? x.x : 0;
+        v[4 * i + 1] = there ? x.y : 0;
+        v[4 * i + 2] = there ? x.z : 0;
+        v[4 * i + 3] = there ? x.w : 0;
       }
     };
     float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
     // S scaled and in two parts to shared memory; all chain threads' S and V are looked at
     auto put_state = [&]() {
-      float m = 0.0f;
+      float ms[4] = {};
 #pragma unroll
-      for (int i = 0; i < W; i += 2) m = fmaxf(fmaxf(m, fabsf(S[i])), fabsf(S[i + 1]));
+      for (int i = 0; i < W; i += 2) ms[i / 2 & 3] = fmaxf(fmaxf(ms[i / 2 & 3], fabsf(S[i])), fabsf(S[i + 1]));
       if (top) {
 #pragma unroll
         for (int i = 0; i < W / 2; ++i)
-          m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i] << 16))), fabsf(__uint_as_float(v[i] & 0xffff0000u)));
+          ms[i & 3] = fmaxf(fmaxf(ms[i & 3], fabsf(__uint_as_float(v[i] << 16))), fabsf(__uint_as_float(v[i] & 0xffff0000u)));
       }
+      float m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
       m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
       if (lane == 0) most[warp] = m;
       named_bar_sync(1, kChainThreads);
@@ -361,13 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       const int by = e == 0 || e == 255 ? 0 : min(max(132 - e, -120), 120);
       up = __uint_as_float((uint32_t)(127 + by) << 23);
       down = __uint_as_float((uint32_t)(127 - by) << 23);
+      float x[W];
 #pragma unroll
-      for (int i = 0; i < W; i += 8) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = S[i + j] * up;
-        put_halves8(smem + C::off_s, 16384, C::panels * 16384, key, col + i, x);
-      }
+      for (int i = 0; i < W; ++i) x[i] = S[i] * up;
+      put_halves<W>(smem + C::off_s, 16384, C::panels * 16384, key, col, x);
     };
     const uint32_t sum_to = smem_u32(smem + C::off_sum);
     const int me = NS > 1 ? (int)rank_in_cluster() : 0;
@@ -391,8 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
             x[j] = fmaf(bk, x[j], __uint_as_float(v[(i + j) / 2] << 16) * bu);
             x[j + 1] = fmaf(bk, x[j + 1], __uint_as_float(v[(i + j) / 2] & 0xffff0000u) * bu);
           }
-#pragma unroll
-          for (int j = 0; j < B; j += 8) put_halves8(smem + C::off_u, 8192, C::panels * 8192, t, col + i + j, x + j);
+          put_halves<B>(smem + C::off_u, 8192, C::panels * 8192, t, col + i, x);
         }
         arrive(kR);
         wait(kD2, c);
@@ -403,11 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           ld_sums<B>(acc + C::d2 + i, n, x);
 #pragma unroll
           for (int j = 0; j < B; ++j) x[j] *= left;
-#pragma unroll
-          for (int j = 0; j < B; j += 8) put_halves8(smem + C::off_u, 8192, C::panels * 8192, t, col + i + j, x + j);
+          put_halves<B>(smem + C::off_u, 8192, C::panels * 8192, t, col + i, x);
         }
         arrive(kU);
-        fetch_v(c + 1);
+        if (c + 1 < chunks) fetch_v(c + 1);
       } else {
         const int64_t row = d.first + c * kRows + t;
         const float by = down * p.scale;
@@ -448,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           for (int i = 0; i < 2 * NS; ++i) ss += sums[i * kRows];
           r = rsqrtf(fmaf(ss, 1.0f / kGdnDim, p.eps));
         }
-        if (p.z) wait(kZ0 + (c & 1), c >> 1);
-        const unsigned char* zs = smem + C::off_z + ((c & 1) * kRows + t) * n * 4;
+        // the thread's own line of z, 32 columns, where its output goes too, on its way to a copy of its own
+        if (p.z) wait(kZ, c);
+        unsigned char* zs = smem + C::off_z + half * kRows * 128 + t * 128;
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
           const float4 w = *reinterpret_cast<const float4*>(gain + col + i);
@@ -457,32 +470,35 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           o[i + 1] *= r * w.y;
           o[i + 2] *= r * w.z;
           o[i + 3] *= r * w.w;
-          if (p.z) {
-            const float4 z = *reinterpret_cast<const float4*>(zs + ((((col + i) >> 2) ^ (t & 7)) << 4));
+        }
+        if (p.z) {
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(zs + (((i >> 2) ^ (t & 7)) << 4));
             o[i] *= gdn_silu(z.x);
             o[i + 1] *= gdn_silu(z.y);
             o[i + 2] *= gdn_silu(z.z);
             o[i + 3] *= gdn_silu(z.w);
           }
         }
-        if (p.z) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[kZFree0 + (c & 1)]);
-        }
         if (c * kRows + t < rows && !*abort) {
           const int64_t to = row * p.out_row + h * p.out_head + col0 + col;
           if (p.out_bf16) {
+            zs += (t & 1) * 64;  // (four lanes' rows on the same banks, not eight)
 #pragma unroll
             for (int i = 0; i < W; i += 8)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + i) =
-                  make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]), pack_bf16(o[i + 4], o[i + 5]),
-                             pack_bf16(o[i + 6], o[i + 7]));
+              *reinterpret_cast<uint4*>(zs + 2 * i) = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
+                                                                 pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
+            fence_async();
+            bulk_s2g(static_cast<__nv_bfloat16*>(p.out) + to, smem_u32(zs), 2 * W);
           } else {
 #pragma unroll
-            for (int i = 0; i < W; i += 4)
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(zs + 4 * i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            fence_async();
+            bulk_s2g(static_cast<float*>(p.out) + to, smem_u32(zs), 4 * W);
           }
         }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
       wait(kD3, c);
       tc_fence_after_sync();
@@ -493,12 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < B; ++j) S[i + j] = fmaf(all, S[i + j], x[j] * down);
       }
+      if (!top) {  // the output has left its place, to z
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kZFree]);
+      }
       if (c + 1 < chunks) {
         put_state();
         wait(kKQ0 + ((c + 1) & 1), (c + 1) >> 1);
         arrive(kS);
       }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!*abort) {
 #pragma unroll
       for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(st + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
@@ -525,42 +547,37 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         float x[32];
         ld_cols<32>(acc + own, x);
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + i + j]);
-            const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + i + j]);
-            y[j] = b * exp2_approx((hi - u.x) + (lo - l.x)) * x[i + j];
-            y[j + 1] = b * exp2_approx((hi - u.y) + (lo - l.y)) * x[i + j + 1];
-            y[j + 2] = b * exp2_approx((hi - u.z) + (lo - l.z)) * x[i + j + 2];
-            y[j + 3] = b * exp2_approx((hi - u.w) + (lo - l.w)) * x[i + j + 3];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = i + j <= last ? y[j] : 0.0f;
-          put_halves8(ap, 0, kPart, r, own + i, y);
-          if (top && (lane >> 4) == i >> 4) {
-            float* to = diag + t * kLd + (i & 8);
-            *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
-          }
+        for (int i = 0; i < 32; i += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + i]);
+          const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + i]);
+          x[i] *= b * exp2_approx((hi - u.x) + (lo - l.x));
+          x[i + 1] *= b * exp2_approx((hi - u.y) + (lo - l.y));
+          x[i + 2] *= b * exp2_approx((hi - u.z) + (lo - l.z));
+          x[i + 3] *= b * exp2_approx((hi - u.w) + (lo - l.w));
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = i <= last ? x[i] : 0.0f;
+        if (top) {
+          float* to = diag + t * kLd;
+          const bool second = lane >= 16;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(to + i) = second ? make_float4(x[16 + i], x[17 + i], x[18 + i], x[19 + i])
+                                                        : make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+        put_halves<32>(ap, 0, kPart, r, own, x);
         if (late) {
           const float f = b * dec->mid[t];
           ld_cols<32>(acc, x);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 u = *reinterpret_cast<const float4*>(&dec->mid[i + j]);
-              y[j] = f * u.x * x[i + j];
-              y[j + 1] = f * u.y * x[i + j + 1];
-              y[j + 2] = f * u.z * x[i + j + 2];
-              y[j + 3] = f * u.w * x[i + j + 3];
-            }
-            put_halves8(ap, 0, kPart, r, i, y);
+          for (int i = 0; i < 32; i += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(&dec->mid[i]);
+            x[i] *= f * u.x;
+            x[i + 1] *= f * u.y;
+            x[i + 2] *= f * u.z;
+            x[i + 3] *= f * u.w;
           }
+          put_halves<32>(ap, 0, kPart, r, 0, x);
         }
       }
       named_bar_sync(2, kPrepThreads);
@@ -585,28 +602,29 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
           for (int j = i - 1; j >= 0; --j) x[j] = fmaf(-x[i], y[j], x[j]);
         }
-        if (lane < 16) {
-          put_halves8(tp, 0, kPart, 16 * w + row, 16 * w, x);
-          put_halves8(tp, 0, kPart, 16 * w + row, 16 * w + 8, x + 8);
-        }
+        if (lane < 16) put_halves<16>(tp, 0, kPart, 16 * w + row, 16 * w, x);
       }
       named_bar_sync(2, kPrepThreads);
       {
         // two blocks of 32: the lower left is -T22 (A21 T11), eight columns to a warp
         const int at = 32 * (w >> 1), j = (at >> 3) + (w & 1);
-        float x[4] = {}, y[4] = {};
+        float x[4] = {}, y[4] = {}, x1[4] = {}, y1[4] = {}, x2[4] = {}, y2[4] = {};  // (products that do not wait for each other)
         FragA a, u;
         FragB b;
         load_a(a, aps, at + 16, at, lane);
         load_a(u, tps, at + 16, at + 16, lane);
         load_b(b, tps, at, j, lane);
-        mma16(x, a.lo, b.hi);
-        mma16(x, a.hi, b.lo);
+        mma16(x1, a.lo, b.hi);
+        mma16(x2, a.hi, b.lo);
         mma16(x, a.hi, b.hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += x1[i] + x2[i];
         turn_b(b, x);
-        mma16(y, u.lo, b.hi);
-        mma16(y, u.hi, b.lo);
+        mma16(y1, u.lo, b.hi);
+        mma16(y2, u.hi, b.lo);
         mma16(y, u.hi, b.hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] += y1[i] + y2[i];
         put_block(tp, at + 16, j, y, -1.0f, lane);
       }
       named_bar_sync(2, kPrepThreads);
@@ -733,114 +751,132 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
       __syncwarp();
     }
-  } else {
-    // ------------------------------------------------------------------ K, Q, z and the decays
+  } else if (warp == 13) {
+    // ------------------------------------------------------------------ K, Q and z
     const int hk = h / p.group;
-    // 16 lanes to a row of K or Q, so rows x0, x0 + 2, ..; a row's piece moves with its number's low three bits
-    const int piece = lane & 15, x0 = lane >> 4;
-    const __half* k0 = p.k + (d.first + x0) * p.k_row + hk * p.k_head + 8 * piece;
-    const __half* q0 = p.q + (d.first + x0) * p.q_row + hk * p.q_head + 8 * piece;
     for (int c = 0; c < chunks; ++c) {
       if (c >= 2) wait(kD3, c - 2);
       const int first = c * kRows, have = min(kRows, rows - first);
-      const uint32_t to = smem_u32(smem + C::off_kq + (c & 1) * 32768) + (piece >> 3) * 16384 + x0 * 128;
-      auto copy = [&](const __half* src, int64_t step, uint32_t dst) {
-        src += (int64_t)first * step;
-#pragma unroll 8
-        for (int u = 0; u < kRows / 2; ++u) {
-          const bool there = 2 * u + x0 < have;
-          copy16(dst + u * 256 + (((piece & 7) ^ ((2 * u + x0) & 7)) << 4), there ? src + 2 * u * step : k0, there);
-        }
-      };
-      copy(k0, p.k_row, to);
-      copy(q0, p.q_row, to + 8192);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      Decays* dec = decays(c);
-      {
-        // Sums of g log2(e), two rows to a lane, in units of 2^-40; a decay of 2^-150 and below is as good as none left
-        // (and sums that grow are cut where 2^G is infinite by far).  A NaN stays one from its row on.
-        const int64_t row = d.first + first + 2 * lane;
-        float g[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
+      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar[kLand0 + (c & 1)], 32768);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (2 * lane + j < have) {
-            g[j] = p.g[(row + j) * p.nv + h];
-            b[j] = p.beta[(row + j) * p.nv + h];
-          }
-        long long x[2];
-        bool odd[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          odd[j] = g[j] != g[j];
-          const float y = fminf(fmaxf(g[j], -104.0f), 5000.0f);  // -150 log(2)
-          const float hi = y * 1.44269504f, lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
-          x[j] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
+        for (int i = 0; i < 2; ++i) {
+          tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, d.first + first, &bar[kLand0 + (c & 1)]);
+          tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, d.first + first, &bar[kLand0 + (c & 1)]);
         }
-        const unsigned any = __ballot_sync(0xffffffffu, odd[0] || odd[1]);
-        long long sum = x[0] + x[1];
+        // (V of two chunks before is in registers since that chunk's state was made)
+        mbar_arrive_expect_tx(&bar[kV0 + (c & 1)], kRows * n * 2);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += y;
-        }
-        const bool before = any & ((1u << lane) - 1);
-        const long long G[2] = {sum - x[1], sum};
-        float hi[2], lo[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const long long u = (G[j] + (1ll << 30)) >> 31;
-          hi[j] = (float)(int)u * (1.0f / 512.0f);
-          lo[j] = (float)(int)(G[j] - (u << 31)) * 9.094947017729282e-13f;  // 2^-40
-          if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
-        }
-        const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
-        const float hi_mid = __shfl_sync(0xffffffffu, hi[1], 15), lo_mid = __shfl_sync(0xffffffffu, lo[1], 15);
-        auto put2 = [&](float* at, float a, float c2) { *reinterpret_cast<float2*>(at + 2 * lane) = make_float2(a, c2); };
-        put2(dec->hi, hi[0], hi[1]);
-        put2(dec->lo, lo[0], lo[1]);
-        put2(dec->beta, b[0], b[1]);
-        put2(dec->keep, exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
-        put2(dec->left, exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
-        float m[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float e = (hi_mid - hi[j]) + (lo_mid - lo[j]);
-          m[j] = exp2_approx(lane < 16 ? e : -e);
-        }
-        put2(dec->mid, m[0], m[1]);
+        for (int i = 0; i < C::panels; ++i)
+          tma_load_3d_tx(smem + C::off_v + ((c & 1) * C::panels + i) * 8192, &maps.v, col0 + 64 * i, h, d.first + first, &bar[kV0 + (c & 1)]);
       }
-      if (p.z) {
-        if (c >= 2) wait(kZFree0 + (c & 1), (c - 2) >> 1);
-        const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
-        const uint32_t zs = smem_u32(smem + C::off_z) + (c & 1) * kRows * n * 4;
-        if (p.z_wide) {
-          constexpr int lanes = n / 4;  // of a row
-#pragma unroll 8
-          for (int u = 0; u < kRows * lanes / 32; ++u) {
-            const int at = u * 32 + lane, x = at / lanes, pc = at % lanes;
-            const bool there = x < have;
-            copy16(zs + x * n * 4 + ((pc ^ (x & 7)) << 4), z0 + (there ? x * p.z_row : 0) + 4 * pc, there);
-          }
-        } else {
-          for (int u = 0; u < kRows * n / 32; ++u) {
-            const int at = u * 32 + lane, x = at / n, cl = at % n;
-            const bool there = x < have;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(zs + x * n * 4 + (((cl >> 2) ^ (x & 7)) << 4) + 4 * (cl & 3)),
-                         "l"(z0 + (there ? x * p.z_row : 0) + cl), "r"(there ? 4 : 0)
-                         : "memory");
-          }
+      __syncwarp();
+      wait(kLand0 + (c & 1), c >> 1);
+      if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
+        for (int i = lane; i < (kRows - have) * 32; i += 32) {
+          const int row = have + (i >> 5), at = i & 31;
+          *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
       if (!dbg.unreachable) arrive(kKQ0 + (c & 1));
       if (p.z) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kZ0 + (c & 1)]);
+        if (c >= 1) wait(kZFree, c - 1);
+        unsigned char* zs = smem + C::off_z;
+        if (p.z_wide) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
+#pragma unroll
+            for (int i = 0; i < n / 32; ++i)
+              tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, d.first + first, &bar[kZ]);
+          }
+          __syncwarp();
+        } else {
+          const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
+#pragma unroll 8
+          for (int u = 0; u < kRows * n / 32; ++u) {
+            const int at = u * 32 + lane, x = at / n, cl = at % n;
+            if (x < have)
+              *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
+                  z0[x * p.z_row + cl];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[kZ]);
+        }
       }
+    }
+    if (*abort) {  // no copy is in flight when the block ends
+      auto drain = [&](int b, int phase) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 100000000ull) {
+        }
+      };
+      for (int c = max(0, chunks - 2); c < chunks; ++c) {
+        drain(kLand0 + (c & 1), c >> 1);
+        drain(kV0 + (c & 1), c >> 1);
+      }
+      if (p.z && p.z_wide) drain(kZ, chunks - 1);
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------------------------ the decays
+    float g[2], b[2];
+    auto fetch = [&](int c) {  // two rows to a lane
+      const int at = c * kRows + 2 * lane;
+      const int64_t row = d.first + at;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        g[j] = at + j < rows ? p.g[(row + j) * p.nv + h] : 0.0f;
+        b[j] = at + j < rows ? p.beta[(row + j) * p.nv + h] : 0.0f;
+      }
+    };
+    fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+      // Sums of g log2(e) in units of 2^-40; a decay of 2^-150 and below is as good as none left (and sums that grow are cut
+      // where 2^G is infinite by far).  A NaN stays one from its row on.
+      long long x[2];
+      bool odd[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        odd[j] = g[j] != g[j];
+        const float y = fminf(fmaxf(g[j], -104.0f), 5000.0f);  // -150 log(2)
+        const float hi = y * 1.44269504f, lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
+        x[j] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
+      }
+      const float beta[2] = {b[0], b[1]};
+      const unsigned any = __ballot_sync(0xffffffffu, odd[0] || odd[1]);
+      fetch(c + 1);
+      long long sum = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const bool before = any & ((1u << lane) - 1);
+      const long long G[2] = {sum - x[1], sum};
+      float hi[2], lo[2], mid[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const long long u = (G[j] + (1ll << 30)) >> 31;
+        hi[j] = (float)(int)u * (1.0f / 512.0f);
+        lo[j] = (float)(int)(G[j] - (u << 31)) * 9.094947017729282e-13f;  // 2^-40
+        if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
+      }
+      const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
+      const float hi_mid = __shfl_sync(0xffffffffu, hi[1], 15), lo_mid = __shfl_sync(0xffffffffu, lo[1], 15);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float e = (hi_mid - hi[j]) + (lo_mid - lo[j]);
+        mid[j] = exp2_approx(lane < 16 ? e : -e);
+      }
+      if (c >= 2) wait(kD3, c - 2);
+      Decays* dec = decays(c);
+      auto put2 = [&](float* at, float y0, float y1) { *reinterpret_cast<float2*>(at + 2 * lane) = make_float2(y0, y1); };
+      put2(dec->hi, hi[0], hi[1]);
+      put2(dec->lo, lo[0], lo[1]);
+      put2(dec->beta, beta[0], beta[1]);
+      put2(dec->keep, exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
+      put2(dec->left, exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
+      put2(dec->mid, mid[0], mid[1]);
+      arrive(kKQ0 + (c & 1));
     }
   }
   tc_fence_before_sync();
@@ -853,8 +889,35 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   }
 }
 
+std::mutex g_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+cudaError_t encoder() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_encode) return cudaSuccess;
+  cudaDriverEntryPointQueryResult q;
+  void* fn = nullptr;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+  g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return cudaSuccess;
+}
+
+// Rows [row][head][128], boxes of 64 rows of one head's 128 bytes.  (A stride that is never taken may be anything.)
+bool rows_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int64_t rows, int heads, int64_t row, int64_t head) {
+  const cuuint64_t elem = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+  const cuuint64_t dim[3] = {kGdnDim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t by_head = heads > 1 ? (cuuint64_t)head * elem : kGdnDim * elem;
+  const cuuint64_t stride[2] = {by_head, rows > 1 ? (cuuint64_t)row * elem : by_head * heads};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), 1, kRows}, one[3] = {1, 1, 1};
+  return g_encode(map, type, 3, const_cast<void*>(base), dim, stride,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int NS>
-cudaError_t launch(const GdnParams& p, const ChunkDebug& dbg, int* status, int dev, cudaStream_t s) {
+cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const ChunkDebug& dbg, int* status, int dev, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = kv_smem_limit(gdn_chunk_kernel<NS>, Cfg<NS>::smem, dev, done);
   if (e != cudaSuccess) return e;
@@ -869,12 +932,22 @@ cudaError_t launch(const GdnParams& p, const ChunkDebug& dbg, int* status, int d
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, dbg, status);
+  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, maps, dbg, status);
 }
 
 }  // namespace
 
 cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, cudaStream_t s) {
+  const cudaError_t e = encoder();
+  if (e != cudaSuccess) return e;
+  ChunkMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  const int nk = p.nv / p.group;
+  if (!rows_map(&maps.k, p.k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.c.rows, nk, p.k_row, p.k_head) ||
+      !rows_map(&maps.q, p.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.c.rows, nk, p.q_row, p.q_head) ||
+      !rows_map(&maps.v, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.c.rows, p.nv, p.v_row, p.v_head) ||
+      (p.z && p.z_wide && !rows_map(&maps.z, p.z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.c.rows, p.nv, p.z_row, p.z_head)))
+    return cudaErrorInvalidValue;
   const ChunkDebug dbg{timeout_ns, unreachable};
-  return launch<2>(p, dbg, status, dev, s);
+  return launch<2>(p, maps, dbg, status, dev, s);
 }
