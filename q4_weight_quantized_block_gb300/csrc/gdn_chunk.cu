@@ -17,11 +17,12 @@
 //
 // A cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own rule: only the
 // norm needs the whole row, and its sums of squares go to the other CTAs by asynchronous stores.  Warps:
-//   0 .. 7    the chain: a warp reads the accumulators' 32 lanes (w % 4) and half their columns (w / 4); lanes 0..63 are K's
-//             or T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128
-//   8 .. 11   T and P T: decays into A and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T,
+//   0 .. 15   the chain: a warp reads the accumulators' 32 lanes (w % 4) and a quarter of their columns (w / 4); lanes 0..63
+//             are K's or T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all
+//             128.  (With eight warps a step took twice as long: one warp issues an instruction in four cycles.)
+//   16 .. 19  T and P T: decays into A and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T,
 //             by m16n8k16 instructions
-//   12        issues the products;  13  copies K, Q and z by TMA;  14  sums the decays.
+//   20        issues the products;  21  copies K, Q, V and z by TMA;  22  sums the decays.
 // The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
 // B's columns, so B's two parts stand side by side as 2 n columns, one read of A for both.
 #include <cuda.h>
@@ -45,7 +46,7 @@
 namespace {
 
 constexpr int kRows = 64;  // of a chunk
-constexpr int kChainThreads = 256, kPrepThreads = 128;
+constexpr int kChainThreads = 512, kPrepThreads = 128;
 constexpr int kThreads = kChainThreads + kPrepThreads + 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
 constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
@@ -62,7 +63,7 @@ struct Decays {
 template <int NS>
 struct Cfg {
   static constexpr int n = kGdnDim / NS;        // value columns of a CTA
-  static constexpr int cols = n / 2;            // of a chain thread
+  static constexpr int cols = n / 4;            // of a chain thread
   static constexpr int panels = (n + 63) / 64;  // of 64 columns, 128 bytes
   static constexpr int off_kq = 0;                                 // two stages of [K; Q]: two panels of 128 rows
   static constexpr int off_tp = off_kq + 2 * 32768;                // [T; P T], two parts
@@ -70,13 +71,13 @@ struct Cfg {
   static constexpr int off_s = off_ap + 2 * kPart;                 // S, two parts
   static constexpr int off_u = off_s + 2 * panels * 16384;         // R, then U, two parts
   static constexpr int off_v = off_u + 2 * panels * 8192;          // two stages of V: panels of 64 columns
-  static constexpr int off_z = off_v + 2 * panels * 8192;          // z, then the output: panels of 32 columns, 128 bytes
+  static constexpr int off_z = off_v + 2 * panels * 8192;          // z: panels of 32 columns, 128 bytes
   static constexpr int off_a = off_z + kRows * n * 4;          // A's blocks of 16 x 16 on the diagonal in f32
   static constexpr int off_dec = off_a + 4 * 16 * kLd * 4;
-  static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 2][64]
-  static constexpr int off_gain = off_sum + 2 * NS * 2 * kRows * 4;
-  static constexpr int off_max = off_gain + n * 4;  // [8]
-  static constexpr int off_bar = off_max + 32;
+  static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 4][64]
+  static constexpr int off_gain = off_sum + 2 * NS * 4 * kRows * 4;
+  static constexpr int off_max = off_gain + n * 4;  // [16]
+  static constexpr int off_bar = off_max + 64;
   static constexpr int smem = off_bar + 192 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
   static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n, dkk = 6 * n;  // TMEM columns
@@ -133,15 +134,40 @@ FAK_DEV bool try_cluster(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-FAK_DEV void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+// Two f32 operations in one instruction.
+FAK_DEV uint64_t pair_bits(float2 a) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a.x), "f"(a.y));
+  return d;
 }
+FAK_DEV float2 bits_pair(uint64_t d) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
+  return a;
+}
+FAK_DEV float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(d);
+}
+FAK_DEV float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(d);
+}
+FAK_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(d);
+}
+FAK_DEV float2 both(float a) { return make_float2(a, a); }
+FAK_DEV float2 bf16_pair(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 
 // Two f32 as the sum of two pairs of f16.
 FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
-  const float2 b = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+  const float2 b = fma2(__half22float2(h), both(-1.0f), make_float2(x, y));
+  const __half2 l = __floats2half2_rn(b.x, b.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -149,10 +175,10 @@ FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
 // Columns of a row (from a multiple of 8 on) of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
 // second part `part` bytes behind the first.  Every value is made before the first is stored, so that none waits for a store's turn.
 template <int N>
-FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int col, const float (&x)[N]) {
+FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int col, const float2 (&x)[N / 2]) {
   uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
-  for (int i = 0; i < N; i += 2) split_half(x[i], x[i + 1], hi[i / 2], lo[i / 2]);
+  for (int i = 0; i < N / 2; ++i) split_half(x[i].x, x[i].y, hi[i], lo[i]);
 #pragma unroll
   for (int i = 0; i < N; i += 8) {
     const int c = col + i;
@@ -163,22 +189,24 @@ FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int c
 }
 
 template <int N>
-FAK_DEV void ld_cols(uint32_t addr, float (&x)[N]) {
+FAK_DEV void ld_cols(uint32_t addr, float2 (&x)[N / 2]) {
   uint32_t r[N];
   tmem_ld_cols<N>(addr, r);
   tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N / 2; ++i) x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 // The sums of two columns each, `apart` columns apart.
 template <int N>
-FAK_DEV void ld_sums(uint32_t addr, int apart, float (&x)[N]) {
+FAK_DEV void ld_sums(uint32_t addr, int apart, float2 (&x)[N / 2]) {
   uint32_t r[N], u[N];
   tmem_ld_cols<N>(addr, r);
   tmem_ld_cols<N>(addr + apart, u);
   tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]) + __uint_as_float(u[i]);
+  for (int i = 0; i < N / 2; ++i)
+    x[i] = add2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
 }
 
 // Operands of m16n8k16, both parts, from a tile of rows of 64 f16.  A: rows r0 .. +15, columns c0 .. +15; B: the same rows,
@@ -250,7 +278,7 @@ template <int NS>
 __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, const __grid_constant__ ChunkMaps maps, ChunkDebug dbg,
                                                                  int* status) {
   using C = Cfg<NS>;
-  constexpr int n = C::n, W = C::cols, B = 32;  // B: columns a chain thread takes at a time
+  constexpr int n = C::n, W = C::cols;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::off_bar);
@@ -279,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 8 : i == kTP || i == kR || i == kU || i == kZFree ? 4 : i == kKQ0 || i == kKQ1 ? 2 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 16 : i == kR || i == kU || i == kZFree ? 8 : i == kTP ? 4 : i == kKQ0 || i == kKQ1 ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
   // T and P T are zero above their blocks on the diagonal, which nothing writes
   for (int i = threadIdx.x; i < 2 * kPart / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + C::off_tp + 16 * i) = make_uint4(0, 0, 0, 0);
-  if (warp == 12) {
+  if (warp == 20) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(C::tmem_cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -317,30 +345,28 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   };
   auto decays = [&](int c) { return reinterpret_cast<Decays*>(smem + C::off_dec) + (c & 3); };
 
-  // registers: the chain's threads hold S; 2 * 160 + 128 + 56 of the 4 * 128 that the block has
-  if (warp < 8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-  else if (warp >= 12)
+  // registers of a thread: 4 * 80 + 104 + 56 of the 6 * 80 that the block has
+  if (warp >= 20)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else if (warp >= 16)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
 
-  if (warp < 8) {
+  if (warp < 16) {
     // ------------------------------------------------------------------ the chain
-    const int quarter = warp & 3, half = warp >> 2;
-    const int col = half * W;                        // of the CTA's columns
+    const int quarter = warp & 3, group = warp >> 2;
+    const int col = group * W;                       // of the CTA's columns
     const uint32_t acc = tmem + ((uint32_t)quarter << 21) + col;  // TMEM: lane 32 quarter
     const int key = 32 * quarter + lane;             // the row of S
     const bool top = quarter < 2;                    // K's and T's rows, else Q's and P T's
     const int t = 32 * (quarter & 1) + lane;         // the row of the chunk
     float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + col;
     float* most = reinterpret_cast<float*>(smem + C::off_max);
-    float S[W];
+    float2 S[W / 2];
 #pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const float4 x = d.fresh ? gdn_zero4() : *reinterpret_cast<const float4*>(st + i);
-      S[i] = x.x;
-      S[i + 1] = x.y;
-      S[i + 2] = x.z;
-      S[i + 3] = x.w;
+    for (int i = 0; i < W / 2; i += 2) {
+      const float4 x = d.fresh ? gdn_zero4() : *reinterpret_cast<const float4*>(st + 2 * i);
+      S[i] = make_float2(x.x, x.y);
+      S[i + 1] = make_float2(x.z, x.w);
     }
     uint32_t v[W / 2];  // of the next chunk
     auto fetch_v = [&](int c) {
@@ -359,28 +385,33 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
     // S scaled and in two parts to shared memory; all chain threads' S and V are looked at
     auto put_state = [&]() {
-      float ms[4] = {};
+      float ms[2] = {};
 #pragma unroll
-      for (int i = 0; i < W; i += 2) ms[i / 2 & 3] = fmaxf(fmaxf(ms[i / 2 & 3], fabsf(S[i])), fabsf(S[i + 1]));
+      for (int i = 0; i < W / 2; ++i) ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(S[i].x)), fabsf(S[i].y));
       if (top) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i)
-          ms[i & 3] = fmaxf(fmaxf(ms[i & 3], fabsf(__uint_as_float(v[i] << 16))), fabsf(__uint_as_float(v[i] & 0xffff0000u)));
+        for (int i = 0; i < W / 2; ++i) {
+          const float2 x = bf16_pair(v[i]);
+          ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(x.x)), fabsf(x.y));
+        }
       }
-      float m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(ms[0], ms[1]))));
       if (lane == 0) most[warp] = m;
       named_bar_sync(1, kChainThreads);
-      const float4 a = *reinterpret_cast<const float4*>(most), b = *reinterpret_cast<const float4*>(most + 4);
-      m = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+      m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(most + i);
+        m = fmaxf(m, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+      }
       // m = 2^e 1.f goes to 2^5 1.f (zeros and infinities: as they are); the inverse is a normal number too
       const int e = (int)(__float_as_uint(m) >> 23);
       const int by = e == 0 || e == 255 ? 0 : min(max(132 - e, -120), 120);
       up = __uint_as_float((uint32_t)(127 + by) << 23);
       down = __uint_as_float((uint32_t)(127 - by) << 23);
-      float x[W];
+      float2 x[W / 2];
 #pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = S[i] * up;
+      for (int i = 0; i < W / 2; ++i) x[i] = mul2(S[i], both(up));
       put_halves<W>(smem + C::off_s, 16384, C::panels * 16384, key, col, x);
     };
     const uint32_t sum_to = smem_u32(smem + C::off_sum);
@@ -392,142 +423,127 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = decays(c);
       const float keep = dec->keep[t], all = dec->keep[kRows - 1];
+      float2 x[W / 2];
       if (top) {
         const float left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
         wait(kD1, c);
         tc_fence_after_sync();
+        ld_sums<W>(acc + C::d1, n, x);
 #pragma unroll
-        for (int i = 0; i < W; i += B) {
-          float x[B];
-          ld_sums<B>(acc + C::d1 + i, n, x);
-#pragma unroll
-          for (int j = 0; j < B; j += 2) {
-            x[j] = fmaf(bk, x[j], __uint_as_float(v[(i + j) / 2] << 16) * bu);
-            x[j + 1] = fmaf(bk, x[j + 1], __uint_as_float(v[(i + j) / 2] & 0xffff0000u) * bu);
-          }
-          put_halves<B>(smem + C::off_u, 8192, C::panels * 8192, t, col + i, x);
-        }
+        for (int i = 0; i < W / 2; ++i) x[i] = fma2(both(bk), x[i], mul2(bf16_pair(v[i]), both(bu)));
+        put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
         arrive(kR);
         wait(kD2, c);
         tc_fence_after_sync();
+        ld_sums<W>(acc + C::d2, n, x);
 #pragma unroll
-        for (int i = 0; i < W; i += B) {
-          float x[B];
-          ld_sums<B>(acc + C::d2 + i, n, x);
-#pragma unroll
-          for (int j = 0; j < B; ++j) x[j] *= left;
-          put_halves<B>(smem + C::off_u, 8192, C::panels * 8192, t, col + i, x);
-        }
+        for (int i = 0; i < W / 2; ++i) x[i] = mul2(x[i], both(left));
+        put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
         arrive(kU);
         if (c + 1 < chunks) fetch_v(c + 1);
       } else {
-        const int64_t row = d.first + c * kRows + t;
         const float by = down * p.scale;
-        float o[W];
+        float2 o[W / 2], f[W / 2];  // f: what the normed output is multiplied by
+#pragma unroll
+        for (int i = 0; i < W / 2; i += 2) {
+          const float4 w = *reinterpret_cast<const float4*>(gain + col + 2 * i);
+          f[i] = make_float2(w.x, w.y);
+          f[i + 1] = make_float2(w.z, w.w);
+        }
+        if (p.z) {
+          wait(kZ, c);
+          const unsigned char* zs = smem + C::off_z + (col >> 5) * kRows * 128 + t * 128;
+#pragma unroll
+          for (int i = 0; i < W / 2; i += 2) {
+            const float4 z = *reinterpret_cast<const float4*>(zs + (((((col & 31) >> 2) + i / 2) ^ (t & 7)) << 4));
+            f[i] = mul2(f[i], make_float2(gdn_silu(z.x), gdn_silu(z.y)));
+            f[i + 1] = mul2(f[i + 1], make_float2(gdn_silu(z.z), gdn_silu(z.w)));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[kZFree]);
+        }
         wait(kD1, c);
         tc_fence_after_sync();
-#pragma unroll
-        for (int i = 0; i < W; i += B) {
-          float x[B];
-          ld_sums<B>(acc + C::d1 + i, n, x);
-#pragma unroll
-          for (int j = 0; j < B; ++j) o[i + j] = keep * x[j];
-        }
+        ld_sums<W>(acc + C::d1, n, o);
         wait(kD2, c);
         tc_fence_after_sync();
+        ld_sums<W>(acc + C::d2, n, x);
 #pragma unroll
-        for (int i = 0; i < W; i += B) {
-          float x[B];
-          ld_sums<B>(acc + C::d2 + i, n, x);
-#pragma unroll
-          for (int j = 0; j < B; ++j) o[i + j] = (o[i + j] + x[j]) * by;
-        }
+        for (int i = 0; i < W / 2; ++i) o[i] = mul2(fma2(both(keep), o[i], x[i]), both(by));
         float r = 1.0f;
         if (p.norm_w) {
           // the row's sum of squares over the cluster's columns
-          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], NS * 2 * kRows * 4);
-          float ss = 0.0f;
+          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], NS * 4 * kRows * 4);
+          float2 ss = both(0.0f);
 #pragma unroll
-          for (int i = 0; i < W; ++i) ss = fmaf(o[i], o[i], ss);
-          const uint32_t at = sum_to + (((c & 1) * NS * 2 + me * 2 + half) * kRows + t) * 4;
+          for (int i = 0; i < W / 2; ++i) ss = fma2(o[i], o[i], ss);
+          const uint32_t at = sum_to + (((c & 1) * NS * 4 + me * 4 + group) * kRows + t) * 4;
 #pragma unroll
-          for (int i = 0; i < NS; ++i) st_async(map_rank(at, i), ss, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
+          for (int i = 0; i < NS; ++i) st_async(map_rank(at, i), ss.x + ss.y, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
           wait(kSum0 + (c & 1), c >> 1);
           if constexpr (NS > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
-          const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 2 * kRows + t;
-          ss = 0.0f;
+          const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 4 * kRows + t;
+          float y = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 2 * NS; ++i) ss += sums[i * kRows];
-          r = rsqrtf(fmaf(ss, 1.0f / kGdnDim, p.eps));
+          for (int i = 0; i < 4 * NS; ++i) y += sums[i * kRows];
+          r = rsqrtf(fmaf(y, 1.0f / kGdnDim, p.eps));
         }
-        // the thread's own line of z, 32 columns, where its output goes too, on its way to a copy of its own
-        if (p.z) wait(kZ, c);
-        unsigned char* zs = smem + C::off_z + half * kRows * 128 + t * 128;
 #pragma unroll
-        for (int i = 0; i < W; i += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(gain + col + i);
-          o[i] *= r * w.x;
-          o[i + 1] *= r * w.y;
-          o[i + 2] *= r * w.z;
-          o[i + 3] *= r * w.w;
-        }
-        if (p.z) {
+        for (int i = 0; i < W / 2; ++i) o[i] = mul2(mul2(o[i], both(r)), f[i]);
+        // The rows turn in S's place, which the product before is done with, so that stores are whole lines: a thread's own
+        // row would be a line for every lane (3,000 cycles a chunk).
+        unsigned char* turn = smem + C::off_s;
+        const int have = min(kRows, rows - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
+        const int64_t to = (int64_t)(d.first + c * kRows) * p.out_row + h * p.out_head + col0;
+        if (p.out_bf16) {
+          constexpr int line = n / 8;  // pieces of a row
 #pragma unroll
-          for (int i = 0; i < W; i += 4) {
-            const float4 z = *reinterpret_cast<const float4*>(zs + (((i >> 2) ^ (t & 7)) << 4));
-            o[i] *= gdn_silu(z.x);
-            o[i + 1] *= gdn_silu(z.y);
-            o[i + 2] *= gdn_silu(z.z);
-            o[i + 3] *= gdn_silu(z.w);
+          for (int i = 0; i < W / 2; i += 4)
+            *reinterpret_cast<uint4*>(turn + t * n * 2 + ((((col + 2 * i) >> 3) ^ (t & 7)) << 4)) =
+                make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
+                           pack_bf16(o[i + 3].x, o[i + 3].y));
+          named_bar_sync(4, kChainThreads / 2);
+#pragma unroll
+          for (int i = 0; i < kRows * line / 256; ++i) {
+            const int at = i * 256 + i0, row = at / line, pc = at % line;
+            if (row < have && !*abort)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
+                  *reinterpret_cast<const uint4*>(turn + row * n * 2 + ((pc ^ (row & 7)) << 4));
+          }
+        } else {
+          constexpr int line = n / 4;
+#pragma unroll
+          for (int i = 0; i < W / 2; i += 2)
+            *reinterpret_cast<float4*>(turn + t * n * 4 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
+                make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
+          named_bar_sync(4, kChainThreads / 2);
+#pragma unroll
+          for (int i = 0; i < kRows * line / 256; ++i) {
+            const int at = i * 256 + i0, row = at / line, pc = at % line;
+            if (row < have && !*abort)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + row * p.out_row + 4 * pc) =
+                  *reinterpret_cast<const float4*>(turn + row * n * 4 + ((pc ^ (row & 7)) << 4));
           }
         }
-        if (c * kRows + t < rows && !*abort) {
-          const int64_t to = row * p.out_row + h * p.out_head + col0 + col;
-          if (p.out_bf16) {
-            zs += (t & 1) * 64;  // (four lanes' rows on the same banks, not eight)
-#pragma unroll
-            for (int i = 0; i < W; i += 8)
-              *reinterpret_cast<uint4*>(zs + 2 * i) = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
-                                                                 pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
-            fence_async();
-            bulk_s2g(static_cast<__nv_bfloat16*>(p.out) + to, smem_u32(zs), 2 * W);
-          } else {
-#pragma unroll
-            for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(zs + 4 * i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            fence_async();
-            bulk_s2g(static_cast<float*>(p.out) + to, smem_u32(zs), 4 * W);
-          }
-        }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
       wait(kD3, c);
       tc_fence_after_sync();
+      ld_sums<W>(acc + C::d3, n, x);
 #pragma unroll
-      for (int i = 0; i < W; i += B) {
-        float x[B];
-        ld_sums<B>(acc + C::d3 + i, n, x);
-#pragma unroll
-        for (int j = 0; j < B; ++j) S[i + j] = fmaf(all, S[i + j], x[j] * down);
-      }
-      if (!top) {  // the output has left its place, to z
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kZFree]);
-      }
+      for (int i = 0; i < W / 2; ++i) S[i] = fma2(both(all), S[i], mul2(x[i], both(down)));
       if (c + 1 < chunks) {
         put_state();
         wait(kKQ0 + ((c + 1) & 1), (c + 1) >> 1);
         arrive(kS);
       }
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!*abort) {
 #pragma unroll
-      for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(st + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < W / 2; i += 2) *reinterpret_cast<float4*>(st + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ------------------------------------------------------------------ T and P T
-    const int w = warp - 8, r = threadIdx.x - kChainThreads;
+    const int w = warp - 16, r = threadIdx.x - kChainThreads;
     float* diag = reinterpret_cast<float*>(smem + C::off_a);
     unsigned char *tp = smem + C::off_tp, *ap = smem + C::off_ap;
     const uint32_t tps = smem_u32(tp), aps = smem_u32(ap);
@@ -544,38 +560,36 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         // before them by way of row 31
         const float hi = dec->hi[t], lo = dec->lo[t], b = top ? dec->beta[t] : 1.0f;
         const int own = 32 * late, last = (top ? lane - 1 : lane);
-        float x[32];
+        float2 x[16];
         ld_cols<32>(acc + own, x);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + i]);
-          const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + i]);
-          x[i] *= b * exp2_approx((hi - u.x) + (lo - l.x));
-          x[i + 1] *= b * exp2_approx((hi - u.y) + (lo - l.y));
-          x[i + 2] *= b * exp2_approx((hi - u.z) + (lo - l.z));
-          x[i + 3] *= b * exp2_approx((hi - u.w) + (lo - l.w));
+        for (int i = 0; i < 16; i += 2) {
+          const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + 2 * i]);
+          const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + 2 * i]);
+          const float2 e0 = add2(fma2(make_float2(u.x, u.y), both(-1.0f), both(hi)), fma2(make_float2(l.x, l.y), both(-1.0f), both(lo)));
+          const float2 e1 = add2(fma2(make_float2(u.z, u.w), both(-1.0f), both(hi)), fma2(make_float2(l.z, l.w), both(-1.0f), both(lo)));
+          x[i] = mul2(mul2(x[i], both(b)), make_float2(exp2_approx(e0.x), exp2_approx(e0.y)));
+          x[i + 1] = mul2(mul2(x[i + 1], both(b)), make_float2(exp2_approx(e1.x), exp2_approx(e1.y)));
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i <= last ? x[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) x[i] = make_float2(2 * i <= last ? x[i].x : 0.0f, 2 * i + 1 <= last ? x[i].y : 0.0f);
         if (top) {
           float* to = diag + t * kLd;
           const bool second = lane >= 16;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(to + i) = second ? make_float4(x[16 + i], x[17 + i], x[18 + i], x[19 + i])
-                                                        : make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          for (int i = 0; i < 8; i += 2)
+            *reinterpret_cast<float4*>(to + 2 * i) = second ? make_float4(x[8 + i].x, x[8 + i].y, x[9 + i].x, x[9 + i].y)
+                                                            : make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
         }
         put_halves<32>(ap, 0, kPart, r, own, x);
         if (late) {
           const float f = b * dec->mid[t];
           ld_cols<32>(acc, x);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(&dec->mid[i]);
-            x[i] *= f * u.x;
-            x[i + 1] *= f * u.y;
-            x[i + 2] *= f * u.z;
-            x[i + 3] *= f * u.w;
+          for (int i = 0; i < 16; i += 2) {
+            const float4 u = *reinterpret_cast<const float4*>(&dec->mid[2 * i]);
+            x[i] = mul2(x[i], mul2(both(f), make_float2(u.x, u.y)));
+            x[i + 1] = mul2(x[i + 1], mul2(both(f), make_float2(u.z, u.w)));
           }
           put_halves<32>(ap, 0, kPart, r, 0, x);
         }
@@ -602,7 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
           for (int j = i - 1; j >= 0; --j) x[j] = fmaf(-x[i], y[j], x[j]);
         }
-        if (lane < 16) put_halves<16>(tp, 0, kPart, 16 * w + row, 16 * w, x);
+        float2 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+        if (lane < 16) put_halves<16>(tp, 0, kPart, 16 * w + row, 16 * w, y);
       }
       named_bar_sync(2, kPrepThreads);
       {
@@ -686,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       // (the next chunk's K K^T comes after the product that reads this: nothing is written over before)
       arrive(kTP);
     }
-  } else if (warp == 12) {
+  } else if (warp == 20) {
     // ------------------------------------------------------------------ the products
     const uint32_t kq = smem_u32(smem + C::off_kq), tp = smem_u32(smem + C::off_tp), ss = smem_u32(smem + C::off_s),
                    us = smem_u32(smem + C::off_u);
@@ -751,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
       __syncwarp();
     }
-  } else if (warp == 13) {
+  } else if (warp == 21) {
     // ------------------------------------------------------------------ K, Q and z
     const int hk = h / p.group;
     for (int c = 0; c < chunks; ++c) {
@@ -816,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
       if (p.z && p.z_wide) drain(kZ, chunks - 1);
     }
-  } else if (warp == 14) {
+  } else if (warp == 22) {
     // ------------------------------------------------------------------ the decays
     float g[2], b[2];
     auto fetch = [&](int c) {  // two rows to a lane
@@ -883,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   __syncthreads();
   // (no CTA leaves while another may still store into it)
   if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (warp == 12) {
+  if (warp == 20) {
     tc_fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
   }
