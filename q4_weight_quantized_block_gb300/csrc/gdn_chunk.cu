@@ -85,7 +85,12 @@ struct Cfg {
   static_assert(dkk + 64 <= tmem_cols, "TMEM");
 };
 
-enum Bars { kLand0, kLand1, kD1, kD2, kD3, kKK, kTP, kKQ0, kKQ1, kV0, kV1, kZ, kZFree, kS, kR, kU, kSum0, kSum1, kDrain, kBars };
+enum Bars { kLand0, kLand1, kD1, kD2, kD3, kKK, kKQ0, kKQ1, kV0, kV1, kZ, kZFree, kSum0, kSum1, kDrain, kBars };
+
+// Named barriers, for waits where a polling warp would take issue slots from those that work (a try of an mbarrier gives
+// up after some 60 cycles; with all waits so, half of all instructions were of such loops).  The products' warp polls, and
+// lets the others go.
+enum Named { kBarMax = 1, kBarPrep, kBarTurn, kBarS, kBarR, kBarU, kBarTP, kBarKK, kBarD1Top, kBarD1Low, kBarD2Top, kBarD2Low, kBarD3 };
 
 template <int M, int N, bool A_MN, bool B_MN>
 constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kS ? 16 : i == kR || i == kU || i == kZFree ? 8 : i == kTP ? 4 : i == kKQ0 || i == kKQ1 ? 2 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : i == kKQ0 || i == kKQ1 ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
 
   // One that runs out is recorded, and no wait of the block waits after it: every warp goes through its chunks, without
-  // results, so that the named barriers, each of one group of warps, stay in step.
+  // results, so that the named barriers stay in step (nothing but such waits lies between two of them).
   auto wait = [&](int b, int phase) {
     bool done = *abort != 0;
     for (int i = 0; i < 512 && !done; ++i) done = mbar_try_wait(&bar[b], phase & 1);
@@ -336,12 +341,26 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     }
     __syncwarp();
   };
+  // The same for warps that may sleep meanwhile.
+  auto doze = [&](int b, int phase) {
+    for (int i = 0; i < 4096 && !*abort && !mbar_try_wait(&bar[b], phase & 1); ++i) __nanosleep(100);
+    wait(b, phase);
+  };
   // What the warp wrote to shared memory and read from TMEM comes before what waits on the barrier, MMAs too.
   auto arrive = [&](int b) {
     fence_async();
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[b]);
+  };
+  auto give = [&](int named, int threads) {
+    fence_async();
+    tc_fence_before_sync();
+    asm volatile("bar.arrive %0, %1;" ::"r"(named), "r"(threads + 32) : "memory");
+  };
+  auto take = [&](int named, int threads) {
+    named_bar_sync(named, threads + 32);
+    tc_fence_after_sync();
   };
   auto decays = [&](int c) { return reinterpret_cast<Decays*>(smem + C::off_dec) + (c & 3); };
 
@@ -397,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
       float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(ms[0], ms[1]))));
       if (lane == 0) most[warp] = m;
-      named_bar_sync(1, kChainThreads);
+      named_bar_sync(kBarMax, kChainThreads);
       m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
@@ -418,28 +437,26 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     const int me = NS > 1 ? (int)rank_in_cluster() : 0;
     if (top) fetch_v(0);
     put_state();
-    wait(kKQ0, 0);
-    arrive(kS);
+    give(kBarS, kChainThreads);
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = decays(c);
-      const float keep = dec->keep[t], all = dec->keep[kRows - 1];
       float2 x[W / 2];
+      float all;
       if (top) {
-        const float left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
-        wait(kD1, c);
-        tc_fence_after_sync();
+        take(kBarD1Top, kChainThreads / 2);
+        const float keep = dec->keep[t], left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
+        all = dec->keep[kRows - 1];
         ld_sums<W>(acc + C::d1, n, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) x[i] = fma2(both(bk), x[i], mul2(bf16_pair(v[i]), both(bu)));
         put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
-        arrive(kR);
-        wait(kD2, c);
-        tc_fence_after_sync();
+        give(kBarR, kChainThreads / 2);
+        take(kBarD2Top, kChainThreads / 2);
         ld_sums<W>(acc + C::d2, n, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) x[i] = mul2(x[i], both(left));
         put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
-        arrive(kU);
+        give(kBarU, kChainThreads / 2);
         if (c + 1 < chunks) fetch_v(c + 1);
       } else {
         const float by = down * p.scale;
@@ -462,11 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[kZFree]);
         }
-        wait(kD1, c);
-        tc_fence_after_sync();
+        take(kBarD1Low, kChainThreads / 2);
+        const float keep = dec->keep[t];
+        all = dec->keep[kRows - 1];
         ld_sums<W>(acc + C::d1, n, o);
-        wait(kD2, c);
-        tc_fence_after_sync();
+        take(kBarD2Low, kChainThreads / 2);
         ld_sums<W>(acc + C::d2, n, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) o[i] = mul2(fma2(both(keep), o[i], x[i]), both(by));
@@ -502,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
             *reinterpret_cast<uint4*>(turn + t * n * 2 + ((((col + 2 * i) >> 3) ^ (t & 7)) << 4)) =
                 make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
                            pack_bf16(o[i + 3].x, o[i + 3].y));
-          named_bar_sync(4, kChainThreads / 2);
+          named_bar_sync(kBarTurn, kChainThreads / 2);
 #pragma unroll
           for (int i = 0; i < kRows * line / 256; ++i) {
             const int at = i * 256 + i0, row = at / line, pc = at % line;
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           for (int i = 0; i < W / 2; i += 2)
             *reinterpret_cast<float4*>(turn + t * n * 4 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
                 make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
-          named_bar_sync(4, kChainThreads / 2);
+          named_bar_sync(kBarTurn, kChainThreads / 2);
 #pragma unroll
           for (int i = 0; i < kRows * line / 256; ++i) {
             const int at = i * 256 + i0, row = at / line, pc = at % line;
@@ -526,15 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           }
         }
       }
-      wait(kD3, c);
-      tc_fence_after_sync();
+      take(kBarD3, kChainThreads);
       ld_sums<W>(acc + C::d3, n, x);
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) S[i] = fma2(both(all), S[i], mul2(x[i], both(down)));
       if (c + 1 < chunks) {
         put_state();
-        wait(kKQ0 + ((c + 1) & 1), (c + 1) >> 1);
-        arrive(kS);
+        give(kBarS, kChainThreads);
       }
     }
     if (!*abort) {
@@ -551,9 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     const int t = r & (kRows - 1);
     const uint32_t acc = tmem + ((uint32_t)w << 21) + C::dkk;
     for (int c = 0; c < chunks; ++c) {
-      wait(kKQ0 + (c & 1), c >> 1);
-      wait(kKK, c);
-      tc_fence_after_sync();
+      take(kBarKK, kPrepThreads);
       const Decays* dec = decays(c);
       {
         // row r of [A; P], from K K^T and Q K^T by the decays: over the row's own 32 columns one exponential each; to the 32
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           put_halves<32>(ap, 0, kPart, r, 0, x);
         }
       }
-      named_bar_sync(2, kPrepThreads);
+      named_bar_sync(kBarPrep, kPrepThreads);
       {
         // row lane % 16 of the inverse of the 16 x 16 block of I + A at 16 w
         const int row = lane & 15;
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
         if (lane < 16) put_halves<16>(tp, 0, kPart, 16 * w + row, 16 * w, y);
       }
-      named_bar_sync(2, kPrepThreads);
+      named_bar_sync(kBarPrep, kPrepThreads);
       {
         // two blocks of 32: the lower left is -T22 (A21 T11), eight columns to a warp
         const int at = 32 * (w >> 1), j = (at >> 3) + (w & 1);
@@ -644,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         for (int i = 0; i < 4; ++i) y[i] += y1[i] + y2[i];
         put_block(tp, at + 16, j, y, -1.0f, lane);
       }
-      named_bar_sync(2, kPrepThreads);
+      named_bar_sync(kBarPrep, kPrepThreads);
       {
         // the block of 64's, 32 x 32, eight columns to a warp
         float x[2][4] = {}, y[2][4] = {};
@@ -677,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
         for (int m = 0; m < 2; ++m) put_block(tp, 32 + 16 * m, w, y[m], -1.0f, lane);
       }
-      named_bar_sync(2, kPrepThreads);
+      named_bar_sync(kBarPrep, kPrepThreads);
       // P T, eight columns at a time: tiles 0 and 1 take ten steps, 2 and 3 six, 4 and 5 three, 6 and 7 one
       for (int j = w; j < 8; j += w < 2 ? 8 : 2) {
         float y[4][4] = {};
@@ -701,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           if (m >= j >> 1) put_block(tp, kRows + 16 * m, j, y[m], 1.0f, lane);
       }
       // (the next chunk's K K^T comes after the product that reads this: nothing is written over before)
-      arrive(kTP);
+      give(kBarTP, kPrepThreads);
     }
   } else if (warp == 20) {
     // ------------------------------------------------------------------ the products
@@ -722,10 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       __syncwarp();
     };
     overlap(0);
+    wait(kKK, 0);
+    give(kBarKK, kPrepThreads);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t kqc = kq + (c & 1) * 32768;
-      wait(kS, c);
-      tc_fence_after_sync();
+      take(kBarS, kChainThreads);
       if (elect_one()) {
         const uint64_t a = umma_desc_sw128(kqc), b = desc_mn(ss, 16384);
 #pragma unroll
@@ -734,9 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         umma_commit(&bar[kD1]);
       }
       __syncwarp();
-      wait(kTP, c);
-      wait(kR, c);
-      tc_fence_after_sync();
+      wait(kD1, c);
+      give(kBarD1Top, kChainThreads / 2);
+      give(kBarD1Low, kChainThreads / 2);
+      take(kBarTP, kPrepThreads);
+      take(kBarR, kChainThreads / 2);
       if (elect_one()) {
         const uint64_t a = umma_desc_sw128(tp), b = desc_mn(us, 8192);
 #pragma unroll
@@ -748,8 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
       __syncwarp();
       if (c + 1 < chunks) overlap(c + 1);
-      wait(kU, c);
-      tc_fence_after_sync();
+      wait(kD2, c);
+      give(kBarD2Top, kChainThreads / 2);
+      give(kBarD2Low, kChainThreads / 2);
+      if (c + 1 < chunks) {
+        wait(kKK, c + 1);
+        give(kBarKK, kPrepThreads);
+      }
+      take(kBarU, kChainThreads / 2);
       if (elect_one()) {
         const uint64_t a = desc_mn(kqc, 16384), b = desc_mn(us, 8192);
 #pragma unroll
@@ -758,6 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         umma_commit(&bar[kD3]);
       }
       __syncwarp();
+      wait(kD3, c);
+      give(kBarD3, kChainThreads);
     }
     if (*abort) {  // what was issued is done with before the TMEM goes
       if (elect_one()) {
@@ -772,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     // ------------------------------------------------------------------ K, Q and z
     const int hk = h / p.group;
     for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) wait(kD3, c - 2);
+      if (c >= 2) doze(kD3, c - 2);
       const int first = c * kRows, have = min(kRows, rows - first);
       unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
       if (elect_one()) {
@@ -789,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           tma_load_3d_tx(smem + C::off_v + ((c & 1) * C::panels + i) * 8192, &maps.v, col0 + 64 * i, h, d.first + first, &bar[kV0 + (c & 1)]);
       }
       __syncwarp();
-      wait(kLand0 + (c & 1), c >> 1);
+      doze(kLand0 + (c & 1), c >> 1);
       if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
         for (int i = lane; i < (kRows - have) * 32; i += 32) {
           const int row = have + (i >> 5), at = i & 31;
@@ -797,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         }
       if (!dbg.unreachable) arrive(kKQ0 + (c & 1));
       if (p.z) {
-        if (c >= 1) wait(kZFree, c - 1);
+        if (c >= 1) doze(kZFree, c - 1);
         unsigned char* zs = smem + C::off_z;
         if (p.z_wide) {
           if (elect_one()) {
@@ -884,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         const float e = (hi_mid - hi[j]) + (lo_mid - lo[j]);
         mid[j] = exp2_approx(lane < 16 ? e : -e);
       }
-      if (c >= 2) wait(kD3, c - 2);
+      if (c >= 2) doze(kD3, c - 2);
       Decays* dec = decays(c);
       auto put2 = [&](float* at, float y0, float y1) { *reinterpret_cast<float2*>(at + 2 * lane) = make_float2(y0, y1); };
       put2(dec->hi, hi[0], hi[1]);
