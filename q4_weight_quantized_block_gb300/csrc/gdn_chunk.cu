@@ -10,9 +10,10 @@
 //
 // Precision.  The state is held in f32 registers, and its products keep 22 bits: the f32 operand goes as the sum of two
 // f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents
-// take them because a chunk's S, R and U are scaled by one power of two: with m the largest of |S| and |V|, lengths of k
-// of at most 1 and 0 <= beta <= 2, |R| <= 25 m and |U|, |S'| <= 281 m, so m goes to 2^5 .. 2^6; what f16 drops is below
-// 2^-25, so 2^-30 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and
+// take them because a chunk's S, R and U are scaled by one power of two.  With m the largest of |S| and |V|, lengths of k
+// of at most 1 and 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m of
+// the chunk before (its own would hold all warps up at a barrier), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what
+// f16 drops is below 2^-25, so 2^-23 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and
 // kept as two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
 //
 // A cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own rule: only the
@@ -76,7 +77,7 @@ struct Cfg {
   static constexpr int off_dec = off_a + 4 * 16 * kLd * 4;
   static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 4][64]
   static constexpr int off_gain = off_sum + 2 * NS * 4 * kRows * 4;
-  static constexpr int off_max = off_gain + n * 4;  // [16]
+  static constexpr int off_max = off_gain + n * 4;  // [8]
   static constexpr int off_bar = off_max + 64;
   static constexpr int smem = off_bar + 192 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : i == kKQ0 || i == kKQ1 ? 2 : 1);
     fence_mbar_init();
   }
+  if (threadIdx.x < 8) reinterpret_cast<unsigned*>(smem + C::off_max)[threadIdx.x] = 0;
   if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
   // T and P T are zero above their blocks on the diagonal, which nothing writes
   for (int i = threadIdx.x; i < 2 * kPart / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + C::off_tp + 16 * i) = make_uint4(0, 0, 0, 0);
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     const bool top = quarter < 2;                    // K's and T's rows, else Q's and P T's
     const int t = 32 * (quarter & 1) + lane;         // the row of the chunk
     float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + col;
-    float* most = reinterpret_cast<float*>(smem + C::off_max);
+    unsigned* most = reinterpret_cast<unsigned*>(smem + C::off_max);  // [4] of S, [4] of V: largest magnitudes, by chunk
     float2 S[W / 2];
 #pragma unroll
     for (int i = 0; i < W / 2; i += 2) {
@@ -401,31 +403,34 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         v[4 * i + 3] = there ? x.w : 0;
       }
     };
-    float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
-    // S scaled and in two parts to shared memory; all chain threads' S and V are looked at
-    auto put_state = [&]() {
+    auto tell = [&](int at, float m) {  // a warp's largest magnitude to the block's
+      const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+      if (lane == 0) atomicMax(&most[at], u);
+    };
+    auto tell_state = [&](int c) {
       float ms[2] = {};
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(S[i].x)), fabsf(S[i].y));
-      if (top) {
+      tell(c & 3, fmaxf(ms[0], ms[1]));
+    };
+    auto tell_values = [&](int c) {
+      float ms[2] = {};
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          const float2 x = bf16_pair(v[i]);
-          ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(x.x)), fabsf(x.y));
-        }
+      for (int i = 0; i < W / 2; ++i) {
+        const float2 x = bf16_pair(v[i]);
+        ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(x.x)), fabsf(x.y));
       }
-      float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(ms[0], ms[1]))));
-      if (lane == 0) most[warp] = m;
-      named_bar_sync(kBarMax, kChainThreads);
-      m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(most + i);
-        m = fmaxf(m, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
-      }
-      // m = 2^e 1.f goes to 2^5 1.f (zeros and infinities: as they are); the inverse is a normal number too
+      tell(4 + (c & 3), fmaxf(ms[0], ms[1]));
+    };
+    float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
+    // S, as it stands before chunk c, scaled and in two parts to shared memory.  The scale goes by the state one chunk
+    // before, whose magnitudes every warp has told by now.
+    auto put_state = [&](int c) {
+      const int b = max(c - 1, 0);
+      const float m = fmaxf(__uint_as_float(most[b & 3]), __uint_as_float(max(most[4 + (b & 3)], most[4 + (c & 3)])));
+      // m = 2^e 1.f goes to 2^-2 1.f (zeros and infinities: as they are); the inverse is a normal number too
       const int e = (int)(__float_as_uint(m) >> 23);
-      const int by = e == 0 || e == 255 ? 0 : min(max(132 - e, -120), 120);
+      const int by = e == 0 || e == 255 ? 0 : min(max(125 - e, -120), 120);
       up = __uint_as_float((uint32_t)(127 + by) << 23);
       down = __uint_as_float((uint32_t)(127 - by) << 23);
       float2 x[W / 2];
@@ -435,9 +440,82 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     };
     const uint32_t sum_to = smem_u32(smem + C::off_sum);
     const int me = NS > 1 ? (int)rank_in_cluster() : 0;
-    if (top) fetch_v(0);
-    put_state();
+    tell_state(0);
+    if (top) {
+      fetch_v(0);
+      tell_values(0);
+    }
+    named_bar_sync(kBarMax, kChainThreads);
+    put_state(0);
     give(kBarS, kChainThreads);
+    // The output of chunk c, whose rows stand in o: its norm, gate and stores come while the next chunk's products run, so
+    // that the state does not wait for them.
+    float2 o[W / 2];
+    auto finish = [&](int c) {
+      float r = 1.0f;
+      if (p.norm_w) {
+        wait(kSum0 + (c & 1), c >> 1);
+        if constexpr (NS > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
+        const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 4 * kRows + t;
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * NS; ++i) y += sums[i * kRows];
+        r = rsqrtf(fmaf(y, 1.0f / kGdnDim, p.eps));
+      }
+#pragma unroll
+      for (int i = 0; i < W / 2; i += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(gain + col + 2 * i);
+        o[i] = mul2(o[i], mul2(make_float2(w.x, w.y), both(r)));
+        o[i + 1] = mul2(o[i + 1], mul2(make_float2(w.z, w.w), both(r)));
+      }
+      if (p.z) {
+        wait(kZ, c);
+        const unsigned char* zs = smem + C::off_z + (col >> 5) * kRows * 128 + t * 128;
+#pragma unroll
+        for (int i = 0; i < W / 2; i += 2) {
+          const float4 z = *reinterpret_cast<const float4*>(zs + (((((col & 31) >> 2) + i / 2) ^ (t & 7)) << 4));
+          o[i] = mul2(o[i], make_float2(gdn_silu(z.x), gdn_silu(z.y)));
+          o[i + 1] = mul2(o[i + 1], make_float2(gdn_silu(z.z), gdn_silu(z.w)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kZFree]);
+      }
+      // The rows turn in S's place, which the chunk's first product is done with, so that stores are whole lines: a thread's
+      // own row would be a line for every lane (3,000 cycles a chunk).
+      unsigned char* turn = smem + C::off_s;
+      const int have = min(kRows, rows - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
+      const int64_t to = (int64_t)(d.first + c * kRows) * p.out_row + h * p.out_head + col0;
+      if (p.out_bf16) {
+        constexpr int line = n / 8;  // pieces of a row
+#pragma unroll
+        for (int i = 0; i < W / 2; i += 4)
+          *reinterpret_cast<uint4*>(turn + t * n * 2 + ((((col + 2 * i) >> 3) ^ (t & 7)) << 4)) =
+              make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
+                         pack_bf16(o[i + 3].x, o[i + 3].y));
+        named_bar_sync(kBarTurn, kChainThreads / 2);
+#pragma unroll
+        for (int i = 0; i < kRows * line / 256; ++i) {
+          const int at = i * 256 + i0, row = at / line, pc = at % line;
+          if (row < have && !*abort)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
+                *reinterpret_cast<const uint4*>(turn + row * n * 2 + ((pc ^ (row & 7)) << 4));
+        }
+      } else {
+        constexpr int line = n / 4;
+#pragma unroll
+        for (int i = 0; i < W / 2; i += 2)
+          *reinterpret_cast<float4*>(turn + t * n * 4 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
+              make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
+        named_bar_sync(kBarTurn, kChainThreads / 2);
+#pragma unroll
+        for (int i = 0; i < kRows * line / 256; ++i) {
+          const int at = i * 256 + i0, row = at / line, pc = at % line;
+          if (row < have && !*abort)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + row * p.out_row + 4 * pc) =
+                *reinterpret_cast<const float4*>(turn + row * n * 4 + ((pc ^ (row & 7)) << 4));
+        }
+      }
+    };
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = decays(c);
       float2 x[W / 2];
@@ -451,96 +529,37 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         for (int i = 0; i < W / 2; ++i) x[i] = fma2(both(bk), x[i], mul2(bf16_pair(v[i]), both(bu)));
         put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
         give(kBarR, kChainThreads / 2);
+        if (c + 1 < chunks) {
+          fetch_v(c + 1);
+          tell_values(c + 1);
+        }
         take(kBarD2Top, kChainThreads / 2);
         ld_sums<W>(acc + C::d2, n, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) x[i] = mul2(x[i], both(left));
         put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
         give(kBarU, kChainThreads / 2);
-        if (c + 1 < chunks) fetch_v(c + 1);
       } else {
-        const float by = down * p.scale;
-        float2 o[W / 2], f[W / 2];  // f: what the normed output is multiplied by
-#pragma unroll
-        for (int i = 0; i < W / 2; i += 2) {
-          const float4 w = *reinterpret_cast<const float4*>(gain + col + 2 * i);
-          f[i] = make_float2(w.x, w.y);
-          f[i + 1] = make_float2(w.z, w.w);
-        }
-        if (p.z) {
-          wait(kZ, c);
-          const unsigned char* zs = smem + C::off_z + (col >> 5) * kRows * 128 + t * 128;
-#pragma unroll
-          for (int i = 0; i < W / 2; i += 2) {
-            const float4 z = *reinterpret_cast<const float4*>(zs + (((((col & 31) >> 2) + i / 2) ^ (t & 7)) << 4));
-            f[i] = mul2(f[i], make_float2(gdn_silu(z.x), gdn_silu(z.y)));
-            f[i + 1] = mul2(f[i + 1], make_float2(gdn_silu(z.z), gdn_silu(z.w)));
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[kZFree]);
-        }
         take(kBarD1Low, kChainThreads / 2);
-        const float keep = dec->keep[t];
+        const float keep = dec->keep[t], by = down * p.scale;
         all = dec->keep[kRows - 1];
-        ld_sums<W>(acc + C::d1, n, o);
+        float2 y[W / 2];
+        ld_sums<W>(acc + C::d1, n, y);
+        if (c > 0) finish(c - 1);
         take(kBarD2Low, kChainThreads / 2);
         ld_sums<W>(acc + C::d2, n, x);
+        float2 ss = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) o[i] = mul2(fma2(both(keep), o[i], x[i]), both(by));
-        float r = 1.0f;
-        if (p.norm_w) {
-          // the row's sum of squares over the cluster's columns
+        for (int i = 0; i < W / 2; ++i) {
+          o[i] = mul2(fma2(both(keep), y[i], x[i]), both(by));
+          ss = fma2(o[i], o[i], ss);
+        }
+        if (p.norm_w && !*abort) {
+          // the row's sum of squares goes to all of the cluster
           if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], NS * 4 * kRows * 4);
-          float2 ss = both(0.0f);
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) ss = fma2(o[i], o[i], ss);
           const uint32_t at = sum_to + (((c & 1) * NS * 4 + me * 4 + group) * kRows + t) * 4;
 #pragma unroll
           for (int i = 0; i < NS; ++i) st_async(map_rank(at, i), ss.x + ss.y, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
-          wait(kSum0 + (c & 1), c >> 1);
-          if constexpr (NS > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
-          const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 4 * kRows + t;
-          float y = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4 * NS; ++i) y += sums[i * kRows];
-          r = rsqrtf(fmaf(y, 1.0f / kGdnDim, p.eps));
-        }
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) o[i] = mul2(mul2(o[i], both(r)), f[i]);
-        // The rows turn in S's place, which the product before is done with, so that stores are whole lines: a thread's own
-        // row would be a line for every lane (3,000 cycles a chunk).
-        unsigned char* turn = smem + C::off_s;
-        const int have = min(kRows, rows - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
-        const int64_t to = (int64_t)(d.first + c * kRows) * p.out_row + h * p.out_head + col0;
-        if (p.out_bf16) {
-          constexpr int line = n / 8;  // pieces of a row
-#pragma unroll
-          for (int i = 0; i < W / 2; i += 4)
-            *reinterpret_cast<uint4*>(turn + t * n * 2 + ((((col + 2 * i) >> 3) ^ (t & 7)) << 4)) =
-                make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
-                           pack_bf16(o[i + 3].x, o[i + 3].y));
-          named_bar_sync(kBarTurn, kChainThreads / 2);
-#pragma unroll
-          for (int i = 0; i < kRows * line / 256; ++i) {
-            const int at = i * 256 + i0, row = at / line, pc = at % line;
-            if (row < have && !*abort)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
-                  *reinterpret_cast<const uint4*>(turn + row * n * 2 + ((pc ^ (row & 7)) << 4));
-          }
-        } else {
-          constexpr int line = n / 4;
-#pragma unroll
-          for (int i = 0; i < W / 2; i += 2)
-            *reinterpret_cast<float4*>(turn + t * n * 4 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
-                make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
-          named_bar_sync(kBarTurn, kChainThreads / 2);
-#pragma unroll
-          for (int i = 0; i < kRows * line / 256; ++i) {
-            const int at = i * 256 + i0, row = at / line, pc = at % line;
-            if (row < have && !*abort)
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + row * p.out_row + 4 * pc) =
-                  *reinterpret_cast<const float4*>(turn + row * n * 4 + ((pc ^ (row & 7)) << 4));
-          }
         }
       }
       take(kBarD3, kChainThreads);
@@ -548,10 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) S[i] = fma2(both(all), S[i], mul2(x[i], both(down)));
       if (c + 1 < chunks) {
-        put_state();
+        put_state(c + 1);
         give(kBarS, kChainThreads);
+        tell_state(c + 1);
+        if (threadIdx.x == 0) most[(c + 3) & 3] = most[4 + ((c + 3) & 3)] = 0;  // (the chunk before this one's: read by all)
       }
     }
+    if (!top) finish(chunks - 1);
     if (!*abort) {
 #pragma unroll
       for (int i = 0; i < W / 2; i += 2) *reinterpret_cast<float4*>(st + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
@@ -794,9 +816,42 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     }
   } else if (warp == 21) {
     // ------------------------------------------------------------------ K, Q and z
+    // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
+    // and those that were are waited for before the block ends.
     const int hk = h / p.group;
+    int copied = 0, gates = 0;  // chunks whose K, Q and V, and whose z, were asked for
+    auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
+    auto load_z = [&](int c) {
+      if (!p.z) return;
+      if (c >= 1) doze(kZFree, c - 1);
+      if (dead()) return;
+      gates = c + 1;
+      unsigned char* zs = smem + C::off_z;
+      const int first = c * kRows, have = min(kRows, rows - first);
+      if (p.z_wide) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
+#pragma unroll
+          for (int i = 0; i < n / 32; ++i) tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, d.first + first, &bar[kZ]);
+        }
+        __syncwarp();
+      } else {
+        const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
+#pragma unroll 8
+        for (int u = 0; u < kRows * n / 32; ++u) {
+          const int at = u * 32 + lane, x = at / n, cl = at % n;
+          if (x < have)
+            *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
+                z0[x * p.z_row + cl];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kZ]);
+      }
+    };
     for (int c = 0; c < chunks; ++c) {
       if (c >= 2) doze(kD3, c - 2);
+      if (dead()) break;
+      copied = c + 1;
       const int first = c * kRows, have = min(kRows, rows - first);
       unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
       if (elect_one()) {
@@ -820,42 +875,20 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
       if (!dbg.unreachable) arrive(kKQ0 + (c & 1));
-      if (p.z) {
-        if (c >= 1) doze(kZFree, c - 1);
-        unsigned char* zs = smem + C::off_z;
-        if (p.z_wide) {
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
-#pragma unroll
-            for (int i = 0; i < n / 32; ++i)
-              tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, d.first + first, &bar[kZ]);
-          }
-          __syncwarp();
-        } else {
-          const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
-#pragma unroll 8
-          for (int u = 0; u < kRows * n / 32; ++u) {
-            const int at = u * 32 + lane, x = at / n, cl = at % n;
-            if (x < have)
-              *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
-                  z0[x * p.z_row + cl];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar[kZ]);
-        }
-      }
+      if (c > 0) load_z(c - 1);  // (wanted when the next chunk is on its way)
     }
-    if (*abort) {  // no copy is in flight when the block ends
+    load_z(chunks - 1);
+    if (dead()) {
       auto drain = [&](int b, int phase) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 100000000ull) {
+        while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
         }
       };
-      for (int c = max(0, chunks - 2); c < chunks; ++c) {
+      for (int c = max(0, copied - 2); c < copied; ++c) {
         drain(kLand0 + (c & 1), c >> 1);
         drain(kV0 + (c & 1), c >> 1);
       }
-      if (p.z && p.z_wide) drain(kZ, chunks - 1);
+      if (gates && p.z_wide) drain(kZ, gates - 1);
     }
   } else if (warp == 22) {
     // ------------------------------------------------------------------ the decays
@@ -924,6 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   __syncthreads();
   // (no CTA leaves while another may still store into it)
   if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (NS > 1 && *abort) {  // (and a store that nothing waited for lands within a microsecond)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 50000) {
+    }
+    __syncwarp();
+  }
   if (warp == 20) {
     tc_fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
