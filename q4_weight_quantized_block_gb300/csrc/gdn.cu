@@ -357,7 +357,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   int st = gdn_view(batch, a->n_slots, &p.c);
   if (st != FAK_OK) return st;
   if (a->out_type != FAK_ROWS_F32 && a->out_type != FAK_ROWS_BF16) return FAK_ERR_INVALID_ARG;
-  if (a->nk < 1 || a->nv < 1 || a->nv > (1 << 16) || a->nv % a->nk || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
+  if (a->nk < 1 || a->nv < 1 || a->nv > 65535 || a->nv % a->nk || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
       (int64_t)batch->n_seqs * a->nv > 0x7fffffff)
     return FAK_ERR_SHAPE;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !(a->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
@@ -413,10 +413,12 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
     if (e != cudaSuccess || a->max_q <= kFew) return fak_cuda_status(e);
   }
   void* status = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
+  cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
   if (e != cudaSuccess) return fak_cuda_status(e);
-  return fak_cuda_status(gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
-                                          static_cast<int*>(status), dev, s));
+  e = gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
+                       static_cast<int*>(status), dev, s);
+  const int st2 = fak_cuda_status(e);
+  return e == cudaErrorMemoryAllocation ? FAK_ERR_NOMEM : st2;
 }
 
 extern "C" int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable) {

@@ -6,7 +6,8 @@
 //   R = diag(beta) (V - diag(exp G) K S),   U = T R,   O = diag(exp G) Q S + (P T) R,
 //   S' = exp(G_64) S + K^T diag(exp(G_64 - G)) U,
 // so that what goes from chunk to chunk is three products: [K; Q] S, [T; P T] R (128 rows each) and K^T U.  T and P T
-// depend on no state: other warps make them a chunk ahead.
+// depend on no state: a first kernel makes them for all chunks and heads (a record of 33 KB each, in a scratch), the second
+// goes through a sequence's chunks.
 //
 // Precision.  The state is held in f32 registers, and its products keep 22 bits: the f32 operand goes as the sum of two
 // f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents
@@ -16,14 +17,17 @@
 // f16 drops is below 2^-25, so 2^-23 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and
 // kept as two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
 //
-// A cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own rule: only the
-// norm needs the whole row, and its sums of squares go to the other CTAs by asynchronous stores.  Warps:
-//   0 .. 15   the chain: a warp reads the accumulators' 32 lanes (w % 4) and a quarter of their columns (w / 4); lanes 0..63
-//             are K's or T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all
-//             128.  (With eight warps a step took twice as long: one warp issues an instruction in four cycles.)
-//   16 .. 19  T and P T: decays into A and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T,
-//             by m16n8k16 instructions
-//   20        issues the products;  21  copies K, Q, V and z by TMA;  22  sums the decays.
+// First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps: decays into A
+// and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T, in place of A and P, by m16n8k16
+// instructions.  (Made by four more warps of the second kernel, a chunk ahead, the same work took longer than a chunk's
+// products, and once for each CTA of a head.)
+//
+// Second kernel: a cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own
+// rule: only the norm needs the whole row, and its sums of squares go to the other CTAs by asynchronous stores.  Warps:
+//   0 .. 15   a warp reads the accumulators' 32 lanes (w % 4) and a quarter of their columns (w / 4); lanes 0..63 are K's or
+//             T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128.  (With
+//             eight warps a step took twice as long: one warp issues an instruction in four cycles.)
+//   16        issues the products;  17  copies K, Q, V, z and the records.
 // The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
 // B's columns, so B's two parts stand side by side as 2 n columns, one read of A for both.
 #include <cuda.h>
@@ -32,6 +36,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -47,19 +52,31 @@
 namespace {
 
 constexpr int kRows = 64;  // of a chunk
-constexpr int kChainThreads = 512, kPrepThreads = 128;
-constexpr int kThreads = kChainThreads + kPrepThreads + 128;
+constexpr int kChainThreads = 512;
+constexpr int kThreads = kChainThreads + 128;
+constexpr int kPrepThreads = 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
 constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
 
-// What a chunk's rows decay by, four chunks' worth (the chain may still read the last one's when the loader is two on).
+// What a chunk's rows decay by, and their strengths: behind [T; P T], two parts, in a chunk's record for a head.
 struct Decays {
-  float keep[kRows];           // exp G_t
-  float left[kRows];           // exp(G_64 - G_t)
+  float keep[kRows];  // exp G_t
+  float left[kRows];  // exp(G_64 - G_t)
   float beta[kRows];
-  float hi[kRows], lo[kRows];  // G_t log2(e): a multiple of 2^-9, and the rest
-  float mid[kRows];            // t >= 32: exp(G_t - G_31), else exp(G_31 - G_t)
 };
+constexpr int kRecord = 2 * kPart + (int)sizeof(Decays);
+static_assert(kRecord % 16 == 0, "bulk copies");
+
+// Where records stand.  dense: chunk c of a sequence s, begin <= c < begin + length, at s * length + c - begin; else chunk c at
+// r0 / 64 + s + c, r0 being the sequence's first row (such starts rise by at least the sequences' numbers of chunks).
+struct Records {
+  unsigned char* at;
+  int begin, length, dense;
+};
+
+FAK_DEV int64_t record_of(const Records& r, const GdnSeq& d, int s, int c) {
+  return r.dense ? (int64_t)s * r.length + (c - r.begin) : (int64_t)(d.r0 / kRows) + s + c;
+}
 
 template <int NS>
 struct Cfg {
@@ -67,31 +84,29 @@ struct Cfg {
   static constexpr int cols = n / 4;            // of a chain thread
   static constexpr int panels = (n + 63) / 64;  // of 64 columns, 128 bytes
   static constexpr int off_kq = 0;                                 // two stages of [K; Q]: two panels of 128 rows
-  static constexpr int off_tp = off_kq + 2 * 32768;                // [T; P T], two parts
-  static constexpr int off_ap = off_tp + 2 * kPart;                // [A; P], two parts
-  static constexpr int off_s = off_ap + 2 * kPart;                 // S, two parts
+  static constexpr int off_tp = off_kq + 2 * 32768;                // two stages of [T; P T], two parts
+  static constexpr int off_s = off_tp + 4 * kPart;                 // S, two parts
   static constexpr int off_u = off_s + 2 * panels * 16384;         // R, then U, two parts
   static constexpr int off_v = off_u + 2 * panels * 8192;          // two stages of V: panels of 64 columns
   static constexpr int off_z = off_v + 2 * panels * 8192;          // z: panels of 32 columns, 128 bytes
-  static constexpr int off_a = off_z + kRows * n * 4;          // A's blocks of 16 x 16 on the diagonal in f32
-  static constexpr int off_dec = off_a + 4 * 16 * kLd * 4;
-  static constexpr int off_sum = off_dec + 4 * (int)sizeof(Decays);  // sums of squares [2][NS * 4][64]
+  static constexpr int off_dec = off_z + kRows * n * 4;
+  static constexpr int off_sum = off_dec + 2 * (int)sizeof(Decays);  // sums of squares [2][NS * 4][64]
   static constexpr int off_gain = off_sum + 2 * NS * 4 * kRows * 4;
   static constexpr int off_max = off_gain + n * 4;  // [8]
   static constexpr int off_bar = off_max + 64;
   static constexpr int smem = off_bar + 192 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
-  static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n, dkk = 6 * n;  // TMEM columns
+  static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n;  // TMEM columns
   static constexpr int tmem_cols = 512;
-  static_assert(dkk + 64 <= tmem_cols, "TMEM");
+  static_assert(6 * n <= tmem_cols, "TMEM");
 };
 
-enum Bars { kLand0, kLand1, kD1, kD2, kD3, kKK, kKQ0, kKQ1, kV0, kV1, kZ, kZFree, kSum0, kSum1, kDrain, kBars };
+enum Bars { kLand0, kLand1, kD1, kD2, kD3, kReady0, kReady1, kZ, kZFree, kSum0, kSum1, kDrain, kBars };
 
 // Named barriers, for waits where a polling warp would take issue slots from those that work (a try of an mbarrier gives
 // up after some 60 cycles; with all waits so, half of all instructions were of such loops).  The products' warp polls, and
 // lets the others go.
-enum Named { kBarMax = 1, kBarPrep, kBarTurn, kBarS, kBarR, kBarU, kBarTP, kBarKK, kBarD1Top, kBarD1Low, kBarD2Top, kBarD2Low, kBarD3 };
+enum Named { kBarMax = 1, kBarTurn, kBarS, kBarR, kBarU, kBarD1Top, kBarD1Low, kBarD2Top, kBarD2Low, kBarD3 };
 
 template <int M, int N, bool A_MN, bool B_MN>
 constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -138,6 +153,10 @@ FAK_DEV bool try_cluster(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+FAK_DEV void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // Two f32 operations in one instruction.
@@ -194,14 +213,6 @@ FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int c
   }
 }
 
-template <int N>
-FAK_DEV void ld_cols(uint32_t addr, float2 (&x)[N / 2]) {
-  uint32_t r[N];
-  tmem_ld_cols<N>(addr, r);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-}
 // The sums of two columns each, `apart` columns apart.
 template <int N>
 FAK_DEV void ld_sums(uint32_t addr, int apart, float2 (&x)[N / 2]) {
@@ -281,8 +292,8 @@ struct ChunkDebug {
 };
 
 template <int NS>
-__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, const __grid_constant__ ChunkMaps maps, ChunkDebug dbg,
-                                                                 int* status) {
+__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, const __grid_constant__ ChunkMaps maps, Records records,
+                                                                 ChunkDebug dbg, int* status) {
   using C = Cfg<NS>;
   constexpr int n = C::n, W = C::cols;
   extern __shared__ unsigned char raw[];
@@ -304,23 +315,24 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   const int rows = d.r1 - d.first;
   if (p.few && rows <= p.few) return;  // the steps' kernel's
   const int col0 = slice * n;
-  for (int i = threadIdx.x; i < (d.first - d.r0) * (n / 4); i += kThreads) {
-    const int row = d.r0 + i / (n / 4);
-    gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (n / 4)), gdn_zero4());
-  }
-  if (rows == 0) return;
-  const int chunks = (rows + kRows - 1) / kRows;
+  const int begin = records.begin, end = min((rows + kRows - 1) / kRows, begin + records.length);  // this launch's chunks
+  if (begin == 0)
+    for (int i = threadIdx.x; i < (d.first - d.r0) * (n / 4); i += kThreads) {
+      const int row = d.r0 + i / (n / 4);
+      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (n / 4)), gdn_zero4());
+    }
+  const int chunks = end - begin;  // counted from 0 below; chunk c's rows are first + 64 c ..
+  if (chunks <= 0) return;
+  const int first_row = d.first + begin * kRows, rows_left = rows - begin * kRows;
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : i == kKQ0 || i == kKQ1 ? 2 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 8) reinterpret_cast<unsigned*>(smem + C::off_max)[threadIdx.x] = 0;
   if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
-  // T and P T are zero above their blocks on the diagonal, which nothing writes
-  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kThreads) *reinterpret_cast<uint4*>(smem + C::off_tp + 16 * i) = make_uint4(0, 0, 0, 0);
-  if (warp == 20) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(C::tmem_cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -364,13 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     named_bar_sync(named, threads + 32);
     tc_fence_after_sync();
   };
-  auto decays = [&](int c) { return reinterpret_cast<Decays*>(smem + C::off_dec) + (c & 3); };
-
-  // registers of a thread: 4 * 80 + 104 + 56 of the 6 * 80 that the block has
-  if (warp >= 20)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  else if (warp >= 16)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+  auto decays = [&](int c) { return reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1); };
 
   if (warp < 16) {
     // ------------------------------------------------------------------ the chain
@@ -385,15 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     float2 S[W / 2];
 #pragma unroll
     for (int i = 0; i < W / 2; i += 2) {
-      const float4 x = d.fresh ? gdn_zero4() : *reinterpret_cast<const float4*>(st + 2 * i);
+      const float4 x = d.fresh && begin == 0 ? gdn_zero4() : *reinterpret_cast<const float4*>(st + 2 * i);
       S[i] = make_float2(x.x, x.y);
       S[i + 1] = make_float2(x.z, x.w);
     }
     uint32_t v[W / 2];  // of the next chunk
     auto fetch_v = [&](int c) {
-      wait(kV0 + (c & 1), c >> 1);
+      wait(kReady0 + (c & 1), c >> 1);
       const unsigned char* src = smem + C::off_v + (c & 1) * C::panels * 8192 + (col >> 6) * 8192 + t * 128;
-      const bool there = c * kRows + t < rows;  // (what stands behind the last row is another's, whatever it holds)
+      const bool there = c * kRows + t < rows_left;  // (what stands behind the last row is another's, whatever it holds)
 #pragma unroll
       for (int i = 0; i < W / 8; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(src + (((((col & 63) >> 3) + i) ^ (t & 7)) << 4));
@@ -483,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       // The rows turn in S's place, which the chunk's first product is done with, so that stores are whole lines: a thread's
       // own row would be a line for every lane (3,000 cycles a chunk).
       unsigned char* turn = smem + C::off_s;
-      const int have = min(kRows, rows - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
-      const int64_t to = (int64_t)(d.first + c * kRows) * p.out_row + h * p.out_head + col0;
+      const int have = min(kRows, rows_left - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
+      const int64_t to = (int64_t)(first_row + c * kRows) * p.out_row + h * p.out_head + col0;
       if (p.out_bf16) {
         constexpr int line = n / 8;  // pieces of a row
 #pragma unroll
@@ -578,58 +584,340 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < W / 2; i += 2) *reinterpret_cast<float4*>(st + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
-  } else if (warp < 20) {
-    // ------------------------------------------------------------------ T and P T
-    const int w = warp - 16, r = threadIdx.x - kChainThreads;
-    float* diag = reinterpret_cast<float*>(smem + C::off_a);
-    unsigned char *tp = smem + C::off_tp, *ap = smem + C::off_ap;
-    const uint32_t tps = smem_u32(tp), aps = smem_u32(ap);
-    const bool top = w < 2, late = w & 1;  // K K^T's rows; rows from 32 on
-    const int t = r & (kRows - 1);
-    const uint32_t acc = tmem + ((uint32_t)w << 21) + C::dkk;
+  } else if (warp == 16) {
+    // ------------------------------------------------------------------ the products
+    const uint32_t kq = smem_u32(smem + C::off_kq), tp = smem_u32(smem + C::off_tp), ss = smem_u32(smem + C::off_s),
+                   us = smem_u32(smem + C::off_u);
     for (int c = 0; c < chunks; ++c) {
-      take(kBarKK, kPrepThreads);
-      const Decays* dec = decays(c);
-      {
-        // row r of [A; P], from K K^T and Q K^T by the decays: over the row's own 32 columns one exponential each; to the 32
-        // before them by way of row 31
-        const float hi = dec->hi[t], lo = dec->lo[t], b = top ? dec->beta[t] : 1.0f;
-        const int own = 32 * late, last = (top ? lane - 1 : lane);
-        float2 x[16];
-        ld_cols<32>(acc + own, x);
+      const uint32_t kqc = kq + (c & 1) * 32768, tpc = tp + (c & 1) * 2 * kPart;
+      wait(kReady0 + (c & 1), c >> 1);
+      take(kBarS, kChainThreads);
+      if (elect_one()) {
+        const uint64_t a = umma_desc_sw128(kqc), b = desc_mn(ss, 16384);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float4 u = *reinterpret_cast<const float4*>(&dec->hi[own + 2 * i]);
-          const float4 l = *reinterpret_cast<const float4*>(&dec->lo[own + 2 * i]);
-          const float2 e0 = add2(fma2(make_float2(u.x, u.y), both(-1.0f), both(hi)), fma2(make_float2(l.x, l.y), both(-1.0f), both(lo)));
-          const float2 e1 = add2(fma2(make_float2(u.z, u.w), both(-1.0f), both(hi)), fma2(make_float2(l.z, l.w), both(-1.0f), both(lo)));
-          x[i] = mul2(mul2(x[i], both(b)), make_float2(exp2_approx(e0.x), exp2_approx(e0.y)));
-          x[i + 1] = mul2(mul2(x[i + 1], both(b)), make_float2(exp2_approx(e1.x), exp2_approx(e1.y)));
+        for (int k = 0; k < 8; ++k)
+          mma_f16(tmem + C::d1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
+        umma_commit(&bar[kD1]);
+      }
+      __syncwarp();
+      wait(kD1, c);
+      give(kBarD1Top, kChainThreads / 2);
+      give(kBarD1Low, kChainThreads / 2);
+      take(kBarR, kChainThreads / 2);
+      if (elect_one()) {
+        const uint64_t a = umma_desc_sw128(tpc), b = desc_mn(us, 8192);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_f16(tmem + C::d2, a + 2 * k, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
+          mma_f16(tmem + C::d2, a + (kPart >> 4) + 2 * k, b + k * (2048 >> 4), kIdesc<128, n, false, true>, 1);
         }
+        umma_commit(&bar[kD2]);
+      }
+      __syncwarp();
+      wait(kD2, c);
+      give(kBarD2Top, kChainThreads / 2);
+      give(kBarD2Low, kChainThreads / 2);
+      take(kBarU, kChainThreads / 2);
+      if (elect_one()) {
+        const uint64_t a = desc_mn(kqc, 16384), b = desc_mn(us, 8192);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = make_float2(2 * i <= last ? x[i].x : 0.0f, 2 * i + 1 <= last ? x[i].y : 0.0f);
-        if (top) {
-          float* to = diag + t * kLd;
-          const bool second = lane >= 16;
-#pragma unroll
-          for (int i = 0; i < 8; i += 2)
-            *reinterpret_cast<float4*>(to + 2 * i) = second ? make_float4(x[8 + i].x, x[8 + i].y, x[9 + i].x, x[9 + i].y)
-                                                            : make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
-        }
-        put_halves<32>(ap, 0, kPart, r, own, x);
-        if (late) {
-          const float f = b * dec->mid[t];
-          ld_cols<32>(acc, x);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float4 u = *reinterpret_cast<const float4*>(&dec->mid[2 * i]);
-            x[i] = mul2(x[i], mul2(both(f), make_float2(u.x, u.y)));
-            x[i + 1] = mul2(x[i + 1], mul2(both(f), make_float2(u.z, u.w)));
-          }
-          put_halves<32>(ap, 0, kPart, r, 0, x);
+        for (int k = 0; k < 4; ++k)
+          mma_f16(tmem + C::d3, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc<128, 2 * n, true, true>, k > 0);
+        umma_commit(&bar[kD3]);
+      }
+      __syncwarp();
+      wait(kD3, c);
+      give(kBarD3, kChainThreads);
+    }
+    if (*abort) {  // what was issued is done with before the TMEM goes
+      if (elect_one()) {
+        umma_commit(&bar[kDrain]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_suspend(&bar[kDrain], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
         }
       }
-      named_bar_sync(kBarPrep, kPrepThreads);
+      __syncwarp();
+    }
+  } else if (warp == 17) {
+    // ------------------------------------------------------------------ K, Q and z
+    // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
+    // and those that were are waited for before the block ends.
+    const int hk = h / p.group;
+    int copied = 0, gates = 0;  // chunks of which all but z, and of which z, was asked for
+    auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
+    auto load_z = [&](int c) {
+      if (!p.z) return;
+      if (c >= 1) doze(kZFree, c - 1);
+      if (dead()) return;
+      gates = c + 1;
+      unsigned char* zs = smem + C::off_z;
+      const int first = c * kRows, have = min(kRows, rows_left - first);
+      if (p.z_wide) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
+#pragma unroll
+          for (int i = 0; i < n / 32; ++i) tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, first_row + first, &bar[kZ]);
+        }
+        __syncwarp();
+      } else {
+        const float* z0 = p.z + (first_row + first) * p.z_row + h * p.z_head + col0;
+#pragma unroll 8
+        for (int u = 0; u < kRows * n / 32; ++u) {
+          const int at = u * 32 + lane, x = at / n, cl = at % n;
+          if (x < have)
+            *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
+                z0[x * p.z_row + cl];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kZ]);
+      }
+    };
+    for (int c = 0; c < chunks; ++c) {
+      if (c >= 2) doze(kD3, c - 2);
+      if (dead()) break;
+      copied = c + 1;
+      const int first = c * kRows, have = min(kRows, rows_left - first);
+      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
+      if (elect_one()) {
+        uint64_t* land = &bar[kLand0 + (c & 1)];
+        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * n * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, first_row + first, land);
+          tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, first_row + first, land);
+        }
+        // (V of two chunks before is in registers since that chunk's state was made)
+#pragma unroll
+        for (int i = 0; i < C::panels; ++i)
+          tma_load_3d_tx(smem + C::off_v + ((c & 1) * C::panels + i) * 8192, &maps.v, col0 + 64 * i, h, first_row + first, land);
+        const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
+        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
+        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
+      }
+      __syncwarp();
+      doze(kLand0 + (c & 1), c >> 1);
+      if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
+        for (int i = lane; i < (kRows - have) * 32; i += 32) {
+          const int row = have + (i >> 5), at = i & 31;
+          *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+      if (!dbg.unreachable) arrive(kReady0 + (c & 1));
+      if (c > 0) load_z(c - 1);  // (wanted when the next chunk is on its way)
+    }
+    load_z(chunks - 1);
+    if (dead()) {
+      auto drain = [&](int b, int phase) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
+        }
+      };
+      for (int c = max(0, copied - 2); c < copied; ++c) {
+        drain(kLand0 + (c & 1), c >> 1);
+      }
+      if (gates && p.z_wide) drain(kZ, gates - 1);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  // (no CTA leaves while another may still store into it)
+  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (NS > 1 && *abort) {  // (and a store that nothing waited for lands within a microsecond)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 50000) {
+    }
+    __syncwarp();
+  }
+  if (warp == 16) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ T and P T
+constexpr int kOffTp = 32768, kOffDiag = kOffTp + 2 * kPart, kOffHi = kOffDiag + 4 * 16 * kLd * 4;  // behind [K; Q]
+constexpr int kPrepSmem = kOffHi + 4 * 3 * kRows * 4 + 1024;
+
+// The sequence and chunk whose record is x, the whole warp: false where there is none.
+FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int64_t x, int lane, GdnSeq& d, int& s, int& c) {
+  auto has = [&](int i, GdnSeq& e) {  // sequence i's chunk at x, or -1
+    e = gdn_seq(p.c, kv_seq(p.c, i), i);
+    const int rows = e.r1 - e.first;
+    if (!e.ok || rows == 0 || (p.few && rows <= p.few)) return -1;
+    const int64_t at = x - (r.dense ? (int64_t)i * r.length - r.begin : (int64_t)(e.r0 / kRows) + i);
+    return at < r.begin || at >= r.begin + r.length || at * kRows >= rows ? -1 : (int)at;
+  };
+  if (r.dense) {
+    s = (int)(x / r.length);
+    return (c = has(s, d)) >= 0;
+  }
+  // where the starts rise, 32 probes a round
+  int lo = 0, hi = p.c.n_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const unsigned b = __ballot_sync(0xffffffffu, i < hi && (int64_t)(p.c.row_start[i] / kRows) + i <= x);
+    const int n = __popc(b);
+    if (n > 1) lo += (n - 1) * step;
+    hi = min(lo + step, hi);
+  }
+  s = lo;
+  if ((c = has(s, d)) >= 0) return true;
+  // where they may fall beside numbers that are out of range: all sequences, where any is
+#pragma unroll 1
+  for (int base = 0; base < p.c.n_seqs; base += 32) {
+    GdnSeq e{0, 0, 0, 0, false, false};
+    const int at = base + lane < p.c.n_seqs ? has(base + lane, e) : -1;
+    const unsigned any = __ballot_sync(0xffffffffu, at >= 0);
+    if (!any) continue;
+    s = base + __ffs(any) - 1;
+    c = has(s, d);
+    return true;
+  }
+  return false;
+}
+
+// Block (x, h): record x, key head h.
+__global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __grid_constant__ GdnParams p, Records records) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q2 = 2 * (lane & 3);
+  const int hk = blockIdx.y;
+  GdnSeq d;
+  int s, c;
+  if (!find_chunk(p, records, blockIdx.x, lane, d, s, c)) return;
+  const int rows = d.r1 - d.first, first = c * kRows, have = min(kRows, rows - first);
+  unsigned char *kq = smem, *tp = smem + kOffTp;
+  const uint32_t kqs = smem_u32(kq), tps = smem_u32(tp);
+  float* diag = reinterpret_cast<float*>(smem + kOffDiag);
+
+  // K and Q, 16 threads to a row of 256 bytes; zeros behind the last row
+  {
+    const int piece = threadIdx.x & 15, x0 = threadIdx.x >> 4;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const __half* src = m ? p.q + (int64_t)(d.first + first) * p.q_row + hk * p.q_head + 8 * piece
+                            : p.k + (int64_t)(d.first + first) * p.k_row + hk * p.k_head + 8 * piece;
+      const int64_t step = m ? p.q_row : p.k_row;
+      const uint32_t dst = kqs + (piece >> 3) * 16384 + m * 8192 + (((piece & 7) ^ x0) << 4);
+#pragma unroll
+      for (int u = 0; u < kRows / 8; ++u) {
+        const int x = 8 * u + x0;
+        copy16(dst + x * 128, x < have ? src + x * step : src, x < have);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // T and P T are zero above their blocks on the diagonal, which nothing writes
+  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kPrepThreads) *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(0, 0, 0, 0);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+
+  // Rows 16 m .. of K K^T (m = w) and of Q K^T (m = 3 - w), ten tiles of 8 columns to a warp
+  float kk[8][4] = {}, qk[8][4] = {};
+  const int mk = w, mq = 3 - w;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
+    uint32_t ak[4], aq[4];
+    ldsm4(ak, at(16 * mk + (lane & 15), 2 * k + (lane >> 4)));
+    ldsm4(aq, at(64 + 16 * mq + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {  // rows 8 j .. +15 of K: two tiles
+      if (j > 2 * max(mk, mq)) continue;
+      uint32_t b[4];
+      ldsm4(b, at(8 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+      const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
+      if (j <= 2 * mk) {
+        mma16(kk[j], ak, b0);
+        mma16(kk[j + 1], ak, b1);
+      }
+      if (j <= 2 * mq) {
+        mma16(qk[j], aq, b0);
+        mma16(qk[j + 1], aq, b1);
+      }
+    }
+  }
+
+  for (int h0 = 0; h0 < p.group; h0 += 4) {
+    const int heads = min(4, p.group - h0);
+    if (w < heads) {
+      // Sums of g log2(e), two rows to a lane, in units of 2^-40; a decay of 2^-150 and below is as good as none left (and
+      // sums that grow are cut where 2^G is infinite by far).  A NaN stays one from its row on.
+      const int h = hk * p.group + h0 + w;
+      float b[2];
+      long long x[2];
+      bool odd[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = 2 * lane + j;
+        const int64_t row = d.first + first + at;
+        const float gate = at < have ? p.g[row * p.nv + h] : 0.0f;
+        b[j] = at < have ? p.beta[row * p.nv + h] : 0.0f;
+        odd[j] = gate != gate;
+        const float y = fminf(fmaxf(gate, -104.0f), 5000.0f);  // -150 log(2)
+        const float hi = y * 1.44269504f, lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
+        x[j] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
+      }
+      const unsigned any = __ballot_sync(0xffffffffu, odd[0] || odd[1]);
+      long long sum = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const bool before = any & ((1u << lane) - 1);
+      const long long G[2] = {sum - x[1], sum};
+      float hi[2], lo[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const long long u = (G[j] + (1ll << 30)) >> 31;
+        hi[j] = (float)(int)u * (1.0f / 512.0f);
+        lo[j] = (float)(int)(G[j] - (u << 31)) * 9.094947017729282e-13f;  // 2^-40
+        if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
+      }
+      const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
+      float* mine = reinterpret_cast<float*>(smem + kOffHi) + w * 3 * kRows + 2 * lane;
+      *reinterpret_cast<float2*>(mine) = make_float2(hi[0], hi[1]);
+      *reinterpret_cast<float2*>(mine + kRows) = make_float2(lo[0], lo[1]);
+      *reinterpret_cast<float2*>(mine + 2 * kRows) = make_float2(b[0], b[1]);
+      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord + 2 * kPart + 8 * lane;
+      *reinterpret_cast<float2*>(record) = make_float2(exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
+      *reinterpret_cast<float2*>(record + 4 * kRows) =
+          make_float2(exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
+      *reinterpret_cast<float2*>(record + 8 * kRows) = make_float2(b[0], b[1]);
+    }
+    __syncthreads();
+    for (int hh = 0; hh < heads; ++hh) {
+      const int h = hk * p.group + h0 + hh;
+      const float* hi = reinterpret_cast<const float*>(smem + kOffHi) + hh * 3 * kRows;
+      const float *lo = hi + kRows, *beta = hi + 2 * kRows;
+      // A and P from K K^T and Q K^T by the decays, to the places of T and P T
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int tile = m ? mq : mk, row = 16 * tile + g;
+        const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
+        const float b0 = m ? 1.0f : beta[row], b1 = m ? 1.0f : beta[row + 8];
+        const int last0 = m ? row : row - 1, last1 = last0 + 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j > 2 * tile + 1) continue;
+          const int col = 8 * j + q2;
+          const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
+          const float* x = m ? qk[j] : kk[j];
+          float y[4] = {b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * x[0], b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * x[1],
+                        b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * x[2], b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * x[3]};
+          // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
+          if (col > last0) y[0] = 0.0f;
+          if (col + 1 > last0) y[1] = 0.0f;
+          if (col > last1) y[2] = 0.0f;
+          if (col + 1 > last1) y[3] = 0.0f;
+          put_block(tp, m * kRows + 16 * tile, j, y, 1.0f, lane);
+          if (!m && j >= 2 * tile) {
+            *reinterpret_cast<float2*>(diag + row * kLd + (col & 15)) = make_float2(y[0], y[1]);
+            *reinterpret_cast<float2*>(diag + (row + 8) * kLd + (col & 15)) = make_float2(y[2], y[3]);
+          }
+        }
+      }
+      __syncthreads();
       {
         // row lane % 16 of the inverse of the 16 x 16 block of I + A at 16 w
         const int row = lane & 15;
@@ -656,14 +944,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
         if (lane < 16) put_halves<16>(tp, 0, kPart, 16 * w + row, 16 * w, y);
       }
-      named_bar_sync(kBarPrep, kPrepThreads);
+      __syncthreads();
       {
         // two blocks of 32: the lower left is -T22 (A21 T11), eight columns to a warp
         const int at = 32 * (w >> 1), j = (at >> 3) + (w & 1);
         float x[4] = {}, y[4] = {}, x1[4] = {}, y1[4] = {}, x2[4] = {}, y2[4] = {};  // (products that do not wait for each other)
         FragA a, u;
         FragB b;
-        load_a(a, aps, at + 16, at, lane);
+        load_a(a, tps, at + 16, at, lane);
         load_a(u, tps, at + 16, at + 16, lane);
         load_b(b, tps, at, j, lane);
         mma16(x1, a.lo, b.hi);
@@ -677,9 +965,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         mma16(y, u.hi, b.hi);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] += y1[i] + y2[i];
+        __syncthreads();  // (A21 is read)
         put_block(tp, at + 16, j, y, -1.0f, lane);
       }
-      named_bar_sync(kBarPrep, kPrepThreads);
+      __syncthreads();
       {
         // the block of 64's, 32 x 32, eight columns to a warp
         float x[2][4] = {}, y[2][4] = {};
@@ -689,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         for (int k = 0; k < 2; ++k) {
           load_b(b, tps, 16 * k, w, lane);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) load_a(a[m], aps, 32 + 16 * m, 16 * k, lane);
+          for (int m = 0; m < 2; ++m) load_a(a[m], tps, 32 + 16 * m, 16 * k, lane);
 #pragma unroll
           for (int m = 0; m < 2; ++m) mma16(x[m], a[m].lo, b.hi);
 #pragma unroll
@@ -709,264 +998,54 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 #pragma unroll
           for (int m = k; m < 2; ++m) mma16(y[m], a[m].hi, b.hi);
         }
+        __syncthreads();  // (A21 is read)
 #pragma unroll
         for (int m = 0; m < 2; ++m) put_block(tp, 32 + 16 * m, w, y[m], -1.0f, lane);
       }
-      named_bar_sync(kBarPrep, kPrepThreads);
-      // P T, eight columns at a time: tiles 0 and 1 take ten steps, 2 and 3 six, 4 and 5 three, 6 and 7 one
-      for (int j = w; j < 8; j += w < 2 ? 8 : 2) {
-        float y[4][4] = {};
-        FragB b;
+      __syncthreads();
+      {
+        // P T in place of P, by blocks of 16 x 16 (m, j): sums over k = j .. m, five steps to a warp
+        const unsigned mine = w == 0 ? 0xffff0030u : w == 1 ? 0xffff3231u : w == 2 ? 0xffff1020u : 0x11223321u;
+        float y[4][2][4] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < j >> 1) continue;
-          load_b(b, tps, 16 * k, j, lane);
-          FragA a[4];
+        for (int i = 0; i < 4; ++i) {
+          const int m = mine >> (8 * i + 4) & 15, j = mine >> (8 * i) & 15;
+          if (m == 15) break;
+          for (int k = j; k <= m; ++k) {
+            FragA a;
+            FragB b[2];
+            load_a(a, tps, kRows + 16 * m, 16 * k, lane);
+            load_b(b[0], tps, 16 * k, 2 * j, lane);
+            load_b(b[1], tps, 16 * k, 2 * j + 1, lane);
 #pragma unroll
-          for (int m = k; m < 4; ++m) load_a(a[m], aps, kRows + 16 * m, 16 * k, lane);
+            for (int u = 0; u < 2; ++u) mma16(y[i][u], a.lo, b[u].hi);
 #pragma unroll
-          for (int m = k; m < 4; ++m) mma16(y[m], a[m].lo, b.hi);
+            for (int u = 0; u < 2; ++u) mma16(y[i][u], a.hi, b[u].lo);
 #pragma unroll
-          for (int m = k; m < 4; ++m) mma16(y[m], a[m].hi, b.lo);
-#pragma unroll
-          for (int m = k; m < 4; ++m) mma16(y[m], a[m].hi, b.hi);
+            for (int u = 0; u < 2; ++u) mma16(y[i][u], a.hi, b[u].hi);
+          }
         }
+        __syncthreads();  // (P is read)
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (m >= j >> 1) put_block(tp, kRows + 16 * m, j, y[m], 1.0f, lane);
-      }
-      // (the next chunk's K K^T comes after the product that reads this: nothing is written over before)
-      give(kBarTP, kPrepThreads);
-    }
-  } else if (warp == 20) {
-    // ------------------------------------------------------------------ the products
-    const uint32_t kq = smem_u32(smem + C::off_kq), tp = smem_u32(smem + C::off_tp), ss = smem_u32(smem + C::off_s),
-                   us = smem_u32(smem + C::off_u);
-    auto overlap = [&](int c) {  // [K; Q] K^T of chunk c
-      wait(kKQ0 + (c & 1), c >> 1);
-      tc_fence_after_sync();
-      if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(kq + (c & 1) * 32768);
+        for (int i = 0; i < 4; ++i) {
+          const int m = mine >> (8 * i + 4) & 15, j = mine >> (8 * i) & 15;
+          if (m == 15) break;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t at = a + (k >> 2) * (16384 >> 4) + (k & 3) * 2;
-          mma_f16(tmem + C::dkk, at, at, kIdesc<128, 64, false, false>, k > 0);
-        }
-        umma_commit(&bar[kKK]);
-      }
-      __syncwarp();
-    };
-    overlap(0);
-    wait(kKK, 0);
-    give(kBarKK, kPrepThreads);
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t kqc = kq + (c & 1) * 32768;
-      take(kBarS, kChainThreads);
-      if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(kqc), b = desc_mn(ss, 16384);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16(tmem + C::d1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
-        umma_commit(&bar[kD1]);
-      }
-      __syncwarp();
-      wait(kD1, c);
-      give(kBarD1Top, kChainThreads / 2);
-      give(kBarD1Low, kChainThreads / 2);
-      take(kBarTP, kPrepThreads);
-      take(kBarR, kChainThreads / 2);
-      if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(tp), b = desc_mn(us, 8192);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mma_f16(tmem + C::d2, a + 2 * k, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
-          mma_f16(tmem + C::d2, a + (kPart >> 4) + 2 * k, b + k * (2048 >> 4), kIdesc<128, n, false, true>, 1);
-        }
-        umma_commit(&bar[kD2]);
-      }
-      __syncwarp();
-      if (c + 1 < chunks) overlap(c + 1);
-      wait(kD2, c);
-      give(kBarD2Top, kChainThreads / 2);
-      give(kBarD2Low, kChainThreads / 2);
-      if (c + 1 < chunks) {
-        wait(kKK, c + 1);
-        give(kBarKK, kPrepThreads);
-      }
-      take(kBarU, kChainThreads / 2);
-      if (elect_one()) {
-        const uint64_t a = desc_mn(kqc, 16384), b = desc_mn(us, 8192);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16(tmem + C::d3, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc<128, 2 * n, true, true>, k > 0);
-        umma_commit(&bar[kD3]);
-      }
-      __syncwarp();
-      wait(kD3, c);
-      give(kBarD3, kChainThreads);
-    }
-    if (*abort) {  // what was issued is done with before the TMEM goes
-      if (elect_one()) {
-        umma_commit(&bar[kDrain]);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_suspend(&bar[kDrain], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
+          for (int u = 0; u < 2; ++u) put_block(tp, kRows + 16 * m, 2 * j + u, y[i][u], 1.0f, lane);
         }
       }
-      __syncwarp();
-    }
-  } else if (warp == 21) {
-    // ------------------------------------------------------------------ K, Q and z
-    // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
-    // and those that were are waited for before the block ends.
-    const int hk = h / p.group;
-    int copied = 0, gates = 0;  // chunks whose K, Q and V, and whose z, were asked for
-    auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
-    auto load_z = [&](int c) {
-      if (!p.z) return;
-      if (c >= 1) doze(kZFree, c - 1);
-      if (dead()) return;
-      gates = c + 1;
-      unsigned char* zs = smem + C::off_z;
-      const int first = c * kRows, have = min(kRows, rows - first);
-      if (p.z_wide) {
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
-#pragma unroll
-          for (int i = 0; i < n / 32; ++i) tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, d.first + first, &bar[kZ]);
-        }
-        __syncwarp();
-      } else {
-        const float* z0 = p.z + (d.first + first) * p.z_row + h * p.z_head + col0;
-#pragma unroll 8
-        for (int u = 0; u < kRows * n / 32; ++u) {
-          const int at = u * 32 + lane, x = at / n, cl = at % n;
-          if (x < have)
-            *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
-                z0[x * p.z_row + cl];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kZ]);
+      fence_async();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(record), "r"(tps), "r"(2 * kPart) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       }
-    };
-    for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) doze(kD3, c - 2);
-      if (dead()) break;
-      copied = c + 1;
-      const int first = c * kRows, have = min(kRows, rows - first);
-      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&bar[kLand0 + (c & 1)], 32768);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, d.first + first, &bar[kLand0 + (c & 1)]);
-          tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, d.first + first, &bar[kLand0 + (c & 1)]);
-        }
-        // (V of two chunks before is in registers since that chunk's state was made)
-        mbar_arrive_expect_tx(&bar[kV0 + (c & 1)], kRows * n * 2);
-#pragma unroll
-        for (int i = 0; i < C::panels; ++i)
-          tma_load_3d_tx(smem + C::off_v + ((c & 1) * C::panels + i) * 8192, &maps.v, col0 + 64 * i, h, d.first + first, &bar[kV0 + (c & 1)]);
-      }
-      __syncwarp();
-      doze(kLand0 + (c & 1), c >> 1);
-      if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
-        for (int i = lane; i < (kRows - have) * 32; i += 32) {
-          const int row = have + (i >> 5), at = i & 31;
-          *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-      if (!dbg.unreachable) arrive(kKQ0 + (c & 1));
-      if (c > 0) load_z(c - 1);  // (wanted when the next chunk is on its way)
-    }
-    load_z(chunks - 1);
-    if (dead()) {
-      auto drain = [&](int b, int phase) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
-        }
-      };
-      for (int c = max(0, copied - 2); c < copied; ++c) {
-        drain(kLand0 + (c & 1), c >> 1);
-        drain(kV0 + (c & 1), c >> 1);
-      }
-      if (gates && p.z_wide) drain(kZ, gates - 1);
-    }
-  } else if (warp == 22) {
-    // ------------------------------------------------------------------ the decays
-    float g[2], b[2];
-    auto fetch = [&](int c) {  // two rows to a lane
-      const int at = c * kRows + 2 * lane;
-      const int64_t row = d.first + at;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        g[j] = at + j < rows ? p.g[(row + j) * p.nv + h] : 0.0f;
-        b[j] = at + j < rows ? p.beta[(row + j) * p.nv + h] : 0.0f;
-      }
-    };
-    fetch(0);
-    for (int c = 0; c < chunks; ++c) {
-      // Sums of g log2(e) in units of 2^-40; a decay of 2^-150 and below is as good as none left (and sums that grow are cut
-      // where 2^G is infinite by far).  A NaN stays one from its row on.
-      long long x[2];
-      bool odd[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        odd[j] = g[j] != g[j];
-        const float y = fminf(fmaxf(g[j], -104.0f), 5000.0f);  // -150 log(2)
-        const float hi = y * 1.44269504f, lo = fmaf(y, 1.44269504f, -hi) + y * 1.92596299e-8f;
-        x[j] = __float2ll_rn(hi * 1099511627776.0f) + __float2ll_rn(lo * 1099511627776.0f);
-      }
-      const float beta[2] = {b[0], b[1]};
-      const unsigned any = __ballot_sync(0xffffffffu, odd[0] || odd[1]);
-      fetch(c + 1);
-      long long sum = x[0] + x[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const bool before = any & ((1u << lane) - 1);
-      const long long G[2] = {sum - x[1], sum};
-      float hi[2], lo[2], mid[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const long long u = (G[j] + (1ll << 30)) >> 31;
-        hi[j] = (float)(int)u * (1.0f / 512.0f);
-        lo[j] = (float)(int)(G[j] - (u << 31)) * 9.094947017729282e-13f;  // 2^-40
-        if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
-      }
-      const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
-      const float hi_mid = __shfl_sync(0xffffffffu, hi[1], 15), lo_mid = __shfl_sync(0xffffffffu, lo[1], 15);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float e = (hi_mid - hi[j]) + (lo_mid - lo[j]);
-        mid[j] = exp2_approx(lane < 16 ? e : -e);
-      }
-      if (c >= 2) doze(kD3, c - 2);
-      Decays* dec = decays(c);
-      auto put2 = [&](float* at, float y0, float y1) { *reinterpret_cast<float2*>(at + 2 * lane) = make_float2(y0, y1); };
-      put2(dec->hi, hi[0], hi[1]);
-      put2(dec->lo, lo[0], lo[1]);
-      put2(dec->beta, beta[0], beta[1]);
-      put2(dec->keep, exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
-      put2(dec->left, exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
-      put2(dec->mid, mid[0], mid[1]);
-      arrive(kKQ0 + (c & 1));
+      __syncthreads();
     }
   }
-  tc_fence_before_sync();
-  __syncthreads();
-  // (no CTA leaves while another may still store into it)
-  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (NS > 1 && *abort) {  // (and a store that nothing waited for lands within a microsecond)
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 50000) {
-    }
-    __syncwarp();
-  }
-  if (warp == 20) {
-    tc_fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
-  }
+  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 std::mutex g_mu;
@@ -997,7 +1076,8 @@ bool rows_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int6
 }
 
 template <int NS>
-cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const ChunkDebug& dbg, int* status, int dev, cudaStream_t s) {
+cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const Records& records, const ChunkDebug& dbg, int* status, int dev,
+                   cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = kv_smem_limit(gdn_chunk_kernel<NS>, Cfg<NS>::smem, dev, done);
   if (e != cudaSuccess) return e;
@@ -1012,13 +1092,15 @@ cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const ChunkDebug& 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, maps, dbg, status);
+  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, maps, records, dbg, status);
 }
+
+constexpr int64_t kScratch = 1LL << 30;  // most bytes of records at a time; more chunks than they hold go in several launches
 
 }  // namespace
 
 cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, cudaStream_t s) {
-  const cudaError_t e = encoder();
+  cudaError_t e = encoder();
   if (e != cudaSuccess) return e;
   ChunkMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -1029,5 +1111,28 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
       (p.z && p.z_wide && !rows_map(&maps.z, p.z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.c.rows, p.nv, p.z_row, p.z_head)))
     return cudaErrorInvalidValue;
   const ChunkDebug dbg{timeout_ns, unreachable};
-  return launch<2>(p, maps, dbg, status, dev, s);
+  // records of all chunks, where they are few enough; else of a stretch of every sequence at a time
+  const int longest = (int)((std::min<int64_t>(p.c.max_q, p.c.rows) + kRows - 1) / kRows);
+  const int64_t head = (int64_t)p.nv * kRecord, all = (p.c.rows / kRows + p.c.n_seqs) * head;
+  Records records{nullptr, 0, longest, 0};
+  int64_t bytes = all;
+  if (all > kScratch) {
+    records.dense = 1;
+    records.length = (int)std::min<int64_t>(longest, std::max<int64_t>(1, kScratch / (p.c.n_seqs * head)));
+    bytes = (int64_t)p.c.n_seqs * records.length * head;
+  }
+  void* scratch = nullptr;
+  e = fak_scratch_alloc(&scratch, (size_t)bytes, s);
+  if (e != cudaSuccess) return cudaErrorMemoryAllocation;
+  records.at = static_cast<unsigned char*>(scratch);
+  static std::atomic<uint64_t> done{0};
+  e = kv_smem_limit(gdn_prepare_kernel, kPrepSmem, dev, done);
+  for (; e == cudaSuccess && records.begin < longest; records.begin += records.length) {
+    const int64_t slots = records.dense ? (int64_t)p.c.n_seqs * records.length : p.c.rows / kRows + p.c.n_seqs;
+    gdn_prepare_kernel<<<dim3((unsigned)slots, (unsigned)nk), kPrepThreads, kPrepSmem, s>>>(p, records);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch<2>(p, maps, records, dbg, status, dev, s);
+  }
+  const cudaError_t f = cudaFreeAsync(scratch, s);
+  return e != cudaSuccess ? e : f;
 }
