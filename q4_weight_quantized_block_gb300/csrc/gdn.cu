@@ -358,7 +358,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   if (st != FAK_OK) return st;
   if (a->out_type != FAK_ROWS_F32 && a->out_type != FAK_ROWS_BF16) return FAK_ERR_INVALID_ARG;
   if (a->nk < 1 || a->nv < 1 || a->nv > 65535 || a->nv % a->nk || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
-      (int64_t)batch->n_seqs * a->nv > 0x7fffffff)
+      (int64_t)batch->n_seqs * a->nv > 0x3fffffff)
     return FAK_ERR_SHAPE;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !(a->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
   if (a->rows && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->out)) return FAK_ERR_INVALID_ARG;

@@ -22,14 +22,15 @@
 // instructions.  (Made by four more warps of the second kernel, a chunk ahead, the same work took longer than a chunk's
 // products, and once for each CTA of a head.)
 //
-// Second kernel: a cluster holds one head of one sequence, a CTA (one on an SM) 128 / NS of its value columns, as its own
-// rule: only the norm needs the whole row, and its sums of squares go to the other CTAs by asynchronous stores.  Warps:
-//   0 .. 15   a warp reads the accumulators' 32 lanes (w % 4) and a quarter of their columns (w / 4); lanes 0..63 are K's or
-//             T's rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128.  (With
-//             eight warps a step took twice as long: one warp issues an instruction in four cycles.)
-//   16        issues the products;  17  copies K, Q, V, z and the records.
+// Second kernel: a cluster of two CTAs (one on an SM) holds one head of one sequence, a CTA 64 of its value columns, as two
+// halves of 32 that go their own ways, so that one's products run while the other's operands are made: only the norm
+// needs the whole row, and its sums of squares go to the other CTA by asynchronous stores.  Warps:
+//   0 .. 7, 8 .. 15  a half each: a warp reads the accumulators' 32 lanes (w % 4) and 16 columns; lanes 0..63 are K's or T's
+//                    rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128.
+//                    (With 32 columns to a warp a step took twice as long: one warp issues an instruction in four cycles.)
+//   16, 17           issue a half's products;  18  copies K, Q, V, z and the records.
 // The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
-// B's columns, so B's two parts stand side by side as 2 n columns, one read of A for both.
+// B's columns, so B's two parts stand side by side as 64 columns, one read of A for both.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -78,35 +79,32 @@ FAK_DEV int64_t record_of(const Records& r, const GdnSeq& d, int s, int c) {
   return r.dense ? (int64_t)s * r.length + (c - r.begin) : (int64_t)(d.r0 / kRows) + s + c;
 }
 
-template <int NS>
-struct Cfg {
-  static constexpr int n = kGdnDim / NS;        // value columns of a CTA
-  static constexpr int cols = n / 4;            // of a chain thread
-  static constexpr int panels = (n + 63) / 64;  // of 64 columns, 128 bytes
-  static constexpr int off_kq = 0;                                 // two stages of [K; Q]: two panels of 128 rows
-  static constexpr int off_tp = off_kq + 2 * 32768;                // two stages of [T; P T], two parts
-  static constexpr int off_s = off_tp + 4 * kPart;                 // S, two parts
-  static constexpr int off_u = off_s + 2 * panels * 16384;         // R, then U, two parts
-  static constexpr int off_v = off_u + 2 * panels * 8192;          // two stages of V: panels of 64 columns
-  static constexpr int off_z = off_v + 2 * panels * 8192;          // z: panels of 32 columns, 128 bytes
-  static constexpr int off_dec = off_z + kRows * n * 4;
-  static constexpr int off_sum = off_dec + 2 * (int)sizeof(Decays);  // sums of squares [2][NS * 4][64]
-  static constexpr int off_gain = off_sum + 2 * NS * 4 * kRows * 4;
-  static constexpr int off_max = off_gain + n * 4;  // [8]
-  static constexpr int off_bar = off_max + 64;
-  static constexpr int smem = off_bar + 192 + 1024;
-  static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
-  static constexpr int d1 = 0, d2 = 2 * n, d3 = 4 * n;  // TMEM columns
-  static constexpr int tmem_cols = 512;
-  static_assert(6 * n <= tmem_cols, "TMEM");
-};
+constexpr int kSlices = 2;                // CTAs of a head
+constexpr int kCols = kGdnDim / kSlices;  // value columns of a CTA
+constexpr int kHalf = kCols / 2;          // of a half
+constexpr int W = kHalf / 2;              // of a thread
+constexpr int kOffKq = 0;                                   // two stages of [K; Q]: two panels of 128 rows
+constexpr int kOffTpt = kOffKq + 2 * 32768;                 // two stages of [T; P T], two parts
+constexpr int kOffS = kOffTpt + 4 * kPart;                  // S of each half: 128 rows of 32 columns' first parts, then second
+constexpr int kOffU = kOffS + 2 * 16384;                    // R, then U, of each half: 64 rows
+constexpr int kOffV = kOffU + 2 * 8192;                     // two stages of V
+constexpr int kOffZ = kOffV + 2 * 8192;                     // z: panels of 32 columns, 128 bytes
+constexpr int kOffDec = kOffZ + kRows * kCols * 4;
+constexpr int kOffSum = kOffDec + 2 * (int)sizeof(Decays);  // sums of squares [2][kSlices * 4][64]
+constexpr int kOffGain = kOffSum + 2 * kSlices * 4 * kRows * 4;
+constexpr int kOffMax = kOffGain + kCols * 4;               // of each half [8]
+constexpr int kOffBar = kOffMax + 64;
+constexpr int kChunkSmem = kOffBar + 192 + 1024;
+static_assert(kChunkSmem <= 232448, "shared memory exceeds the 227 KB per-block limit");
+constexpr int kAccD1 = 0, kAccD2 = 64, kAccD3 = 128, kAccHalf = 192;  // TMEM columns
+constexpr int kTmemCols = 512;
 
-enum Bars { kLand0, kLand1, kD1, kD2, kD3, kReady0, kReady1, kZ, kZFree, kSum0, kSum1, kDrain, kBars };
+enum Bars { kLand0, kLand1, kReady0, kReady1, kD1, kD2 = kD1 + 2, kD3 = kD2 + 2, kZ = kD3 + 2, kZFree, kSum0, kSum1, kDrain, kBars = kDrain + 2 };
 
-// Named barriers, for waits where a polling warp would take issue slots from those that work (a try of an mbarrier gives
-// up after some 60 cycles; with all waits so, half of all instructions were of such loops).  The products' warp polls, and
-// lets the others go.
-enum Named { kBarMax = 1, kBarTurn, kBarS, kBarR, kBarU, kBarD1Top, kBarD1Low, kBarD2Top, kBarD2Low, kBarD3 };
+// Named barriers of the first half (the second's are kNamed further on), for waits where a polling warp would take issue slots
+// from those that work (a try of an mbarrier gives up after some 60 cycles; with all waits so, half of all instructions were
+// of such loops).  The products' warp polls, and lets the others go.
+enum Named { kBarTurn = 1, kBarS, kBarR, kBarU, kBarD1, kBarD2, kBarD3, kNamed = 7 };
 
 template <int M, int N, bool A_MN, bool B_MN>
 constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
@@ -128,6 +126,9 @@ FAK_DEV uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
 
 FAK_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+FAK_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 FAK_DEV uint32_t rank_in_cluster() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -213,6 +214,20 @@ FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int c
   }
 }
 
+// The same for a tile of 32 columns, whose second parts stand behind the first in a row of 128 bytes.
+template <int N>
+FAK_DEV void put_sides(unsigned char* tile, int row, int col, const float2 (&x)[N / 2]) {
+  uint32_t hi[N / 2], lo[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) split_half(x[i].x, x[i].y, hi[i], lo[i]);
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    const int at = row * 128 + ((((col + i) >> 3) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(tile + at) = make_uint4(hi[i / 2], hi[i / 2 + 1], hi[i / 2 + 2], hi[i / 2 + 3]);
+    *reinterpret_cast<uint4*>(tile + (at ^ 64)) = make_uint4(lo[i / 2], lo[i / 2 + 1], lo[i / 2 + 2], lo[i / 2 + 3]);
+  }
+}
+
 // The sums of two columns each, `apart` columns apart.
 template <int N>
 FAK_DEV void ld_sums(uint32_t addr, int apart, float2 (&x)[N / 2]) {
@@ -291,20 +306,18 @@ struct ChunkDebug {
   int unreachable;  // a test's: 1 where K and Q are never to count as landed
 };
 
-template <int NS>
-__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p, const __grid_constant__ ChunkMaps maps, Records records,
+__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p,
+                                                                 const __grid_constant__ ChunkMaps maps, Records records,
                                                                  ChunkDebug dbg, int* status) {
-  using C = Cfg<NS>;
-  constexpr int n = C::n, W = C::cols;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::off_bar);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 8 * kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::off_bar + 8 * kBars + 4);
-  float* gain = reinterpret_cast<float*>(smem + C::off_gain);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 8 * kBars + 4);
+  float* gain = reinterpret_cast<float*>(smem + kOffGain);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int slice = blockIdx.x % NS, unit = blockIdx.x / NS;
+  const int slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
   const int s = unit / p.nv, h = unit - s * p.nv;
   const KvSeq seq = kv_seq(p.c, s);
   const GdnSeq d = gdn_seq(p.c, seq, s);
@@ -314,14 +327,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   }
   const int rows = d.r1 - d.first;
   if (p.few && rows <= p.few) return;  // the steps' kernel's
-  const int col0 = slice * n;
+  const int col0 = slice * kCols;
   const int begin = records.begin, end = min((rows + kRows - 1) / kRows, begin + records.length);  // this launch's chunks
   if (begin == 0)
-    for (int i = threadIdx.x; i < (d.first - d.r0) * (n / 4); i += kThreads) {
-      const int row = d.r0 + i / (n / 4);
-      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (n / 4)), gdn_zero4());
+    for (int i = threadIdx.x; i < (d.first - d.r0) * (kCols / 4); i += kThreads) {
+      const int row = d.r0 + i / (kCols / 4);
+      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (kCols / 4)), gdn_zero4());
     }
-  const int chunks = end - begin;  // counted from 0 below; chunk c's rows are first + 64 c ..
+  const int chunks = end - begin;  // counted from 0 below
   if (chunks <= 0) return;
   const int first_row = d.first + begin * kRows, rows_left = rows - begin * kRows;
 
@@ -330,24 +343,24 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : 1);
     fence_mbar_init();
   }
-  if (threadIdx.x < 8) reinterpret_cast<unsigned*>(smem + C::off_max)[threadIdx.x] = 0;
-  if (threadIdx.x < n) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
+  if (threadIdx.x < 16) reinterpret_cast<unsigned*>(smem + kOffMax)[threadIdx.x] = 0;
+  if (threadIdx.x < kCols) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
   if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(C::tmem_cols)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_async();
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
   // One that runs out is recorded, and no wait of the block waits after it: every warp goes through its chunks, without
   // results, so that the named barriers stay in step (nothing but such waits lies between two of them).
   auto wait = [&](int b, int phase) {
-    bool done = *abort != 0;
+    bool done = mbar_try_wait(&bar[b], phase & 1) || *abort != 0;
     for (int i = 0; i < 512 && !done; ++i) done = mbar_try_wait(&bar[b], phase & 1);
     if (!done && !mbar_wait_bounded(&bar[b], phase & 1, abort, dbg.timeout_ns)) {
       if (!*abort) atomicCAS(status, 0, FAK_ERR_TIMEOUT);
@@ -361,12 +374,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     wait(b, phase);
   };
   // What the warp wrote to shared memory and read from TMEM comes before what waits on the barrier, MMAs too.
-  auto arrive = [&](int b) {
-    fence_async();
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[b]);
-  };
   auto give = [&](int named, int threads) {
     fence_async();
     tc_fence_before_sync();
@@ -376,18 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     named_bar_sync(named, threads + 32);
     tc_fence_after_sync();
   };
-  auto decays = [&](int c) { return reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1); };
 
   if (warp < 16) {
-    // ------------------------------------------------------------------ the chain
-    const int quarter = warp & 3, group = warp >> 2;
-    const int col = group * W;                       // of the CTA's columns
-    const uint32_t acc = tmem + ((uint32_t)quarter << 21) + col;  // TMEM: lane 32 quarter
-    const int key = 32 * quarter + lane;             // the row of S
-    const bool top = quarter < 2;                    // K's and T's rows, else Q's and P T's
-    const int t = 32 * (quarter & 1) + lane;         // the row of the chunk
-    float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + col;
-    unsigned* most = reinterpret_cast<unsigned*>(smem + C::off_max);  // [4] of S, [4] of V: largest magnitudes, by chunk
+    // ------------------------------------------------------------------ a half's chain
+    const int half = warp >> 3, named = half * kNamed;
+    const int quarter = warp & 3, col = ((warp >> 2) & 1) * W;  // of the half's columns
+    const uint32_t acc = tmem + ((uint32_t)quarter << 21) + half * kAccHalf + col;  // TMEM: lane 32 quarter
+    const int key = 32 * quarter + lane;      // the row of S
+    const bool top = quarter < 2;             // K's and T's rows, else Q's and P T's
+    const int t = 32 * (quarter & 1) + lane;  // the row of the chunk
+    unsigned char *ss = smem + kOffS + half * 16384, *us = smem + kOffU + half * 8192;
+    float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + half * kHalf + col;
+    unsigned* most = reinterpret_cast<unsigned*>(smem + kOffMax) + 8 * half;  // [4] of S, [4] of V: largest magnitudes, by chunk
     float2 S[W / 2];
 #pragma unroll
     for (int i = 0; i < W / 2; i += 2) {
@@ -398,18 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     uint32_t v[W / 2];  // of the next chunk
     auto fetch_v = [&](int c) {
       wait(kReady0 + (c & 1), c >> 1);
-      const unsigned char* src = smem + C::off_v + (c & 1) * C::panels * 8192 + (col >> 6) * 8192 + t * 128;
+      const unsigned char* src = smem + kOffV + (c & 1) * 8192 + t * 128;
       const bool there = c * kRows + t < rows_left;  // (what stands behind the last row is another's, whatever it holds)
 #pragma unroll
       for (int i = 0; i < W / 8; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + (((((col & 63) >> 3) + i) ^ (t & 7)) << 4));
+        const uint4 x = *reinterpret_cast<const uint4*>(src + ((((half * kHalf + col) >> 3) + i) ^ (t & 7)) * 16);
         v[4 * i] = there ? x.x : 0;
         v[4 * i + 1] = there ? x.y : 0;
         v[4 * i + 2] = there ? x.z : 0;
         v[4 * i + 3] = there ? x.w : 0;
       }
     };
-    auto tell = [&](int at, float m) {  // a warp's largest magnitude to the block's
+    auto tell = [&](int at, float m) {  // a warp's largest magnitude to the half's
       const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
       if (lane == 0) atomicMax(&most[at], u);
     };
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     // before, whose magnitudes every warp has told by now.
     auto put_state = [&](int c) {
       const int b = max(c - 1, 0);
-      const float m = fmaxf(__uint_as_float(most[b & 3]), __uint_as_float(max(most[4 + (b & 3)], most[4 + (c & 3)])));
+      const float m = __uint_as_float(max(most[b & 3], max(most[4 + (b & 3)], most[4 + (c & 3)])));
       // m = 2^e 1.f goes to 2^-2 1.f (zeros and infinities: as they are); the inverse is a normal number too
       const int e = (int)(__float_as_uint(m) >> 23);
       const int by = e == 0 || e == 255 ? 0 : min(max(125 - e, -120), 120);
@@ -442,204 +449,210 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       float2 x[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) x[i] = mul2(S[i], both(up));
-      put_halves<W>(smem + C::off_s, 16384, C::panels * 16384, key, col, x);
+      put_sides<W>(ss, key, col, x);
     };
-    const uint32_t sum_to = smem_u32(smem + C::off_sum);
-    const int me = NS > 1 ? (int)rank_in_cluster() : 0;
+    const uint32_t sum_to = smem_u32(smem + kOffSum);
+    const int me = (int)rank_in_cluster();
     tell_state(0);
     if (top) {
       fetch_v(0);
       tell_values(0);
     }
-    named_bar_sync(kBarMax, kChainThreads);
+    named_bar_sync(named + kBarTurn, 256);
     put_state(0);
-    give(kBarS, kChainThreads);
-    // The output of chunk c, whose rows stand in o: its norm, gate and stores come while the next chunk's products run, so
-    // that the state does not wait for them.
+    give(named + kBarS, 256);
+
+    // The output of a chunk, whose rows stand in o, is finished while the next chunk's products run, so that the state does
+    // not wait for it: its norm and gate between the next chunk's first two products, its stores between the last two.  The
+    // rows turn in S's place, which the first product is done with, so that stores are whole lines: a thread's own row would
+    // be a line for every lane (3,000 cycles a chunk).
     float2 o[W / 2];
     auto finish = [&](int c) {
       float r = 1.0f;
       if (p.norm_w) {
         wait(kSum0 + (c & 1), c >> 1);
-        if constexpr (NS > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
-        const float* sums = reinterpret_cast<const float*>(smem + C::off_sum) + (c & 1) * NS * 4 * kRows + t;
+        try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
+        const float* sums = reinterpret_cast<const float*>(smem + kOffSum) + (c & 1) * kSlices * 4 * kRows + t;
         float y = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4 * NS; ++i) y += sums[i * kRows];
+        for (int i = 0; i < 4 * kSlices; ++i) y += sums[i * kRows];
         r = rsqrtf(fmaf(y, 1.0f / kGdnDim, p.eps));
       }
 #pragma unroll
       for (int i = 0; i < W / 2; i += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(gain + col + 2 * i);
+        const float4 w = *reinterpret_cast<const float4*>(gain + half * kHalf + col + 2 * i);
         o[i] = mul2(o[i], mul2(make_float2(w.x, w.y), both(r)));
         o[i + 1] = mul2(o[i + 1], mul2(make_float2(w.z, w.w), both(r)));
       }
       if (p.z) {
         wait(kZ, c);
-        const unsigned char* zs = smem + C::off_z + (col >> 5) * kRows * 128 + t * 128;
+        const unsigned char* zs = smem + kOffZ + half * kRows * 128 + t * 128;
 #pragma unroll
         for (int i = 0; i < W / 2; i += 2) {
-          const float4 z = *reinterpret_cast<const float4*>(zs + (((((col & 31) >> 2) + i / 2) ^ (t & 7)) << 4));
+          const float4 z = *reinterpret_cast<const float4*>(zs + ((((col >> 2) + i / 2) ^ (t & 7)) << 4));
           o[i] = mul2(o[i], make_float2(gdn_silu(z.x), gdn_silu(z.y)));
           o[i + 1] = mul2(o[i + 1], make_float2(gdn_silu(z.z), gdn_silu(z.w)));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[kZFree]);
       }
-      // The rows turn in S's place, which the chunk's first product is done with, so that stores are whole lines: a thread's
-      // own row would be a line for every lane (3,000 cycles a chunk).
-      unsigned char* turn = smem + C::off_s;
-      const int have = min(kRows, rows_left - c * kRows), i0 = (warp >> 2) * 64 + (warp & 1) * 32 + lane;  // of 256
-      const int64_t to = (int64_t)(first_row + c * kRows) * p.out_row + h * p.out_head + col0;
       if (p.out_bf16) {
-        constexpr int line = n / 8;  // pieces of a row
 #pragma unroll
         for (int i = 0; i < W / 2; i += 4)
-          *reinterpret_cast<uint4*>(turn + t * n * 2 + ((((col + 2 * i) >> 3) ^ (t & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(ss + t * 64 + ((((col + 2 * i) >> 3) ^ ((t >> 1) & 3)) << 4)) =
               make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
                          pack_bf16(o[i + 3].x, o[i + 3].y));
-        named_bar_sync(kBarTurn, kChainThreads / 2);
-#pragma unroll
-        for (int i = 0; i < kRows * line / 256; ++i) {
-          const int at = i * 256 + i0, row = at / line, pc = at % line;
-          if (row < have && !*abort)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
-                *reinterpret_cast<const uint4*>(turn + row * n * 2 + ((pc ^ (row & 7)) << 4));
-        }
       } else {
-        constexpr int line = n / 4;
 #pragma unroll
         for (int i = 0; i < W / 2; i += 2)
-          *reinterpret_cast<float4*>(turn + t * n * 4 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
+          *reinterpret_cast<float4*>(ss + t * 128 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
               make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
-        named_bar_sync(kBarTurn, kChainThreads / 2);
+      }
+    };
+    auto store = [&](int c) {
+      named_bar_sync(named + kBarTurn, 128);
+      const int have = *abort ? 0 : min(kRows, rows_left - c * kRows), i0 = ((warp >> 2) & 1) * 64 + t;  // of 128
+      const int64_t to = (int64_t)(first_row + c * kRows) * p.out_row + h * p.out_head + col0 + half * kHalf;
+      if (p.out_bf16) {
 #pragma unroll
-        for (int i = 0; i < kRows * line / 256; ++i) {
-          const int at = i * 256 + i0, row = at / line, pc = at % line;
-          if (row < have && !*abort)
+        for (int i = 0; i < 2; ++i) {
+          const int at = i * 128 + i0, row = at >> 2, pc = at & 3;
+          if (row < have)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
+                *reinterpret_cast<const uint4*>(ss + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = i * 128 + i0, row = at >> 3, pc = at & 7;
+          if (row < have)
             *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + row * p.out_row + 4 * pc) =
-                *reinterpret_cast<const float4*>(turn + row * n * 4 + ((pc ^ (row & 7)) << 4));
+                *reinterpret_cast<const float4*>(ss + row * 128 + ((pc ^ (row & 7)) << 4));
         }
       }
     };
     for (int c = 0; c < chunks; ++c) {
-      const Decays* dec = decays(c);
+      const Decays* dec = reinterpret_cast<const Decays*>(smem + kOffDec) + (c & 1);
       float2 x[W / 2];
       float all;
       if (top) {
-        take(kBarD1Top, kChainThreads / 2);
+        take(named + kBarD1, 128);
         const float keep = dec->keep[t], left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
         all = dec->keep[kRows - 1];
-        ld_sums<W>(acc + C::d1, n, x);
+        ld_sums<W>(acc + kAccD1, kHalf, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) x[i] = fma2(both(bk), x[i], mul2(bf16_pair(v[i]), both(bu)));
-        put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
-        give(kBarR, kChainThreads / 2);
+        put_sides<W>(us, t, col, x);
+        give(named + kBarR, 128);
         if (c + 1 < chunks) {
           fetch_v(c + 1);
           tell_values(c + 1);
         }
-        take(kBarD2Top, kChainThreads / 2);
-        ld_sums<W>(acc + C::d2, n, x);
+        take(named + kBarD2, 128);
+        ld_sums<W>(acc + kAccD2, kHalf, x);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) x[i] = mul2(x[i], both(left));
-        put_halves<W>(smem + C::off_u, 8192, C::panels * 8192, t, col, x);
-        give(kBarU, kChainThreads / 2);
+        put_sides<W>(us, t, col, x);
+        give(named + kBarU, 128);
       } else {
-        take(kBarD1Low, kChainThreads / 2);
+        wait(kD1 + half, c);
+        tc_fence_after_sync();
         const float keep = dec->keep[t], by = down * p.scale;
         all = dec->keep[kRows - 1];
         float2 y[W / 2];
-        ld_sums<W>(acc + C::d1, n, y);
+        ld_sums<W>(acc + kAccD1, kHalf, y);
         if (c > 0) finish(c - 1);
-        take(kBarD2Low, kChainThreads / 2);
-        ld_sums<W>(acc + C::d2, n, x);
-        float2 ss = both(0.0f);
+        wait(kD2 + half, c);
+        tc_fence_after_sync();
+        ld_sums<W>(acc + kAccD2, kHalf, x);
+        float2 sq = both(0.0f);
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
           o[i] = mul2(fma2(both(keep), y[i], x[i]), both(by));
-          ss = fma2(o[i], o[i], ss);
+          sq = fma2(o[i], o[i], sq);
         }
         if (p.norm_w && !*abort) {
           // the row's sum of squares goes to all of the cluster
-          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], NS * 4 * kRows * 4);
-          const uint32_t at = sum_to + (((c & 1) * NS * 4 + me * 4 + group) * kRows + t) * 4;
+          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], kSlices * 4 * kRows * 4);
+          const uint32_t at = sum_to + (((c & 1) * kSlices * 4 + me * 4 + (warp >> 2)) * kRows + t) * 4;
 #pragma unroll
-          for (int i = 0; i < NS; ++i) st_async(map_rank(at, i), ss.x + ss.y, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
+          for (int i = 0; i < kSlices; ++i) st_async(map_rank(at, i), sq.x + sq.y, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
         }
+        if (c > 0) store(c - 1);
       }
-      take(kBarD3, kChainThreads);
-      ld_sums<W>(acc + C::d3, n, x);
+      take(named + kBarD3, 256);
+      ld_sums<W>(acc + kAccD3, kHalf, x);
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) S[i] = fma2(both(all), S[i], mul2(x[i], both(down)));
       if (c + 1 < chunks) {
         put_state(c + 1);
-        give(kBarS, kChainThreads);
+        give(named + kBarS, 256);
         tell_state(c + 1);
-        if (threadIdx.x == 0) most[(c + 3) & 3] = most[4 + ((c + 3) & 3)] = 0;  // (the chunk before this one's: read by all)
+        if ((threadIdx.x & 255) == 0) most[(c + 3) & 3] = most[4 + ((c + 3) & 3)] = 0;  // (the chunk before this one's: read by all)
       }
     }
-    if (!top) finish(chunks - 1);
+    if (!top) {
+      finish(chunks - 1);
+      store(chunks - 1);
+    }
     if (!*abort) {
 #pragma unroll
       for (int i = 0; i < W / 2; i += 2) *reinterpret_cast<float4*>(st + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
     }
-  } else if (warp == 16) {
-    // ------------------------------------------------------------------ the products
-    const uint32_t kq = smem_u32(smem + C::off_kq), tp = smem_u32(smem + C::off_tp), ss = smem_u32(smem + C::off_s),
-                   us = smem_u32(smem + C::off_u);
+  } else if (warp < 18) {
+    // ------------------------------------------------------------------ a half's products
+    const int half = warp - 16, named = half * kNamed;
+    const uint32_t kq = smem_u32(smem + kOffKq), tp = smem_u32(smem + kOffTpt), acc = tmem + half * kAccHalf;
+    const uint64_t ss = desc_mn(smem_u32(smem + kOffS + half * 16384), 0), us = desc_mn(smem_u32(smem + kOffU + half * 8192), 0);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t kqc = kq + (c & 1) * 32768, tpc = tp + (c & 1) * 2 * kPart;
       wait(kReady0 + (c & 1), c >> 1);
-      take(kBarS, kChainThreads);
+      take(named + kBarS, 256);
       if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(kqc), b = desc_mn(ss, 16384);
+        const uint64_t a = umma_desc_sw128(kqc);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_f16(tmem + C::d1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
-        umma_commit(&bar[kD1]);
+          mma_f16(acc + kAccD1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, ss + k * (2048 >> 4), kIdesc<128, 64, false, true>, k > 0);
+        umma_commit(&bar[kD1 + half]);
       }
       __syncwarp();
-      wait(kD1, c);
-      give(kBarD1Top, kChainThreads / 2);
-      give(kBarD1Low, kChainThreads / 2);
-      take(kBarR, kChainThreads / 2);
+      wait(kD1 + half, c);
+      give(named + kBarD1, 128);
+      take(named + kBarR, 128);
       if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(tpc), b = desc_mn(us, 8192);
+        const uint64_t a = umma_desc_sw128(tpc);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_f16(tmem + C::d2, a + 2 * k, b + k * (2048 >> 4), kIdesc<128, 2 * n, false, true>, k > 0);
-          mma_f16(tmem + C::d2, a + (kPart >> 4) + 2 * k, b + k * (2048 >> 4), kIdesc<128, n, false, true>, 1);
+          mma_f16(acc + kAccD2, a + 2 * k, us + k * (2048 >> 4), kIdesc<128, 64, false, true>, k > 0);
+          mma_f16(acc + kAccD2, a + (kPart >> 4) + 2 * k, us + k * (2048 >> 4), kIdesc<128, 64, false, true>, 1);
         }
-        umma_commit(&bar[kD2]);
+        umma_commit(&bar[kD2 + half]);
       }
       __syncwarp();
-      wait(kD2, c);
-      give(kBarD2Top, kChainThreads / 2);
-      give(kBarD2Low, kChainThreads / 2);
-      take(kBarU, kChainThreads / 2);
+      wait(kD2 + half, c);
+      give(named + kBarD2, 128);
+      take(named + kBarU, 128);
       if (elect_one()) {
-        const uint64_t a = desc_mn(kqc, 16384), b = desc_mn(us, 8192);
+        const uint64_t a = desc_mn(kqc, 16384);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f16(tmem + C::d3, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc<128, 2 * n, true, true>, k > 0);
-        umma_commit(&bar[kD3]);
+        for (int k = 0; k < 4; ++k) mma_f16(acc + kAccD3, a + k * (2048 >> 4), us + k * (2048 >> 4), kIdesc<128, 64, true, true>, k > 0);
+        umma_commit(&bar[kD3 + half]);
       }
       __syncwarp();
-      wait(kD3, c);
-      give(kBarD3, kChainThreads);
+      wait(kD3 + half, c);
+      give(named + kBarD3, 256);
     }
-    if (*abort) {  // what was issued is done with before the TMEM goes
+    if (__any_sync(0xffffffffu, *abort != 0)) {  // what was issued is done with before the TMEM goes
       if (elect_one()) {
-        umma_commit(&bar[kDrain]);
+        umma_commit(&bar[kDrain + half]);
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_suspend(&bar[kDrain], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
+        while (!mbar_try_wait_suspend(&bar[kDrain + half], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
         }
       }
       __syncwarp();
     }
-  } else if (warp == 17) {
-    // ------------------------------------------------------------------ K, Q and z
+  } else if (warp == 18) {
+    // ------------------------------------------------------------------ K, Q, V, z and the records
     // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
     // and those that were are waited for before the block ends.
     const int hk = h / p.group;
@@ -650,20 +663,21 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       if (c >= 1) doze(kZFree, c - 1);
       if (dead()) return;
       gates = c + 1;
-      unsigned char* zs = smem + C::off_z;
+      unsigned char* zs = smem + kOffZ;
       const int first = c * kRows, have = min(kRows, rows_left - first);
       if (p.z_wide) {
         if (elect_one()) {
-          mbar_arrive_expect_tx(&bar[kZ], kRows * n * 4);
+          mbar_arrive_expect_tx(&bar[kZ], kRows * kCols * 4);
 #pragma unroll
-          for (int i = 0; i < n / 32; ++i) tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, first_row + first, &bar[kZ]);
+          for (int i = 0; i < kCols / 32; ++i)
+            tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, first_row + first, &bar[kZ]);
         }
         __syncwarp();
       } else {
         const float* z0 = p.z + (first_row + first) * p.z_row + h * p.z_head + col0;
 #pragma unroll 8
-        for (int u = 0; u < kRows * n / 32; ++u) {
-          const int at = u * 32 + lane, x = at / n, cl = at % n;
+        for (int u = 0; u < kRows * kCols / 32; ++u) {
+          const int at = u * 32 + lane, x = at / kCols, cl = at % kCols;
           if (x < have)
             *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
                 z0[x * p.z_row + cl];
@@ -673,26 +687,27 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       }
     };
     for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) doze(kD3, c - 2);
+      if (c >= 2) {
+        doze(kD3, c - 2);
+        doze(kD3 + 1, c - 2);
+      }
       if (dead()) break;
       copied = c + 1;
       const int first = c * kRows, have = min(kRows, rows_left - first);
-      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
+      unsigned char* to = smem + kOffKq + (c & 1) * 32768;
       if (elect_one()) {
         uint64_t* land = &bar[kLand0 + (c & 1)];
-        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * n * 2);
+        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * kCols * 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, first_row + first, land);
           tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, first_row + first, land);
         }
         // (V of two chunks before is in registers since that chunk's state was made)
-#pragma unroll
-        for (int i = 0; i < C::panels; ++i)
-          tma_load_3d_tx(smem + C::off_v + ((c & 1) * C::panels + i) * 8192, &maps.v, col0 + 64 * i, h, first_row + first, land);
+        tma_load_3d_tx(smem + kOffV + (c & 1) * 8192, &maps.v, col0, h, first_row + first, land);
         const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
-        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
-        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
+        bulk_g2s_nohint(smem + kOffTpt + (c & 1) * 2 * kPart, record, 2 * kPart, land);
+        bulk_g2s_nohint(smem + kOffDec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
       }
       __syncwarp();
       doze(kLand0 + (c & 1), c >> 1);
@@ -701,7 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
           const int row = have + (i >> 5), at = i & 31;
           *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
-      if (!dbg.unreachable) arrive(kReady0 + (c & 1));
+      if (!dbg.unreachable) {
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kReady0 + (c & 1)]);
+      }
       if (c > 0) load_z(c - 1);  // (wanted when the next chunk is on its way)
     }
     load_z(chunks - 1);
@@ -711,17 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
         while (!mbar_try_wait_suspend(&bar[b], phase & 1, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
         }
       };
-      for (int c = max(0, copied - 2); c < copied; ++c) {
-        drain(kLand0 + (c & 1), c >> 1);
-      }
+      for (int c = max(0, copied - 2); c < copied; ++c) drain(kLand0 + (c & 1), c >> 1);
       if (gates && p.z_wide) drain(kZ, gates - 1);
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  // (no CTA leaves while another may still store into it)
-  if constexpr (NS > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (NS > 1 && *abort) {  // (and a store that nothing waited for lands within a microsecond)
+  cluster_sync();  // (no CTA leaves while another may still store into it)
+  if (*abort) {    // (and a store that nothing waited for lands within a microsecond)
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 50000) {
     }
@@ -729,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   }
   if (warp == 16) {
     tc_fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::tmem_cols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -1075,24 +1091,23 @@ bool rows_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int6
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NS>
 cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const Records& records, const ChunkDebug& dbg, int* status, int dev,
                    cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = kv_smem_limit(gdn_chunk_kernel<NS>, Cfg<NS>::smem, dev, done);
+  cudaError_t e = kv_smem_limit(gdn_chunk_kernel, kChunkSmem, dev, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * NS));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * kSlices));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<NS>::smem;
+  cfg.dynamicSmemBytes = kChunkSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = NS;
+  at[0].val.clusterDim.x = kSlices;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NS>, p, maps, records, dbg, status);
+  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel, p, maps, records, dbg, status);
 }
 
 constexpr int64_t kScratch = 1LL << 30;  // most bytes of records at a time; more chunks than they hold go in several launches
@@ -1131,7 +1146,7 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
     const int64_t slots = records.dense ? (int64_t)p.c.n_seqs * records.length : p.c.rows / kRows + p.c.n_seqs;
     gdn_prepare_kernel<<<dim3((unsigned)slots, (unsigned)nk), kPrepThreads, kPrepSmem, s>>>(p, records);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch<2>(p, maps, records, dbg, status, dev, s);
+    if (e == cudaSuccess) e = launch(p, maps, records, dbg, status, dev, s);
   }
   const cudaError_t f = cudaFreeAsync(scratch, s);
   return e != cudaSuccess ? e : f;
