@@ -399,6 +399,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   p.z_wide = !(((uintptr_t)a->z & 15) | ((p.z_row | p.z_head) & 3)) && fits(p.z_row, a->rows, 4) && fits(p.z_head, a->nv, 4);
   p.state = a->state;
   p.out = a->out;
+  p.out_wide = fits(p.out_row, a->rows, 4) && fits(p.out_head, a->nv, 4);
   p.scale = a->scale;
   p.eps = a->eps;
   p.nv = a->nv;

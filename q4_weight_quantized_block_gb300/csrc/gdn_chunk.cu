@@ -10,27 +10,25 @@
 // goes through a sequence's chunks.
 //
 // Precision.  The state is held in f32 registers, and its products keep 22 bits: the f32 operand goes as the sum of two
-// f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents
-// take them because a chunk's S, R and U are scaled by one power of two.  With m the largest of |S| and |V|, lengths of k
-// of at most 1 and 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m of
-// the chunk before (its own would hold all warps up at a barrier), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what
-// f16 drops is below 2^-25, so 2^-23 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and
-// kept as two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
+// f16, the other one is f16 already (q, k) or two f16 too (T; the small parts' product is left out).  (Where the output is
+// bf16, what only it takes goes by its first part alone, off by 2^-12.)  f16's exponents take them because a value column's
+// S, R and U are scaled by one power of two.  With m the largest of the column's |S| and |V|, lengths of k of at most 1 and
+// 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m of the chunk before (by
+// which time it is known), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what f16 drops is below 2^-25, so 2^-23 m.  T
+// and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and kept as two f32, so that
+// decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
 //
 // First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps: decays into A
 // and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T, in place of A and P, by m16n8k16
-// instructions.  (Made by four more warps of the second kernel, a chunk ahead, the same work took longer than a chunk's
-// products, and once for each CTA of a head.)
+// instructions.
 //
-// Second kernel: a cluster of two CTAs (one on an SM) holds one head of one sequence, a CTA 64 of its value columns, as two
-// halves of 32 that go their own ways, so that one's products run while the other's operands are made: only the norm
-// needs the whole row, and its sums of squares go to the other CTA by asynchronous stores.  Warps:
-//   0 .. 7, 8 .. 15  a half each: a warp reads the accumulators' 32 lanes (w % 4) and 16 columns; lanes 0..63 are K's or T's
-//                    rows (R, then U, to shared memory as f16), 64..127 Q's or P T's (the output); S's rows in all 128.
-//                    (With 32 columns to a warp a step took twice as long: one warp issues an instruction in four cycles.)
-//   16, 17           issue a half's products;  18  copies K, Q, V, z and the records.
-// The products read their operands from shared memory at 128 bytes a cycle: a step of 16 takes 128 rows of A (4 KB) and
-// B's columns, so B's two parts stand side by side as 64 columns, one read of A for both.
+// Second kernel: a warp holds 16 value columns of one head of one sequence, as S^T in the accumulators of m16n8k16 (64
+// registers a thread).  Those are laid out as the next product's first operand is, so that S^T, R^T and U^T go from product
+// to product in registers: S^T K^T, S^T Q^T, R^T T^T, R^T (P T)^T, U^T K.  No warp waits for another but through the copies
+// of K, Q, V, z and the records, which one more warp makes, and for the norm's sums of squares, a chunk later.  400
+// instructions of 8 cycles each a chunk and warp: 3,200 cycles, at one warp to a scheduler.
+// (The same products by tcgen05, 64 columns to a CTA, took 6,200 cycles a chunk: 128 rows of S, R or U go through shared
+// memory for each of three products that wait for one another, some 700 cycles for a product and as many for its operand.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,8 +51,6 @@
 namespace {
 
 constexpr int kRows = 64;  // of a chunk
-constexpr int kChainThreads = 512;
-constexpr int kThreads = kChainThreads + 128;
 constexpr int kPrepThreads = 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
 constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
@@ -79,50 +75,25 @@ FAK_DEV int64_t record_of(const Records& r, const GdnSeq& d, int s, int c) {
   return r.dense ? (int64_t)s * r.length + (c - r.begin) : (int64_t)(d.r0 / kRows) + s + c;
 }
 
-constexpr int kSlices = 2;                // CTAs of a head
-constexpr int kCols = kGdnDim / kSlices;  // value columns of a CTA
-constexpr int kHalf = kCols / 2;          // of a half
-constexpr int W = kHalf / 2;              // of a thread
-constexpr int kOffKq = 0;                                   // two stages of [K; Q]: two panels of 128 rows
-constexpr int kOffTpt = kOffKq + 2 * 32768;                 // two stages of [T; P T], two parts
-constexpr int kOffS = kOffTpt + 4 * kPart;                  // S of each half: 128 rows of 32 columns' first parts, then second
-constexpr int kOffU = kOffS + 2 * 16384;                    // R, then U, of each half: 64 rows
-constexpr int kOffV = kOffU + 2 * 8192;                     // two stages of V
-constexpr int kOffZ = kOffV + 2 * 8192;                     // z: panels of 32 columns, 128 bytes
-constexpr int kOffDec = kOffZ + kRows * kCols * 4;
-constexpr int kOffSum = kOffDec + 2 * (int)sizeof(Decays);  // sums of squares [2][kSlices * 4][64]
-constexpr int kOffGain = kOffSum + 2 * kSlices * 4 * kRows * 4;
-constexpr int kOffMax = kOffGain + kCols * 4;               // of each half [8]
-constexpr int kOffBar = kOffMax + 64;
-constexpr int kChunkSmem = kOffBar + 192 + 1024;
-static_assert(kChunkSmem <= 232448, "shared memory exceeds the 227 KB per-block limit");
-constexpr int kAccD1 = 0, kAccD2 = 64, kAccD3 = 128, kAccHalf = 192;  // TMEM columns
-constexpr int kTmemCols = 512;
+// Of the second kernel: NW warps, 16 columns each, and the copies'.
+template <int NW>
+struct Cfg {
+  static constexpr int cols = 16 * NW;                              // value columns of a CTA
+  static constexpr int slices = kGdnDim / cols;                     // CTAs of a head
+  static constexpr int threads = 32 * NW + 32;
+  static constexpr int off_kq = 0;                                  // two stages of [K; Q]: two panels of 128 rows
+  static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two parts
+  static constexpr int off_v = off_tp + 4 * kPart;                  // two stages of V: panels of 64 columns, 128 bytes
+  static constexpr int off_z = off_v + 2 * kRows * cols * 2;        // z: panels of 32 columns, 128 bytes
+  static constexpr int off_out = off_z + kRows * cols * 4;          // the output, f32 or bf16: panels of 128 bytes
+  static constexpr int off_dec = off_out + kRows * cols * 4;
+  static constexpr int off_sum = off_dec + 2 * (int)sizeof(Decays);  // sums of squares [2][8][64], then 1 / norms [NW][64]
+  static constexpr int off_bar = off_sum + (2 * 8 + NW) * kRows * 4;
+  static constexpr int smem = off_bar + 128 + 1024;
+  static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
+};
 
-enum Bars { kLand0, kLand1, kReady0, kReady1, kD1, kD2 = kD1 + 2, kD3 = kD2 + 2, kZ = kD3 + 2, kZFree, kSum0, kSum1, kDrain, kBars = kDrain + 2 };
-
-// Named barriers of the first half (the second's are kNamed further on), for waits where a polling warp would take issue slots
-// from those that work (a try of an mbarrier gives up after some 60 cycles; with all waits so, half of all instructions were
-// of such loops).  The products' warp polls, and lets the others go.
-enum Named { kBarTurn = 1, kBarS, kBarR, kBarU, kBarD1, kBarD2, kBarD3, kNamed = 7 };
-
-template <int M, int N, bool A_MN, bool B_MN>
-constexpr uint32_t kIdesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-                            ((uint32_t)(M >> 4) << 24);
-
-FAK_DEV void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-
-// 128-byte swizzle with M or N running: 64 of them by 8 k atoms, the next 64 `lbo` bytes on, the next 8 k 1024 bytes on
-FAK_DEV uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+enum Bars { kLand0, kLand1, kReady0, kReady1, kFree0, kFree1, kZ, kZFree, kSum0, kSum1, kOut, kOutFree, kBars };
 
 FAK_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -214,33 +185,6 @@ FAK_DEV void put_halves(unsigned char* tile, int panel, int part, int row, int c
   }
 }
 
-// The same for a tile of 32 columns, whose second parts stand behind the first in a row of 128 bytes.
-template <int N>
-FAK_DEV void put_sides(unsigned char* tile, int row, int col, const float2 (&x)[N / 2]) {
-  uint32_t hi[N / 2], lo[N / 2];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) split_half(x[i].x, x[i].y, hi[i], lo[i]);
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    const int at = row * 128 + ((((col + i) >> 3) ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(tile + at) = make_uint4(hi[i / 2], hi[i / 2 + 1], hi[i / 2 + 2], hi[i / 2 + 3]);
-    *reinterpret_cast<uint4*>(tile + (at ^ 64)) = make_uint4(lo[i / 2], lo[i / 2 + 1], lo[i / 2 + 2], lo[i / 2 + 3]);
-  }
-}
-
-// The sums of two columns each, `apart` columns apart.
-template <int N>
-FAK_DEV void ld_sums(uint32_t addr, int apart, float2 (&x)[N / 2]) {
-  uint32_t r[N], u[N];
-  tmem_ld_cols<N>(addr, r);
-  tmem_ld_cols<N>(addr + apart, u);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i)
-    x[i] = add2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
-}
-
 // Operands of m16n8k16, both parts, from a tile of rows of 64 f16.  A: rows r0 .. +15, columns c0 .. +15; B: the same rows,
 // columns 8 j .. +7.
 struct FragA {
@@ -270,7 +214,7 @@ FAK_DEV void load_b(FragB& b, uint32_t tile, int r0, int j, int lane) {
                : "memory");
 }
 FAK_DEV void mma16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
@@ -298,7 +242,7 @@ FAK_DEV void put_block(unsigned char* tile, int r0, int j, const float (&c)[4], 
 }
 
 struct ChunkMaps {
-  CUtensorMap k, q, v, z;
+  CUtensorMap k, q, v, z, out;
 };
 
 struct ChunkDebug {
@@ -306,18 +250,50 @@ struct ChunkDebug {
   int unreachable;  // a test's: 1 where K and Q are never to count as landed
 };
 
-__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p,
-                                                                 const __grid_constant__ ChunkMaps maps, Records records,
-                                                                 ChunkDebug dbg, int* status) {
+FAK_DEV void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FAK_DEV void stsm4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+FAK_DEV void mma16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two tiles of accumulators (16 x 8 each) as an operand A of 16 x 16, both parts.
+FAK_DEV void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], const float2 (&x)[2], const float2 (&y)[2]) {
+  split_half(x[0].x, x[0].y, hi[0], lo[0]);
+  split_half(x[1].x, x[1].y, hi[1], lo[1]);
+  split_half(y[0].x, y[0].y, hi[2], lo[2]);
+  split_half(y[1].x, y[1].y, hi[3], lo[3]);
+}
+// A row of 128 bytes' 16-byte piece in a tile of 128-byte swizzle.
+FAK_DEV uint32_t piece(int row, int at) { return row * 128 + ((at ^ (row & 7)) << 4); }
+
+// 2^by for a column whose largest magnitude is m = 2^e 1.f, which goes to 2^-2 1.f (zeros and infinities: as they are)
+FAK_DEV int scale_by(float m) {
+  const int e = (int)(__float_as_uint(m) >> 23);
+  return e == 0 || e == 255 ? 0 : min(max(125 - e, -120), 120);
+}
+FAK_DEV float two_to(int by) { return __uint_as_float((uint32_t)(127 + by) << 23); }
+
+template <int NW, bool F32>
+__global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p,
+                                                                        const __grid_constant__ ChunkMaps maps, Records records,
+                                                                        ChunkDebug dbg, int* status) {
+  using C = Cfg<NW>;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 8 * kBars + 4);
-  float* gain = reinterpret_cast<float*>(smem + kOffGain);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::off_bar);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::off_bar + 8 * kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
+  const int slice = blockIdx.x % C::slices, unit = blockIdx.x / C::slices;
   const int s = unit / p.nv, h = unit - s * p.nv;
   const KvSeq seq = kv_seq(p.c, s);
   const GdnSeq d = gdn_seq(p.c, seq, s);
@@ -327,12 +303,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
   }
   const int rows = d.r1 - d.first;
   if (p.few && rows <= p.few) return;  // the steps' kernel's
-  const int col0 = slice * kCols;
+  const int col0 = slice * C::cols;
   const int begin = records.begin, end = min((rows + kRows - 1) / kRows, begin + records.length);  // this launch's chunks
   if (begin == 0)
-    for (int i = threadIdx.x; i < (d.first - d.r0) * (kCols / 4); i += kThreads) {
-      const int row = d.r0 + i / (kCols / 4);
-      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (kCols / 4)), gdn_zero4());
+    for (int i = threadIdx.x; i < (d.first - d.r0) * (C::cols / 4); i += C::threads) {
+      const int row = d.r0 + i / (C::cols / 4);
+      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (C::cols / 4)), gdn_zero4());
     }
   const int chunks = end - begin;  // counted from 0 below
   if (chunks <= 0) return;
@@ -340,25 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kZFree ? 8 : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kFree0 || i == kFree1 || i == kZFree || i == kOut ? NW : 1);
     fence_mbar_init();
   }
-  if (threadIdx.x < 16) reinterpret_cast<unsigned*>(smem + kOffMax)[threadIdx.x] = 0;
-  if (threadIdx.x < kCols) gain[threadIdx.x] = p.norm_w ? p.norm_w[col0 + threadIdx.x] : 1.0f;
-  if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  fence_async();
-  tc_fence_before_sync();
   __syncthreads();
-  cluster_sync();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  if constexpr (C::slices > 1) cluster_sync();
 
-  // One that runs out is recorded, and no wait of the block waits after it: every warp goes through its chunks, without
-  // results, so that the named barriers stay in step (nothing but such waits lies between two of them).
+  // One that runs out is recorded, and no wait of the block waits after it.
   auto wait = [&](int b, int phase) {
     bool done = mbar_try_wait(&bar[b], phase & 1) || *abort != 0;
     for (int i = 0; i < 512 && !done; ++i) done = mbar_try_wait(&bar[b], phase & 1);
@@ -368,362 +332,435 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
     }
     __syncwarp();
   };
-  // The same for warps that may sleep meanwhile.
-  auto doze = [&](int b, int phase) {
-    for (int i = 0; i < 4096 && !*abort && !mbar_try_wait(&bar[b], phase & 1); ++i) __nanosleep(100);
-    wait(b, phase);
+  auto arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[b]);
   };
-  // What the warp wrote to shared memory and read from TMEM comes before what waits on the barrier, MMAs too.
-  auto give = [&](int named, int threads) {
-    fence_async();
-    tc_fence_before_sync();
-    asm volatile("bar.arrive %0, %1;" ::"r"(named), "r"(threads + 32) : "memory");
-  };
-  auto take = [&](int named, int threads) {
-    named_bar_sync(named, threads + 32);
-    tc_fence_after_sync();
-  };
+  auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
 
-  if (warp < 16) {
-    // ------------------------------------------------------------------ a half's chain
-    const int half = warp >> 3, named = half * kNamed;
-    const int quarter = warp & 3, col = ((warp >> 2) & 1) * W;  // of the half's columns
-    const uint32_t acc = tmem + ((uint32_t)quarter << 21) + half * kAccHalf + col;  // TMEM: lane 32 quarter
-    const int key = 32 * quarter + lane;      // the row of S
-    const bool top = quarter < 2;             // K's and T's rows, else Q's and P T's
-    const int t = 32 * (quarter & 1) + lane;  // the row of the chunk
-    unsigned char *ss = smem + kOffS + half * 16384, *us = smem + kOffU + half * 8192;
-    float* st = p.state + (((int64_t)d.slot * p.nv + h) * kGdnDim + key) * kGdnDim + col0 + half * kHalf + col;
-    unsigned* most = reinterpret_cast<unsigned*>(smem + kOffMax) + 8 * half;  // [4] of S, [4] of V: largest magnitudes, by chunk
-    float2 S[W / 2];
+  if (warp < NW) {
+    // ------------------------------------------------------------------ 16 columns
+    const int g = lane >> 2, q2 = 2 * (lane & 3);
+    const uint32_t base = smem_u32(smem);
+    // S^T: tile i, keys 8 i + q2 and the next; columns g and g + 8
+    float* st = p.state + ((int64_t)d.slot * p.nv + h) * kGdnState + col0 + 16 * warp + g;
+    const bool empty = d.fresh && begin == 0;
+    float2 S[16][2];
 #pragma unroll
-    for (int i = 0; i < W / 2; i += 2) {
-      const float4 x = d.fresh && begin == 0 ? gdn_zero4() : *reinterpret_cast<const float4*>(st + 2 * i);
-      S[i] = make_float2(x.x, x.y);
-      S[i + 1] = make_float2(x.z, x.w);
-    }
-    uint32_t v[W / 2];  // of the next chunk
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float* at = st + (8 * i + q2) * kGdnDim + 8 * u;
+        S[i][u] = empty ? both(0.0f) : make_float2(at[0], at[kGdnDim]);
+      }
+    uint32_t v[4][4];  // of the next chunk: rows 16 i + q2 and the next, + 8; columns g, g + 8
     auto fetch_v = [&](int c) {
       wait(kReady0 + (c & 1), c >> 1);
-      const unsigned char* src = smem + kOffV + (c & 1) * 8192 + t * 128;
-      const bool there = c * kRows + t < rows_left;  // (what stands behind the last row is another's, whatever it holds)
+      const uint32_t tile = base + C::off_v + (c & 1) * kRows * C::cols * 2 + (warp >> 2) * kRows * 128;
 #pragma unroll
-      for (int i = 0; i < W / 8; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src + ((((half * kHalf + col) >> 3) + i) ^ (t & 7)) * 16);
-        v[4 * i] = there ? x.x : 0;
-        v[4 * i + 1] = there ? x.y : 0;
-        v[4 * i + 2] = there ? x.z : 0;
-        v[4 * i + 3] = there ? x.w : 0;
+      for (int i = 0; i < 4; ++i)
+        ldsm4_trans(v[i], tile + piece(16 * i + (lane & 7) + ((lane >> 4) << 3), (2 * warp + ((lane >> 3) & 1)) & 7));
+      const int have = rows_left - c * kRows;
+      if (have < kRows) {  // what stands behind the last row is another's, whatever it holds
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = 16 * i + 8 * (u >> 1) + q2;
+            v[i][u] = row + 1 < have ? v[i][u] : row < have ? v[i][u] & 0xffffu : 0;
+          }
       }
     };
-    auto tell = [&](int at, float m) {  // a warp's largest magnitude to the half's
-      const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-      if (lane == 0) atomicMax(&most[at], u);
-    };
-    auto tell_state = [&](int c) {
-      float ms[2] = {};
+    auto most_of = [&](float& a, float& b) {  // over the four lanes of columns g and g + 8
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(S[i].x)), fabsf(S[i].y));
-      tell(c & 3, fmaxf(ms[0], ms[1]));
-    };
-    auto tell_values = [&](int c) {
-      float ms[2] = {};
-#pragma unroll
-      for (int i = 0; i < W / 2; ++i) {
-        const float2 x = bf16_pair(v[i]);
-        ms[i & 1] = fmaxf(fmaxf(ms[i & 1], fabsf(x.x)), fabsf(x.y));
+      for (int o = 1; o < 4; o <<= 1) {
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
       }
-      tell(4 + (c & 3), fmaxf(ms[0], ms[1]));
     };
-    float up = 1.0f, down = 1.0f;  // the chunk's power of two, and one over it
-    // S, as it stands before chunk c, scaled and in two parts to shared memory.  The scale goes by the state one chunk
-    // before, whose magnitudes every warp has told by now.
-    auto put_state = [&](int c) {
-      const int b = max(c - 1, 0);
-      const float m = __uint_as_float(max(most[b & 3], max(most[4 + (b & 3)], most[4 + (c & 3)])));
-      // m = 2^e 1.f goes to 2^-2 1.f (zeros and infinities: as they are); the inverse is a normal number too
-      const int e = (int)(__float_as_uint(m) >> 23);
-      const int by = e == 0 || e == 255 ? 0 : min(max(125 - e, -120), 120);
-      up = __uint_as_float((uint32_t)(127 + by) << 23);
-      down = __uint_as_float((uint32_t)(127 - by) << 23);
-      float2 x[W / 2];
+    auto most_v = [&](float (&m)[2]) {
+      float2 a[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) x[i] = mul2(S[i], both(up));
-      put_sides<W>(ss, key, col, x);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 x = bf16_pair(v[i][u]);
+          a[u & 1] = make_float2(fmaxf(a[u & 1].x, fabsf(x.x)), fmaxf(a[u & 1].y, fabsf(x.y)));
+        }
+      m[0] = fmaxf(a[0].x, a[0].y);
+      m[1] = fmaxf(a[1].x, a[1].y);
+      most_of(m[0], m[1]);
     };
-    const uint32_t sum_to = smem_u32(smem + kOffSum);
-    const int me = (int)rank_in_cluster();
-    tell_state(0);
-    if (top) {
-      fetch_v(0);
-      tell_values(0);
+    // the state's scale, column by column: S holds the state times up
+    float ms[2] = {}, mv[2];
+    fetch_v(0);
+    most_v(mv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) ms[u] = fmaxf(ms[u], fmaxf(fabsf(S[i][u].x), fabsf(S[i][u].y)));
+    most_of(ms[0], ms[1]);
+    int by[2];
+    float up[2], down[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      by[u] = scale_by(fmaxf(ms[u], mv[u]));
+      up[u] = two_to(by[u]);
+      down[u] = two_to(-by[u]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[i][u] = mul2(S[i][u], both(up[u]));
     }
-    named_bar_sync(named + kBarTurn, 256);
-    put_state(0);
-    give(named + kBarS, 256);
 
-    // The output of a chunk, whose rows stand in o, is finished while the next chunk's products run, so that the state does
-    // not wait for it: its norm and gate between the next chunk's first two products, its stores between the last two.  The
-    // rows turn in S's place, which the first product is done with, so that stores are whole lines: a thread's own row would
-    // be a line for every lane (3,000 cycles a chunk).
-    float2 o[W / 2];
+    const int me = (int)rank_in_cluster();
+    float* sums = reinterpret_cast<float*>(smem + C::off_sum);
+    float* norms = sums + (2 * 8 + warp) * kRows;
+    float gain[2] = {1.0f, 1.0f};
+    if (p.norm_w) {
+      gain[0] = p.norm_w[col0 + 16 * warp + g];
+      gain[1] = p.norm_w[col0 + 16 * warp + g + 8];
+    }
+    // The output of a chunk, o, is finished while the next chunk is on its way: the norm's sums come from the cluster's warps.
+    float2 o[8][2];
     auto finish = [&](int c) {
-      float r = 1.0f;
       if (p.norm_w) {
         wait(kSum0 + (c & 1), c >> 1);
-        try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
-        const float* sums = reinterpret_cast<const float*>(smem + kOffSum) + (c & 1) * kSlices * 4 * kRows + t;
-        float y = 0.0f;
+        if constexpr (C::slices > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
+        float2 y = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < 4 * kSlices; ++i) y += sums[i * kRows];
-        r = rsqrtf(fmaf(y, 1.0f / kGdnDim, p.eps));
-      }
+        for (int i = 0; i < 8; ++i) y = add2(y, *reinterpret_cast<const float2*>(sums + ((c & 1) * 8 + i) * kRows + 2 * lane));
+        __syncwarp();  // (the chunk before is done with the norms)
+        *reinterpret_cast<float2*>(norms + 2 * lane) =
+            make_float2(rsqrtf(fmaf(y.x, 1.0f / kGdnDim, p.eps)), rsqrtf(fmaf(y.y, 1.0f / kGdnDim, p.eps)));
+        __syncwarp();
 #pragma unroll
-      for (int i = 0; i < W / 2; i += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(gain + half * kHalf + col + 2 * i);
-        o[i] = mul2(o[i], mul2(make_float2(w.x, w.y), both(r)));
-        o[i + 1] = mul2(o[i + 1], mul2(make_float2(w.z, w.w), both(r)));
+        for (int i = 0; i < 8; ++i) {
+          const float2 r = *reinterpret_cast<const float2*>(norms + 8 * i + q2);
+          o[i][0] = mul2(o[i][0], mul2(r, both(gain[0])));
+          o[i][1] = mul2(o[i][1], mul2(r, both(gain[1])));
+        }
       }
       if (p.z) {
         wait(kZ, c);
-        const unsigned char* zs = smem + kOffZ + half * kRows * 128 + t * 128;
+        const unsigned char* zs = smem + C::off_z + (warp >> 1) * kRows * 128;
 #pragma unroll
-        for (int i = 0; i < W / 2; i += 2) {
-          const float4 z = *reinterpret_cast<const float4*>(zs + ((((col >> 2) + i / 2) ^ (t & 7)) << 4));
-          o[i] = mul2(o[i], make_float2(gdn_silu(z.x), gdn_silu(z.y)));
-          o[i + 1] = mul2(o[i + 1], make_float2(gdn_silu(z.z), gdn_silu(z.w)));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kZFree]);
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int at = 16 * (warp & 1) + g + 8 * u;  // column of the panel
+            const float a = *reinterpret_cast<const float*>(zs + piece(8 * i + q2, at >> 2) + 4 * (at & 3));
+            const float b = *reinterpret_cast<const float*>(zs + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3));
+            o[i][u] = mul2(o[i][u], make_float2(gdn_silu(a), gdn_silu(b)));
+          }
+        arrive(kZFree);
       }
-      if (p.out_bf16) {
+      if (c > 0) wait(kOutFree, c - 1);
+      if constexpr (F32) {
+        unsigned char* to = smem + C::off_out + (warp >> 1) * kRows * 128;
 #pragma unroll
-        for (int i = 0; i < W / 2; i += 4)
-          *reinterpret_cast<uint4*>(ss + t * 64 + ((((col + 2 * i) >> 3) ^ ((t >> 1) & 3)) << 4)) =
-              make_uint4(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i + 1].x, o[i + 1].y), pack_bf16(o[i + 2].x, o[i + 2].y),
-                         pack_bf16(o[i + 3].x, o[i + 3].y));
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int at = 16 * (warp & 1) + g + 8 * u;
+            *reinterpret_cast<float*>(to + piece(8 * i + q2, at >> 2) + 4 * (at & 3)) = o[i][u].x;
+            *reinterpret_cast<float*>(to + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3)) = o[i][u].y;
+          }
       } else {
+        const uint32_t to = base + C::off_out + (warp >> 2) * kRows * 128;
 #pragma unroll
-        for (int i = 0; i < W / 2; i += 2)
-          *reinterpret_cast<float4*>(ss + t * 128 + ((((col + 2 * i) >> 2) ^ (t & 7)) << 4)) =
-              make_float4(o[i].x, o[i].y, o[i + 1].x, o[i + 1].y);
+        for (int i = 0; i < 8; i += 2)
+          stsm4_trans(to + piece(8 * i + (lane & 7) + ((lane >> 4) << 3), (2 * warp + ((lane >> 3) & 1)) & 7),
+                      pack_bf16(o[i][0].x, o[i][0].y), pack_bf16(o[i][1].x, o[i][1].y), pack_bf16(o[i + 1][0].x, o[i + 1][0].y),
+                      pack_bf16(o[i + 1][1].x, o[i + 1][1].y));
       }
+      fence_async();
+      arrive(kOut);
     };
-    auto store = [&](int c) {
-      named_bar_sync(named + kBarTurn, 128);
-      const int have = *abort ? 0 : min(kRows, rows_left - c * kRows), i0 = ((warp >> 2) & 1) * 64 + t;  // of 128
-      const int64_t to = (int64_t)(first_row + c * kRows) * p.out_row + h * p.out_head + col0 + half * kHalf;
-      if (p.out_bf16) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = i * 128 + i0, row = at >> 2, pc = at & 3;
-          if (row < have)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + row * p.out_row + 8 * pc) =
-                *reinterpret_cast<const uint4*>(ss + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = i * 128 + i0, row = at >> 3, pc = at & 7;
-          if (row < have)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to + row * p.out_row + 4 * pc) =
-                *reinterpret_cast<const float4*>(ss + row * 128 + ((pc ^ (row & 7)) << 4));
-        }
-      }
-    };
+
     for (int c = 0; c < chunks; ++c) {
-      const Decays* dec = reinterpret_cast<const Decays*>(smem + kOffDec) + (c & 1);
-      float2 x[W / 2];
-      float all;
-      if (top) {
-        take(named + kBarD1, 128);
-        const float keep = dec->keep[t], left = dec->left[t], beta = dec->beta[t], bu = beta * up, bk = -beta * keep;
-        all = dec->keep[kRows - 1];
-        ld_sums<W>(acc + kAccD1, kHalf, x);
+      const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
+      // S^T K^T and S^T Q^T
+      float2 ks[8][2] = {}, qs[8][2] = {};
+      ms[0] = ms[1] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) x[i] = fma2(both(bk), x[i], mul2(bf16_pair(v[i]), both(bu)));
-        put_sides<W>(us, t, col, x);
-        give(named + kBarR, 128);
-        if (c + 1 < chunks) {
-          fetch_v(c + 1);
-          tell_values(c + 1);
+      for (int k = 0; k < 8; ++k) {
+        uint32_t hi[4], lo[4];
+        split_a(hi, lo, S[2 * k], S[2 * k + 1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          ms[u] = fmaxf(fmaxf(fmaxf(ms[u], fabsf(S[2 * k][u].x)), fabsf(S[2 * k][u].y)),
+                        fmaxf(fabsf(S[2 * k + 1][u].x), fabsf(S[2 * k + 1][u].y)));
+        const uint32_t panel = kq + (k >> 2) * 16384;
+        const int at = 2 * (k & 3) + ((lane >> 3) & 1);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          uint32_t b[4], e[4];
+          const int row = 8 * j + (lane & 7) + ((lane >> 4) << 3);
+          ldsm4(b, panel + piece(row, at));
+          ldsm4(e, panel + 8192 + piece(row, at));
+          mma16(ks[j], lo, b[0], b[1]);
+          mma16(ks[j + 1], lo, b[2], b[3]);
+          if constexpr (F32) {
+            mma16(qs[j], lo, e[0], e[1]);
+            mma16(qs[j + 1], lo, e[2], e[3]);
+          }
+          mma16(qs[j], hi, e[0], e[1]);
+          mma16(qs[j + 1], hi, e[2], e[3]);
+          mma16(ks[j], hi, b[0], b[1]);
+          mma16(ks[j + 1], hi, b[2], b[3]);
         }
-        take(named + kBarD2, 128);
-        ld_sums<W>(acc + kAccD2, kHalf, x);
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) x[i] = mul2(x[i], both(left));
-        put_sides<W>(us, t, col, x);
-        give(named + kBarU, 128);
-      } else {
-        wait(kD1 + half, c);
-        tc_fence_after_sync();
-        const float keep = dec->keep[t], by = down * p.scale;
-        all = dec->keep[kRows - 1];
-        float2 y[W / 2];
-        ld_sums<W>(acc + kAccD1, kHalf, y);
-        if (c > 0) finish(c - 1);
-        wait(kD2 + half, c);
-        tc_fence_after_sync();
-        ld_sums<W>(acc + kAccD2, kHalf, x);
-        float2 sq = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          o[i] = mul2(fma2(both(keep), y[i], x[i]), both(by));
-          sq = fma2(o[i], o[i], sq);
-        }
-        if (p.norm_w && !*abort) {
-          // the row's sum of squares goes to all of the cluster
-          if (warp == 2 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], kSlices * 4 * kRows * 4);
-          const uint32_t at = sum_to + (((c & 1) * kSlices * 4 + me * 4 + (warp >> 2)) * kRows + t) * 4;
-#pragma unroll
-          for (int i = 0; i < kSlices; ++i) st_async(map_rank(at, i), sq.x + sq.y, map_rank(smem_u32(&bar[kSum0 + (c & 1)]), i));
-        }
-        if (c > 0) store(c - 1);
       }
-      take(named + kBarD3, 256);
-      ld_sums<W>(acc + kAccD3, kHalf, x);
+      if (c > 0) finish(c - 1);
+      // R^T = beta (V^T - exp(G) S^T K^T), as an operand; O^T = exp(G) S^T Q^T
+      uint32_t rh[4][4], rl[4][4];
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i) S[i] = fma2(both(all), S[i], mul2(x[i], both(down)));
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * i + e;
+          const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
+          const float2 beta = *reinterpret_cast<const float2*>(dec->beta + 8 * j + q2);
+          const float2 bk = mul2(mul2(beta, both(-1.0f)), keep);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ks[j][u] = fma2(bk, ks[j][u], mul2(bf16_pair(v[i][2 * e + u]), mul2(beta, both(up[u]))));
+            o[j][u] = mul2(keep, qs[j][u]);
+          }
+        }
+        split_a(rh[i], rl[i], ks[2 * i], ks[2 * i + 1]);
+      }
+      // U^T = R^T T^T, O^T += R^T (P T)^T: rows 16 j .. of T and P T by columns 16 i .., i <= j
+      float2 ut[8][2] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i <= j; ++i) {
+          uint32_t th[4], tl[4], ph[4];
+          const int row = 16 * j + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
+          ldsm4(th, tp + piece(row, at));
+          ldsm4(tl, tp + kPart + piece(row, at));
+          ldsm4(ph, tp + 8192 + piece(row, at));
+          mma16(ut[2 * j], rl[i], th[0], th[1]);
+          mma16(ut[2 * j + 1], rl[i], th[2], th[3]);
+          mma16(o[2 * j], rh[i], ph[0], ph[1]);
+          mma16(o[2 * j + 1], rh[i], ph[2], ph[3]);
+          mma16(ut[2 * j], rh[i], tl[0], tl[1]);
+          mma16(ut[2 * j + 1], rh[i], tl[2], tl[3]);
+          if constexpr (F32) {
+            uint32_t pl[4];
+            ldsm4(pl, tp + kPart + 8192 + piece(row, at));
+            mma16(o[2 * j], rl[i], ph[0], ph[1]);
+            mma16(o[2 * j + 1], rl[i], ph[2], ph[3]);
+            mma16(o[2 * j], rh[i], pl[0], pl[1]);
+            mma16(o[2 * j + 1], rh[i], pl[2], pl[3]);
+          }
+          mma16(ut[2 * j], rh[i], th[0], th[1]);
+          mma16(ut[2 * j + 1], rh[i], th[2], th[3]);
+        }
+      // the next chunk's values, its scale, and U^T diag(exp(G_64 - G)) in it, as an operand
+      const float all = dec->keep[kRows - 1];
+      float ratio[2] = {1.0f, 1.0f};
+      const float sc[2] = {down[0] * p.scale, down[1] * p.scale};
       if (c + 1 < chunks) {
-        put_state(c + 1);
-        give(named + kBarS, 256);
-        tell_state(c + 1);
-        if ((threadIdx.x & 255) == 0) most[(c + 3) & 3] = most[4 + ((c + 3) & 3)] = 0;  // (the chunk before this one's: read by all)
+        fetch_v(c + 1);
+        most_of(ms[0], ms[1]);
+        float old[2] = {mv[0], mv[1]};
+        most_v(mv);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int to = scale_by(fmaxf(ms[u] * down[u], fmaxf(old[u], mv[u])));
+          ratio[u] = two_to(min(max(to - by[u], -126), 127));
+          by[u] = to;
+          up[u] = two_to(to);
+          down[u] = two_to(-to);
+        }
+      }
+      uint32_t uh[4][4], ul[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * i + e;
+          const float2 left = *reinterpret_cast<const float2*>(dec->left + 8 * j + q2);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) ut[j][u] = mul2(ut[j][u], mul2(left, both(ratio[u])));
+        }
+        split_a(uh[i], ul[i], ut[2 * i], ut[2 * i + 1]);
+      }
+      // S^T = exp(G_64) S^T + U^T K
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) S[i][u] = mul2(S[i][u], both(all * ratio[u]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          uint32_t b[4], e[4];
+          const int row = 16 * i + (lane & 15), at = (j & 7) + (lane >> 4);
+          const uint32_t panel = kq + (j >> 3) * 16384;
+          ldsm4_trans(b, panel + piece(row, at));
+          ldsm4_trans(e, panel + piece(row, at + 2));
+          mma16(S[j], ul[i], b[0], b[1]);
+          mma16(S[j + 1], ul[i], b[2], b[3]);
+          mma16(S[j + 2], ul[i], e[0], e[1]);
+          mma16(S[j + 3], ul[i], e[2], e[3]);
+          mma16(S[j], uh[i], b[0], b[1]);
+          mma16(S[j + 1], uh[i], b[2], b[3]);
+          mma16(S[j + 2], uh[i], e[0], e[1]);
+          mma16(S[j + 3], uh[i], e[2], e[3]);
+        }
+      arrive(kFree0 + (c & 1));
+      // O, and its columns' share of the rows' sums of squares: to 8 rows' sums over 8 lanes, then one over the lanes' halves
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(sc[u]));
+      if (p.norm_w && !dead()) {
+        if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], 8 * kRows * 4);
+        float2 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fma2(o[j][0], o[j][0], mul2(o[j][1], o[j][1]));
+        // lanes 16, then 8, then 4 apart: each keeps half of what it has, and adds the other's
+#pragma unroll
+        for (int w = 4; w >= 1; w >>= 1) {
+          const bool high = lane & (4 * w);
+#pragma unroll
+          for (int j = 0; j < w; ++j) {
+            const float2 mine = high ? y[j + w] : y[j], give = high ? y[j] : y[j + w];
+            y[j].x = mine.x + __shfl_xor_sync(0xffffffffu, give.x, 4 * w);
+            y[j].y = mine.y + __shfl_xor_sync(0xffffffffu, give.y, 4 * w);
+          }
+        }
+        // tile of the lane: its bits 4, 3, 2
+        const int row = 8 * ((lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)) + q2;
+        const uint32_t at = smem_u32(sums + ((c & 1) * 8 + me * NW + warp) * kRows + row), on = smem_u32(&bar[kSum0 + (c & 1)]);
+#pragma unroll
+        for (int i = 0; i < C::slices; ++i) {
+          st_async(map_rank(at, i), y[0].x, map_rank(on, i));
+          st_async(map_rank(at + 4, i), y[0].y, map_rank(on, i));
+        }
       }
     }
-    if (!top) {
-      finish(chunks - 1);
-      store(chunks - 1);
-    }
+    finish(chunks - 1);
     if (!*abort) {
 #pragma unroll
-      for (int i = 0; i < W / 2; i += 2) *reinterpret_cast<float4*>(st + 2 * i) = make_float4(S[i].x, S[i].y, S[i + 1].x, S[i + 1].y);
-    }
-  } else if (warp < 18) {
-    // ------------------------------------------------------------------ a half's products
-    const int half = warp - 16, named = half * kNamed;
-    const uint32_t kq = smem_u32(smem + kOffKq), tp = smem_u32(smem + kOffTpt), acc = tmem + half * kAccHalf;
-    const uint64_t ss = desc_mn(smem_u32(smem + kOffS + half * 16384), 0), us = desc_mn(smem_u32(smem + kOffU + half * 8192), 0);
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t kqc = kq + (c & 1) * 32768, tpc = tp + (c & 1) * 2 * kPart;
-      wait(kReady0 + (c & 1), c >> 1);
-      take(named + kBarS, 256);
-      if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(kqc);
+      for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16(acc + kAccD1, a + (k >> 2) * (16384 >> 4) + (k & 3) * 2, ss + k * (2048 >> 4), kIdesc<128, 64, false, true>, k > 0);
-        umma_commit(&bar[kD1 + half]);
-      }
-      __syncwarp();
-      wait(kD1 + half, c);
-      give(named + kBarD1, 128);
-      take(named + kBarR, 128);
-      if (elect_one()) {
-        const uint64_t a = umma_desc_sw128(tpc);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mma_f16(acc + kAccD2, a + 2 * k, us + k * (2048 >> 4), kIdesc<128, 64, false, true>, k > 0);
-          mma_f16(acc + kAccD2, a + (kPart >> 4) + 2 * k, us + k * (2048 >> 4), kIdesc<128, 64, false, true>, 1);
+        for (int u = 0; u < 2; ++u) {
+          float* at = st + (8 * i + q2) * kGdnDim + 8 * u;
+          at[0] = S[i][u].x * down[u];
+          at[kGdnDim] = S[i][u].y * down[u];
         }
-        umma_commit(&bar[kD2 + half]);
-      }
-      __syncwarp();
-      wait(kD2 + half, c);
-      give(named + kBarD2, 128);
-      take(named + kBarU, 128);
-      if (elect_one()) {
-        const uint64_t a = desc_mn(kqc, 16384);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f16(acc + kAccD3, a + k * (2048 >> 4), us + k * (2048 >> 4), kIdesc<128, 64, true, true>, k > 0);
-        umma_commit(&bar[kD3 + half]);
-      }
-      __syncwarp();
-      wait(kD3 + half, c);
-      give(named + kBarD3, 256);
     }
-    if (__any_sync(0xffffffffu, *abort != 0)) {  // what was issued is done with before the TMEM goes
-      if (elect_one()) {
-        umma_commit(&bar[kDrain + half]);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_suspend(&bar[kDrain + half], 0, 20000u) && globaltimer_ns() - t0 < 1000000000ull) {
-        }
-      }
-      __syncwarp();
-    }
-  } else if (warp == 18) {
-    // ------------------------------------------------------------------ K, Q, V, z and the records
+  } else {
+    // ------------------------------------------------------------------ the copies
     // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
     // and those that were are waited for before the block ends.
     const int hk = h / p.group;
     int copied = 0, gates = 0;  // chunks of which all but z, and of which z, was asked for
-    auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
+    auto load = [&](int c) {
+      if (c >= 2) wait(kFree0 + (c & 1), (c - 2) >> 1);
+      if (dead()) return;
+      copied = c + 1;
+      const int row = first_row + c * kRows;
+      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
+      if (elect_one()) {
+        uint64_t* land = &bar[kLand0 + (c & 1)];
+        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * C::cols * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, row, land);
+          tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, row, land);
+        }
+#pragma unroll
+        for (int i = 0; i < C::cols / 64; ++i)
+          tma_load_3d_tx(smem + C::off_v + (c & 1) * kRows * C::cols * 2 + i * kRows * 128, &maps.v, col0 + 64 * i, h, row, land);
+        const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
+        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
+        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
+      }
+      __syncwarp();
+    };
+    auto landed = [&](int c) {
+      wait(kLand0 + (c & 1), c >> 1);
+      const int have = rows_left - c * kRows;
+      unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
+      if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
+        for (int i = lane; i < (kRows - have) * 32; i += 32) {
+          const int row = have + (i >> 5), at = i & 31;
+          *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+      if (!dbg.unreachable) arrive(kReady0 + (c & 1));
+    };
     auto load_z = [&](int c) {
       if (!p.z) return;
-      if (c >= 1) doze(kZFree, c - 1);
+      if (c >= 1) wait(kZFree, c - 1);
       if (dead()) return;
       gates = c + 1;
-      unsigned char* zs = smem + kOffZ;
+      unsigned char* zs = smem + C::off_z;
       const int first = c * kRows, have = min(kRows, rows_left - first);
       if (p.z_wide) {
         if (elect_one()) {
-          mbar_arrive_expect_tx(&bar[kZ], kRows * kCols * 4);
+          mbar_arrive_expect_tx(&bar[kZ], kRows * C::cols * 4);
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i)
+          for (int i = 0; i < C::cols / 32; ++i)
             tma_load_3d_tx(zs + i * kRows * 128, &maps.z, col0 + 32 * i, h, first_row + first, &bar[kZ]);
         }
         __syncwarp();
       } else {
         const float* z0 = p.z + (first_row + first) * p.z_row + h * p.z_head + col0;
 #pragma unroll 8
-        for (int u = 0; u < kRows * kCols / 32; ++u) {
-          const int at = u * 32 + lane, x = at / kCols, cl = at % kCols;
+        for (int u = 0; u < kRows * C::cols / 32; ++u) {
+          const int at = u * 32 + lane, x = at / C::cols, cl = at % C::cols;
           if (x < have)
-            *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + x * 128 + ((((cl >> 2) & 7) ^ (x & 7)) << 4) + 4 * (cl & 3)) =
-                z0[x * p.z_row + cl];
+            *reinterpret_cast<float*>(zs + (cl >> 5) * kRows * 128 + piece(x, (cl >> 2) & 7) + 4 * (cl & 3)) = z0[x * p.z_row + cl];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kZ]);
+        arrive(kZ);
       }
     };
-    for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) {
-        doze(kD3, c - 2);
-        doze(kD3 + 1, c - 2);
-      }
-      if (dead()) break;
-      copied = c + 1;
-      const int first = c * kRows, have = min(kRows, rows_left - first);
-      unsigned char* to = smem + kOffKq + (c & 1) * 32768;
-      if (elect_one()) {
-        uint64_t* land = &bar[kLand0 + (c & 1)];
-        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * kCols * 2);
+    auto store = [&](int c) {  // the output of chunk c
+      wait(kOut, c);
+      if (dead()) return;
+      const int have = min(kRows, rows_left - c * kRows), row = first_row + c * kRows;
+      constexpr int line = F32 ? 32 : 64;  // columns of a panel
+      const unsigned char* from = smem + C::off_out;
+      if (p.out_wide && have == kRows) {
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, first_row + first, land);
-          tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, first_row + first, land);
+          for (int i = 0; i < C::cols / line; ++i)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
+                         "r"(col0 + line * i), "r"(h), "r"(row), "r"(smem_u32(from + i * kRows * 128))
+                         : "memory");
+          asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
-        // (V of two chunks before is in registers since that chunk's state was made)
-        tma_load_3d_tx(smem + kOffV + (c & 1) * 8192, &maps.v, col0, h, first_row + first, land);
-        const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
-        bulk_g2s_nohint(smem + kOffTpt + (c & 1) * 2 * kPart, record, 2 * kPart, land);
-        bulk_g2s_nohint(smem + kOffDec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
-      }
-      __syncwarp();
-      doze(kLand0 + (c & 1), c >> 1);
-      if (have < kRows)  // the rows behind the sequence's last: others', whatever they hold
-        for (int i = lane; i < (kRows - have) * 32; i += 32) {
-          const int row = have + (i >> 5), at = i & 31;
-          *reinterpret_cast<uint4*>(to + (at >> 4) * 16384 + ((at >> 3) & 1) * 8192 + row * 128 + ((at & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-      if (!dbg.unreachable) {
-        fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kReady0 + (c & 1)]);
+      } else {
+        constexpr int pieces = C::cols * (F32 ? 4 : 2) / 16;  // of a row
+        unsigned char* out = static_cast<unsigned char*>(p.out) + ((int64_t)row * p.out_row + h * p.out_head + col0) * (F32 ? 4 : 2);
+        for (int i = lane; i < have * pieces; i += 32) {
+          const int x = i / pieces, at = i % pieces;
+          *reinterpret_cast<uint4*>(out + x * p.out_row * (F32 ? 4 : 2) + 16 * at) =
+              *reinterpret_cast<const uint4*>(from + (at >> 3) * kRows * 128 + piece(x, at & 7));
+        }
       }
-      if (c > 0) load_z(c - 1);  // (wanted when the next chunk is on its way)
+      arrive(kOutFree);
+    };
+    load(0);
+    if (chunks > 1) load(1);
+    landed(0);
+    load_z(0);
+    for (int c = 0; c < chunks && !dead(); ++c) {
+      if (c + 1 < chunks) landed(c + 1);
+      if (c > 0) {
+        store(c - 1);
+        load_z(c);
+      }
+      if (c + 2 < chunks) load(c + 2);
     }
-    load_z(chunks - 1);
+    store(chunks - 1);
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
     if (dead()) {
       auto drain = [&](int b, int phase) {
         const uint64_t t0 = globaltimer_ns();
@@ -734,18 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const __grid_con
       if (gates && p.z_wide) drain(kZ, gates - 1);
     }
   }
-  tc_fence_before_sync();
   __syncthreads();
-  cluster_sync();  // (no CTA leaves while another may still store into it)
-  if (*abort) {    // (and a store that nothing waited for lands within a microsecond)
+  if constexpr (C::slices > 1) cluster_sync();  // (no CTA leaves while another may still store into it)
+  if (*abort) {                                 // (and a store that nothing waited for lands within a microsecond)
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 50000) {
     }
-    __syncwarp();
-  }
-  if (warp == 16) {
-    tc_fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -1091,23 +1122,25 @@ bool rows_map(CUtensorMap* map, const void* base, CUtensorMapDataType type, int6
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int NW, bool F32>
 cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const Records& records, const ChunkDebug& dbg, int* status, int dev,
                    cudaStream_t s) {
+  using C = Cfg<NW>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = kv_smem_limit(gdn_chunk_kernel, kChunkSmem, dev, done);
+  cudaError_t e = kv_smem_limit(gdn_chunk_kernel<NW, F32>, C::smem, dev, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * kSlices));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kChunkSmem;
+  cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * C::slices));
+  cfg.blockDim = dim3(C::threads);
+  cfg.dynamicSmemBytes = C::smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kSlices;
+  at[0].val.clusterDim.x = C::slices;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel, p, maps, records, dbg, status);
+  return cudaLaunchKernelEx(&cfg, gdn_chunk_kernel<NW, F32>, p, maps, records, dbg, status);
 }
 
 constexpr int64_t kScratch = 1LL << 30;  // most bytes of records at a time; more chunks than they hold go in several launches
@@ -1123,7 +1156,9 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
   if (!rows_map(&maps.k, p.k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.c.rows, nk, p.k_row, p.k_head) ||
       !rows_map(&maps.q, p.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.c.rows, nk, p.q_row, p.q_head) ||
       !rows_map(&maps.v, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.c.rows, p.nv, p.v_row, p.v_head) ||
-      (p.z && p.z_wide && !rows_map(&maps.z, p.z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.c.rows, p.nv, p.z_row, p.z_head)))
+      (p.z && p.z_wide && !rows_map(&maps.z, p.z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.c.rows, p.nv, p.z_row, p.z_head)) ||
+      (p.out_wide && !rows_map(&maps.out, p.out, p.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.c.rows,
+                               p.nv, p.out_row, p.out_head)))
     return cudaErrorInvalidValue;
   const ChunkDebug dbg{timeout_ns, unreachable};
   // records of all chunks, where they are few enough; else of a stretch of every sequence at a time
@@ -1146,7 +1181,7 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
     const int64_t slots = records.dense ? (int64_t)p.c.n_seqs * records.length : p.c.rows / kRows + p.c.n_seqs;
     gdn_prepare_kernel<<<dim3((unsigned)slots, (unsigned)nk), kPrepThreads, kPrepSmem, s>>>(p, records);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch(p, maps, records, dbg, status, dev, s);
+    if (e == cudaSuccess) e = p.out_bf16 ? launch<4, false>(p, maps, records, dbg, status, dev, s) : launch<4, true>(p, maps, records, dbg, status, dev, s);
   }
   const cudaError_t f = cudaFreeAsync(scratch, s);
   return e != cudaSuccess ? e : f;

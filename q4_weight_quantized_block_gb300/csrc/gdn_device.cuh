@@ -37,7 +37,7 @@ struct GdnParams {
   int64_t q_row, q_head, k_row, k_head, v_row, v_head, z_row, z_head, out_row, out_head;
   float scale, eps;
   int nv, group;
-  bool out_bf16, z_wide;  // z_wide: every vector of z stands on a multiple of 16 bytes
+  bool out_bf16, z_wide, out_wide;  // z_wide: every vector of z stands on a multiple of 16 bytes; both: strides that TMA takes
   int few;  // most rows of a sequence that goes through the steps' kernel
 };
 
