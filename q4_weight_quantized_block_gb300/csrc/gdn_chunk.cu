@@ -80,20 +80,25 @@ template <int NW>
 struct Cfg {
   static constexpr int cols = 16 * NW;                              // value columns of a CTA
   static constexpr int slices = kGdnDim / cols;                     // CTAs of a head
-  static constexpr int threads = 32 * NW + 32;
+  static constexpr int threads = 64 * NW + 32;
   static constexpr int off_kq = 0;                                  // two stages of [K; Q]: two panels of 128 rows
   static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two parts
-  static constexpr int off_v = off_tp + 4 * kPart;                  // two stages of V: panels of 64 columns, 128 bytes
-  static constexpr int off_z = off_v + 2 * kRows * cols * 2;        // z: panels of 32 columns, 128 bytes
+  static constexpr int off_v = off_tp + 4 * kPart;                  // V: panels of 64 columns, 128 bytes
+  static constexpr int off_frag = off_v + kRows * cols * 2;         // each warp's S (8) and R (4) as operands, two parts
+  static constexpr int off_z = off_frag + NW * 12 * 1024;           // z: panels of 32 columns, 128 bytes
   static constexpr int off_out = off_z + kRows * cols * 4;          // the output, f32 or bf16: panels of 128 bytes
   static constexpr int off_dec = off_out + kRows * cols * 4;
   static constexpr int off_sum = off_dec + 2 * (int)sizeof(Decays);  // sums of squares [2][8][64], then 1 / norms [NW][64]
-  static constexpr int off_bar = off_sum + (2 * 8 + NW) * kRows * 4;
+  static constexpr int off_down = off_sum + (2 * 8 + NW) * kRows * 4;  // one over the columns' scales
+  static constexpr int off_bar = off_down + cols * 4;
   static constexpr int smem = off_bar + 128 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
 };
 
-enum Bars { kLand0, kLand1, kReady0, kReady1, kFree0, kFree1, kZ, kZFree, kSum0, kSum1, kOut, kOutFree, kBars };
+// Named barriers of a pair of warps (pair w: 3 w on).
+enum Named { kBarS = 1, kBarR, kBarUsed };
+
+enum Bars { kLand0, kLand1, kReady0, kReady1, kFree0, kFree1, kVFree, kZ, kZFree, kSum0, kSum1, kOut, kOutFree, kBars };
 
 FAK_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
 
   if (threadIdx.x == 0) {
     *abort = 0;
-    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kFree0 || i == kFree1 || i == kZFree || i == kOut ? NW : 1);
+    for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i == kFree0 || i == kFree1 ? 2 * NW : i == kVFree || i == kZFree || i == kOut ? NW : 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -356,10 +361,11 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
     uint32_t v[4][4];  // of the next chunk: rows 16 i + q2 and the next, + 8; columns g, g + 8
     auto fetch_v = [&](int c) {
       wait(kReady0 + (c & 1), c >> 1);
-      const uint32_t tile = base + C::off_v + (c & 1) * kRows * C::cols * 2 + (warp >> 2) * kRows * 128;
+      const uint32_t tile = base + C::off_v + (warp >> 2) * kRows * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         ldsm4_trans(v[i], tile + piece(16 * i + (lane & 7) + ((lane >> 4) << 3), (2 * warp + ((lane >> 3) & 1)) & 7));
+      arrive(kVFree);
       const int have = rows_left - c * kRows;
       if (have < kRows) {  // what stands behind the last row is another's, whatever it holds
 #pragma unroll
@@ -411,81 +417,25 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
       for (int i = 0; i < 16; ++i) S[i][u] = mul2(S[i][u], both(up[u]));
     }
 
-    const int me = (int)rank_in_cluster();
-    float* sums = reinterpret_cast<float*>(smem + C::off_sum);
-    float* norms = sums + (2 * 8 + warp) * kRows;
-    float gain[2] = {1.0f, 1.0f};
-    if (p.norm_w) {
-      gain[0] = p.norm_w[col0 + 16 * warp + g];
-      gain[1] = p.norm_w[col0 + 16 * warp + g + 8];
-    }
-    // The output of a chunk, o, is finished while the next chunk is on its way: the norm's sums come from the cluster's warps.
-    float2 o[8][2];
-    auto finish = [&](int c) {
-      if (p.norm_w) {
-        wait(kSum0 + (c & 1), c >> 1);
-        if constexpr (C::slices > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
-        float2 y = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y = add2(y, *reinterpret_cast<const float2*>(sums + ((c & 1) * 8 + i) * kRows + 2 * lane));
-        __syncwarp();  // (the chunk before is done with the norms)
-        *reinterpret_cast<float2*>(norms + 2 * lane) =
-            make_float2(rsqrtf(fmaf(y.x, 1.0f / kGdnDim, p.eps)), rsqrtf(fmaf(y.y, 1.0f / kGdnDim, p.eps)));
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 r = *reinterpret_cast<const float2*>(norms + 8 * i + q2);
-          o[i][0] = mul2(o[i][0], mul2(r, both(gain[0])));
-          o[i][1] = mul2(o[i][1], mul2(r, both(gain[1])));
-        }
-      }
-      if (p.z) {
-        wait(kZ, c);
-        const unsigned char* zs = smem + C::off_z + (warp >> 1) * kRows * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int at = 16 * (warp & 1) + g + 8 * u;  // column of the panel
-            const float a = *reinterpret_cast<const float*>(zs + piece(8 * i + q2, at >> 2) + 4 * (at & 3));
-            const float b = *reinterpret_cast<const float*>(zs + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3));
-            o[i][u] = mul2(o[i][u], make_float2(gdn_silu(a), gdn_silu(b)));
-          }
-        arrive(kZFree);
-      }
-      if (c > 0) wait(kOutFree, c - 1);
-      if constexpr (F32) {
-        unsigned char* to = smem + C::off_out + (warp >> 1) * kRows * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int at = 16 * (warp & 1) + g + 8 * u;
-            *reinterpret_cast<float*>(to + piece(8 * i + q2, at >> 2) + 4 * (at & 3)) = o[i][u].x;
-            *reinterpret_cast<float*>(to + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3)) = o[i][u].y;
-          }
-      } else {
-        const uint32_t to = base + C::off_out + (warp >> 2) * kRows * 128;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-          stsm4_trans(to + piece(8 * i + (lane & 7) + ((lane >> 4) << 3), (2 * warp + ((lane >> 3) & 1)) & 7),
-                      pack_bf16(o[i][0].x, o[i][0].y), pack_bf16(o[i][1].x, o[i][1].y), pack_bf16(o[i + 1][0].x, o[i + 1][0].y),
-                      pack_bf16(o[i + 1][1].x, o[i + 1][1].y));
-      }
-      fence_async();
-      arrive(kOut);
-    };
-
+    uint4* frag = reinterpret_cast<uint4*>(smem + C::off_frag) + warp * 24 * 32 + lane;
+    float* downs = reinterpret_cast<float*>(smem + C::off_down) + 16 * warp;
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
       const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
-      // S^T K^T and S^T Q^T
-      float2 ks[8][2] = {}, qs[8][2] = {};
+      // S^T, as an operand, to the output's warp too; S^T K^T
+      float2 ks[8][2] = {};
       ms[0] = ms[1] = 0.0f;
+      if (c > 0) named_bar_sync(3 * warp + kBarUsed, 64);
+      if ((lane & 3) == 0) {
+        downs[g] = down[0];
+        downs[g + 8] = down[1];
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         uint32_t hi[4], lo[4];
         split_a(hi, lo, S[2 * k], S[2 * k + 1]);
+        frag[2 * k * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        frag[(2 * k + 1) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           ms[u] = fmaxf(fmaxf(fmaxf(ms[u], fabsf(S[2 * k][u].x)), fabsf(S[2 * k][u].y)),
@@ -493,25 +443,23 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
         const uint32_t panel = kq + (k >> 2) * 16384;
         const int at = 2 * (k & 3) + ((lane >> 3) & 1);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
+        for (int j = 0; j < 8; j += 4) {
           uint32_t b[4], e[4];
           const int row = 8 * j + (lane & 7) + ((lane >> 4) << 3);
           ldsm4(b, panel + piece(row, at));
-          ldsm4(e, panel + 8192 + piece(row, at));
+          ldsm4(e, panel + piece(row + 16, at));
           mma16(ks[j], lo, b[0], b[1]);
           mma16(ks[j + 1], lo, b[2], b[3]);
-          if constexpr (F32) {
-            mma16(qs[j], lo, e[0], e[1]);
-            mma16(qs[j + 1], lo, e[2], e[3]);
-          }
-          mma16(qs[j], hi, e[0], e[1]);
-          mma16(qs[j + 1], hi, e[2], e[3]);
+          mma16(ks[j + 2], lo, e[0], e[1]);
+          mma16(ks[j + 3], lo, e[2], e[3]);
           mma16(ks[j], hi, b[0], b[1]);
           mma16(ks[j + 1], hi, b[2], b[3]);
+          mma16(ks[j + 2], hi, e[0], e[1]);
+          mma16(ks[j + 3], hi, e[2], e[3]);
         }
       }
-      if (c > 0) finish(c - 1);
-      // R^T = beta (V^T - exp(G) S^T K^T), as an operand; O^T = exp(G) S^T Q^T
+      asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarS) : "memory");
+      // R^T = beta (V^T - exp(G) S^T K^T), as an operand
       uint32_t rh[4][4], rl[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -524,43 +472,49 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             ks[j][u] = fma2(bk, ks[j][u], mul2(bf16_pair(v[i][2 * e + u]), mul2(beta, both(up[u]))));
-            o[j][u] = mul2(keep, qs[j][u]);
           }
         }
         split_a(rh[i], rl[i], ks[2 * i], ks[2 * i + 1]);
+        frag[(16 + 2 * i) * 32] = make_uint4(rh[i][0], rh[i][1], rh[i][2], rh[i][3]);
+        frag[(17 + 2 * i) * 32] = make_uint4(rl[i][0], rl[i][1], rl[i][2], rl[i][3]);
       }
-      // U^T = R^T T^T, O^T += R^T (P T)^T: rows 16 j .. of T and P T by columns 16 i .., i <= j
+      asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarR) : "memory");
+      // U^T = R^T T^T: rows 16 j .. of T by columns 16 i .., i <= j
       float2 ut[8][2] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; j += 2)
 #pragma unroll
-        for (int i = 0; i <= j; ++i) {
-          uint32_t th[4], tl[4], ph[4];
-          const int row = 16 * j + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
-          ldsm4(th, tp + piece(row, at));
-          ldsm4(tl, tp + kPart + piece(row, at));
-          ldsm4(ph, tp + 8192 + piece(row, at));
-          mma16(ut[2 * j], rl[i], th[0], th[1]);
-          mma16(ut[2 * j + 1], rl[i], th[2], th[3]);
-          mma16(o[2 * j], rh[i], ph[0], ph[1]);
-          mma16(o[2 * j + 1], rh[i], ph[2], ph[3]);
-          mma16(ut[2 * j], rh[i], tl[0], tl[1]);
-          mma16(ut[2 * j + 1], rh[i], tl[2], tl[3]);
-          if constexpr (F32) {
-            uint32_t pl[4];
-            ldsm4(pl, tp + kPart + 8192 + piece(row, at));
-            mma16(o[2 * j], rl[i], ph[0], ph[1]);
-            mma16(o[2 * j + 1], rl[i], ph[2], ph[3]);
-            mma16(o[2 * j], rh[i], pl[0], pl[1]);
-            mma16(o[2 * j + 1], rh[i], pl[2], pl[3]);
+        for (int i = 0; i <= j + 1; ++i) {
+          // two row blocks beside each other, where both have the columns
+          uint32_t th[2][4], tl[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (i > j + u) continue;
+            const int row = 16 * (j + u) + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
+            ldsm4(th[u], tp + piece(row, at));
+            ldsm4(tl[u], tp + kPart + piece(row, at));
           }
-          mma16(ut[2 * j], rh[i], th[0], th[1]);
-          mma16(ut[2 * j + 1], rh[i], th[2], th[3]);
+#pragma unroll
+          for (int w = 0; w < 3; ++w)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (i > j + u) continue;
+              const int x = 2 * (j + u);
+              if (w == 0) {
+                mma16(ut[x], rl[i], th[u][0], th[u][1]);
+                mma16(ut[x + 1], rl[i], th[u][2], th[u][3]);
+              } else if (w == 1) {
+                mma16(ut[x], rh[i], tl[u][0], tl[u][1]);
+                mma16(ut[x + 1], rh[i], tl[u][2], tl[u][3]);
+              } else {
+                mma16(ut[x], rh[i], th[u][0], th[u][1]);
+                mma16(ut[x + 1], rh[i], th[u][2], th[u][3]);
+              }
+            }
         }
       // the next chunk's values, its scale, and U^T diag(exp(G_64 - G)) in it, as an operand
       const float all = dec->keep[kRows - 1];
       float ratio[2] = {1.0f, 1.0f};
-      const float sc[2] = {down[0] * p.scale, down[1] * p.scale};
       if (c + 1 < chunks) {
         fetch_v(c + 1);
         most_of(ms[0], ms[1]);
@@ -611,38 +565,8 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
           mma16(S[j + 3], uh[i], e[2], e[3]);
         }
       arrive(kFree0 + (c & 1));
-      // O, and its columns' share of the rows' sums of squares: to 8 rows' sums over 8 lanes, then one over the lanes' halves
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(sc[u]));
-      if (p.norm_w && !dead()) {
-        if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], 8 * kRows * 4);
-        float2 y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = fma2(o[j][0], o[j][0], mul2(o[j][1], o[j][1]));
-        // lanes 16, then 8, then 4 apart: each keeps half of what it has, and adds the other's
-#pragma unroll
-        for (int w = 4; w >= 1; w >>= 1) {
-          const bool high = lane & (4 * w);
-#pragma unroll
-          for (int j = 0; j < w; ++j) {
-            const float2 mine = high ? y[j + w] : y[j], give = high ? y[j] : y[j + w];
-            y[j].x = mine.x + __shfl_xor_sync(0xffffffffu, give.x, 4 * w);
-            y[j].y = mine.y + __shfl_xor_sync(0xffffffffu, give.y, 4 * w);
-          }
-        }
-        // tile of the lane: its bits 4, 3, 2
-        const int row = 8 * ((lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)) + q2;
-        const uint32_t at = smem_u32(sums + ((c & 1) * 8 + me * NW + warp) * kRows + row), on = smem_u32(&bar[kSum0 + (c & 1)]);
-#pragma unroll
-        for (int i = 0; i < C::slices; ++i) {
-          st_async(map_rank(at, i), y[0].x, map_rank(on, i));
-          st_async(map_rank(at + 4, i), y[0].y, map_rank(on, i));
-        }
-      }
     }
-    finish(chunks - 1);
+    named_bar_sync(3 * warp + kBarUsed, 64);
     if (!*abort) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -653,6 +577,168 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
           at[kGdnDim] = S[i][u].y * down[u];
         }
     }
+  } else if (warp < 2 * NW) {
+    // ------------------------------------------------------------------ their output
+    const int w = warp - NW, g = lane >> 2, q2 = 2 * (lane & 3);
+    const uint32_t base = smem_u32(smem);
+    const int me = (int)rank_in_cluster();
+    float* sums = reinterpret_cast<float*>(smem + C::off_sum);
+    float* norms = sums + (2 * 8 + w) * kRows;
+    float gain[2] = {1.0f, 1.0f};
+    if (p.norm_w) {
+      gain[0] = p.norm_w[col0 + 16 * w + g];
+      gain[1] = p.norm_w[col0 + 16 * w + g + 8];
+    }
+    // The output of a chunk, o, is finished while the next chunk is on its way: the norm's sums come from the cluster's warps.
+    float2 o[8][2];
+    auto finish = [&](int c) {
+      if (p.norm_w) {
+        wait(kSum0 + (c & 1), c >> 1);
+        if constexpr (C::slices > 1) try_cluster(&bar[kSum0 + (c & 1)], c >> 1 & 1);  // (an acquire of the others' stores)
+        float2 y = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y = add2(y, *reinterpret_cast<const float2*>(sums + ((c & 1) * 8 + i) * kRows + 2 * lane));
+        __syncwarp();  // (the chunk before is done with the norms)
+        *reinterpret_cast<float2*>(norms + 2 * lane) =
+            make_float2(rsqrtf(fmaf(y.x, 1.0f / kGdnDim, p.eps)), rsqrtf(fmaf(y.y, 1.0f / kGdnDim, p.eps)));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 r = *reinterpret_cast<const float2*>(norms + 8 * i + q2);
+          o[i][0] = mul2(o[i][0], mul2(r, both(gain[0])));
+          o[i][1] = mul2(o[i][1], mul2(r, both(gain[1])));
+        }
+      }
+      if (p.z) {
+        wait(kZ, c);
+        const unsigned char* zs = smem + C::off_z + (w >> 1) * kRows * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int at = 16 * (w & 1) + g + 8 * u;  // column of the panel
+            const float a = *reinterpret_cast<const float*>(zs + piece(8 * i + q2, at >> 2) + 4 * (at & 3));
+            const float b = *reinterpret_cast<const float*>(zs + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3));
+            o[i][u] = mul2(o[i][u], make_float2(gdn_silu(a), gdn_silu(b)));
+          }
+        arrive(kZFree);
+      }
+      if (c > 0) wait(kOutFree, c - 1);
+      if constexpr (F32) {
+        unsigned char* to = smem + C::off_out + (w >> 1) * kRows * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int at = 16 * (w & 1) + g + 8 * u;
+            *reinterpret_cast<float*>(to + piece(8 * i + q2, at >> 2) + 4 * (at & 3)) = o[i][u].x;
+            *reinterpret_cast<float*>(to + piece(8 * i + q2 + 1, at >> 2) + 4 * (at & 3)) = o[i][u].y;
+          }
+      } else {
+        const uint32_t to = base + C::off_out + (w >> 2) * kRows * 128;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          stsm4_trans(to + piece(8 * i + (lane & 7) + ((lane >> 4) << 3), (2 * w + ((lane >> 3) & 1)) & 7),
+                      pack_bf16(o[i][0].x, o[i][0].y), pack_bf16(o[i][1].x, o[i][1].y), pack_bf16(o[i + 1][0].x, o[i + 1][0].y),
+                      pack_bf16(o[i + 1][1].x, o[i + 1][1].y));
+      }
+      fence_async();
+      arrive(kOut);
+    };
+
+    const uint4* frag = reinterpret_cast<const uint4*>(smem + C::off_frag) + w * 24 * 32 + lane;
+    const float* downs = reinterpret_cast<const float*>(smem + C::off_down) + 16 * w;
+    for (int c = 0; c < chunks; ++c) {
+      const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
+      if (c > 0) finish(c - 1);
+      named_bar_sync(3 * w + kBarS, 64);
+      // O^T = exp(G) S^T Q^T
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = both(0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint4 x = frag[2 * k * 32], y = frag[(2 * k + 1) * 32];
+        const uint32_t hi[4] = {x.x, x.y, x.z, x.w}, lo[4] = {y.x, y.y, y.z, y.w};
+        const uint32_t panel = kq + 8192 + (k >> 2) * 16384;
+        const int at = 2 * (k & 3) + ((lane >> 3) & 1);
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          uint32_t b[4], e[4];
+          const int row = 8 * j + (lane & 7) + ((lane >> 4) << 3);
+          ldsm4(b, panel + piece(row, at));
+          ldsm4(e, panel + piece(row + 16, at));
+          mma16(o[j], lo, b[0], b[1]);
+          mma16(o[j + 1], lo, b[2], b[3]);
+          mma16(o[j + 2], lo, e[0], e[1]);
+          mma16(o[j + 3], lo, e[2], e[3]);
+          mma16(o[j], hi, b[0], b[1]);
+          mma16(o[j + 1], hi, b[2], b[3]);
+          mma16(o[j + 2], hi, e[0], e[1]);
+          mma16(o[j + 3], hi, e[2], e[3]);
+        }
+      }
+      const float sc[2] = {downs[g] * p.scale, downs[g + 8] * p.scale};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
+        o[j][0] = mul2(keep, o[j][0]);
+        o[j][1] = mul2(keep, o[j][1]);
+      }
+      // O^T += R^T (P T)^T
+      named_bar_sync(3 * w + kBarR, 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = frag[(16 + 2 * i) * 32], y = frag[(17 + 2 * i) * 32];
+        const uint32_t rh[4] = {x.x, x.y, x.z, x.w}, rl[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = i; j < 4; ++j) {
+          uint32_t ph[4], pl[4];
+          const int row = 16 * j + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
+          ldsm4(ph, tp + 8192 + piece(row, at));
+          ldsm4(pl, tp + kPart + 8192 + piece(row, at));
+          mma16(o[2 * j], rl, ph[0], ph[1]);
+          mma16(o[2 * j + 1], rl, ph[2], ph[3]);
+          mma16(o[2 * j], rh, pl[0], pl[1]);
+          mma16(o[2 * j + 1], rh, pl[2], pl[3]);
+          mma16(o[2 * j], rh, ph[0], ph[1]);
+          mma16(o[2 * j + 1], rh, ph[2], ph[3]);
+        }
+      }
+      asm volatile("bar.arrive %0, 64;" ::"r"(3 * w + kBarUsed) : "memory");
+      arrive(kFree0 + (c & 1));
+      // O, and its columns' share of the rows' sums of squares: to 8 rows' sums over 8 lanes, then one over the lanes' halves
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(sc[u]));
+      if (p.norm_w && !dead()) {
+        if (w == 0 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], 8 * kRows * 4);
+        float2 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fma2(o[j][0], o[j][0], mul2(o[j][1], o[j][1]));
+        // lanes 16, then 8, then 4 apart: each keeps half of what it has, and adds the other's
+#pragma unroll
+        for (int m = 4; m >= 1; m >>= 1) {
+          const bool high = lane & (4 * m);
+#pragma unroll
+          for (int j = 0; j < m; ++j) {
+            const float2 mine = high ? y[j + m] : y[j], give = high ? y[j] : y[j + m];
+            y[j].x = mine.x + __shfl_xor_sync(0xffffffffu, give.x, 4 * m);
+            y[j].y = mine.y + __shfl_xor_sync(0xffffffffu, give.y, 4 * m);
+          }
+        }
+        // tile of the lane: its bits 4, 3, 2
+        const int row = 8 * ((lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)) + q2;
+        const uint32_t at = smem_u32(sums + ((c & 1) * 8 + me * NW + w) * kRows + row), on = smem_u32(&bar[kSum0 + (c & 1)]);
+#pragma unroll
+        for (int i = 0; i < C::slices; ++i) {
+          st_async(map_rank(at, i), y[0].x, map_rank(on, i));
+          st_async(map_rank(at + 4, i), y[0].y, map_rank(on, i));
+        }
+      }
+    }
+    finish(chunks - 1);
   } else {
     // ------------------------------------------------------------------ the copies
     // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
@@ -661,6 +747,7 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
     int copied = 0, gates = 0;  // chunks of which all but z, and of which z, was asked for
     auto load = [&](int c) {
       if (c >= 2) wait(kFree0 + (c & 1), (c - 2) >> 1);
+      if (c >= 1) wait(kVFree, c - 1);
       if (dead()) return;
       copied = c + 1;
       const int row = first_row + c * kRows;
@@ -675,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
         }
 #pragma unroll
         for (int i = 0; i < C::cols / 64; ++i)
-          tma_load_3d_tx(smem + C::off_v + (c & 1) * kRows * C::cols * 2 + i * kRows * 128, &maps.v, col0 + 64 * i, h, row, land);
+          tma_load_3d_tx(smem + C::off_v + i * kRows * 128, &maps.v, col0 + 64 * i, h, row, land);  // (the last chunk's is in registers)
         const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
         bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
         bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
@@ -747,8 +834,8 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
       arrive(kOutFree);
     };
     load(0);
-    if (chunks > 1) load(1);
     landed(0);
+    if (chunks > 1) load(1);
     load_z(0);
     for (int c = 0; c < chunks && !dead(); ++c) {
       if (c + 1 < chunks) landed(c + 1);
