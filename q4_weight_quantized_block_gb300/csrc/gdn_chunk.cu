@@ -80,7 +80,7 @@ template <int NW>
 struct Cfg {
   static constexpr int cols = 16 * NW;                              // value columns of a CTA
   static constexpr int slices = kGdnDim / cols;                     // CTAs of a head
-  static constexpr int threads = 64 * NW + 32;
+  static constexpr int threads = 64 * NW + 128;
   static constexpr int off_kq = 0;                                  // two stages of [K; Q]: two panels of 128 rows
   static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two parts
   static constexpr int off_v = off_tp + 4 * kPart;                  // V: panels of 64 columns, 128 bytes
@@ -343,6 +343,13 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
   };
   auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
 
+  // registers of a thread: 232 + 208 + 56 of the 3 * 168 that the block has
+  if (warp < NW)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+  else if (warp < 2 * NW)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp < NW) {
     // ------------------------------------------------------------------ 16 columns
     const int g = lane >> 2, q2 = 2 * (lane & 3);
@@ -739,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
       }
     }
     finish(chunks - 1);
-  } else {
+  } else if (warp == 2 * NW) {
     // ------------------------------------------------------------------ the copies
     // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
     // and those that were are waited for before the block ends.
