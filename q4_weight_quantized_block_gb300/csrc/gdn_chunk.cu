@@ -233,7 +233,22 @@ FAK_DEV void turn_b(FragB& b, const float (&c)[4]) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(b.lo[i]) : "r"(lo));
   }
 }
-// sign * a product's 16 x 8, both parts, at rows r0 .. +15, columns 8 j .. +7 of a tile
+// sign * two products' 16 x 8, beside each other, both parts, at rows r0 .. +15, columns 8 j .. +15 of a tile
+FAK_DEV void put_tiles(uint32_t tile, int r0, int j, const float (&a)[4], const float (&b)[4], float sign, int lane) {
+  uint32_t hi[4], lo[4];
+  split_half(sign * a[0], sign * a[1], hi[0], lo[0]);
+  split_half(sign * a[2], sign * a[3], hi[1], lo[1]);
+  split_half(sign * b[0], sign * b[1], hi[2], lo[2]);
+  split_half(sign * b[2], sign * b[3], hi[3], lo[3]);
+  const int row = r0 + (lane & 15);
+  const uint32_t at = tile + row * 128 + (((j + (lane >> 4)) ^ (row & 7)) << 4);
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+               : "memory");
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at + kPart), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
+               "r"(lo[3])
+               : "memory");
+}
+// The same for one product.
 FAK_DEV void put_block(unsigned char* tile, int r0, int j, const float (&c)[4], float sign, int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -875,8 +890,9 @@ __global__ void __launch_bounds__(Cfg<NW>::threads, 1) gdn_chunk_kernel(const __
 }
 
 // ------------------------------------------------------------------ T and P T
-constexpr int kOffTp = 32768, kOffDiag = kOffTp + 2 * kPart, kOffHi = kOffDiag + 4 * 16 * kLd * 4;  // behind [K; Q]
-constexpr int kPrepSmem = kOffHi + 4 * 3 * kRows * 4 + 1024;
+// [K; Q], and in their place, once their products are in registers, [T; P T]; A's blocks on the diagonal in f32; four heads' decays
+constexpr int kOffDiag = 2 * kPart, kOffHi = kOffDiag + 4 * 16 * kLd * 4, kHeadDecays = 7 * kRows;
+constexpr int kPrepSmem = kOffHi + 4 * kHeadDecays * 4 + 1024;
 
 // The sequence and chunk whose record is x, the whole warp: false where there is none.
 FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int64_t x, int lane, GdnSeq& d, int& s, int& c) {
@@ -917,7 +933,7 @@ FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int64_t x, int lan
 }
 
 // Block (x, h): record x, key head h.
-__global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __grid_constant__ GdnParams p, Records records) {
+__global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __grid_constant__ GdnParams p, Records records) {
   extern __shared__ unsigned char raw[];
   unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q2 = 2 * (lane & 3);
@@ -926,8 +942,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
   int s, c;
   if (!find_chunk(p, records, blockIdx.x, lane, d, s, c)) return;
   const int rows = d.r1 - d.first, first = c * kRows, have = min(kRows, rows - first);
-  unsigned char *kq = smem, *tp = smem + kOffTp;
-  const uint32_t kqs = smem_u32(kq), tps = smem_u32(tp);
+  unsigned char* tp = smem;
+  const uint32_t kqs = smem_u32(smem), tps = kqs;
   float* diag = reinterpret_cast<float*>(smem + kOffDiag);
 
   // K and Q, 16 threads to a row of 256 bytes; zeros behind the last row
@@ -947,8 +963,6 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  // T and P T are zero above their blocks on the diagonal, which nothing writes
-  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kPrepThreads) *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(0, 0, 0, 0);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
@@ -977,6 +991,10 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
       }
     }
   }
+
+  __syncthreads();
+  // T and P T are zero above their blocks on the diagonal, which nothing writes
+  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kPrepThreads) *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(0, 0, 0, 0);
 
   for (int h0 = 0; h0 < p.group; h0 += 4) {
     const int heads = min(4, p.group - h0);
@@ -1016,7 +1034,19 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
         if (before || odd[0] || (j == 1 && odd[1])) lo[j] = __uint_as_float(0x7fffffffu);
       }
       const float hi_end = __shfl_sync(0xffffffffu, hi[1], 31), lo_end = __shfl_sync(0xffffffffu, lo[1], 31);
-      float* mine = reinterpret_cast<float*>(smem + kOffHi) + w * 3 * kRows + 2 * lane;
+      // of a head: G as two f32, beta, exp(G_t - G of the last row before t's 16), exp(G of row 16 i - 1 - G_s), i = 1, 2, 3
+      float* mine = reinterpret_cast<float*>(smem + kOffHi) + w * kHeadDecays + 2 * lane;
+      float ref_hi[4], ref_lo[4];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        ref_hi[i] = __shfl_sync(0xffffffffu, hi[1], 8 * i - 1);
+        ref_lo[i] = __shfl_sync(0xffffffffu, lo[1], 8 * i - 1);
+        *reinterpret_cast<float2*>(mine + (3 + i) * kRows) =
+            make_float2(exp2_approx((ref_hi[i] - hi[0]) + (ref_lo[i] - lo[0])), exp2_approx((ref_hi[i] - hi[1]) + (ref_lo[i] - lo[1])));
+      }
+      const int own = lane >> 3;
+      const float rh = own == 1 ? ref_hi[1] : own == 2 ? ref_hi[2] : ref_hi[3], rl = own == 1 ? ref_lo[1] : own == 2 ? ref_lo[2] : ref_lo[3];
+      *reinterpret_cast<float2*>(mine + 3 * kRows) = make_float2(exp2_approx((hi[0] - rh) + (lo[0] - rl)), exp2_approx((hi[1] - rh) + (lo[1] - rl)));
       *reinterpret_cast<float2*>(mine) = make_float2(hi[0], hi[1]);
       *reinterpret_cast<float2*>(mine + kRows) = make_float2(lo[0], lo[1]);
       *reinterpret_cast<float2*>(mine + 2 * kRows) = make_float2(b[0], b[1]);
@@ -1029,33 +1059,51 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
     __syncthreads();
     for (int hh = 0; hh < heads; ++hh) {
       const int h = hk * p.group + h0 + hh;
-      const float* hi = reinterpret_cast<const float*>(smem + kOffHi) + hh * 3 * kRows;
+      const float* hi = reinterpret_cast<const float*>(smem + kOffHi) + hh * kHeadDecays;
       const float *lo = hi + kRows, *beta = hi + 2 * kRows;
-      // A and P from K K^T and Q K^T by the decays, to the places of T and P T
+      // A and P from K K^T and Q K^T by the decays, to the places of T and P T: within the rows' own 16 columns one exponential
+      // each, before them by way of the last row before the 16
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int tile = m ? mq : mk, row = 16 * tile + g;
-        const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
         const float b0 = m ? 1.0f : beta[row], b1 = m ? 1.0f : beta[row + 8];
-        const int last0 = m ? row : row - 1, last1 = last0 + 8;
+        const float f0 = b0 * hi[3 * kRows + row], f1 = b1 * hi[3 * kRows + row + 8];
+        const float* upto = hi + (3 + tile) * kRows;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j > 2 * tile + 1) continue;
-          const int col = 8 * j + q2;
-          const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
-          const float* x = m ? qk[j] : kk[j];
-          float y[4] = {b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * x[0], b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * x[1],
-                        b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * x[2], b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * x[3]};
-          // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
-          if (col > last0) y[0] = 0.0f;
-          if (col + 1 > last0) y[1] = 0.0f;
-          if (col > last1) y[2] = 0.0f;
-          if (col + 1 > last1) y[3] = 0.0f;
-          put_block(tp, m * kRows + 16 * tile, j, y, 1.0f, lane);
-          if (!m && j >= 2 * tile) {
-            *reinterpret_cast<float2*>(diag + row * kLd + (col & 15)) = make_float2(y[0], y[1]);
-            *reinterpret_cast<float2*>(diag + (row + 8) * kLd + (col & 15)) = make_float2(y[2], y[3]);
+        for (int j = 0; j < 8; j += 2) {
+          if (j > 2 * tile) continue;
+          float y[2][4];
+          if (j < 2 * tile) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 u = *reinterpret_cast<const float2*>(upto + 8 * (j + e) + q2);
+              const float* x = m ? qk[j + e] : kk[j + e];
+              const float2 top = mul2(mul2(u, both(f0)), make_float2(x[0], x[1])), low = mul2(mul2(u, both(f1)), make_float2(x[2], x[3]));
+              y[e][0] = top.x;
+              y[e][1] = top.y;
+              y[e][2] = low.x;
+              y[e][3] = low.y;
+            }
+          } else {
+            const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
+            const int last = m ? g : g - 1;  // of row g's own 16 columns; row g + 8's: 8 more
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = 8 * e + q2, col = 8 * j + at;
+              const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
+              const float* x = m ? qk[j + e] : kk[j + e];
+              // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
+              y[e][0] = at <= last ? b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * x[0] : 0.0f;
+              y[e][1] = at + 1 <= last ? b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * x[1] : 0.0f;
+              y[e][2] = at <= last + 8 ? b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * x[2] : 0.0f;
+              y[e][3] = at + 1 <= last + 8 ? b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * x[3] : 0.0f;
+              if (!m) {
+                *reinterpret_cast<float2*>(diag + row * kLd + at) = make_float2(y[e][0], y[e][1]);
+                *reinterpret_cast<float2*>(diag + (row + 8) * kLd + at) = make_float2(y[e][2], y[e][3]);
+              }
+            }
           }
+          put_tiles(tps, m * kRows + 16 * tile, j, y[0], y[1], 1.0f, lane);
         }
       }
       __syncthreads();
@@ -1171,8 +1219,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prepare_kernel(const __gr
         for (int i = 0; i < 4; ++i) {
           const int m = mine >> (8 * i + 4) & 15, j = mine >> (8 * i) & 15;
           if (m == 15) break;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) put_block(tp, kRows + 16 * m, 2 * j + u, y[i][u], 1.0f, lane);
+          put_tiles(tps, kRows + 16 * m, 2 * j, y[i][0], y[i][1], 1.0f, lane);
         }
       }
       fence_async();
