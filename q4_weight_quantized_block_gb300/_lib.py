@@ -1,6 +1,7 @@
 """ctypes binding over libfak.so: argument marshalling only (see include/fak.h)."""
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -502,85 +503,99 @@ class GDNBatch:
         self.ref = ctypes.addressof(self.desc)
 
 
-def _half_type():
-    """torch's float16."""
-    global _half_type
+def _gdn_types():
+    """torch's float32, bfloat16 and float16."""
+    global _gdn_types
     import torch
-    t = torch.float16
-    _half_type = lambda: t
-    return t
+    types = torch.float32, torch.bfloat16, torch.float16
+    _gdn_types = lambda: types
+    return types
 
 
-def _whole(t, shape, dtype, where):
-    """Pointer of a contiguous tensor of this shape and type."""
-    if t.shape != shape:
-        raise FakError(2, where)
-    if t.dtype != dtype or not t.is_contiguous():
-        raise FakError(1, where)
-    return t.data_ptr()
+# The calls' arguments as C lays them out (GdnRows, GdnArgs and NormArgs below the names of their fields): these calls are
+# bound by the host where rows are few, and a ctypes structure takes three times as long to fill.
+_GDN_ROWS = struct.Struct("@iiiifqPPPqqqPPPPPPPPP")
+_GDN_ARGS = struct.Struct("@iiiiiffqPPPqqqqqqPPPPPqqPqq")
+_NORM_ARGS = struct.Struct("@iiiiiifffqPPPqqqPPPqq")
 
 
-def _cols(t, rows, cols, dtype, where):
-    """Pointer and row stride of rows [rows, cols] with neighbouring values in a row."""
-    if t.shape != (rows, cols):
-        raise FakError(2, where)
-    if t.dtype != dtype or (t.stride(1) != 1 and cols > 1):
-        raise FakError(1, where)
-    return t.data_ptr(), t.stride(0)
-
-
-def _on_device(d, tensors, where):
-    """Whether all that are given are on CUDA device d, the current one."""
-    if d < 0 or any(t is not None and t.get_device() != d for t in tensors) or _current_device() != d:
-        raise FakError(8, where)
+def _refuse(status, where):
+    raise FakError(status, where)
 
 
 def fak_gdn_conv(batch, x, b, a, conv_w, a_log, dt_bias, conv_state, q, k, v, g, beta, eps=1e-6, stream=None):
     """x [rows, (2 nk + nv) 128], b and a [rows, nv], f32 or bf16 (views with row strides are fine); conv_w
     [(2 nk + nv) 128, 4], a_log and dt_bias [nv], conv_state [n_slots, 3, (2 nk + nv) 128] f32; out: q, k
     [rows, nk, 128] f16, v [rows, nv, 128] bf16, g and beta [rows, nv] f32."""
-    where, dtype, (f32, bf16), f16 = "fak_gdn_conv", x.dtype, _float_types(), _half_type()
-    if q.dim() != 3 or v.dim() != 3 or conv_state.dim() != 3:
-        raise FakError(2, where)
-    if dtype != f32 and dtype != bf16:
-        raise FakError(1, where)
-    rows, nk, nv = x.shape[0], q.shape[1], v.shape[1]
-    chans = (2 * nk + nv) * 128
-    xp, xr = _cols(x, rows, chans, dtype, where)
-    bp, br = _cols(b, rows, nv, dtype, where)
-    ap, ar = _cols(a, rows, nv, dtype, where)
-    r = GdnRows(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nk, nv, conv_state.shape[0], eps, rows, xp, bp, ap, xr,
-                br, ar, _whole(conv_w, (chans, 4), f32, where), _whole(a_log, (nv,), f32, where),
-                _whole(dt_bias, (nv,), f32, where), _whole(conv_state, (conv_state.shape[0], 3, chans), f32, where),
-                _whole(q, (rows, nk, 128), f16, where), _whole(k, (rows, nk, 128), f16, where),
-                _whole(v, (rows, nv, 128), bf16, where), _whole(g, (rows, nv), f32, where),
-                _whole(beta, (rows, nv), f32, where))
-    _on_device(batch.device, (x, b, a, conv_w, a_log, dt_bias, conv_state, q, k, v, g, beta), where)
-    _check(lib.fak_gdn_conv(batch.ref, ctypes.addressof(r), _stream(stream)), where)
+    dtype, (f32, bf16, f16) = x.dtype, _gdn_types()
+    qs, vs, cs, xs, per = q.shape, v.shape, conv_state.shape, x.shape, b.shape
+    if len(qs) != 3 or len(vs) != 3 or len(cs) != 3 or len(xs) != 2 or len(per) != 2:
+        _refuse(2, "fak_gdn_conv")
+    rows, nk, dk = qs
+    nv, chans = vs[1], xs[1]
+    if (dk != 128 or vs[2] != 128 or chans != (2 * nk + nv) * 128 or xs[0] != rows
+            or vs[0] != rows or k.shape != qs or per[0] != rows or per[1] != nv or a.shape != per or g.shape != per
+            or beta.shape != per or cs[1] != 3 or cs[2] != chans or conv_w.shape != (chans, 4) or a_log.shape != (nv,)
+            or dt_bias.shape != (nv,)):
+        _refuse(2, "fak_gdn_conv")
+    xr, xc = x.stride()
+    br, bc = b.stride()
+    ar, ac = a.stride()
+    if ((dtype != f32 and dtype != bf16) or b.dtype != dtype or a.dtype != dtype or xc != 1 or (nv > 1 and (bc != 1 or ac != 1))
+            or q.dtype != f16 or k.dtype != f16 or v.dtype != bf16 or g.dtype != f32 or beta.dtype != f32 or conv_w.dtype != f32
+            or a_log.dtype != f32 or dt_bias.dtype != f32 or conv_state.dtype != f32
+            or not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()
+                    and conv_w.is_contiguous() and a_log.is_contiguous() and dt_bias.is_contiguous()
+                    and conv_state.is_contiguous())):
+        _refuse(1, "fak_gdn_conv")
+    d = batch.device
+    if (d < 0 or x.get_device() != d or b.get_device() != d or a.get_device() != d or conv_w.get_device() != d
+            or a_log.get_device() != d or dt_bias.get_device() != d or conv_state.get_device() != d or q.get_device() != d
+            or k.get_device() != d or v.get_device() != d or g.get_device() != d or beta.get_device() != d
+            or _current_device() != d):
+        _refuse(8, "fak_gdn_conv")
+    args = _GDN_ROWS.pack(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nk, nv, cs[0], eps, rows, x.data_ptr(), b.data_ptr(),
+                          a.data_ptr(), xr, br, ar, conv_w.data_ptr(), a_log.data_ptr(), dt_bias.data_ptr(),
+                          conv_state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr())
+    _check(lib.fak_gdn_conv(batch.ref, args, _stream(stream)), "fak_gdn_conv")
 
 
 def fak_gdn_attn(batch, q, k, v, g, beta, state, out, max_q, scale=None, z=None, norm_w=None, eps=1e-6, stream=None):
     """q, k [rows, nk, 128] f16, v [rows, nv, 128] bf16, z (f32) and out (f32 or bf16) as v (views with strides are fine);
     g, beta [rows, nv] f32; state [n_slots, nv, 128, 128] f32; scale defaults to 128^-1/2."""
-    where, (f32, bf16), f16 = "fak_gdn_attn", _float_types(), _half_type()
-    if q.dim() != 3 or v.dim() != 3 or k.shape != q.shape or v.shape[0] != q.shape[0] or out.shape != v.shape or (
-            z is not None and z.shape != v.shape) or state.dim() != 4:
-        raise FakError(2, where)
-    if out.dtype != f32 and out.dtype != bf16:
-        raise FakError(1, where)
-    rows, nk, nv = q.shape[0], q.shape[1], v.shape[1]
-    qp, qr, qh = _heads(q, nk, 128, f16, where)
-    kp, kr, kh = _heads(k, nk, 128, f16, where)
-    vp, vr, vh = _heads(v, nv, 128, bf16, where)
-    op, orow, oh = _heads(out, nv, 128, out.dtype, where)
-    zp, zr, zh = (None, 0, 0) if z is None else _heads(z, nv, 128, f32, where)
-    a = GdnArgs(nk, nv, max_q, FAK_ROWS_F32 if out.dtype == f32 else FAK_ROWS_BF16, state.shape[0],
-                128 ** -0.5 if scale is None else scale, eps, rows, qp, kp, vp, qr, qh, kr, kh, vr, vh,
-                _whole(g, (rows, nv), f32, where), _whole(beta, (rows, nv), f32, where),
-                _whole(state, (state.shape[0], nv, 128, 128), f32, where), _gain(norm_w, 128, f32, where), zp, zr, zh, op,
-                orow, oh)
-    _on_device(batch.device, (q, k, v, g, beta, state, out, z, norm_w), where)
-    _check(lib.fak_gdn_attn(batch.ref, ctypes.addressof(a), _stream(stream)), where)
+    (f32, bf16, f16), kind = _gdn_types(), out.dtype
+    qs, vs, ss = q.shape, v.shape, state.shape
+    if len(qs) != 3 or len(vs) != 3 or len(ss) != 4:
+        _refuse(2, "fak_gdn_attn")
+    rows, nk, dk = qs
+    nv = vs[1]
+    if (dk != 128 or vs[2] != 128 or k.shape != qs or vs[0] != rows or out.shape != vs or (z is not None and z.shape != vs)
+            or ss[1] != nv or ss[2] != 128 or ss[3] != 128 or g.shape != (rows, nv) or beta.shape != (rows, nv)
+            or (norm_w is not None and norm_w.numel() != 128)):
+        _refuse(2, "fak_gdn_attn")
+    qr, qh, qc = q.stride()
+    kr, kh, kc = k.stride()
+    vr, vh, vc = v.stride()
+    outr, outh, outc = out.stride()
+    zr, zh, zc = (0, 0, 1) if z is None else z.stride()
+    if ((kind != f32 and kind != bf16) or q.dtype != f16 or k.dtype != f16 or v.dtype != bf16 or g.dtype != f32
+            or beta.dtype != f32 or state.dtype != f32 or (z is not None and z.dtype != f32)
+            or (norm_w is not None and (norm_w.dtype != f32 or not norm_w.is_contiguous()))
+            or qc != 1 or kc != 1 or vc != 1 or outc != 1 or zc != 1
+            or not (g.is_contiguous() and beta.is_contiguous() and state.is_contiguous())):
+        _refuse(1, "fak_gdn_attn")
+    d = batch.device
+    if (d < 0 or q.get_device() != d or k.get_device() != d or v.get_device() != d or g.get_device() != d
+            or beta.get_device() != d or state.get_device() != d or out.get_device() != d
+            or (z is not None and z.get_device() != d) or (norm_w is not None and norm_w.get_device() != d)
+            or _current_device() != d):
+        _refuse(8, "fak_gdn_attn")
+    args = _GDN_ARGS.pack(nk, nv, max_q, FAK_ROWS_F32 if kind == f32 else FAK_ROWS_BF16, ss[0],
+                          128 ** -0.5 if scale is None else scale, eps, rows, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh,
+                          kr, kh, vr, vh, g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+                          0 if norm_w is None else norm_w.data_ptr(), 0 if z is None else z.data_ptr(), zr, zh, out.data_ptr(),
+                          outr, outh)
+    _check(lib.fak_gdn_attn(batch.ref, args, _stream(stream)), "fak_gdn_attn")
 
 
 def fak_gdn_debug_wait(timeout_ns=0, unreachable=0):
@@ -592,22 +607,51 @@ def fak_residual_norm(h, y=None, n=None, w=None, post_norm=False, y_w=None, gate
                       eps=1e-6, gain_offset=0.0, stream=None):
     """h, y and n [rows, d], each f32 or bf16 (views with row strides are fine); gains w and y_w [d] f32; gate f32, of h's
     shape (expanded from one row, one column or one value too)."""
-    where, types, f32 = "fak_residual_norm", _float_types(), _float_types()[0]
-    if h.dim() != 2 or any(t is not None and t.shape != h.shape for t in (y, n, gate)):
-        raise FakError(2, where)
-    rows, d = h.shape
-    for t in (h, y, n):
-        if t is not None and (t.dtype not in types or (t.stride(1) != 1 and d > 1)):
-            raise FakError(1, where)
-    if gate is not None and (gate.dtype != f32 or (gate.stride(1) not in (0, 1) and d > 1)):
-        raise FakError(1, where)
-    kind = lambda t: FAK_ROWS_F32 if t is None or t.dtype == f32 else FAK_ROWS_BF16
-    row = lambda t: 0 if t is None else t.stride(0)
-    a = NormArgs(kind(h), kind(y), kind(n), d, int(post_norm), FAK_GATE_SIGMOID if gate_sigmoid else FAK_GATE_LINEAR, scale,
-                 eps, gain_offset, rows, _ptr(h), _ptr(y), _ptr(n), row(h), row(y), row(n), _gain(w, d, f32, where),
-                 _gain(y_w, d, f32, where), _ptr(gate), row(gate), 0 if gate is None or d == 1 else gate.stride(1))
-    _on_device(h.get_device(), (h, y, n, w, y_w, gate), where)
-    _check(lib.fak_residual_norm(ctypes.addressof(a), _stream(stream)), where)
+    f32, bf16, _ = _gdn_types()
+    shape, dev = h.shape, h.get_device()
+    if len(shape) != 2:
+        _refuse(2, "fak_residual_norm")
+    rows, d = shape
+    away = dev < 0 or _current_device() != dev  # (told last)
+    kinds, at, steps = [0, 0, 0], [0, 0, 0], [0, 0, 0]
+    for i, t in enumerate((h, y, n)):
+        if t is None:
+            continue
+        if t.shape != shape:
+            _refuse(2, "fak_residual_norm")
+        dtype, (row, col) = t.dtype, t.stride()
+        if (dtype != f32 and dtype != bf16) or (col != 1 and d > 1):
+            _refuse(1, "fak_residual_norm")
+        if t.get_device() != dev:
+            away = True
+        kinds[i], at[i], steps[i] = FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, t.data_ptr(), row
+    gains = [0, 0]
+    for i, t in enumerate((w, y_w)):
+        if t is None:
+            continue
+        if t.dtype != f32 or not t.is_contiguous():
+            _refuse(1, "fak_residual_norm")
+        if t.numel() != d:
+            _refuse(2, "fak_residual_norm")
+        if t.get_device() != dev:
+            away = True
+        gains[i] = t.data_ptr()
+    gp = gr = gc = 0
+    if gate is not None:
+        if gate.shape != shape:
+            _refuse(2, "fak_residual_norm")
+        gr, gc = gate.stride()
+        if gate.dtype != f32 or (gc != 0 and gc != 1 and d > 1):
+            _refuse(1, "fak_residual_norm")
+        if gate.get_device() != dev:
+            away = True
+        gp, gc = gate.data_ptr(), 0 if d == 1 else gc
+    if away:
+        _refuse(8, "fak_residual_norm")
+    args = _NORM_ARGS.pack(kinds[0], kinds[1], kinds[2], d, 1 if post_norm else 0, FAK_GATE_SIGMOID if gate_sigmoid else FAK_GATE_LINEAR,
+                           scale, eps, gain_offset, rows, at[0], at[1], at[2], steps[0], steps[1], steps[2], gains[0], gains[1],
+                           gp, gr, gc)
+    _check(lib.fak_residual_norm(args, _stream(stream)), "fak_residual_norm")
 
 
 # ------------------------------------------------------------------ decode context

@@ -100,26 +100,68 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = load4(p.conv_w + (ch + i) * 4);
 
-  auto emit = [&](int64_t row, const float4& x0, const float4& x1, const float4& x2, const float4& x3) {
+  auto taps = [&](const float4& x0, const float4& x1, const float4& x2, const float4& x3) {
     float4 c;
-    c.x = fmaf(w[0].w, x3.x, fmaf(w[0].z, x2.x, fmaf(w[0].y, x1.x, w[0].x * x0.x)));
-    c.y = fmaf(w[1].w, x3.y, fmaf(w[1].z, x2.y, fmaf(w[1].y, x1.y, w[1].x * x0.y)));
-    c.z = fmaf(w[2].w, x3.z, fmaf(w[2].z, x2.z, fmaf(w[2].y, x1.z, w[2].x * x0.z)));
-    c.w = fmaf(w[3].w, x3.w, fmaf(w[3].z, x2.w, fmaf(w[3].y, x1.w, w[3].x * x0.w)));
-    c.x = gdn_silu(c.x);
-    c.y = gdn_silu(c.y);
-    c.z = gdn_silu(c.z);
-    c.w = gdn_silu(c.w);
-    if (head >= 2 * p.nk) {
-      gdn_put4(p.v, true, (row * p.nv + head - 2 * p.nk) * kGdnDim + 4 * lane, c);
-      return;
-    }
-    const float r = rsqrtf(gdn_warp_sum(fmaf(c.x, c.x, fmaf(c.y, c.y, fmaf(c.z, c.z, c.w * c.w)))) + p.eps);
+    c.x = gdn_silu(fmaf(w[0].w, x3.x, fmaf(w[0].z, x2.x, fmaf(w[0].y, x1.x, w[0].x * x0.x))));
+    c.y = gdn_silu(fmaf(w[1].w, x3.y, fmaf(w[1].z, x2.y, fmaf(w[1].y, x1.y, w[1].x * x0.y))));
+    c.z = gdn_silu(fmaf(w[2].w, x3.z, fmaf(w[2].z, x2.z, fmaf(w[2].y, x1.z, w[2].x * x0.z))));
+    c.w = gdn_silu(fmaf(w[3].w, x3.w, fmaf(w[3].z, x2.w, fmaf(w[3].y, x1.w, w[3].x * x0.w))));
+    return c;
+  };
+  const bool value = head >= 2 * p.nk, key = head >= p.nk;
+  __half* unit = (key ? p.k : p.q) + (int64_t)(head - (key ? p.nk : 0)) * kGdnDim + 4 * lane;  // of row 0, of a query or key
+  auto put_unit = [&](int64_t row, const float4& c, float r) {
     const __half2 a = __floats2half2_rn(c.x * r, c.y * r), b = __floats2half2_rn(c.z * r, c.w * r);
-    const bool key = head >= p.nk;
-    *reinterpret_cast<uint2*>((key ? p.k : p.q) + (row * p.nk + head - (key ? p.nk : 0)) * kGdnDim + 4 * lane) =
+    *reinterpret_cast<uint2*>(unit + row * p.nk * kGdnDim) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   };
+  auto put_value = [&](int64_t row, const float4& c) {
+    gdn_put4(p.v, true, (row * p.nv + head - 2 * p.nk) * kGdnDim + 4 * lane, c);
+  };
+  auto emit = [&](int64_t row, const float4& x0, const float4& x1, const float4& x2, const float4& x3) {
+    const float4 c = taps(x0, x1, x2, x3);
+    if (value)
+      put_value(row, c);
+    else
+      put_unit(row, c, rsqrtf(gdn_warp_sum(fmaf(c.x, c.x, fmaf(c.y, c.y, fmaf(c.z, c.z, c.w * c.w)))) + p.eps));
+  };
+
+  if constexpr (R == 8) {
+    // rows in the midst of a sequence: all of them together
+    int s;
+    const KvSeq q = kv_locate(p.c, base, lane, s);
+    const GdnSeq e = gdn_seq(p.c, q, s);
+    if (__all_sync(0xffffffffu, e.ok && base >= e.first + 3 && base + R <= e.r1)) {
+      float4 c[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) c[i] = taps(in[i], in[i + 1], in[i + 2], in[i + 3]);
+      if (value) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) put_value(base + i, c[i]);
+        return;
+      }
+      // the rows' sums over the lanes: lanes 16, 8 and 4 apart each keep half of their rows and add the other's; then the
+      // four lanes that have the same row
+      float ss[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) ss[i] = fmaf(c[i].x, c[i].x, fmaf(c[i].y, c[i].y, fmaf(c[i].z, c[i].z, c[i].w * c[i].w)));
+#pragma unroll
+      for (int m = 4; m >= 1; m >>= 1) {
+        const bool high = lane & (4 * m);
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+          const float give = high ? ss[i] : ss[i + m];
+          ss[i] = (high ? ss[i + m] : ss[i]) + __shfl_xor_sync(0xffffffffu, give, 4 * m);
+        }
+      }
+      ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], 2);
+      ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], 1);
+      const float r = rsqrtf(ss[0] + p.eps);
+#pragma unroll
+      for (int i = 0; i < R; ++i) put_unit(base + i, c[i], __shfl_sync(0xffffffffu, r, 4 * i));
+      return;
+    }
+  }
 
   GdnSeq d{0, 0, 0, 0, false, false};
   int64_t known = -1;  // d is that of the rows below

@@ -204,7 +204,11 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (wide)
-    e = a->d <= 4096 ? launch<4, 1>(p, s) : a->d <= 8192 ? launch<4, 2>(p, s) : a->d <= 16384 ? launch<4, 4>(p, s) : launch<4, 8>(p, s);
+    e = a->rows >= 608 && a->d >= 1024 && a->d <= 16384 ? launch<4, 4>(p, s)
+        : a->d <= 4096                                   ? launch<4, 1>(p, s)
+        : a->d <= 8192                                   ? launch<4, 2>(p, s)
+        : a->d <= 16384                                  ? launch<4, 4>(p, s)
+                                                         : launch<4, 8>(p, s);
   else
     e = a->d <= 1024 ? launch<1, 1>(p, s) : a->d <= 8192 ? launch<1, 8>(p, s) : launch<1, 32>(p, s);
   return fak_cuda_status(e);
