@@ -58,7 +58,7 @@ FAK_DEV float4 load_row4(const T* p) {
 // it; of a sequence that begins in it, it takes the first three rows even behind its range.  So a sequence's old state
 // is read, and its new one written, by one block alone, the one that has its first row, and no other block waits.
 template <int R, bool WIDE, typename T>
-__global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_constant__ ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, R == 8 ? 3 : 4) gdn_conv_kernel(const __grid_constant__ ConvParams p) {
   const int lane = threadIdx.x & 31;
   const int head = blockIdx.y * kConvWarps + (threadIdx.x >> 5);
   const int heads = 2 * p.nk + p.nv;
@@ -89,12 +89,14 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
   const int64_t chans = (int64_t)heads * kGdnDim;
   const int64_t ch = (int64_t)head * kGdnDim + 4 * lane;
   const T* x = static_cast<const T*>(p.x) + ch;
-  // the rows from three before the range on, all asked for at once
-  float4 in[R + 3];
+  // the rows from three before the range on, all asked for at once (a single row: itself, which every way needs)
+  constexpr int kIn = R == 1 ? 1 : R + 3;
+  const bool inside = R == 1 || (base >= 3 && base + R <= p.c.rows);
+  float4 in[kIn];
+  if (inside) {
+    const T* at = x + (R == 1 ? base : base - 3) * p.x_row;
 #pragma unroll
-  for (int i = 0; i < R + 3; ++i) {
-    const int64_t row = base - 3 + i;
-    in[i] = row >= 0 && row < p.c.rows ? load_row4<WIDE>(x + row * p.x_row) : gdn_zero4();
+    for (int i = 0; i < kIn; ++i, at += p.x_row) in[i] = load_row4<WIDE>(at);
   }
   float4 w[4];  // of the lane's four channels: the taps, oldest first
 #pragma unroll
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
     int s;
     const KvSeq q = kv_locate(p.c, base, lane, s);
     const GdnSeq e = gdn_seq(p.c, q, s);
-    if (__all_sync(0xffffffffu, e.ok && base >= e.first + 3 && base + R <= e.r1)) {
+    if (__all_sync(0xffffffffu, inside && e.ok && base >= e.first + 3 && base + R <= e.r1)) {
       float4 c[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) c[i] = taps(in[i], in[i + 1], in[i + 2], in[i + 3]);
@@ -166,10 +168,8 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
   GdnSeq d{0, 0, 0, 0, false, false};
   int64_t known = -1;  // d is that of the rows below
   const bool tells = head == 0 && lane == 0;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int64_t row = base + i;
-    if (row >= end) break;
+#pragma unroll 1
+  for (int64_t row = base; row < end; ++row) {
     if (row >= known) {
       int s;
       KvSeq q = kv_locate(p.c, row, lane, s);
@@ -185,8 +185,10 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
     }
     if (!d.ok || row < d.first) continue;
     const int64_t at = row - d.first;
+    const T* here = x + row * p.x_row;
+    const float4 now = R == 1 ? in[0] : load_row4<WIDE>(here);
     if (at >= 3) {
-      emit(row, in[i], in[i + 1], in[i + 2], in[i + 3]);
+      emit(row, load_row4<WIDE>(here - 3 * p.x_row), load_row4<WIDE>(here - 2 * p.x_row), load_row4<WIDE>(here - p.x_row), now);
       continue;
     }
     if (at > 0) continue;  // taken with the first
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
       h2 = load4(st + 2 * chans);
     }
     const int n = d.r1 - d.first;
-    float4 y = in[i + 3];
+    float4 y = now;
     emit(row, h0, h1, h2, y);
     for (int j = 1; j < min(n, 3); ++j) {
       h0 = h1;
