@@ -429,8 +429,8 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
       (((uintptr_t)a->g | (uintptr_t)a->beta | (uintptr_t)a->z) & 3))
     return FAK_ERR_ALIGN;
   if (a->rows == 0 || batch->n_seqs == 0) return FAK_OK;
-  int dev = 0;
-  if ((st = kv_device(&dev, nullptr)) != FAK_OK) return st;
+  int dev = 0, sms = 0;
+  if ((st = kv_device(&dev, &sms)) != FAK_OK) return st;
   p.c.rows = a->rows;
   p.c.max_q = a->max_q;
   p.q = static_cast<const __half*>(a->q);
@@ -461,7 +461,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
   if (e != cudaSuccess) return fak_cuda_status(e);
   e = gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
-                       static_cast<int*>(status), dev, s);
+                       static_cast<int*>(status), dev, sms, s);
   const int st2 = fak_cuda_status(e);
   return e == cudaErrorMemoryAllocation ? FAK_ERR_NOMEM : st2;
 }

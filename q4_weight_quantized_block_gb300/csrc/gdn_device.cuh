@@ -79,4 +79,5 @@ FAK_DEV float gdn_warp_sum(float x) {
 }
 
 // Host: the launch of the chunks' kernel (gdn_chunk.cu).
-cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, cudaStream_t s);
+cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, int unreachable, int* status, int dev, int sms,
+                             cudaStream_t s);

@@ -138,6 +138,76 @@ def test_attn_split_prompt_goes_on(fak):
     assert float((o1 - o2).norm() / o1.norm()) < 1e-4
 
 
+def many(n, seed, most=200):
+    """Lengths of n sequences: tokens, short and long ones, some with no rows, some that go on, one padded."""
+    gen = torch.Generator().manual_seed(seed)
+    pick = lambda hi: int(torch.randint(hi, (1,), generator=gen))  # noqa: E731
+    out = []
+    for _ in range(n):
+        rows = (0, 1, 1 + pick(20), 1 + pick(most))[pick(4)]
+        out.append((rows, rows + (0 if pick(2) else pick(500))))
+    return out[:-1] + [(90, 70)]
+
+
+@pytest.mark.parametrize("n,nk,nv", [(40, 1, 4), (70, 2, 2), (150, 1, 1)])
+def test_attn_many_sequences(fak, n, nk, nv):
+    """More sequences than a warp looks over at a time, and more heads of them than go at once."""
+    attn_case(fak, many(n, n), nk, nv, seed=n)
+
+
+@pytest.mark.parametrize("nv", [5, 8, 11])
+def test_attn_many_heads_to_a_key_head(fak, nv):
+    attn_case(fak, [(130, 200), (70, 70), (3, 9)], 1, nv)
+
+
+@pytest.mark.parametrize("bad", [-5, 10 ** 6, 0])
+def test_attn_bad_starts_among_many(fak, bad):
+    """A start that is out of range takes its two sequences with it, wherever it stands; so does one that falls."""
+    lengths = [(n + 9, n + 9) for n, _ in many(39, 3)] + [(300, 300)]
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 3)
+    q, k, v, g, beta, z, w = G.inputs(1, 2, rows, 3)
+    state = torch.full((slots, 2, 128, 128), NAN, device="cuda")
+    old = start.tolist()
+    start[20] = bad
+    o = torch.full((rows, 2, 128), 7.0, device="cuda")
+    fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, state, o, 300, z=z, norm_w=w)
+    assert fak.fak_device_status() == 7
+    for s in range(40):
+        r = slice(old[s], old[s + 1])
+        if s == 19:  # ends before it begins, or behind the last row
+            assert bool((o[r] == 7).all()) and bool(state[slot[s]].isnan().all())
+        elif s != 20:
+            want, S, m = G.gdn_ref(*(t[r] for t in (q, k, v, g, beta)), torch.zeros_like(state[slot[s]]), 128 ** -0.5)
+            assert float((state[slot[s]].double() - S).abs().max()) <= 2.0 ** -20 * (r.stop - r.start) ** 0.5 * m
+    assert fak.fak_device_status() == 0
+
+
+def test_attn_more_chunks_than_a_launch_takes(fak):
+    """Records of 33,536 bytes a chunk and head: where all of them pass 1 GiB, a call goes over them in parts."""
+    lengths = [(19000, 19000), (2, 2), (13003, 20000)]
+    nk, nv = 4, 64
+    start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 4)
+    assert (rows // 64 + 3) * nv * 33536 > 1 << 30
+    q, k, v, g, beta, z, w = G.inputs(nk, nv, rows, 4)
+    s0 = torch.randn(slots, nv, 128, 128, device="cuda") * 0.3
+    a, oa = s0.clone(), torch.zeros(rows, nv, 128, device="cuda")
+    fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, a, oa, 19000)
+    b, ob = s0.clone(), torch.zeros_like(oa)
+    for i, (n, t) in enumerate(lengths):  # one sequence at a time
+        r = slice(int(start[i]), int(start[i + 1]))
+        one = fak.GDNBatch(torch.tensor([0, n], dtype=torch.int32, device="cuda"), kv_len[i:i + 1], slot[i:i + 1])
+        fak.fak_gdn_attn(one, q[r], k[r], v[r], g[r], beta[r], b, ob[r], n)
+    assert fak.fak_device_status() == 0
+    # each is off by the tests' tolerance at most; a column's length is at least what it is at the end, values are 9 at most
+    for i, (n, _) in enumerate(lengths):
+        r = slice(int(start[i]), int(start[i + 1]))
+        tol = 2 * 2.0 ** -20 * n ** 0.5 * max(float(b[slot[i]].norm(dim=1).max()), float(v[r].abs().max()))
+        assert float((a[slot[i]] - b[slot[i]]).abs().max()) <= tol
+        assert float((oa[r] - ob[r]).abs().max()) <= tol * 128 ** -0.5 + 2.0 ** -23 * float(ob[r].abs().max())
+    rest = [i for i in range(slots) if i not in slot.tolist()]
+    assert torch.equal(a[rest], s0[rest])
+
+
 def test_attn_bad_values_stay_in_their_sequence(fak):
     """Infinities and NaN in one sequence's rows and in the rows of no sequence reach no other sequence."""
     lengths = [(70, 70), (70, 75), (1, 4), (70, 70), (1, 2)]
