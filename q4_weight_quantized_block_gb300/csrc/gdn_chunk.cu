@@ -1004,29 +1004,31 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
-  // Rows 16 m .. of K K^T (m = w) and of Q K^T (m = 3 - w), ten tiles of 8 columns to a warp
-  float kk[8][4] = {}, qk[8][4] = {};
-  const int mk = w, mq = 3 - w;
+  // Of K K^T and Q K^T, 16 rows by 16 columns at a time, on and below the diagonal: rows 16 w .. of the first (parts 0 .. w) and
+  // 16 (3 - w) .. of the second (parts w + 1 .. 4), five to a warp.
+  float x[5][8] = {};
+  auto place = [&](int i, int& m, int& tile, int& j) {  // part i: product, rows, columns
+    m = i > w;
+    tile = m ? 3 - w : w;
+    j = m ? i - w - 1 : i;
+  };
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
     uint32_t ak[4], aq[4];
-    ldsm4(ak, at(16 * mk + (lane & 15), 2 * k + (lane >> 4)));
-    ldsm4(aq, at(64 + 16 * mq + (lane & 15), 2 * k + (lane >> 4)));
+    ldsm4(ak, at(16 * w + (lane & 15), 2 * k + (lane >> 4)));
+    ldsm4(aq, at(64 + 16 * (3 - w) + (lane & 15), 2 * k + (lane >> 4)));
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {  // rows 8 j .. +15 of K: two tiles
-      if (j > 2 * max(mk, mq)) continue;
-      uint32_t b[4];
-      ldsm4(b, at(8 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+    for (int i = 0; i < 5; ++i) {
+      int m, tile, j;
+      place(i, m, tile, j);
+      uint32_t b[4], a[4];
+      ldsm4(b, at(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u] = m ? aq[u] : ak[u];
       const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
-      if (j <= 2 * mk) {
-        mma16(kk[j], ak, b0);
-        mma16(kk[j + 1], ak, b1);
-      }
-      if (j <= 2 * mq) {
-        mma16(qk[j], aq, b0);
-        mma16(qk[j + 1], aq, b1);
-      }
+      mma16(*reinterpret_cast<float(*)[4]>(x[i]), a, b0);
+      mma16(*reinterpret_cast<float(*)[4]>(x[i] + 4), a, b1);
     }
   }
 
@@ -1102,47 +1104,44 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       // A and P from K K^T and Q K^T by the decays, to the places of T and P T: within the rows' own 16 columns one exponential
       // each, before them by way of the last row before the 16
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int tile = m ? mq : mk, row = 16 * tile + g;
+      for (int i = 0; i < 5; ++i) {
+        int m, tile, j;
+        place(i, m, tile, j);
+        const int row = 16 * tile + g;
         const float b0 = m ? 1.0f : beta[row], b1 = m ? 1.0f : beta[row + 8];
-        const float f0 = b0 * hi[3 * kRows + row], f1 = b1 * hi[3 * kRows + row + 8];
-        const float* upto = hi + (3 + tile) * kRows;
+        float y[2][4];
+        if (j < tile) {
+          const float f0 = b0 * hi[3 * kRows + row], f1 = b1 * hi[3 * kRows + row + 8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          if (j > 2 * tile) continue;
-          float y[2][4];
-          if (j < 2 * tile) {
+          for (int e = 0; e < 2; ++e) {
+            const float2 u = *reinterpret_cast<const float2*>(hi + (3 + tile) * kRows + 16 * j + 8 * e + q2);
+            const float* z = x[i] + 4 * e;
+            const float2 top = mul2(mul2(u, both(f0)), make_float2(z[0], z[1])), low = mul2(mul2(u, both(f1)), make_float2(z[2], z[3]));
+            y[e][0] = top.x;
+            y[e][1] = top.y;
+            y[e][2] = low.x;
+            y[e][3] = low.y;
+          }
+        } else {
+          const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
+          const int last = m ? g : g - 1;  // of row g's own 16 columns; row g + 8's: 8 more
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 u = *reinterpret_cast<const float2*>(upto + 8 * (j + e) + q2);
-              const float* x = m ? qk[j + e] : kk[j + e];
-              const float2 top = mul2(mul2(u, both(f0)), make_float2(x[0], x[1])), low = mul2(mul2(u, both(f1)), make_float2(x[2], x[3]));
-              y[e][0] = top.x;
-              y[e][1] = top.y;
-              y[e][2] = low.x;
-              y[e][3] = low.y;
-            }
-          } else {
-            const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
-            const int last = m ? g : g - 1;  // of row g's own 16 columns; row g + 8's: 8 more
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int at = 8 * e + q2, col = 8 * j + at;
-              const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
-              const float* x = m ? qk[j + e] : kk[j + e];
-              // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
-              y[e][0] = at <= last ? b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * x[0] : 0.0f;
-              y[e][1] = at + 1 <= last ? b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * x[1] : 0.0f;
-              y[e][2] = at <= last + 8 ? b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * x[2] : 0.0f;
-              y[e][3] = at + 1 <= last + 8 ? b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * x[3] : 0.0f;
-              if (!m) {
-                *reinterpret_cast<float2*>(diag + row * kLd + at) = make_float2(y[e][0], y[e][1]);
-                *reinterpret_cast<float2*>(diag + (row + 8) * kLd + at) = make_float2(y[e][2], y[e][3]);
-              }
+          for (int e = 0; e < 2; ++e) {
+            const int at = 8 * e + q2, col = 16 * j + at;
+            const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
+            const float* z = x[i] + 4 * e;
+            // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
+            y[e][0] = at <= last ? b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * z[0] : 0.0f;
+            y[e][1] = at + 1 <= last ? b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * z[1] : 0.0f;
+            y[e][2] = at <= last + 8 ? b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * z[2] : 0.0f;
+            y[e][3] = at + 1 <= last + 8 ? b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * z[3] : 0.0f;
+            if (!m) {
+              *reinterpret_cast<float2*>(diag + row * kLd + at) = make_float2(y[e][0], y[e][1]);
+              *reinterpret_cast<float2*>(diag + (row + 8) * kLd + at) = make_float2(y[e][2], y[e][3]);
             }
           }
-          put_tiles(tps, m * kRows + 16 * tile, j, y[0], y[1], 1.0f, lane);
         }
+        put_tiles(tps, m * kRows + 16 * tile, 2 * j, y[0], y[1], 1.0f, lane);
       }
       __syncthreads();
       {
