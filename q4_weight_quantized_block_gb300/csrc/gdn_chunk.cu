@@ -1001,41 +1001,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
-
   // Of K K^T and Q K^T, 16 rows by 16 columns at a time, on and below the diagonal: rows 16 w .. of the first (parts 0 .. w) and
   // 16 (3 - w) .. of the second (parts w + 1 .. 4), five to a warp.
-  float x[5][8] = {};
+  float dots[5][8] = {};
   auto place = [&](int i, int& m, int& tile, int& j) {  // part i: product, rows, columns
     m = i > w;
     tile = m ? 3 - w : w;
     j = m ? i - w - 1 : i;
   };
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
-    uint32_t ak[4], aq[4];
-    ldsm4(ak, at(16 * w + (lane & 15), 2 * k + (lane >> 4)));
-    ldsm4(aq, at(64 + 16 * (3 - w) + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      int m, tile, j;
-      place(i, m, tile, j);
-      uint32_t b[4], a[4];
-      ldsm4(b, at(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) a[u] = m ? aq[u] : ak[u];
-      const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
-      mma16(*reinterpret_cast<float(*)[4]>(x[i]), a, b0);
-      mma16(*reinterpret_cast<float(*)[4]>(x[i] + 4), a, b1);
-    }
-  }
-
-  __syncthreads();
-  // T and P T are zero above their blocks on the diagonal, which nothing writes
-  for (int i = threadIdx.x; i < 2 * kPart / 16; i += kPrepThreads) *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(0, 0, 0, 0);
-
   for (int h0 = 0; h0 < p.group; h0 += 4) {
     const int heads = min(4, p.group - h0);
     if (w < heads) {
@@ -1096,6 +1069,32 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
           make_float2(exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
       *reinterpret_cast<float2*>(record + 8 * kRows) = make_float2(b[0], b[1]);
     }
+    if (h0 == 0) {  // (the gates come while K and Q do)
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
+        uint32_t ak[4], aq[4];
+        ldsm4(ak, at(16 * w + (lane & 15), 2 * k + (lane >> 4)));
+        ldsm4(aq, at(64 + 16 * (3 - w) + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          int m, tile, j;
+          place(i, m, tile, j);
+          uint32_t b[4], a[4];
+          ldsm4(b, at(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) a[u] = m ? aq[u] : ak[u];
+          const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
+          mma16(*reinterpret_cast<float(*)[4]>(dots[i]), a, b0);
+          mma16(*reinterpret_cast<float(*)[4]>(dots[i] + 4), a, b1);
+        }
+      }
+      __syncthreads();
+      // T and P T are zero above their blocks on the diagonal, which nothing writes
+      for (int i = threadIdx.x; i < 2 * kPart / 16; i += kPrepThreads) *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
     for (int hh = 0; hh < heads; ++hh) {
       const int h = hk * p.group + h0 + hh;
@@ -1115,7 +1114,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 u = *reinterpret_cast<const float2*>(hi + (3 + tile) * kRows + 16 * j + 8 * e + q2);
-            const float* z = x[i] + 4 * e;
+            const float* z = dots[i] + 4 * e;
             const float2 top = mul2(mul2(u, both(f0)), make_float2(z[0], z[1])), low = mul2(mul2(u, both(f1)), make_float2(z[2], z[3]));
             y[e][0] = top.x;
             y[e][1] = top.y;
@@ -1129,7 +1128,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
           for (int e = 0; e < 2; ++e) {
             const int at = 8 * e + q2, col = 16 * j + at;
             const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
-            const float* z = x[i] + 4 * e;
+            const float* z = dots[i] + 4 * e;
             // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
             y[e][0] = at <= last ? b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * z[0] : 0.0f;
             y[e][1] = at + 1 <= last ? b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * z[1] : 0.0f;
