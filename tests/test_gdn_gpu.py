@@ -155,6 +155,14 @@ def test_attn_many_sequences(fak, n, nk, nv):
     attn_case(fak, many(n, n), nk, nv, seed=n)
 
 
+@pytest.mark.parametrize("wild", [False, True])
+def test_attn_from_rows_to_chunks(fak, wild):
+    """On both sides of the length from which a sequence goes over chunks; alone, the rows of the call decide."""
+    attn_case(fak, [(28, 28), (29, 29), (27, 400), (30, 100), (1, 1)], 2, 4, wild=wild)
+    for n in (28, 29):
+        attn_case(fak, [(n, n + 5)], 1, 2, wild=wild, pad_rows=0, max_q=5000)
+
+
 @pytest.mark.parametrize("nv", [5, 8, 11])
 def test_attn_many_heads_to_a_key_head(fak, nv):
     attn_case(fak, [(130, 200), (70, 70), (3, 9)], 1, nv)
