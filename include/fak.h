@@ -572,7 +572,7 @@ int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable);
  * A ragged batch, in device memory, read when the kernels run.  Rows and positions as in
  * fak_kv_batch: rows row_start[s] .. row_start[s+1]-1 are sequence s's, the last of its
  * kv_len[s] positions; rows at negative positions are padding, rows from row_start[n_seqs]
- * on belong to no sequence.  A sequence whose first new row stands at position 0 begins
+ * on belong to no sequence, and no row to two (starts rise).  A sequence whose first new row stands at position 0 begins
  * with an empty state (what its slot holds is not read); any other goes on with its
  * slot's.  Its slot is left with the state behind its last row; a sequence without new
  * rows leaves its slot as it was.  Two sequences of one call in one slot race.  A sequence
@@ -614,9 +614,12 @@ int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_strea
  *   if norm_w: o = o / sqrt(mean o^2 + eps) * norm_w;  if z: o = o * silu(z).
  * Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and 0 <= beta <= 2, g <= 0: beyond
  * that the rule itself grows without bound, and a result may be an infinity or NaN before its f32 form is.
- * State, products with it and sums are f32 (of prompts: products of 22 significand bits, sums of f32); out is
- * rounded once.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds reaches
- * its own sequence alone.  Deterministic. */
+ * State, products with it and sums are f32; out is rounded once.  Sequences of more than 28 rows go over chunks of 64, on
+ * the tensor cores, with products of 22 significand bits and f32 sums; what they need besides, 33,536 bytes for 64 rows of a
+ * head, comes from the library-owned pool of the batched GEMV's scratch, freed on the same stream (kept for later calls; a
+ * graph memory node under stream capture): at most 1 GiB (or one chunk of every sequence) at a time, longer calls go in parts.
+ * FAK_ERR_NOMEM if it cannot be had.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds
+ * reaches its own sequence alone (where it is no number, up to 63 rows before it too).  Deterministic. */
 typedef struct {
     int32_t nk, nv;             /* key heads, value heads, nv a multiple of nk */
     int32_t max_q;              /* bound on the sequences' rows; a sequence above it is left out, recorded */

@@ -9,26 +9,35 @@
 // depend on no state: a first kernel makes them for all chunks and heads (a record of 33 KB each, in a scratch), the second
 // goes through a sequence's chunks.
 //
-// Precision.  The state is held in f32 registers, and its products keep 22 bits: the f32 operand goes as the sum of two
-// f16, the other one is f16 already (q, k) or two f16 too (T; the small parts' product is left out).  (Where the output is
-// bf16, what only it takes goes by its first part alone, off by 2^-12.)  f16's exponents take them because a value column's
-// S, R and U are scaled by one power of two.  With m the largest of the column's |S| and |V|, lengths of k of at most 1 and
-// 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m of the chunk before (by
-// which time it is known), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what f16 drops is below 2^-25, so 2^-23 m.  T
-// and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and kept as two f32, so that
-// decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
+// Precision.  The state is held in f32 registers, and products keep 22 bits: the f32 operand goes as the sum of two
+// f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents take
+// them because a value column's S, R and U are scaled by one power of two.  With m the largest of the column's |S| and |V|,
+// lengths of k of at most 1 and 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m
+// of the chunk before (by which time it is known), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what f16 drops is below
+// 2^-25, so 2^-23 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and kept as
+// two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
 //
 // First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps: decays into A
 // and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T, in place of A and P, by m16n8k16
-// instructions.
+// instructions.  Steps that wait for one another on 64 x 64 matrices: 104 us for 128 chunks of 48 heads on 16 key heads, of which
+// the records' 206 MB are 30 us; four blocks to an SM hide part of it (issue slots 31 %, tensor pipe 13 % busy).
 //
-// Second kernel: a warp holds 16 value columns of one head of one sequence, as S^T in the accumulators of m16n8k16 (64
+// Second kernel: two CTAs to a head, 64 value columns each; a warp holds 16 columns, as S^T in the accumulators of m16n8k16 (64
 // registers a thread).  Those are laid out as the next product's first operand is, so that S^T, R^T and U^T go from product
-// to product in registers: S^T K^T, S^T Q^T, R^T T^T, R^T (P T)^T, U^T K.  No warp waits for another but through the copies
-// of K, Q, V, z and the records, which one more warp makes, and for the norm's sums of squares, a chunk later.  400
-// instructions of 8 cycles each a chunk and warp: 3,200 cycles, at one warp to a scheduler.
-// (The same products by tcgen05, 64 columns to a CTA, took 6,200 cycles a chunk: 128 rows of S, R or U go through shared
-// memory for each of three products that wait for one another, some 700 cycles for a product and as many for its operand.)
+// to product in registers: S^T K^T, R^T T^T, U^T K.  A second warp to the same columns takes S^T and R^T as operands from shared
+// memory and makes what only the output wants: S^T Q^T, R^T (P T)^T, the norm (its sums of squares from all eight such warps of
+// the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  316
+// instructions of 8 cycles of the tensor cores for the state and 188 for the output, 4,032 cycles a chunk on each of an SM's four
+// parts; a chunk takes 6,100 (3.2 us): one warp's way through three products, the splitting into f16 and the scales, and shared
+// memory, whose operands a warp of 16 columns takes for itself alone (fragments 60 % of its cycles).
+//
+// What did not help: the same products by tcgen05, 64 columns to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through
+// shared memory for each of three products that wait for one another, some 700 cycles for a product and as many for its operand);
+// one CTA to a head with eight warps that make their outputs too (12,700 for both halves of a head); two warps to the same
+// columns, each with half of the keys and rows (6,400 to 7,000: what they exchange fills shared memory); several sequences'
+// heads one behind the other in a CTA, split evenly (a chunk 7 % longer); records without the zeros above the diagonal (fewer
+// bytes, yet 7 % more time of the second kernel for one prompt); records of the next 32 chunks beside the chunks of these (3 %
+// less for one prompt of 8,192, at the price of the kernel twice).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
