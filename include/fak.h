@@ -617,8 +617,8 @@ int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_strea
  * State, products with it and sums are f32; out is rounded once.  Sequences of more than 28 rows go over chunks of 64, on
  * the tensor cores, with products of 22 significand bits and f32 sums; what they need besides, 33,536 bytes for 64 rows of a
  * head, comes from the library-owned pool of the batched GEMV's scratch, freed on the same stream (kept for later calls; a
- * graph memory node under stream capture): at most 1 GiB (or one chunk of every sequence) at a time, longer calls go in parts.
- * FAK_ERR_NOMEM if it cannot be had.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds
+ * graph memory node under stream capture): at most 1 GiB at a time (or one chunk's of all heads), longer calls go in parts.
+ * FAK_ERR_NOMEM, and nothing done, if it cannot be had.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds
  * reaches its own sequence alone (where it is no number, up to 63 rows before it too).  Deterministic. */
 typedef struct {
     int32_t nk, nv;             /* key heads, value heads, nv a multiple of nk */

@@ -21,9 +21,6 @@ __device__ int g_gdn_status;
 constexpr unsigned long long kGdnTimeout = 2000000000ull;
 std::atomic<unsigned long long> g_gdn_timeout{kGdnTimeout};
 std::atomic<int> g_gdn_unreachable{0};
-// Most rows of a sequence that goes row by row.  48 heads of one sequence take 8.3 us for 6 rows and 24.6 for 24 that way, and 27.3
-// by chunks of 64, however many of the 64 there are; of 16 sequences 33, 103 and 130 us, of 64 131, 373 and 450.
-constexpr int kFew = 28;
 
 FAK_DEV void gdn_record() { atomicCAS(&g_gdn_status, 0, FAK_ERR_DEVICE); }
 
@@ -452,21 +449,21 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   p.group = a->nv / a->nk;
   p.out_bf16 = a->out_type == FAK_ROWS_BF16;
   cudaStream_t s = (cudaStream_t)stream;
-  // Sequences of more than kFew rows go over chunks of 64, the others row by row.
-  const bool few = std::min<int64_t>(a->max_q, a->rows) <= kFew;
-  if (few || batch->n_seqs > 1) {
-    p.few = kFew;
-    gdn_step_kernel<<<(unsigned)(batch->n_seqs * a->nv), kStepThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || few) return fak_cuda_status(e);
+  // Sequences of more than kGdnFew rows go over chunks of 64, the others row by row.  (The chunks first: where their scratch
+  // cannot be had, nothing is launched.)
+  const bool few = std::min<int64_t>(a->max_q, a->rows) <= kGdnFew;
+  if (few || batch->n_seqs > 1) p.few = kGdnFew;
+  if (!few) {
+    void* status = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
+    if (e != cudaSuccess) return fak_cuda_status(e);
+    e = gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
+                         static_cast<int*>(status), dev, sms, s);
+    st = fak_cuda_status(e);
+    if (e != cudaSuccess) return e == cudaErrorMemoryAllocation ? FAK_ERR_NOMEM : st;
   }
-  void* status = nullptr;
-  cudaError_t e = cudaGetSymbolAddress(&status, g_gdn_status);
-  if (e != cudaSuccess) return fak_cuda_status(e);
-  e = gdn_chunk_launch(p, g_gdn_timeout.load(std::memory_order_relaxed), g_gdn_unreachable.load(std::memory_order_relaxed),
-                       static_cast<int*>(status), dev, sms, s);
-  const int st2 = fak_cuda_status(e);
-  return e == cudaErrorMemoryAllocation ? FAK_ERR_NOMEM : st2;
+  if (p.few) gdn_step_kernel<<<(unsigned)(batch->n_seqs * a->nv), kStepThreads, 0, s>>>(p);
+  return fak_cuda_status(cudaGetLastError());
 }
 
 extern "C" int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable) {

@@ -73,23 +73,32 @@ struct Decays {
 constexpr int kRecord = 2 * kPart + (int)sizeof(Decays);
 static_assert(kRecord % 16 == 0, "bulk copies");
 
-// Where records stand.  dense: chunk c of a sequence s, begin <= c < begin + length, at s * length + c - begin; else chunk c at
-// r0 / 64 + s + c, r0 being the sequence's first row (such starts rise by at least the sequences' numbers of chunks).
+// Where records stand.  dense: chunk c of a sequence s, begin <= c < begin + length, at s * length + c - begin.  Else a sequence
+// has its place behind those before it, chunk c at place + c, of which begin .. begin + length are there.  The place is told by
+// the sequence's first row r0 (and by the sequences before it): r0 / 64 + s, or, where there are more sequences than rows make
+// such chunks, r0 / kGdnFew, which rises by at least its chunks over a sequence of more than that many rows (no others have
+// records).
 // order: the sequences, those of many chunks first; null where all go at once.
 struct Records {
   unsigned char* at;
-  int begin, length, dense;
+  int begin, length;
+  bool dense, by_row;
   int* order;
 };
+static_assert(kGdnFew <= 32, "a chunk and a row take two places");
 
-// Chunks of a sequence in this launch.
-FAK_DEV int chunks_of(const GdnParams& p, const Records& r, const GdnSeq& d) {
-  const int rows = d.r1 - d.first;
-  return !d.ok || (p.few && rows <= p.few) ? 0 : max(0, min((rows + kRows - 1) / kRows - r.begin, r.length));
-}
+FAK_DEV int place_of(const Records& r, int r0, int s) { return r.by_row ? r0 / kGdnFew : r0 / kRows + s; }
 
 FAK_DEV int64_t record_of(const Records& r, const GdnSeq& d, int s, int c) {
-  return r.dense ? (int64_t)s * r.length + (c - r.begin) : (int64_t)(d.r0 / kRows) + s + c;
+  return r.dense ? (int64_t)s * r.length + (c - r.begin) : (int64_t)place_of(r, d.r0, s) + c - r.begin;
+}
+
+// A sequence's chunks in this launch.
+FAK_DEV void chunks_of(const GdnParams& p, const Records& r, const GdnSeq& d, int s, int& begin, int& end) {
+  const int rows = d.r1 - d.first;
+  const int from = r.dense ? r.begin : r.begin - place_of(r, d.r0, s);
+  begin = max(from, 0);
+  end = !d.ok || (p.few && rows <= p.few) ? 0 : min((rows + kRows - 1) / kRows, from + r.length);
 }
 
 // Of the second kernel: NW warps of 16 columns, as many for their output, and the copies'.
@@ -340,8 +349,9 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
   const int rows = d.r1 - d.first;
   if (p.few && rows <= p.few) return;  // the steps' kernel's
   const int col0 = slice * C::cols;
-  const int begin = records.begin, end = min((rows + kRows - 1) / kRows, begin + records.length);  // this launch's chunks
-  if (begin == 0)
+  int begin, end;
+  chunks_of(p, records, d, s, begin, end);
+  if (records.begin == 0)
     for (int i = threadIdx.x; i < (d.first - d.r0) * (C::cols / 4); i += C::threads) {
       const int row = d.r0 + i / (C::cols / 4);
       gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (C::cols / 4)), gdn_zero4());
@@ -782,6 +792,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
     // A barrier takes a copy's bytes only when it is done with the copy before: after a wait that gave up no copy is issued,
     // and those that were are waited for before the block ends.
     const int hk = h / p.group;
+    const unsigned char* record0 = records.at + (record_of(records, d, s, begin) * p.nv + h) * kRecord;
     int copied = 0, gates = 0;  // chunks of which all but z, and of which z, was asked for
     auto load = [&](int c) {
       if (c >= 2) wait(kFree0 + (c & 1), (c - 2) >> 1);
@@ -801,7 +812,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < C::cols / 64; ++i)
           tma_load_3d_tx(smem + C::off_v + i * kRows * 128, &maps.v, col0 + 64 * i, h, row, land);  // (the last chunk's is in registers)
-        const unsigned char* record = records.at + (record_of(records, d, s, begin + c) * p.nv + h) * kRecord;
+        const unsigned char* record = record0 + (int64_t)c * p.nv * kRecord;
         bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
         bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
       }
@@ -911,23 +922,23 @@ constexpr int kOffDiag = 2 * kPart, kOffHi = kOffDiag + 4 * 16 * kLd * 4, kHeadD
 constexpr int kPrepSmem = kOffHi + 4 * kHeadDecays * 4 + 1024;
 
 // The sequence and chunk whose record is x, the whole warp: false where there is none.
-FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int64_t x, int lane, GdnSeq& d, int& s, int& c) {
+FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int x, int lane, GdnSeq& d, int& s, int& c) {
   auto has = [&](int i, GdnSeq& e) {  // sequence i's chunk at x, or -1
     e = gdn_seq(p.c, kv_seq(p.c, i), i);
     const int rows = e.r1 - e.first;
     if (!e.ok || rows == 0 || (p.few && rows <= p.few)) return -1;
-    const int64_t at = x - (r.dense ? (int64_t)i * r.length - r.begin : (int64_t)(e.r0 / kRows) + i);
-    return at < r.begin || at >= r.begin + r.length || at * kRows >= rows ? -1 : (int)at;
+    const int at = x + r.begin - (r.dense ? i * r.length : place_of(r, e.r0, i));
+    return at < 0 || (r.dense && (at < r.begin || at >= r.begin + r.length)) || (int64_t)at * kRows >= rows ? -1 : at;
   };
   if (r.dense) {
-    s = (int)(x / r.length);
+    s = x / r.length;
     return (c = has(s, d)) >= 0;
   }
   // where the starts rise, 32 probes a round
   int lo = 0, hi = p.c.n_seqs;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const unsigned b = __ballot_sync(0xffffffffu, i < hi && (int64_t)(p.c.row_start[i] / kRows) + i <= x);
+    const unsigned b = __ballot_sync(0xffffffffu, i < hi && place_of(r, p.c.row_start[i], i) <= x + r.begin);
     const int n = __popc(b);
     if (n > 1) lo += (n - 1) * step;
     hi = min(lo + step, hi);
@@ -959,10 +970,15 @@ FAK_DEV int class_of(int n) {
 // The order of the sequences, by one block: those of the highest classes first.  (CTAs start in that order, and those that start
 // last are the shortest: 16 prompts of 1 to 2,048 rows and 16 heads take 305 us, in the batch's order 332.)
 FAK_DEV void make_order(const GdnParams& p, const Records& r, int* count) {
+  auto of = [&](int i) {
+    int begin, end;
+    chunks_of(p, r, gdn_seq(p.c, kv_seq(p.c, i), i), i, begin, end);
+    return class_of(max(end - begin, 0));
+  };
   for (int i = threadIdx.x; i < kClasses; i += kPrepThreads) count[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < p.c.n_seqs; i += kPrepThreads)
-    atomicAdd(&count[class_of(chunks_of(p, r, gdn_seq(p.c, kv_seq(p.c, i), i)))], 1);
+    atomicAdd(&count[of(i)], 1);
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = kClasses - 1, sum = 0; i >= 0; --i) {
@@ -972,7 +988,7 @@ FAK_DEV void make_order(const GdnParams& p, const Records& r, int* count) {
     }
   __syncthreads();
   for (int i = threadIdx.x; i < p.c.n_seqs; i += kPrepThreads)
-    r.order[atomicAdd(&count[class_of(chunks_of(p, r, gdn_seq(p.c, kv_seq(p.c, i), i)))], 1)] = i;
+    r.order[atomicAdd(&count[of(i)], 1)] = i;
 }
 
 // Block (x, h): record x, key head h; one more block for the order.
@@ -1346,16 +1362,20 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
                                p.nv, p.out_row, p.out_head)))
     return cudaErrorInvalidValue;
   const ChunkDebug dbg{timeout_ns, unreachable};
-  // records of all chunks, where they are few enough; else of a stretch of every sequence at a time
-  const int longest = (int)((std::min<int64_t>(p.c.max_q, p.c.rows) + kRows - 1) / kRows);
-  const int64_t head = (int64_t)p.nv * kRecord, all = (p.c.rows / kRows + p.c.n_seqs) * head;
-  Records records{nullptr, 0, longest, 0, nullptr};
-  int64_t bytes = all;
-  if (all > kScratch) {
-    records.dense = 1;
-    records.length = (int)std::min<int64_t>(longest, std::max<int64_t>(1, kScratch / (p.c.n_seqs * head)));
-    bytes = (int64_t)p.c.n_seqs * records.length * head;
+  // Records of all chunks, where they are few enough; else of a stretch of every sequence at a time, or, where that would be short
+  // (below 16 chunks), of a stretch of all places.
+  const int64_t longest = (std::min<int64_t>(p.c.max_q, p.c.rows) + kRows - 1) / kRows, head = (int64_t)p.nv * kRecord;
+  const int64_t by_seq = p.c.rows / kRows + p.c.n_seqs, by_row = p.few ? p.c.rows / kGdnFew + 1 : by_seq;
+  const int64_t places = std::min(by_seq, by_row), most = std::max<int64_t>(1, kScratch / head);
+  Records records{nullptr, 0, (int)std::min(places, most), false, by_row < by_seq, nullptr};
+  int64_t slots = records.length, all = places;  // records of a launch; what begin goes up to
+  if (places > most && most / p.c.n_seqs >= 16) {
+    records.dense = true;
+    records.length = (int)std::min(longest, most / p.c.n_seqs);
+    slots = p.c.n_seqs * (int64_t)records.length;
+    all = longest;
   }
+  const int64_t bytes = slots * head;
   void* scratch = nullptr;
   const bool ordered = p.c.n_seqs > 1 && (int64_t)p.c.n_seqs * p.nv * C::slices > sms;
   e = fak_scratch_alloc(&scratch, (size_t)bytes + (ordered ? 4 * (size_t)p.c.n_seqs : 0), s);
@@ -1364,8 +1384,7 @@ cudaError_t gdn_chunk_launch(const GdnParams& p, unsigned long long timeout_ns, 
   if (ordered) records.order = reinterpret_cast<int*>(records.at + bytes);
   static std::atomic<uint64_t> done{0};
   e = kv_smem_limit(gdn_prepare_kernel, kPrepSmem, dev, done);
-  for (; e == cudaSuccess && records.begin < longest; records.begin += records.length) {
-    const int64_t slots = records.dense ? (int64_t)p.c.n_seqs * records.length : p.c.rows / kRows + p.c.n_seqs;
+  for (; e == cudaSuccess && records.begin < all; records.begin += records.length) {
     gdn_prepare_kernel<<<dim3((unsigned)(slots + ordered), (unsigned)nk), kPrepThreads, kPrepSmem, s>>>(p, records, (int)slots);
     e = cudaGetLastError();
     if (e == cudaSuccess) e = p.out_bf16 ? launch<false>(p, maps, records, dbg, status, dev, s) : launch<true>(p, maps, records, dbg, status, dev, s);

@@ -190,9 +190,13 @@ def test_attn_bad_starts_among_many(fak, bad):
     assert fak.fak_device_status() == 0
 
 
-def test_attn_more_chunks_than_a_launch_takes(fak):
-    """Records of 33,536 bytes a chunk and head: where all of them pass 1 GiB, a call goes over them in parts."""
+@pytest.mark.parametrize("name", ["few sequences", "many sequences"])
+def test_attn_more_chunks_than_a_launch_takes(fak, name):
+    """Records of 33,536 bytes a chunk and head: where all of them pass 1 GiB, a call goes over them in parts, of every
+    sequence, or, where these would be short, of the batch."""
     lengths = [(19000, 19000), (2, 2), (13003, 20000)]
+    if name == "many sequences":
+        lengths = [(600 + 37 * i % 301, (i % 3) * 1000 + 901) for i in range(38)] + [(1, 50), (30, 30), (4000, 4000)]
     nk, nv = 4, 64
     start, kv_len, slot, rows, slots = G.batch_tensors(lengths, 4)
     assert (rows // 64 + 3) * nv * 33536 > 1 << 30
