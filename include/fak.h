@@ -641,9 +641,9 @@ typedef struct {
 } fak_gdn_args;
 int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* args, fak_stream_t stream);
 
-/* Every wait of its kernels is bounded (2 s); one that runs out records FAK_ERR_TIMEOUT, and its head's results and state
- * are not written from there on.  Test hooks, for all later calls of the process: the limit in nanoseconds (0: the
- * default), and with unreachable = 1 waits that can never complete. */
+/* Every wait of its kernels is bounded (2 s); one that runs out records FAK_ERR_TIMEOUT, and the call's results and states
+ * are then not to be used.  Test hooks, for all later calls of the process: the limit in nanoseconds (0: the default), and
+ * with unreachable = 1 waits that can never complete. */
 int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable);
 
 /* ------------------------------------------------------------------ norms around a block

@@ -94,6 +94,12 @@ def test_strides_of_single_rows_and_heads_are_not_looked_at(fak):
     assert fak.lib.fak_gdn_attn(ref(b), ref(a), None) == 0 and fak.lib.fak_gdn_conv(ref(b), ref(r), None) == 0
 
 
+def test_debug_wait_refuses(fak):
+    for args in ((-1, 0), (0, 2), (1000, -1)):
+        assert fak.lib.fak_gdn_debug_wait(*args) == 1
+    assert fak.lib.fak_gdn_debug_wait(0, 0) == 0
+
+
 def test_binding_refuses_wrong_tensors(fak):
     torch = pytest.importorskip("torch")
     i32 = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731

@@ -315,6 +315,75 @@ def test_attn_same_bits_again_captured_and_on_another_stream(fak):
     assert fak.fak_device_status() == 0
 
 
+def test_attn_two_calls_at_once(fak):
+    """On two streams, each with its own scratch."""
+    lengths = [(700, 700), (1, 9), (130, 400), (64, 64)]
+    calls = []
+    for seed in (21, 22):
+        start, kv_len, slot, rows, slots = G.batch_tensors(lengths, seed)
+        q, k, v, g, beta, z, w = G.inputs(2, 16, rows, seed)
+        calls.append((fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, torch.randn(slots, 16, 128, 128, device="cuda"), z, w, rows))
+    outs = []
+    for at_once in (False, True):
+        streams = [torch.cuda.Stream() if at_once else torch.cuda.current_stream() for _ in calls]
+        here = []
+        for s, (batch, q, k, v, g, beta, s0, z, w, rows) in zip(streams, calls):
+            here.append((s0.clone(), torch.zeros(rows, 16, 128, device="cuda")))
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            for s, (state, o), (batch, q, k, v, g, beta, s0, z, w, rows) in zip(streams, here, calls):
+                with torch.cuda.stream(s):
+                    fak.fak_gdn_attn(batch, q, k, v, g, beta, state, o, 700, z=z, norm_w=w)
+        torch.cuda.synchronize()
+        outs += here
+    assert fak.fak_device_status() == 0
+    for i in range(2):
+        assert torch.equal(outs[i][0], outs[2 + i][0]) and torch.equal(outs[i][1], outs[2 + i][1])
+
+
+def test_offsets_that_pass_32_bits(fak):
+    """Rows, and slots of the pools, more than 2^31 elements behind the first."""
+    far, rows = 1 << 20, 2200
+    lengths = [(2150, 2150), (1, 5), (49, 49)]
+    start, kv_len, _, _, _ = G.batch_tensors(lengths, 0)
+    slots = 1500
+    slot = torch.tensor([slots - 1, slots - 3, slots - 2], dtype=torch.int32, device="cuda")
+    nk, nv = 2, 96
+    state = torch.empty(slots, nv, 128, 128, device="cuda")
+    assert state.numel() > 1 << 31 and far * (rows - 100) > 1 << 31
+    state[-3:] = 0.3 * torch.randn(3, nv, 128, 128, device="cuda")
+    keep = state[-3:].clone()
+    q, k, v, g, beta, z, w = G.inputs(nk, nv, rows, 31)
+
+    def view(t):
+        big = torch.empty(rows * far, dtype=t.dtype, device="cuda").view(rows, far)
+        big = big[:, :t.shape[1] * 128].unflatten(1, (t.shape[1], 128))
+        return big.copy_(t)
+
+    o = view(torch.zeros(rows, nv, 128, device="cuda", dtype=torch.bfloat16))
+    fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), view(q), view(k), view(v), g, beta, state, o, 2150, z=view(z), norm_w=w)
+    assert fak.fak_device_status() == 0
+    near = torch.empty(3, nv, 128, 128, device="cuda").copy_(keep)
+    on = torch.zeros(rows, nv, 128, device="cuda", dtype=torch.bfloat16)
+    fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot - (slots - 3)), q, k, v, g, beta, near, on, 2150, z=z, norm_w=w)
+    assert torch.equal(o, on) and torch.equal(state[-3:], near)
+    del state, o
+    chans = (2 * nk + 4) * 128
+    x, b, a = torch.randn(rows, chans, device="cuda"), torch.randn(rows, 4, device="cuda"), torch.randn(rows, 4, device="cuda")
+    big = torch.empty(rows * far, device="cuda").view(rows, far)[:, :chans].copy_(x)
+    conv_w, a_log, dt = torch.randn(chans, 4, device="cuda"), torch.rand(4, device="cuda"), torch.rand(4, device="cuda")
+    got = []
+    for t, n in ((x, 3), (big, 1 << 20)):
+        st = torch.zeros(n, 3, chans, device="cuda")
+        assert n == 3 or st.numel() > 1 << 31
+        out = [torch.zeros(rows, nk, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+        out += [torch.zeros(rows, 4, 128, dtype=torch.bfloat16, device="cuda"), *(torch.zeros(rows, 4, device="cuda") for _ in range(2))]
+        fak.fak_gdn_conv(fak.GDNBatch(start, kv_len, slot - (slots - n)), t, b, a, conv_w, a_log, dt, st, *out, eps=G.EPS)
+        got.append(out + [st[-3:].clone()])
+    assert fak.fak_device_status() == 0
+    assert all(torch.equal(i, j) for i, j in zip(*got)) and bool(got[0][0].any())
+
+
 # ------------------------------------------------------------------ the convolution
 def conv_case(fak, lengths, nk, nv, kind=torch.float32, seed=1, pad_rows=2, views=True):
     gen = torch.Generator(device="cuda").manual_seed(seed)
