@@ -28,7 +28,7 @@
 // memory and makes what only the output wants: S^T Q^T, R^T (P T)^T, the norm (its sums of squares from all eight such warps of
 // the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  316
 // instructions of 8 cycles of the tensor cores for the state and 188 for the output, 4,032 cycles a chunk on each of an SM's four
-// parts; a chunk takes 6,100 (3.2 us): one warp's way through three products, the splitting into f16 and the scales, and shared
+// parts; a chunk takes 6,000 (3.2 us): one warp's way through three products, the splitting into f16 and the scales, and shared
 // memory, whose operands a warp of 16 columns takes for itself alone (fragments 60 % of its cycles).
 //
 // What did not help: the same products by tcgen05, 64 columns to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through
@@ -121,10 +121,12 @@ struct C {
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
 };
 
+constexpr int kRegs = 168;  // of a thread at launch
+
 // Named barriers of a pair of warps (pair w: 3 w on).
 enum Named { kBarS = 1, kBarR, kBarUsed };
 
-enum Bars { kLand0, kLand1, kReady0, kReady1, kFree0, kFree1, kVFree, kZ, kZFree, kSum0, kSum1, kOut, kOutFree, kBars };
+enum Bars { kLand0, kLand1, kReady0, kReady1, kFree0, kFree1, kLandV, kVFree, kZ, kZFree, kSum0, kSum1, kOut, kOutFree, kBars };
 
 FAK_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -384,13 +386,14 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
   };
   auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
 
-  // registers of a thread: 232 + 208 + 56 of the 3 * 168 that the block has
+  // registers of a thread: 224 + 208 + 72 of the 3 * kRegs that the block has.  (The copies' warp wants more than 56, beside which
+  // the others could have 232 and 208: 254 us for 8 chunks in place of 248.)
   if (warp < NW)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   else if (warp < 2 * NW)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp < NW) {
     // ------------------------------------------------------------------ 16 columns
     const int g = lane >> 2, q2 = 2 * (lane & 3);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
       }
     uint32_t v[4][4];  // of the next chunk: rows 16 i + q2 and the next, + 8; columns g, g + 8
     auto fetch_v = [&](int c) {
-      wait(kReady0 + (c & 1), c >> 1);
+      wait(kLandV, c);
       const uint32_t tile = base + C::off_v + (warp >> 2) * kRows * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -470,6 +473,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
       const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
+      wait(kReady0 + (c & 1), c >> 1);
       // S^T, as an operand, to the output's warp too; S^T K^T
       float2 ks[8][2] = {};
       ms[0] = ms[1] = 0.0f;
@@ -527,6 +531,23 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         frag[(17 + 2 * i) * 32] = make_uint4(rl[i][0], rl[i][1], rl[i][2], rl[i][3]);
       }
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarR) : "memory");
+      // the next chunk's values and its scale
+      const float all = dec->keep[kRows - 1];
+      float ratio[2] = {1.0f, 1.0f};
+      if (c + 1 < chunks) {
+        fetch_v(c + 1);
+        most_of(ms[0], ms[1]);
+        float old[2] = {mv[0], mv[1]};
+        most_v(mv);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int to = scale_by(fmaxf(ms[u] * down[u], fmaxf(old[u], mv[u])));
+          ratio[u] = two_to(min(max(to - by[u], -126), 127));
+          by[u] = to;
+          up[u] = two_to(to);
+          down[u] = two_to(-to);
+        }
+      }
       // U^T = R^T T^T: rows 16 j .. of T by columns 16 i .., i <= j
       float2 ut[8][2] = {};
 #pragma unroll
@@ -560,23 +581,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
               }
             }
         }
-      // the next chunk's values, its scale, and U^T diag(exp(G_64 - G)) in it, as an operand
-      const float all = dec->keep[kRows - 1];
-      float ratio[2] = {1.0f, 1.0f};
-      if (c + 1 < chunks) {
-        fetch_v(c + 1);
-        most_of(ms[0], ms[1]);
-        float old[2] = {mv[0], mv[1]};
-        most_v(mv);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int to = scale_by(fmaxf(ms[u] * down[u], fmaxf(old[u], mv[u])));
-          ratio[u] = two_to(min(max(to - by[u], -126), 127));
-          by[u] = to;
-          up[u] = two_to(to);
-          down[u] = two_to(-to);
-        }
-      }
+      // U^T diag(exp(G_64 - G)) in the next chunk's scale, as an operand
       uint32_t uh[4][4], ul[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -793,25 +798,31 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
     // and those that were are waited for before the block ends.
     const int hk = h / p.group;
     const unsigned char* record0 = records.at + (record_of(records, d, s, begin) * p.nv + h) * kRecord;
-    int copied = 0, gates = 0;  // chunks of which all but z, and of which z, was asked for
+    int values = 0, copied = 0, gates = 0;  // chunks of which V, of which K, Q and the record, of which z was asked for
+    auto load_v = [&](int c) {  // (which goes to registers amid the chunk before)
+      if (c >= 1) wait(kVFree, c - 1);
+      if (dead()) return;
+      values = c + 1;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar[kLandV], kRows * C::cols * 2);
+        tma_load_3d_tx(smem + C::off_v, &maps.v, col0, h, first_row + c * kRows, &bar[kLandV]);
+      }
+      __syncwarp();
+    };
     auto load = [&](int c) {
       if (c >= 2) wait(kFree0 + (c & 1), (c - 2) >> 1);
-      if (c >= 1) wait(kVFree, c - 1);
       if (dead()) return;
       copied = c + 1;
       const int row = first_row + c * kRows;
       unsigned char* to = smem + C::off_kq + (c & 1) * 32768;
       if (elect_one()) {
         uint64_t* land = &bar[kLand0 + (c & 1)];
-        mbar_arrive_expect_tx(land, 32768 + kRecord + kRows * C::cols * 2);
+        mbar_arrive_expect_tx(land, 32768 + kRecord);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           tma_load_3d_tx(to + i * 16384, &maps.k, 64 * i, hk, row, land);
           tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, row, land);
         }
-#pragma unroll
-        for (int i = 0; i < C::cols / 64; ++i)
-          tma_load_3d_tx(smem + C::off_v + i * kRows * 128, &maps.v, col0 + 64 * i, h, row, land);  // (the last chunk's is in registers)
         const unsigned char* record = record0 + (int64_t)c * p.nv * kRecord;
         bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
         bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
@@ -882,17 +893,24 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
       }
       arrive(kOutFree);
     };
+    load_v(0);
     load(0);
-    landed(0);
-    if (chunks > 1) load(1);
     load_z(0);
+    landed(0);
+    if (chunks > 1) {
+      load_v(1);
+      load(1);
+    }
     for (int c = 0; c < chunks && !dead(); ++c) {
-      if (c + 1 < chunks) landed(c + 1);
       if (c > 0) {
         store(c - 1);
         load_z(c);
       }
-      if (c + 2 < chunks) load(c + 2);
+      if (c + 1 < chunks) landed(c + 1);
+      if (c + 2 < chunks) {
+        load_v(c + 2);
+        load(c + 2);
+      }
     }
     store(chunks - 1);
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -904,6 +922,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         }
       };
       for (int c = max(0, copied - 2); c < copied; ++c) drain(kLand0 + (c & 1), c >> 1);
+      if (values) drain(kLandV, values - 1);
       if (gates && p.z_wide) drain(kZ, gates - 1);
     }
   }
@@ -1097,7 +1116,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
     if (h0 == 0) {  // (the gates come while K and Q do)
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < 8; ++k) {
         auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
         uint32_t ak[4], aq[4];
@@ -1330,6 +1349,11 @@ cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const Records& rec
   static std::atomic<uint64_t> done{0};
   cudaError_t e = kv_smem_limit(gdn_chunk_kernel<F32>, C::smem, dev, done);
   if (e != cudaSuccess) return e;
+  static const int regs = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, gdn_chunk_kernel<F32>) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != kRegs) return cudaErrorNotSupported;  // (with fewer, its warps would wait for registers that nobody gives back)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * C::slices));
   cfg.blockDim = dim3(C::threads);
