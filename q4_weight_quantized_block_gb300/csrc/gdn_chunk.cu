@@ -195,11 +195,12 @@ FAK_DEV float2 bf16_pair(uint32_t w) { return make_float2(__uint_as_float(w << 1
 
 // Two f32 as the sum of two pairs of f16.
 FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 b = fma2(__half22float2(h), both(-1.0f), make_float2(x, y));
-  const __half2 l = __floats2half2_rn(b.x, b.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
+  float a, b;  // x and y less their first parts: exact; f16 operands and -1 to an f32 sum (1 % of a prompt's time)
+  asm("{\n .reg .b16 p, q, m;\n mov.b32 {p, q}, %2;\n mov.b16 m, 0xBC00;\n fma.rn.f32.f16 %0, p, m, %3;\n fma.rn.f32.f16 %1, q, m, %4;\n}"
+      : "=f"(a), "=f"(b)
+      : "r"(hi), "f"(x), "f"(y));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
 }
 
 // Columns of a row (from a multiple of 8 on) of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
