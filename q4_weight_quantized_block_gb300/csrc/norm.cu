@@ -24,11 +24,21 @@ struct NormParams {
   bool h_bf16, y_bf16, n_bf16, post, sigmoid;
 };
 
-// V neighbouring values (1 or 4) of an f32 or bf16 row.
+// V neighbouring values (1, 2 or 4) of an f32 or bf16 row.
 template <int V>
 FAK_DEV void get(const void* p, bool bf16, int64_t at, float (&x)[V]) {
   if constexpr (V == 1) {
     x[0] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]) : static_cast<const float*>(p)[at];
+  } else if constexpr (V == 2) {
+    if (bf16) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + at);
+      x[0] = __uint_as_float(w << 16);
+      x[1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+      const float2 w = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+      x[0] = w.x;
+      x[1] = w.y;
+    }
   } else if (bf16) {
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at);
     x[0] = __uint_as_float(w.x << 16);
@@ -51,6 +61,11 @@ FAK_DEV void put(void* p, bool bf16, int64_t at, const float (&x)[V]) {
       static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(x[0]);
     else
       static_cast<float*>(p)[at] = x[0];
+  } else if constexpr (V == 2) {
+    if (bf16)
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + at) = __floats2bfloat162_rn(x[0], x[1]);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(x[0], x[1]);
   } else if (bf16) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
@@ -195,21 +210,33 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
   p.n_bf16 = nb;
   p.post = a->post_norm != 0;
   p.sigmoid = a->gate_kind == FAK_GATE_SIGMOID;
-  // four values at a time where every row of every operand stands on a multiple of 16 bytes
-  const int64_t strides = p.h_row * (hb ? 2 : 4) | (a->y ? p.y_row * (yb ? 2 : 4) : 0) | (a->n ? p.n_row * (nb ? 2 : 4) : 0) |
-                          (p.gate && p.gate_col ? p.gate_row * 4 : 0);
-  const uintptr_t starts = (uintptr_t)a->h | (uintptr_t)a->y | (uintptr_t)a->n | (uintptr_t)a->w | (uintptr_t)a->y_w |
-                           (p.gate && p.gate_col ? (uintptr_t)a->gate : 0);
-  const bool wide = a->d % 4 == 0 && !(strides & 15) && !(starts & 15);
+  // As many values at a time as every row of every operand stands on a multiple of: 4, 2 or 1.
+  const auto by = [&](int v) {
+    const auto rows = [&](const void* at, int64_t row, int elem) { return !at || (!((uintptr_t)at & (v * elem - 1)) && row % v == 0); };
+    return a->d % v == 0 && rows(a->h, p.h_row, hb ? 2 : 4) && rows(a->y, p.y_row, yb ? 2 : 4) && rows(a->n, p.n_row, nb ? 2 : 4) &&
+           rows(a->w, 0, 4) && rows(a->y_w, 0, 4) && (!p.gate_col || rows(p.gate, p.gate_row, 4));
+  };
+  // (16,384 rows of 1,500 on multiples of 8 bytes take 64 us by fours, 153 by ones; 3,451 of 7,510 107 us by twos, 185.)
+  // Many rows: 16 values to a thread, so that several blocks are on an SM, where that spills no registers; few: the fewest values
+  // that 1,024 threads allow.
+  const bool many = a->rows >= 608 && a->d >= 1024 && a->d <= 16384;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (wide)
-    e = a->rows >= 608 && a->d >= 1024 && a->d <= 16384 ? launch<4, 4>(p, s)
-        : a->d <= 4096                                   ? launch<4, 1>(p, s)
-        : a->d <= 8192                                   ? launch<4, 2>(p, s)
-        : a->d <= 16384                                  ? launch<4, 4>(p, s)
-                                                         : launch<4, 8>(p, s);
+  if (by(4))
+    e = many             ? launch<4, 4>(p, s)
+        : a->d <= 4096   ? launch<4, 1>(p, s)
+        : a->d <= 8192   ? launch<4, 2>(p, s)
+        : a->d <= 16384  ? launch<4, 4>(p, s)
+                         : launch<4, 8>(p, s);
+  else if (by(2))
+    e = many || (a->d > 8192 && a->d <= 16384) ? launch<2, 8>(p, s)
+        : a->d <= 2048                         ? launch<2, 1>(p, s)
+        : a->d <= 8192                         ? launch<2, 4>(p, s)
+                                               : launch<2, 16>(p, s);
   else
-    e = a->d <= 1024 ? launch<1, 1>(p, s) : a->d <= 8192 ? launch<1, 8>(p, s) : launch<1, 32>(p, s);
+    e = a->d <= 1024    ? launch<1, 1>(p, s)
+        : a->d <= 8192  ? launch<1, 8>(p, s)
+        : a->d <= 16384 ? launch<1, 16>(p, s)
+                        : launch<1, 32>(p, s);
   return fak_cuda_status(e);
 }

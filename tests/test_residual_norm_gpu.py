@@ -66,6 +66,19 @@ def test_widths(fak, d):
     case(fak, 5, d, seed=d)
 
 
+@pytest.mark.parametrize("d", [6, 30, 1022, 2050, 4094, 8190, 8194, 16382, 20002, 32766])
+def test_widths_by_twos(fak, d):
+    case(fak, 5, d, seed=d)
+    case(fak, 3, d, "bf16", "bf16", "f32", gate="one", seed=d + 1)
+    case(fak, 3, d, "bf16", "f32", "bf16", gate="none", views=True, seed=d + 2)
+
+
+@pytest.mark.parametrize("d", [1001, 1026, 1500, 5122, 9999, 10004, 16390])
+def test_many_rows_of_odd_widths(fak, d):
+    case(fak, 700, d, "bf16", seed=d)
+    case(fak, 700, d, "f32", "bf16", "f32", gate="slice", views=True, seed=d + 1)
+
+
 @pytest.mark.parametrize("ht", list(T))
 @pytest.mark.parametrize("yt", list(T))
 @pytest.mark.parametrize("nt", list(T))
