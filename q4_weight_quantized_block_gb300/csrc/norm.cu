@@ -90,11 +90,12 @@ FAK_DEV float block_sum(float x, float* red) {
 
 // Block r: row r; thread t holds the values V (t + i * threads) .. + V - 1 for i < PER.  A row's loads are all asked for
 // before the first is used.
-template <int V, int PER>
+// GATE: with a gate; its registers cost blocks on an SM (16,384 rows of 5,120 without one take 169 us, 177 with its registers).
+template <int V, int PER, bool GATE>
 __global__ void __launch_bounds__(1024) residual_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[2][32];
   const int64_t row = blockIdx.x;
-  float h[PER][V], y[PER][V], gate[PER][V];
+  float h[PER][V], y[PER][V], gate[GATE ? PER : 1][V];
   bool in[PER];
   int at[PER];
 #pragma unroll
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const __grid_consta
     if (!in[i]) continue;
     get<V>(p.h, p.h_bf16, row * p.h_row + at[i], h[i]);
     if (p.y) get<V>(p.y, p.y_bf16, row * p.y_row + at[i], y[i]);
-    if (p.gate) {
+    if (GATE && p.gate) {  // (tested again: without it the compiler spreads the loads, 256 us for 16,384 x 5,120 in place of 225)
       if (p.gate_col) {
         get<V>(p.gate, false, row * p.gate_row + at[i], gate[i]);
       } else {
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const __grid_consta
         float x = y[i][j];
         if (p.post) x *= r;
         if (gain) x *= p.offset + w[j];
-        if (p.gate) x *= p.sigmoid ? 1.0f / (1.0f + expf(-gate[i][j])) : gate[i][j];
+        if (GATE && p.gate) x *= p.sigmoid ? 1.0f / (1.0f + expf(-gate[i][j])) : gate[i][j];
         h[i][j] = fmaf(p.scale, x, h[i][j]);
       }
       put<V>(p.h, p.h_bf16, row * p.h_row + at[i], h[i]);
@@ -164,7 +165,10 @@ template <int V, int PER>
 cudaError_t launch(const NormParams& p, cudaStream_t s) {
   const int units = (p.d + V - 1) / V;
   const int threads = ((units + PER - 1) / PER + 31) / 32 * 32;
-  residual_norm_kernel<V, PER><<<(unsigned)p.rows, threads, 0, s>>>(p);
+  if (p.gate)
+    residual_norm_kernel<V, PER, true><<<(unsigned)p.rows, threads, 0, s>>>(p);
+  else
+    residual_norm_kernel<V, PER, false><<<(unsigned)p.rows, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -216,9 +220,10 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
     return a->d % v == 0 && rows(a->h, p.h_row, hb ? 2 : 4) && rows(a->y, p.y_row, yb ? 2 : 4) && rows(a->n, p.n_row, nb ? 2 : 4) &&
            rows(a->w, 0, 4) && rows(a->y_w, 0, 4) && (!p.gate_col || rows(p.gate, p.gate_row, 4));
   };
-  // (16,384 rows of 1,500 on multiples of 8 bytes take 64 us by fours, 153 by ones; 3,451 of 7,510 107 us by twos, 185.)
-  // Many rows: 16 values to a thread, so that several blocks are on an SM, where that spills no registers; few: the fewest values
-  // that 1,024 threads allow.
+  // (16,384 rows of 1,500 on multiples of 8 bytes take 60 us by fours, 153 by ones; 3,451 of 7,510 77 us by twos, 100 by ones.)
+  // Many rows: 16 values to a thread, so that several blocks are on an SM, by ones from 4,096 values on
+  // and without a gate (3,451 of 7,511: 100 us, by 8 to a thread 189; 1,391 of 2,559: 21 and 18); few: the fewest values that
+  // 1,024 threads allow.
   const bool many = a->rows >= 608 && a->d >= 1024 && a->d <= 16384;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
@@ -234,9 +239,9 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
         : a->d <= 8192                         ? launch<2, 4>(p, s)
                                                : launch<2, 16>(p, s);
   else
-    e = a->d <= 1024    ? launch<1, 1>(p, s)
-        : a->d <= 8192  ? launch<1, 8>(p, s)
-        : a->d <= 16384 ? launch<1, 16>(p, s)
-                        : launch<1, 32>(p, s);
+    e = a->d <= 1024                              ? launch<1, 1>(p, s)
+        : a->d <= (many && !p.gate ? 4096 : 8192) ? launch<1, 8>(p, s)
+        : a->d <= 16384                           ? launch<1, 16>(p, s)
+                                                  : launch<1, 32>(p, s);
   return fak_cuda_status(e);
 }
