@@ -965,7 +965,14 @@ FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int x, int lane, G
   }
   s = lo;
   if ((c = has(s, d)) >= 0) return true;
-  // where they may fall beside numbers that are out of range: all sequences, where any is
+  // a place of none, unless starts are out of range or fall: then all sequences
+  bool odd = false;
+#pragma unroll 8
+  for (int i = lane; i < p.c.n_seqs; i += 32) {
+    const int r0 = p.c.row_start[i], r1 = p.c.row_start[i + 1];
+    odd |= r0 < 0 || r1 < r0 || r1 > p.c.rows;
+  }
+  if (!__any_sync(0xffffffffu, odd)) return false;
 #pragma unroll 1
   for (int base = 0; base < p.c.n_seqs; base += 32) {
     GdnSeq e{0, 0, 0, 0, false, false};
