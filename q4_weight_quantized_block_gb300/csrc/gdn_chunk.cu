@@ -9,35 +9,38 @@
 // depend on no state: a first kernel makes them for all chunks and heads (a record of 33 KB each, in a scratch), the second
 // goes through a sequence's chunks.
 //
-// Precision.  The state is held in f32 registers, and products keep 22 bits: the f32 operand goes as the sum of two
-// f16, the other one is f16 already (q, k) or two f16 too (T, P T; the small parts' product is left out).  f16's exponents take
-// them because a value column's S, R and U are scaled by one power of two.  With m the largest of the column's |S| and |V|,
-// lengths of k of at most 1 and 0 <= beta <= 2: |R| <= 25 m, |U| <= 281 m, and the next chunk's |S| <= 140 m.  The scale goes by m
-// of the chunk before (by which time it is known), so m goes to 2^-2 .. 2^-1, U stays below 2^15, and what f16 drops is below
-// 2^-25, so 2^-23 m.  T and P T need no scale: |T|, and so P T, is at most 3.  Sums of decays are made in fixed point and kept as
-// two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only.
+// Precision.  The state is held in f32 registers; products keep 21 to 22 bits, and each is off by no more than that part of what its
+// own row and column have: of a row's value, or of what the rows before brought to the column and the decays have left.  R is
+// as large as a row's values, which differ at will, and T and P T shrink by the decays: both go as two tf32 each (the small
+// parts' product is left out), which have f32's exponents.  The state, and U by the decays to the chunk's end, go as the sum
+// of two f16, q and k are f16 already.  f16's exponents take them because a value column is scaled by one power of two, by its largest
+// |exp(G_64) S| or |exp(G_64 - G) U|, m, which goes to 2^8 .. 2^9: with elements of k of at most 1 the state behind is
+// at most 65 m, below 2^15.1, and what f16 drops is below 2^-25, so 2^-33 m.  T and P T are made without their decays, by products of
+// two f16 (|T| is at most 2 then, with lengths of k of at most 1 and 0 <= beta <= 2) and multiplied by them at the end, so that their
+// errors decay too.  Sums of decays are made in fixed point and kept as two f32, so that decays over neighbouring rows,
+// differences of large sums, are off by 2^-22 only.
 //
-// First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps: decays into A
-// and P; inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, and P T, in place of A and P, by m16n8k16
-// instructions.  Steps that wait for one another on 64 x 64 matrices: 104 us for 128 chunks of 48 heads on 16 key heads, of which
-// the records' 206 MB are 30 us; four blocks to an SM hide part of it (issue slots 31 %, tensor pipe 13 % busy).
+// First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps:
+// inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, in place of A, and P T by m16n8k16
+// instructions; both by their decays to the record.  Steps that wait for one another on 64 x 64 matrices: 118 us for 128 chunks of 48
+// heads on 16 key heads; four blocks to an SM hide part of it.
 //
 // Second kernel: two CTAs to a head, 64 value columns each; a warp holds 16 columns, as S^T in the accumulators of m16n8k16 (64
 // registers a thread).  Those are laid out as the next product's first operand is, so that S^T, R^T and U^T go from product
-// to product in registers: S^T K^T, R^T T^T, U^T K.  A second warp to the same columns takes S^T and R^T as operands from shared
+// to product in registers: S^T K^T, R^T T^T (m16n8k8), U^T K.  A second warp to the same columns takes S^T and R^T from shared
 // memory and makes what only the output wants: S^T Q^T, R^T (P T)^T, the norm (its sums of squares from all eight such warps of
-// the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  316
-// instructions of 8 cycles of the tensor cores for the state and 188 for the output, 4,032 cycles a chunk on each of an SM's four
-// parts; a chunk takes 6,000 (3.2 us): one warp's way through three products, the splitting into f16 and the scales, and shared
-// memory, whose operands a warp of 16 columns takes for itself alone (fragments 60 % of its cycles).
+// the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  364
+// instructions of 8 cycles of the tensor cores for the state and 236 for the output, 4,800 cycles a chunk on each of an SM's four
+// parts; a chunk takes 7,900 (4.1 us): one warp's way through three products, the splitting into parts and the scales, and shared
+// memory, whose operands a warp of 16 columns takes for itself alone.
 //
-// What did not help: the same products by tcgen05, 64 columns to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through
-// shared memory for each of three products that wait for one another, some 700 cycles for a product and as many for its operand);
-// one CTA to a head with eight warps that make their outputs too (12,700 for both halves of a head); two warps to the same
-// columns, each with half of the keys and rows (6,400 to 7,000: what they exchange fills shared memory); several sequences'
-// heads one behind the other in a CTA, split evenly (a chunk 7 % longer); records without the zeros above the diagonal (fewer
-// bytes, yet 7 % more time of the second kernel for one prompt); records of the next 32 chunks beside the chunks of these (3 %
-// less for one prompt of 8,192, at the price of the kernel twice).
+// What did not help (measured with R, T and P T as two f16, a chunk of 6,000 cycles then): the same products by tcgen05, 64 columns
+// to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through shared memory for each of three products that wait for one
+// another, some 700 cycles for a product and as many for its operand); one CTA to a head with eight warps that make their outputs
+// too (12,700 for both halves of a head); two warps to the same columns, each with half of the keys and rows (6,400 to 7,000: what
+// they exchange fills shared memory); several sequences' heads one behind the other in a CTA, split evenly (a chunk 7 % longer);
+// records without the zeros above the diagonal (fewer bytes, yet 7 % more time of the second kernel for one prompt); records of the
+// next 32 chunks beside the chunks of these (3 % less for one prompt of 8,192, at the price of the kernel twice).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,15 +65,16 @@ namespace {
 constexpr int kRows = 64;  // of a chunk
 constexpr int kPrepThreads = 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
-constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
+constexpr int kPart = 16384;   // from a matrix's first parts to its second: 128 rows of 64 f16
+constexpr int kPanel = 16384;  // 32 columns of [T; P T] in f32: 128 rows of 128 bytes
 
-// What a chunk's rows decay by, and their strengths: behind [T; P T], two parts, in a chunk's record for a head.
+// What a chunk's rows decay by, and their strengths: behind [T; P T], in a chunk's record for a head.
 struct Decays {
   float keep[kRows];  // exp G_t
   float left[kRows];  // exp(G_64 - G_t)
   float beta[kRows];
 };
-constexpr int kRecord = 2 * kPart + (int)sizeof(Decays);
+constexpr int kRecord = 2 * kPanel + (int)sizeof(Decays);
 static_assert(kRecord % 16 == 0, "bulk copies");
 
 // Where records stand.  dense: chunk c of a sequence s, begin <= c < begin + length, at s * length + c - begin.  Else a sequence
@@ -108,9 +112,9 @@ struct C {
   static constexpr int slices = kGdnDim / cols;                     // CTAs of a head
   static constexpr int threads = 64 * NW + 128;
   static constexpr int off_kq = 0;                                  // two stages of [K; Q]: two panels of 128 rows
-  static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two parts
-  static constexpr int off_v = off_tp + 4 * kPart;                  // V: panels of 64 columns, 128 bytes
-  static constexpr int off_frag = off_v + kRows * cols * 2;         // each warp's S (8) and R (4) as operands, two parts
+  static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two panels
+  static constexpr int off_v = off_tp + 4 * kPanel;                 // V: panels of 64 columns, 128 bytes
+  static constexpr int off_frag = off_v + kRows * cols * 2;         // each warp's S (two f16) and R (f32) as operands
   static constexpr int off_z = off_frag + NW * 12 * 1024;           // z: panels of 32 columns, 128 bytes
   static constexpr int off_out = off_z + kRows * cols * 4;          // the output, f32 or bf16: panels of 128 bytes
   static constexpr int off_dec = off_out + kRows * cols * 4;
@@ -321,13 +325,73 @@ FAK_DEV void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], const float2 (&x)[2],
   split_half(y[0].x, y[0].y, hi[2], lo[2]);
   split_half(y[1].x, y[1].y, hi[3], lo[3]);
 }
+// Where the columns 8 at + 2 q and the next of a row of [T; P T] stand: 32 bytes of eight columns, those of four rows in turn on
+// all banks.
+FAK_DEV int pair_at(int row, int at, int q) { return (at >> 2) * kPanel + row * 128 + (((at & 3) ^ (row & 3)) << 5) + 8 * q; }
+// Operands of m16n8k8 as two tf32, so that they keep their own exponents: of T, which has 23 bits (the first part rounded, the
+// second exact), and of R (the first 11 bits and the next 11).  NaN and infinities stay what they are in the first parts.
+FAK_DEV void split_t(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+FAK_DEV void split_r(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+}
+// To 23 bits (as split_t wants it, which would carry a NaN's last bits into its sign).
+FAK_DEV float round_t(float x) { return x == x ? __uint_as_float((__float_as_uint(x) + 1u) & ~1u) : __uint_as_float(0x7fc00000u); }
+FAK_DEV void mma8(float2 (&c)[2], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc += R^T T^T for one warp's 16 columns, T (or P T) lower triangular from `t` on: tiles of 8 rows by 8, those on and below
+// the diagonal.  r(j): rows 8 j .. of R, an accumulator's values in the order of an operand A, columns 2 q and 2 q + 1 of the
+// product before being k = q and q + 4 here.
+template <typename F>
+FAK_DEV void triangle(float2 (&acc)[8][2], F r, const unsigned char* t, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t rh[2][4], rl[2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4 x = r(i + e);
+      split_r(x.x, rh[e][0], rl[e][0]);
+      split_r(x.y, rh[e][1], rl[e][1]);
+      split_r(x.z, rh[e][2], rl[e][2]);
+      split_r(x.w, rh[e][3], rl[e][3]);
+    }
+#pragma unroll
+    for (int j = i; j < 8; j += 4) {
+      uint32_t th[2][4][2], tl[2][4][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (j + u >= 8 || i + e > j + u) continue;
+          const float2 x = *reinterpret_cast<const float2*>(t + pair_at(8 * (j + u) + (lane >> 2), i + e, lane & 3));
+          split_t(x.x, th[e][u][0], tl[e][u][0]);
+          split_t(x.y, th[e][u][1], tl[e][u][1]);
+        }
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (j + u >= 8 || i + e > j + u) continue;
+            mma8(acc[j + u], w == 0 ? rl[e] : rh[e], w == 1 ? tl[e][u] : th[e][u]);
+          }
+    }
+  }
+}
 // A row of 128 bytes' 16-byte piece in a tile of 128-byte swizzle.
 FAK_DEV uint32_t piece(int row, int at) { return row * 128 + ((at ^ (row & 7)) << 4); }
 
-// 2^by for a column whose largest magnitude is m = 2^e 1.f, which goes to 2^-2 1.f (zeros and infinities: as they are)
+// 2^by for a column whose largest magnitude is m = 2^e 1.f, which goes to 2^8 1.f (zeros and infinities: as they are)
 FAK_DEV int scale_by(float m) {
   const int e = (int)(__float_as_uint(m) >> 23);
-  return e == 0 || e == 255 ? 0 : min(max(125 - e, -120), 120);
+  return e == 0 || e == 255 ? 0 : min(max(135 - e, -120), 120);
 }
 FAK_DEV float two_to(int by) { return __uint_as_float((uint32_t)(127 + by) << 23); }
 
@@ -436,44 +500,30 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
       }
     };
-    auto most_v = [&](float (&m)[2]) {
-      float2 a[2] = {both(0.0f), both(0.0f)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 x = bf16_pair(v[i][u]);
-          a[u & 1] = make_float2(fmaxf(a[u & 1].x, fabsf(x.x)), fmaxf(a[u & 1].y, fabsf(x.y)));
-        }
-      m[0] = fmaxf(a[0].x, a[0].y);
-      m[1] = fmaxf(a[1].x, a[1].y);
-      most_of(m[0], m[1]);
-    };
-    // the state's scale, column by column: S holds the state times up
-    float ms[2] = {}, mv[2];
+    // the state's scale, column by column: S holds the state times 2^by
+    float ms[2] = {};
     fetch_v(0);
-    most_v(mv);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) ms[u] = fmaxf(ms[u], fmaxf(fabsf(S[i][u].x), fabsf(S[i][u].y)));
     most_of(ms[0], ms[1]);
     int by[2];
-    float up[2], down[2];
+    float down[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      by[u] = scale_by(fmaxf(ms[u], mv[u]));
-      up[u] = two_to(by[u]);
+      by[u] = scale_by(ms[u]);
       down[u] = two_to(-by[u]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[i][u] = mul2(S[i][u], both(up[u]));
+      for (int i = 0; i < 16; ++i) S[i][u] = mul2(S[i][u], both(two_to(by[u])));
     }
 
     uint4* frag = reinterpret_cast<uint4*>(smem + C::off_frag) + warp * 24 * 32 + lane;
     float* downs = reinterpret_cast<float*>(smem + C::off_down) + 16 * warp;
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
-      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768;
+      const unsigned char* tp = smem + C::off_tp + (c & 1) * 2 * kPanel;
       wait(kReady0 + (c & 1), c >> 1);
       // S^T, as an operand, to the output's warp too; S^T K^T
       float2 ks[8][2] = {};
@@ -512,89 +562,49 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         }
       }
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarS) : "memory");
-      // R^T = beta (V^T - exp(G) S^T K^T), as an operand
-      uint32_t rh[4][4], rl[4][4];
+      // R^T = beta (V^T - exp(G) S^T K^T), to the output's warp too
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < 8; ++j) {
+        const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
+        const float2 beta = *reinterpret_cast<const float2*>(dec->beta + 8 * j + q2);
+        const float2 bk = mul2(mul2(beta, both(-1.0f)), keep);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = 2 * i + e;
-          const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
-          const float2 beta = *reinterpret_cast<const float2*>(dec->beta + 8 * j + q2);
-          const float2 bk = mul2(mul2(beta, both(-1.0f)), keep);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            ks[j][u] = fma2(bk, ks[j][u], mul2(bf16_pair(v[i][2 * e + u]), mul2(beta, both(up[u]))));
-          }
-        }
-        split_a(rh[i], rl[i], ks[2 * i], ks[2 * i + 1]);
-        frag[(16 + 2 * i) * 32] = make_uint4(rh[i][0], rh[i][1], rh[i][2], rh[i][3]);
-        frag[(17 + 2 * i) * 32] = make_uint4(rl[i][0], rl[i][1], rl[i][2], rl[i][3]);
+        for (int u = 0; u < 2; ++u)
+          ks[j][u] = fma2(mul2(bk, both(down[u])), ks[j][u], mul2(bf16_pair(v[j >> 1][2 * (j & 1) + u]), beta));
+        frag[(16 + j) * 32] = make_uint4(__float_as_uint(ks[j][0].x), __float_as_uint(ks[j][1].x), __float_as_uint(ks[j][0].y),
+                                         __float_as_uint(ks[j][1].y));
       }
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarR) : "memory");
-      // the next chunk's values and its scale
+      if (c + 1 < chunks) fetch_v(c + 1);
+      // U^T = R^T T^T
+      float2 ut[8][2] = {};
+      triangle(ut, [&](int j) { return make_float4(ks[j][0].x, ks[j][1].x, ks[j][0].y, ks[j][1].y); }, tp, lane);
+      // U^T diag(exp(G_64 - G)) in the next chunk's scale, as an operand; the scale by what is left of S and of U
       const float all = dec->keep[kRows - 1];
-      float ratio[2] = {1.0f, 1.0f};
-      if (c + 1 < chunks) {
-        fetch_v(c + 1);
-        most_of(ms[0], ms[1]);
-        float old[2] = {mv[0], mv[1]};
-        most_v(mv);
+      float most[2] = {ms[0] * down[0] * all, ms[1] * down[1] * all};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 left = *reinterpret_cast<const float2*>(dec->left + 8 * j + q2);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int to = scale_by(fmaxf(ms[u] * down[u], fmaxf(old[u], mv[u])));
-          ratio[u] = two_to(min(max(to - by[u], -126), 127));
-          by[u] = to;
-          up[u] = two_to(to);
-          down[u] = two_to(-to);
+          ut[j][u] = mul2(ut[j][u], left);
+          most[u] = fmaxf(fmaxf(most[u], fabsf(ut[j][u].x)), fabsf(ut[j][u].y));
         }
       }
-      // U^T = R^T T^T: rows 16 j .. of T by columns 16 i .., i <= j
-      float2 ut[8][2] = {};
+      most_of(most[0], most[1]);
+      float ratio[2];
 #pragma unroll
-      for (int j = 0; j < 4; j += 2)
+      for (int u = 0; u < 2; ++u) {
+        const int to = scale_by(most[u]);
+        ratio[u] = two_to(min(max(to - by[u], -126), 127));
+        by[u] = to;
+        down[u] = two_to(-to);
 #pragma unroll
-        for (int i = 0; i <= j + 1; ++i) {
-          // two row blocks beside each other, where both have the columns
-          uint32_t th[2][4], tl[2][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (i > j + u) continue;
-            const int row = 16 * (j + u) + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
-            ldsm4(th[u], tp + piece(row, at));
-            ldsm4(tl[u], tp + kPart + piece(row, at));
-          }
-#pragma unroll
-          for (int w = 0; w < 3; ++w)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (i > j + u) continue;
-              const int x = 2 * (j + u);
-              if (w == 0) {
-                mma16(ut[x], rl[i], th[u][0], th[u][1]);
-                mma16(ut[x + 1], rl[i], th[u][2], th[u][3]);
-              } else if (w == 1) {
-                mma16(ut[x], rh[i], tl[u][0], tl[u][1]);
-                mma16(ut[x + 1], rh[i], tl[u][2], tl[u][3]);
-              } else {
-                mma16(ut[x], rh[i], th[u][0], th[u][1]);
-                mma16(ut[x + 1], rh[i], th[u][2], th[u][3]);
-              }
-            }
-        }
-      // U^T diag(exp(G_64 - G)) in the next chunk's scale, as an operand
+        for (int j = 0; j < 8; ++j) ut[j][u] = mul2(ut[j][u], both(two_to(to)));
+      }
       uint32_t uh[4][4], ul[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = 2 * i + e;
-          const float2 left = *reinterpret_cast<const float2*>(dec->left + 8 * j + q2);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) ut[j][u] = mul2(ut[j][u], mul2(left, both(ratio[u])));
-        }
-        split_a(uh[i], ul[i], ut[2 * i], ut[2 * i + 1]);
-      }
+      for (int i = 0; i < 4; ++i) split_a(uh[i], ul[i], ut[2 * i], ut[2 * i + 1]);
       // S^T = exp(G_64) S^T + U^T K
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -704,7 +714,8 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
     const float* downs = reinterpret_cast<const float*>(smem + C::off_down) + 16 * w;
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
-      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768;
+      const unsigned char* tp = smem + C::off_tp + (c & 1) * 2 * kPanel;
       if (c > 0) finish(c - 1);
       named_bar_sync(3 * w + kBarS, 64);
       // O^T = exp(G) S^T Q^T
@@ -732,40 +743,29 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
           mma16(o[j + 3], hi, e[2], e[3]);
         }
       }
-      const float sc[2] = {downs[g] * p.scale, downs[g + 8] * p.scale};
+      const float sc[2] = {downs[g], downs[g + 8]};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
-        o[j][0] = mul2(keep, o[j][0]);
-        o[j][1] = mul2(keep, o[j][1]);
+        o[j][0] = mul2(mul2(o[j][0], both(sc[0])), keep);
+        o[j][1] = mul2(mul2(o[j][1], both(sc[1])), keep);
       }
       // O^T += R^T (P T)^T
       named_bar_sync(3 * w + kBarR, 64);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = frag[(16 + 2 * i) * 32], y = frag[(17 + 2 * i) * 32];
-        const uint32_t rh[4] = {x.x, x.y, x.z, x.w}, rl[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = i; j < 4; ++j) {
-          uint32_t ph[4], pl[4];
-          const int row = 16 * j + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
-          ldsm4(ph, tp + 8192 + piece(row, at));
-          ldsm4(pl, tp + kPart + 8192 + piece(row, at));
-          mma16(o[2 * j], rl, ph[0], ph[1]);
-          mma16(o[2 * j + 1], rl, ph[2], ph[3]);
-          mma16(o[2 * j], rh, pl[0], pl[1]);
-          mma16(o[2 * j + 1], rh, pl[2], pl[3]);
-          mma16(o[2 * j], rh, ph[0], ph[1]);
-          mma16(o[2 * j + 1], rh, ph[2], ph[3]);
-        }
-      }
+      triangle(
+          o,
+          [&](int j) {
+            const uint4 x = frag[(16 + j) * 32];
+            return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+          },
+          tp + kRows * 128, lane);
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * w + kBarUsed) : "memory");
       arrive(kFree0 + (c & 1));
       // O, and its columns' share of the rows' sums of squares: to 8 rows' sums over 8 lanes, then one over the lanes' halves
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(sc[u]));
+        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(p.scale));
       if (p.norm_w && !dead()) {
         if (w == 0 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], 8 * kRows * 4);
         float2 y[8];
@@ -825,8 +825,8 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
           tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, row, land);
         }
         const unsigned char* record = record0 + (int64_t)c * p.nv * kRecord;
-        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
-        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
+        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPanel, record, 2 * kPanel, land);
+        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPanel, sizeof(Decays), land);
       }
       __syncwarp();
     };
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       *reinterpret_cast<float2*>(mine) = make_float2(hi[0], hi[1]);
       *reinterpret_cast<float2*>(mine + kRows) = make_float2(lo[0], lo[1]);
       *reinterpret_cast<float2*>(mine + 2 * kRows) = make_float2(b[0], b[1]);
-      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord + 2 * kPart + 8 * lane;
+      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord + 2 * kPanel + 8 * lane;
       *reinterpret_cast<float2*>(record) = make_float2(exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
       *reinterpret_cast<float2*>(record + 4 * kRows) =
           make_float2(exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
@@ -1152,40 +1152,33 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       const int h = hk * p.group + h0 + hh;
       const float* hi = reinterpret_cast<const float*>(smem + kOffHi) + hh * kHeadDecays;
       const float *lo = hi + kRows, *beta = hi + 2 * kRows;
-      // A and P from K K^T and Q K^T by the decays, to the places of T and P T: within the rows' own 16 columns one exponential
-      // each, before them by way of the last row before the 16
+      // A from K K^T and the strengths, to T's place; P, the same for all heads, to that behind it
 #pragma unroll
       for (int i = 0; i < 5; ++i) {
         int m, tile, j;
         place(i, m, tile, j);
+        if (m && (h0 || hh)) continue;
         const int row = 16 * tile + g;
         const float b0 = m ? 1.0f : beta[row], b1 = m ? 1.0f : beta[row + 8];
         float y[2][4];
-        if (j < tile) {
-          const float f0 = b0 * hi[3 * kRows + row], f1 = b1 * hi[3 * kRows + row + 8];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 u = *reinterpret_cast<const float2*>(hi + (3 + tile) * kRows + 16 * j + 8 * e + q2);
-            const float* z = dots[i] + 4 * e;
-            const float2 top = mul2(mul2(u, both(f0)), make_float2(z[0], z[1])), low = mul2(mul2(u, both(f1)), make_float2(z[2], z[3]));
-            y[e][0] = top.x;
-            y[e][1] = top.y;
-            y[e][2] = low.x;
-            y[e][3] = low.y;
-          }
-        } else {
-          const float h0r = hi[row], l0r = lo[row], h1r = hi[row + 8], l1r = lo[row + 8];
+        for (int e = 0; e < 2; ++e) {
+          const float* z = dots[i] + 4 * e;
+          y[e][0] = b0 * z[0];
+          y[e][1] = b0 * z[1];
+          y[e][2] = b1 * z[2];
+          y[e][3] = b1 * z[3];
+        }
+        if (j == tile) {
           const int last = m ? g : g - 1;  // of row g's own 16 columns; row g + 8's: 8 more
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at = 8 * e + q2, col = 16 * j + at;
-            const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
-            const float* z = dots[i] + 4 * e;
+            const int at = 8 * e + q2;
             // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
-            y[e][0] = at <= last ? b0 * exp2_approx((h0r - hc.x) + (l0r - lc.x)) * z[0] : 0.0f;
-            y[e][1] = at + 1 <= last ? b0 * exp2_approx((h0r - hc.y) + (l0r - lc.y)) * z[1] : 0.0f;
-            y[e][2] = at <= last + 8 ? b1 * exp2_approx((h1r - hc.x) + (l1r - lc.x)) * z[2] : 0.0f;
-            y[e][3] = at + 1 <= last + 8 ? b1 * exp2_approx((h1r - hc.y) + (l1r - lc.y)) * z[3] : 0.0f;
+            y[e][0] = at <= last ? y[e][0] : 0.0f;
+            y[e][1] = at + 1 <= last ? y[e][1] : 0.0f;
+            y[e][2] = at <= last + 8 ? y[e][2] : 0.0f;
+            y[e][3] = at + 1 <= last + 8 ? y[e][3] : 0.0f;
             if (!m) {
               *reinterpret_cast<float2*>(diag + row * kLd + at) = make_float2(y[e][0], y[e][1]);
               *reinterpret_cast<float2*>(diag + (row + 8) * kLd + at) = make_float2(y[e][2], y[e][3]);
@@ -1281,7 +1274,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       }
       __syncthreads();
       {
-        // P T in place of P, by blocks of 16 x 16 (m, j): sums over k = j .. m, five steps to a warp
+        // P T, by blocks of 16 x 16 (m, j): sums over k = j .. m, five steps to a warp
         const unsigned mine = w == 0 ? 0xffff0030u : w == 1 ? 0xffff3231u : w == 2 ? 0xffff1020u : 0x11223321u;
         float y[4][2][4] = {};
 #pragma unroll
@@ -1302,26 +1295,46 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
             for (int u = 0; u < 2; ++u) mma16(y[i][u], a.hi, b[u].hi);
           }
         }
-        __syncthreads();  // (P is read)
+        // both by their decays to the record: within the rows' own 16 columns one exponential each, before them by way of the last
+        // row before the 16
+        unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int m = mine >> (8 * i + 4) & 15, j = mine >> (8 * i) & 15;
           if (m == 15) break;
-          put_tiles(tps, kRows + 16 * m, 2 * j, y[i][0], y[i][1], 1.0f, lane);
+          FragA a;
+          load_a(a, tps, 16 * m, 16 * j, lane);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int row = 16 * m + 8 * u + g;
+            const float f = hi[3 * kRows + row], hr = hi[row], lr = lo[row];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (j == m && e > u) continue;  // above the diagonal: nothing reads it
+              const int col = 16 * j + 8 * e + q2;
+              float2 by;
+              if (j < m) {
+                by = mul2(*reinterpret_cast<const float2*>(hi + (3 + m) * kRows + col), both(f));
+              } else {
+                const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
+                by = make_float2(exp2_approx((hr - hc.x) + (lr - lc.x)), exp2_approx((hr - hc.y) + (lr - lc.y)));
+              }
+              const float2 t1 = __half22float2(*reinterpret_cast<const __half2*>(&a.hi[2 * e + u]));
+              const float2 t2 = __half22float2(*reinterpret_cast<const __half2*>(&a.lo[2 * e + u]));
+              float2 t = mul2(add2(t1, t2), by), pt = mul2(make_float2(y[i][e][2 * u], y[i][e][2 * u + 1]), by);
+              if (j == m && e == u) {  // (a zero that masks is put there: it must not meet an infinity)
+                if (q2 > g) t.x = pt.x = 0.0f;
+                if (q2 + 1 > g) t.y = pt.y = 0.0f;
+              }
+              *reinterpret_cast<float2*>(record + pair_at(row, 2 * j + e, lane & 3)) = make_float2(round_t(t.x), round_t(t.y));
+              *reinterpret_cast<float2*>(record + pair_at(kRows + row, 2 * j + e, lane & 3)) = make_float2(round_t(pt.x), round_t(pt.y));
+            }
+          }
         }
       }
-      fence_async();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord;
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(record), "r"(tps), "r"(2 * kPart) : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      }
-      __syncthreads();
+      __syncthreads();  // (T is read)
     }
   }
-  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 std::mutex g_mu;
