@@ -612,7 +612,7 @@ int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_strea
  * head h / (nv / nk), over a sequence's rows in order:
  *   S = exp(g) S;  S += k (beta (v - S^T k))^T;  o = scale S^T q;
  *   if norm_w: o = o / sqrt(mean o^2 + eps) * norm_w;  if z: o = o * silu(z).
- * Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and 0 <= beta <= 2, g <= 0: beyond
+ * Queries have any length.  Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and 0 <= beta <= 2, g <= 0: beyond
  * that the rule itself grows without bound, and a result may be an infinity or NaN before its f32 form is.
  * State, products with it and sums are f32; out is rounded once.  Sequences of more than 28 rows go over chunks of 64, on
  * the tensor cores, with products of 21 to 22 significand bits and f32 sums: what a row is off by goes by its own value and by what the

@@ -16,8 +16,8 @@
 // of two f16, q and k are f16 already.  f16's exponents take them because a value column is scaled by one power of two, by its largest
 // |exp(G_64) S| or |exp(G_64 - G) U|, m, which goes to 2^8 .. 2^9: with elements of k of at most 1 the state behind is
 // at most 65 m, below 2^15.1, and what f16 drops is below 2^-25, so 2^-33 m.  T and P T are made without their decays, by products of
-// two f16 (|T| is at most 2 then, with lengths of k of at most 1 and 0 <= beta <= 2) and multiplied by them at the end, so that their
-// errors decay too.  Sums of decays are made in fixed point and kept as two f32, so that decays over neighbouring rows,
+// two f16 (|T| is at most 2 then, with lengths of k of at most 1 and 0 <= beta <= 2; rows of P by a power of two each) and multiplied by
+// them at the end, so that their errors decay too.  Sums of decays are made in fixed point and kept as two f32, so that decays over neighbouring rows,
 // differences of large sums, are off by 2^-22 only.
 //
 // First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps:
@@ -937,9 +937,10 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ T and P T
-// [K; Q], and in their place, once their products are in registers, [T; P T]; A's blocks on the diagonal in f32; four heads' decays
+// [K; Q], and in their place, once their products are in registers, [T; P]; A's blocks on the diagonal in f32; four heads' decays; one
+// over the scales of P's rows
 constexpr int kOffDiag = 2 * kPart, kOffHi = kOffDiag + 4 * 16 * kLd * 4, kHeadDecays = 7 * kRows;
-constexpr int kPrepSmem = kOffHi + 4 * kHeadDecays * 4 + 1024;
+constexpr int kOffScale = kOffHi + 4 * kHeadDecays * 4, kPrepSmem = kOffScale + kRows * 4 + 1024;
 
 // The sequence and chunk whose record is x, the whole warp: false where there is none.
 FAK_DEV bool find_chunk(const GdnParams& p, const Records& r, int x, int lane, GdnSeq& d, int& s, int& c) {
@@ -1035,6 +1036,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
   unsigned char* tp = smem;
   const uint32_t kqs = smem_u32(smem), tps = kqs;
   float* diag = reinterpret_cast<float*>(smem + kOffDiag);
+  float* scales = reinterpret_cast<float*>(smem + kOffScale);
 
   // K and Q, 16 threads to a row of 256 bytes; zeros behind the last row
   {
@@ -1141,6 +1143,34 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
           const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
           mma16(*reinterpret_cast<float(*)[4]>(dots[i]), a, b0);
           mma16(*reinterpret_cast<float(*)[4]>(dots[i] + 4), a, b1);
+        }
+      }
+      // Queries are as long as they are: each row of P goes by a power of two of its own, its largest to 2^8 .. 2^9.
+      {
+        const int row = 16 * (3 - w) + g;
+        float most[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          int m, tile, j;
+          place(i, m, tile, j);
+          if (!m) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (j < tile || 8 * (e >> 2) + q2 + (e & 1) <= g + 4 * (e & 2)) most[e >> 1 & 1] = fmaxf(most[e >> 1 & 1], fabsf(dots[i][e]));
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 1));
+          most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 2));
+          const int by = scale_by(most[u]);
+          if ((lane & 3) == 0) scales[row + 8 * u] = two_to(-by);
+#pragma unroll
+          for (int i = 0; i < 5; ++i)
+            if (i > w) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if ((e >> 1 & 1) == u) dots[i][e] *= two_to(by);
+            }
         }
       }
       __syncthreads();
@@ -1307,7 +1337,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int row = 16 * m + 8 * u + g;
-            const float f = hi[3 * kRows + row], hr = hi[row], lr = lo[row];
+            const float f = hi[3 * kRows + row], hr = hi[row], lr = lo[row], down = scales[row];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               if (j == m && e > u) continue;  // above the diagonal: nothing reads it
@@ -1321,7 +1351,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
               }
               const float2 t1 = __half22float2(*reinterpret_cast<const __half2*>(&a.hi[2 * e + u]));
               const float2 t2 = __half22float2(*reinterpret_cast<const __half2*>(&a.lo[2 * e + u]));
-              float2 t = mul2(add2(t1, t2), by), pt = mul2(make_float2(y[i][e][2 * u], y[i][e][2 * u + 1]), by);
+              float2 t = mul2(add2(t1, t2), by), pt = mul2(mul2(make_float2(y[i][e][2 * u], y[i][e][2 * u + 1]), both(down)), by);
               if (j == m && e == u) {  // (a zero that masks is put there: it must not meet an infinity)
                 if (q2 > g) t.x = pt.x = 0.0f;
                 if (q2 + 1 > g) t.y = pt.y = 0.0f;

@@ -134,3 +134,19 @@ def test_a_large_state_that_goes(fak):
         g[10:11] = -float("inf")
         g[100:101] = -100.0
     check(fak, change)
+
+
+@pytest.mark.parametrize("size", [1e-2, 1e-5, 1e3, 2e5])
+def test_queries_of_any_length(fak, size):
+    """Short ones down to f16's smallest steps, and long ones up to its end."""
+    def change(q, k, v, g, beta):
+        q.copy_((q.double() * size).clamp(-65504, 65504))
+    check(fak, change)
+
+
+def test_queries_of_different_lengths(fak):
+    def change(q, k, v, g, beta):
+        q[::3] *= 1e-3
+        q[1::3] *= 1e3
+        q[4::8] = 0
+    check(fak, change)
