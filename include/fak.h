@@ -578,7 +578,9 @@ int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable);
  * rows leaves its slot as it was.  Two sequences of one call in one slot race.  A sequence
  * whose numbers are out of range (row_start as in fak_kv_batch, kv_len negative, slot
  * outside [0, n_slots)) is left out: nothing of it is read or written, and FAK_ERR_DEVICE
- * is recorded. */
+ * is recorded.  (Where a row_start lies below one before it, fak_gdn_attn may leave out
+ * other sequences of more than 28 rows too, and a row that two sequences claim is one of
+ * theirs.) */
 typedef struct {
     int32_t n_seqs;
     const int32_t* row_start; /* device [n_seqs + 1] */

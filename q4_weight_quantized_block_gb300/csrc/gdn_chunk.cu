@@ -415,6 +415,23 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
   }
   const int rows = d.r1 - d.first;
   if (p.few && rows <= p.few) return;  // the steps' kernel's
+  // Where starts fall, two sequences that are in range may have the same records: both are left out.
+  if (!records.dense && p.c.n_seqs > 1) {
+    bool falls = false, same = false;
+    for (int i = threadIdx.x; i < p.c.n_seqs; i += C::threads) falls |= p.c.row_start[i + 1] < p.c.row_start[i];
+    if (__syncthreads_or(falls)) {
+      const int mine = place_of(records, d.r0, s), behind = mine + (rows + kRows - 1) / kRows;
+      for (int i = threadIdx.x; i < p.c.n_seqs; i += C::threads) {
+        const GdnSeq e = gdn_seq(p.c, kv_seq(p.c, i), i);
+        const int n = e.r1 - e.first, at = place_of(records, e.r0, i);
+        same |= i != s && e.ok && n > p.few && at < behind && mine < at + (n + kRows - 1) / kRows;
+      }
+      if (__syncthreads_or(same)) {
+        if (threadIdx.x == 0) atomicCAS(status, 0, FAK_ERR_DEVICE);
+        return;
+      }
+    }
+  }
   const int col0 = slice * C::cols;
   int begin, end;
   chunks_of(p, records, d, s, begin, end);

@@ -1,0 +1,64 @@
+"""fak_gdn_attn and fak_gdn_conv on batches whose numbers are out of range: a sequence comes out right or not at all."""
+import pytest
+
+torch = pytest.importorskip("torch")
+import _gdn as G
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def fak():
+    from q4_weight_quantized_block_gb300 import build
+    build.build()
+    import q4_weight_quantized_block_gb300 as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# starts, and the sequences that are left out besides those whose own bounds fall: sequence s has its records from place
+# start / 64 + s on, one for 64 rows (where there are many sequences, from start / 28 on: disjoint rows never share one)
+FALLING = {
+    # both at 3
+    "one place": ([192, 256, 64, 128], [0, 2]),
+    # 5 to 7, 3 to 5, 7
+    "one place, longer": ([320, 500, 100, 256, 300], [0, 2, 3]),
+    "no place in common": ([300, 400, 0, 100], []),
+    "few rows": ([192, 212, 64, 128], []),
+}
+
+
+@pytest.mark.parametrize("name", list(FALLING))
+@pytest.mark.parametrize("spare", [0, 40])
+def test_starts_that_fall(fak, name, spare):
+    """Sequences of disjoint rows; with spare, sequences without rows behind them."""
+    starts, out = FALLING[name]
+    out = [] if spare else out
+    rows, n = 512, len(starts) - 1
+    lengths = [b - a for a, b in zip(starts, starts[1:])]
+    start = i32(*(starts + [starts[-1]] * spare))
+    kv_len = i32(*([max(m, 0) for m in lengths] + [0] * spare))
+    slot = torch.randperm(n + spare + 2, generator=torch.Generator().manual_seed(3))[:n + spare].to(torch.int32).cuda()
+    q, k, v, g, beta, _, _ = G.inputs(1, 2, rows, 8)
+    state = torch.full((n + spare + 2, 2, 128, 128), NAN, device="cuda")
+    o = torch.full((rows, 2, 128), 7.0, device="cuda")
+    fak.fak_gdn_attn(fak.GDNBatch(start, kv_len, slot), q, k, v, g, beta, state, o, 256)
+    assert fak.fak_device_status() == 7
+    seen = torch.zeros(rows, dtype=torch.bool)
+    for s, m in enumerate(lengths):
+        if m < 0 or s in out:
+            assert bool(state[slot[s]].isnan().all())
+            continue
+        r = slice(starts[s], starts[s + 1])
+        seen[r] = True
+        want, S, most = G.gdn_ref(*(t[r] for t in (q, k, v, g, beta)), torch.zeros_like(state[slot[s]]), 128 ** -0.5)
+        tol = 2.0 ** -20 * m ** 0.5 * most  # (as the operator's other tests have it)
+        assert float((state[slot[s]].double() - S).abs().max()) <= tol
+        assert float((o[r].double() - want).abs().max()) <= tol * 128 ** -0.5 + 2.0 ** -23 * float(want.abs().max())
+    assert bool((o[~seen.cuda()] == 7).all())
+    assert fak.fak_device_status() == 0
