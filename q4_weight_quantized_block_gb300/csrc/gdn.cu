@@ -83,6 +83,10 @@ __global__ void __launch_bounds__(kConvThreads, R == 8 ? 3 : 4) gdn_conv_kernel(
         p.beta[row * p.nv + h] = 1.0f / (1.0f + expf(-b));
       }
     }
+    // numbers out of range are recorded even where no row is looked for with them (by the first block, for all sequences)
+    if (base == 0)
+      for (int s = lane; s < p.c.n_seqs; s += 32)
+        if (!gdn_seq(p.c, kv_seq(p.c, s), s).ok) gdn_record();
     return;
   }
   const int64_t chans = (int64_t)heads * kGdnDim;

@@ -62,3 +62,35 @@ def test_starts_that_fall(fak, name, spare):
         assert float((o[r].double() - want).abs().max()) <= tol * 128 ** -0.5 + 2.0 ** -23 * float(want.abs().max())
     assert bool((o[~seen.cuda()] == 7).all())
     assert fak.fak_device_status() == 0
+
+
+BAD = {
+    "slot of a sequence without rows": ([0, 5, 5, 9], [5, 3, 4], [0, 99, 1]),
+    "negative slot, the last": ([0, 5, 9, 9], [5, 4, 0], [0, 1, -1]),
+    "length of a sequence without rows": ([0, 0, 5, 9], [-1, 5, 4], [2, 0, 1]),
+    "a start that falls, its rows another's": ([0, 9, 4, 9], [9, 4, 5], [0, 1, 2]),
+}
+
+
+@pytest.mark.parametrize("name", list(BAD))
+@pytest.mark.parametrize("rows", [9, 900])
+@pytest.mark.parametrize("spare", [0, 70])
+def test_sequences_that_no_row_leads_to_are_recorded(fak, name, rows, spare):
+    """By both operators, with few rows and many, and among more sequences than a warp looks at together."""
+    starts, lens, slots = BAD[name]
+    if spare:
+        starts, lens, slots = starts + [starts[-1]] * spare, lens + [0] * spare, slots + [3] * spare
+    batch = fak.GDNBatch(i32(*starts), i32(*lens), i32(*slots))
+    x, ba = torch.randn(rows, 512, device="cuda"), torch.randn(rows, 2, device="cuda")
+    q, k = (torch.empty(rows, 1, 128, dtype=torch.float16, device="cuda") for _ in range(2))
+    v = torch.empty(rows, 2, 128, dtype=torch.bfloat16, device="cuda")
+    g, beta = torch.empty(rows, 2, device="cuda"), torch.empty(rows, 2, device="cuda")
+    conv_state, zero = torch.zeros(4, 3, 512, device="cuda"), torch.zeros(2, device="cuda")
+    fak.fak_gdn_conv(batch, x, ba, ba, torch.randn(512, 4, device="cuda"), zero, zero, conv_state, q, k, v, g, beta)
+    assert fak.fak_device_status() == 7
+    q, k, v, g, beta, _, _ = G.inputs(1, 2, rows, 8)
+    fak.fak_gdn_attn(batch, q, k, v, g, beta, torch.zeros(4, 2, 128, 128, device="cuda"), torch.empty(rows, 2, 128, device="cuda"), 9)
+    assert fak.fak_device_status() == 7
+    good = fak.GDNBatch(i32(0, 5, 9), i32(5, 4), i32(0, 1))
+    fak.fak_gdn_conv(good, x, ba, ba, torch.randn(512, 4, device="cuda"), zero, zero, conv_state, q, k, v, g, beta)
+    assert fak.fak_device_status() == 0
