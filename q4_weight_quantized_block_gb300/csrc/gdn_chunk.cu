@@ -1417,11 +1417,14 @@ cudaError_t launch(const GdnParams& p, const ChunkMaps& maps, const Records& rec
   static std::atomic<uint64_t> done{0};
   cudaError_t e = kv_smem_limit(gdn_chunk_kernel<F32>, C::smem, dev, done);
   if (e != cudaSuccess) return e;
-  static const int regs = [] {
+  static std::atomic<int> regs{0};  // (a query that fails is made again by the next call)
+  if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, gdn_chunk_kernel<F32>) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != kRegs) return cudaErrorNotSupported;  // (with fewer, its warps would wait for registers that nobody gives back)
+    e = cudaFuncGetAttributes(&a, gdn_chunk_kernel<F32>);
+    if (e != cudaSuccess) return e;
+    regs.store(a.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < kRegs) return cudaErrorNotSupported;  // (its warps would wait for registers that nobody gives back)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.c.n_seqs * p.nv * C::slices));
   cfg.blockDim = dim3(C::threads);
