@@ -517,6 +517,7 @@ def _gdn_types():
 _GDN_ROWS = struct.Struct("@iiiifqPPPqqqPPPPPPPPP")
 _GDN_ARGS = struct.Struct("@iiiiiffqPPPqqqqqqPPPPPqqPqq")
 _NORM_ARGS = struct.Struct("@iiiiiifffqPPPqqqPPPqq")
+_UNPACKED = struct.error, OverflowError, TypeError, ValueError  # numbers that their fields do not hold
 
 
 def _refuse(status, where):
@@ -554,9 +555,12 @@ def fak_gdn_conv(batch, x, b, a, conv_w, a_log, dt_bias, conv_state, q, k, v, g,
             or k.get_device() != d or v.get_device() != d or g.get_device() != d or beta.get_device() != d
             or _current_device() != d):
         _refuse(8, "fak_gdn_conv")
-    args = _GDN_ROWS.pack(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nk, nv, cs[0], eps, rows, x.data_ptr(), b.data_ptr(),
-                          a.data_ptr(), xr, br, ar, conv_w.data_ptr(), a_log.data_ptr(), dt_bias.data_ptr(),
-                          conv_state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr())
+    try:
+        args = _GDN_ROWS.pack(FAK_ROWS_F32 if dtype == f32 else FAK_ROWS_BF16, nk, nv, cs[0], eps, rows, x.data_ptr(),
+                              b.data_ptr(), a.data_ptr(), xr, br, ar, conv_w.data_ptr(), a_log.data_ptr(), dt_bias.data_ptr(),
+                              conv_state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr())
+    except _UNPACKED:
+        _refuse(1, "fak_gdn_conv")
     _check(lib.fak_gdn_conv(batch.ref, args, _stream(stream)), "fak_gdn_conv")
 
 
@@ -590,11 +594,14 @@ def fak_gdn_attn(batch, q, k, v, g, beta, state, out, max_q, scale=None, z=None,
             or (z is not None and z.get_device() != d) or (norm_w is not None and norm_w.get_device() != d)
             or _current_device() != d):
         _refuse(8, "fak_gdn_attn")
-    args = _GDN_ARGS.pack(nk, nv, max_q, FAK_ROWS_F32 if kind == f32 else FAK_ROWS_BF16, ss[0],
-                          128 ** -0.5 if scale is None else scale, eps, rows, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh,
-                          kr, kh, vr, vh, g.data_ptr(), beta.data_ptr(), state.data_ptr(),
-                          0 if norm_w is None else norm_w.data_ptr(), 0 if z is None else z.data_ptr(), zr, zh, out.data_ptr(),
-                          outr, outh)
+    try:
+        args = _GDN_ARGS.pack(nk, nv, max_q, FAK_ROWS_F32 if kind == f32 else FAK_ROWS_BF16, ss[0],
+                              128 ** -0.5 if scale is None else scale, eps, rows, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr,
+                              qh, kr, kh, vr, vh, g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+                              0 if norm_w is None else norm_w.data_ptr(), 0 if z is None else z.data_ptr(), zr, zh,
+                              out.data_ptr(), outr, outh)
+    except _UNPACKED:
+        _refuse(1, "fak_gdn_attn")
     _check(lib.fak_gdn_attn(batch.ref, args, _stream(stream)), "fak_gdn_attn")
 
 
@@ -648,9 +655,12 @@ def fak_residual_norm(h, y=None, n=None, w=None, post_norm=False, y_w=None, gate
         gp, gc = gate.data_ptr(), 0 if d == 1 else gc
     if away:
         _refuse(8, "fak_residual_norm")
-    args = _NORM_ARGS.pack(kinds[0], kinds[1], kinds[2], d, 1 if post_norm else 0, FAK_GATE_SIGMOID if gate_sigmoid else FAK_GATE_LINEAR,
-                           scale, eps, gain_offset, rows, at[0], at[1], at[2], steps[0], steps[1], steps[2], gains[0], gains[1],
-                           gp, gr, gc)
+    try:
+        args = _NORM_ARGS.pack(kinds[0], kinds[1], kinds[2], d, 1 if post_norm else 0,
+                               FAK_GATE_SIGMOID if gate_sigmoid else FAK_GATE_LINEAR, scale, eps, gain_offset, rows, at[0], at[1],
+                               at[2], steps[0], steps[1], steps[2], gains[0], gains[1], gp, gr, gc)
+    except _UNPACKED:
+        _refuse(1, "fak_residual_norm")
     _check(lib.fak_residual_norm(args, _stream(stream)), "fak_residual_norm")
 
 

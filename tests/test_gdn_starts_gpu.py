@@ -1,4 +1,5 @@
-"""fak_gdn_attn and fak_gdn_conv on batches whose numbers are out of range: a sequence comes out right or not at all."""
+"""The Gated DeltaNet operators and the norm around a block where numbers are out of range: a sequence comes out right or not at
+all, a call's arguments are refused as others are."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -94,3 +95,25 @@ def test_sequences_that_no_row_leads_to_are_recorded(fak, name, rows, spare):
     good = fak.GDNBatch(i32(0, 5, 9), i32(5, 4), i32(0, 1))
     fak.fak_gdn_conv(good, x, ba, ba, torch.randn(512, 4, device="cuda"), zero, zero, conv_state, q, k, v, g, beta)
     assert fak.fak_device_status() == 0
+
+
+@pytest.mark.parametrize("over", [dict(max_q=1 << 31), dict(max_q=2.5), dict(scale=1e39), dict(scale="1"), dict(eps=1e300), dict(eps=None)])
+def test_numbers_that_the_call_cannot_hold_are_refused(fak, over):
+    """By the binding, with its own error."""
+    batch = fak.GDNBatch(i32(0, 3), i32(3), i32(0))
+    q, k, v, g, beta, _, _ = G.inputs(1, 2, 3, 8)
+    state, o, h = torch.zeros(1, 2, 128, 128, device="cuda"), torch.empty(3, 2, 128, device="cuda"), torch.ones(3, 64, device="cuda")
+    with pytest.raises(fak.FakError) as e:
+        fak.fak_gdn_attn(batch, q, k, v, g, beta, state, o, **{**dict(max_q=3), **over})
+    assert e.value.status == 1
+    if "max_q" in over:
+        return
+    with pytest.raises(fak.FakError) as e:
+        fak.fak_residual_norm(h, h.clone(), h.clone(), **over)
+    assert e.value.status == 1
+    if "eps" in over:
+        x, ba, n = torch.randn(3, 512, device="cuda"), torch.randn(3, 2, device="cuda"), torch.zeros(2, device="cuda")
+        with pytest.raises(fak.FakError) as e:
+            fak.fak_gdn_conv(batch, x, ba, ba, torch.randn(512, 4, device="cuda"), n, n, torch.zeros(1, 3, 512, device="cuda"), q, k, v, g,
+                             beta, **over)
+        assert e.value.status == 1
