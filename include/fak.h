@@ -639,7 +639,7 @@ typedef struct {
     const float* norm_w;        /* device [128], 16-byte aligned; NULL: no norm */
     const float* z;             /* device f32, any strides (wide loads where vectors stand on 16 bytes); NULL: no gate */
     int64_t z_row, z_head;
-    void* out;                  /* device, 16-byte aligned, strides too */
+    void* out;                  /* device, 16-byte aligned, strides too, which are no smaller than a vector */
     int64_t out_row, out_head;
 } fak_gdn_args;
 int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* args, fak_stream_t stream);
@@ -657,7 +657,7 @@ int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable);
  * in f32 (n from h before h's own rounding), each result rounded once.  gain_offset is 0, or 1 for gains
  * stored as w - 1; a NULL gain is a gain of 1, whatever the offset.  y NULL: h stays as it is (and is not
  * written), n is its norm; n NULL: no norm.  gate is f32: one value for each value, channel or row, by strides
- * (gate_row, gate_col; a stride of 0 repeats).  h, y, n and gate do not overlap.
+ * (gate_row, gate_col; a stride of 0 repeats).  h, y, n and gate do not overlap, nor do rows of what is written.
  * d is 1 to 32768.  Rows whose starts and strides are multiples of 16 bytes (and d of 4) take wide loads;
  * any others are as right.  One launch. */
 enum { FAK_GATE_LINEAR = 0, FAK_GATE_SIGMOID = 1 };

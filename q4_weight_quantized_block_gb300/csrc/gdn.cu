@@ -429,6 +429,8 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   if (!fits(p.q_row, a->rows, 2) || !fits(p.q_head, a->nk, 2) || !fits(p.k_row, a->rows, 2) || !fits(p.k_head, a->nk, 2) ||
       !fits(p.v_row, a->rows, 2) || !fits(p.v_head, a->nv, 2))
     return FAK_ERR_INVALID_ARG;
+  const auto meet = [](int64_t stride, int64_t n) { return n > 1 && stride > -kGdnDim && stride < kGdnDim; };  // vectors written over one another
+  if (meet(a->out_row, a->rows) || meet(a->out_head, a->nv)) return FAK_ERR_INVALID_ARG;
   if ((bits & 15) || (two & 7) || (out & (a->out_type == FAK_ROWS_F32 ? 3 : 7)) || 
       (((uintptr_t)a->g | (uintptr_t)a->beta | (uintptr_t)a->z) & 3))
     return FAK_ERR_ALIGN;

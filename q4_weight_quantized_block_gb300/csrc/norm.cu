@@ -195,6 +195,9 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
                          (yb ? 0 : (uintptr_t)a->y) | (nb ? 0 : (uintptr_t)a->n);
   const uintptr_t all = (uintptr_t)a->h | (uintptr_t)a->y | (uintptr_t)a->n;
   if ((f32s & 3) || (all & 1)) return FAK_ERR_ALIGN;
+  // rows that are written over one another
+  const auto meet = [&](int64_t row) { return a->rows > 1 && row > -(int64_t)a->d && row < a->d; };
+  if ((a->h && a->y && meet(a->h_row)) || (a->n && meet(a->n_row))) return FAK_ERR_INVALID_ARG;
   if (a->rows == 0 || (!a->y && !a->n)) return FAK_OK;
   const int st = kv_device(nullptr, nullptr);
   if (st != FAK_OK) return st;
