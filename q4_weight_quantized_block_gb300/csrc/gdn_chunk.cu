@@ -436,10 +436,8 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
   int begin, end;
   chunks_of(p, records, d, s, begin, end);
   if (records.begin == 0)
-    for (int i = threadIdx.x; i < (d.first - d.r0) * (C::cols / 4); i += C::threads) {
-      const int row = d.r0 + i / (C::cols / 4);
-      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * (i % (C::cols / 4)), gdn_zero4());
-    }
+    for (int row = d.r0 + (int)threadIdx.x / (C::cols / 4); row < d.first; row += C::threads / (C::cols / 4))
+      gdn_put4(p.out, p.out_bf16, row * p.out_row + h * p.out_head + col0 + 4 * ((int)threadIdx.x % (C::cols / 4)), gdn_zero4());
   const int chunks = end - begin;  // counted from 0 below
   if (chunks <= 0) return;
   const int first_row = d.first + begin * kRows, rows_left = rows - begin * kRows;
