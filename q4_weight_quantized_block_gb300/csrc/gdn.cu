@@ -66,6 +66,12 @@ __global__ void __launch_bounds__(kConvThreads, R == 8 ? 3 : 4) gdn_conv_kernel(
   const int64_t base = (int64_t)blockIdx.x * R;
   const int64_t end = min(base + R, p.c.rows);
   if (head == heads) {
+    // numbers out of range are recorded even where no row is looked for with them (by the first block, for all sequences)
+    if (base == 0) {
+#pragma unroll 4
+      for (int s = lane; s < p.c.n_seqs; s += 32)
+        if (!gdn_seq(p.c, kv_seq(p.c, s), s).ok) gdn_record();
+    }
     for (int64_t row = base; row < end; ++row) {
       int s;
       KvSeq q = kv_locate(p.c, row, lane, s);
@@ -84,10 +90,6 @@ __global__ void __launch_bounds__(kConvThreads, R == 8 ? 3 : 4) gdn_conv_kernel(
         p.beta[row * p.nv + h] = 1.0f / (1.0f + expf(-b));
       }
     }
-    // numbers out of range are recorded even where no row is looked for with them (by the first block, for all sequences)
-    if (base == 0)
-      for (int s = lane; s < p.c.n_seqs; s += 32)
-        if (!gdn_seq(p.c, kv_seq(p.c, s), s).ok) gdn_record();
     return;
   }
   const int64_t chans = (int64_t)heads * kGdnDim;
