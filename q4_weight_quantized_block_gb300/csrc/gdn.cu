@@ -366,7 +366,7 @@ extern "C" int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* r, f
   if (r->type != FAK_ROWS_F32 && r->type != FAK_ROWS_BF16) return FAK_ERR_INVALID_ARG;
   if (r->nk < 1 || r->nv < 1 || r->nk > (1 << 16) || r->nv > (1 << 16) || r->rows < 0 || r->rows > 0x7fffffff) return FAK_ERR_SHAPE;
   if (r->rows && (!r->x || !r->b || !r->a || !r->q || !r->k || !r->v || !r->g || !r->beta)) return FAK_ERR_INVALID_ARG;
-  if (!r->conv_w || !r->a_log || !r->dt_bias || !r->conv_state || !(r->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
+  if (!r->conv_w || !r->a_log || !r->dt_bias || !r->conv_state || !(r->eps >= 0.0f) || !std::isfinite(r->eps)) return FAK_ERR_INVALID_ARG;
   const int elem = r->type == FAK_ROWS_F32 ? 4 : 2;
   p.x_row = kv_stride(r->x_row, r->rows);
   p.b_row = kv_stride(r->b_row, r->rows);
@@ -410,7 +410,7 @@ extern "C" int fak_gdn_attn(const fak_gdn_batch* batch, const fak_gdn_args* a, f
   if (a->nk < 1 || a->nv < 1 || a->nv > 65535 || a->nv % a->nk || a->rows < 0 || a->rows > 0x7fffffff || a->max_q < 0 ||
       (int64_t)batch->n_seqs * a->nv > 0x3fffffff)
     return FAK_ERR_SHAPE;
-  if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !(a->eps >= 0.0f)) return FAK_ERR_INVALID_ARG;
+  if (!(a->scale > 0.0f) || !std::isfinite(a->scale) || !(a->eps >= 0.0f) || !std::isfinite(a->eps)) return FAK_ERR_INVALID_ARG;
   if (a->rows && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->out)) return FAK_ERR_INVALID_ARG;
   if (!a->state) return FAK_ERR_INVALID_ARG;
   p.q_row = kv_stride(a->q_row, a->rows);

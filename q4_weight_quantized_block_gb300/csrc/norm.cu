@@ -180,7 +180,7 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
     if (t != FAK_ROWS_F32 && t != FAK_ROWS_BF16) return FAK_ERR_INVALID_ARG;
   if (a->gate_kind != FAK_GATE_LINEAR && a->gate_kind != FAK_GATE_SIGMOID) return FAK_ERR_INVALID_ARG;
   if (a->d < 1 || a->d > 32768 || a->rows < 0 || a->rows > 0x7fffffff) return FAK_ERR_SHAPE;
-  if (!(a->eps >= 0.0f) || !std::isfinite(a->scale) || !std::isfinite(a->gain_offset) || (a->gate_col != 0 && a->gate_col != 1))
+  if (!(a->eps >= 0.0f) || !std::isfinite(a->eps) || !std::isfinite(a->scale) || !std::isfinite(a->gain_offset) || (a->gate_col != 0 && a->gate_col != 1))
     return FAK_ERR_INVALID_ARG;
   if (a->rows && !a->h) return FAK_ERR_INVALID_ARG;
   NormParams p;
