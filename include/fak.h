@@ -618,7 +618,7 @@ int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_strea
  * that the rule itself grows without bound, and a result may be an infinity or NaN before its f32 form is.
  * State, products with it and sums are f32; out is rounded once.  Sequences of more than 28 rows go over chunks of 64, on
  * the tensor cores, with products of 21 to 22 significand bits and f32 sums: what a row is off by goes by its own value and by what the
- * rows before it have brought to the same column, less what has decayed, whatever the rows behind it hold.  What they need besides, 33,536 bytes for 64 rows of a
+ * rows before it have brought to the same column, less what has decayed (to below 2^-126: all of it), whatever the rows behind it hold.  What they need besides, 33,792 bytes for 64 rows of a
  * head, comes from the library-owned pool of the batched GEMV's scratch, freed on the same stream (kept for later calls; a
  * graph memory node under stream capture): at most 1 GiB at a time (or one chunk's of all heads), longer calls go in parts.
  * FAK_ERR_NOMEM, and nothing done, if it cannot be had.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds

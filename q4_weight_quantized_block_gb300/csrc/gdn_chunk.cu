@@ -10,31 +10,34 @@
 // goes through a sequence's chunks.
 //
 // Precision.  The state is held in f32 registers; products keep 21 to 22 bits, and each is off by no more than that part of what its
-// own row and column have: of a row's value, or of what the rows before brought to the column and the decays have left.  R is
-// as large as a row's values, which differ at will, and T and P T shrink by the decays: both go as two tf32 each (the small
-// parts' product is left out), which have f32's exponents.  The state, and U by the decays to the chunk's end, go as the sum
-// of two f16, q and k are f16 already.  f16's exponents take them because a value column is scaled by one power of two, by its largest
-// |exp(G_64) S| or |exp(G_64 - G) U|, m, which goes to 2^8 .. 2^9: with elements of k of at most 1 the state behind is
-// at most 65 m, below 2^15.1, and what f16 drops is below 2^-25, so 2^-33 m.  T and P T are made without their decays, by products of
-// two f16 (|T| is at most 2 then, with lengths of k of at most 1 and 0 <= beta <= 2; rows of P by a power of two each) and multiplied by
-// them at the end, so that their errors decay too.  Sums of decays are made in fixed point and kept as two f32, so that decays over neighbouring rows,
-// differences of large sums, are off by 2^-22 only.
+// own row and column have: of a row's value, or of what the rows before brought to the column and the decays have left.
+//   S, and U by the decays to the chunk's end, go as the sum of two f16 (q and k are f16 already), a value column scaled by one
+// power of two: by m, the largest of exp(G_64) |S| and exp(G_64 - G) |V|, which goes to 2^6 .. 2^7.  With lengths of k of at most 1 and
+// 0 <= beta <= 2 the U so decayed is at most 282 m and the S behind 140 m, below 2^15.2, and what f16 drops is below 2^-25, so 2^-31 m.
+//   R is as large as a row's values, which differ at will.  It goes as two f16, the second times 2^11, where these hold what the
+// column's rows need (halves_hold), T and P T times 2^14 in the same way; products with second parts have sums of their own.  A column
+// of a million times a row's own value still goes so; where one does not, the warp takes the chunk's rows one by one in f32.
+//   T and P T are made without their decays, by products of two f16 (|T| is at most 2 then; rows of P are by a power of two of a
+// query of length 1 to 2) and multiplied by them at the end, so that their errors decay too.  Sums of decays are made in fixed
+// point and kept as two f32, so that decays over neighbouring rows, differences of large sums, are off by 2^-22 only; those over a
+// stretch of rows that are below 2^-126 are zeros.
 //
-// First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps:
-// inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, in place of A, and P T by m16n8k16
-// instructions; both by their decays to the record.  Steps that wait for one another on 64 x 64 matrices: 118 us for 128 chunks of 48
-// heads on 16 key heads; four blocks to an SM hide part of it.
+// First kernel: a block takes a chunk and a key head, whose K K^T and Q K^T its value heads share, four warps: A and P;
+// inverses of 16 x 16 blocks by substitution, joined to 32 and to 64, in place of A, and P T, in place of P, by m16n8k16
+// instructions; both by their decays.  Steps that wait for one another on 64 x 64 matrices: 118 us for 128 chunks of 48 heads on 16 key
+// heads, of which the records' 208 MB are 31 us; four blocks to an SM hide part of it.
 //
 // Second kernel: two CTAs to a head, 64 value columns each; a warp holds 16 columns, as S^T in the accumulators of m16n8k16 (64
 // registers a thread).  Those are laid out as the next product's first operand is, so that S^T, R^T and U^T go from product
-// to product in registers: S^T K^T, R^T T^T (m16n8k8), U^T K.  A second warp to the same columns takes S^T and R^T from shared
+// to product in registers: S^T K^T, R^T T^T, U^T K.  A second warp to the same columns takes S^T and R^T as operands from shared
 // memory and makes what only the output wants: S^T Q^T, R^T (P T)^T, the norm (its sums of squares from all eight such warps of
-// the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  364
-// instructions of 8 cycles of the tensor cores for the state and 236 for the output, 4,800 cycles a chunk on each of an SM's four
-// parts; a chunk takes 7,900 (4.1 us): one warp's way through three products, the splitting into parts and the scales, and shared
-// memory, whose operands a warp of 16 columns takes for itself alone.
+// the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  316
+// instructions of 8 cycles of the tensor cores for the state and 188 for the output, 4,032 cycles a chunk on each of an SM's four
+// parts; a chunk takes 6,700 (3.5 us): one warp's way through three products, the splitting into f16 and the scales, and shared
+// memory, whose operands a warp of 16 columns takes for itself alone.  (R, T and P T as two tf32 each, which hold any column: 521 us
+// for a prompt's 128 chunks in place of 448.)
 //
-// What did not help (measured with R, T and P T as two f16, a chunk of 6,000 cycles then): the same products by tcgen05, 64 columns
+// What did not help (measured with R, T and P T as two f16 under one scale, which hold less; a chunk of 6,000 cycles then): the same products by tcgen05, 64 columns
 // to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through shared memory for each of three products that wait for one
 // another, some 700 cycles for a product and as many for its operand); one CTA to a head with eight warps that make their outputs
 // too (12,700 for both halves of a head); two warps to the same columns, each with half of the keys and rows (6,400 to 7,000: what
@@ -65,16 +68,16 @@ namespace {
 constexpr int kRows = 64;  // of a chunk
 constexpr int kPrepThreads = 128;
 constexpr int kLd = 20;  // f32 blocks of 16 x 16 in shared memory: rows of 80 bytes
-constexpr int kPart = 16384;   // from a matrix's first parts to its second: 128 rows of 64 f16
-constexpr int kPanel = 16384;  // 32 columns of [T; P T] in f32: 128 rows of 128 bytes
+constexpr int kPart = 16384;  // from a matrix's first parts to its second: 128 rows of 64 f16
 
-// What a chunk's rows decay by, and their strengths: behind [T; P T], in a chunk's record for a head.
+// What a chunk's rows decay by, and their strengths: behind [T; P T], two parts, in a chunk's record for a head.
 struct Decays {
   float keep[kRows];  // exp G_t
   float left[kRows];  // exp(G_64 - G_t)
   float beta[kRows];
+  float up[kRows];    // what the rows of P T are times: powers of two
 };
-constexpr int kRecord = 2 * kPanel + (int)sizeof(Decays);
+constexpr int kRecord = 2 * kPart + (int)sizeof(Decays);
 static_assert(kRecord % 16 == 0, "bulk copies");
 
 // Where records stand.  dense: chunk c of a sequence s, begin <= c < begin + length, at s * length + c - begin.  Else a sequence
@@ -112,15 +115,16 @@ struct C {
   static constexpr int slices = kGdnDim / cols;                     // CTAs of a head
   static constexpr int threads = 64 * NW + 128;
   static constexpr int off_kq = 0;                                  // two stages of [K; Q]: two panels of 128 rows
-  static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two panels
-  static constexpr int off_v = off_tp + 4 * kPanel;                 // V: panels of 64 columns, 128 bytes
-  static constexpr int off_frag = off_v + kRows * cols * 2;         // each warp's S (two f16) and R (f32) as operands
+  static constexpr int off_tp = off_kq + 2 * 32768;                 // two stages of [T; P T], two parts
+  static constexpr int off_v = off_tp + 4 * kPart;                 // V: panels of 64 columns, 128 bytes
+  static constexpr int off_frag = off_v + kRows * cols * 2;         // each warp's S (8) and R (4) as operands, two parts
   static constexpr int off_z = off_frag + NW * 12 * 1024;           // z: panels of 32 columns, 128 bytes
   static constexpr int off_out = off_z + kRows * cols * 4;          // the output, f32 or bf16: panels of 128 bytes
   static constexpr int off_dec = off_out + kRows * cols * 4;
   static constexpr int off_sum = off_dec + 2 * (int)sizeof(Decays);  // sums of squares [2][8][64], then 1 / norms [NW][64]
   static constexpr int off_down = off_sum + (2 * 8 + NW) * kRows * 4;  // one over the columns' scales
-  static constexpr int off_bar = off_down + cols * 4;
+  static constexpr int off_by = off_down + cols * 4;                // the scales of R's columns, then the warps' ways
+  static constexpr int off_bar = off_by + cols * 4 + 16;
   static constexpr int smem = off_bar + 128 + 1024;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-block limit");
 };
@@ -207,6 +211,17 @@ FAK_DEV void split_half(float x, float y, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
 }
 
+// Two f32 as the sum of two pairs of f16, the second times 2^11: the second has f16's full exponents, and what both drop is below 2^-36.
+FAK_DEV void split_wide(float2 x, uint32_t& hi, uint32_t& lo) {
+  const float2 y = mul2(x, both(2048.0f));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x.y), "f"(x.x));
+  float a, b;
+  asm("{\n .reg .b16 p, q, m;\n mov.b32 {p, q}, %2;\n mov.b16 m, 0xE800;\n fma.rn.f32.f16 %0, p, m, %3;\n fma.rn.f32.f16 %1, q, m, %4;\n}"
+      : "=f"(a), "=f"(b)
+      : "r"(hi), "f"(y.x), "f"(y.y));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
+}
+
 // Columns of a row (from a multiple of 8 on) of a tile of f16 parts, its panels of 64 columns `panel` bytes apart, the
 // second part `part` bytes behind the first.  Every value is made before the first is stored, so that none waits for a store's turn.
 template <int N>
@@ -266,13 +281,18 @@ FAK_DEV void turn_b(FragB& b, const float (&c)[4]) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(b.lo[i]) : "r"(lo));
   }
 }
-// sign * two products' 16 x 8, beside each other, both parts, at rows r0 .. +15, columns 8 j .. +15 of a tile
-FAK_DEV void put_tiles(uint32_t tile, int r0, int j, const float (&a)[4], const float (&b)[4], float sign, int lane) {
+// Two products' 16 x 8, beside each other, both parts, at rows r0 .. +15, columns 8 j .. +15 of a tile (WIDE: as split_wide has them).
+template <bool WIDE>
+FAK_DEV void put_tiles(uint32_t tile, int r0, int j, const float (&a)[4], const float (&b)[4], int lane) {
   uint32_t hi[4], lo[4];
-  split_half(sign * a[0], sign * a[1], hi[0], lo[0]);
-  split_half(sign * a[2], sign * a[3], hi[1], lo[1]);
-  split_half(sign * b[0], sign * b[1], hi[2], lo[2]);
-  split_half(sign * b[2], sign * b[3], hi[3], lo[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* x = (i < 2 ? a : b) + 2 * (i & 1);
+    if constexpr (WIDE)
+      split_wide(make_float2(x[0], x[1]), hi[i], lo[i]);
+    else
+      split_half(x[0], x[1], hi[i], lo[i]);
+  }
   const int row = r0 + (lane & 15);
   const uint32_t at = tile + row * 128 + (((j + (lane >> 4)) ^ (row & 7)) << 4);
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
@@ -325,75 +345,25 @@ FAK_DEV void split_a(uint32_t (&hi)[4], uint32_t (&lo)[4], const float2 (&x)[2],
   split_half(y[0].x, y[0].y, hi[2], lo[2]);
   split_half(y[1].x, y[1].y, hi[3], lo[3]);
 }
-// Where the columns 8 at + 2 q and the next of a row of [T; P T] stand: 32 bytes of eight columns, those of four rows in turn on
-// all banks.
-FAK_DEV int pair_at(int row, int at, int q) { return (at >> 2) * kPanel + row * 128 + (((at & 3) ^ (row & 3)) << 5) + 8 * q; }
-// Operands of m16n8k8 as two tf32, so that they keep their own exponents: of T, which has 23 bits (the first part rounded, the
-// second exact), and of R (the first 11 bits and the next 11).  NaN and infinities stay what they are in the first parts.
-FAK_DEV void split_t(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
-FAK_DEV void split_r(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
-}
-// To 23 bits (as split_t wants it, which would carry a NaN's last bits into its sign).
-FAK_DEV float round_t(float x) { return x == x ? __uint_as_float((__float_as_uint(x) + 1u) & ~1u) : __uint_as_float(0x7fc00000u); }
-FAK_DEV void mma8(float2 (&c)[2], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-// acc += R^T T^T for one warp's 16 columns, T (or P T) lower triangular from `t` on: tiles of 8 rows by 8, those on and below
-// the diagonal.  r(j): rows 8 j .. of R, an accumulator's values in the order of an operand A, columns 2 q and 2 q + 1 of the
-// product before being k = q and q + 4 here.
-template <typename F>
-FAK_DEV void triangle(float2 (&acc)[8][2], F r, const unsigned char* t, int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    uint32_t rh[2][4], rl[2][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 x = r(i + e);
-      split_r(x.x, rh[e][0], rl[e][0]);
-      split_r(x.y, rh[e][1], rl[e][1]);
-      split_r(x.z, rh[e][2], rl[e][2]);
-      split_r(x.w, rh[e][3], rl[e][3]);
-    }
-#pragma unroll
-    for (int j = i; j < 8; j += 4) {
-      uint32_t th[2][4][2], tl[2][4][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (j + u >= 8 || i + e > j + u) continue;
-          const float2 x = *reinterpret_cast<const float2*>(t + pair_at(8 * (j + u) + (lane >> 2), i + e, lane & 3));
-          split_t(x.x, th[e][u][0], tl[e][u][0]);
-          split_t(x.y, th[e][u][1], tl[e][u][1]);
-        }
-#pragma unroll
-      for (int w = 0; w < 3; ++w)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (j + u >= 8 || i + e > j + u) continue;
-            mma8(acc[j + u], w == 0 ? rl[e] : rh[e], w == 1 ? tl[e][u] : th[e][u]);
-          }
-    }
-  }
-}
 // A row of 128 bytes' 16-byte piece in a tile of 128-byte swizzle.
 FAK_DEV uint32_t piece(int row, int at) { return row * 128 + ((at ^ (row & 7)) << 4); }
 
-// 2^by for a column whose largest magnitude is m = 2^e 1.f, which goes to 2^8 1.f (zeros and infinities: as they are)
+// 2^by for a column whose largest magnitude is m = 2^e 1.f, which goes to 2^6 1.f (zeros and infinities: as they are)
 FAK_DEV int scale_by(float m) {
   const int e = (int)(__float_as_uint(m) >> 23);
-  return e == 0 || e == 255 ? 0 : min(max(135 - e, -120), 120);
+  return e == 0 || e == 255 ? 0 : min(max(133 - e, -120), 120);
 }
 FAK_DEV float two_to(int by) { return __uint_as_float((uint32_t)(127 + by) << 23); }
+
+// Whether f16 parts (split_wide's) hold a column of R, and its scale: m the largest of the column's |S| and |V|, `least` the least that a
+// row of it goes by: its |V|, or what is left of rows before.  m goes to 2^10 .. 2^11, so that R, at most 25 m, stays below 2^15.7,
+// and the parts drop 2^-46 m of it; of T, times 2^14, 2^-50.  `least` has to be 2^-22 m, for this to be no more than 2^-21 of it
+// (a zero is not, but where all are), and m a number from 2^-100 on.
+FAK_DEV bool halves_hold(float m, float least, int& by) {
+  const int e = (int)(__float_as_uint(m) >> 23);
+  by = m == 0.0f ? 0 : 137 - e;
+  return m == 0.0f || (e >= 27 && e < 255 && least >= m * 2.384185791015625e-7f);
+}
 
 template <bool F32>
 __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_constant__ GdnParams p,
@@ -490,6 +460,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         S[i][u] = empty ? both(0.0f) : make_float2(at[0], at[kGdnDim]);
       }
     uint32_t v[4][4];  // of the next chunk: rows 16 i + q2 and the next, + 8; columns g, g + 8
+    float most_v[2], least_v[2];  // of its columns: the largest and the smallest magnitude
     auto fetch_v = [&](int c) {
       wait(kLandV, c);
       const uint32_t tile = base + C::off_v + (warp >> 2) * kRows * 128;
@@ -498,14 +469,37 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         ldsm4_trans(v[i], tile + piece(16 * i + (lane & 7) + ((lane >> 4) << 3), (2 * warp + ((lane >> 3) & 1)) & 7));
       arrive(kVFree);
       const int have = rows_left - c * kRows;
+      uint32_t hi[2] = {0, 0}, lo[2] = {0x7f807f80u, 0x7f807f80u};
+      auto look = [&](uint32_t x, uint32_t y, int u) {  // two rows' magnitudes
+        asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(hi[u]) : "r"(x));
+        asm("min.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(lo[u]) : "r"(y));
+      };
       if (have < kRows) {  // what stands behind the last row is another's, whatever it holds
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int row = 16 * i + 8 * (u >> 1) + q2;
-            v[i][u] = row + 1 < have ? v[i][u] : row < have ? v[i][u] & 0xffffu : 0;
+            const uint32_t there = row + 1 < have ? 0xffffffffu : row < have ? 0xffffu : 0;
+            v[i][u] &= there;
+            look(v[i][u], v[i][u] | (~there & 0x7f807f80u), u & 1);
           }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) look(v[i][u], v[i][u], u & 1);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float2 a = bf16_pair(hi[u]), b = bf16_pair(lo[u]);
+        most_v[u] = fmaxf(fabsf(a.x), fabsf(a.y));
+        least_v[u] = fminf(fabsf(b.x), fabsf(b.y));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          most_v[u] = fmaxf(most_v[u], __shfl_xor_sync(0xffffffffu, most_v[u], o));
+          least_v[u] = fminf(least_v[u], __shfl_xor_sync(0xffffffffu, least_v[u], o));
+        }
       }
     };
     auto most_of = [&](float& a, float& b) {  // over the four lanes of columns g and g + 8
@@ -535,14 +529,112 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
 
     uint4* frag = reinterpret_cast<uint4*>(smem + C::off_frag) + warp * 24 * 32 + lane;
     float* downs = reinterpret_cast<float*>(smem + C::off_down) + 16 * warp;
+    int *bys = reinterpret_cast<int*>(smem + C::off_by) + 16 * warp, *ways = reinterpret_cast<int*>(smem + C::off_by) + C::cols + warp;
+    // Where a row's value alone is too little of its column (halves_hold): the values to the place of R, in the order of the output's
+    // accumulators, and the decays of rows lane and lane + 32; then row by row by the least that value and what is left of those
+    // before come to.
+    auto look_closer = [&](int c, float (&by_row)[2]) {
+      const int have = min(kRows, rows_left - c * kRows);
+      const float* gates = p.g + (int64_t)(first_row + c * kRows) * p.nv + h;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) by_row[i] = expf(gates[(int64_t)min(lane + 32 * i, have - 1) * p.nv]);
+      float* o = reinterpret_cast<float*>(frag - lane + 16 * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 a = bf16_pair(v[i >> 1][2 * (i & 1)]), b = bf16_pair(v[i >> 1][2 * (i & 1) + 1]);
+        *reinterpret_cast<float4*>(o + i * 128 + 16 * g + 2 * q2) = make_float4(a.x, b.x, a.y, b.y);
+      }
+      __syncwarp();
+      // column lane & 15
+      const int from = 4 * (lane & 7), u = lane >> 3 & 1;
+      const float s0 = __shfl_sync(0xffffffffu, ms[0] * down[0], from), s1 = __shfl_sync(0xffffffffu, ms[1] * down[1], from);
+      const float v0 = __shfl_sync(0xffffffffu, most_v[0], from), v1 = __shfl_sync(0xffffffffu, most_v[1], from);
+      float here = u ? s1 : s0, least = __uint_as_float(0x7f800000u);
+      const float most = fmaxf(here, u ? v1 : v0);
+#pragma unroll 4
+      for (int t = 0; t < have; ++t) {
+        const float e = __shfl_sync(0xffffffffu, t < 32 ? by_row[0] : by_row[1], t & 31);
+        here = fmaxf(fabsf(o[(t >> 3) * 128 + 16 * (lane & 7) + 2 * (t & 7) + u]), e * here);
+        least = fminf(least, here);
+      }
+      int by;
+      return (bool)__all_sync(0xffffffffu, halves_hold(most, least, by));
+    };
+    // A chunk's rows one by one in f32, as gdn_step_kernel has them: where f16 parts do not hold R.  The rows' outputs go to their values'
+    // places.  (22 us for 64 rows, whose way by f16 parts takes 3.6.)
+    auto rows_one_by_one = [&](int c, const Decays* dec, const float (&by_row)[2]) {
+      const int have = min(kRows, rows_left - c * kRows);
+      const unsigned char* kq = smem + C::off_kq + (c & 1) * 32768;
+      float* o = reinterpret_cast<float*>(frag - lane + 16 * 32) + 16 * g;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) S[i][u] = mul2(S[i][u], both(down[u]));
+#pragma unroll 1
+      for (int t = 0; t < have; ++t) {
+        float2* here = reinterpret_cast<float2*>(o + (t >> 3) * 128 + 2 * (t & 7));
+        const float e = __shfl_sync(0xffffffffu, t < 32 ? by_row[0] : by_row[1], t & 31), beta = dec->beta[t];
+        const float x[2] = {here->x, here->y};
+        float2 k[16], y[2][2] = {};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          k[i] = __half22float2(*reinterpret_cast<const __half2*>(kq + (i >> 3) * 16384 + piece(t, i & 7) + 2 * q2));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) y[u][i & 1] = fma2(k[i], S[i][u], y[u][i & 1]);
+        }
+        float a[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          a[u] = (y[u][0].x + y[u][0].y) + (y[u][1].x + y[u][1].y);
+#pragma unroll
+          for (int m = 1; m < 4; m <<= 1) a[u] += __shfl_xor_sync(0xffffffffu, a[u], m);
+          a[u] = beta * (x[u] - e * a[u]);
+          y[u][0] = y[u][1] = both(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(kq + 8192 + (i >> 3) * 16384 + piece(t, i & 7) + 2 * q2));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            S[i][u] = fma2(k[i], both(a[u]), mul2(S[i][u], both(e)));
+            y[u][i & 1] = fma2(q, S[i][u], y[u][i & 1]);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          a[u] = (y[u][0].x + y[u][0].y) + (y[u][1].x + y[u][1].y);
+#pragma unroll
+          for (int m = 1; m < 4; m <<= 1) a[u] += __shfl_xor_sync(0xffffffffu, a[u], m);
+        }
+        if ((lane & 3) == 0) *here = make_float2(a[0], a[1]);  // (behind the shuffles: read by all four)
+      }
+      if (lane == 0) *ways = 1;
+      asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarR) : "memory");
+      float most[2] = {};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) most[u] = fmaxf(most[u], fmaxf(fabsf(S[i][u].x), fabsf(S[i][u].y)));
+      most_of(most[0], most[1]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        by[u] = scale_by(most[u]);
+        down[u] = two_to(-by[u]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i][u] = mul2(S[i][u], both(two_to(by[u])));
+      }
+    };
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
-      const uint32_t kq = base + C::off_kq + (c & 1) * 32768;
-      const unsigned char* tp = smem + C::off_tp + (c & 1) * 2 * kPanel;
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
       wait(kReady0 + (c & 1), c >> 1);
       // S^T, as an operand, to the output's warp too; S^T K^T
       float2 ks[8][2] = {};
       ms[0] = ms[1] = 0.0f;
+      // (beside the products: R's scales, and the state's next by what is left of S and of the rows' values)
+      float left_most[2] = {}, ratio[2], uup[2], rup[2];
+      int next[2];
+      bool hold;
       if (c > 0) named_bar_sync(3 * warp + kBarUsed, 64);
       if ((lane & 3) == 0) {
         downs[g] = down[0];
@@ -558,6 +650,39 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         for (int u = 0; u < 2; ++u)
           ms[u] = fmaxf(fmaxf(fmaxf(ms[u], fabsf(S[2 * k][u].x)), fabsf(S[2 * k][u].y)),
                         fmaxf(fabsf(S[2 * k + 1][u].x), fabsf(S[2 * k + 1][u].y)));
+        const float2 left = *reinterpret_cast<const float2*>(dec->left + 8 * k + q2);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float2 y = mul2(bf16_pair(v[k >> 1][2 * (k & 1) + u]), left);
+          left_most[u] = fmaxf(fmaxf(left_most[u], fabsf(y.x)), fabsf(y.y));
+        }
+        if (k == 7) {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              ms[u] = fmaxf(ms[u], __shfl_xor_sync(0xffffffffu, ms[u], o));
+              left_most[u] = fmaxf(left_most[u], __shfl_xor_sync(0xffffffffu, left_most[u], o));
+            }
+          const float all = dec->keep[kRows - 1];
+          int rby[2];
+          hold = true;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float most = ms[u] * down[u];
+            hold &= halves_hold(fmaxf(most, most_v[u]), least_v[u], rby[u]);
+            rup[u] = two_to(rby[u]);
+            next[u] = scale_by(fmaxf(most * all, left_most[u]));
+            ratio[u] = all * two_to(min(max(next[u] - by[u], -126), 127));
+            uup[u] = two_to(min(max(next[u] - rby[u] - 14, -126), 127));  // (T is times 2^14)
+          }
+          if ((lane & 3) == 0) {
+            bys[g] = rby[0];
+            bys[g + 8] = rby[1];
+          }
+          if (lane == 0) *ways = 0;
+          hold = __all_sync(0xffffffffu, hold);
+        }
         const uint32_t panel = kq + (k >> 2) * 16384;
         const int at = 2 * (k & 3) + ((lane >> 3) & 1);
 #pragma unroll
@@ -577,45 +702,87 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
         }
       }
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarS) : "memory");
-      // R^T = beta (V^T - exp(G) S^T K^T), to the output's warp too
+      // R^T = beta (V^T - exp(G) S^T K^T) by its columns' scales, as an operand
+      if (!hold) {
+        float by_row[2];
+        if (!look_closer(c, by_row)) {
+          rows_one_by_one(c, dec, by_row);
+          if (c + 1 < chunks) fetch_v(c + 1);
+          arrive(kFree0 + (c & 1));
+          continue;
+        }
+        __syncwarp();
+      }
+      const float sup[2] = {down[0] * rup[0], down[1] * rup[1]};
+      uint32_t rh[4][4], rl[4][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
-        const float2 beta = *reinterpret_cast<const float2*>(dec->beta + 8 * j + q2);
-        const float2 bk = mul2(mul2(beta, both(-1.0f)), keep);
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          ks[j][u] = fma2(mul2(bk, both(down[u])), ks[j][u], mul2(bf16_pair(v[j >> 1][2 * (j & 1) + u]), beta));
-        frag[(16 + j) * 32] = make_uint4(__float_as_uint(ks[j][0].x), __float_as_uint(ks[j][1].x), __float_as_uint(ks[j][0].y),
-                                         __float_as_uint(ks[j][1].y));
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * i + e;
+          const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
+          const float2 beta = *reinterpret_cast<const float2*>(dec->beta + 8 * j + q2);
+          const float2 bk = mul2(mul2(beta, both(-1.0f)), keep);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ks[j][u] = fma2(mul2(bk, both(sup[u])), ks[j][u], mul2(bf16_pair(v[i][2 * e + u]), mul2(beta, both(rup[u]))));
+            split_wide(ks[j][u], rh[i][2 * e + u], rl[i][2 * e + u]);
+          }
+        }
+        frag[(16 + 2 * i) * 32] = make_uint4(rh[i][0], rh[i][1], rh[i][2], rh[i][3]);
+        frag[(17 + 2 * i) * 32] = make_uint4(rl[i][0], rl[i][1], rl[i][2], rl[i][3]);
       }
       asm volatile("bar.arrive %0, 64;" ::"r"(3 * warp + kBarR) : "memory");
       if (c + 1 < chunks) fetch_v(c + 1);
-      // U^T = R^T T^T
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        by[u] = next[u];
+        down[u] = two_to(-next[u]);
+      }
+      // U^T = R^T T^T: rows 16 j .. of T by columns 16 i .., i <= j
       float2 ut[8][2] = {};
-      triangle(ut, [&](int j) { return make_float4(ks[j][0].x, ks[j][1].x, ks[j][0].y, ks[j][1].y); }, tp, lane);
-      // U^T diag(exp(G_64 - G)) in the next chunk's scale, as an operand; the scale by what is left of S and of U
-      const float all = dec->keep[kRows - 1];
-      float most[2] = {ms[0] * down[0] * all, ms[1] * down[1] * all};
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        float2 low[4][2] = {};  // of the products with second parts, times 2^11
+#pragma unroll
+        for (int i = 0; i <= j + 1; ++i) {
+          // two row blocks beside each other, where both have the columns
+          uint32_t th[2][4], tl[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (i > j + u) continue;
+            const int row = 16 * (j + u) + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
+            ldsm4(th[u], tp + piece(row, at));
+            ldsm4(tl[u], tp + kPart + piece(row, at));
+          }
+#pragma unroll
+          for (int w = 0; w < 3; ++w)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (i > j + u) continue;
+              if (w == 0) {
+                mma16(low[2 * u], rl[i], th[u][0], th[u][1]);
+                mma16(low[2 * u + 1], rl[i], th[u][2], th[u][3]);
+              } else if (w == 1) {
+                mma16(low[2 * u], rh[i], tl[u][0], tl[u][1]);
+                mma16(low[2 * u + 1], rh[i], tl[u][2], tl[u][3]);
+              } else {
+                mma16(ut[2 * (j + u)], rh[i], th[u][0], th[u][1]);
+                mma16(ut[2 * (j + u) + 1], rh[i], th[u][2], th[u][3]);
+              }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ut[2 * j + u][e] = fma2(low[u][e], both(1.0f / 2048.0f), ut[2 * j + u][e]);
+      }
+      // U^T diag(exp(G_64 - G)) in the next chunk's scale, as an operand
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 left = *reinterpret_cast<const float2*>(dec->left + 8 * j + q2);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          ut[j][u] = mul2(ut[j][u], left);
-          most[u] = fmaxf(fmaxf(most[u], fabsf(ut[j][u].x)), fabsf(ut[j][u].y));
-        }
-      }
-      most_of(most[0], most[1]);
-      float ratio[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int to = scale_by(most[u]);
-        ratio[u] = two_to(min(max(to - by[u], -126), 127));
-        by[u] = to;
-        down[u] = two_to(-to);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ut[j][u] = mul2(ut[j][u], both(two_to(to)));
+        for (int u = 0; u < 2; ++u) ut[j][u] = mul2(ut[j][u], mul2(left, both(uup[u])));
       }
       uint32_t uh[4][4], ul[4][4];
 #pragma unroll
@@ -624,7 +791,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) S[i][u] = mul2(S[i][u], both(all * ratio[u]));
+        for (int u = 0; u < 2; ++u) S[i][u] = mul2(S[i][u], both(ratio[u]));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -727,10 +894,10 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
 
     const uint4* frag = reinterpret_cast<const uint4*>(smem + C::off_frag) + w * 24 * 32 + lane;
     const float* downs = reinterpret_cast<const float*>(smem + C::off_down) + 16 * w;
+    const int *bys = reinterpret_cast<const int*>(smem + C::off_by) + 16 * w, *ways = reinterpret_cast<const int*>(smem + C::off_by) + C::cols + w;
     for (int c = 0; c < chunks; ++c) {
       const Decays* dec = reinterpret_cast<const Decays*>(smem + C::off_dec) + (c & 1);
-      const uint32_t kq = base + C::off_kq + (c & 1) * 32768;
-      const unsigned char* tp = smem + C::off_tp + (c & 1) * 2 * kPanel;
+      const uint32_t kq = base + C::off_kq + (c & 1) * 32768, tp = base + C::off_tp + (c & 1) * 2 * kPart;
       if (c > 0) finish(c - 1);
       named_bar_sync(3 * w + kBarS, 64);
       // O^T = exp(G) S^T Q^T
@@ -758,29 +925,60 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
           mma16(o[j + 3], hi, e[2], e[3]);
         }
       }
-      const float sc[2] = {downs[g], downs[g + 8]};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 keep = *reinterpret_cast<const float2*>(dec->keep + 8 * j + q2);
-        o[j][0] = mul2(mul2(o[j][0], both(sc[0])), keep);
-        o[j][1] = mul2(mul2(o[j][1], both(sc[1])), keep);
-      }
-      // O^T += R^T (P T)^T
+      // O^T += R^T (P T)^T, in the scales of R's columns and of P T's rows
       named_bar_sync(3 * w + kBarR, 64);
-      triangle(
-          o,
-          [&](int j) {
-            const uint4 x = frag[(16 + j) * 32];
-            return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
-          },
-          tp + kRows * 128, lane);
-      asm volatile("bar.arrive %0, 64;" ::"r"(3 * w + kBarUsed) : "memory");
+      if (*ways) {  // made row by row
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 x = frag[(16 + j) * 32];
+          o[j][0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.z));
+          o[j][1] = make_float2(__uint_as_float(x.y), __uint_as_float(x.w));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(p.scale));
+        }
+        asm volatile("bar.arrive %0, 64;" ::"r"(3 * w + kBarUsed) : "memory");
+      } else {
+        const int rby[2] = {bys[g], bys[g + 8]};
+        const float sc[2] = {downs[g] * two_to(rby[0] + 14), downs[g + 8] * two_to(rby[1] + 14)};
+        const float rdown[2] = {p.scale * two_to(-14 - rby[0]), p.scale * two_to(-14 - rby[1])};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 keep = mul2(*reinterpret_cast<const float2*>(dec->keep + 8 * j + q2), *reinterpret_cast<const float2*>(dec->up + 8 * j + q2));
+          o[j][0] = mul2(mul2(o[j][0], both(sc[0])), keep);
+          o[j][1] = mul2(mul2(o[j][1], both(sc[1])), keep);
+        }
+        float2 low[8][2] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = frag[(16 + 2 * i) * 32], y = frag[(17 + 2 * i) * 32];
+          const uint32_t rh[4] = {x.x, x.y, x.z, x.w}, rl[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = i; j < 4; ++j) {
+            uint32_t ph[4], pl[4];
+            const int row = 16 * j + (lane & 7) + ((lane >> 4) << 3), at = 2 * i + ((lane >> 3) & 1);
+            ldsm4(ph, tp + 8192 + piece(row, at));
+            ldsm4(pl, tp + kPart + 8192 + piece(row, at));
+            mma16(low[2 * j], rl, ph[0], ph[1]);
+            mma16(low[2 * j + 1], rl, ph[2], ph[3]);
+            mma16(low[2 * j], rh, pl[0], pl[1]);
+            mma16(low[2 * j + 1], rh, pl[2], pl[3]);
+            mma16(o[2 * j], rh, ph[0], ph[1]);
+            mma16(o[2 * j + 1], rh, ph[2], ph[3]);
+          }
+        }
+        asm volatile("bar.arrive %0, 64;" ::"r"(3 * w + kBarUsed) : "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // (one over a power of two)
+          const float2 up = *reinterpret_cast<const float2*>(dec->up + 8 * j + q2);
+          const float2 back = make_float2(__uint_as_float(0x7f000000u - __float_as_uint(up.x)), __uint_as_float(0x7f000000u - __float_as_uint(up.y)));
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            o[j][u] = mul2(mul2(fma2(low[j][u], both(1.0f / 2048.0f), o[j][u]), both(rdown[u])), back);
+        }
+      }
       arrive(kFree0 + (c & 1));
       // O, and its columns' share of the rows' sums of squares: to 8 rows' sums over 8 lanes, then one over the lanes' halves
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) o[j][u] = mul2(o[j][u], both(p.scale));
       if (p.norm_w && !dead()) {
         if (w == 0 && lane == 0) mbar_arrive_expect_tx(&bar[kSum0 + (c & 1)], 8 * kRows * 4);
         float2 y[8];
@@ -840,8 +1038,8 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
           tma_load_3d_tx(to + i * 16384 + 8192, &maps.q, 64 * i, hk, row, land);
         }
         const unsigned char* record = record0 + (int64_t)c * p.nv * kRecord;
-        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPanel, record, 2 * kPanel, land);
-        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPanel, sizeof(Decays), land);
+        bulk_g2s_nohint(smem + C::off_tp + (c & 1) * 2 * kPart, record, 2 * kPart, land);
+        bulk_g2s_nohint(smem + C::off_dec + (c & 1) * sizeof(Decays), record + 2 * kPart, sizeof(Decays), land);
       }
       __syncwarp();
     };
@@ -1132,7 +1330,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       *reinterpret_cast<float2*>(mine) = make_float2(hi[0], hi[1]);
       *reinterpret_cast<float2*>(mine + kRows) = make_float2(lo[0], lo[1]);
       *reinterpret_cast<float2*>(mine + 2 * kRows) = make_float2(b[0], b[1]);
-      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord + 2 * kPanel + 8 * lane;
+      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord + 2 * kPart + 8 * lane;
       *reinterpret_cast<float2*>(record) = make_float2(exp2_approx(hi[0] + lo[0]), exp2_approx(hi[1] + lo[1]));
       *reinterpret_cast<float2*>(record + 4 * kRows) =
           make_float2(exp2_approx((hi_end - hi[0]) + (lo_end - lo[0])), exp2_approx((hi_end - hi[1]) + (lo_end - lo[1])));
@@ -1141,6 +1339,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
     if (h0 == 0) {  // (the gates come while K and Q do)
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
+      float squares[8] = {};  // Q Q^T of the rows 16 (3 - w) ..
 #pragma unroll 2
       for (int k = 0; k < 8; ++k) {
         auto at = [&](int row, int piece) { return kqs + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4); };
@@ -1159,32 +1358,29 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
           mma16(*reinterpret_cast<float(*)[4]>(dots[i]), a, b0);
           mma16(*reinterpret_cast<float(*)[4]>(dots[i] + 4), a, b1);
         }
-      }
-      // Queries are as long as they are: each row of P goes by a power of two of its own, its largest to 2^8 .. 2^9.
-      {
-        const int row = 16 * (3 - w) + g;
-        float most[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          int m, tile, j;
-          place(i, m, tile, j);
-          if (!m) continue;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (j < tile || 8 * (e >> 2) + q2 + (e & 1) <= g + 4 * (e & 2)) most[e >> 1 & 1] = fmaxf(most[e >> 1 & 1], fabsf(dots[i][e]));
+        {
+          uint32_t b[4];
+          ldsm4(b, at(64 + 16 * (3 - w) + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+          const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
+          mma16(*reinterpret_cast<float(*)[4]>(squares), aq, b0);
+          mma16(*reinterpret_cast<float(*)[4]>(squares + 4), aq, b1);
         }
+      }
+      // Queries are as long as they are: each row of P, and of P T, goes by a power of two by which its query's length is 1 .. 2.
+      {
+        const int from = 4 * g + (g >> 1);  // the lane that has rows g's and g + 8's sums of squares
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 1));
-          most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 2));
-          const int by = scale_by(most[u]);
-          if ((lane & 3) == 0) scales[row + 8 * u] = two_to(-by);
+          const float ss = __shfl_sync(0xffffffffu, g & 1 ? squares[6 * u + 1] : squares[6 * u], from);
+          const int e = (int)(__float_as_uint(ss) >> 23);
+          const float up = two_to(e == 0 || e == 255 ? 0 : -((e - 127) >> 1));
+          if ((lane & 3) == 0) scales[16 * (3 - w) + g + 8 * u] = up;
 #pragma unroll
           for (int i = 0; i < 5; ++i)
             if (i > w) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if ((e >> 1 & 1) == u) dots[i][e] *= two_to(by);
+              for (int x = 0; x < 8; ++x)
+                if ((x >> 1 & 1) == u) dots[i][x] *= up;
             }
         }
       }
@@ -1197,12 +1393,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
       const int h = hk * p.group + h0 + hh;
       const float* hi = reinterpret_cast<const float*>(smem + kOffHi) + hh * kHeadDecays;
       const float *lo = hi + kRows, *beta = hi + 2 * kRows;
-      // A from K K^T and the strengths, to T's place; P, the same for all heads, to that behind it
+      // A from K K^T and the strengths, and P, to the places of T and P T
 #pragma unroll
       for (int i = 0; i < 5; ++i) {
         int m, tile, j;
         place(i, m, tile, j);
-        if (m && (h0 || hh)) continue;
         const int row = 16 * tile + g;
         const float b0 = m ? 1.0f : beta[row], b1 = m ? 1.0f : beta[row + 8];
         float y[2][4];
@@ -1230,7 +1425,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
             }
           }
         }
-        put_tiles(tps, m * kRows + 16 * tile, 2 * j, y[0], y[1], 1.0f, lane);
+        put_tiles<false>(tps, m * kRows + 16 * tile, 2 * j, y[0], y[1], lane);
       }
       __syncthreads();
       {
@@ -1340,46 +1535,59 @@ __global__ void __launch_bounds__(kPrepThreads, 4) gdn_prepare_kernel(const __gr
             for (int u = 0; u < 2; ++u) mma16(y[i][u], a.hi, b[u].hi);
           }
         }
-        // both by their decays to the record: within the rows' own 16 columns one exponential each, before them by way of the last
-        // row before the 16
-        unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord;
+        __syncthreads();  // (T and P are read)
+        // T, and P T in P's place, by their decays and 2^14: within the rows' own 16 columns one exponential each, before them by way of
+        // the last row before the 16
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int m = mine >> (8 * i + 4) & 15, j = mine >> (8 * i) & 15;
           if (m == 15) break;
           FragA a;
           load_a(a, tps, 16 * m, 16 * j, lane);
+          float t[2][4];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int row = 16 * m + 8 * u + g;
-            const float f = hi[3 * kRows + row], hr = hi[row], lr = lo[row], down = scales[row];
+            const float f = hi[3 * kRows + row] * 16384.0f, hr = hi[row], lr = lo[row];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (j == m && e > u) continue;  // above the diagonal: nothing reads it
-              const int col = 16 * j + 8 * e + q2;
+              const int at = 8 * e + q2, col = 16 * j + at;
               float2 by;
               if (j < m) {
                 by = mul2(*reinterpret_cast<const float2*>(hi + (3 + m) * kRows + col), both(f));
               } else {
                 const float2 hc = *reinterpret_cast<const float2*>(hi + col), lc = *reinterpret_cast<const float2*>(lo + col);
-                by = make_float2(exp2_approx((hr - hc.x) + (lr - lc.x)), exp2_approx((hr - hc.y) + (lr - lc.y)));
+                by = mul2(make_float2(exp2_approx((hr - hc.x) + (lr - lc.x)), exp2_approx((hr - hc.y) + (lr - lc.y))), both(16384.0f));
               }
               const float2 t1 = __half22float2(*reinterpret_cast<const __half2*>(&a.hi[2 * e + u]));
               const float2 t2 = __half22float2(*reinterpret_cast<const __half2*>(&a.lo[2 * e + u]));
-              float2 t = mul2(add2(t1, t2), by), pt = mul2(mul2(make_float2(y[i][e][2 * u], y[i][e][2 * u + 1]), both(down)), by);
-              if (j == m && e == u) {  // (a zero that masks is put there: it must not meet an infinity)
-                if (q2 > g) t.x = pt.x = 0.0f;
-                if (q2 + 1 > g) t.y = pt.y = 0.0f;
-              }
-              *reinterpret_cast<float2*>(record + pair_at(row, 2 * j + e, lane & 3)) = make_float2(round_t(t.x), round_t(t.y));
-              *reinterpret_cast<float2*>(record + pair_at(kRows + row, 2 * j + e, lane & 3)) = make_float2(round_t(pt.x), round_t(pt.y));
+              float2 x = mul2(add2(t1, t2), by), z = mul2(make_float2(y[i][e][2 * u], y[i][e][2 * u + 1]), by);
+              // (a zero that masks is put there, not multiplied by: it must not meet an infinity)
+              if (j == m && at > g + 8 * u) x.x = z.x = 0.0f;
+              if (j == m && at + 1 > g + 8 * u) x.y = z.y = 0.0f;
+              t[e][2 * u] = x.x;
+              t[e][2 * u + 1] = x.y;
+              y[i][e][2 * u] = z.x;
+              y[i][e][2 * u + 1] = z.y;
             }
           }
+          put_tiles<true>(tps, 16 * m, 2 * j, t[0], t[1], lane);
+          put_tiles<true>(tps, kRows + 16 * m, 2 * j, y[i][0], y[i][1], lane);
         }
       }
-      __syncthreads();  // (T is read)
+      fence_async();
+      __syncthreads();
+      unsigned char* record = records.at + ((int64_t)blockIdx.x * p.nv + h) * kRecord;
+      if (threadIdx.x < kRows) reinterpret_cast<Decays*>(record + 2 * kPart)->up[threadIdx.x] = scales[threadIdx.x];
+      if (threadIdx.x == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(record), "r"(tps), "r"(2 * kPart) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      }
+      __syncthreads();
     }
   }
+  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 std::mutex g_mu;
