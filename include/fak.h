@@ -572,15 +572,15 @@ int fak_paged_attn_debug_wait(int64_t timeout_ns, int unreachable);
  * A ragged batch, in device memory, read when the kernels run.  Rows and positions as in
  * fak_kv_batch: rows row_start[s] .. row_start[s+1]-1 are sequence s's, the last of its
  * kv_len[s] positions; rows at negative positions are padding, rows from row_start[n_seqs]
- * on belong to no sequence, and no row to two (starts rise).  A sequence whose first new row stands at position 0 begins
- * with an empty state (what its slot holds is not read); any other goes on with its
- * slot's.  Its slot is left with the state behind its last row; a sequence without new
+ * on belong to no sequence, and no row to two (starts rise).  A sequence whose first new
+ * row stands at position 0 begins with an empty state (what its slot holds is not read);
+ * any other goes on with its slot's.  Its slot is left with the state behind its last row; a sequence without new
  * rows leaves its slot as it was.  Two sequences of one call in one slot race.  A sequence
  * whose numbers are out of range (row_start as in fak_kv_batch, kv_len negative, slot
  * outside [0, n_slots)) is left out: nothing of it is read or written, and FAK_ERR_DEVICE
  * is recorded.  (Where a row_start lies below one before it, fak_gdn_attn may leave out
- * other sequences of more than 28 rows too, and a row that two sequences claim is one of
- * theirs.) */
+ * other sequences of more than 28 rows too, and a row that two sequences claim may hold
+ * anything, as may their slots.) */
 typedef struct {
     int32_t n_seqs;
     const int32_t* row_start; /* device [n_seqs + 1] */
@@ -614,15 +614,19 @@ int fak_gdn_conv(const fak_gdn_batch* batch, const fak_gdn_rows* rows, fak_strea
  * head h / (nv / nk), over a sequence's rows in order:
  *   S = exp(g) S;  S += k (beta (v - S^T k))^T;  o = scale S^T q;
  *   if norm_w: o = o / sqrt(mean o^2 + eps) * norm_w;  if z: o = o * silu(z).
- * Queries have any length.  Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and 0 <= beta <= 2, g <= 0: beyond
- * that the rule itself grows without bound, and a result may be an infinity or NaN before its f32 form is.
+ * Queries have any length.  Keys have lengths of at most 1 (as fak_gdn_conv leaves them, to f16's rounding) and
+ * 0 <= beta <= 2, g <= 0: beyond that the rule itself grows without bound, and a result may be an infinity or NaN before its
+ * f32 form is.
  * State, products with it and sums are f32; out is rounded once.  Sequences of more than 28 rows go over chunks of 64, on
- * the tensor cores, with products of 21 to 22 significand bits and f32 sums: what a row is off by goes by its own value and by what the
- * rows before it have brought to the same column, less what has decayed (to below 2^-126: all of it), whatever the rows behind it hold.  What they need besides, 33,792 bytes for 64 rows of a
- * head, comes from the library-owned pool of the batched GEMV's scratch, freed on the same stream (kept for later calls; a
- * graph memory node under stream capture): at most 1 GiB at a time (or one chunk's of all heads), longer calls go in parts.
- * FAK_ERR_NOMEM, and nothing done, if it cannot be had.  A padding row gets zeros; rows of no sequence are left as they were.  What a row holds
- * reaches its own sequence alone (where it is no number, up to 63 rows before it too).  Deterministic. */
+ * the tensor cores, with products of 21 to 22 significand bits and f32 sums: what a row is off by goes by its own value and by
+ * what the rows before it have brought to the same column, less what has decayed (to below 2^-126 over rows of a chunk: all of
+ * it), whatever the rows behind it hold.  (Where 64 values of a column and its state differ by more than 2^22 and decays have
+ * left no more, 16 columns of a chunk take six times as long.)  What these sequences need besides, 33,792 bytes of each
+ * head for min(rows / 64 + n_seqs, rows / 28 + 1) chunks, comes from the library-owned pool of the batched GEMV's scratch, freed
+ * on the same stream (kept for later calls; a graph memory node under stream capture): at most 1 GiB at a time (or one chunk's
+ * of all heads), longer calls go in parts.  FAK_ERR_NOMEM, and nothing done, if it cannot be had.  A padding row gets zeros;
+ * rows of no sequence are left as they were.  What a row holds reaches its own sequence alone (a value, key, query or gate that
+ * is no number up to 63 rows before it too, as does an infinite key, query or gate).  Deterministic. */
 typedef struct {
     int32_t nk, nv;             /* key heads, value heads, nv a multiple of nk */
     int32_t max_q;              /* bound on the sequences' rows; a sequence above it is left out, recorded */
@@ -658,8 +662,8 @@ int fak_gdn_debug_wait(int64_t timeout_ns, int unreachable);
  * stored as w - 1; a NULL gain is a gain of 1, whatever the offset.  y NULL: h stays as it is (and is not
  * written), n is its norm; n NULL: no norm.  gate is f32: one value for each value, channel or row, by strides
  * (gate_row, gate_col; a stride of 0 repeats).  h, y, n and gate do not overlap, nor do rows of what is written.
- * d is 1 to 32768.  Rows whose starts and strides are multiples of 16 bytes (and d of 4) take wide loads;
- * any others are as right.  One launch. */
+ * d is 1 to 32768.  Values go four at a time where every operand's start, its row stride and d are multiples of four
+ * values, two where they are of two; any others are as right.  One launch. */
 enum { FAK_GATE_LINEAR = 0, FAK_GATE_SIGMOID = 1 };
 typedef struct {
     int32_t h_type, y_type, n_type; /* FAK_ROWS_F32 or FAK_ROWS_BF16 */

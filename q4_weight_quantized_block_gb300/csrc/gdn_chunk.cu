@@ -33,9 +33,10 @@
 // memory and makes what only the output wants: S^T Q^T, R^T (P T)^T, the norm (its sums of squares from all eight such warps of
 // the head, a chunk later), the gate, the store.  One more warp issues the copies of K, Q, V, z and the records.  316
 // instructions of 8 cycles of the tensor cores for the state and 188 for the output, 4,032 cycles a chunk on each of an SM's four
-// parts; a chunk takes 6,700 (3.5 us): one warp's way through three products, the splitting into f16 and the scales, and shared
+// parts; a chunk takes 6,700 to 7,000 (3.5 to 3.6 us): one warp's way through three products, the splitting into f16 and the scales, and shared
 // memory, whose operands a warp of 16 columns takes for itself alone.  (R, T and P T as two tf32 each, which hold any column: 521 us
-// for a prompt's 128 chunks in place of 448.)
+// for a prompt's 128 chunks in place of 448.  Under one scale of the column's largest value, with no sums of their own for
+// second parts and no look at what the rows need: 397, and rows beside one of 10^4 times their size lost digits.)
 //
 // What did not help (measured with R, T and P T as two f16 under one scale, which hold less; a chunk of 6,000 cycles then): the same products by tcgen05, 64 columns
 // to a CTA (6,200 cycles a chunk: 128 rows of S, R or U go through shared memory for each of three products that wait for one
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(C::threads, 1) gdn_chunk_kernel(const __grid_c
   auto dead = [&]() { return __any_sync(0xffffffffu, *abort != 0); };
 
   // registers of a thread: 224 + 208 + 72 of the 3 * kRegs that the block has.  (The copies' warp wants more than 56, beside which
-  // the others could have 232 and 208: 254 us for 8 chunks in place of 248.)
+  // the others could have 232 and 208: 2 % longer for 8 chunks; 232 + 200 + 72: as long.)
   if (warp < NW)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   else if (warp < 2 * NW)
@@ -1209,7 +1210,7 @@ FAK_DEV int class_of(int n) {
 }
 
 // The order of the sequences, by one block: those of the highest classes first.  (CTAs start in that order, and those that start
-// last are the shortest: 16 prompts of 1 to 2,048 rows and 16 heads take 305 us, in the batch's order 332.)
+// last are the shortest: 16 prompts of 1 to 2,048 rows and 16 heads take 8 % longer in the batch's order.)
 FAK_DEV void make_order(const GdnParams& p, const Records& r, int* count) {
   auto of = [&](int i) {
     int begin, end;

@@ -10,8 +10,8 @@
 constexpr int kGdnDim = 128;  // key and value dims of a head
 constexpr int kGdnState = kGdnDim * kGdnDim;
 
-// Most rows of a sequence that goes row by row.  48 heads of one sequence take 8.3 us for 6 rows and 24.6 for 24 that way, and 27.3
-// by chunks of 64, however many of the 64 there are; of 16 sequences 33, 103 and 130 us, of 64 131, 373 and 450.
+// Most rows of a sequence that goes row by row.  48 heads of one sequence take 8.4 us for 6 rows and 28.2 for 28 that way, and 31.0
+// by chunks of 64, however many of the 64 there are; of 16 sequences 33, 119 and 146 us, of 64 130, 429 and 465.
 constexpr int kGdnFew = 28;
 
 // A sequence's rows that are no padding [first, r1), its slot, whether it begins with an empty state.

@@ -1,5 +1,7 @@
 // fak_residual_norm: the norm after a block, its gate and scale, the residual sum and the norm before the next block, in
-// one pass: a block of threads holds a row in registers from its loads to its stores.
+// one pass: a block of threads holds a row in registers from its loads to its stores.  (Of rows of more than 16,384 values, or
+// 8,192 on single values, 1,024 threads of 64 registers hold a part only; the rest goes through local memory: 2,048 rows of 32,768 take
+// 195 us, floor 138, with a gate 468, floor 178; of 32,767 on single values 536 and 1,085.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -226,7 +228,9 @@ extern "C" int fak_residual_norm(const fak_norm_args* a, fak_stream_t stream) {
   // (16,384 rows of 1,500 on multiples of 8 bytes take 60 us by fours, 153 by ones; 3,451 of 7,510 77 us by twos, 100 by ones.)
   // Many rows: 16 values to a thread, so that several blocks are on an SM, by ones from 4,096 values on
   // and without a gate (3,451 of 7,511: 100 us, by 8 to a thread 189; 1,391 of 2,559: 21 and 18); few: the fewest values that
-  // 1,024 threads allow.
+  // 1,024 threads allow, but by twos and ones no fewer than 4 and 8 above 2,048 and 1,024.
+  // On both sides of the cut, by fours, 16 to a thread and the fewest: 304 rows of 8,192 8.4 and 9.6 us, of 5,120 6.6 and 6.0; 608 of 8,192
+  // 14.4 and 15.7, of 5,120 10.4 and 9.9, of 1,024 3.7 and 2.6; 4,096 of 8,192 72 and 83, of 5,120 46.7 both, of 1,024 12.0 and 11.6.
   const bool many = a->rows >= 608 && a->d >= 1024 && a->d <= 16384;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
